@@ -463,6 +463,143 @@ vpce_status vpce_embedding_backward(const void* grad_out, vpce_dtype grad_dtype,
                                     void* workspace, size_t workspace_bytes, vpce_stream_t stream);
 
 /*
+ * Log probabilities of given tokens, with the entropy and the most likely
+ * alternatives of each row, from vocabulary-sharded logits: what a sampler, an
+ * evaluation or a policy-gradient step reads off the LM head.  The pages'
+ * combine ("Distributed Training III: Model Parallelism", CMU 11-868 Lecture
+ * 16 notes, §5.5) carries over: each shard's part of a row reduces to its
+ * maximum and its sums, and no full row is gathered.  With x = z / temperature
+ * and p = softmax(x) over all V columns,
+ *     logp[r]    = ln p_r[y_r]
+ *     entropy[r] = -sum_k p_rk ln p_rk
+ *     top_ids[r] = the `top` columns of largest logit, largest first; equal
+ *                  logits rank by column, lowest first
+ *     top_logp[r][j] = ln p_r[top_ids[r][j]].
+ * The logits are read once; nothing but the outputs is written.
+ *   shards .. ld     as vpce_forward (read only).
+ *   targets          device int64[s], or NULL when logp_out is NULL.  A target
+ *                    equal to ignore_index skips its row: its logits are not
+ *                    read, its top ids are -1 and its other outputs 0.  A
+ *                    target outside [0, V) gives logp NaN; the row's other
+ *                    outputs do not depend on the target.  Without targets
+ *                    every row is scored.
+ *   temperature      > 0, finite, with a finite inverse.
+ *   top              0..VPCE_MAX_TOP alternatives, at most V.
+ *   logp_out, entropy_out   device float[s], or NULL.
+ *   top_ids_out      device int64[s][top]; required when top > 0, else NULL.
+ *   top_logp_out     device float[s][top], or NULL.
+ *   stats_out        device float[s][4], 16-byte aligned, or NULL: the row's
+ *                    largest logit, ln sum_k exp((z_k - largest) /
+ *                    temperature), its entropy and 0, for
+ *                    vpce_logprob_backward.
+ *   flag_out         device int or NULL: set to 0, then bit 0
+ *                    (VPCE_FLAG_BAD_TARGET) if some target is outside [0, V),
+ *                    bit 1 (VPCE_FLAG_WAIT_TIMEOUT) if a wait gave up.
+ * At least one output is required.  Logits of -inf (masked columns) have
+ * probability 0 and add nothing to the entropy; as alternatives they come
+ * last, with top_logp -inf.  A row with no finite largest logit (every column
+ * -inf, or some +inf or NaN) has no distribution: logp, entropy, top_logp and
+ * the statistics past the first are NaN, and the alternatives are ordered by
+ * value, NaN first.  Results are bitwise reproducible.
+ */
+#define VPCE_MAX_TOP 32
+vpce_status vpce_logprob_forward(const void* const* shards, vpce_dtype dtype, int t, int64_t s,
+                                 const int64_t* vocab_start, int64_t ld, const int64_t* targets,
+                                 int64_t ignore_index, float temperature, int top, float* logp_out,
+                                 float* entropy_out, int64_t* top_ids_out, float* top_logp_out, float* stats_out,
+                                 int* flag_out, vpce_stream_t stream);
+
+/*
+ * Gradient of vpce_logprob_forward's outputs with respect to the logits.  With
+ * upstream gradients g_l of logp, g_H of entropy and g_j of top_logp,
+ *     dz_k = (g_l [k = y] + sum_j g_j [k = top_ids_j]
+ *             - p_k (g_l + sum_j g_j + g_H (ln p_k + entropy))) / temperature
+ * in the shards' dtype (one rounding from fp32).
+ *   shards .. temperature   the forward's (unchanged logits).
+ *   stats            the forward's stats_out.
+ *   grad_logp        device float[s] or NULL (no such gradient); needs targets.
+ *   grad_entropy     device float[s] or NULL.
+ *   top, top_ids, grad_top_logp   device int64[s][top] and float[s][top], or
+ *                    top = 0.  Entries outside [0, V) are skipped; an id that
+ *                    occurs twice counts twice.
+ *   grad_shards      host array of t device pointers of the shards' dtype, row
+ *                    stride ld_grad elements (0: dense), written in full: rows
+ *                    of ignored targets get zeros.  grad_shards[i] may be
+ *                    shards[i] (in place, same stride); other overlaps are not
+ *                    allowed.  Padding columns are not written.
+ * At least one upstream gradient is required.  Columns at -inf get 0.  A row
+ * without a distribution gets NaN, and so does, when grad_logp is given, a row
+ * whose target is outside [0, V).
+ */
+vpce_status vpce_logprob_backward(const void* const* shards, vpce_dtype dtype, int t, int64_t s,
+                                  const int64_t* vocab_start, int64_t ld, const int64_t* targets,
+                                  int64_t ignore_index, float temperature, const float* stats,
+                                  const float* grad_logp, const float* grad_entropy, int top,
+                                  const int64_t* top_ids, const float* grad_top_logp, void* const* grad_shards,
+                                  int64_t ld_grad, vpce_stream_t stream);
+
+/*
+ * Scaled embedding lookup with dropout over a table split by vocabulary
+ * (vpce_embedding_forward's table and method):
+ *     out[r, c] = scale / (1 - D / 65536) * m(r, c) * table[ids[r], c],
+ *     m(r, c)   = 0 where the 16 random bits of (r, c) are < D, else 1,
+ *     D         = drop_p * 65536 rounded to the nearest integer, at most 65535,
+ * so the expectation is scale * table[ids[r], c] exactly.  The bits come from
+ * Philox4x32-10 (Salmon, Moraes, Dror, Shaw, "Parallel random numbers: as easy
+ * as 1, 2, 3", SC 2011): key = the seed's two 32-bit words, low first; counter
+ * = (c / 8, r, offset's low word, offset's high word); the 16 bits of column c
+ * are half c % 8 of the block's four words, low halves first.  The mask is
+ * never stored: vpce_embedding_dropout_backward forms it again.
+ *   table_shards, dtype, t, vocab_start, h, ld_table   as
+ *                 vpce_embedding_forward (V, h < 2^31).
+ *   ids           device int64[s].  padding_id gives a zero row, whether it
+ *                 lies in [0, V) or not (INT64_MIN: no padding); any other id
+ *                 outside [0, V) gives a zero row and the flag.
+ *   scale         finite.
+ *   drop_p        0 <= drop_p < 1; D = 0 drops nothing and reads no rng.
+ *   rng           device int64[2]: seed and offset, any bits; read by the
+ *                 kernel, so that a captured graph draws new masks after the
+ *                 two words change.  May be NULL when D = 0.
+ *   out           device [s, h] of out_dtype, row stride ld_out (0 = h); the
+ *                 product is formed in fp32 and rounded once.
+ *   flag_out      device int or NULL, as vpce_embedding_forward.
+ * A dropped element is 0 whatever the table holds.
+ */
+vpce_status vpce_embedding_dropout_forward(const void* const* table_shards, vpce_dtype dtype, int t,
+                                           const int64_t* vocab_start, int64_t h, int64_t ld_table,
+                                           const int64_t* ids, int64_t s, int64_t padding_id, float scale,
+                                           float drop_p, const int64_t* rng, void* out, vpce_dtype out_dtype,
+                                           int64_t ld_out, int* flag_out, vpce_stream_t stream);
+
+/*
+ * Gradient of vpce_embedding_dropout_forward with respect to the table:
+ *     grad_table[v, c] (=, or += when accumulate) scale / (1 - D / 65536) *
+ *         sum over r with ids[r] = v of m(r, c) * grad_out[r, c],
+ * v != padding_id; ids equal to padding_id or outside [0, V) contribute
+ * nothing.  Sums are fp32 in an order fixed by the ids, so results are bitwise
+ * reproducible.
+ *   grad_out      device [s, h] of grad_dtype, row stride ld_grad (0 = h),
+ *                 element aligned.
+ *   ids, padding_id, scale, drop_p, rng   the forward's (rng's words as the
+ *                 forward read them).
+ *   grad_shards   host array of t device float pointers, shard i [w_i, h], row
+ *                 stride ld_grad_table (0 = h), element aligned.
+ *   accumulate    0: every element of the shards is written (zeros for ids
+ *                 that do not occur); 1: the sums are added to what they hold,
+ *                 and rows of ids that do not occur are left alone.
+ *   workspace     vpce_embedding_dropout_backward_workspace_bytes(s, V, h)
+ *                 bytes (0 for sizes out of range), 256-byte aligned, caller
+ *                 owned, no initialisation needed.
+ */
+size_t vpce_embedding_dropout_backward_workspace_bytes(int64_t s, int64_t V, int64_t h);
+vpce_status vpce_embedding_dropout_backward(const void* grad_out, vpce_dtype grad_dtype, int64_t ld_grad,
+                                            const int64_t* ids, int64_t s, int64_t padding_id, float scale,
+                                            float drop_p, const int64_t* rng, float* const* grad_shards, int t,
+                                            const int64_t* vocab_start, int64_t h, int64_t ld_grad_table,
+                                            int accumulate, void* workspace, size_t workspace_bytes,
+                                            vpce_stream_t stream);
+
+/*
  * Synchronise `stream`, then copy the workspace error flag to *flag (bit 0:
  * bad target seen by the last forward; bit 1: a device wait timed out, in
  * which case the forward's loss is NaN).

@@ -26,10 +26,12 @@ NVCC_FLAGS = ["-O3", "-lineinfo", "-std=c++17", "-Xcompiler", "-fPIC", "-Xptxas"
 
 LIBS = {
     "libvpce.so": ["vpce_api.cu", "vpce_forward.cu", "vpce_backward.cu", "vpce_fused.cu", "vpce_static.cu",
-                   "vpce_gemm.cu", "vpce_gemm_bwd.cu", "vpce_embed.cu", "vpce_lmhead_bwd.cu"],
+                   "vpce_gemm.cu", "vpce_gemm_bwd.cu", "vpce_embed.cu", "vpce_lmhead_bwd.cu", "vpce_logprob.cu",
+                   "vpce_logprob_bwd.cu", "vpce_embed_dropout.cu"],
     "libvpce_synth.so": ["synth_gen.cu"],
 }
-HEADERS = ["vpce_device.cuh", "vpce_kernels.cuh", "vpce_chunk.cuh", "vpce_tc.cuh"]
+HEADERS = ["vpce_device.cuh", "vpce_kernels.cuh", "vpce_chunk.cuh", "vpce_tc.cuh", "vpce_logprob.cuh",
+           "vpce_embed_dropout.cuh"]
 LINK: dict[str, list[str]] = {}
 
 

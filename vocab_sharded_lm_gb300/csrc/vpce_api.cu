@@ -5,7 +5,9 @@
 #include <cstring>
 #include <mutex>
 
+#include "vpce_embed_dropout.cuh"
 #include "vpce_kernels.cuh"
+#include "vpce_logprob.cuh"
 
 namespace vpce {
 cudaError_t set_backward_smem();
@@ -106,13 +108,14 @@ bool aligned(const void* p, size_t a) { return (reinterpret_cast<uintptr_t>(p) %
 // Shared validation of the logits description; fills the geometry.
 // from_zero: the shards cover the whole vocabulary (vocab_start[0] = 0);
 // otherwise they may be one rank's part of it (vocab_start[0] >= 0).
+// need_targets: a batch with rows has targets.
 vpce_status check_logits(const void* const* shards, vpce_dtype dtype, int t, int64_t s,
                          const int64_t* vocab_start, int64_t ld, const int64_t* targets, ShardSet* sh,
-                         long long* V, bool from_zero = true) {
+                         long long* V, bool from_zero = true, bool need_targets = true) {
   if (dtype != VPCE_FP32 && dtype != VPCE_BF16) return VPCE_ERR_DTYPE;
   if (t < 1 || t > VPCE_MAX_SHARDS || s < 0 || s > (int64_t(1) << 31)) return VPCE_ERR_INVALID_ARG;
   if (shards == nullptr || vocab_start == nullptr) return VPCE_ERR_INVALID_ARG;
-  if (s > 0 && targets == nullptr) return VPCE_ERR_INVALID_ARG;
+  if (s > 0 && need_targets && targets == nullptr) return VPCE_ERR_INVALID_ARG;
   if (targets != nullptr && !aligned(targets, 8)) return VPCE_ERR_ALIGNMENT;
   const int eb = dtype == VPCE_BF16 ? 2 : 4;
   if (from_zero ? vocab_start[0] != 0 : vocab_start[0] < 0) return VPCE_ERR_INVALID_ARG;
@@ -790,6 +793,201 @@ vpce_status vpce_embedding_backward(const void* grad_out, vpce_dtype grad_dtype,
   const cudaError_t e = launch_embed_backward(grad_out, grad_dtype == VPCE_BF16, ldg,
                                               reinterpret_cast<const long long*>(ids), s, gsh, t, vocab_start[t],
                                               h, workspace, sms, reinterpret_cast<cudaStream_t>(stream));
+  return e == cudaSuccess ? VPCE_OK : VPCE_ERR_CUDA;
+}
+
+// The scores' temperature: positive, with a finite inverse.
+static bool good_temperature(float temperature) {
+  return std::isfinite(temperature) && temperature > 0.f && std::isfinite(1.442695041f / temperature);
+}
+
+vpce_status vpce_logprob_forward(const void* const* shards, vpce_dtype dtype, int t, int64_t s,
+                                 const int64_t* vocab_start, int64_t ld, const int64_t* targets,
+                                 int64_t ignore_index, float temperature, int top, float* logp_out,
+                                 float* entropy_out, int64_t* top_ids_out, float* top_logp_out, float* stats_out,
+                                 int* flag_out, vpce_stream_t stream) {
+  LogprobParams p;
+  vpce_status st = check_logits(shards, dtype, t, s, vocab_start, ld, targets, &p.sh, &p.V, /*from_zero=*/true,
+                                /*need_targets=*/logp_out != nullptr);
+  if (st != VPCE_OK) return st;
+  if (!good_temperature(temperature)) return VPCE_ERR_INVALID_ARG;
+  if (top < 0 || top > VPCE_MAX_TOP || top > p.V) return VPCE_ERR_INVALID_ARG;
+  if (top > 0 ? (s > 0 && top_ids_out == nullptr) : (top_ids_out != nullptr || top_logp_out != nullptr))
+    return VPCE_ERR_INVALID_ARG;
+  if (logp_out == nullptr && entropy_out == nullptr && top_ids_out == nullptr && stats_out == nullptr && s > 0)
+    return VPCE_ERR_INVALID_ARG;
+  if (!aligned(logp_out, 4) || !aligned(entropy_out, 4) || !aligned(top_ids_out, 8) || !aligned(top_logp_out, 4) ||
+      !aligned(stats_out, 16) || !aligned(flag_out, 4))
+    return VPCE_ERR_ALIGNMENT;
+  int sms = 0;
+  if ((st = device_setup(&sms)) != VPCE_OK) return st;
+  cudaStream_t cs = reinterpret_cast<cudaStream_t>(stream);
+  if (flag_out != nullptr && cudaMemsetAsync(flag_out, 0, sizeof(int), cs) != cudaSuccess) {
+    cudaGetLastError();
+    return VPCE_ERR_CUDA;
+  }
+  if (s == 0) return VPCE_OK;
+  p.t = t;
+  p.s = s;
+  p.targets = reinterpret_cast<const long long*>(targets);
+  p.ignore_index = ignore_index;
+  p.inv_t = 1.f / temperature;
+  p.top = top;
+  p.logp = logp_out;
+  p.entropy = entropy_out;
+  p.top_ids = reinterpret_cast<long long*>(top_ids_out);
+  p.top_logp = top_logp_out;
+  p.stats = reinterpret_cast<float4*>(stats_out);
+  p.flag = flag_out;
+  if (dtype == VPCE_BF16) launch_logprob_forward<__nv_bfloat16>(p, sms, cs);
+  else launch_logprob_forward<float>(p, sms, cs);
+  return launch_status();
+}
+
+vpce_status vpce_logprob_backward(const void* const* shards, vpce_dtype dtype, int t, int64_t s,
+                                  const int64_t* vocab_start, int64_t ld, const int64_t* targets,
+                                  int64_t ignore_index, float temperature, const float* stats,
+                                  const float* grad_logp, const float* grad_entropy, int top,
+                                  const int64_t* top_ids, const float* grad_top_logp, void* const* grad_shards,
+                                  int64_t ld_grad, vpce_stream_t stream) {
+  LogprobBwdParams p;
+  ShardSet gsh;
+  vpce_status st = check_logits(shards, dtype, t, s, vocab_start, ld, targets, &p.sh, &p.V, /*from_zero=*/true,
+                                /*need_targets=*/grad_logp != nullptr);
+  if (st != VPCE_OK) return st;
+  if ((st = check_logits(reinterpret_cast<const void* const*>(grad_shards), dtype, t, s, vocab_start, ld_grad,
+                         nullptr, &gsh, &p.V, /*from_zero=*/true, /*need_targets=*/false)) != VPCE_OK)
+    return st;
+  if (!good_temperature(temperature)) return VPCE_ERR_INVALID_ARG;
+  if (top < 0 || top > VPCE_MAX_TOP || top > p.V) return VPCE_ERR_INVALID_ARG;
+  if (s > 0) {
+    if (stats == nullptr) return VPCE_ERR_INVALID_ARG;
+    if (grad_logp == nullptr && grad_entropy == nullptr && top == 0) return VPCE_ERR_INVALID_ARG;
+    if (top > 0 && (top_ids == nullptr || grad_top_logp == nullptr)) return VPCE_ERR_INVALID_ARG;
+  }
+  if (!aligned(stats, 16) || !aligned(grad_logp, 4) || !aligned(grad_entropy, 4) || !aligned(top_ids, 8) ||
+      !aligned(grad_top_logp, 4))
+    return VPCE_ERR_ALIGNMENT;
+  for (int i = 0; i < t; ++i) {
+    // in place means the same rows
+    if (s > 1 && gsh.ptr[i] == p.sh.ptr[i] && gsh.ld_bytes[i] != p.sh.ld_bytes[i]) return VPCE_ERR_INVALID_ARG;
+    p.grad[i] = const_cast<unsigned char*>(gsh.ptr[i]);
+    p.ld_grad_bytes[i] = gsh.ld_bytes[i];
+  }
+  int sms = 0;
+  if ((st = device_setup(&sms)) != VPCE_OK) return st;
+  if (s == 0) return VPCE_OK;
+  p.t = t;
+  p.s = s;
+  p.targets = reinterpret_cast<const long long*>(targets);
+  p.ignore_index = ignore_index;
+  p.inv_t = 1.f / temperature;
+  p.stats = reinterpret_cast<const float4*>(stats);
+  p.g_logp = grad_logp;
+  p.g_entropy = grad_entropy;
+  p.top = top;
+  p.top_ids = reinterpret_cast<const long long*>(top_ids);
+  p.g_top = grad_top_logp;
+  cudaStream_t cs = reinterpret_cast<cudaStream_t>(stream);
+  if (dtype == VPCE_BF16) launch_logprob_backward<__nv_bfloat16>(p, sms, cs);
+  else launch_logprob_backward<float>(p, sms, cs);
+  return launch_status();
+}
+
+// What the lookup and its gradient share: sizes, scale, dropout and ids.
+static vpce_status check_embed_dropout(int t, const int64_t* vocab_start, int64_t h, const int64_t* ids, int64_t s,
+                                       float scale, float drop_p, const int64_t* rng, EmbedDropParams* p) {
+  if (t < 1 || t > VPCE_MAX_SHARDS || s < 0 || s > (int64_t(1) << 31) || h < 1 || h >= (int64_t(1) << 31) ||
+      vocab_start == nullptr || vocab_start[t] >= (int64_t(1) << 31))
+    return VPCE_ERR_INVALID_ARG;
+  if (!std::isfinite(scale) || !(drop_p >= 0.f && drop_p < 1.f)) return VPCE_ERR_INVALID_ARG;
+  const int drop = int(std::floor(double(drop_p) * 65536.0 + 0.5));
+  p->drop = unsigned(drop < 65535 ? drop : 65535);
+  const double factor = double(scale) * (65536.0 / double(65536 - p->drop));
+  p->factor = float(factor);
+  if (!std::isfinite(p->factor)) return VPCE_ERR_INVALID_ARG;
+  if (s > 0 && (ids == nullptr || (p->drop > 0 && rng == nullptr))) return VPCE_ERR_INVALID_ARG;
+  if (!aligned(ids, 8) || !aligned(rng, 8)) return VPCE_ERR_ALIGNMENT;
+  p->t = t;
+  p->V = vocab_start[t];
+  p->h = h;
+  p->ids = reinterpret_cast<const long long*>(ids);
+  p->s = s;
+  p->rng = reinterpret_cast<const unsigned long long*>(rng);
+  p->flag = nullptr;
+  p->accumulate = 0;
+  return VPCE_OK;
+}
+
+vpce_status vpce_embedding_dropout_forward(const void* const* table_shards, vpce_dtype dtype, int t,
+                                           const int64_t* vocab_start, int64_t h, int64_t ld_table,
+                                           const int64_t* ids, int64_t s, int64_t padding_id, float scale,
+                                           float drop_p, const int64_t* rng, void* out, vpce_dtype out_dtype,
+                                           int64_t ld_out, int* flag_out, vpce_stream_t stream) {
+  if ((dtype != VPCE_FP32 && dtype != VPCE_BF16) || (out_dtype != VPCE_FP32 && out_dtype != VPCE_BF16))
+    return VPCE_ERR_DTYPE;
+  EmbedDropParams p;
+  vpce_status st = check_embed_dropout(t, vocab_start, h, ids, s, scale, drop_p, rng, &p);
+  if (st != VPCE_OK) return st;
+  const int eb = dtype == VPCE_BF16 ? 2 : 4, ob = out_dtype == VPCE_BF16 ? 2 : 4;
+  const int64_t ldt = ld_table == 0 ? h : ld_table, ldo = ld_out == 0 ? h : ld_out;
+  if (ldt < h || ldo < h) return VPCE_ERR_INVALID_ARG;
+  if ((st = split_table(table_shards, t, vocab_start, ldt, eb, s > 0, &p.sh)) != VPCE_OK) return st;
+  if (s > 0 && out == nullptr) return VPCE_ERR_INVALID_ARG;
+  if (!aligned(out, size_t(ob)) || !aligned(flag_out, 4)) return VPCE_ERR_ALIGNMENT;
+  int sms = 0;
+  if ((st = device_setup(&sms)) != VPCE_OK) return st;
+  cudaStream_t cs = reinterpret_cast<cudaStream_t>(stream);
+  if (flag_out != nullptr && cudaMemsetAsync(flag_out, 0, sizeof(int), cs) != cudaSuccess) {
+    cudaGetLastError();
+    return VPCE_ERR_CUDA;
+  }
+  if (s == 0) return VPCE_OK;
+  p.padding_id = padding_id;
+  p.out = static_cast<unsigned char*>(out);
+  p.ld_out_bytes = ldo * ob;
+  p.flag = flag_out;
+  launch_embed_dropout_forward(p, dtype == VPCE_BF16, out_dtype == VPCE_BF16, sms, cs);
+  return launch_status();
+}
+
+size_t vpce_embedding_dropout_backward_workspace_bytes(int64_t s, int64_t V, int64_t h) {
+  if (s < 0 || s > (int64_t(1) << 31) || V < 1 || V >= (int64_t(1) << 31) || h < 1 || h >= (int64_t(1) << 31))
+    return 0;
+  return embed_dropout_workspace_bytes(s, V, h);
+}
+
+vpce_status vpce_embedding_dropout_backward(const void* grad_out, vpce_dtype grad_dtype, int64_t ld_grad,
+                                            const int64_t* ids, int64_t s, int64_t padding_id, float scale,
+                                            float drop_p, const int64_t* rng, float* const* grad_shards, int t,
+                                            const int64_t* vocab_start, int64_t h, int64_t ld_grad_table,
+                                            int accumulate, void* workspace, size_t workspace_bytes,
+                                            vpce_stream_t stream) {
+  if (grad_dtype != VPCE_FP32 && grad_dtype != VPCE_BF16) return VPCE_ERR_DTYPE;
+  EmbedDropParams p;
+  vpce_status st = check_embed_dropout(t, vocab_start, h, ids, s, scale, drop_p, rng, &p);
+  if (st != VPCE_OK) return st;
+  const int eb = grad_dtype == VPCE_BF16 ? 2 : 4;
+  const int64_t ldg = ld_grad == 0 ? h : ld_grad, ldt = ld_grad_table == 0 ? h : ld_grad_table;
+  if (ldg < h || ldt < h || (accumulate != 0 && accumulate != 1)) return VPCE_ERR_INVALID_ARG;
+  // an empty batch still writes the table's zeros, so the shards are needed
+  if ((st = split_table(reinterpret_cast<const void* const*>(grad_shards), t, vocab_start, ldt, 4,
+                        /*need_ptrs=*/true, &p.sh)) != VPCE_OK)
+    return st;
+  if (s > 0 && grad_out == nullptr) return VPCE_ERR_INVALID_ARG;
+  if (!aligned(grad_out, size_t(eb))) return VPCE_ERR_ALIGNMENT;
+  if (workspace == nullptr) return VPCE_ERR_INVALID_ARG;
+  if (!aligned(workspace, 256)) return VPCE_ERR_ALIGNMENT;
+  if (workspace_bytes < embed_dropout_workspace_bytes(s, p.V, h)) return VPCE_ERR_WORKSPACE;
+  int sms = 0;
+  if ((st = device_setup(&sms)) != VPCE_OK) return st;
+  if (s == 0 && accumulate) return VPCE_OK;
+  p.padding_id = padding_id;
+  p.out = const_cast<unsigned char*>(static_cast<const unsigned char*>(grad_out));
+  p.ld_out_bytes = ldg * eb;
+  p.accumulate = accumulate;
+  const cudaError_t e = launch_embed_dropout_backward(p, grad_dtype == VPCE_BF16, workspace, sms,
+                                                      reinterpret_cast<cudaStream_t>(stream));
   return e == cudaSuccess ? VPCE_OK : VPCE_ERR_CUDA;
 }
 

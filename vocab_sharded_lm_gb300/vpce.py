@@ -10,6 +10,7 @@ from __future__ import annotations
 import ctypes
 import os
 import threading
+from typing import Any, NamedTuple
 
 PKG = os.path.dirname(os.path.abspath(__file__))
 LIB_PATH = os.path.join(PKG, "_lib", "libvpce.so")
@@ -32,6 +33,8 @@ VPCE_FLAG_BAD_TARGET = 1
 VPCE_FLAG_WAIT_TIMEOUT = 2
 VPCE_STATIC_SCRATCH_BYTES = 8 * 1024 * 1024
 VPCE_LMHEAD_MAX_GROUPS = 256
+VPCE_MAX_TOP = 32
+INT64_MIN = -(1 << 63)
 
 _lib = None
 _lock = threading.Lock()
@@ -113,6 +116,22 @@ def load_library(path: str | None = None) -> ctypes.CDLL:
         lib.vpce_embedding_backward.restype = ctypes.c_int
         lib.vpce_embedding_backward.argtypes = [_P, ctypes.c_int, _I64, _P, _I64, _P, ctypes.c_int, _I64P, _I64,
                                                 _I64, _P, ctypes.c_size_t, _P]
+        lib.vpce_logprob_forward.restype = ctypes.c_int
+        lib.vpce_logprob_forward.argtypes = [_P, ctypes.c_int, ctypes.c_int, _I64, _P, _I64, _P, _I64,
+                                             ctypes.c_float, ctypes.c_int, _P, _P, _P, _P, _P, _P, _P]
+        lib.vpce_logprob_backward.restype = ctypes.c_int
+        lib.vpce_logprob_backward.argtypes = [_P, ctypes.c_int, ctypes.c_int, _I64, _P, _I64, _P, _I64,
+                                              ctypes.c_float, _P, _P, _P, ctypes.c_int, _P, _P, _P, _I64, _P]
+        lib.vpce_embedding_dropout_forward.restype = ctypes.c_int
+        lib.vpce_embedding_dropout_forward.argtypes = [_P, ctypes.c_int, ctypes.c_int, _P, _I64, _I64, _P, _I64,
+                                                       _I64, ctypes.c_float, ctypes.c_float, _P, _P, ctypes.c_int,
+                                                       _I64, _P, _P]
+        lib.vpce_embedding_dropout_backward_workspace_bytes.restype = ctypes.c_size_t
+        lib.vpce_embedding_dropout_backward_workspace_bytes.argtypes = [_I64, _I64, _I64]
+        lib.vpce_embedding_dropout_backward.restype = ctypes.c_int
+        lib.vpce_embedding_dropout_backward.argtypes = [_P, ctypes.c_int, _I64, _P, _I64, _I64, ctypes.c_float,
+                                                        ctypes.c_float, _P, _P, ctypes.c_int, _P, _I64, _I64,
+                                                        ctypes.c_int, _P, ctypes.c_size_t, _P]
         lib.vpce_read_error_flag.restype = ctypes.c_int
         lib.vpce_read_error_flag.argtypes = [_P, ctypes.POINTER(ctypes.c_int), _P]
         lib.vpce_status_string.restype = ctypes.c_char_p
@@ -655,4 +674,229 @@ def vpce_embedding_backward(grad_out, ids, grad_shards, vocab_start=None, *, wor
                                            _stream_ptr(stream)))
     if code != VPCE_OK:
         raise VPCEError(code, "vpce_embedding_backward")
+    return grad_shards
+
+
+# ----------------------------------------------------------------------------
+# log probabilities of given tokens, entropy and top alternatives
+# ----------------------------------------------------------------------------
+class LogprobResult(NamedTuple):
+    """What :func:`vpce_logprob_forward` computed: float32 ``logp`` [s] (None
+    without targets), ``entropy`` [s], int64 ``top_ids`` and float32
+    ``top_logp`` [s, top] (None for ``top=0``), and ``stats`` [s, 4] for
+    :func:`vpce_logprob_backward`."""
+    logp: Any
+    entropy: Any
+    top_ids: Any
+    top_logp: Any
+    stats: Any
+
+
+def _buffer(x, shape, dtype, device, name):
+    """``x`` checked, or a new tensor: contiguous CUDA memory of this shape."""
+    import torch
+
+    if x is None:
+        return torch.empty(shape, dtype=dtype, device=device)
+    if x.dtype != dtype or tuple(x.shape) != shape or not x.is_cuda or not x.is_contiguous():
+        raise ValueError(f"{name} must be a contiguous CUDA {dtype} tensor of shape {shape}")
+    return x
+
+
+def _addr(x):
+    return None if x is None else x.data_ptr()
+
+
+def _check_targets(targets, s):
+    import torch
+
+    if targets is not None and (targets.dtype != torch.int64 or not targets.is_cuda or targets.numel() != s
+                                or not targets.is_contiguous()):
+        raise ValueError("targets must be a contiguous CUDA int64 tensor with one entry per row")
+
+
+def _check_flag(flag):
+    import torch
+
+    if flag is not None and (flag.dtype != torch.int32 or not flag.is_cuda or flag.numel() != 1):
+        raise ValueError("flag must be a CUDA int32 tensor of one element")
+
+
+def vpce_logprob_forward(shards, targets=None, vocab_start=None, *, ignore_index: int = -100,
+                         temperature: float = 1.0, top: int = 0, logp_out=None, entropy_out=None, top_ids_out=None,
+                         top_logp_out=None, stats_out=None, flag=None, stream=None) -> LogprobResult:
+    """Log probability of each row's target under softmax(logits /
+    temperature), the entropy, and the ``top`` most likely columns with their
+    log probabilities (equal logits by column, lowest first), from
+    vocabulary-sharded logits read once.  Rows whose target is
+    ``ignore_index`` give zeros and top ids -1; without ``targets`` every row
+    is scored.  The ``*_out`` tensors are allocated where not given; ``flag``
+    (CUDA int32 scalar) receives bit 0 if a target was outside [0, V)."""
+    import torch
+
+    dtype, s, vs, ld = _describe(shards, vocab_start)
+    dev = shards[0].device
+    _check_targets(targets, s)
+    _check_flag(flag)
+    if targets is None and logp_out is not None:
+        raise ValueError("logp_out needs targets")
+    top = int(top)
+    if not 0 <= top <= VPCE_MAX_TOP:
+        raise ValueError(f"top must be 0..{VPCE_MAX_TOP}")
+    if top == 0 and (top_ids_out is not None or top_logp_out is not None):
+        raise ValueError("top_ids_out and top_logp_out need top > 0")
+    f32 = torch.float32
+    logp = _buffer(logp_out, (s,), f32, dev, "logp_out") if targets is not None else None
+    entropy = _buffer(entropy_out, (s,), f32, dev, "entropy_out")
+    ids = _buffer(top_ids_out, (s, top), torch.int64, dev, "top_ids_out") if top else None
+    top_logp = _buffer(top_logp_out, (s, top), f32, dev, "top_logp_out") if top else None
+    stats = _buffer(stats_out, (s, 4), f32, dev, "stats_out")
+    code = load_library().vpce_logprob_forward(_ptr_array([sh.data_ptr() for sh in shards]), dtype, len(shards), s,
+                                               _i64_array(vs), ld, _addr(targets), ignore_index, temperature, top,
+                                               _addr(logp), _addr(entropy), _addr(ids), _addr(top_logp),
+                                               _addr(stats), _addr(flag), _stream_ptr(stream))
+    if code != VPCE_OK:
+        raise VPCEError(code, "vpce_logprob_forward")
+    return LogprobResult(logp, entropy, ids, top_logp, stats)
+
+
+def vpce_logprob_backward(shards, targets, stats, vocab_start=None, *, ignore_index: int = -100,
+                          temperature: float = 1.0, grad_logp=None, grad_entropy=None, top_ids=None,
+                          grad_top_logp=None, grad_shards=None, stream=None):
+    """Gradient of :func:`vpce_logprob_forward`'s outputs with respect to the
+    logits, for float32 upstream gradients ``grad_logp`` [s], ``grad_entropy``
+    [s] and ``grad_top_logp`` [s, top] (with the forward's ``top_ids``; each
+    may be left out).  ``stats`` is the forward's.  Written into
+    ``grad_shards``, a list like ``shards``: None allocates it, and passing
+    ``shards`` itself overwrites the logits in place.  Returns the list."""
+    import torch
+
+    dtype, s, vs, ld = _describe(shards, vocab_start)
+    dev = shards[0].device
+    _check_targets(targets, s)
+    f32 = torch.float32
+    _buffer(stats, (s, 4), f32, dev, "stats")
+    for g, name in ((grad_logp, "grad_logp"), (grad_entropy, "grad_entropy")):
+        if g is not None:
+            _buffer(g, (s,), f32, dev, name)
+    if (top_ids is None) != (grad_top_logp is None):
+        raise ValueError("top_ids and grad_top_logp go together")
+    top = 0
+    if top_ids is not None:
+        top = top_ids.shape[-1]
+        _buffer(top_ids, (s, top), torch.int64, dev, "top_ids")
+        _buffer(grad_top_logp, (s, top), f32, dev, "grad_top_logp")
+    if grad_shards is None:
+        grad_shards = [torch.empty(sh.shape, dtype=sh.dtype, device=dev) for sh in shards]
+    if len(grad_shards) != len(shards) or any(g.shape != sh.shape for g, sh in zip(grad_shards, shards)):
+        raise ValueError("grad_shards must have the shards' shapes")
+    gdtype, _, _, ld_grad = _describe(grad_shards, vs)
+    if gdtype != dtype:
+        raise ValueError("grad_shards must have the shards' dtype")
+    code = load_library().vpce_logprob_backward(_ptr_array([sh.data_ptr() for sh in shards]), dtype, len(shards), s,
+                                                _i64_array(vs), ld, _addr(targets), ignore_index, temperature,
+                                                _addr(stats), _addr(grad_logp), _addr(grad_entropy), top,
+                                                _addr(top_ids), _addr(grad_top_logp),
+                                                _ptr_array([g.data_ptr() for g in grad_shards]), ld_grad,
+                                                _stream_ptr(stream))
+    if code != VPCE_OK:
+        raise VPCEError(code, "vpce_logprob_backward")
+    return grad_shards
+
+
+# ----------------------------------------------------------------------------
+# scaled embedding lookup with dropout
+# ----------------------------------------------------------------------------
+def _check_rng(rng):
+    import torch
+
+    if rng is not None and (rng.dtype != torch.int64 or not rng.is_cuda or rng.numel() != 2
+                            or not rng.is_contiguous()):
+        raise ValueError("rng must be a CUDA int64 tensor of two elements (seed, offset)")
+
+
+def _check_ids(ids, s=None):
+    import torch
+
+    if ids.dtype != torch.int64 or not ids.is_cuda or ids.dim() != 1 or not ids.is_contiguous() \
+            or (s is not None and ids.numel() != s):
+        raise ValueError("ids must be a contiguous 1-D CUDA int64 tensor, one entry per row")
+
+
+def _row_stride(x, h):
+    return x.stride(0) if x.shape[0] > 1 else h
+
+
+def vpce_embedding_dropout_forward(table_shards, ids, vocab_start=None, *, scale: float = 1.0, p: float = 0.0,
+                                   rng=None, padding_id=None, out=None, out_dtype=None, flag=None, stream=None):
+    """Rows ``scale * dropout(table[ids], p)`` of a vocabulary-split table.
+    ``rng`` (CUDA int64 ``[seed, offset]``) keys the mask, which is a function
+    of (seed, offset, row, column) and never stored: pass the same words to
+    :func:`vpce_embedding_dropout_backward`, and other ones to the next call.
+    ``padding_id`` (None: none) gives zero rows; other ids outside [0, V) give
+    zero rows and bit 0 of ``flag``.  The output is ``out_dtype`` (the table's
+    by default)."""
+    import torch
+
+    dtype, h, ld, vs = _table_desc(table_shards, vocab_start)
+    if dtype is None:
+        raise TypeError("table dtype must be bf16 or fp32")
+    _check_ids(ids)
+    _check_rng(rng)
+    _check_flag(flag)
+    s = ids.numel()
+    if out is None:
+        out = torch.empty((s, h), dtype=out_dtype or table_shards[0].dtype, device=ids.device)
+    elif out.dim() != 2 or tuple(out.shape) != (s, h) or not out.is_cuda or (h > 1 and out.stride(1) != 1):
+        raise ValueError("out must be a CUDA [s, h] tensor with contiguous columns")
+    elif out_dtype is not None and out.dtype != out_dtype:
+        raise TypeError("out is not of out_dtype")
+    odt = {torch.bfloat16: VPCE_BF16, torch.float32: VPCE_FP32}.get(out.dtype)
+    if odt is None:
+        raise TypeError("out dtype must be bf16 or fp32")
+    code = load_library().vpce_embedding_dropout_forward(
+        _ptr_array([e.data_ptr() for e in table_shards]), dtype, len(table_shards), _i64_array(vs), h, ld,
+        _addr(ids), s, INT64_MIN if padding_id is None else int(padding_id), scale, p, _addr(rng), _addr(out), odt,
+        _row_stride(out, h), _addr(flag), _stream_ptr(stream))
+    if code != VPCE_OK:
+        raise VPCEError(code, "vpce_embedding_dropout_forward")
+    return out
+
+
+def vpce_embedding_dropout_backward_workspace_bytes(s: int, V: int, h: int) -> int:
+    return int(load_library().vpce_embedding_dropout_backward_workspace_bytes(int(s), int(V), int(h)))
+
+
+def vpce_embedding_dropout_backward(grad_out, ids, grad_shards, vocab_start=None, *, scale: float = 1.0,
+                                    p: float = 0.0, rng=None, padding_id=None, accumulate: bool = True,
+                                    workspace=None, stream=None):
+    """Gradient of :func:`vpce_embedding_dropout_forward` with respect to the
+    table, into the fp32 ``grad_shards`` (in place): added to what they hold,
+    or, with ``accumulate=False``, written in full (zero rows for ids that do
+    not occur).  ``scale``, ``p``, ``rng`` and ``padding_id`` are the
+    forward's."""
+    import torch
+
+    gdt, h, ld, vs = _table_desc(grad_shards, vocab_start)
+    if gdt != VPCE_FP32:
+        raise TypeError("gradient table shards must be fp32")
+    if grad_out.dim() != 2 or grad_out.shape[1] != h or not grad_out.is_cuda or (h > 1 and grad_out.stride(1) != 1):
+        raise ValueError("grad_out must be a CUDA [s, h] tensor with contiguous columns")
+    code_dt = {torch.bfloat16: VPCE_BF16, torch.float32: VPCE_FP32}.get(grad_out.dtype)
+    if code_dt is None:
+        raise TypeError("grad_out dtype must be bf16 or fp32")
+    s = grad_out.shape[0]
+    _check_ids(ids, s)
+    _check_rng(rng)
+    lib = load_library()
+    if workspace is None:
+        workspace = torch.empty(lib.vpce_embedding_dropout_backward_workspace_bytes(s, vs[-1], h), dtype=torch.uint8,
+                                device=ids.device)
+    code = lib.vpce_embedding_dropout_backward(
+        _addr(grad_out), code_dt, _row_stride(grad_out, h), _addr(ids), s,
+        INT64_MIN if padding_id is None else int(padding_id), scale, p, _addr(rng),
+        _ptr_array([g.data_ptr() for g in grad_shards]), len(grad_shards), _i64_array(vs), h, ld,
+        int(bool(accumulate)), _addr(workspace), workspace.numel(), _stream_ptr(stream))
+    if code != VPCE_OK:
+        raise VPCEError(code, "vpce_embedding_dropout_backward")
     return grad_shards
