@@ -483,7 +483,7 @@ vpce_status vpce_embedding_backward(const void* grad_out, vpce_dtype grad_dtype,
  *                    target outside [0, V) gives logp NaN; the row's other
  *                    outputs do not depend on the target.  Without targets
  *                    every row is scored.
- *   temperature      > 0, finite, with a finite inverse.
+ *   temperature      1e-30 .. 1e30.
  *   top              0..VPCE_MAX_TOP alternatives, at most V.
  *   logp_out, entropy_out   device float[s], or NULL.
  *   top_ids_out      device int64[s][top]; required when top > 0, else NULL.

@@ -797,10 +797,9 @@ vpce_status vpce_embedding_backward(const void* grad_out, vpce_dtype grad_dtype,
   return e == cudaSuccess ? VPCE_OK : VPCE_ERR_CUDA;
 }
 
-// The scores' temperature: positive, with a finite inverse.
-static bool good_temperature(float temperature) {
-  return std::isfinite(temperature) && temperature > 0.f && std::isfinite(1.442695041f / temperature);
-}
+// The scores' temperature: far enough from 0 and infinity that a masked
+// logit's distance from the others stays a masked one after the division.
+static bool good_temperature(float temperature) { return temperature >= 1e-30f && temperature <= 1e30f; }
 
 vpce_status vpce_logprob_forward(const void* const* shards, vpce_dtype dtype, int t, int64_t s,
                                  const int64_t* vocab_start, int64_t ld, const int64_t* targets,

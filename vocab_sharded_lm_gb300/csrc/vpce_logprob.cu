@@ -1,25 +1,29 @@
 // Log probabilities of given tokens, entropy and top alternatives of rows of
 // vocabulary-sharded logits, in one pass.
 //
-// With m the row's largest z and v_k = (z_k - m) log2(e) / T,
+// With c = log2(e) / T and an offset K = c max_k z_k as rounded to fp32,
+//     v_k = c z_k - K (one fused multiply-add, one rounding),
 //     S = sum_k 2^v_k,  U = sum_k v_k 2^v_k,
-//     logp_y = (z_y - m) / T - ln S,  entropy = ln S - ln2 U / S.
-// v is formed by subtracting first: bf16 logits subtract exactly, and rows
-// filled with the type's lowest finite value stay finite.  v is clamped at
-// -256, where 2^v is 0 in fp32, so a column at -inf adds 0 (not 0 * inf).
+//     entropy = ln S - ln2 U / S,   logp_y = (z_y - max) / T - ln S',
+// where ln S' = ln S + ln2 (K - c max) is the sum relative to the largest
+// logit itself.  Any offset gives the same entropy and probabilities, so K's
+// own rounding costs nothing.  Logits below -2^21 / c enter at that floor,
+// where 2^v is 0: a column at -inf adds 0 and not 0 * inf.  Rows whose largest
+// logit is itself 2^20 / c or more from 0 (filled with the type's lowest value,
+// say) are summed again by subtraction (sum_far).
 //
 // A row is cut into pieces (part of one shard, 16-byte vectors).  The warp
 // that takes a piece streams it into registers and leaves, per lane, (max, S,
 // U) of the vectors that lane read.  The warp that completes a row folds these
 // in a fixed order whatever warp made them, so results repeat bit for bit.
 //
-// Top alternatives without a second pass: a lane's maximum over its share of
-// a piece (its batch) is in the partials already.  The top-th largest of 64
-// batch-group maxima bounds the top-th largest logit from below, so every
-// alternative lies in a batch whose maximum reaches the bound: some 20 to 45
-// batches of a row's 1000, re-read while they are still in L2.  Candidates
-// are 64-bit words (order-preserving key of the value, complement of the
-// column), so one comparison ranks by value, then lowest column.
+// Top alternatives without a second pass: the maxima of a lane's quarters of a
+// piece (batches of 4 vectors a step) are kept with the partials.  The top-th
+// largest of 128 group maxima bounds the top-th largest logit from below, so
+// every alternative lies in a batch whose maximum reaches the bound: about
+// `top` batches of a row's 4000, re-read in one round trip.  Candidates are
+// 64-bit words (order-preserving key of the value, complement of the column),
+// so one comparison ranks by value, then lowest column.
 #include <cooperative_groups.h>
 
 #include "vpce_logprob.cuh"
@@ -30,43 +34,40 @@ namespace {
 
 namespace cg = cooperative_groups;
 
-constexpr int kLpThreads = 256;
-constexpr int kLpWarps = kLpThreads / 32;
-constexpr int kLpMaxPieces = 64;   // pieces per row
-constexpr int kLpSlots = 3;        // rows with partials in shared memory at a time
+constexpr int kLpStream = 12;      // warps that stream pieces
+constexpr int kLpFinish = 4;       // warps that finish rows
+constexpr int kLpThreads = 32 * (kLpStream + kLpFinish);  // one CTA per SM
+constexpr int kLpMaxPieces = 64;   // pieces per row (as many as shards can be)
+constexpr int kLpPieces = 40;      // aimed at: leaves room for 6 rows' partials
+constexpr int kLpMaxSlots = 8;     // rows with partials in shared memory at a time, at most
+constexpr int kLpPartBytes = 32 * int(sizeof(float4) + 2 * sizeof(float));  // a piece's partials
+constexpr int kLpPartSmem = 192 * 1024;
 constexpr int kLpCand = 128;       // candidate words per warp
-constexpr int kLpList = 64;        // batches listed per warp before they are re-read
-constexpr float kLpFloor = -256.f;
+constexpr int kLpList = 128;       // batches listed per warp before they are re-read
+constexpr float kLpFloor = -256.f;      // 2^v is 0 here
+constexpr float kLpFar = 1048576.f;      // |K| from here on: K's rounding is no longer small (sum_far)
 
 template <typename T> struct LpShape;
-template <> struct LpShape<__nv_bfloat16> {
-  static constexpr int kVecs = 16;
-  static constexpr int kCtas = 2;
-};
-template <> struct LpShape<float> {
-  static constexpr int kVecs = 12;
-  static constexpr int kCtas = 2;
-};
+template <> struct LpShape<__nv_bfloat16> { static constexpr int kVecs = 16; };
+template <> struct LpShape<float> { static constexpr int kVecs = 16; };
 
-// How a row is cut: piece i covers vectors [off, off + len) of its shard's
-// 16-byte aligned body; the shard's first piece also takes the elements
-// before and after the body.
-struct LpPlan {
-  int pieces;      // per row
-  int len;         // vectors per piece: a multiple of 32 U
-};
-
-struct Piece {
-  int shard;
+// Part of a row: vectors [off, off + p.len) of its shard's 16-byte aligned
+// body; the shard's first piece also takes the elements before and after the
+// body.
+struct __align__(16) Piece {
+  const unsigned char* base;  // the shard
+  long long ld;               // its row stride in bytes
+  unsigned bytes;             // of a row
+  int col;                    // its first column
   int off;
+  int pad;
 };
 
-struct LpSmem {
-  float* m;            // [slots][pieces][32]
-  float* s;
-  float* u;
-  unsigned long long (*cand)[kLpCand];
-  unsigned short (*list)[kLpList];
+// A warp's room for finding a row's alternatives.
+struct Scratch {
+  unsigned long long cand[kLpCand];
+  unsigned short list[kLpList];
+  int n;
 };
 
 __device__ __forceinline__ float lane_max(const uint4& v, __nv_bfloat16) {
@@ -79,7 +80,7 @@ __device__ __forceinline__ float lane_max(const uint4& v, float) {
                  max_nan(__uint_as_float(v.z), __uint_as_float(v.w)));
 }
 template <int U>
-__device__ __forceinline__ float vecs_max(const uint4 (&q)[U], __nv_bfloat16) {
+__device__ __forceinline__ float vecs_max(const uint4* q, __nv_bfloat16) {
   const __nv_bfloat162* b = reinterpret_cast<const __nv_bfloat162*>(q);
   __nv_bfloat162 x = b[0];
 #pragma unroll
@@ -87,7 +88,7 @@ __device__ __forceinline__ float vecs_max(const uint4 (&q)[U], __nv_bfloat16) {
   return max_nan(__low2float(x), __high2float(x));
 }
 template <int U>
-__device__ __forceinline__ float vecs_max(const uint4 (&q)[U], float) {
+__device__ __forceinline__ float vecs_max(const uint4* q, float) {
   float x = lane_max(q[0], 0.f);
 #pragma unroll
   for (int j = 1; j < U; ++j) x = max_nan(x, lane_max(q[j], 0.f));
@@ -101,40 +102,53 @@ __device__ __forceinline__ uint4 lp_pad(float) {
   return make_uint4(0xff800000u, 0xff800000u, 0xff800000u, 0xff800000u);
 }
 
-// A lane's running maximum and sums.
+// The offset of a maximum: c m, never below -2^20 (which a NaN, or nothing
+// unmasked, gives).  Rounded here: a product fused into a later difference
+// would not be the offset that the sums were formed with.
+__device__ __forceinline__ float offset_of(float m, float c) { return fmaxf(__fmul_rn(m, c), -kLpFar); }
+
+// A lane's running offset and sums.
 struct Acc {
-  float m, s, u;
-  // move the maximum up to nm: 2^v and v 2^v of every term change by the same
-  // shift (v' = v + d).  fmaxf turns the NaN of (-inf) - (-inf) into the floor.
-  __device__ __forceinline__ void raise(float nm, float c) {
-    const float d = fmaxf((m - nm) * c, kLpFloor);
+  float k, s, u;
+  // move the offset up to nk: every v changes by the same shift
+  __device__ __forceinline__ void raise(float nk) {
+    const float d = fmaxf(k - nk, kLpFloor);
     const float e = ex2(d);
     u = fmaf(s, d, u) * e;
     s *= e;
-    m = nm;
+    k = nk;
   }
 };
 
-__device__ __forceinline__ void add_pair(float x0, float x1, f32x2 nm, f32x2 c, f32x2& s, f32x2& u) {
+__device__ __forceinline__ void add_pair(float x0, float x1, f32x2 c, f32x2 nk, f32x2& s, f32x2& u) {
+  const f32x2 v = f2_fma(f2_pack(x0, x1), c, nk);
   float a, b;
-  f2_unpack(f2_mul(f2_add(f2_pack(x0, x1), nm), c), a, b);
-  a = fmaxf(a, kLpFloor);
-  b = fmaxf(b, kLpFloor);
+  f2_unpack(v, a, b);
   const f32x2 e = f2_pack(ex2(a), ex2(b));
   s = f2_add(s, e);
-  u = f2_fma(f2_pack(a, b), e, u);
+  u = f2_fma(v, e, u);
 }
-__device__ __forceinline__ void add_vec(const uint4& v, f32x2 nm, f32x2 c, f32x2 (&s)[2], f32x2 (&u)[2],
-                                        __nv_bfloat16) {
-  add_pair(bf16_lo(v.x), bf16_hi(v.x), nm, c, s[0], u[0]);
-  add_pair(bf16_lo(v.y), bf16_hi(v.y), nm, c, s[1], u[1]);
-  add_pair(bf16_lo(v.z), bf16_hi(v.z), nm, c, s[0], u[0]);
-  add_pair(bf16_lo(v.w), bf16_hi(v.w), nm, c, s[1], u[1]);
+// logits are raised to `low` first (bf16: two at a time)
+__device__ __forceinline__ void add_vec(const uint4& v, __nv_bfloat162 low, f32x2 c, f32x2 nk, f32x2 (&s)[2],
+                                        f32x2 (&u)[2], __nv_bfloat16) {
+  const unsigned w[4] = {v.x, v.y, v.z, v.w};
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    const __nv_bfloat162 h = __hmax2(*reinterpret_cast<const __nv_bfloat162*>(&w[i]), low);
+    const unsigned q = *reinterpret_cast<const unsigned*>(&h);
+    add_pair(bf16_lo(q), bf16_hi(q), c, nk, s[i & 1], u[i & 1]);
+  }
 }
-__device__ __forceinline__ void add_vec(const uint4& v, f32x2 nm, f32x2 c, f32x2 (&s)[2], f32x2 (&u)[2], float) {
-  add_pair(__uint_as_float(v.x), __uint_as_float(v.y), nm, c, s[0], u[0]);
-  add_pair(__uint_as_float(v.z), __uint_as_float(v.w), nm, c, s[1], u[1]);
+__device__ __forceinline__ void add_vec(const uint4& v, float low, f32x2 c, f32x2 nk, f32x2 (&s)[2], f32x2 (&u)[2],
+                                        float) {
+  add_pair(fmaxf(__uint_as_float(v.x), low), fmaxf(__uint_as_float(v.y), low), c, nk, s[0], u[0]);
+  add_pair(fmaxf(__uint_as_float(v.z), low), fmaxf(__uint_as_float(v.w), low), c, nk, s[1], u[1]);
 }
+// the floor of a logit
+__device__ __forceinline__ __nv_bfloat162 low_of(float c, __nv_bfloat16) {
+  return __float2bfloat162_rn(-2.f * kLpFar / c);
+}
+__device__ __forceinline__ float low_of(float c, float) { return -2.f * kLpFar / c; }
 
 // The row segment of a shard: 16-byte aligned body and ragged ends.
 struct Seg {
@@ -142,13 +156,14 @@ struct Seg {
   int head, nv, tail;  // elements before the body, vectors in it, elements after
 };
 template <typename T>
-__device__ __forceinline__ Seg segment(const LogprobParams& p, int shard, long long row) {
-  const Unit g = make_unit_at(p.sh, shard, row, Elem<T>::kBytes);
+__device__ __forceinline__ Seg segment(const Piece& pc, long long row) {
   Seg q;
-  q.addr = g.addr;
-  q.head = int(g.head) / Elem<T>::kBytes;
-  q.nv = int(g.body >> 4);
-  q.tail = int(g.tail) / Elem<T>::kBytes;
+  q.addr = pc.base + row * pc.ld;
+  const unsigned off = unsigned(reinterpret_cast<uintptr_t>(q.addr)) & 15u;
+  const unsigned head = min((16u - off) & 15u, pc.bytes), rest = pc.bytes - head;
+  q.head = int(head) / Elem<T>::kBytes;
+  q.nv = int(rest >> 4);
+  q.tail = int(rest & 15u) / Elem<T>::kBytes;
   return q;
 }
 template <typename T>
@@ -164,15 +179,20 @@ __device__ __forceinline__ int ragged_column(const Seg& q, int l) {
   return -1;
 }
 
-// One piece by one warp: the lane's (max, S, U).
+// vectors per batch and step
+template <typename T> constexpr int kLpBatch = LpShape<T>::kVecs / 4;
+
+// One piece by one warp: the lane's (max, S, U), and the maxima of its batches.
 template <typename T, int U>
 __device__ __forceinline__ Acc piece_stats(const LogprobParams& p, const Piece& pc, int len, long long row, float c,
-                                           int lane) {
-  const Seg g = segment<T>(p, pc.shard, row);
+                                           int lane, float4& bm) {
+  const Seg g = segment<T>(pc, row);
   const uint4* v = body<T>(g);
-  Acc a{-INFINITY, 0.f, 0.f};
+  Acc a{-kLpFar, 0.f, 0.f};
+  bm = make_float4(-INFINITY, -INFINITY, -INFINITY, -INFINITY);
   const int end = min(pc.off + len, g.nv);
   const f32x2 cc = f2_pack(c, c);
+  const auto low = low_of(c, T());
 #pragma unroll 1
   for (int base = pc.off; base < end; base += 32 * U) {
     uint4 q[U];
@@ -181,29 +201,58 @@ __device__ __forceinline__ Acc piece_stats(const LogprobParams& p, const Piece& 
       const int i = base + lane + 32 * j;
       q[j] = i < end ? __ldcs(v + i) : lp_pad(T());
     }
-    const float cm = vecs_max<U>(q, T());
-    if (!(cm <= a.m)) a.raise(max_nan(a.m, cm), c);
-    const f32x2 nm = f2_pack(-a.m, -a.m);
+    bm.x = max_nan(bm.x, vecs_max<U / 4>(q, T()));
+    bm.y = max_nan(bm.y, vecs_max<U / 4>(q + U / 4, T()));
+    bm.z = max_nan(bm.z, vecs_max<U / 4>(q + U / 2, T()));
+    bm.w = max_nan(bm.w, vecs_max<U / 4>(q + 3 * (U / 4), T()));
+    const float nk = offset_of(max_nan(max_nan(bm.x, bm.y), max_nan(bm.z, bm.w)), c);
+    if (nk > a.k) a.raise(nk);
+    const f32x2 off = f2_pack(-a.k, -a.k);
     f32x2 s[2] = {f2_pack(a.s, 0.f), f2_pack(0.f, 0.f)}, u[2] = {f2_pack(a.u, 0.f), f2_pack(0.f, 0.f)};
 #pragma unroll
-    for (int j = 0; j < U; ++j) add_vec(q[j], nm, cc, s, u, T());
+    for (int j = 0; j < U; ++j) add_vec(q[j], low, cc, off, s, u, T());
     float x0, x1;
     f2_unpack(f2_add(s[0], s[1]), x0, x1);
     a.s = x0 + x1;
     f2_unpack(f2_add(u[0], u[1]), x0, x1);
     a.u = x0 + x1;
   }
-  if (pc.off == 0) {
+  if (pc.off == 0 && (g.head | g.tail) != 0) {
     const int col = ragged_column<T>(g, lane);
     if (col >= 0) {
       const float x = Elem<T>::load(g.addr + (long long)col * Elem<T>::kBytes);
-      if (!(x <= a.m)) a.raise(max_nan(a.m, x), c);
-      const float w = fmaxf((x - a.m) * c, kLpFloor), e = ex2(w);
+      bm.x = max_nan(bm.x, x);
+      const float nk = offset_of(x, c);
+      if (nk > a.k) a.raise(nk);
+      const float w = fmaf(fmaxf(x, low_of(c, 0.f)), c, -a.k), e = ex2(w);
       a.s += e;
       a.u = fmaf(w, e, a.u);
     }
   }
   return a;
+}
+
+// S and U of a row relative to its largest logit M, by subtraction, for rows
+// whose logits are too large for the offset form (one warp; rare).
+template <typename T>
+__device__ __noinline__ float2 sum_far(const LogprobParams& p, long long row, float M, float c, int lane) {
+  float S = 0.f, W = 0.f;
+  for (int i = 0; i < p.t; ++i) {
+    const unsigned char* at = p.sh.ptr[i] + row * p.sh.ld_bytes[i];
+    const long long n = p.sh.start[i + 1] - p.sh.start[i];
+    for (long long k = lane; k < n; k += 32) {
+      const float v = fmaxf((Elem<T>::load(at + k * Elem<T>::kBytes) - M) * c, kLpFloor);
+      const float e = ex2(v);
+      S += e;
+      W = fmaf(v, e, W);
+    }
+  }
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) {
+    S += __shfl_xor_sync(kFull, S, o);
+    W += __shfl_xor_sync(kFull, W, o);
+  }
+  return make_float2(S, W);
 }
 
 // ---------------------------------------------------------------------------
@@ -214,6 +263,28 @@ __device__ __forceinline__ float key_value(unsigned k) {
   return __uint_as_float(k & 0x80000000u ? k & 0x7fffffffu : ~k);
 }
 
+// Sorts n candidates (at most 32 W) and keeps the first `top`, in place.
+template <int W>
+__device__ __forceinline__ void rank_words(unsigned long long* cand, int n, int top, int lane) {
+  unsigned long long w[W];
+  int rank[W];
+#pragma unroll
+  for (int i = 0; i < W; ++i) {
+    w[i] = lane + 32 * i < n ? cand[lane + 32 * i] : 0ull;
+    rank[i] = 0;
+  }
+  for (int j = 0; j < n; ++j) {
+    const unsigned long long x = cand[j];
+#pragma unroll
+    for (int i = 0; i < W; ++i) rank[i] += x > w[i];
+  }
+  __syncwarp();
+#pragma unroll
+  for (int i = 0; i < W; ++i)
+    if (lane + 32 * i < n && rank[i] < top) cand[rank[i]] = w[i];
+  __syncwarp();
+}
+
 // The candidates of one warp: cand[0 .. n) hold the words seen so far that
 // beat `floor`; when full they are cut to the `top` best.
 struct Best {
@@ -222,25 +293,9 @@ struct Best {
   int n, top;
 
   // sorts cand[0 .. n) descending and keeps the first `top`
-  __device__ __noinline__ void cut(int lane) {
+  __device__ __forceinline__ void cut(int lane) {
     __syncwarp();
-    unsigned long long w[kLpCand / 32];
-    int rank[kLpCand / 32];
-#pragma unroll
-    for (int i = 0; i < kLpCand / 32; ++i) {
-      w[i] = lane + 32 * i < n ? cand[lane + 32 * i] : 0ull;
-      rank[i] = 0;
-    }
-    for (int j = 0; j < n; ++j) {
-      const unsigned long long x = cand[j];
-#pragma unroll
-      for (int i = 0; i < kLpCand / 32; ++i) rank[i] += x > w[i];
-    }
-    __syncwarp();
-#pragma unroll
-    for (int i = 0; i < kLpCand / 32; ++i)
-      if (lane + 32 * i < n && rank[i] < top) cand[rank[i]] = w[i];
-    __syncwarp();
+    rank_words<kLpCand / 32>(cand, n, top, lane);
     if (n >= top) {
       n = top;
       floor = cand[top - 1];
@@ -264,103 +319,92 @@ __device__ __forceinline__ unsigned long long word(unsigned key, unsigned col) {
   return ((unsigned long long)key << 32) | (unsigned)~col;
 }
 
-// The `top` best columns of a row, sorted, into best.cand[0 .. top).  m: the
-// row's batch maxima [pieces][32].
+// One batch of a row: number (piece, quarter, lane) as 128 piece + 32 quarter
+// + lane.  Lane l (0..3) of the four that re-read it takes vector l of the
+// batch's four in every step; lane 0 also takes the ragged element.
 template <typename T, int U>
-__device__ __forceinline__ void find_top(const LogprobParams& p, const LpPlan& plan, const Piece* piece,
-                                         const float* m, long long row, Best& best, unsigned short* list, int lane) {
+struct Batch {
+  const uint4* src;            // the lane's vector of step 0
+  int left, col;               // steps it has a vector in; its first column
+  const unsigned char* rag;    // ragged element or null
+  int ragcol;
+  __device__ __forceinline__ void at(const LogprobParams& p, const Piece* piece, long long row,
+                                     int code, int l) {
+    const Piece pc = piece[code >> 7];
+    const Seg g = segment<T>(pc, row);
+    const int quarter = (code >> 5) & 3;
+    const int first = pc.off + (code & 31) + 32 * (quarter * (U / 4) + l);
+    const int end = min(pc.off + p.len, g.nv);
+    left = end > first ? (end - first + 32 * U - 1) / (32 * U) : 0;
+    src = body<T>(g) + first;
+    col = pc.col + g.head + first * Elem<T>::kPerVec;
+    if (pc.off == 0 && l == 0 && quarter == 0) {
+      const int rc = ragged_column<T>(g, code & 31);
+      if (rc >= 0) {
+        rag = g.addr + (long long)rc * Elem<T>::kBytes;
+        ragcol = rc + pc.col;
+      }
+    }
+  }
+};
+
+__device__ __forceinline__ float quarter_max(const float4& b, int i) {
+  return i < 2 ? (i == 0 ? b.x : b.y) : (i == 2 ? b.z : b.w);
+}
+
+// The `top` best columns of a row, sorted, into w.cand[0 .. top), for any row:
+// batches that may beat the worst of the best so far are re-read in order, and
+// a full candidate buffer is cut to the best.  Rows with many equal logits
+// come here.
+template <typename T, int U>
+__device__ __noinline__ void find_top_any(const LogprobParams& p, const Piece* piece,
+                                          const float4* bm, long long row, unsigned bound, Scratch& w, int lane) {
   constexpr int EPV = Elem<T>::kPerVec;
-  // lower bound: the top-th largest of the maxima of 64 groups of batches
-  // (lane, piece parity)
-  unsigned a = 0, b = 0;
-  for (int i = 0; i < plan.pieces; i += 2) {
-    a = max(a, value_key(m[i * 32 + lane]));
-    if (i + 1 < plan.pieces) b = max(b, value_key(m[(i + 1) * 32 + lane]));
-  }
-  unsigned bound = 0;
-  for (int seen = 0; seen < p.top;) {
-    bound = __reduce_max_sync(kFull, max(a, b));
-    seen += __popc(__ballot_sync(kFull, a == bound)) + __popc(__ballot_sync(kFull, b == bound));
-    if (a == bound) a = 0;
-    if (b == bound) b = 0;
-    if (bound == 0) break;
-  }
+  Best best;
+  best.cand = w.cand;
   best.n = 0;
   best.top = p.top;
   // a word beats the floor if its key is at least `bound`
   best.floor = ((unsigned long long)bound << 32) > 0 ? ((unsigned long long)bound << 32) - 1 : 0ull;
-
-  int i = 0, listed = 0;
-  while (true) {
-    // list the batches that may hold a word above the floor
-    while (i < plan.pieces && listed + 32 <= kLpList) {
-      const bool in = word(value_key(m[i * 32 + lane]), 0) > best.floor;
-      const unsigned mk = __ballot_sync(kFull, in);
-      if (in) list[listed + __popc(mk & ((1u << lane) - 1u))] = (unsigned short)(i * 32 + lane);
-      listed += __popc(mk);
-      ++i;
-    }
-    __syncwarp();
-    if (listed == 0) break;
-    // re-read them: half a warp per batch, four batches per half in flight
-    const int half = lane >> 4, hl = lane & 15;
-    for (int l0 = 0; l0 < listed; l0 += 8) {
-      const uint4* src[4];
-      int left[4], col[4], rag[4];
-      Seg seg[4];
+  for (int i = 0; i < p.pieces; ++i) {
+    const float4 b = bm[i * 32 + lane];
+    for (int quarter = 0; quarter < 4; ++quarter) {
+      // the columns of a batch are no lower than its first vector's
+      const Piece pc = piece[i];
+      const unsigned low = unsigned(pc.col) +
+                           (pc.off == 0 ? 0u : unsigned(pc.off + 32 * quarter * (U / 4)) * EPV);
+      unsigned mk = __ballot_sync(kFull, word(value_key(quarter_max(b, quarter)), low) > best.floor);
+      while (mk != 0) {
+        // eight batches at a time, lowest lanes first
+        int code = -1;
+        for (int k = 0; k < 8 && mk != 0; ++k) {
+          const int l = __ffs(mk) - 1;
+          mk &= mk - 1;
+          if ((lane >> 2) == k) code = i * 128 + quarter * 32 + l;
+        }
+        Batch<T, U> bt;
+        bt.left = 0;
+        bt.rag = nullptr;
+        bt.src = nullptr;
+        bt.col = bt.ragcol = 0;
+        if (code >= 0) bt.at(p, piece, row, code, lane & 3);
+        for (int step = 0; __any_sync(kFull, step < bt.left); ++step) {
+          const bool has = step < bt.left;
+          const uint4 q = has ? bt.src[step * 32 * U] : lp_pad(T());
+          float x[EPV];
+          unpack(q, x, T());
+#pragma unroll 1
+          for (int e = 0; e < EPV; ++e) {
+            float xe = x[0];
 #pragma unroll
-      for (int k = 0; k < 4; ++k) {
-        const int l = l0 + 2 * k + half;
-        const int code = l < listed ? list[l] : -1;
-        left[k] = 0;
-        rag[k] = -1;
-        col[k] = 0;
-        src[k] = nullptr;
-        if (code >= 0) {
-          const Piece pc = piece[code >> 5];
-          seg[k] = segment<T>(p, pc.shard, row);
-          const int bl = code & 31, first = pc.off + bl + 32 * hl;
-          const int end = min(pc.off + plan.len, seg[k].nv);
-          left[k] = end > first ? (end - first + 511) / 512 : 0;
-          src[k] = body<T>(seg[k]) + first;
-          col[k] = int(p.sh.start[pc.shard]) + seg[k].head + first * EPV;
-          if (pc.off == 0 && hl == 0) {
-            const int rc = ragged_column<T>(seg[k], bl);
-            if (rc >= 0) rag[k] = rc + int(p.sh.start[pc.shard]);
-            if (rc >= 0) seg[k].addr += (long long)rc * Elem<T>::kBytes;
+            for (int f = 1; f < EPV; ++f) xe = e == f ? x[f] : xe;
+            best.offer(has ? word(value_key(xe), unsigned(bt.col + step * 32 * U * EPV + e)) : 0ull, lane);
           }
         }
-      }
-      // the vectors of a batch are 32 apart; lane hl takes every 16th of them
-      for (int step = 0;; ++step) {
-        uint4 q[4];
-        bool any = false;
-#pragma unroll
-        for (int k = 0; k < 4; ++k) {
-          q[k] = step < left[k] ? src[k][step * 512] : lp_pad(T());
-          any |= step < left[k];
-        }
-        if (!__any_sync(kFull, any)) break;
-#pragma unroll
-        for (int k = 0; k < 4; ++k) {
-          const bool has = step < left[k];
-          const unsigned vk = has ? value_key(lane_max(q[k], T())) : 0;
-          if (!__any_sync(kFull, has && word(vk, 0) > best.floor)) continue;
-          float x[EPV];
-          unpack(q[k], x, T());
-#pragma unroll
-          for (int e = 0; e < EPV; ++e)
-            best.offer(has ? word(value_key(x[e]), unsigned(col[k] + step * 512 * EPV + e)) : 0ull, lane);
-        }
-      }
-#pragma unroll
-      for (int k = 0; k < 4; ++k) {
-        if (!__any_sync(kFull, rag[k] >= 0)) continue;
-        best.offer(rag[k] >= 0 ? word(value_key(Elem<T>::load(seg[k].addr)), unsigned(rag[k])) : 0ull, lane);
+        const bool has = bt.rag != nullptr;
+        best.offer(has ? word(value_key(Elem<T>::load(bt.rag)), unsigned(bt.ragcol)) : 0ull, lane);
       }
     }
-    listed = 0;
-    __syncwarp();
   }
   best.cut(lane);
 }
@@ -380,10 +424,40 @@ __device__ __forceinline__ void write_ignored(const LogprobParams& p, long long 
   }
 }
 
+// The top-th largest key among the lanes' four values (sorted here).
+__device__ __forceinline__ unsigned bound_key(float4 x, int top) {
+  unsigned a = value_key(x.x), b = value_key(x.y), c = value_key(x.z), d = value_key(x.w);
+  auto order = [](unsigned& hi, unsigned& lo) {
+    const unsigned h = max(hi, lo);
+    lo = min(hi, lo);
+    hi = h;
+  };
+  order(a, b);
+  order(c, d);
+  order(a, c);
+  order(b, d);
+  order(b, c);
+  unsigned bound = 0;
+  for (int seen = 0; seen < top;) {
+    bound = __reduce_max_sync(kFull, a);
+    const bool mine = a == bound;
+    seen += __popc(__ballot_sync(kFull, mine));
+    if (mine) {
+      a = b;
+      b = c;
+      c = d;
+      d = 0;
+    }
+  }
+  return bound;
+}
+
 template <typename T, int U>
-__device__ __forceinline__ void finish_row(const LogprobParams& p, const LpPlan& plan, const Piece* piece,
-                                           const float* m, const float* s, const float* u, long long row, long long y,
-                                           unsigned long long* cand, unsigned short* list, int lane) {
+__device__ __forceinline__ void finish_row(const LogprobParams& p, const Piece* piece,
+                                           const float4* bm, const float* s, const float* u, long long row,
+                                           long long y, Scratch& w, int lane) {
+  constexpr int EPV = Elem<T>::kPerVec;
+  constexpr int kIn = 6;  // batches in flight per four lanes
   const float c = p.inv_t * kLog2e;
   const float nan = __int_as_float(0x7fc00000);
   const bool in = p.targets != nullptr && y >= 0 && y < p.V;
@@ -393,15 +467,29 @@ __device__ __forceinline__ void finish_row(const LogprobParams& p, const LpPlan&
     while (y >= p.sh.start[i + 1]) ++i;
     zy = Elem<T>::load(p.sh.ptr[i] + row * p.sh.ld_bytes[i] + (y - p.sh.start[i]) * Elem<T>::kBytes);
   }
-  // lanes fold their own partials in piece order, then the warp in a fixed tree
-  float M = -INFINITY;
-  for (int i = 0; i < plan.pieces; ++i) M = max_nan(M, m[i * 32 + lane]);
+  // maxima: of the lane's quarters over the pieces, and of the row
+  float4 x = make_float4(-INFINITY, -INFINITY, -INFINITY, -INFINITY);
+#pragma unroll 4
+  for (int i = 0; i < p.pieces; ++i) {
+    const float4 b = bm[i * 32 + lane];
+    x.x = max_nan(x.x, b.x);
+    x.y = max_nan(x.y, b.y);
+    x.z = max_nan(x.z, b.z);
+    x.w = max_nan(x.w, b.w);
+  }
+  float M = max_nan(max_nan(x.x, x.y), max_nan(x.z, x.w));
 #pragma unroll
   for (int o = 16; o > 0; o >>= 1) M = max_nan(M, __shfl_xor_sync(kFull, M, o));
+
+  // the sums: lanes fold their own partials in piece order, then
+  // the warp in a fixed tree
   float S = 0.f, W = 0.f;
-  for (int i = 0; i < plan.pieces; ++i) {
-    Acc a{m[i * 32 + lane], s[i * 32 + lane], u[i * 32 + lane]};
-    a.raise(M, c);
+  const float K = offset_of(M, c);
+#pragma unroll 4
+  for (int i = 0; i < p.pieces; ++i) {
+    const float4 b = bm[i * 32 + lane];
+    Acc a{offset_of(max_nan(max_nan(b.x, b.y), max_nan(b.z, b.w)), c), s[i * 32 + lane], u[i * 32 + lane]};
+    a.raise(K);
     S += a.s;
     W += a.u;
   }
@@ -410,130 +498,220 @@ __device__ __forceinline__ void finish_row(const LogprobParams& p, const LpPlan&
     S += __shfl_xor_sync(kFull, S, o);
     W += __shfl_xor_sync(kFull, W, o);
   }
+
+  // list the batches that reach the bound
+  unsigned bound = 0;
+  float floor = 0.f;
+  int listed = 0;
+  if (p.top > 0) {
+    bound = bound_key(x, p.top);
+    floor = key_value(bound);  // a NaN bound lists every batch
+    if (lane == 0) w.n = 0;
+    for (int i = 0; i < p.pieces; ++i) {
+      const float4 b = bm[i * 32 + lane];
+      const bool f[4] = {!(b.x < floor), !(b.y < floor), !(b.z < floor), !(b.w < floor)};
+      if (!__any_sync(kFull, f[0] | f[1] | f[2] | f[3])) continue;
+#pragma unroll
+      for (int k = 0; k < 4; ++k) {
+        const unsigned mk = __ballot_sync(kFull, f[k]);
+        const int at = listed + __popc(mk & ((1u << lane) - 1u));
+        if (f[k] && at < kLpList) w.list[at] = (unsigned short)(i * 128 + k * 32 + lane);
+        listed += __popc(mk);
+      }
+    }
+    __syncwarp();
+  }
+  const bool few = listed <= kLpList;
+  Batch<T, U> bt[kIn];
+  uint4 q[kIn];
+  auto fetch = [&](int l0) {
+#pragma unroll
+    for (int k = 0; k < kIn; ++k) {
+      const int l = l0 + 8 * k + (lane >> 2);
+      bt[k].left = 0;
+      if (l < listed) bt[k].at(p, piece, row, w.list[l], lane & 3);
+      q[k] = bt[k].left > 0 ? *bt[k].src : lp_pad(T());
+    }
+  };
+  if (p.top > 0 && few) fetch(0);
+
   // no finite largest logit (nothing unmasked, +inf or NaN): no distribution
   const bool ok = isfinite(M);
-  const float ls = ok ? logf(S) : nan;
-  const float ent = ok ? ls - 0.6931471806f * (W / S) : nan;
+  float shift = fmaf(-M, c, K);  // K - c M, the rounding of K
+  if (ok && !(fabsf(K) < kLpFar)) {
+    const float2 far = sum_far<T>(p, row, M, c, lane);
+    S = far.x;
+    W = far.y;
+    shift = 0.f;
+  }
+  const float ln2 = 0.6931471806f;
+  const float ls = ok ? logf(S) + ln2 * shift : nan;
+  const float ent = ok ? logf(S) - ln2 * (W / S) : nan;
   if (lane == 0) {
     if (p.entropy) p.entropy[row] = ent;
     if (p.stats) p.stats[row] = make_float4(M, ls, ent, 0.f);
     if (p.logp) p.logp[row] = in ? (zy - M) * p.inv_t - ls : nan;
     if (p.targets != nullptr && !in && p.flag != nullptr) atomicOr(p.flag, VPCE_FLAG_BAD_TARGET);
   }
-  if (p.top > 0) {
-    Best best;
-    best.cand = cand;
-    find_top<T, U>(p, plan, piece, m, row, best, list, lane);
-    if (lane < p.top) {
-      const unsigned long long w = best.cand[lane];
-      p.top_ids[row * p.top + lane] = (long long)unsigned(~unsigned(w));
-      if (p.top_logp) p.top_logp[row * p.top + lane] = (key_value(unsigned(w >> 32)) - M) * p.inv_t - ls;
+  if (p.top == 0) return;
+
+  int n = kLpCand + 1;
+  if (few) {
+    auto offer = [&](float v, int col) {
+      if (v < floor) return;
+      const int at = atomicAdd(&w.n, 1);
+      if (at < kLpCand) w.cand[at] = word(value_key(v), unsigned(col));
+    };
+    for (int l0 = 0;;) {
+      for (int step = 0;;) {
+#pragma unroll
+        for (int k = 0; k < kIn; ++k) {
+          if (step >= bt[k].left || lane_max(q[k], T()) < floor) continue;
+          float v[EPV];
+          unpack(q[k], v, T());
+#pragma unroll
+          for (int e = 0; e < EPV; ++e) offer(v[e], bt[k].col + step * 32 * U * EPV + e);
+        }
+        ++step;
+        if (step * 32 * U >= p.len) break;
+#pragma unroll
+        for (int k = 0; k < kIn; ++k) q[k] = step < bt[k].left ? bt[k].src[step * 32 * U] : lp_pad(T());
+      }
+      l0 += 8 * kIn;
+      if (l0 >= listed) break;
+      fetch(l0);
+    }
+    // the ragged elements of the listed batches that have one
+    for (int l = lane; l < listed; l += 32) {
+      Batch<T, U> b;
+      b.rag = nullptr;
+      b.at(p, piece, row, w.list[l], 0);
+      if (b.rag != nullptr) offer(Elem<T>::load(b.rag), b.ragcol);
     }
     __syncwarp();
+    n = *(volatile int*)&w.n;
   }
+  if (n <= 64) rank_words<2>(w.cand, n, p.top, lane);
+  else if (n <= kLpCand) rank_words<kLpCand / 32>(w.cand, n, p.top, lane);
+  else find_top_any<T, U>(p, piece, bm, row, bound, w, lane);
+  if (lane < p.top) {
+    const unsigned long long best = w.cand[lane];
+    p.top_ids[row * p.top + lane] = (long long)unsigned(~unsigned(best));
+    if (p.top_logp) p.top_logp[row * p.top + lane] = (key_value(unsigned(best >> 32)) - M) * p.inv_t - ls;
+  }
+  __syncwarp();
 }
 
 // The pieces of a row: every shard cut into ceil(vectors / len) of them, one
 // at least.  Thread 0 writes the table.
 template <typename T>
-__device__ __forceinline__ void cut_row(const LogprobParams& p, const LpPlan& plan, Piece* piece) {
+__device__ __forceinline__ void cut_row(const LogprobParams& p, Piece* piece) {
   int n = 0;
   for (int i = 0; i < p.t; ++i) {
     const int nv = int((p.sh.start[i + 1] - p.sh.start[i]) / Elem<T>::kPerVec);
-    for (int off = 0; off == 0 || off < nv; off += plan.len) piece[n++] = Piece{i, off};
+    for (int off = 0; off == 0 || off < nv; off += p.len)
+      piece[n++] = Piece{p.sh.ptr[i], p.sh.ld_bytes[i],
+                         unsigned(p.sh.start[i + 1] - p.sh.start[i]) * unsigned(Elem<T>::kBytes), int(p.sh.start[i]),
+                         off, 0};
   }
 }
 
-// Persistent form: a CTA per row at a time, its warps taking pieces from a
-// shared counter and running ahead into the next rows while one of them
-// finishes a row.  A row's partials stay in one of kLpSlots places.
+// Persistent form: a CTA per row at a time.  The streaming warps take pieces
+// from a shared counter, run ahead into the next rows and leave partials in
+// one of p.slots places; the finishing warps take the complete rows in turn.
+// Finishing a row is a chain of dependent steps (10 to 15 us, against 5.7 us
+// to stream a 256 KB row), so four rows are finished at a time; finished by
+// the streaming warps themselves, the same steps cost the stream its registers.
 template <typename T>
-__global__ void __launch_bounds__(kLpThreads, LpShape<T>::kCtas)
-    logprob_forward_kernel(const __grid_constant__ LogprobParams p, const LpPlan plan) {
+__global__ void __launch_bounds__(kLpThreads, 1)
+    logprob_forward_kernel(const __grid_constant__ LogprobParams p) {
   constexpr int U = LpShape<T>::kVecs;
   extern __shared__ __align__(16) unsigned char lp_smem[];
   __shared__ Piece piece[kLpMaxPieces];
-  __shared__ unsigned long long cand[kLpWarps][kLpCand];
-  __shared__ unsigned short list[kLpWarps][kLpList];
-  __shared__ int next;                      // pieces taken
-  __shared__ int done[kLpSlots];            // pieces of the slot's row that are complete
-  __shared__ volatile int finished[kLpSlots];  // rows finished in the slot
+  __shared__ Scratch scratch[kLpFinish];
+  __shared__ uint64_t full[kLpMaxSlots], empty[kLpMaxSlots];
+  __shared__ int next;  // pieces taken
   __shared__ volatile int stop;
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-  const int n = plan.pieces * 32;
-  float* sm = reinterpret_cast<float*>(lp_smem);
-  float* ss = sm + kLpSlots * n;
-  float* su = ss + kLpSlots * n;
+  const int n = p.pieces * 32;
+  float4* sm = reinterpret_cast<float4*>(lp_smem);
+  float* ss = reinterpret_cast<float*>(sm + p.slots * n);
+  float* su = ss + p.slots * n;
   if (threadIdx.x == 0) {
-    next = 0;
+    next = kLpStream;
     stop = 0;
-    for (int i = 0; i < kLpSlots; ++i) done[i] = finished[i] = 0;
-    cut_row<T>(p, plan, piece);
+    for (int i = 0; i < kLpMaxSlots; ++i) {
+      mbar_init(&full[i], p.pieces);
+      mbar_init(&empty[i], 1);
+    }
+    fence_mbar_init();
+    cut_row<T>(p, piece);
   }
   __syncthreads();
-  const float c = p.inv_t * kLog2e;
-  const long long rows = (p.s - blockIdx.x + gridDim.x - 1) / gridDim.x;  // this CTA's rows
-  while (true) {
-    int it = 0;
-    if (lane == 0) it = atomicAdd(&next, 1);
-    it = __shfl_sync(kFull, it, 0);
-    const long long k = it / plan.pieces;
-    if (k >= rows) break;
-    const int i = it - int(k) * plan.pieces;
-    const int slot = int(k % kLpSlots);
-    const long long row = blockIdx.x + k * gridDim.x;
-    const long long y = p.targets != nullptr ? __ldg(p.targets + row) : 0;
-    const bool ignored = p.targets != nullptr && y == p.ignore_index;
-    Acc a;
-    if (!ignored) a = piece_stats<T, U>(p, piece[i], plan.len, row, c, lane);
-    // the slot's earlier row has to be finished
-    const int turn = int(k / kLpSlots);
-    int go = 1;
-    if (lane == 0) {
-      if (finished[slot] < turn) {
-        const long long t0 = clock64();
-        while (finished[slot] < turn && !stop) {
-          if (clock64() - t0 > kWaitLimitCycles) stop = 1;
-          __nanosleep(100);
-        }
-        go = !stop;
+  const int rows = int((p.s - blockIdx.x + gridDim.x - 1) / gridDim.x);  // this CTA's rows
+  if (warp < kLpStream) {
+    const float c = p.inv_t * kLog2e;
+    // the piece in hand: number i of the CTA's row k; the next one is taken,
+    // and its row's target loaded, while this one streams
+    int taken = 0, i = warp, k = 0;
+    while (i >= p.pieces) {
+      i -= p.pieces;
+      ++k;
+    }
+    bool ignored = false;
+    if (p.targets != nullptr && k < rows)
+      ignored = __ldg(p.targets + blockIdx.x + (long long)k * gridDim.x) == p.ignore_index;
+    while (k < rows) {
+      if (lane == 0) taken = atomicAdd(&next, 1);
+      Acc a;
+      float4 bm;
+      if (!ignored)
+        a = piece_stats<T, U>(p, piece[i], p.len, blockIdx.x + (long long)k * gridDim.x, c, lane, bm);
+      const int slot = k % p.slots, turn = k / p.slots;
+      if (turn > 0 && !mbar_wait_warp(&empty[slot], (turn - 1) & 1)) {
+        stop = 1;
+        break;
       }
-      __threadfence_block();
+      if (!ignored) {
+        const int at = slot * n + i * 32 + lane;
+        sm[at] = bm;
+        ss[at] = a.s;
+        su[at] = a.u;
+      }
+      __syncwarp();
+      if (lane == 0) mbar_arrive_local(&full[slot]);
+      const int k0 = k;
+      i = __shfl_sync(kFull, taken, 0) - k * p.pieces;
+      while (i >= p.pieces) {
+        i -= p.pieces;
+        ++k;
+      }
+      if (p.targets != nullptr && k != k0 && k < rows)
+        ignored = __ldg(p.targets + blockIdx.x + (long long)k * gridDim.x) == p.ignore_index;
     }
-    if (!__shfl_sync(kFull, go, 0)) break;
-    __syncwarp();
-    if (!ignored) {
-      const int at = slot * n + i * 32 + lane;
-      sm[at] = a.m;
-      ss[at] = a.s;
-      su[at] = a.u;
-    }
-    __syncwarp();
-    int last = 0;
-    if (lane == 0) {
-      __threadfence_block();
-      last = atomicAdd(&done[slot], 1) == plan.pieces - 1;
-      __threadfence_block();
-    }
-    if (!__shfl_sync(kFull, last, 0)) continue;
-    __syncwarp();
-    if (ignored) write_ignored(p, row, lane);
-    else
-      finish_row<T, U>(p, plan, piece, sm + slot * n, ss + slot * n, su + slot * n, row, y, cand[warp], list[warp],
-                       lane);
-    __syncwarp();
-    if (lane == 0) {
-      done[slot] = 0;
-      __threadfence_block();
-      finished[slot] = turn + 1;
+  } else {
+    for (int k = warp - kLpStream; k < rows; k += kLpFinish) {
+      const long long row = blockIdx.x + (long long)k * gridDim.x;
+      const long long y = p.targets != nullptr ? __ldg(p.targets + row) : 0;
+      const int slot = k % p.slots;
+      if (!mbar_wait_warp(&full[slot], (k / p.slots) & 1)) {
+        stop = 1;
+        break;
+      }
+      if (p.targets != nullptr && y == p.ignore_index) write_ignored(p, row, lane);
+      else
+        finish_row<T, U>(p, piece, sm + slot * n, ss + slot * n, su + slot * n, row, y, scratch[warp - kLpStream],
+                         lane);
+      __syncwarp();
+      if (lane == 0) mbar_arrive_local(&empty[slot]);
     }
   }
   __syncthreads();
   if (stop) {  // a wait gave up: nothing of this CTA's rows is to be believed
     if (threadIdx.x == 0 && p.flag != nullptr) atomicOr(p.flag, VPCE_FLAG_WAIT_TIMEOUT);
     const float nan = __int_as_float(0x7fc00000);
-    for (long long k = threadIdx.x; k < rows; k += kLpThreads) {
-      const long long row = blockIdx.x + k * gridDim.x;
+    for (int k = threadIdx.x; k < rows; k += kLpThreads) {
+      const long long row = blockIdx.x + (long long)k * gridDim.x;
       if (p.logp) p.logp[row] = nan;
       if (p.entropy) p.entropy[row] = nan;
       if (p.stats) p.stats[row] = make_float4(nan, nan, nan, 0.f);
@@ -547,42 +725,38 @@ __global__ void __launch_bounds__(kLpThreads, LpShape<T>::kCtas)
 
 }  // namespace
 
+// One step (a warp's 32 U vectors) per piece, more when the row would have
+// too many pieces.
 template <typename T>
-static LpPlan plan_pieces(const LogprobParams& p, int limit) {
-  constexpr int kStep = 32 * LpShape<T>::kVecs;
-  LpPlan plan;
-  // one step per piece, more when the row would have too many pieces
-  for (long long steps = 1;; steps *= 2) {
-    const long long len = steps * kStep;
+static void cut_plan(LogprobParams& p, int limit) {
+  for (long long len = 32 * LpShape<T>::kVecs;; len *= 2) {
     long long n = 0;
     for (int i = 0; i < p.t; ++i) {
       const long long nv = (p.sh.start[i + 1] - p.sh.start[i]) / Elem<T>::kPerVec;
       n += nv > 0 ? (nv + len - 1) / len : 1;
     }
-    if (n <= limit) {
-      plan.pieces = int(n);
-      plan.len = int(len);
-      return plan;
+    if (n <= limit || n == p.t) {
+      p.pieces = int(n);
+      p.len = int(len);
+      return;
     }
   }
 }
 
 template <typename T>
-void launch_logprob_forward(const LogprobParams& p, int sms, cudaStream_t st) {
-  const LpPlan plan = plan_pieces<T>(p, kLpMaxPieces);
-  const long long cap = (long long)sms * LpShape<T>::kCtas;
-  // equal numbers of rows per CTA: with one row more than CTAs, half the CTAs
-  // and two rows each
-  const long long turns = (p.s + cap - 1) / cap;
-  const int grid = int((p.s + turns - 1) / turns);
-  const size_t smem = size_t(kLpSlots) * plan.pieces * 32 * 3 * sizeof(float);
-  logprob_forward_kernel<T><<<grid, kLpThreads, smem, st>>>(p, plan);
+void launch_logprob_forward(LogprobParams p, int sms, cudaStream_t st) {
+  cut_plan<T>(p, kLpPieces);
+  const int slots = kLpPartSmem / (p.pieces * kLpPartBytes);
+  p.slots = slots < kLpMaxSlots ? slots : kLpMaxSlots;
+  const int grid = int(p.s < sms ? p.s : sms);
+  const size_t smem = size_t(p.slots) * p.pieces * kLpPartBytes;
+  logprob_forward_kernel<T><<<grid, kLpThreads, smem, st>>>(p);
 }
-template void launch_logprob_forward<float>(const LogprobParams&, int, cudaStream_t);
-template void launch_logprob_forward<__nv_bfloat16>(const LogprobParams&, int, cudaStream_t);
+template void launch_logprob_forward<float>(LogprobParams, int, cudaStream_t);
+template void launch_logprob_forward<__nv_bfloat16>(LogprobParams, int, cudaStream_t);
 
 cudaError_t set_logprob_smem() {
-  const int bytes = kLpSlots * kLpMaxPieces * 32 * 3 * int(sizeof(float));
+  const int bytes = kLpPartSmem;
   const cudaError_t e = cudaFuncSetAttribute(logprob_forward_kernel<float>,
                                              cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
   if (e != cudaSuccess) return e;

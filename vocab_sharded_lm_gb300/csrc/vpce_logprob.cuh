@@ -21,6 +21,7 @@ struct LogprobParams {
   float* top_logp;           // [s][top]
   float4* stats;             // [s]: largest logit, ln sum exp((z - max) / T), entropy, 0
   int* flag;
+  int pieces, len, slots;    // set by the launch: pieces of a row, vectors in each, rows held at a time
 };
 
 struct LogprobBwdParams {
@@ -58,7 +59,7 @@ __device__ __forceinline__ float max_nan(float a, float b) {
 }
 
 template <typename T>
-void launch_logprob_forward(const LogprobParams& p, int sms, cudaStream_t st);
+void launch_logprob_forward(LogprobParams p, int sms, cudaStream_t st);
 template <typename T>
 void launch_logprob_backward(const LogprobBwdParams& p, int sms, cudaStream_t st);
 
