@@ -34,8 +34,8 @@ namespace {
 
 namespace cg = cooperative_groups;
 
-constexpr int kLpStream = 12;      // warps that stream pieces
-constexpr int kLpFinish = 4;       // warps that finish rows
+constexpr int kLpStream = 13;      // warps that stream pieces
+constexpr int kLpFinish = 3;       // warps that finish rows
 constexpr int kLpThreads = 32 * (kLpStream + kLpFinish);  // one CTA per SM
 constexpr int kLpMaxPieces = 64;   // pieces per row (as many as shards can be)
 constexpr int kLpPieces = 40;      // aimed at: leaves room for 6 rows' partials
@@ -179,57 +179,39 @@ __device__ __forceinline__ int ragged_column(const Seg& q, int l) {
   return -1;
 }
 
-// vectors per batch and step
-template <typename T> constexpr int kLpBatch = LpShape<T>::kVecs / 4;
-
-// One piece by one warp: the lane's (max, S, U), and the maxima of its batches.
-template <typename T, int U>
-__device__ __forceinline__ Acc piece_stats(const LogprobParams& p, const Piece& pc, int len, long long row, float c,
-                                           int lane, float4& bm) {
-  const Seg g = segment<T>(pc, row);
-  const uint4* v = body<T>(g);
-  Acc a{-kLpFar, 0.f, 0.f};
-  bm = make_float4(-INFINITY, -INFINITY, -INFINITY, -INFINITY);
-  const int end = min(pc.off + len, g.nv);
-  const f32x2 cc = f2_pack(c, c);
+// Half a step of a piece (H vectors a lane): its sums, and the maxima of its
+// two batches.
+template <typename T, int H>
+__device__ __forceinline__ void half_stats(const uint4 (&q)[H], Acc& a, float& m0, float& m1, float c) {
+  m0 = max_nan(m0, vecs_max<H / 2>(q, T()));
+  m1 = max_nan(m1, vecs_max<H / 2>(q + H / 2, T()));
+  const float nk = offset_of(max_nan(m0, m1), c);
+  if (nk > a.k) a.raise(nk);
+  const f32x2 cc = f2_pack(c, c), off = f2_pack(-a.k, -a.k);
   const auto low = low_of(c, T());
-#pragma unroll 1
-  for (int base = pc.off; base < end; base += 32 * U) {
-    uint4 q[U];
+  f32x2 s[2] = {f2_pack(a.s, 0.f), f2_pack(0.f, 0.f)}, u[2] = {f2_pack(a.u, 0.f), f2_pack(0.f, 0.f)};
 #pragma unroll
-    for (int j = 0; j < U; ++j) {
-      const int i = base + lane + 32 * j;
-      q[j] = i < end ? __ldcs(v + i) : lp_pad(T());
-    }
-    bm.x = max_nan(bm.x, vecs_max<U / 4>(q, T()));
-    bm.y = max_nan(bm.y, vecs_max<U / 4>(q + U / 4, T()));
-    bm.z = max_nan(bm.z, vecs_max<U / 4>(q + U / 2, T()));
-    bm.w = max_nan(bm.w, vecs_max<U / 4>(q + 3 * (U / 4), T()));
-    const float nk = offset_of(max_nan(max_nan(bm.x, bm.y), max_nan(bm.z, bm.w)), c);
-    if (nk > a.k) a.raise(nk);
-    const f32x2 off = f2_pack(-a.k, -a.k);
-    f32x2 s[2] = {f2_pack(a.s, 0.f), f2_pack(0.f, 0.f)}, u[2] = {f2_pack(a.u, 0.f), f2_pack(0.f, 0.f)};
-#pragma unroll
-    for (int j = 0; j < U; ++j) add_vec(q[j], low, cc, off, s, u, T());
-    float x0, x1;
-    f2_unpack(f2_add(s[0], s[1]), x0, x1);
-    a.s = x0 + x1;
-    f2_unpack(f2_add(u[0], u[1]), x0, x1);
-    a.u = x0 + x1;
-  }
-  if (pc.off == 0 && (g.head | g.tail) != 0) {
-    const int col = ragged_column<T>(g, lane);
-    if (col >= 0) {
-      const float x = Elem<T>::load(g.addr + (long long)col * Elem<T>::kBytes);
-      bm.x = max_nan(bm.x, x);
-      const float nk = offset_of(x, c);
-      if (nk > a.k) a.raise(nk);
-      const float w = fmaf(fmaxf(x, low_of(c, 0.f)), c, -a.k), e = ex2(w);
-      a.s += e;
-      a.u = fmaf(w, e, a.u);
-    }
-  }
-  return a;
+  for (int j = 0; j < H; ++j) add_vec(q[j], low, cc, off, s, u, T());
+  float x0, x1;
+  f2_unpack(f2_add(s[0], s[1]), x0, x1);
+  a.s = x0 + x1;
+  f2_unpack(f2_add(u[0], u[1]), x0, x1);
+  a.u = x0 + x1;
+}
+
+// The ragged element a lane takes with a shard's first piece (-inf: none).
+template <typename T>
+__device__ __forceinline__ float ragged_value(const Seg& g, int lane) {
+  const int col = ragged_column<T>(g, lane);
+  return col >= 0 ? Elem<T>::load(g.addr + (long long)col * Elem<T>::kBytes) : -INFINITY;
+}
+__device__ __forceinline__ void add_ragged(float x, Acc& a, float& m0, float c) {
+  m0 = max_nan(m0, x);
+  const float nk = offset_of(x, c);
+  if (nk > a.k) a.raise(nk);
+  const float v = fmaf(fmaxf(x, low_of(c, 0.f)), c, -a.k), e = ex2(v);
+  a.s += e;
+  a.u = fmaf(v, e, a.u);
 }
 
 // S and U of a row relative to its largest logit M, by subtraction, for rows
@@ -620,7 +602,7 @@ __device__ __forceinline__ void cut_row(const LogprobParams& p, Piece* piece) {
 // from a shared counter, run ahead into the next rows and leave partials in
 // one of p.slots places; the finishing warps take the complete rows in turn.
 // Finishing a row is a chain of dependent steps (10 to 15 us, against 5.7 us
-// to stream a 256 KB row), so four rows are finished at a time; finished by
+// to stream a 256 KB row), so three rows are finished at a time; finished by
 // the streaming warps themselves, the same steps cost the stream its registers.
 template <typename T>
 __global__ void __launch_bounds__(kLpThreads, 1)
@@ -638,7 +620,7 @@ __global__ void __launch_bounds__(kLpThreads, 1)
   float* ss = reinterpret_cast<float*>(sm + p.slots * n);
   float* su = ss + p.slots * n;
   if (threadIdx.x == 0) {
-    next = kLpStream;
+    next = 2 * kLpStream;
     stop = 0;
     for (int i = 0; i < kLpMaxSlots; ++i) {
       mbar_init(&full[i], p.pieces);
@@ -650,44 +632,91 @@ __global__ void __launch_bounds__(kLpThreads, 1)
   __syncthreads();
   const int rows = int((p.s - blockIdx.x + gridDim.x - 1) / gridDim.x);  // this CTA's rows
   if (warp < kLpStream) {
+    constexpr int H = U / 2;
     const float c = p.inv_t * kLog2e;
-    // the piece in hand: number i of the CTA's row k; the next one is taken,
-    // and its row's target loaded, while this one streams
-    int taken = 0, i = warp, k = 0;
-    while (i >= p.pieces) {
-      i -= p.pieces;
-      ++k;
-    }
-    bool ignored = false;
-    if (p.targets != nullptr && k < rows)
-      ignored = __ldg(p.targets + blockIdx.x + (long long)k * gridDim.x) == p.ignore_index;
-    while (k < rows) {
+    // piece i of the CTA's row k, and the next one taken; a row's target is
+    // loaded when the row is first taken, a piece ahead of its use
+    struct Taken {
+      int i, k;
+      long long y;
+    };
+    auto settle = [&](Taken& x, int i, int k) {
+      const int was = x.k;
+      while (i >= p.pieces) {
+        i -= p.pieces;
+        ++k;
+      }
+      if (p.targets != nullptr && k != was && k < rows)
+        x.y = __ldg(p.targets + blockIdx.x + (long long)k * gridDim.x);
+      x.i = i;
+      x.k = k;
+    };
+    Taken cur{0, -1, 0}, nxt;
+    settle(cur, warp, 0);
+    nxt = cur;
+    settle(nxt, warp + kLpStream - cur.k * p.pieces, cur.k);
+    const uint4* v = nullptr;  // the piece in hand: its shard's body, its vectors [base, end)
+    int base = 0, end = 0;
+    float ragged = -INFINITY;
+    uint4 qa[H], qb[H];
+    auto load = [&](uint4 (&q)[H], int from) {
+#pragma unroll
+      for (int j = 0; j < H; ++j) {
+        const int x = from + lane + 32 * j;
+        q[j] = x < end ? __ldcs(v + x) : lp_pad(T());
+      }
+    };
+    auto ignored = [&](const Taken& x) { return p.targets != nullptr && x.y == p.ignore_index; };
+    auto begin = [&](const Taken& x) {
+      if (x.k >= rows || ignored(x)) return;
+      const Piece pc = piece[x.i];
+      const Seg g = segment<T>(pc, blockIdx.x + (long long)x.k * gridDim.x);
+      v = body<T>(g);
+      base = pc.off;
+      end = min(pc.off + p.len, g.nv);
+      ragged = -INFINITY;
+      if (pc.off == 0 && (g.head | g.tail) != 0) ragged = ragged_value<T>(g, lane);
+      load(qa, base);
+    };
+    begin(cur);
+    // one piece's loads are under way while the one before is summed
+    while (cur.k < rows) {
+      const Taken now = cur;
+      const bool skip = ignored(now);
+      Acc a{-kLpFar, 0.f, 0.f};
+      float4 bm = make_float4(-INFINITY, -INFINITY, -INFINITY, -INFINITY);
+      int taken = 0;
       if (lane == 0) taken = atomicAdd(&next, 1);
-      Acc a;
-      float4 bm;
-      if (!ignored)
-        a = piece_stats<T, U>(p, piece[i], p.len, blockIdx.x + (long long)k * gridDim.x, c, lane, bm);
-      const int slot = k % p.slots, turn = k / p.slots;
+      if (!skip) {
+        if (ragged > -INFINITY || isnan(ragged)) add_ragged(ragged, a, bm.x, c);
+#pragma unroll 1
+        while (base + 32 * U < end) {
+          load(qb, base + 32 * H);
+          half_stats<T, H>(qa, a, bm.x, bm.y, c);
+          base += 32 * U;
+          load(qa, base);
+          half_stats<T, H>(qb, a, bm.z, bm.w, c);
+        }
+        load(qb, base + 32 * H);
+        half_stats<T, H>(qa, a, bm.x, bm.y, c);
+      }
+      cur = nxt;
+      begin(cur);
+      settle(nxt, __shfl_sync(kFull, taken, 0) - cur.k * p.pieces, cur.k);
+      if (!skip) half_stats<T, H>(qb, a, bm.z, bm.w, c);
+      const int slot = now.k % p.slots, turn = now.k / p.slots;
       if (turn > 0 && !mbar_wait_warp(&empty[slot], (turn - 1) & 1)) {
         stop = 1;
         break;
       }
-      if (!ignored) {
-        const int at = slot * n + i * 32 + lane;
+      if (!skip) {
+        const int at = slot * n + now.i * 32 + lane;
         sm[at] = bm;
         ss[at] = a.s;
         su[at] = a.u;
       }
       __syncwarp();
       if (lane == 0) mbar_arrive_local(&full[slot]);
-      const int k0 = k;
-      i = __shfl_sync(kFull, taken, 0) - k * p.pieces;
-      while (i >= p.pieces) {
-        i -= p.pieces;
-        ++k;
-      }
-      if (p.targets != nullptr && k != k0 && k < rows)
-        ignored = __ldg(p.targets + blockIdx.x + (long long)k * gridDim.x) == p.ignore_index;
     }
   } else {
     for (int k = warp - kLpStream; k < rows; k += kLpFinish) {
