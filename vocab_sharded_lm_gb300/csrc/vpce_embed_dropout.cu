@@ -4,8 +4,18 @@
 // with m(r, c) = 0 where the 16 random bits of (r, c) are below D and 1
 // elsewhere.  The bits come from a counter-based generator keyed by the call's
 // (seed, offset), so the gradient forms the same mask again and no mask is
-// stored.  The gradient of a table row is the sum of f m(r, c) g[r, c] over
-// its tokens' rows in ascending order.
+// stored.  One generator block serves 8 columns, the 16 bytes a lane moves.
+//
+// Gradient: dE[v, c] = f sum over the rows r of token v, ascending, of
+// m(r, c) g[r, c].  Two launches.
+//   sort   Each CTA owns a range of ids.  It reads all ids once to count the
+//          tokens below its range (its place in the sorted order) and once to
+//          collect its own in row order, and sorts those by a stable counting
+//          sort in shared memory: no global sort passes and no grid barrier.
+//   sum    A persistent grid: runs of more than kLong rows a CTA at a time
+//          (its warps sum contiguous slices, added in order), then groups of
+//          16 sorted rows a warp at a time, all 16 rows' loads in flight, then,
+//          when the table is overwritten, the rows of ids that do not occur.
 #include "vpce_embed_dropout.cuh"
 
 namespace vpce {
@@ -13,6 +23,7 @@ namespace vpce {
 namespace {
 
 constexpr int kEdThreads = 256;
+constexpr int kEdWarps = kEdThreads / 32;
 
 __device__ __forceinline__ int shard_holding(const ShardSet& sh, int t, long long id) {
   int lo = 0, hi = t;  // start[lo] <= id < start[hi]
@@ -24,72 +35,546 @@ __device__ __forceinline__ int shard_holding(const ShardSet& sh, int t, long lon
   return lo;
 }
 
+// ---------------------------------------------------------------------------
+// eight columns at a time
+// ---------------------------------------------------------------------------
+template <typename T> struct Eight;  // as loaded
+template <> struct Eight<__nv_bfloat16> {
+  uint4 v;
+  __device__ __forceinline__ void get(float (&x)[8]) const { unpack(v, x, __nv_bfloat16()); }
+};
+template <> struct Eight<float> {
+  float4 a, b;
+  __device__ __forceinline__ void get(float (&x)[8]) const {
+    x[0] = a.x, x[1] = a.y, x[2] = a.z, x[3] = a.w;
+    x[4] = b.x, x[5] = b.y, x[6] = b.z, x[7] = b.w;
+  }
+};
+__device__ __forceinline__ void clear(Eight<__nv_bfloat16>& e) { e.v = make_uint4(0u, 0u, 0u, 0u); }
+__device__ __forceinline__ void clear(Eight<float>& e) { e.a = e.b = make_float4(0.f, 0.f, 0.f, 0.f); }
+
+// Columns [0, n) of eight at p (n <= 8; the others 0).  vec: p is 16-byte
+// aligned.
+__device__ __forceinline__ void load8(Eight<__nv_bfloat16>& e, const unsigned char* p, int n, bool vec) {
+  if (vec && n == 8) {
+    e.v = __ldcs(reinterpret_cast<const uint4*>(p));
+    return;
+  }
+  const unsigned short* h = reinterpret_cast<const unsigned short*>(p);
+  unsigned w[4] = {0u, 0u, 0u, 0u};
+#pragma unroll
+  for (int j = 0; j < 8; ++j)
+    if (j < n) w[j >> 1] |= unsigned(__ldg(h + j)) << (16 * (j & 1));
+  e.v = make_uint4(w[0], w[1], w[2], w[3]);
+}
+__device__ __forceinline__ void load8(Eight<float>& e, const unsigned char* p, int n, bool vec) {
+  const float4* q = reinterpret_cast<const float4*>(p);
+  if (vec && n == 8) {
+    e.a = __ldcs(q);
+    e.b = __ldcs(q + 1);
+    return;
+  }
+  const float* f = reinterpret_cast<const float*>(p);
+  float x[8];
+#pragma unroll
+  for (int j = 0; j < 8; ++j) x[j] = j < n ? __ldg(f + j) : 0.f;
+  e.a = make_float4(x[0], x[1], x[2], x[3]);
+  e.b = make_float4(x[4], x[5], x[6], x[7]);
+}
+__device__ __forceinline__ void store8(unsigned char* p, const float (&x)[8], int n, bool vec, __nv_bfloat16) {
+  if (vec && n == 8) {
+    __stcs(reinterpret_cast<uint4*>(p), pack(x, __nv_bfloat16()));
+    return;
+  }
+#pragma unroll
+  for (int j = 0; j < 8; ++j)
+    if (j < n) Elem<__nv_bfloat16>::store(p + 2 * j, x[j]);
+}
+__device__ __forceinline__ void store8(unsigned char* p, const float (&x)[8], int n, bool vec, float) {
+  if (vec && n == 8) {
+    __stcs(reinterpret_cast<float4*>(p), make_float4(x[0], x[1], x[2], x[3]));
+    __stcs(reinterpret_cast<float4*>(p) + 1, make_float4(x[4], x[5], x[6], x[7]));
+    return;
+  }
+#pragma unroll
+  for (int j = 0; j < 8; ++j)
+    if (j < n) reinterpret_cast<float*>(p)[j] = x[j];
+}
+
+// Zeroes the dropped ones of eight values.  A word's high half is below D
+// where the word is below D << 16, its low half where the word shifted up is.
+__device__ __forceinline__ void drop8(float (&x)[8], const uint4& bits, unsigned limit) {
+  const unsigned w[4] = {bits.x, bits.y, bits.z, bits.w};
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    x[2 * i] = (w[i] << 16) < limit ? 0.f : x[2 * i];
+    x[2 * i + 1] = w[i] < limit ? 0.f : x[2 * i + 1];
+  }
+}
+
+// ---------------------------------------------------------------------------
+// forward
+// ---------------------------------------------------------------------------
+constexpr int kEfBlocks = 8;  // 8-column blocks per lane and unit
+
+// One unit per warp at a time: kEfBlocks * 256 columns of a row.
 template <typename TI, typename TO>
 __global__ void __launch_bounds__(kEdThreads) embed_dropout_forward_kernel(const __grid_constant__ EmbedDropParams p) {
-  const long long blocks = (p.h + 7) / 8;
+  constexpr int IB = Elem<TI>::kBytes, OB = Elem<TO>::kBytes;
+  const int lane = threadIdx.x & 31;
   const unsigned long long seed = p.drop ? p.rng[0] : 0, offset = p.drop ? p.rng[1] : 0;
-  for (long long r = blockIdx.x; r < p.s; r += gridDim.x) {
-    const long long id = p.ids[r];
-    const bool in = id >= 0 && id < p.V, live = in && id != p.padding_id;
-    if (!in && id != p.padding_id && threadIdx.x == 0 && p.flag != nullptr) atomicOr(p.flag, VPCE_FLAG_BAD_TARGET);
-    const int i = in ? shard_holding(p.sh, p.t, id) : 0;
-    const unsigned char* src = in ? p.sh.ptr[i] + (id - p.sh.start[i]) * p.sh.ld_bytes[i] : nullptr;
+  const unsigned limit = p.drop << 16;
+  const long long per = (p.h + 256 * kEfBlocks - 1) / (256 * kEfBlocks);
+  const long long units = p.s * per, nw = (long long)gridDim.x * kEdWarps;
+  for (long long w = (long long)blockIdx.x * kEdWarps + (threadIdx.x >> 5); w < units; w += nw) {
+    const long long r = per == 1 ? w : w / per;
+    const long long c0 = (w - r * per) * (256 * kEfBlocks) + lane * 8;
+    const long long id = __ldg(p.ids + r);
+    const bool pad = id == p.padding_id, in = id >= 0 && id < p.V, live = in && !pad;
+    if (!in && !pad && lane == 0 && p.flag != nullptr) atomicOr(p.flag, VPCE_FLAG_BAD_TARGET);
+    const int i = live ? shard_holding(p.sh, p.t, id) : 0;
+    const unsigned char* src = live ? p.sh.ptr[i] + (id - p.sh.start[i]) * p.sh.ld_bytes[i] : nullptr;
     unsigned char* dst = p.out + r * p.ld_out_bytes;
-    for (long long b = threadIdx.x; b < blocks; b += kEdThreads) {
-      uint4 bits = make_uint4(0u, 0u, 0u, 0u);
-      if (p.drop && live) bits = drop_block(seed, offset, r, unsigned(b));
-      for (int j = 0; j < 8; ++j) {
-        const long long c = b * 8 + j;
-        if (c >= p.h) break;
-        float v = 0.f;
-        if (live && drop_keeps(bits, j, p.drop)) v = Elem<TI>::load(src + c * Elem<TI>::kBytes) * p.factor;
-        Elem<TO>::store(dst + c * Elem<TO>::kBytes, v);
-      }
+    const bool vi = (reinterpret_cast<uintptr_t>(src) & 15) == 0, vo = (reinterpret_cast<uintptr_t>(dst) & 15) == 0;
+    Eight<TI> q[kEfBlocks];
+#pragma unroll
+    for (int k = 0; k < kEfBlocks; ++k) {
+      const long long c = c0 + 256 * k;
+      if (live && c < p.h) load8(q[k], src + c * IB, int(min(8LL, p.h - c)), vi);
+      else clear(q[k]);
+    }
+#pragma unroll
+    for (int k = 0; k < kEfBlocks; ++k) {
+      const long long c = c0 + 256 * k;
+      if (c >= p.h) break;
+      float x[8];
+      q[k].get(x);
+#pragma unroll
+      for (int j = 0; j < 8; ++j) x[j] *= p.factor;
+      if (p.drop && live) drop8(x, drop_block(seed, offset, r, unsigned(c >> 3)), limit);
+      store8(dst + c * OB, x, int(min(8LL, p.h - c)), vo, TO());
     }
   }
 }
 
-// One CTA per table row: finds the row's tokens in order and adds their
-// gradient rows.
-template <typename T>
-__global__ void __launch_bounds__(kEdThreads) embed_dropout_backward_kernel(const __grid_constant__ EmbedDropParams p) {
-  __shared__ int list[kEdThreads];
-  __shared__ int wcount[kEdThreads / 32];
+// ---------------------------------------------------------------------------
+// sort
+// ---------------------------------------------------------------------------
+constexpr int kSortThreads = 1024;
+constexpr int kSortWarps = kSortThreads / 32;
+constexpr int kDigits = 1024;  // bins of one counting pass
+constexpr int kLong = 64;      // runs with more rows are summed by a whole CTA
+constexpr int kGroup = 16;     // sorted rows per warp task
+constexpr int kMaxLists = 1024;  // CTAs of the sort, at most
+template <typename T> constexpr int kInFlight = sizeof(T) == 2 ? 16 : 8;  // rows' loads per lane
+
+struct SortHead {
+  long long valid;              // tokens with a gradient
+  unsigned long long taken[3];  // the sum's task counters
+};
+
+struct SortParams {
+  const long long* ids;
+  long long s;
+  long long V;
+  long long padding_id;
+  int range;          // ids per CTA, a multiple of 32
+  int* row[2];        // [s] rows, before and after a pass
+  int* key[2];        // [s] ids less the CTA's first
+  int* sorted_id;     // [s]
+  int* sorted_row;    // [s]
+  unsigned* present;  // bit per id
+  int2* runs;         // long runs, (first position, rows); a CTA's from its first position / (kLong + 1) on
+  int2* lists;        // per CTA: first of its long runs, how many
+  SortHead* head;
+};
+
+// Exclusive scan of one int per thread of the CTA, and the total.
+__device__ __forceinline__ int cta_scan(int v, int* tmp, int& total) {
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  int x = v;
+#pragma unroll
+  for (int o = 1; o < 32; o <<= 1) {
+    const int y = __shfl_up_sync(kFull, x, o);
+    if (lane >= o) x += y;
+  }
+  __syncthreads();
+  if (lane == 31) tmp[warp] = x;
+  __syncthreads();
+  int before = 0;
+  total = 0;
+  for (int w = 0; w < kSortWarps; ++w) {
+    before += w < warp ? tmp[w] : 0;
+    total += tmp[w];
+  }
+  return before + x - v;
+}
+
+__global__ void __launch_bounds__(kSortThreads, 1) embed_sort_kernel(const __grid_constant__ SortParams p) {
+  extern __shared__ int count[];  // [warps][kDigits]
+  __shared__ int nlong;
+  __shared__ int tmp[kSortWarps], wmine[kSortWarps], wlow[kSortWarps];
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-  const unsigned long long seed = p.drop ? p.rng[0] : 0, offset = p.drop ? p.rng[1] : 0;
-  for (long long v = blockIdx.x; v < p.V; v += gridDim.x) {
-    const int i = shard_holding(p.sh, p.t, v);
-    float* row = reinterpret_cast<float*>(const_cast<unsigned char*>(p.sh.ptr[i]) + (v - p.sh.start[i]) * p.sh.ld_bytes[i]);
-    if (!p.accumulate)
-      for (long long c = tid; c < p.h; c += kEdThreads) row[c] = 0.f;
-    if (v == p.padding_id) continue;
-    for (long long r0 = 0; r0 < p.s; r0 += kEdThreads) {
-      const bool mine = r0 + tid < p.s && p.ids[r0 + tid] == v;
-      const unsigned m = __ballot_sync(kFull, mine);
-      __syncthreads();
-      if (lane == 0) wcount[warp] = __popc(m);
-      __syncthreads();
-      int before = 0, n = 0;
-      for (int w = 0; w < kEdThreads / 32; ++w) {
-        before += w < warp ? wcount[w] : 0;
-        n += wcount[w];
+  const long long lo = (long long)blockIdx.x * p.range, hi = min(p.V, lo + p.range);
+  // this warp's slice of the ids
+  const long long per = ((p.s + kSortWarps - 1) / kSortWarps + 31) / 32 * 32;
+  const long long r0 = warp * per, r1 = min(p.s, r0 + per);
+  int mine = 0, low = 0;
+#pragma unroll 4
+  for (long long r = r0 + lane; r < r1; r += 32) {
+    const long long id = __ldg(p.ids + r);
+    const bool ok = id != p.padding_id;
+    mine += ok && id >= lo && id < hi;
+    low += ok && id >= 0 && id < lo;
+  }
+  mine = __reduce_add_sync(kFull, mine);
+  low = __reduce_add_sync(kFull, low);
+  if (lane == 0) {
+    wmine[warp] = mine;
+    wlow[warp] = low;
+  }
+  for (int i = tid; i < int((hi - lo + 31) / 32); i += kSortThreads) p.present[lo / 32 + i] = 0u;
+  if (blockIdx.x == 0 && tid < 3) p.head->taken[tid] = 0;
+  if (tid == 0) nlong = 0;
+  __syncthreads();
+  int n = 0, at = 0;
+  long long base = 0;
+  for (int w = 0; w < kSortWarps; ++w) {
+    at += w < warp ? wmine[w] : 0;
+    n += wmine[w];
+    base += wlow[w];
+  }
+  if (blockIdx.x == gridDim.x - 1 && tid == 0) p.head->valid = base + n;
+  if (n == 0) {
+    if (tid == 0) p.lists[blockIdx.x] = make_int2(0, 0);
+    return;
+  }
+  const int first_run = int(base / (kLong + 1));  // n tokens hold at most n / (kLong + 1) long runs
+  int *key = p.key[0] + base, *row = p.row[0] + base, *key2 = p.key[1] + base, *row2 = p.row[1] + base;
+  if (mine > 0) {
+    for (long long r = r0; r < r1; r += 32) {
+      const long long id = r + lane < r1 ? __ldg(p.ids + r + lane) : -1;
+      const bool in = id != p.padding_id && id >= lo && id < hi && r + lane < r1;
+      const unsigned m = __ballot_sync(kFull, in);
+      if (in) {
+        const int k = at + __popc(m & ((1u << lane) - 1u));
+        key[k] = int(id - lo);
+        row[k] = int(r) + lane;
       }
-      if (n == 0) continue;
-      if (mine) list[before + __popc(m & ((1u << lane) - 1u))] = int(r0) + tid;
-      __syncthreads();
-      for (long long b = tid; b < (p.h + 7) / 8; b += kEdThreads) {
-        float acc[8] = {};
-        for (int k = 0; k < n; ++k) {
-          const long long r = list[k];
-          uint4 bits = make_uint4(0u, 0u, 0u, 0u);
-          if (p.drop) bits = drop_block(seed, offset, r, unsigned(b));
-          for (int j = 0; j < 8; ++j)
-            if (b * 8 + j < p.h && drop_keeps(bits, j, p.drop))
-              acc[j] += Elem<T>::load(p.out + r * p.ld_out_bytes + (b * 8 + j) * Elem<T>::kBytes);
+      at += __popc(m);
+    }
+  }
+  // stable counting passes, kDigits bins each; the warps take contiguous
+  // slices of the list (fewer warps for short lists: less to clear and scan)
+  const int warps = min(kSortWarps, (n + 127) / 128);
+  const int slice = ((n + warps - 1) / warps + 31) / 32 * 32;
+  for (int shift = 0; shift == 0 || ((p.range - 1) >> shift) > 0; shift += 10) {
+    const int bins = min(kDigits, ((p.range - 1) >> shift) + 1);
+    for (int i = tid; i < warps * kDigits; i += kSortThreads) count[i] = 0;
+    __syncthreads();
+    const int k0 = min(n, warp * slice), k1 = warp < warps ? min(n, k0 + slice) : k0;
+    int* mycount = count + warp * kDigits;
+    for (int k = k0; k < k1; k += 32) {
+      const bool in = k + lane < k1;
+      const int d = in ? (key[k + lane] >> shift) & (kDigits - 1) : -1;
+      const unsigned m = __match_any_sync(kFull, d);
+      if (in && lane == __ffs(m) - 1) mycount[d] += __popc(m);
+      __syncwarp();
+    }
+    __syncthreads();
+    int sum = 0;
+    if (tid < bins)
+      for (int w = 0; w < warps; ++w) sum += count[w * kDigits + tid];
+    int total;
+    int pos = cta_scan(sum, tmp, total);
+    if (tid < bins)
+      for (int w = 0; w < warps; ++w) {
+        const int x = count[w * kDigits + tid];
+        count[w * kDigits + tid] = pos;
+        pos += x;
+      }
+    __syncthreads();
+    for (int k = k0; k < k1; k += 32) {
+      const bool in = k + lane < k1;
+      const int kk = in ? key[k + lane] : 0;
+      const int d = in ? (kk >> shift) & (kDigits - 1) : -1;
+      const unsigned m = __match_any_sync(kFull, d);
+      if (in) {
+        const int to = mycount[d] + __popc(m & ((1u << lane) - 1u));
+        key2[to] = kk;
+        row2[to] = row[k + lane];
+      }
+      __syncwarp();
+      if (in && lane == __ffs(m) - 1) mycount[d] += __popc(m);
+      __syncwarp();
+    }
+    __syncthreads();
+    int* x = key;
+    key = key2;
+    key2 = x;
+    x = row;
+    row = row2;
+    row2 = x;
+  }
+  // sorted ids and rows, the ids that occur, the long runs
+  for (int k = tid; k < n; k += kSortThreads) {
+    const int kk = key[k];
+    p.sorted_id[base + k] = int(lo) + kk;
+    p.sorted_row[base + k] = row[k];
+    if (k == 0 || key[k - 1] != kk) {
+      atomicOr(p.present + (lo + kk) / 32, 1u << (kk & 31));
+      if (k + kLong < n && key[k + kLong] == kk) {
+        int a = k + kLong, b = n;  // the run's end is in (a, b]
+        while (b - a > 1) {
+          const int mid = a + (b - a) / 2;
+          if (key[mid] == kk) a = mid;
+          else b = mid;
         }
-        for (int j = 0; j < 8; ++j)
-          if (b * 8 + j < p.h) row[b * 8 + j] += acc[j] * p.factor;
+        p.runs[first_run + atomicAdd(&nlong, 1)] = make_int2(int(base) + k, b - k);
       }
+    }
+  }
+  __syncthreads();
+  if (tid == 0) p.lists[blockIdx.x] = make_int2(first_run, nlong);
+}
+
+// ---------------------------------------------------------------------------
+// sum
+// ---------------------------------------------------------------------------
+struct SumParams {
+  EmbedDropParams e;  // e.sh: the gradient shards; e.out: the gradient rows
+  const int* id;
+  const int* row;
+  const unsigned* present;
+  const int2* runs;
+  const int2* lists;
+  int nlists;
+  SortHead* head;
+};
+
+// a run's eight columns into the table: one store, or one addition that needs
+// no answer (each element gets one, so the order cannot matter)
+__device__ __forceinline__ void put8(float* p, const float (&x)[8], int n, bool vec, int accumulate) {
+  if (vec && n == 8) {
+    if (accumulate) {
+      asm volatile("red.global.add.v4.f32 [%0], {%1, %2, %3, %4};" ::"l"(p), "f"(x[0]), "f"(x[1]), "f"(x[2]), "f"(x[3])
+                   : "memory");
+      asm volatile("red.global.add.v4.f32 [%0], {%1, %2, %3, %4};" ::"l"(p + 4), "f"(x[4]), "f"(x[5]), "f"(x[6]),
+                   "f"(x[7])
+                   : "memory");
+    } else {
+      __stcs(reinterpret_cast<float4*>(p), make_float4(x[0], x[1], x[2], x[3]));
+      __stcs(reinterpret_cast<float4*>(p) + 1, make_float4(x[4], x[5], x[6], x[7]));
+    }
+    return;
+  }
+#pragma unroll
+  for (int j = 0; j < 8; ++j)
+    if (j < n) {
+      if (accumulate) p[j] += x[j];
+      else p[j] = x[j];
+    }
+}
+
+__device__ __forceinline__ float* table_row(const EmbedDropParams& e, int id) {
+  const int i = shard_holding(e.sh, e.t, id);
+  return reinterpret_cast<float*>(const_cast<unsigned char*>(e.sh.ptr[i]) + (id - e.sh.start[i]) * e.sh.ld_bytes[i]);
+}
+
+template <typename T>
+struct RowSource {
+  const EmbedDropParams& e;
+  unsigned long long seed, offset;
+  unsigned limit;
+  long long c;  // the lane's first column
+  int n;        // columns it has, 0..8
+  bool vec;     // gradient rows are 16-byte aligned
+  __device__ __forceinline__ void load(Eight<T>& q, int r) const {
+    if (n > 0) load8(q, e.out + r * e.ld_out_bytes + c * Elem<T>::kBytes, n, vec);
+    else clear(q);
+  }
+  __device__ __forceinline__ void add(float (&acc)[8], const Eight<T>& q, int r) const {
+    float x[8];
+    q.get(x);
+    if (e.drop) drop8(x, drop_block(seed, offset, r, unsigned(c >> 3)), limit);
+#pragma unroll
+    for (int j = 0; j < 8; ++j) acc[j] += x[j];
+  }
+};
+
+template <typename T>
+__global__ void __launch_bounds__(kEdThreads, 2) embed_sum_kernel(const __grid_constant__ SumParams p) {
+  __shared__ float part[kEdWarps][8][32];
+  __shared__ unsigned long long task;
+  __shared__ int upto[kMaxLists];
+  const EmbedDropParams& e = p.e;
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  constexpr int kIn = kInFlight<T>;
+  const int blocks = int((e.h + 255) / 256);  // column blocks of a warp
+  RowSource<T> src{e, e.drop ? e.rng[0] : 0, e.drop ? e.rng[1] : 0, e.drop << 16, 0, 0,
+                   ((reinterpret_cast<uintptr_t>(e.out) | e.ld_out_bytes) & 15) == 0};
+  auto columns = [&](int block) {
+    src.c = (long long)block * 256 + lane * 8;
+    src.n = int(max(0LL, min(8LL, e.h - src.c)));
+  };
+  auto flush = [&](float* row, float (&acc)[8]) {
+#pragma unroll
+    for (int j = 0; j < 8; ++j) acc[j] *= e.factor;
+    float* at = row + src.c;
+    if (src.n > 0) put8(at, acc, src.n, (reinterpret_cast<uintptr_t>(at) & 15) == 0, e.accumulate);
+  };
+
+  // long runs: (run, column block) per CTA; warp w sums the w-th eighth of the
+  // rows, and the eighths are added in order
+  if (warp == 0) {
+    int carry = 0;
+    for (int i0 = 0; i0 < p.nlists; i0 += 32) {
+      int x = i0 + lane < p.nlists ? p.lists[i0 + lane].y : 0;
+#pragma unroll
+      for (int o = 1; o < 32; o <<= 1) {
+        const int y = __shfl_up_sync(kFull, x, o);
+        if (lane >= o) x += y;
+      }
+      if (i0 + lane < p.nlists) upto[i0 + lane] = carry + x;
+      carry += __shfl_sync(kFull, x, 31);
+    }
+  }
+  __syncthreads();
+  const int valid = int(p.head->valid);
+  const unsigned long long long_tasks = (unsigned long long)upto[p.nlists - 1] * blocks;
+  while (long_tasks > 0) {
+    __syncthreads();
+    if (threadIdx.x == 0) task = atomicAdd(&p.head->taken[0], 1ull);
+    __syncthreads();
+    if (task >= long_tasks) break;
+    const int nth = int(task / blocks);
+    int l = 0;  // the list that holds it: the first with upto > nth
+    for (int step = 512; step > 0; step >>= 1)
+      if (l + step <= p.nlists - 1 && upto[l + step - 1] <= nth) l += step;
+    const int2 run = p.runs[p.lists[l].x + nth - (l > 0 ? upto[l - 1] : 0)];
+    columns(int(task % blocks));
+    const int each = (run.y + kEdWarps - 1) / kEdWarps;
+    const int k0 = run.x + min(run.y, warp * each), k1 = run.x + min(run.y, (warp + 1) * each);
+    float acc[8] = {};
+    for (int k = k0; k < k1; k += 32) {
+      const int m = min(32, k1 - k);
+      const int r32 = lane < m ? p.row[k + lane] : 0;
+      for (int b = 0; b < m; b += kIn) {
+        Eight<T> q[kIn];
+#pragma unroll
+        for (int j = 0; j < kIn; ++j) {
+          const int r = __shfl_sync(kFull, r32, b + j);
+          if (b + j < m) src.load(q[j], r);
+          else clear(q[j]);
+        }
+#pragma unroll
+        for (int j = 0; j < kIn; ++j) {
+          const int r = __shfl_sync(kFull, r32, b + j);
+          if (b + j < m) src.add(acc, q[j], r);
+        }
+      }
+    }
+#pragma unroll
+    for (int j = 0; j < 8; ++j) part[warp][j][lane] = acc[j];
+    __syncthreads();
+    if (warp == 0) {
+#pragma unroll
+      for (int j = 0; j < 8; ++j)
+        for (int w = 1; w < kEdWarps; ++w) acc[j] += part[w][j][lane];
+      flush(table_row(e, p.id[run.x]), acc);
+    }
+  }
+
+  // short runs: the runs that start in a group of 16 sorted rows
+  const int groups = (valid + kGroup - 1) / kGroup;
+  const unsigned long long short_tasks = (unsigned long long)groups * blocks;
+  while (true) {
+    unsigned long long tk = 0;
+    if (lane == 0) tk = atomicAdd(&p.head->taken[1], 1ull);
+    tk = __shfl_sync(kFull, tk, 0);
+    if (tk >= short_tasks) break;
+    const int g = int(tk / blocks) * kGroup;
+    columns(int(tk % blocks));
+    float acc[8] = {};
+    float* cur = nullptr;  // table row of the run being summed
+    bool done = false;
+    for (int k = g; !done; k += kGroup) {
+      // 16 positions; lane l holds position k + l
+      const int pos = k + lane;
+      const bool here = lane < kGroup && pos < valid;
+      const int id = here ? p.id[pos] : -1;
+      const int r16 = here ? p.row[pos] : 0;
+      const int prev = here && pos > 0 ? p.id[pos - 1] : -1;
+      const bool head = here && id != prev;
+      const bool is_long = head && pos + kLong < valid && p.id[pos + kLong] == id;
+      const unsigned heads = __ballot_sync(kFull, head), longs = __ballot_sync(kFull, is_long),
+                     heres = __ballot_sync(kFull, here);
+      float* trow = head ? table_row(e, id) : nullptr;
+      // the positions to sum: from the group's first head (or, past the group,
+      // from its start) to the first head past the group or the first long run
+      int a = 0, b = __popc(heres);
+      if (k == g) {
+        if (heads == 0) break;
+        a = __ffs(heads) - 1;
+      } else if (heads != 0) {
+        b = __ffs(heads) - 1;
+        done = true;
+      }
+      if (longs != 0 && __ffs(longs) - 1 < b) {  // a long run starts here: summed above
+        // the last head of the 16 (a long run reaches past them)
+        b = __ffs(longs) - 1;
+        done = true;
+      }
+      if (b < kGroup) done = true;
+      for (int part = 0; part < kGroup; part += kIn) {
+        if (part >= b) break;
+        Eight<T> q[kIn];
+#pragma unroll
+        for (int i = 0; i < kIn; ++i) {
+          const int j = part + i, r = __shfl_sync(kFull, r16, j);
+          if (j >= a && j < b) src.load(q[i], r);
+          else clear(q[i]);
+        }
+#pragma unroll
+        for (int i = 0; i < kIn; ++i) {
+          const int j = part + i, r = __shfl_sync(kFull, r16, j);
+          const unsigned long long t = __shfl_sync(kFull, reinterpret_cast<unsigned long long>(trow), j);
+          if (j < a || j >= b) continue;
+          if (heads >> j & 1u) {
+            if (cur != nullptr) flush(cur, acc);
+#pragma unroll
+            for (int x = 0; x < 8; ++x) acc[x] = 0.f;
+            cur = reinterpret_cast<float*>(t);
+          }
+          src.add(acc, q[i], r);
+        }
+      }
+    }
+    if (cur != nullptr) flush(cur, acc);
+  }
+  if (e.accumulate) return;
+
+  // rows of ids that do not occur: 8 ids per warp task
+  const long long zero_tasks = (e.V + 7) / 8;
+  while (true) {
+    unsigned long long got = 0;
+    if (lane == 0) got = atomicAdd(&p.head->taken[2], 1ull);
+    const long long tk = (long long)__shfl_sync(kFull, got, 0);
+    if (tk >= zero_tasks) break;
+    const unsigned bits = p.present[tk / 4] >> (8 * (tk & 3));
+    for (int j = 0; j < 8; ++j) {
+      const long long id = tk * 8 + j;
+      if (id >= e.V) break;
+      if (bits >> j & 1u) continue;
+      float* row = table_row(e, int(id));
+      // 16-byte stores between ragged ends
+      const int head = min(int(e.h), int((16 - (reinterpret_cast<uintptr_t>(row) & 15)) & 15) / 4);
+      const int nv = (int(e.h) - head) / 4, tail = int(e.h) - head - 4 * nv;
+      float4* v = reinterpret_cast<float4*>(row + head);
+#pragma unroll 4
+      for (int i = lane; i < nv; i += 32) __stcs(v + i, make_float4(0.f, 0.f, 0.f, 0.f));
+      if (lane < head) row[lane] = 0.f;
+      if (lane < tail) row[head + 4 * nv + lane] = 0.f;
     }
   }
 }
@@ -98,22 +583,82 @@ __global__ void __launch_bounds__(kEdThreads) embed_dropout_backward_kernel(cons
 
 void launch_embed_dropout_forward(const EmbedDropParams& p, bool table_bf16, bool out_bf16, int sms,
                                   cudaStream_t st) {
-  const long long cap = (long long)sms * 8;
-  const int grid = int(p.s < cap ? p.s : cap);
+  const long long units = p.s * ((p.h + 256 * kEfBlocks - 1) / (256 * kEfBlocks));
+  const long long want = (units + kEdWarps - 1) / kEdWarps, cap = (long long)sms * 8;
+  const int grid = int(want < cap ? want : cap);
   if (table_bf16 && out_bf16) embed_dropout_forward_kernel<__nv_bfloat16, __nv_bfloat16><<<grid, kEdThreads, 0, st>>>(p);
   else if (table_bf16) embed_dropout_forward_kernel<__nv_bfloat16, float><<<grid, kEdThreads, 0, st>>>(p);
   else if (out_bf16) embed_dropout_forward_kernel<float, __nv_bfloat16><<<grid, kEdThreads, 0, st>>>(p);
   else embed_dropout_forward_kernel<float, float><<<grid, kEdThreads, 0, st>>>(p);
 }
 
-size_t embed_dropout_workspace_bytes(long long, long long, long long) { return 256; }
+namespace {
 
-cudaError_t launch_embed_dropout_backward(const EmbedDropParams& p, bool grad_bf16, void*, int sms, cudaStream_t st) {
-  const long long cap = (long long)sms * 8;
-  const int grid = int(p.V < cap ? p.V : cap);
-  if (grad_bf16) embed_dropout_backward_kernel<__nv_bfloat16><<<grid, kEdThreads, 0, st>>>(p);
-  else embed_dropout_backward_kernel<float><<<grid, kEdThreads, 0, st>>>(p);
+struct EdLayout {
+  size_t head, lists, row[2], key[2], sid, srow, present, runs, total;
+  EdLayout(long long s, long long V) {
+    const size_t n = round256(sizeof(int) * size_t(s));
+    head = 0;
+    lists = 256;
+    size_t at = lists + round256(sizeof(int2) * kMaxLists);
+    for (int i = 0; i < 2; ++i) {
+      row[i] = at;
+      key[i] = at + n;
+      at += 2 * n;
+    }
+    sid = at;
+    srow = sid + n;
+    present = srow + n;
+    runs = present + round256(sizeof(unsigned) * size_t((V + 31) / 32));
+    total = runs + round256(sizeof(int2) * size_t(s / (kLong + 1) + 1));
+  }
+};
+constexpr size_t kSortSmem = sizeof(int) * kSortWarps * kDigits;
+
+}  // namespace
+
+size_t embed_dropout_workspace_bytes(long long s, long long V, long long) { return EdLayout(s, V).total; }
+
+cudaError_t launch_embed_dropout_backward(const EmbedDropParams& p, bool grad_bf16, void* ws, int sms,
+                                          cudaStream_t st) {
+  const EdLayout L(p.s, p.V);
+  unsigned char* w = static_cast<unsigned char*>(ws);
+  SortParams q;
+  q.ids = p.ids;
+  q.s = p.s;
+  q.V = p.V;
+  q.padding_id = p.padding_id;
+  const int parts = sms < kMaxLists ? sms : kMaxLists;
+  q.range = int(((p.V + parts - 1) / parts + 31) / 32 * 32);
+  for (int i = 0; i < 2; ++i) {
+    q.row[i] = reinterpret_cast<int*>(w + L.row[i]);
+    q.key[i] = reinterpret_cast<int*>(w + L.key[i]);
+  }
+  q.sorted_id = reinterpret_cast<int*>(w + L.sid);
+  q.sorted_row = reinterpret_cast<int*>(w + L.srow);
+  q.present = reinterpret_cast<unsigned*>(w + L.present);
+  q.runs = reinterpret_cast<int2*>(w + L.runs);
+  q.lists = reinterpret_cast<int2*>(w + L.lists);
+  q.head = reinterpret_cast<SortHead*>(w + L.head);
+  const int ctas = int((p.V + q.range - 1) / q.range);
+  embed_sort_kernel<<<ctas, kSortThreads, kSortSmem, st>>>(q);
+  SumParams u;
+  u.e = p;
+  u.id = q.sorted_id;
+  u.row = q.sorted_row;
+  u.present = q.present;
+  u.runs = q.runs;
+  u.lists = q.lists;
+  u.nlists = ctas;
+  u.head = q.head;
+  const int grid = sms * 2;
+  if (grad_bf16) embed_sum_kernel<__nv_bfloat16><<<grid, kEdThreads, 0, st>>>(u);
+  else embed_sum_kernel<float><<<grid, kEdThreads, 0, st>>>(u);
   return cudaGetLastError();
+}
+
+cudaError_t set_embed_dropout_smem() {
+  return cudaFuncSetAttribute(embed_sort_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, int(kSortSmem));
 }
 
 }  // namespace vpce

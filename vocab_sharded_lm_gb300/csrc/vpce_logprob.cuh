@@ -40,6 +40,8 @@ struct LogprobBwdParams {
   int top;
   const long long* top_ids;  // [s][top]
   const float* g_top;        // [s][top]
+  int chunks;                // set by the launch: chunks of a row,
+  int first[VPCE_MAX_SHARDS + 1];  // and the first one of each shard
 };
 
 // Order-preserving keys of fp32 values: a NaN of either sign is the largest
@@ -61,6 +63,6 @@ __device__ __forceinline__ float max_nan(float a, float b) {
 template <typename T>
 void launch_logprob_forward(LogprobParams p, int sms, cudaStream_t st);
 template <typename T>
-void launch_logprob_backward(const LogprobBwdParams& p, int sms, cudaStream_t st);
+void launch_logprob_backward(LogprobBwdParams p, int sms, cudaStream_t st);
 
 }  // namespace vpce
