@@ -949,7 +949,7 @@ vpce_status vpce_embedding_dropout_forward(const void* const* table_shards, vpce
   p.out = static_cast<unsigned char*>(out);
   p.ld_out_bytes = ldo * ob;
   p.flag = flag_out;
-  launch_embed_dropout_forward(p, dtype == VPCE_BF16, out_dtype == VPCE_BF16, sms, cs);
+  launch_embed_dropout_forward(p, dtype == VPCE_BF16, out_dtype == VPCE_BF16, cs);
   return launch_status();
 }
 

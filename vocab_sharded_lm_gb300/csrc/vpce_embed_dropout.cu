@@ -8,14 +8,17 @@
 //
 // Gradient: dE[v, c] = f sum over the rows r of token v, ascending, of
 // m(r, c) g[r, c].  Two launches.
-//   sort   Each CTA owns a range of ids.  It reads all ids once to count the
-//          tokens below its range (its place in the sorted order) and once to
-//          collect its own in row order, and sorts those by a stable counting
-//          sort in shared memory: no global sort passes and no grid barrier.
-//   sum    A persistent grid: runs of more than kLong rows a CTA at a time
-//          (its warps sum contiguous slices, added in order), then groups of
-//          16 sorted rows a warp at a time, all 16 rows' loads in flight, then,
-//          when the table is overwritten, the rows of ids that do not occur.
+//   sort   CTA b owns the ids congruent to b (so that frequent ids, which are
+//          neighbours in most vocabularies, spread).  It reads all ids once to
+//          count the tokens of the CTAs before it (its place in the sorted
+//          order) and once to collect its own in row order, and sorts those by
+//          a stable counting sort in shared memory: no passes over the whole
+//          batch and no grid barrier.
+//   sum    A warp per task of 256 columns: a segment of at most 128 rows of a
+//          run longer than kLong (the last segment to finish adds a run's
+//          partial sums in order), or the runs that start in 16 sorted rows, up
+//          to 16 rows' loads in flight.  Then, when the table is overwritten,
+//          the rows of ids that do not occur.
 #include "vpce_embed_dropout.cuh"
 
 namespace vpce {
@@ -115,45 +118,47 @@ __device__ __forceinline__ void drop8(float (&x)[8], const uint4& bits, unsigned
 // ---------------------------------------------------------------------------
 // forward
 // ---------------------------------------------------------------------------
-constexpr int kEfBlocks = 8;  // 8-column blocks per lane and unit
+constexpr int kEfBlocks = 4;  // 8-column blocks per lane and unit
 
-// One unit per warp at a time: kEfBlocks * 256 columns of a row.
+// One unit per warp: kEfBlocks * 256 columns of a row.
 template <typename TI, typename TO>
 __global__ void __launch_bounds__(kEdThreads) embed_dropout_forward_kernel(const __grid_constant__ EmbedDropParams p) {
   constexpr int IB = Elem<TI>::kBytes, OB = Elem<TO>::kBytes;
   const int lane = threadIdx.x & 31;
-  const unsigned long long seed = p.drop ? p.rng[0] : 0, offset = p.drop ? p.rng[1] : 0;
-  const unsigned limit = p.drop << 16;
   const long long per = (p.h + 256 * kEfBlocks - 1) / (256 * kEfBlocks);
-  const long long units = p.s * per, nw = (long long)gridDim.x * kEdWarps;
-  for (long long w = (long long)blockIdx.x * kEdWarps + (threadIdx.x >> 5); w < units; w += nw) {
-    const long long r = per == 1 ? w : w / per;
-    const long long c0 = (w - r * per) * (256 * kEfBlocks) + lane * 8;
-    const long long id = __ldg(p.ids + r);
-    const bool pad = id == p.padding_id, in = id >= 0 && id < p.V, live = in && !pad;
-    if (!in && !pad && lane == 0 && p.flag != nullptr) atomicOr(p.flag, VPCE_FLAG_BAD_TARGET);
-    const int i = live ? shard_holding(p.sh, p.t, id) : 0;
-    const unsigned char* src = live ? p.sh.ptr[i] + (id - p.sh.start[i]) * p.sh.ld_bytes[i] : nullptr;
-    unsigned char* dst = p.out + r * p.ld_out_bytes;
-    const bool vi = (reinterpret_cast<uintptr_t>(src) & 15) == 0, vo = (reinterpret_cast<uintptr_t>(dst) & 15) == 0;
-    Eight<TI> q[kEfBlocks];
+  const long long w = (long long)blockIdx.x * kEdWarps + (threadIdx.x >> 5);
+  const long long r = w / per;
+  if (r >= p.s) return;
+  const long long c0 = (w - r * per) * (256 * kEfBlocks) + lane * 8;
+  const long long id = __ldg(p.ids + r);
+  const bool pad = id == p.padding_id, in = id >= 0 && id < p.V, live = in && !pad;
+  if (!in && !pad && lane == 0 && p.flag != nullptr) atomicOr(p.flag, VPCE_FLAG_BAD_TARGET);
+  const int i = live ? shard_holding(p.sh, p.t, id) : 0;
+  const unsigned char* src = live ? p.sh.ptr[i] + (id - p.sh.start[i]) * p.sh.ld_bytes[i] : nullptr;
+  unsigned char* dst = p.out + r * p.ld_out_bytes;
+  const bool vi = (reinterpret_cast<uintptr_t>(src) & 15) == 0, vo = (reinterpret_cast<uintptr_t>(dst) & 15) == 0;
+  Eight<TI> q[kEfBlocks];
 #pragma unroll
-    for (int k = 0; k < kEfBlocks; ++k) {
-      const long long c = c0 + 256 * k;
-      if (live && c < p.h) load8(q[k], src + c * IB, int(min(8LL, p.h - c)), vi);
-      else clear(q[k]);
-    }
+  for (int k = 0; k < kEfBlocks; ++k) {
+    const long long c = c0 + 256 * k;
+    if (live && c < p.h) load8(q[k], src + c * IB, int(min(8LL, p.h - c)), vi);
+    else clear(q[k]);
+  }
+  DropKey key;
+  if (p.drop) key.set(p.rng);
+  const unsigned limit = p.drop << 16;
 #pragma unroll
-    for (int k = 0; k < kEfBlocks; ++k) {
-      const long long c = c0 + 256 * k;
-      if (c >= p.h) break;
-      float x[8];
-      q[k].get(x);
+  for (int k = 0; k < kEfBlocks; ++k) {
+    const long long c = c0 + 256 * k;
+    if (c >= p.h) break;
+    uint4 bits = make_uint4(~0u, ~0u, ~0u, ~0u);
+    if (p.drop && live) bits = drop_block(key, r, unsigned(c >> 3));
+    float x[8];
+    q[k].get(x);
 #pragma unroll
-      for (int j = 0; j < 8; ++j) x[j] *= p.factor;
-      if (p.drop && live) drop8(x, drop_block(seed, offset, r, unsigned(c >> 3)), limit);
-      store8(dst + c * OB, x, int(min(8LL, p.h - c)), vo, TO());
-    }
+    for (int j = 0; j < 8; ++j) x[j] *= p.factor;
+    drop8(x, bits, limit);
+    store8(dst + c * OB, x, int(min(8LL, p.h - c)), vo, TO());
   }
 }
 
@@ -165,12 +170,19 @@ constexpr int kSortWarps = kSortThreads / 32;
 constexpr int kDigits = 1024;  // bins of one counting pass
 constexpr int kLong = 64;      // runs with more rows are summed by a whole CTA
 constexpr int kGroup = 16;     // sorted rows per warp task
-constexpr int kMaxLists = 1024;  // CTAs of the sort, at most
+constexpr int kSeg = 128;      // rows of a long run per warp task
+constexpr int kOwnBits = 7;    // the sort's CTAs: 2^kOwnBits
+constexpr int kOwners = 1 << kOwnBits;
 template <typename T> constexpr int kInFlight = sizeof(T) == 2 ? 16 : 8;  // rows' loads per lane
 
+struct Segment {
+  int at, rows;      // its first sorted position, its rows
+  int first, count;  // the run's first segment and how many it has
+};
+
 struct SortHead {
-  long long valid;              // tokens with a gradient
-  unsigned long long taken[3];  // the sum's task counters
+  long long valid;           // tokens with a gradient
+  unsigned long long taken;  // the zero rows' task counter
 };
 
 struct SortParams {
@@ -178,14 +190,17 @@ struct SortParams {
   long long s;
   long long V;
   long long padding_id;
-  int range;          // ids per CTA, a multiple of 32
+  int range;          // local ids (id / kOwners) of a CTA
+  int words;          // of a CTA's part of `present`
+  int blocks;         // column blocks of the sum
   int* row[2];        // [s] rows, before and after a pass
-  int* key[2];        // [s] ids less the CTA's first
+  int* key[2];        // [s] local ids
   int* sorted_id;     // [s]
   int* sorted_row;    // [s]
-  unsigned* present;  // bit per id
-  int2* runs;         // long runs, (first position, rows); a CTA's from its first position / (kLong + 1) on
-  int2* lists;        // per CTA: first of its long runs, how many
+  unsigned* present;  // [kOwners][words], a bit per local id
+  Segment* segs;      // of the long runs; a CTA's from its first position / 64 on
+  int2* lists;        // per CTA: first of its segments, how many
+  int* done;          // [segments][blocks], cleared at each run's first segment
   SortHead* head;
 };
 
@@ -212,10 +227,13 @@ __device__ __forceinline__ int cta_scan(int v, int* tmp, int& total) {
 
 __global__ void __launch_bounds__(kSortThreads, 1) embed_sort_kernel(const __grid_constant__ SortParams p) {
   extern __shared__ int count[];  // [warps][kDigits]
-  __shared__ int nlong;
+  __shared__ int nseg;
   __shared__ int tmp[kSortWarps], wmine[kSortWarps], wlow[kSortWarps];
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-  const long long lo = (long long)blockIdx.x * p.range, hi = min(p.V, lo + p.range);
+  const int own = blockIdx.x;
+  auto owner = [&](long long id) {  // kOwners and more: no gradient
+    return id >= 0 && id < p.V && id != p.padding_id ? int(id) & (kOwners - 1) : kOwners;
+  };
   // this warp's slice of the ids
   const long long per = ((p.s + kSortWarps - 1) / kSortWarps + 31) / 32 * 32;
   const long long r0 = warp * per, r1 = min(p.s, r0 + per);
@@ -223,9 +241,9 @@ __global__ void __launch_bounds__(kSortThreads, 1) embed_sort_kernel(const __gri
 #pragma unroll 4
   for (long long r = r0 + lane; r < r1; r += 32) {
     const long long id = __ldg(p.ids + r);
-    const bool ok = id != p.padding_id;
-    mine += ok && id >= lo && id < hi;
-    low += ok && id >= 0 && id < lo;
+    const int o = owner(id);
+    mine += o == own;
+    low += o < own;
   }
   mine = __reduce_add_sync(kFull, mine);
   low = __reduce_add_sync(kFull, low);
@@ -233,9 +251,10 @@ __global__ void __launch_bounds__(kSortThreads, 1) embed_sort_kernel(const __gri
     wmine[warp] = mine;
     wlow[warp] = low;
   }
-  for (int i = tid; i < int((hi - lo + 31) / 32); i += kSortThreads) p.present[lo / 32 + i] = 0u;
-  if (blockIdx.x == 0 && tid < 3) p.head->taken[tid] = 0;
-  if (tid == 0) nlong = 0;
+  unsigned* present = p.present + (long long)own * p.words;
+  for (int i = tid; i < p.words; i += kSortThreads) present[i] = 0u;
+  if (own == 0 && tid == 0) p.head->taken = 0;
+  if (tid == 0) nseg = 0;
   __syncthreads();
   int n = 0, at = 0;
   long long base = 0;
@@ -244,21 +263,21 @@ __global__ void __launch_bounds__(kSortThreads, 1) embed_sort_kernel(const __gri
     n += wmine[w];
     base += wlow[w];
   }
-  if (blockIdx.x == gridDim.x - 1 && tid == 0) p.head->valid = base + n;
+  if (own == kOwners - 1 && tid == 0) p.head->valid = base + n;
   if (n == 0) {
-    if (tid == 0) p.lists[blockIdx.x] = make_int2(0, 0);
+    if (tid == 0) p.lists[own] = make_int2(0, 0);
     return;
   }
-  const int first_run = int(base / (kLong + 1));  // n tokens hold at most n / (kLong + 1) long runs
+  const int first_seg = int(base / kLong);  // n tokens hold at most n / kLong segments of long runs
   int *key = p.key[0] + base, *row = p.row[0] + base, *key2 = p.key[1] + base, *row2 = p.row[1] + base;
   if (mine > 0) {
     for (long long r = r0; r < r1; r += 32) {
       const long long id = r + lane < r1 ? __ldg(p.ids + r + lane) : -1;
-      const bool in = id != p.padding_id && id >= lo && id < hi && r + lane < r1;
+      const bool in = owner(id) == own;
       const unsigned m = __ballot_sync(kFull, in);
       if (in) {
         const int k = at + __popc(m & ((1u << lane) - 1u));
-        key[k] = int(id - lo);
+        key[k] = int(id >> kOwnBits);
         row[k] = int(r) + lane;
       }
       at += __popc(m);
@@ -319,10 +338,10 @@ __global__ void __launch_bounds__(kSortThreads, 1) embed_sort_kernel(const __gri
   // sorted ids and rows, the ids that occur, the long runs
   for (int k = tid; k < n; k += kSortThreads) {
     const int kk = key[k];
-    p.sorted_id[base + k] = int(lo) + kk;
+    p.sorted_id[base + k] = (kk << kOwnBits) + own;
     p.sorted_row[base + k] = row[k];
     if (k == 0 || key[k - 1] != kk) {
-      atomicOr(p.present + (lo + kk) / 32, 1u << (kk & 31));
+      atomicOr(present + kk / 32, 1u << (kk & 31));
       if (k + kLong < n && key[k + kLong] == kk) {
         int a = k + kLong, b = n;  // the run's end is in (a, b]
         while (b - a > 1) {
@@ -330,12 +349,16 @@ __global__ void __launch_bounds__(kSortThreads, 1) embed_sort_kernel(const __gri
           if (key[mid] == kk) a = mid;
           else b = mid;
         }
-        p.runs[first_run + atomicAdd(&nlong, 1)] = make_int2(int(base) + k, b - k);
+        const int rows = b - k, count = (rows + kSeg - 1) / kSeg;
+        const int first = first_seg + atomicAdd(&nseg, count);
+        for (int i = 0; i < count; ++i)
+          p.segs[first + i] = Segment{int(base) + k + i * kSeg, min(kSeg, rows - i * kSeg), first, count};
+        for (int i = 0; i < p.blocks; ++i) p.done[(long long)first * p.blocks + i] = 0;
       }
     }
   }
   __syncthreads();
-  if (tid == 0) p.lists[blockIdx.x] = make_int2(first_run, nlong);
+  if (tid == 0) p.lists[own] = make_int2(first_seg, nseg);
 }
 
 // ---------------------------------------------------------------------------
@@ -346,9 +369,11 @@ struct SumParams {
   const int* id;
   const int* row;
   const unsigned* present;
-  const int2* runs;
+  int words;
+  const Segment* segs;
   const int2* lists;
-  int nlists;
+  int* done;
+  float* part;        // [segments][blocks * 256] partial sums
   SortHead* head;
 };
 
@@ -384,7 +409,7 @@ __device__ __forceinline__ float* table_row(const EmbedDropParams& e, int id) {
 template <typename T>
 struct RowSource {
   const EmbedDropParams& e;
-  unsigned long long seed, offset;
+  DropKey key;
   unsigned limit;
   long long c;  // the lane's first column
   int n;        // columns it has, 0..8
@@ -396,7 +421,7 @@ struct RowSource {
   __device__ __forceinline__ void add(float (&acc)[8], const Eight<T>& q, int r) const {
     float x[8];
     q.get(x);
-    if (e.drop) drop8(x, drop_block(seed, offset, r, unsigned(c >> 3)), limit);
+    if (e.drop) drop8(x, drop_block(key, r, unsigned(c >> 3)), limit);
 #pragma unroll
     for (int j = 0; j < 8; ++j) acc[j] += x[j];
   }
@@ -404,15 +429,13 @@ struct RowSource {
 
 template <typename T>
 __global__ void __launch_bounds__(kEdThreads, 2) embed_sum_kernel(const __grid_constant__ SumParams p) {
-  __shared__ float part[kEdWarps][8][32];
-  __shared__ unsigned long long task;
-  __shared__ int upto[kMaxLists];
+  __shared__ int upto[kOwners];  // segments of the lists so far
+  constexpr int kIn = kInFlight<T>;
   const EmbedDropParams& e = p.e;
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-  constexpr int kIn = kInFlight<T>;
   const int blocks = int((e.h + 255) / 256);  // column blocks of a warp
-  RowSource<T> src{e, e.drop ? e.rng[0] : 0, e.drop ? e.rng[1] : 0, e.drop << 16, 0, 0,
-                   ((reinterpret_cast<uintptr_t>(e.out) | e.ld_out_bytes) & 15) == 0};
+  RowSource<T> src{e, {}, e.drop << 16, 0, 0, ((reinterpret_cast<uintptr_t>(e.out) | e.ld_out_bytes) & 15) == 0};
+  if (e.drop) src.key.set(e.rng);
   auto columns = [&](int block) {
     src.c = (long long)block * 256 + lane * 8;
     src.n = int(max(0LL, min(8LL, e.h - src.c)));
@@ -423,79 +446,84 @@ __global__ void __launch_bounds__(kEdThreads, 2) embed_sum_kernel(const __grid_c
     float* at = row + src.c;
     if (src.n > 0) put8(at, acc, src.n, (reinterpret_cast<uintptr_t>(at) & 15) == 0, e.accumulate);
   };
-
-  // long runs: (run, column block) per CTA; warp w sums the w-th eighth of the
-  // rows, and the eighths are added in order
   if (warp == 0) {
     int carry = 0;
-    for (int i0 = 0; i0 < p.nlists; i0 += 32) {
-      int x = i0 + lane < p.nlists ? p.lists[i0 + lane].y : 0;
+#pragma unroll
+    for (int i0 = 0; i0 < kOwners; i0 += 32) {
+      int x = p.lists[i0 + lane].y;
 #pragma unroll
       for (int o = 1; o < 32; o <<= 1) {
         const int y = __shfl_up_sync(kFull, x, o);
         if (lane >= o) x += y;
       }
-      if (i0 + lane < p.nlists) upto[i0 + lane] = carry + x;
+      upto[i0 + lane] = carry + x;
       carry += __shfl_sync(kFull, x, 31);
     }
   }
   __syncthreads();
   const int valid = int(p.head->valid);
-  const unsigned long long long_tasks = (unsigned long long)upto[p.nlists - 1] * blocks;
-  while (long_tasks > 0) {
-    __syncthreads();
-    if (threadIdx.x == 0) task = atomicAdd(&p.head->taken[0], 1ull);
-    __syncthreads();
-    if (task >= long_tasks) break;
-    const int nth = int(task / blocks);
-    int l = 0;  // the list that holds it: the first with upto > nth
-    for (int step = 512; step > 0; step >>= 1)
-      if (l + step <= p.nlists - 1 && upto[l + step - 1] <= nth) l += step;
-    const int2 run = p.runs[p.lists[l].x + nth - (l > 0 ? upto[l - 1] : 0)];
-    columns(int(task % blocks));
-    const int each = (run.y + kEdWarps - 1) / kEdWarps;
-    const int k0 = run.x + min(run.y, warp * each), k1 = run.x + min(run.y, (warp + 1) * each);
+  const long long groups = (valid + kGroup - 1) / kGroup;
+  const long long nsegs = upto[kOwners - 1];
+  const long long tasks = (nsegs + groups) * blocks, nw = (long long)gridDim.x * kEdWarps;
+  // long tasks first; neighbouring warps take neighbouring columns
+  for (long long tk = (long long)blockIdx.x * kEdWarps + warp; tk < tasks; tk += nw) {
+    const long long unit = tk / blocks;
+    const int block = int(tk - unit * blocks);
+    columns(block);
     float acc[8] = {};
-    for (int k = k0; k < k1; k += 32) {
-      const int m = min(32, k1 - k);
-      const int r32 = lane < m ? p.row[k + lane] : 0;
-      for (int b = 0; b < m; b += kIn) {
-        Eight<T> q[kIn];
+    if (unit < nsegs) {
+      // a segment of a long run
+      int l = 0;  // the list that holds it: the first with upto > unit
 #pragma unroll
-        for (int j = 0; j < kIn; ++j) {
-          const int r = __shfl_sync(kFull, r32, b + j);
-          if (b + j < m) src.load(q[j], r);
-          else clear(q[j]);
-        }
+      for (int step = kOwners / 2; step > 0; step >>= 1)
+        if (upto[l + step - 1] <= unit) l += step;
+      const int slot = p.lists[l].x + int(unit) - (l > 0 ? upto[l - 1] : 0);
+      const Segment sg = p.segs[slot];
+      for (int k = 0; k < sg.rows; k += 32) {
+        const int m = min(32, sg.rows - k);
+        const int r32 = lane < m ? p.row[sg.at + k + lane] : 0;
+        for (int b = 0; b < m; b += kIn) {
+          Eight<T> q[kIn];
 #pragma unroll
-        for (int j = 0; j < kIn; ++j) {
-          const int r = __shfl_sync(kFull, r32, b + j);
-          if (b + j < m) src.add(acc, q[j], r);
+          for (int j = 0; j < kIn; ++j) {
+            const int r = __shfl_sync(kFull, r32, b + j);
+            if (b + j < m) src.load(q[j], r);
+            else clear(q[j]);
+          }
+#pragma unroll
+          for (int j = 0; j < kIn; ++j) {
+            const int r = __shfl_sync(kFull, r32, b + j);
+            if (b + j < m) src.add(acc, q[j], r);
+          }
         }
       }
-    }
+      if (sg.count > 1) {
+        // leave the partial sum; the run's last segment to get here adds them
+        const long long width = (long long)blocks * 256;
+        float4* mine = reinterpret_cast<float4*>(p.part + slot * width + src.c);
+        __stcg(mine, make_float4(acc[0], acc[1], acc[2], acc[3]));
+        __stcg(mine + 1, make_float4(acc[4], acc[5], acc[6], acc[7]));
+        __threadfence();
+        __syncwarp();
+        int arrived = 0;
+        if (lane == 0) arrived = atomicAdd(p.done + (long long)sg.first * blocks + block, 1);
+        if (__shfl_sync(kFull, arrived, 0) != sg.count - 1) continue;
+        __threadfence();
 #pragma unroll
-    for (int j = 0; j < 8; ++j) part[warp][j][lane] = acc[j];
-    __syncthreads();
-    if (warp == 0) {
-#pragma unroll
-      for (int j = 0; j < 8; ++j)
-        for (int w = 1; w < kEdWarps; ++w) acc[j] += part[w][j][lane];
-      flush(table_row(e, p.id[run.x]), acc);
+        for (int j = 0; j < 8; ++j) acc[j] = 0.f;
+#pragma unroll 4
+        for (int i = 0; i < sg.count; ++i) {
+          const float4* at = reinterpret_cast<const float4*>(p.part + (sg.first + i) * width + src.c);
+          const float4 x = __ldcg(at), y = __ldcg(at + 1);
+          acc[0] += x.x, acc[1] += x.y, acc[2] += x.z, acc[3] += x.w;
+          acc[4] += y.x, acc[5] += y.y, acc[6] += y.z, acc[7] += y.w;
+        }
+      }
+      flush(table_row(e, p.id[sg.at]), acc);
+      continue;
     }
-  }
-
-  // short runs: the runs that start in a group of 16 sorted rows
-  const int groups = (valid + kGroup - 1) / kGroup;
-  const unsigned long long short_tasks = (unsigned long long)groups * blocks;
-  while (true) {
-    unsigned long long tk = 0;
-    if (lane == 0) tk = atomicAdd(&p.head->taken[1], 1ull);
-    tk = __shfl_sync(kFull, tk, 0);
-    if (tk >= short_tasks) break;
-    const int g = int(tk / blocks) * kGroup;
-    columns(int(tk % blocks));
-    float acc[8] = {};
+    // the runs that start in a group of 16 sorted rows
+    const int g = int(unit - nsegs) * kGroup;
     float* cur = nullptr;  // table row of the run being summed
     bool done = false;
     for (int k = g; !done; k += kGroup) {
@@ -505,27 +533,22 @@ __global__ void __launch_bounds__(kEdThreads, 2) embed_sum_kernel(const __grid_c
       const int id = here ? p.id[pos] : -1;
       const int r16 = here ? p.row[pos] : 0;
       const int prev = here && pos > 0 ? p.id[pos - 1] : -1;
+      const int far = here && pos + kLong < valid ? p.id[pos + kLong] : -1;
       const bool head = here && id != prev;
-      const bool is_long = head && pos + kLong < valid && p.id[pos + kLong] == id;
-      const unsigned heads = __ballot_sync(kFull, head), longs = __ballot_sync(kFull, is_long),
+      const unsigned heads = __ballot_sync(kFull, head), longs = __ballot_sync(kFull, head && far == id),
                      heres = __ballot_sync(kFull, here);
       float* trow = head ? table_row(e, id) : nullptr;
-      // the positions to sum: from the group's first head (or, past the group,
-      // from its start) to the first head past the group or the first long run
+      // the positions to sum: from the group's first head (past the group, from
+      // the start) to the first head past the group or the first long run
       int a = 0, b = __popc(heres);
       if (k == g) {
         if (heads == 0) break;
         a = __ffs(heads) - 1;
       } else if (heads != 0) {
         b = __ffs(heads) - 1;
-        done = true;
       }
-      if (longs != 0 && __ffs(longs) - 1 < b) {  // a long run starts here: summed above
-        // the last head of the 16 (a long run reaches past them)
-        b = __ffs(longs) - 1;
-        done = true;
-      }
-      if (b < kGroup) done = true;
+      if (longs != 0) b = min(b, __ffs(longs) - 1);
+      done = b < kGroup;
       for (int part = 0; part < kGroup; part += kIn) {
         if (part >= b) break;
         Eight<T> q[kIn];
@@ -554,19 +577,25 @@ __global__ void __launch_bounds__(kEdThreads, 2) embed_sum_kernel(const __grid_c
   }
   if (e.accumulate) return;
 
-  // rows of ids that do not occur: 8 ids per warp task
-  const long long zero_tasks = (e.V + 7) / 8;
+  // rows of ids that do not occur: about 64 KB per warp task
+  const int each = int(max(1LL, min(32LL, 16384 / e.h)));
+  const long long zero_tasks = (e.V + each - 1) / each;
   while (true) {
     unsigned long long got = 0;
-    if (lane == 0) got = atomicAdd(&p.head->taken[2], 1ull);
+    if (lane == 0) got = atomicAdd(&p.head->taken, 1ull);
     const long long tk = (long long)__shfl_sync(kFull, got, 0);
     if (tk >= zero_tasks) break;
-    const unsigned bits = p.present[tk / 4] >> (8 * (tk & 3));
-    for (int j = 0; j < 8; ++j) {
-      const long long id = tk * 8 + j;
-      if (id >= e.V) break;
-      if (bits >> j & 1u) continue;
-      float* row = table_row(e, int(id));
+    const long long mine = tk * each + lane;
+    bool absent = false;
+    if (lane < each && mine < e.V) {
+      const int local = int(mine >> kOwnBits);
+      absent = !(p.present[(mine & (kOwners - 1)) * p.words + local / 32] >> (local & 31) & 1u);
+    }
+    unsigned todo = __ballot_sync(kFull, absent);
+    while (todo != 0) {
+      const int l = __ffs(todo) - 1;
+      todo &= todo - 1;
+      float* row = table_row(e, int(tk * each + l));
       // 16-byte stores between ragged ends
       const int head = min(int(e.h), int((16 - (reinterpret_cast<uintptr_t>(row) & 15)) & 15) / 4);
       const int nv = (int(e.h) - head) / 4, tail = int(e.h) - head - 4 * nv;
@@ -581,11 +610,9 @@ __global__ void __launch_bounds__(kEdThreads, 2) embed_sum_kernel(const __grid_c
 
 }  // namespace
 
-void launch_embed_dropout_forward(const EmbedDropParams& p, bool table_bf16, bool out_bf16, int sms,
-                                  cudaStream_t st) {
+void launch_embed_dropout_forward(const EmbedDropParams& p, bool table_bf16, bool out_bf16, cudaStream_t st) {
   const long long units = p.s * ((p.h + 256 * kEfBlocks - 1) / (256 * kEfBlocks));
-  const long long want = (units + kEdWarps - 1) / kEdWarps, cap = (long long)sms * 8;
-  const int grid = int(want < cap ? want : cap);
+  const unsigned grid = unsigned((units + kEdWarps - 1) / kEdWarps);
   if (table_bf16 && out_bf16) embed_dropout_forward_kernel<__nv_bfloat16, __nv_bfloat16><<<grid, kEdThreads, 0, st>>>(p);
   else if (table_bf16) embed_dropout_forward_kernel<__nv_bfloat16, float><<<grid, kEdThreads, 0, st>>>(p);
   else if (out_bf16) embed_dropout_forward_kernel<float, __nv_bfloat16><<<grid, kEdThreads, 0, st>>>(p);
@@ -595,12 +622,16 @@ void launch_embed_dropout_forward(const EmbedDropParams& p, bool table_bf16, boo
 namespace {
 
 struct EdLayout {
-  size_t head, lists, row[2], key[2], sid, srow, present, runs, total;
-  EdLayout(long long s, long long V) {
-    const size_t n = round256(sizeof(int) * size_t(s));
+  size_t head, lists, row[2], key[2], sid, srow, present, segs, done, part, total;
+  int range, words, blocks;
+  EdLayout(long long s, long long V, long long h) {
+    const size_t n = round256(sizeof(int) * size_t(s)), slots = size_t(s / kLong + 1);
+    range = int((V + kOwners - 1) / kOwners);
+    words = (range + 31) / 32;
+    blocks = int((h + 255) / 256);
     head = 0;
     lists = 256;
-    size_t at = lists + round256(sizeof(int2) * kMaxLists);
+    size_t at = lists + round256(sizeof(int2) * kOwners);
     for (int i = 0; i < 2; ++i) {
       row[i] = at;
       key[i] = at + n;
@@ -609,27 +640,30 @@ struct EdLayout {
     sid = at;
     srow = sid + n;
     present = srow + n;
-    runs = present + round256(sizeof(unsigned) * size_t((V + 31) / 32));
-    total = runs + round256(sizeof(int2) * size_t(s / (kLong + 1) + 1));
+    segs = present + round256(sizeof(unsigned) * size_t(kOwners) * size_t(words));
+    done = segs + round256(sizeof(Segment) * slots);
+    part = done + round256(sizeof(int) * slots * size_t(blocks));
+    total = part + sizeof(float) * slots * size_t(blocks) * 256;
   }
 };
 constexpr size_t kSortSmem = sizeof(int) * kSortWarps * kDigits;
 
 }  // namespace
 
-size_t embed_dropout_workspace_bytes(long long s, long long V, long long) { return EdLayout(s, V).total; }
+size_t embed_dropout_workspace_bytes(long long s, long long V, long long h) { return EdLayout(s, V, h).total; }
 
 cudaError_t launch_embed_dropout_backward(const EmbedDropParams& p, bool grad_bf16, void* ws, int sms,
                                           cudaStream_t st) {
-  const EdLayout L(p.s, p.V);
+  const EdLayout L(p.s, p.V, p.h);
   unsigned char* w = static_cast<unsigned char*>(ws);
   SortParams q;
   q.ids = p.ids;
   q.s = p.s;
   q.V = p.V;
   q.padding_id = p.padding_id;
-  const int parts = sms < kMaxLists ? sms : kMaxLists;
-  q.range = int(((p.V + parts - 1) / parts + 31) / 32 * 32);
+  q.range = L.range;
+  q.words = L.words;
+  q.blocks = L.blocks;
   for (int i = 0; i < 2; ++i) {
     q.row[i] = reinterpret_cast<int*>(w + L.row[i]);
     q.key[i] = reinterpret_cast<int*>(w + L.key[i]);
@@ -637,19 +671,21 @@ cudaError_t launch_embed_dropout_backward(const EmbedDropParams& p, bool grad_bf
   q.sorted_id = reinterpret_cast<int*>(w + L.sid);
   q.sorted_row = reinterpret_cast<int*>(w + L.srow);
   q.present = reinterpret_cast<unsigned*>(w + L.present);
-  q.runs = reinterpret_cast<int2*>(w + L.runs);
+  q.segs = reinterpret_cast<Segment*>(w + L.segs);
   q.lists = reinterpret_cast<int2*>(w + L.lists);
+  q.done = reinterpret_cast<int*>(w + L.done);
   q.head = reinterpret_cast<SortHead*>(w + L.head);
-  const int ctas = int((p.V + q.range - 1) / q.range);
-  embed_sort_kernel<<<ctas, kSortThreads, kSortSmem, st>>>(q);
+  embed_sort_kernel<<<kOwners, kSortThreads, kSortSmem, st>>>(q);
   SumParams u;
   u.e = p;
   u.id = q.sorted_id;
   u.row = q.sorted_row;
   u.present = q.present;
-  u.runs = q.runs;
+  u.words = L.words;
+  u.segs = q.segs;
   u.lists = q.lists;
-  u.nlists = ctas;
+  u.done = q.done;
+  u.part = reinterpret_cast<float*>(w + L.part);
   u.head = q.head;
   const int grid = sms * 2;
   if (grad_bf16) embed_sum_kernel<__nv_bfloat16><<<grid, kEdThreads, 0, st>>>(u);
