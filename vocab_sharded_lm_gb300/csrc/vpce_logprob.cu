@@ -12,10 +12,13 @@
 // logit is itself 2^20 / c or more from 0 (filled with the type's lowest value,
 // say) are summed again by subtraction (sum_far).
 //
-// A row is cut into pieces (part of one shard, 16-byte vectors).  The warp
-// that takes a piece streams it into registers and leaves, per lane, (max, S,
-// U) of the vectors that lane read.  The warp that completes a row folds these
-// in a fixed order whatever warp made them, so results repeat bit for bit.
+// A row is cut into pieces (part of one shard, 16-byte vectors).  A streaming
+// warp takes pieces from a shared counter and reads them through two 4 KB
+// buffers of its own that the bulk-copy engine refills while it sums, so the
+// bytes in flight do not depend on registers or on the arithmetic between
+// loads.  It leaves the piece's (max, S, U); the warp that finishes the row
+// folds these in a fixed order whatever warp made them, so results repeat bit
+// for bit.
 //
 // Top alternatives without a second pass: the maxima of a lane's quarters of a
 // piece (batches of 4 vectors a step) are kept with the partials.  The top-th
@@ -34,22 +37,40 @@ namespace {
 
 namespace cg = cooperative_groups;
 
-constexpr int kLpStream = 13;      // warps that stream pieces
-constexpr int kLpFinish = 3;       // warps that finish rows
+constexpr int kLpStream = 16;      // warps that stream pieces
+constexpr int kLpFinish = 4;       // warps that finish rows
 constexpr int kLpThreads = 32 * (kLpStream + kLpFinish);  // one CTA per SM
+constexpr int kLpVecs = 8;         // vectors per lane and unit
+constexpr int kLpUnit = 32 * kLpVecs;             // vectors per unit: one buffer
+constexpr int kLpStep = 2 * kLpUnit;              // vectors per step: four batches of 4 vectors a lane
+constexpr int kLpRing = kLpStream * 2 * kLpUnit * 16;  // bytes of all buffers
 constexpr int kLpMaxPieces = 64;   // pieces per row (as many as shards can be)
-constexpr int kLpPieces = 40;      // aimed at: leaves room for 6 rows' partials
+constexpr int kLpPieces = 40;      // aimed at
 constexpr int kLpMaxSlots = 8;     // rows with partials in shared memory at a time, at most
-constexpr int kLpPartBytes = 32 * int(sizeof(float4) + 2 * sizeof(float));  // a piece's partials
-constexpr int kLpPartSmem = 192 * 1024;
+constexpr int kLpPartSmem = 88 * 1024;  // their room
 constexpr int kLpCand = 128;       // candidate words per warp
 constexpr int kLpList = 128;       // batches listed per warp before they are re-read
 constexpr float kLpFloor = -256.f;      // 2^v is 0 here
 constexpr float kLpFar = 1048576.f;      // |K| from here on: K's rounding is no longer small (sum_far)
 
-template <typename T> struct LpShape;
-template <> struct LpShape<__nv_bfloat16> { static constexpr int kVecs = 16; };
-template <> struct LpShape<float> { static constexpr int kVecs = 16; };
+// The maxima of a lane's four batches of a piece; bf16 ones are kept as they
+// are (a maximum is one of its values).
+template <typename T> struct BatchMax;
+template <> struct BatchMax<float> {
+  float4 v;
+  __device__ __forceinline__ void set(const float4& x) { v = x; }
+  __device__ __forceinline__ float4 get() const { return v; }
+};
+template <> struct BatchMax<__nv_bfloat16> {
+  uint2 v;
+  __device__ __forceinline__ void set(const float4& x) {
+    v.x = __float_as_uint(x.x) >> 16 | (__float_as_uint(x.y) & 0xffff0000u);
+    v.y = __float_as_uint(x.z) >> 16 | (__float_as_uint(x.w) & 0xffff0000u);
+  }
+  __device__ __forceinline__ float4 get() const {
+    return make_float4(bf16_lo(v.x), bf16_hi(v.x), bf16_lo(v.y), bf16_hi(v.y));
+  }
+};
 
 // Part of a row: vectors [off, off + p.len) of its shard's 16-byte aligned
 // body; the shard's first piece also takes the elements before and after the
@@ -102,6 +123,12 @@ __device__ __forceinline__ uint4 lp_pad(float) {
   return make_uint4(0xff800000u, 0xff800000u, 0xff800000u, 0xff800000u);
 }
 
+// the value of a key
+__device__ __forceinline__ float key_value(unsigned k) {
+  if (k == 0xffffffffu) return __int_as_float(0x7fc00000);
+  return __uint_as_float(k & 0x80000000u ? k & 0x7fffffffu : ~k);
+}
+
 // The offset of a maximum: c m, never below -2^20 (which a NaN, or nothing
 // unmasked, gives).  Rounded here: a product fused into a later difference
 // would not be the offset that the sums were formed with.
@@ -144,11 +171,10 @@ __device__ __forceinline__ void add_vec(const uint4& v, float low, f32x2 c, f32x
   add_pair(fmaxf(__uint_as_float(v.x), low), fmaxf(__uint_as_float(v.y), low), c, nk, s[0], u[0]);
   add_pair(fmaxf(__uint_as_float(v.z), low), fmaxf(__uint_as_float(v.w), low), c, nk, s[1], u[1]);
 }
-// the floor of a logit
-__device__ __forceinline__ __nv_bfloat162 low_of(float c, __nv_bfloat16) {
-  return __float2bfloat162_rn(-2.f * kLpFar / c);
+__device__ __forceinline__ __nv_bfloat162 packed_low(float floor, __nv_bfloat16) {
+  return __float2bfloat162_rn(floor);
 }
-__device__ __forceinline__ float low_of(float c, float) { return -2.f * kLpFar / c; }
+__device__ __forceinline__ float packed_low(float floor, float) { return floor; }
 
 // The row segment of a shard: 16-byte aligned body and ragged ends.
 struct Seg {
@@ -179,19 +205,14 @@ __device__ __forceinline__ int ragged_column(const Seg& q, int l) {
   return -1;
 }
 
-// Half a step of a piece (H vectors a lane): its sums, and the maxima of its
-// two batches.
-template <typename T, int H>
-__device__ __forceinline__ void half_stats(const uint4 (&q)[H], Acc& a, float& m0, float& m1, float c) {
-  m0 = max_nan(m0, vecs_max<H / 2>(q, T()));
-  m1 = max_nan(m1, vecs_max<H / 2>(q + H / 2, T()));
-  const float nk = offset_of(max_nan(m0, m1), c);
-  if (nk > a.k) a.raise(nk);
+// A unit's sums, its batches' maxima m0 and m1 known and the offset raised.
+template <typename T>
+__device__ __forceinline__ void unit_sums(const uint4 (&q)[kLpVecs], Acc& a, float c, float floor) {
   const f32x2 cc = f2_pack(c, c), off = f2_pack(-a.k, -a.k);
-  const auto low = low_of(c, T());
+  const auto low = packed_low(floor, T());
   f32x2 s[2] = {f2_pack(a.s, 0.f), f2_pack(0.f, 0.f)}, u[2] = {f2_pack(a.u, 0.f), f2_pack(0.f, 0.f)};
 #pragma unroll
-  for (int j = 0; j < H; ++j) add_vec(q[j], low, cc, off, s, u, T());
+  for (int j = 0; j < kLpVecs; ++j) add_vec(q[j], low, cc, off, s, u, T());
   float x0, x1;
   f2_unpack(f2_add(s[0], s[1]), x0, x1);
   a.s = x0 + x1;
@@ -204,14 +225,6 @@ template <typename T>
 __device__ __forceinline__ float ragged_value(const Seg& g, int lane) {
   const int col = ragged_column<T>(g, lane);
   return col >= 0 ? Elem<T>::load(g.addr + (long long)col * Elem<T>::kBytes) : -INFINITY;
-}
-__device__ __forceinline__ void add_ragged(float x, Acc& a, float& m0, float c) {
-  m0 = max_nan(m0, x);
-  const float nk = offset_of(x, c);
-  if (nk > a.k) a.raise(nk);
-  const float v = fmaf(fmaxf(x, low_of(c, 0.f)), c, -a.k), e = ex2(v);
-  a.s += e;
-  a.u = fmaf(v, e, a.u);
 }
 
 // S and U of a row relative to its largest logit M, by subtraction, for rows
@@ -240,11 +253,6 @@ __device__ __noinline__ float2 sum_far(const LogprobParams& p, long long row, fl
 // ---------------------------------------------------------------------------
 // top alternatives
 // ---------------------------------------------------------------------------
-__device__ __forceinline__ float key_value(unsigned k) {
-  if (k == 0xffffffffu) return __int_as_float(0x7fc00000);
-  return __uint_as_float(k & 0x80000000u ? k & 0x7fffffffu : ~k);
-}
-
 // Sorts n candidates (at most 32 W) and keeps the first `top`, in place.
 template <int W>
 __device__ __forceinline__ void rank_words(unsigned long long* cand, int n, int top, int lane) {
@@ -304,7 +312,7 @@ __device__ __forceinline__ unsigned long long word(unsigned key, unsigned col) {
 // One batch of a row: number (piece, quarter, lane) as 128 piece + 32 quarter
 // + lane.  Lane l (0..3) of the four that re-read it takes vector l of the
 // batch's four in every step; lane 0 also takes the ragged element.
-template <typename T, int U>
+template <typename T>
 struct Batch {
   const uint4* src;            // the lane's vector of step 0
   int left, col;               // steps it has a vector in; its first column
@@ -315,9 +323,9 @@ struct Batch {
     const Piece pc = piece[code >> 7];
     const Seg g = segment<T>(pc, row);
     const int quarter = (code >> 5) & 3;
-    const int first = pc.off + (code & 31) + 32 * (quarter * (U / 4) + l);
+    const int first = pc.off + (code & 31) + 32 * (4 * quarter + l);
     const int end = min(pc.off + p.len, g.nv);
-    left = end > first ? (end - first + 32 * U - 1) / (32 * U) : 0;
+    left = end > first ? (end - first + kLpStep - 1) / kLpStep : 0;
     src = body<T>(g) + first;
     col = pc.col + g.head + first * Elem<T>::kPerVec;
     if (pc.off == 0 && l == 0 && quarter == 0) {
@@ -338,9 +346,9 @@ __device__ __forceinline__ float quarter_max(const float4& b, int i) {
 // batches that may beat the worst of the best so far are re-read in order, and
 // a full candidate buffer is cut to the best.  Rows with many equal logits
 // come here.
-template <typename T, int U>
-__device__ __noinline__ void find_top_any(const LogprobParams& p, const Piece* piece,
-                                          const float4* bm, long long row, unsigned bound, Scratch& w, int lane) {
+template <typename T>
+__device__ __noinline__ void find_top_any(const LogprobParams& p, const Piece* piece, const BatchMax<T>* bm,
+                                          long long row, unsigned bound, Scratch& w, int lane) {
   constexpr int EPV = Elem<T>::kPerVec;
   Best best;
   best.cand = w.cand;
@@ -349,12 +357,12 @@ __device__ __noinline__ void find_top_any(const LogprobParams& p, const Piece* p
   // a word beats the floor if its key is at least `bound`
   best.floor = ((unsigned long long)bound << 32) > 0 ? ((unsigned long long)bound << 32) - 1 : 0ull;
   for (int i = 0; i < p.pieces; ++i) {
-    const float4 b = bm[i * 32 + lane];
+    const float4 b = bm[i * 32 + lane].get();
     for (int quarter = 0; quarter < 4; ++quarter) {
       // the columns of a batch are no lower than its first vector's
       const Piece pc = piece[i];
       const unsigned low = unsigned(pc.col) +
-                           (pc.off == 0 ? 0u : unsigned(pc.off + 32 * quarter * (U / 4)) * EPV);
+                           (pc.off == 0 ? 0u : unsigned(pc.off + 128 * quarter) * EPV);
       unsigned mk = __ballot_sync(kFull, word(value_key(quarter_max(b, quarter)), low) > best.floor);
       while (mk != 0) {
         // eight batches at a time, lowest lanes first
@@ -364,7 +372,7 @@ __device__ __noinline__ void find_top_any(const LogprobParams& p, const Piece* p
           mk &= mk - 1;
           if ((lane >> 2) == k) code = i * 128 + quarter * 32 + l;
         }
-        Batch<T, U> bt;
+        Batch<T> bt;
         bt.left = 0;
         bt.rag = nullptr;
         bt.src = nullptr;
@@ -372,7 +380,7 @@ __device__ __noinline__ void find_top_any(const LogprobParams& p, const Piece* p
         if (code >= 0) bt.at(p, piece, row, code, lane & 3);
         for (int step = 0; __any_sync(kFull, step < bt.left); ++step) {
           const bool has = step < bt.left;
-          const uint4 q = has ? bt.src[step * 32 * U] : lp_pad(T());
+          const uint4 q = has ? bt.src[step * kLpStep] : lp_pad(T());
           float x[EPV];
           unpack(q, x, T());
 #pragma unroll 1
@@ -380,7 +388,7 @@ __device__ __noinline__ void find_top_any(const LogprobParams& p, const Piece* p
             float xe = x[0];
 #pragma unroll
             for (int f = 1; f < EPV; ++f) xe = e == f ? x[f] : xe;
-            best.offer(has ? word(value_key(xe), unsigned(bt.col + step * 32 * U * EPV + e)) : 0ull, lane);
+            best.offer(has ? word(value_key(xe), unsigned(bt.col + step * kLpStep * EPV + e)) : 0ull, lane);
           }
         }
         const bool has = bt.rag != nullptr;
@@ -434,12 +442,11 @@ __device__ __forceinline__ unsigned bound_key(float4 x, int top) {
   return bound;
 }
 
-template <typename T, int U>
-__device__ __forceinline__ void finish_row(const LogprobParams& p, const Piece* piece,
-                                           const float4* bm, const float* s, const float* u, long long row,
-                                           long long y, Scratch& w, int lane) {
+template <typename T>
+__device__ __forceinline__ void finish_row(const LogprobParams& p, const Piece* piece, const BatchMax<T>* bm,
+                                           const float4* sums, long long row, long long y, Scratch& w, int lane) {
   constexpr int EPV = Elem<T>::kPerVec;
-  constexpr int kIn = 6;  // batches in flight per four lanes
+  constexpr int kIn = 4;  // batches in flight per four lanes
   const float c = p.inv_t * kLog2e;
   const float nan = __int_as_float(0x7fc00000);
   const bool in = p.targets != nullptr && y >= 0 && y < p.V;
@@ -449,32 +456,17 @@ __device__ __forceinline__ void finish_row(const LogprobParams& p, const Piece* 
     while (y >= p.sh.start[i + 1]) ++i;
     zy = Elem<T>::load(p.sh.ptr[i] + row * p.sh.ld_bytes[i] + (y - p.sh.start[i]) * Elem<T>::kBytes);
   }
-  // maxima: of the lane's quarters over the pieces, and of the row
-  float4 x = make_float4(-INFINITY, -INFINITY, -INFINITY, -INFINITY);
-#pragma unroll 4
-  for (int i = 0; i < p.pieces; ++i) {
-    const float4 b = bm[i * 32 + lane];
-    x.x = max_nan(x.x, b.x);
-    x.y = max_nan(x.y, b.y);
-    x.z = max_nan(x.z, b.z);
-    x.w = max_nan(x.w, b.w);
-  }
-  float M = max_nan(max_nan(x.x, x.y), max_nan(x.z, x.w));
+  // the pieces' sums, two pieces a lane, added in a fixed tree
+  const float4 none = make_float4(-INFINITY, 0.f, 0.f, 0.f);
+  const float4 s0 = lane < p.pieces ? sums[lane] : none, s1 = lane + 32 < p.pieces ? sums[lane + 32] : none;
+  float M = max_nan(s0.x, s1.x);
 #pragma unroll
   for (int o = 16; o > 0; o >>= 1) M = max_nan(M, __shfl_xor_sync(kFull, M, o));
-
-  // the sums: lanes fold their own partials in piece order, then
-  // the warp in a fixed tree
-  float S = 0.f, W = 0.f;
   const float K = offset_of(M, c);
-#pragma unroll 4
-  for (int i = 0; i < p.pieces; ++i) {
-    const float4 b = bm[i * 32 + lane];
-    Acc a{offset_of(max_nan(max_nan(b.x, b.y), max_nan(b.z, b.w)), c), s[i * 32 + lane], u[i * 32 + lane]};
-    a.raise(K);
-    S += a.s;
-    W += a.u;
-  }
+  Acc a0{offset_of(s0.x, c), s0.y, s0.z}, a1{offset_of(s1.x, c), s1.y, s1.z};
+  a0.raise(K);
+  a1.raise(K);
+  float S = a0.s + a1.s, W = a0.u + a1.u;
 #pragma unroll
   for (int o = 16; o > 0; o >>= 1) {
     S += __shfl_xor_sync(kFull, S, o);
@@ -486,11 +478,21 @@ __device__ __forceinline__ void finish_row(const LogprobParams& p, const Piece* 
   float floor = 0.f;
   int listed = 0;
   if (p.top > 0) {
+    // maxima of the lane's quarters over the pieces
+    float4 x = make_float4(-INFINITY, -INFINITY, -INFINITY, -INFINITY);
+#pragma unroll 4
+    for (int i = 0; i < p.pieces; ++i) {
+      const float4 b = bm[i * 32 + lane].get();
+      x.x = max_nan(x.x, b.x);
+      x.y = max_nan(x.y, b.y);
+      x.z = max_nan(x.z, b.z);
+      x.w = max_nan(x.w, b.w);
+    }
     bound = bound_key(x, p.top);
     floor = key_value(bound);  // a NaN bound lists every batch
     if (lane == 0) w.n = 0;
     for (int i = 0; i < p.pieces; ++i) {
-      const float4 b = bm[i * 32 + lane];
+      const float4 b = bm[i * 32 + lane].get();
       const bool f[4] = {!(b.x < floor), !(b.y < floor), !(b.z < floor), !(b.w < floor)};
       if (!__any_sync(kFull, f[0] | f[1] | f[2] | f[3])) continue;
 #pragma unroll
@@ -504,7 +506,7 @@ __device__ __forceinline__ void finish_row(const LogprobParams& p, const Piece* 
     __syncwarp();
   }
   const bool few = listed <= kLpList;
-  Batch<T, U> bt[kIn];
+  Batch<T> bt[kIn];
   uint4 q[kIn];
   auto fetch = [&](int l0) {
 #pragma unroll
@@ -552,12 +554,12 @@ __device__ __forceinline__ void finish_row(const LogprobParams& p, const Piece* 
           float v[EPV];
           unpack(q[k], v, T());
 #pragma unroll
-          for (int e = 0; e < EPV; ++e) offer(v[e], bt[k].col + step * 32 * U * EPV + e);
+          for (int e = 0; e < EPV; ++e) offer(v[e], bt[k].col + step * kLpStep * EPV + e);
         }
         ++step;
-        if (step * 32 * U >= p.len) break;
+        if (step * kLpStep >= p.len) break;
 #pragma unroll
-        for (int k = 0; k < kIn; ++k) q[k] = step < bt[k].left ? bt[k].src[step * 32 * U] : lp_pad(T());
+        for (int k = 0; k < kIn; ++k) q[k] = step < bt[k].left ? bt[k].src[step * kLpStep] : lp_pad(T());
       }
       l0 += 8 * kIn;
       if (l0 >= listed) break;
@@ -565,7 +567,7 @@ __device__ __forceinline__ void finish_row(const LogprobParams& p, const Piece* 
     }
     // the ragged elements of the listed batches that have one
     for (int l = lane; l < listed; l += 32) {
-      Batch<T, U> b;
+      Batch<T> b;
       b.rag = nullptr;
       b.at(p, piece, row, w.list[l], 0);
       if (b.rag != nullptr) offer(Elem<T>::load(b.rag), b.ragcol);
@@ -575,7 +577,7 @@ __device__ __forceinline__ void finish_row(const LogprobParams& p, const Piece* 
   }
   if (n <= 64) rank_words<2>(w.cand, n, p.top, lane);
   else if (n <= kLpCand) rank_words<kLpCand / 32>(w.cand, n, p.top, lane);
-  else find_top_any<T, U>(p, piece, bm, row, bound, w, lane);
+  else find_top_any<T>(p, piece, bm, row, bound, w, lane);
   if (lane < p.top) {
     const unsigned long long best = w.cand[lane];
     p.top_ids[row * p.top + lane] = (long long)unsigned(~unsigned(best));
@@ -601,24 +603,22 @@ __device__ __forceinline__ void cut_row(const LogprobParams& p, Piece* piece) {
 // Persistent form: a CTA per row at a time.  The streaming warps take pieces
 // from a shared counter, run ahead into the next rows and leave partials in
 // one of p.slots places; the finishing warps take the complete rows in turn.
-// Finishing a row is a chain of dependent steps (10 to 15 us, against 5.7 us
-// to stream a 256 KB row), so three rows are finished at a time; finished by
-// the streaming warps themselves, the same steps cost the stream its registers.
+// Finishing a row is a chain of dependent steps, longer than streaming one, so
+// several rows are finished at a time; done by the streaming warps themselves,
+// the same steps cost the stream its registers.
 template <typename T>
 __global__ void __launch_bounds__(kLpThreads, 1)
     logprob_forward_kernel(const __grid_constant__ LogprobParams p) {
-  constexpr int U = LpShape<T>::kVecs;
-  extern __shared__ __align__(16) unsigned char lp_smem[];
+  extern __shared__ __align__(128) unsigned char lp_smem[];
   __shared__ Piece piece[kLpMaxPieces];
   __shared__ Scratch scratch[kLpFinish];
-  __shared__ uint64_t full[kLpMaxSlots], empty[kLpMaxSlots];
+  __shared__ uint64_t full[kLpMaxSlots], empty[kLpMaxSlots], landed[kLpStream][2];
   __shared__ int next;  // pieces taken
   __shared__ volatile int stop;
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-  const int n = p.pieces * 32;
-  float4* sm = reinterpret_cast<float4*>(lp_smem);
-  float* ss = reinterpret_cast<float*>(sm + p.slots * n);
-  float* su = ss + p.slots * n;
+  // [ring | sums [slots][pieces] | batch maxima [slots][pieces][32]]
+  float4* sums = reinterpret_cast<float4*>(lp_smem + kLpRing);
+  BatchMax<T>* maxima = reinterpret_cast<BatchMax<T>*>(sums + p.slots * p.pieces);
   if (threadIdx.x == 0) {
     next = 2 * kLpStream;
     stop = 0;
@@ -626,15 +626,23 @@ __global__ void __launch_bounds__(kLpThreads, 1)
       mbar_init(&full[i], p.pieces);
       mbar_init(&empty[i], 1);
     }
+    for (int i = 0; i < kLpStream; ++i) {
+      mbar_init(&landed[i][0], 1);
+      mbar_init(&landed[i][1], 1);
+    }
     fence_mbar_init();
     cut_row<T>(p, piece);
   }
   __syncthreads();
   const int rows = int((p.s - blockIdx.x + gridDim.x - 1) / gridDim.x);  // this CTA's rows
   if (warp < kLpStream) {
-    constexpr int H = U / 2;
-    const float c = p.inv_t * kLog2e;
-    // piece i of the CTA's row k, and the next one taken; a row's target is
+    const float c = p.inv_t * kLog2e, floor = -2.f * kLpFar / c;
+    const uint4* ring = reinterpret_cast<const uint4*>(lp_smem) + warp * kLpStep;
+    uint64_t* bar = landed[warp];
+    const uint64_t policy = policy_evict_first();
+    const int units = p.len / kLpUnit;  // of a piece, an even number
+    unsigned parity = 0;                // bit b: the phase of buffer b to wait for
+    // piece i of the CTA's row k, and the one after it; a row's target is
     // loaded when the row is first taken, a piece ahead of its use
     struct Taken {
       int i, k;
@@ -651,72 +659,129 @@ __global__ void __launch_bounds__(kLpThreads, 1)
       x.i = i;
       x.k = k;
     };
+    // what a piece streams
+    struct Stream {
+      const uint4* v;  // its vectors
+      int n;
+      float ragged;
+      bool live;       // a row of this CTA, not ignored
+    };
+    auto describe = [&](const Taken& x) {
+      Stream q{nullptr, 0, -INFINITY, false};
+      if (x.k >= rows || (p.targets != nullptr && x.y == p.ignore_index)) return q;
+      const Piece pc = piece[x.i];
+      const Seg g = segment<T>(pc, blockIdx.x + (long long)x.k * gridDim.x);
+      q.v = body<T>(g) + pc.off;
+      q.n = max(0, min(p.len, g.nv - pc.off));
+      if (pc.off == 0 && (g.head | g.tail) != 0) q.ragged = ragged_value<T>(g, lane);
+      q.live = true;
+      return q;
+    };
+    // starts unit u of a piece into buffer u % 2 (an empty unit loads nothing)
+    auto fetch = [&](const Stream& q, int u) {
+      const int left = min(kLpUnit, q.n - u * kLpUnit);
+      if (lane == 0 && left > 0) {
+        uint64_t* b = &bar[u & 1];
+        mbar_arrive_expect_tx(b, unsigned(left) * 16);
+        bulk_load(const_cast<uint4*>(ring) + (u & 1) * kLpUnit, q.v + u * kLpUnit, unsigned(left) * 16, b, policy);
+      }
+    };
     Taken cur{0, -1, 0}, nxt;
     settle(cur, warp, 0);
     nxt = cur;
     settle(nxt, warp + kLpStream - cur.k * p.pieces, cur.k);
-    const uint4* v = nullptr;  // the piece in hand: its shard's body, its vectors [base, end)
-    int base = 0, end = 0;
-    float ragged = -INFINITY;
-    uint4 qa[H], qb[H];
-    auto load = [&](uint4 (&q)[H], int from) {
-#pragma unroll
-      for (int j = 0; j < H; ++j) {
-        const int x = from + lane + 32 * j;
-        q[j] = x < end ? __ldcs(v + x) : lp_pad(T());
-      }
-    };
-    auto ignored = [&](const Taken& x) { return p.targets != nullptr && x.y == p.ignore_index; };
-    auto begin = [&](const Taken& x) {
-      if (x.k >= rows || ignored(x)) return;
-      const Piece pc = piece[x.i];
-      const Seg g = segment<T>(pc, blockIdx.x + (long long)x.k * gridDim.x);
-      v = body<T>(g);
-      base = pc.off;
-      end = min(pc.off + p.len, g.nv);
-      ragged = -INFINITY;
-      if (pc.off == 0 && (g.head | g.tail) != 0) ragged = ragged_value<T>(g, lane);
-      load(qa, base);
-    };
-    begin(cur);
-    // one piece's loads are under way while the one before is summed
+    Stream now = describe(cur);
+    fetch(now, 0);
+    fetch(now, 1);
+    bool alive = true;
     while (cur.k < rows) {
-      const Taken now = cur;
-      const bool skip = ignored(now);
-      Acc a{-kLpFar, 0.f, 0.f};
-      float4 bm = make_float4(-INFINITY, -INFINITY, -INFINITY, -INFINITY);
       int taken = 0;
       if (lane == 0) taken = atomicAdd(&next, 1);
-      if (!skip) {
-        if (ragged > -INFINITY || isnan(ragged)) add_ragged(ragged, a, bm.x, c);
+      const Stream then = describe(nxt);
+      Acc a{-kLpFar, 0.f, 0.f};
+      float4 bm = make_float4(-INFINITY, -INFINITY, -INFINITY, -INFINITY);
+      unsigned key = 0;  // of the piece's largest logit so far
+      if (now.live) {
+        float m0 = now.ragged, m1 = -INFINITY;  // the ragged element belongs to the first batch
 #pragma unroll 1
-        while (base + 32 * U < end) {
-          load(qb, base + 32 * H);
-          half_stats<T, H>(qa, a, bm.x, bm.y, c);
-          base += 32 * U;
-          load(qa, base);
-          half_stats<T, H>(qb, a, bm.z, bm.w, c);
+        for (int u = 0; u < units; ++u) {
+          const int n = now.n - u * kLpUnit, b = u & 1;
+          uint4 q[kLpVecs];
+          if (n > 0) {
+            if (!mbar_wait_warp(&bar[b], parity >> b & 1)) {
+              alive = false;
+              break;
+            }
+            parity ^= 1u << b;
+#pragma unroll
+            for (int j = 0; j < kLpVecs; ++j) q[j] = ring[b * kLpUnit + lane + 32 * j];
+            if (n < kLpUnit) {
+#pragma unroll
+              for (int j = 0; j < kLpVecs; ++j)
+                if (lane + 32 * j >= n) q[j] = lp_pad(T());
+            }
+            m0 = max_nan(m0, vecs_max<kLpVecs / 2>(q, T()));
+            m1 = max_nan(m1, vecs_max<kLpVecs / 2>(q + kLpVecs / 2, T()));
+          }
+          // every lane has its vectors once the warp has their maximum: only
+          // then may the buffer be written again
+          const unsigned was = key;
+          key = max(key, __reduce_max_sync(kFull, value_key(max_nan(m0, m1))));
+          if (key != 0u) {
+            if (u + 2 < units) fetch(now, u + 2);
+            else if (then.live) fetch(then, u + 2 - units);
+          }
+          if (key != was) {
+            const float nk = offset_of(key_value(key), c);
+            if (nk > a.k) a.raise(nk);
+          }
+          if (n > 0) unit_sums<T>(q, a, c, floor);
+          if (u == 0 && now.ragged != -INFINITY) {
+            const float v = fmaf(fmaxf(now.ragged, floor), c, -a.k), e = ex2(v);
+            a.s += e;
+            a.u = fmaf(v, e, a.u);
+          }
+          if (b == 0) {
+            bm.x = max_nan(bm.x, m0);
+            bm.y = max_nan(bm.y, m1);
+          } else {
+            bm.z = max_nan(bm.z, m0);
+            bm.w = max_nan(bm.w, m1);
+          }
+          m0 = m1 = -INFINITY;
         }
-        load(qb, base + 32 * H);
-        half_stats<T, H>(qa, a, bm.x, bm.y, c);
+        if (!alive) break;
+#pragma unroll
+        for (int o = 16; o > 0; o >>= 1) {
+          a.s += __shfl_xor_sync(kFull, a.s, o);
+          a.u += __shfl_xor_sync(kFull, a.u, o);
+        }
+      } else if (then.live) {
+        fetch(then, 0);
+        fetch(then, 1);
       }
-      cur = nxt;
-      begin(cur);
-      settle(nxt, __shfl_sync(kFull, taken, 0) - cur.k * p.pieces, cur.k);
-      if (!skip) half_stats<T, H>(qb, a, bm.z, bm.w, c);
-      const int slot = now.k % p.slots, turn = now.k / p.slots;
+      const int slot = cur.k % p.slots, turn = cur.k / p.slots;
       if (turn > 0 && !mbar_wait_warp(&empty[slot], (turn - 1) & 1)) {
-        stop = 1;
+        alive = false;
+        now = then;  // its copies are the ones in flight
         break;
       }
-      if (!skip) {
-        const int at = slot * n + now.i * 32 + lane;
-        sm[at] = bm;
-        ss[at] = a.s;
-        su[at] = a.u;
+      if (now.live) {
+        const int at = slot * p.pieces + cur.i;
+        maxima[at * 32 + lane].set(bm);
+        if (lane == 0) sums[at] = make_float4(key_value(key), a.s, a.u, 0.f);
       }
       __syncwarp();
       if (lane == 0) mbar_arrive_local(&full[slot]);
+      cur = nxt;
+      now = then;
+      settle(nxt, __shfl_sync(kFull, taken, 0) - cur.k * p.pieces, cur.k);
+    }
+    if (!alive) {
+      stop = 1;
+      // let this warp's copies land before the CTA leaves
+      mbar_wait_warp(&bar[0], parity & 1);
+      mbar_wait_warp(&bar[1], parity >> 1 & 1);
     }
   } else {
     for (int k = warp - kLpStream; k < rows; k += kLpFinish) {
@@ -729,8 +794,8 @@ __global__ void __launch_bounds__(kLpThreads, 1)
       }
       if (p.targets != nullptr && y == p.ignore_index) write_ignored(p, row, lane);
       else
-        finish_row<T, U>(p, piece, sm + slot * n, ss + slot * n, su + slot * n, row, y, scratch[warp - kLpStream],
-                         lane);
+        finish_row<T>(p, piece, maxima + slot * p.pieces * 32, sums + slot * p.pieces, row, y,
+                      scratch[warp - kLpStream], lane);
       __syncwarp();
       if (lane == 0) mbar_arrive_local(&empty[slot]);
     }
@@ -754,11 +819,11 @@ __global__ void __launch_bounds__(kLpThreads, 1)
 
 }  // namespace
 
-// One step (a warp's 32 U vectors) per piece, more when the row would have
+// One step per piece, more when the row would have
 // too many pieces.
 template <typename T>
 static void cut_plan(LogprobParams& p, int limit) {
-  for (long long len = 32 * LpShape<T>::kVecs;; len *= 2) {
+  for (long long len = kLpStep;; len *= 2) {
     long long n = 0;
     for (int i = 0; i < p.t; ++i) {
       const long long nv = (p.sh.start[i + 1] - p.sh.start[i]) / Elem<T>::kPerVec;
@@ -775,17 +840,17 @@ static void cut_plan(LogprobParams& p, int limit) {
 template <typename T>
 void launch_logprob_forward(LogprobParams p, int sms, cudaStream_t st) {
   cut_plan<T>(p, kLpPieces);
-  const int slots = kLpPartSmem / (p.pieces * kLpPartBytes);
-  p.slots = slots < kLpMaxSlots ? slots : kLpMaxSlots;
+  const int part = p.pieces * int(sizeof(float4) + 32 * sizeof(BatchMax<T>));
+  p.slots = kLpPartSmem / part < kLpMaxSlots ? kLpPartSmem / part : kLpMaxSlots;
   const int grid = int(p.s < sms ? p.s : sms);
-  const size_t smem = size_t(p.slots) * p.pieces * kLpPartBytes;
+  const size_t smem = kLpRing + size_t(p.slots) * part;
   logprob_forward_kernel<T><<<grid, kLpThreads, smem, st>>>(p);
 }
 template void launch_logprob_forward<float>(LogprobParams, int, cudaStream_t);
 template void launch_logprob_forward<__nv_bfloat16>(LogprobParams, int, cudaStream_t);
 
 cudaError_t set_logprob_smem() {
-  const int bytes = kLpPartSmem;
+  const int bytes = kLpRing + kLpPartSmem;
   const cudaError_t e = cudaFuncSetAttribute(logprob_forward_kernel<float>,
                                              cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
   if (e != cudaSuccess) return e;

@@ -694,11 +694,11 @@ class LogprobResult(NamedTuple):
 
 def _buffer(x, shape, dtype, device, name):
     """``x`` checked, or a new tensor: contiguous CUDA memory of this shape."""
-    import torch
-
     if x is None:
+        import torch
+
         return torch.empty(shape, dtype=dtype, device=device)
-    if x.dtype != dtype or tuple(x.shape) != shape or not x.is_cuda or not x.is_contiguous():
+    if x.dtype != dtype or x.shape != shape or not x.is_cuda or not x.is_contiguous():
         raise ValueError(f"{name} must be a contiguous CUDA {dtype} tensor of shape {shape}")
     return x
 
@@ -707,10 +707,56 @@ def _addr(x):
     return None if x is None else x.data_ptr()
 
 
+def _column_shards(shards, vocab_start):
+    """What the C entries take of a list of logits shards: dtype, rows, the
+    pointers, the vocabulary offsets, the row stride (0: each is dense).  One
+    look at each tensor: a decode step calls this for every token."""
+    import torch
+
+    if not shards:
+        raise ValueError("need at least one shard")
+    first = shards[0]
+    dt = first.dtype
+    s = first.shape[0] if first.dim() == 2 else -1
+    code = VPCE_BF16 if dt is torch.bfloat16 else VPCE_FP32 if dt is torch.float32 else None
+    if code is None:
+        raise TypeError(f"unsupported logits dtype {dt}")
+    ptrs, starts, lds, dense = [], [0], set(), True
+    for sh in shards:
+        shape, stride = sh.shape, sh.stride()
+        if len(shape) != 2 or shape[0] != s or sh.dtype is not dt or not sh.is_cuda:
+            raise ValueError("shards must be 2-D CUDA tensors of one dtype and row count")
+        w = shape[1]
+        if stride[1] != 1 and w > 1:
+            raise ValueError("shard columns must be contiguous")
+        dense = dense and stride[0] == w
+        lds.add(stride[0])
+        starts.append(starts[-1] + w)
+        ptrs.append(sh.data_ptr())
+    if vocab_start is None:
+        vocab_start = starts
+    elif len(vocab_start) != len(starts) or list(vocab_start) != starts:
+        raise ValueError(f"vocab_start must be the shards' offsets {starts}")
+    if s <= 1 or dense:
+        ld = 0
+    elif len(lds) == 1:
+        ld = lds.pop()
+    else:
+        raise ValueError("shards must share one row stride or each be dense")
+    n = len(ptrs)
+    return code, s, (ctypes.c_void_p * n)(*ptrs), (ctypes.c_int64 * (n + 1))(*starts), ld
+
+
+def _raw_stream(stream):
+    import torch
+
+    return (torch.cuda.current_stream() if stream is None else stream).cuda_stream
+
+
 def _check_targets(targets, s):
     import torch
 
-    if targets is not None and (targets.dtype != torch.int64 or not targets.is_cuda or targets.numel() != s
+    if targets is not None and (targets.dtype is not torch.int64 or not targets.is_cuda or targets.numel() != s
                                 or not targets.is_contiguous()):
         raise ValueError("targets must be a contiguous CUDA int64 tensor with one entry per row")
 
@@ -734,7 +780,7 @@ def vpce_logprob_forward(shards, targets=None, vocab_start=None, *, ignore_index
     (CUDA int32 scalar) receives bit 0 if a target was outside [0, V)."""
     import torch
 
-    dtype, s, vs, ld = _describe(shards, vocab_start)
+    dtype, s, ptrs, starts, ld = _column_shards(shards, vocab_start)
     dev = shards[0].device
     _check_targets(targets, s)
     _check_flag(flag)
@@ -751,10 +797,9 @@ def vpce_logprob_forward(shards, targets=None, vocab_start=None, *, ignore_index
     ids = _buffer(top_ids_out, (s, top), torch.int64, dev, "top_ids_out") if top else None
     top_logp = _buffer(top_logp_out, (s, top), f32, dev, "top_logp_out") if top else None
     stats = _buffer(stats_out, (s, 4), f32, dev, "stats_out")
-    code = load_library().vpce_logprob_forward(_ptr_array([sh.data_ptr() for sh in shards]), dtype, len(shards), s,
-                                               _i64_array(vs), ld, _addr(targets), ignore_index, temperature, top,
-                                               _addr(logp), _addr(entropy), _addr(ids), _addr(top_logp),
-                                               _addr(stats), _addr(flag), _stream_ptr(stream))
+    code = (_lib or load_library()).vpce_logprob_forward(
+        ptrs, dtype, len(shards), s, starts, ld, _addr(targets), ignore_index, temperature, top, _addr(logp),
+        _addr(entropy), _addr(ids), _addr(top_logp), _addr(stats), _addr(flag), _raw_stream(stream))
     if code != VPCE_OK:
         raise VPCEError(code, "vpce_logprob_forward")
     return LogprobResult(logp, entropy, ids, top_logp, stats)
@@ -771,7 +816,7 @@ def vpce_logprob_backward(shards, targets, stats, vocab_start=None, *, ignore_in
     ``shards`` itself overwrites the logits in place.  Returns the list."""
     import torch
 
-    dtype, s, vs, ld = _describe(shards, vocab_start)
+    dtype, s, ptrs, starts, ld = _column_shards(shards, vocab_start)
     dev = shards[0].device
     _check_targets(targets, s)
     f32 = torch.float32
@@ -788,17 +833,16 @@ def vpce_logprob_backward(shards, targets, stats, vocab_start=None, *, ignore_in
         _buffer(grad_top_logp, (s, top), f32, dev, "grad_top_logp")
     if grad_shards is None:
         grad_shards = [torch.empty(sh.shape, dtype=sh.dtype, device=dev) for sh in shards]
-    if len(grad_shards) != len(shards) or any(g.shape != sh.shape for g, sh in zip(grad_shards, shards)):
-        raise ValueError("grad_shards must have the shards' shapes")
-    gdtype, _, _, ld_grad = _describe(grad_shards, vs)
-    if gdtype != dtype:
-        raise ValueError("grad_shards must have the shards' dtype")
-    code = load_library().vpce_logprob_backward(_ptr_array([sh.data_ptr() for sh in shards]), dtype, len(shards), s,
-                                                _i64_array(vs), ld, _addr(targets), ignore_index, temperature,
-                                                _addr(stats), _addr(grad_logp), _addr(grad_entropy), top,
-                                                _addr(top_ids), _addr(grad_top_logp),
-                                                _ptr_array([g.data_ptr() for g in grad_shards]), ld_grad,
-                                                _stream_ptr(stream))
+    if grad_shards is shards:
+        gptrs, ld_grad = ptrs, ld
+    else:
+        gdtype, gs, gptrs, gstarts, ld_grad = _column_shards(grad_shards, None)
+        if gdtype != dtype or gs != s or gstarts[:] != starts[:]:
+            raise ValueError("grad_shards must have the shards' dtype and shapes")
+    code = (_lib or load_library()).vpce_logprob_backward(
+        ptrs, dtype, len(shards), s, starts, ld, _addr(targets), ignore_index, temperature, _addr(stats),
+        _addr(grad_logp), _addr(grad_entropy), top, _addr(top_ids), _addr(grad_top_logp), gptrs, ld_grad,
+        _raw_stream(stream))
     if code != VPCE_OK:
         raise VPCEError(code, "vpce_logprob_backward")
     return grad_shards
@@ -823,6 +867,35 @@ def _check_ids(ids, s=None):
         raise ValueError("ids must be a contiguous 1-D CUDA int64 tensor, one entry per row")
 
 
+def _row_shards(shards, vocab_start):
+    """What the C entries take of a list of table shards [w_i, h]: dtype, h,
+    the pointers, the vocabulary offsets, the row stride."""
+    import torch
+
+    if not shards:
+        raise ValueError("need at least one shard")
+    dt = shards[0].dtype
+    code = VPCE_BF16 if dt is torch.bfloat16 else VPCE_FP32 if dt is torch.float32 else None
+    if code is None:
+        raise TypeError("table shards must be bf16 or fp32")
+    h = shards[0].shape[-1]
+    ptrs, starts, lds = [], [0], set()
+    for e in shards:
+        shape, stride = e.shape, e.stride()
+        if len(shape) != 2 or shape[1] != h or e.dtype is not dt or not e.is_cuda or (stride[1] != 1 and h > 1):
+            raise ValueError("table shards must be 2-D CUDA tensors [w_i, h] of one dtype, contiguous columns")
+        if shape[0] > 1:
+            lds.add(stride[0])
+        starts.append(starts[-1] + shape[0])
+        ptrs.append(e.data_ptr())
+    if len(lds) > 1:
+        raise ValueError("table shards must share one row stride")
+    if vocab_start is not None and (len(vocab_start) != len(starts) or list(vocab_start) != starts):
+        raise ValueError(f"vocab_start must be the shards' offsets {starts}")
+    n = len(ptrs)
+    return code, h, (ctypes.c_void_p * n)(*ptrs), (ctypes.c_int64 * (n + 1))(*starts), lds.pop() if lds else h
+
+
 def _row_stride(x, h):
     return x.stride(0) if x.shape[0] > 1 else h
 
@@ -838,9 +911,7 @@ def vpce_embedding_dropout_forward(table_shards, ids, vocab_start=None, *, scale
     by default)."""
     import torch
 
-    dtype, h, ld, vs = _table_desc(table_shards, vocab_start)
-    if dtype is None:
-        raise TypeError("table dtype must be bf16 or fp32")
+    dtype, h, ptrs, starts, ld = _row_shards(table_shards, vocab_start)
     _check_ids(ids)
     _check_rng(rng)
     _check_flag(flag)
@@ -854,10 +925,10 @@ def vpce_embedding_dropout_forward(table_shards, ids, vocab_start=None, *, scale
     odt = {torch.bfloat16: VPCE_BF16, torch.float32: VPCE_FP32}.get(out.dtype)
     if odt is None:
         raise TypeError("out dtype must be bf16 or fp32")
-    code = load_library().vpce_embedding_dropout_forward(
-        _ptr_array([e.data_ptr() for e in table_shards]), dtype, len(table_shards), _i64_array(vs), h, ld,
-        _addr(ids), s, INT64_MIN if padding_id is None else int(padding_id), scale, p, _addr(rng), _addr(out), odt,
-        _row_stride(out, h), _addr(flag), _stream_ptr(stream))
+    code = (_lib or load_library()).vpce_embedding_dropout_forward(
+        ptrs, dtype, len(table_shards), starts, h, ld, _addr(ids), s,
+        INT64_MIN if padding_id is None else int(padding_id), scale, p, _addr(rng), _addr(out), odt,
+        _row_stride(out, h), _addr(flag), _raw_stream(stream))
     if code != VPCE_OK:
         raise VPCEError(code, "vpce_embedding_dropout_forward")
     return out
@@ -877,7 +948,7 @@ def vpce_embedding_dropout_backward(grad_out, ids, grad_shards, vocab_start=None
     forward's."""
     import torch
 
-    gdt, h, ld, vs = _table_desc(grad_shards, vocab_start)
+    gdt, h, ptrs, starts, ld = _row_shards(grad_shards, vocab_start)
     if gdt != VPCE_FP32:
         raise TypeError("gradient table shards must be fp32")
     if grad_out.dim() != 2 or grad_out.shape[1] != h or not grad_out.is_cuda or (h > 1 and grad_out.stride(1) != 1):
@@ -888,15 +959,14 @@ def vpce_embedding_dropout_backward(grad_out, ids, grad_shards, vocab_start=None
     s = grad_out.shape[0]
     _check_ids(ids, s)
     _check_rng(rng)
-    lib = load_library()
+    lib = _lib or load_library()
     if workspace is None:
-        workspace = torch.empty(lib.vpce_embedding_dropout_backward_workspace_bytes(s, vs[-1], h), dtype=torch.uint8,
-                                device=ids.device)
+        workspace = torch.empty(lib.vpce_embedding_dropout_backward_workspace_bytes(s, starts[-1], h),
+                                dtype=torch.uint8, device=ids.device)
     code = lib.vpce_embedding_dropout_backward(
         _addr(grad_out), code_dt, _row_stride(grad_out, h), _addr(ids), s,
-        INT64_MIN if padding_id is None else int(padding_id), scale, p, _addr(rng),
-        _ptr_array([g.data_ptr() for g in grad_shards]), len(grad_shards), _i64_array(vs), h, ld,
-        int(bool(accumulate)), _addr(workspace), workspace.numel(), _stream_ptr(stream))
+        INT64_MIN if padding_id is None else int(padding_id), scale, p, _addr(rng), ptrs, len(grad_shards), starts,
+        h, ld, int(bool(accumulate)), _addr(workspace), workspace.numel(), _raw_stream(stream))
     if code != VPCE_OK:
         raise VPCEError(code, "vpce_embedding_dropout_backward")
     return grad_shards
