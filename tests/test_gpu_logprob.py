@@ -108,6 +108,8 @@ CASES = [
     (200, 4999, [0, 1, 2, 3, 1000, 2500, 4000, 4998, 4999], "bf16", "columns", 5, 1.0),
     (31, 4999, [0, 2500, 4999], "fp32", "padded", 20, 0.3),
     (700, 1537, [0, 800, 1537], "bf16", "dense", 3, 1.0),
+    (30, 64 * 31, [31 * i for i in range(65)], "fp32", "dense", 32, 1.0),   # as many shards as there can be
+    (30, 64 * 31, [31 * i for i in range(65)], "bf16", "columns", 8, 1.0),
 ]
 
 
@@ -208,6 +210,27 @@ def test_bad_targets_raise_the_flag():
     assert flag.item() == vpce.VPCE_FLAG_BAD_TARGET and ref["bad"]
     vpce.vpce_logprob_forward(_place(z, vs, "fp32", "dense"), torch.from_numpy(y % V).cuda(), vs, flag=flag)
     assert flag.item() == 0
+
+
+@pytest.mark.parametrize("dtype,V", [("bf16", 40), ("bf16", 5000), ("fp32", 257)])
+def test_many_short_rows(dtype, V):
+    # every CTA works through some hundred rows of one to three pieces
+    s, top = 40000, 4
+    gen = torch.Generator(device="cuda")
+    gen.manual_seed(V)
+    z = torch.randn(s, V, device="cuda", generator=gen).mul_(3).to(torch.bfloat16 if dtype == "bf16" else torch.float32)
+    y = torch.randint(0, V, (s,), device="cuda", generator=gen)
+    y[::5] = -100
+    r = vpce.vpce_logprob_forward([z], y, top=top)
+    lp = torch.log_softmax(z.double(), 1)
+    live = y != -100
+    want = lp.gather(1, y.clamp(min=0)[:, None])[:, 0]
+    assert float((r.logp.double() - want)[live].abs().max()) <= 2e-5 * float(want.abs().max())
+    ent = -(lp.exp() * lp).sum(1)
+    assert float((r.entropy.double() - ent)[live].abs().max()) <= 2e-5 * (2 + np.log(V))
+    order = torch.argsort(z.double(), dim=1, descending=True, stable=True)[:, :top]
+    assert torch.equal(r.top_ids[live], order[live])
+    assert not r.logp[~live].any() and bool((r.top_ids[~live] == -1).all())
 
 
 def test_empty_batch():

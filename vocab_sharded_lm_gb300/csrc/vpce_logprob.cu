@@ -37,17 +37,20 @@ namespace {
 
 namespace cg = cooperative_groups;
 
-constexpr int kLpStream = 16;      // warps that stream pieces
-constexpr int kLpFinish = 4;       // warps that finish rows
-constexpr int kLpThreads = 32 * (kLpStream + kLpFinish);  // one CTA per SM
+// Warps that stream pieces and warps that finish rows, one CTA per SM.
+template <typename T> struct LpShape;
+template <> struct LpShape<__nv_bfloat16> { static constexpr int kStream = 16, kFinish = 4; };
+template <> struct LpShape<float> { static constexpr int kStream = 12, kFinish = 4; };
+template <typename T> constexpr int kLpThreads = 32 * (LpShape<T>::kStream + LpShape<T>::kFinish);
 constexpr int kLpVecs = 8;         // vectors per lane and unit
 constexpr int kLpUnit = 32 * kLpVecs;             // vectors per unit: one buffer
 constexpr int kLpStep = 2 * kLpUnit;              // vectors per step: four batches of 4 vectors a lane
-constexpr int kLpRing = kLpStream * 2 * kLpUnit * 16;  // bytes of all buffers
+template <typename T> constexpr int kLpRing = LpShape<T>::kStream * 2 * kLpUnit * 16;  // bytes of all buffers
 constexpr int kLpMaxPieces = 64;   // pieces per row (as many as shards can be)
 constexpr int kLpPieces = 40;      // aimed at
-constexpr int kLpMaxSlots = 8;     // rows with partials in shared memory at a time, at most
-constexpr int kLpPartSmem = 88 * 1024;  // their room
+constexpr int kLpSlots = 8;        // rows with partials in shared memory at a time, where there is room
+constexpr int kLpMaxSlots = 192;   // and where rows are short
+constexpr int kLpSmem = 215 * 1024;     // room for the buffers and them
 constexpr int kLpCand = 128;       // candidate words per warp
 constexpr int kLpList = 128;       // batches listed per warp before they are re-read
 constexpr float kLpFloor = -256.f;      // 2^v is 0 here
@@ -607,26 +610,27 @@ __device__ __forceinline__ void cut_row(const LogprobParams& p, Piece* piece) {
 // several rows are finished at a time; done by the streaming warps themselves,
 // the same steps cost the stream its registers.
 template <typename T>
-__global__ void __launch_bounds__(kLpThreads, 1)
+__global__ void __launch_bounds__(kLpThreads<T>, 1)
     logprob_forward_kernel(const __grid_constant__ LogprobParams p) {
+  constexpr int kStream = LpShape<T>::kStream, kFinish = LpShape<T>::kFinish;
   extern __shared__ __align__(128) unsigned char lp_smem[];
   __shared__ Piece piece[kLpMaxPieces];
-  __shared__ Scratch scratch[kLpFinish];
-  __shared__ uint64_t full[kLpMaxSlots], empty[kLpMaxSlots], landed[kLpStream][2];
+  __shared__ Scratch scratch[kFinish];
+  __shared__ uint64_t full[kLpMaxSlots], empty[kLpMaxSlots], landed[kStream][2];
   __shared__ int next;  // pieces taken
   __shared__ volatile int stop;
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   // [ring | sums [slots][pieces] | batch maxima [slots][pieces][32]]
-  float4* sums = reinterpret_cast<float4*>(lp_smem + kLpRing);
+  float4* sums = reinterpret_cast<float4*>(lp_smem + kLpRing<T>);
   BatchMax<T>* maxima = reinterpret_cast<BatchMax<T>*>(sums + p.slots * p.pieces);
   if (threadIdx.x == 0) {
-    next = 2 * kLpStream;
+    next = 2 * kStream;
     stop = 0;
     for (int i = 0; i < kLpMaxSlots; ++i) {
       mbar_init(&full[i], p.pieces);
       mbar_init(&empty[i], 1);
     }
-    for (int i = 0; i < kLpStream; ++i) {
+    for (int i = 0; i < kStream; ++i) {
       mbar_init(&landed[i][0], 1);
       mbar_init(&landed[i][1], 1);
     }
@@ -635,7 +639,7 @@ __global__ void __launch_bounds__(kLpThreads, 1)
   }
   __syncthreads();
   const int rows = int((p.s - blockIdx.x + gridDim.x - 1) / gridDim.x);  // this CTA's rows
-  if (warp < kLpStream) {
+  if (warp < kStream) {
     const float c = p.inv_t * kLog2e, floor = -2.f * kLpFar / c;
     const uint4* ring = reinterpret_cast<const uint4*>(lp_smem) + warp * kLpStep;
     uint64_t* bar = landed[warp];
@@ -689,7 +693,7 @@ __global__ void __launch_bounds__(kLpThreads, 1)
     Taken cur{0, -1, 0}, nxt;
     settle(cur, warp, 0);
     nxt = cur;
-    settle(nxt, warp + kLpStream - cur.k * p.pieces, cur.k);
+    settle(nxt, warp + kStream - cur.k * p.pieces, cur.k);
     Stream now = describe(cur);
     fetch(now, 0);
     fetch(now, 1);
@@ -784,7 +788,7 @@ __global__ void __launch_bounds__(kLpThreads, 1)
       mbar_wait_warp(&bar[1], parity >> 1 & 1);
     }
   } else {
-    for (int k = warp - kLpStream; k < rows; k += kLpFinish) {
+    for (int k = warp - kStream; k < rows && warp - kStream < p.team; k += p.team) {
       const long long row = blockIdx.x + (long long)k * gridDim.x;
       const long long y = p.targets != nullptr ? __ldg(p.targets + row) : 0;
       const int slot = k % p.slots;
@@ -795,7 +799,7 @@ __global__ void __launch_bounds__(kLpThreads, 1)
       if (p.targets != nullptr && y == p.ignore_index) write_ignored(p, row, lane);
       else
         finish_row<T>(p, piece, maxima + slot * p.pieces * 32, sums + slot * p.pieces, row, y,
-                      scratch[warp - kLpStream], lane);
+                      scratch[warp - kStream], lane);
       __syncwarp();
       if (lane == 0) mbar_arrive_local(&empty[slot]);
     }
@@ -804,7 +808,7 @@ __global__ void __launch_bounds__(kLpThreads, 1)
   if (stop) {  // a wait gave up: nothing of this CTA's rows is to be believed
     if (threadIdx.x == 0 && p.flag != nullptr) atomicOr(p.flag, VPCE_FLAG_WAIT_TIMEOUT);
     const float nan = __int_as_float(0x7fc00000);
-    for (int k = threadIdx.x; k < rows; k += kLpThreads) {
+    for (int k = threadIdx.x; k < rows; k += kLpThreads<T>) {
       const long long row = blockIdx.x + (long long)k * gridDim.x;
       if (p.logp) p.logp[row] = nan;
       if (p.entropy) p.entropy[row] = nan;
@@ -841,21 +845,32 @@ template <typename T>
 void launch_logprob_forward(LogprobParams p, int sms, cudaStream_t st) {
   cut_plan<T>(p, kLpPieces);
   const int part = p.pieces * int(sizeof(float4) + 32 * sizeof(BatchMax<T>));
-  p.slots = kLpPartSmem / part < kLpMaxSlots ? kLpPartSmem / part : kLpMaxSlots;
+  // Slots.  Row k waits for row k - slots by a barrier's parity, which cannot
+  // tell it from row k - 2 slots, so none may be two turns ahead of an
+  // unfinished row r.  Rows r + slots, r + slots + team, .. are finished by
+  // r's warp and block meanwhile (the others go on); all their pieces up to
+  // row r + 2 slots are in the hands of streaming warps, which hold three at
+  // most: (slots / team) * pieces >= 3 kStream rules it out.  And as slots is a
+  // multiple of the team, a slot's rows are finished by one warp, in order.
+  const int room = (kLpSmem - kLpRing<T>) / part;
+  const int rows_each = (3 * LpShape<T>::kStream + p.pieces - 1) / p.pieces;  // slots per finishing warp
+  p.team = LpShape<T>::kFinish;
+  while (p.team > 1 && rows_each * p.team > room) --p.team;
+  p.slots = rows_each * p.team;
+  while (p.slots + p.team <= room && p.slots + p.team <= kLpSlots) p.slots += p.team;
   const int grid = int(p.s < sms ? p.s : sms);
-  const size_t smem = kLpRing + size_t(p.slots) * part;
-  logprob_forward_kernel<T><<<grid, kLpThreads, smem, st>>>(p);
+  const size_t smem = kLpRing<T> + size_t(p.slots) * part;
+  logprob_forward_kernel<T><<<grid, kLpThreads<T>, smem, st>>>(p);
 }
 template void launch_logprob_forward<float>(LogprobParams, int, cudaStream_t);
 template void launch_logprob_forward<__nv_bfloat16>(LogprobParams, int, cudaStream_t);
 
 cudaError_t set_logprob_smem() {
-  const int bytes = kLpRing + kLpPartSmem;
   const cudaError_t e = cudaFuncSetAttribute(logprob_forward_kernel<float>,
-                                             cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
+                                             cudaFuncAttributeMaxDynamicSharedMemorySize, kLpSmem);
   if (e != cudaSuccess) return e;
   return cudaFuncSetAttribute(logprob_forward_kernel<__nv_bfloat16>, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                              bytes);
+                              kLpSmem);
 }
 
 }  // namespace vpce

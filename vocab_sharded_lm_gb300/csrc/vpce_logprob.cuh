@@ -21,7 +21,9 @@ struct LogprobParams {
   float* top_logp;           // [s][top]
   float4* stats;             // [s]: largest logit, ln sum exp((z - max) / T), entropy, 0
   int* flag;
-  int pieces, len, slots;    // set by the launch: pieces of a row, vectors in each, rows held at a time
+  // set by the launch: pieces of a row, vectors in each, rows held at a time,
+  // warps that finish rows
+  int pieces, len, slots, team;
 };
 
 struct LogprobBwdParams {
