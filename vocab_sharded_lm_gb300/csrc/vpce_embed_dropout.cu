@@ -14,7 +14,7 @@
 //          order) and once to collect its own in row order, and sorts those by
 //          a stable counting sort in shared memory: no passes over the whole
 //          batch and no grid barrier.
-//   sum    A warp per task of 256 columns: a segment of at most 128 rows of a
+//   sum    A warp per task of 256 columns: a segment of at most 64 rows of a
 //          run longer than kLong (the last segment to finish adds a run's
 //          partial sums in order), or the runs that start in 16 sorted rows, up
 //          to 16 rows' loads in flight.  Then, when the table is overwritten,
@@ -168,9 +168,10 @@ __global__ void __launch_bounds__(kEdThreads) embed_dropout_forward_kernel(const
 constexpr int kSortThreads = 1024;
 constexpr int kSortWarps = kSortThreads / 32;
 constexpr int kDigits = 1024;  // bins of one counting pass
-constexpr int kLong = 64;      // runs with more rows are summed by a whole CTA
+constexpr int kLong = 64;      // runs with more rows are summed in segments
 constexpr int kGroup = 16;     // sorted rows per warp task
-constexpr int kSeg = 128;      // rows of a long run per warp task
+constexpr int kSeg = 64;       // rows of a long run per warp task
+constexpr int kSegShare = 32;  // n sorted tokens hold at most n / 32 segments: ceil(L / 64) <= L / 32 for L > 64
 constexpr int kOwnBits = 7;    // the sort's CTAs: 2^kOwnBits
 constexpr int kOwners = 1 << kOwnBits;
 template <typename T> constexpr int kInFlight = sizeof(T) == 2 ? 16 : 8;  // rows' loads per lane
@@ -198,7 +199,7 @@ struct SortParams {
   int* sorted_id;     // [s]
   int* sorted_row;    // [s]
   unsigned* present;  // [kOwners][words], a bit per local id
-  Segment* segs;      // of the long runs; a CTA's from its first position / 64 on
+  Segment* segs;      // of the long runs; a CTA's from its first position / kSegShare on
   int2* lists;        // per CTA: first of its segments, how many
   int* done;          // [segments][blocks], cleared at each run's first segment
   SortHead* head;
@@ -238,7 +239,7 @@ __global__ void __launch_bounds__(kSortThreads, 1) embed_sort_kernel(const __gri
   const long long per = ((p.s + kSortWarps - 1) / kSortWarps + 31) / 32 * 32;
   const long long r0 = warp * per, r1 = min(p.s, r0 + per);
   int mine = 0, low = 0;
-#pragma unroll 4
+#pragma unroll 8
   for (long long r = r0 + lane; r < r1; r += 32) {
     const long long id = __ldg(p.ids + r);
     const int o = owner(id);
@@ -268,19 +269,24 @@ __global__ void __launch_bounds__(kSortThreads, 1) embed_sort_kernel(const __gri
     if (tid == 0) p.lists[own] = make_int2(0, 0);
     return;
   }
-  const int first_seg = int(base / kLong);  // n tokens hold at most n / kLong segments of long runs
+  const int first_seg = int(base / kSegShare);
   int *key = p.key[0] + base, *row = p.row[0] + base, *key2 = p.key[1] + base, *row2 = p.row[1] + base;
   if (mine > 0) {
-    for (long long r = r0; r < r1; r += 32) {
-      const long long id = r + lane < r1 ? __ldg(p.ids + r + lane) : -1;
-      const bool in = owner(id) == own;
-      const unsigned m = __ballot_sync(kFull, in);
-      if (in) {
-        const int k = at + __popc(m & ((1u << lane) - 1u));
-        key[k] = int(id >> kOwnBits);
-        row[k] = int(r) + lane;
+    for (long long r = r0; r < r1; r += 256) {
+      long long id[8];  // eight loads in flight
+#pragma unroll
+      for (int j = 0; j < 8; ++j) id[j] = r + 32 * j + lane < r1 ? __ldg(p.ids + r + 32 * j + lane) : -1;
+#pragma unroll
+      for (int j = 0; j < 8; ++j) {
+        const bool in = owner(id[j]) == own;
+        const unsigned m = __ballot_sync(kFull, in);
+        if (in) {
+          const int k = at + __popc(m & ((1u << lane) - 1u));
+          key[k] = int(id[j] >> kOwnBits);
+          row[k] = int(r) + 32 * j + lane;
+        }
+        at += __popc(m);
       }
-      at += __popc(m);
     }
   }
   // stable counting passes, kDigits bins each; the warps take contiguous
@@ -625,7 +631,7 @@ struct EdLayout {
   size_t head, lists, row[2], key[2], sid, srow, present, segs, done, part, total;
   int range, words, blocks;
   EdLayout(long long s, long long V, long long h) {
-    const size_t n = round256(sizeof(int) * size_t(s)), slots = size_t(s / kLong + 1);
+    const size_t n = round256(sizeof(int) * size_t(s)), slots = size_t(s / kSegShare + 1);
     range = int((V + kOwners - 1) / kOwners);
     words = (range + 31) / 32;
     blocks = int((h + 255) / 256);
