@@ -590,16 +590,25 @@ __device__ __forceinline__ void finish_row(const LogprobParams& p, const Piece* 
 }
 
 // The pieces of a row: every shard cut into ceil(vectors / len) of them, one
-// at least.  Thread 0 writes the table.
+// at least.  One warp writes the table, a lane per shard.
 template <typename T>
-__device__ __forceinline__ void cut_row(const LogprobParams& p, Piece* piece) {
-  int n = 0;
-  for (int i = 0; i < p.t; ++i) {
-    const int nv = int((p.sh.start[i + 1] - p.sh.start[i]) / Elem<T>::kPerVec);
-    for (int off = 0; off == 0 || off < nv; off += p.len)
-      piece[n++] = Piece{p.sh.ptr[i], p.sh.ld_bytes[i],
-                         unsigned(p.sh.start[i + 1] - p.sh.start[i]) * unsigned(Elem<T>::kBytes), int(p.sh.start[i]),
-                         off, 0};
+__device__ __forceinline__ void cut_row(const LogprobParams& p, Piece* piece, int lane) {
+  int before = 0;
+  for (int i0 = 0; i0 < p.t; i0 += 32) {
+    const int i = i0 + lane;
+    const int w = i < p.t ? int(p.sh.start[i + 1] - p.sh.start[i]) : 0;
+    const int nv = w / Elem<T>::kPerVec;
+    const int mine = i < p.t ? max(1, (nv + p.len - 1) / p.len) : 0;
+    int upto = mine;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+      const int x = __shfl_up_sync(kFull, upto, o);
+      if (lane >= o) upto += x;
+    }
+    for (int k = 0; k < mine; ++k)
+      piece[before + upto - mine + k] = Piece{p.sh.ptr[i],          p.sh.ld_bytes[i], unsigned(w) * unsigned(Elem<T>::kBytes),
+                                              int(p.sh.start[i]), k * p.len,        0};
+    before += __shfl_sync(kFull, upto, 31);
   }
 }
 
@@ -626,17 +635,14 @@ __global__ void __launch_bounds__(kLpThreads<T>, 1)
   if (threadIdx.x == 0) {
     next = 2 * kStream;
     stop = 0;
-    for (int i = 0; i < kLpMaxSlots; ++i) {
-      mbar_init(&full[i], p.pieces);
-      mbar_init(&empty[i], 1);
-    }
-    for (int i = 0; i < kStream; ++i) {
-      mbar_init(&landed[i][0], 1);
-      mbar_init(&landed[i][1], 1);
-    }
-    fence_mbar_init();
-    cut_row<T>(p, piece);
   }
+  for (int i = threadIdx.x; i < p.slots; i += kLpThreads<T>) {
+    mbar_init(&full[i], p.pieces);
+    mbar_init(&empty[i], 1);
+  }
+  if (threadIdx.x < 2 * kStream) mbar_init(&landed[threadIdx.x / 2][threadIdx.x % 2], 1);
+  fence_mbar_init();
+  if (warp == kStream) cut_row<T>(p, piece, lane);
   __syncthreads();
   const int rows = int((p.s - blockIdx.x + gridDim.x - 1) / gridDim.x);  // this CTA's rows
   if (warp < kStream) {

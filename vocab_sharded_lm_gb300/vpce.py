@@ -747,10 +747,14 @@ def _column_shards(shards, vocab_start):
     return code, s, (ctypes.c_void_p * n)(*ptrs), (ctypes.c_int64 * (n + 1))(*starts), ld
 
 
-def _raw_stream(stream):
+def _raw_stream(stream, like):
+    """The stream's handle; None is the current stream of ``like``'s device
+    (read as an integer: building a Stream object costs some microseconds)."""
     import torch
 
-    return (torch.cuda.current_stream() if stream is None else stream).cuda_stream
+    if stream is not None:
+        return stream.cuda_stream
+    return torch._C._cuda_getCurrentRawStream(like.get_device())
 
 
 def _check_targets(targets, s):
@@ -799,7 +803,7 @@ def vpce_logprob_forward(shards, targets=None, vocab_start=None, *, ignore_index
     stats = _buffer(stats_out, (s, 4), f32, dev, "stats_out")
     code = (_lib or load_library()).vpce_logprob_forward(
         ptrs, dtype, len(shards), s, starts, ld, _addr(targets), ignore_index, temperature, top, _addr(logp),
-        _addr(entropy), _addr(ids), _addr(top_logp), _addr(stats), _addr(flag), _raw_stream(stream))
+        _addr(entropy), _addr(ids), _addr(top_logp), _addr(stats), _addr(flag), _raw_stream(stream, shards[0]))
     if code != VPCE_OK:
         raise VPCEError(code, "vpce_logprob_forward")
     return LogprobResult(logp, entropy, ids, top_logp, stats)
@@ -842,7 +846,7 @@ def vpce_logprob_backward(shards, targets, stats, vocab_start=None, *, ignore_in
     code = (_lib or load_library()).vpce_logprob_backward(
         ptrs, dtype, len(shards), s, starts, ld, _addr(targets), ignore_index, temperature, _addr(stats),
         _addr(grad_logp), _addr(grad_entropy), top, _addr(top_ids), _addr(grad_top_logp), gptrs, ld_grad,
-        _raw_stream(stream))
+        _raw_stream(stream, shards[0]))
     if code != VPCE_OK:
         raise VPCEError(code, "vpce_logprob_backward")
     return grad_shards
@@ -928,7 +932,7 @@ def vpce_embedding_dropout_forward(table_shards, ids, vocab_start=None, *, scale
     code = (_lib or load_library()).vpce_embedding_dropout_forward(
         ptrs, dtype, len(table_shards), starts, h, ld, _addr(ids), s,
         INT64_MIN if padding_id is None else int(padding_id), scale, p, _addr(rng), _addr(out), odt,
-        _row_stride(out, h), _addr(flag), _raw_stream(stream))
+        _row_stride(out, h), _addr(flag), _raw_stream(stream, ids))
     if code != VPCE_OK:
         raise VPCEError(code, "vpce_embedding_dropout_forward")
     return out
@@ -966,7 +970,7 @@ def vpce_embedding_dropout_backward(grad_out, ids, grad_shards, vocab_start=None
     code = lib.vpce_embedding_dropout_backward(
         _addr(grad_out), code_dt, _row_stride(grad_out, h), _addr(ids), s,
         INT64_MIN if padding_id is None else int(padding_id), scale, p, _addr(rng), ptrs, len(grad_shards), starts,
-        h, ld, int(bool(accumulate)), _addr(workspace), workspace.numel(), _raw_stream(stream))
+        h, ld, int(bool(accumulate)), _addr(workspace), workspace.numel(), _raw_stream(stream, ids))
     if code != VPCE_OK:
         raise VPCEError(code, "vpce_embedding_dropout_backward")
     return grad_shards
