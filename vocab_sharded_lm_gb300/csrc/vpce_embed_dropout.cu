@@ -19,6 +19,13 @@
 //          partial sums in order), or the runs that start in 16 sorted rows, up
 //          to 16 rows' loads in flight.  Then, when the table is overwritten,
 //          the rows of ids that do not occur.
+//
+// Measured at s = 8192 Zipf ids, h = 8192, V = 128256, bf16, dropout 0.1: the
+// lookup 0.057 ms (0.042 without dropout; its output and distinct rows are
+// 0.026 ms of HBM traffic: the generator's wide products bound it), the sort
+// 0.012 ms, the gradient 0.62 ms written in full (4.2 GB of table, 6.9 TB/s) and
+// 0.11 ms accumulated.  Longer segments cost more (128 rows: 0.123 ms
+// accumulated), and so did long runs summed by whole CTAs (0.142 ms).
 #include "vpce_embed_dropout.cuh"
 
 namespace vpce {
