@@ -198,6 +198,25 @@ def test_forward_and_backward_are_adjoint_on_the_device():
     assert abs(a - b) <= 1e-4 * float((out.double() * g.cuda().double()).abs().sum())
 
 
+def test_another_stream_gives_the_same_bits():
+    V, h, s, vs = 400, 264, 900, [0, 150, 400]
+    x, _ = _table(13, V, h, "bf16")
+    g, _ = _table(14, s, h, "bf16")
+    tab, gx, ids = _shards(x, vs), g.cuda(), torch.from_numpy(_ids("zipf", s, V, 4)).cuda()
+    kw = dict(p=0.2, rng=_rng(8, 9))
+    out = vpce.vpce_embedding_dropout_forward(tab, ids, vs, **kw)
+    gs = [torch.zeros(vs[i + 1] - vs[i], h, device="cuda") for i in range(2)]
+    vpce.vpce_embedding_dropout_backward(gx, ids, gs, vs, **kw)
+    gs2 = [torch.zeros_like(q) for q in gs]
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    out2 = vpce.vpce_embedding_dropout_forward(tab, ids, vs, stream=side, **kw)
+    vpce.vpce_embedding_dropout_backward(gx, ids, gs2, vs, stream=side, **kw)
+    junk = torch.full((1 << 22,), 7, dtype=torch.uint8, device="cuda")   # the workspace is not up for reuse here
+    side.synchronize()
+    assert torch.equal(out, out2) and all(torch.equal(a, b) for a, b in zip(gs, gs2)) and junk[0] == 7
+
+
 def test_graph_replay_draws_a_new_mask():
     V, h, s, vs = 200, 96, 50, [0, 90, 200]
     x, xd = _table(11, V, h, "bf16")

@@ -747,14 +747,30 @@ def _column_shards(shards, vocab_start):
     return code, s, (ctypes.c_void_p * n)(*ptrs), (ctypes.c_int64 * (n + 1))(*starts), ld
 
 
-def _raw_stream(stream, like):
-    """The stream's handle; None is the current stream of ``like``'s device
-    (read as an integer: building a Stream object costs some microseconds)."""
+def _raw_stream(like):
+    """Handle of the current stream of ``like``'s device (read as an integer:
+    building a Stream object costs some microseconds)."""
     import torch
 
-    if stream is not None:
-        return stream.cuda_stream
     return torch._C._cuda_getCurrentRawStream(like.get_device())
+
+
+def _on_stream(fn):
+    """``stream=`` of a call: the whole call is made with that stream current,
+    so that what it allocates (outputs, workspace) belongs to the stream that
+    uses it."""
+    import functools
+
+    @functools.wraps(fn)
+    def call(*args, stream=None, **kw):
+        if stream is None:
+            return fn(*args, **kw)
+        import torch
+
+        with torch.cuda.stream(stream):
+            return fn(*args, **kw)
+
+    return call
 
 
 def _check_targets(targets, s):
@@ -772,9 +788,10 @@ def _check_flag(flag):
         raise ValueError("flag must be a CUDA int32 tensor of one element")
 
 
+@_on_stream
 def vpce_logprob_forward(shards, targets=None, vocab_start=None, *, ignore_index: int = -100,
                          temperature: float = 1.0, top: int = 0, logp_out=None, entropy_out=None, top_ids_out=None,
-                         top_logp_out=None, stats_out=None, flag=None, stream=None) -> LogprobResult:
+                         top_logp_out=None, stats_out=None, flag=None) -> LogprobResult:
     """Log probability of each row's target under softmax(logits /
     temperature), the entropy, and the ``top`` most likely columns with their
     log probabilities (equal logits by column, lowest first), from
@@ -803,15 +820,16 @@ def vpce_logprob_forward(shards, targets=None, vocab_start=None, *, ignore_index
     stats = _buffer(stats_out, (s, 4), f32, dev, "stats_out")
     code = (_lib or load_library()).vpce_logprob_forward(
         ptrs, dtype, len(shards), s, starts, ld, _addr(targets), ignore_index, temperature, top, _addr(logp),
-        _addr(entropy), _addr(ids), _addr(top_logp), _addr(stats), _addr(flag), _raw_stream(stream, shards[0]))
+        _addr(entropy), _addr(ids), _addr(top_logp), _addr(stats), _addr(flag), _raw_stream(shards[0]))
     if code != VPCE_OK:
         raise VPCEError(code, "vpce_logprob_forward")
     return LogprobResult(logp, entropy, ids, top_logp, stats)
 
 
+@_on_stream
 def vpce_logprob_backward(shards, targets, stats, vocab_start=None, *, ignore_index: int = -100,
                           temperature: float = 1.0, grad_logp=None, grad_entropy=None, top_ids=None,
-                          grad_top_logp=None, grad_shards=None, stream=None):
+                          grad_top_logp=None, grad_shards=None):
     """Gradient of :func:`vpce_logprob_forward`'s outputs with respect to the
     logits, for float32 upstream gradients ``grad_logp`` [s], ``grad_entropy``
     [s] and ``grad_top_logp`` [s, top] (with the forward's ``top_ids``; each
@@ -846,7 +864,7 @@ def vpce_logprob_backward(shards, targets, stats, vocab_start=None, *, ignore_in
     code = (_lib or load_library()).vpce_logprob_backward(
         ptrs, dtype, len(shards), s, starts, ld, _addr(targets), ignore_index, temperature, _addr(stats),
         _addr(grad_logp), _addr(grad_entropy), top, _addr(top_ids), _addr(grad_top_logp), gptrs, ld_grad,
-        _raw_stream(stream, shards[0]))
+        _raw_stream(shards[0]))
     if code != VPCE_OK:
         raise VPCEError(code, "vpce_logprob_backward")
     return grad_shards
@@ -904,8 +922,9 @@ def _row_stride(x, h):
     return x.stride(0) if x.shape[0] > 1 else h
 
 
+@_on_stream
 def vpce_embedding_dropout_forward(table_shards, ids, vocab_start=None, *, scale: float = 1.0, p: float = 0.0,
-                                   rng=None, padding_id=None, out=None, out_dtype=None, flag=None, stream=None):
+                                   rng=None, padding_id=None, out=None, out_dtype=None, flag=None):
     """Rows ``scale * dropout(table[ids], p)`` of a vocabulary-split table.
     ``rng`` (CUDA int64 ``[seed, offset]``) keys the mask, which is a function
     of (seed, offset, row, column) and never stored: pass the same words to
@@ -932,7 +951,7 @@ def vpce_embedding_dropout_forward(table_shards, ids, vocab_start=None, *, scale
     code = (_lib or load_library()).vpce_embedding_dropout_forward(
         ptrs, dtype, len(table_shards), starts, h, ld, _addr(ids), s,
         INT64_MIN if padding_id is None else int(padding_id), scale, p, _addr(rng), _addr(out), odt,
-        _row_stride(out, h), _addr(flag), _raw_stream(stream, ids))
+        _row_stride(out, h), _addr(flag), _raw_stream(ids))
     if code != VPCE_OK:
         raise VPCEError(code, "vpce_embedding_dropout_forward")
     return out
@@ -942,9 +961,10 @@ def vpce_embedding_dropout_backward_workspace_bytes(s: int, V: int, h: int) -> i
     return int(load_library().vpce_embedding_dropout_backward_workspace_bytes(int(s), int(V), int(h)))
 
 
+@_on_stream
 def vpce_embedding_dropout_backward(grad_out, ids, grad_shards, vocab_start=None, *, scale: float = 1.0,
                                     p: float = 0.0, rng=None, padding_id=None, accumulate: bool = True,
-                                    workspace=None, stream=None):
+                                    workspace=None):
     """Gradient of :func:`vpce_embedding_dropout_forward` with respect to the
     table, into the fp32 ``grad_shards`` (in place): added to what they hold,
     or, with ``accumulate=False``, written in full (zero rows for ids that do
@@ -970,7 +990,7 @@ def vpce_embedding_dropout_backward(grad_out, ids, grad_shards, vocab_start=None
     code = lib.vpce_embedding_dropout_backward(
         _addr(grad_out), code_dt, _row_stride(grad_out, h), _addr(ids), s,
         INT64_MIN if padding_id is None else int(padding_id), scale, p, _addr(rng), ptrs, len(grad_shards), starts,
-        h, ld, int(bool(accumulate)), _addr(workspace), workspace.numel(), _raw_stream(stream, ids))
+        h, ld, int(bool(accumulate)), _addr(workspace), workspace.numel(), _raw_stream(ids))
     if code != VPCE_OK:
         raise VPCEError(code, "vpce_embedding_dropout_backward")
     return grad_shards
