@@ -197,6 +197,32 @@ def backward_rows_raw(shard_ptrs, dtype, t, s, vocab_start, ld, targets_ptr, ign
 # ----------------------------------------------------------------------------
 # torch-tensor forms
 # ----------------------------------------------------------------------------
+def _row_ld(x, width, name):
+    """Row stride of ``x`` [rows, width] for a C entry.  The entries read a
+    stride of 0 as "dense", so rows that share memory (an expanded tensor's)
+    must never reach them as they are."""
+    if x.shape[0] <= 1:
+        return width
+    ld = x.stride(0)
+    if ld == 0:
+        raise ValueError(f"{name}: all rows share one row's memory (row stride 0); pass x.contiguous()")
+    return ld
+
+
+def _shared_ld(shards, width, name):
+    """The one row stride of a list of table or weight shards."""
+    lds = {_row_ld(x, width, name) for x in shards if x.shape[0] > 1}
+    if len(lds) > 1:
+        raise ValueError(f"{name} must share one row stride")
+    return lds.pop() if lds else width
+
+
+def _rows_of_their_own(x):
+    """``x``, or a dense copy of it (on the current stream) where all rows
+    share one row's memory: the gradient of a sum over rows arrives that way."""
+    return x.contiguous() if x.shape[0] > 1 and x.stride(0) == 0 else x
+
+
 def _describe(shards, vocab_start):
     import torch
 
@@ -216,6 +242,7 @@ def _describe(shards, vocab_start):
             raise ValueError("shards must be 2-D CUDA tensors of one dtype and row count")
         if sh.stride(1) != 1:
             raise ValueError("shard columns must be contiguous")
+        _row_ld(sh, sh.shape[1], "shards")
         widths.append(sh.shape[1])
     if vocab_start is None:
         vocab_start = [0]
@@ -464,11 +491,8 @@ def vpce_lmhead_forward(hidden, weight_shards, targets, vocab_start=None, *, ign
     for w in weight_shards:
         if w.dtype != torch.bfloat16 or w.dim() != 2 or not w.is_cuda or w.shape[1] != h or w.stride(1) != 1:
             raise ValueError("weight shards must be CUDA bf16 [w_i, h] tensors with contiguous columns")
-    strides = {w.stride(0) for w in weight_shards if w.shape[0] > 1}
-    if len(strides) > 1:
-        raise ValueError("weight shards must share one row stride")
-    ld_w = strides.pop() if strides else h
-    ld_x = hidden.stride(0) if s > 1 else h
+    ld_w = _shared_ld(weight_shards, h, "weight shards")
+    ld_x = _row_ld(hidden, h, "hidden")
     if vocab_start is None:
         vocab_start = [0]
         for w in weight_shards:
@@ -506,26 +530,26 @@ def vpce_lmhead_backward(hidden, weight_shards, targets, fwd_workspace, vocab_st
         for w in weight_shards:
             vocab_start.append(vocab_start[-1] + w.shape[0])
     vocab_start = [int(v) for v in vocab_start]
-    strides = {w.stride(0) for w in weight_shards if w.shape[0] > 1}
-    ld_w = strides.pop() if len(strides) == 1 else h
+    ld_w = _shared_ld(weight_shards, h, "weight shards")
+    ld_x = _row_ld(hidden, h, "hidden")
     dev = hidden.device
     if grad_hidden is None:
         grad_hidden = torch.empty((s, h), dtype=torch.bfloat16, device=dev)
     if grad_weight_shards is None:
         grad_weight_shards = [torch.zeros((w.shape[0], h), dtype=torch.float32, device=dev) for w in weight_shards]
-    gstr = {g.stride(0) for g in grad_weight_shards if g.shape[0] > 1}
-    ld_gw = gstr.pop() if len(gstr) == 1 else h
+    ld_gx = _row_ld(grad_hidden, h, "grad_hidden")
+    ld_gw = _shared_ld(grad_weight_shards, h, "grad_weight_shards")
     if grad_rows is not None:
         _check_grad_rows(grad_rows, s)
     if workspace is None:
         workspace = torch.empty(vpce_lmhead_backward_workspace_bytes(vocab_start[-1], h), dtype=torch.uint8,
                                 device=dev)
     code = int(load_library().vpce_lmhead_backward(
-        ctypes.c_void_p(hidden.data_ptr()), int(hidden.stride(0) if s > 1 else h),
+        ctypes.c_void_p(hidden.data_ptr()), int(ld_x),
         ctypes.cast(_ptr_array([w.data_ptr() for w in weight_shards]), _P), int(ld_w), len(weight_shards), int(s),
         int(h), _i64_array(vocab_start), ctypes.c_void_p(targets.data_ptr()), int(ignore_index), float(grad_output),
         _ptr(grad_rows), ctypes.c_void_p(fwd_workspace.data_ptr()), fwd_workspace.numel(),
-        ctypes.c_void_p(grad_hidden.data_ptr()), int(grad_hidden.stride(0) if s > 1 else h),
+        ctypes.c_void_p(grad_hidden.data_ptr()), int(ld_gx),
         ctypes.cast(_ptr_array([g.data_ptr() for g in grad_weight_shards]), _P), int(ld_gw),
         ctypes.c_void_p(workspace.data_ptr()), workspace.numel(), _stream_ptr(stream)))
     if code != VPCE_OK:
@@ -546,10 +570,7 @@ def _table_desc(shards, vocab_start):
     for e in shards:
         if e.dtype != dt or e.dim() != 2 or e.shape[1] != h or not e.is_cuda or e.stride(1) != 1:
             raise ValueError("table shards must be 2-D CUDA tensors [w_i, h] of one dtype, contiguous columns")
-    strides = {e.stride(0) for e in shards if e.shape[0] > 1}
-    if len(strides) > 1:
-        raise ValueError("table shards must share one row stride")
-    ld = strides.pop() if strides else h
+    ld = _shared_ld(shards, h, "table shards")
     if vocab_start is None:
         vocab_start = [0]
         for e in shards:
@@ -581,11 +602,8 @@ def vpce_lmhead_forward_backward(hidden, weight_shards, targets, vocab_start=Non
     for w in weight_shards:
         if w.dtype != torch.bfloat16 or w.dim() != 2 or not w.is_cuda or w.shape[1] != h or w.stride(1) != 1:
             raise ValueError("weight shards must be CUDA bf16 [w_i, h] tensors with contiguous columns")
-    strides = {w.stride(0) for w in weight_shards if w.shape[0] > 1}
-    if len(strides) > 1:
-        raise ValueError("weight shards must share one row stride")
-    ld_w = strides.pop() if strides else h
-    ld_x = hidden.stride(0) if s > 1 else h
+    ld_w = _shared_ld(weight_shards, h, "weight shards")
+    ld_x = _row_ld(hidden, h, "hidden")
     if vocab_start is None:
         vocab_start = [0]
         for w in weight_shards:
@@ -598,8 +616,8 @@ def vpce_lmhead_forward_backward(hidden, weight_shards, targets, vocab_start=Non
         grad_hidden = torch.empty((s, h), dtype=torch.bfloat16, device=dev)
     if grad_weight_shards is None:
         grad_weight_shards = [torch.zeros((w.shape[0], h), dtype=torch.float32, device=dev) for w in weight_shards]
-    gstr = {g.stride(0) for g in grad_weight_shards if g.shape[0] > 1}
-    ld_gw = gstr.pop() if len(gstr) == 1 else h
+    ld_gx = _row_ld(grad_hidden, h, "grad_hidden")
+    ld_gw = _shared_ld(grad_weight_shards, h, "grad_weight_shards")
     if grad_rows is not None:
         _check_grad_rows(grad_rows, s)
     if workspace is None:
@@ -610,7 +628,7 @@ def vpce_lmhead_forward_backward(hidden, weight_shards, targets, vocab_start=Non
         ctypes.c_void_p(hidden.data_ptr()), int(ld_x), ctypes.cast(_ptr_array([w.data_ptr() for w in weight_shards]), _P),
         int(ld_w), len(weight_shards), int(s), int(h), _i64_array(vocab_start), ctypes.c_void_p(targets.data_ptr()),
         int(ignore_index), red, float(grad_output), _ptr(grad_rows), _ptr(loss_out), _ptr(row_loss_out),
-        ctypes.c_void_p(grad_hidden.data_ptr()), int(grad_hidden.stride(0) if s > 1 else h),
+        ctypes.c_void_p(grad_hidden.data_ptr()), int(ld_gx),
         ctypes.cast(_ptr_array([g.data_ptr() for g in grad_weight_shards]), _P), int(ld_gw),
         ctypes.c_void_p(workspace.data_ptr()), workspace.numel(), _stream_ptr(stream)))
     if code != VPCE_OK:
@@ -632,7 +650,7 @@ def vpce_embedding_forward(table_shards, ids, vocab_start=None, *, out=None, fla
     s = ids.numel()
     if out is None:
         out = torch.empty((s, h), dtype=table_shards[0].dtype, device=ids.device)
-    ld_out = out.stride(0) if s > 1 else h
+    ld_out = _row_ld(out, h, "out")
     lib = load_library()
     code = int(lib.vpce_embedding_forward(ctypes.cast(_ptr_array([e.data_ptr() for e in table_shards]), _P),
                                           int(dtype), len(table_shards), _i64_array(vs), int(h), int(ld),
@@ -663,10 +681,13 @@ def vpce_embedding_backward(grad_out, ids, grad_shards, vocab_start=None, *, wor
     s = grad_out.shape[0]
     if ids.dtype != torch.int64 or not ids.is_cuda or ids.numel() != s:
         raise ValueError("ids must be a CUDA int64 tensor with one entry per row")
+    if s > 1 and grad_out.stride(0) == 0:
+        with torch.cuda.stream(stream):  # None: the current one
+            grad_out = _rows_of_their_own(grad_out)
     if workspace is None:
         workspace = torch.empty(vpce_embedding_backward_workspace_bytes(), dtype=torch.uint8, device=ids.device)
     lib = load_library()
-    code = int(lib.vpce_embedding_backward(_ptr(grad_out), int(code_dt), int(grad_out.stride(0) if s > 1 else h),
+    code = int(lib.vpce_embedding_backward(_ptr(grad_out), int(code_dt), int(_row_ld(grad_out, h, "grad_out")),
                                            ctypes.c_void_p(ids.data_ptr()), int(s),
                                            ctypes.cast(_ptr_array([g.data_ptr() for g in grad_shards]), _P),
                                            len(grad_shards), _i64_array(vs), int(h), int(ld),
@@ -729,6 +750,8 @@ def _column_shards(shards, vocab_start):
         w = shape[1]
         if stride[1] != 1 and w > 1:
             raise ValueError("shard columns must be contiguous")
+        if stride[0] == 0:
+            _row_ld(sh, w, "shards")
         dense = dense and stride[0] == w
         lds.add(stride[0])
         starts.append(starts[-1] + w)
@@ -907,7 +930,7 @@ def _row_shards(shards, vocab_start):
         if len(shape) != 2 or shape[1] != h or e.dtype is not dt or not e.is_cuda or (stride[1] != 1 and h > 1):
             raise ValueError("table shards must be 2-D CUDA tensors [w_i, h] of one dtype, contiguous columns")
         if shape[0] > 1:
-            lds.add(stride[0])
+            lds.add(_row_ld(e, h, "table shards"))
         starts.append(starts[-1] + shape[0])
         ptrs.append(e.data_ptr())
     if len(lds) > 1:
@@ -916,10 +939,6 @@ def _row_shards(shards, vocab_start):
         raise ValueError(f"vocab_start must be the shards' offsets {starts}")
     n = len(ptrs)
     return code, h, (ctypes.c_void_p * n)(*ptrs), (ctypes.c_int64 * (n + 1))(*starts), lds.pop() if lds else h
-
-
-def _row_stride(x, h):
-    return x.stride(0) if x.shape[0] > 1 else h
 
 
 @_on_stream
@@ -951,7 +970,7 @@ def vpce_embedding_dropout_forward(table_shards, ids, vocab_start=None, *, scale
     code = (_lib or load_library()).vpce_embedding_dropout_forward(
         ptrs, dtype, len(table_shards), starts, h, ld, _addr(ids), s,
         INT64_MIN if padding_id is None else int(padding_id), scale, p, _addr(rng), _addr(out), odt,
-        _row_stride(out, h), _addr(flag), _raw_stream(ids))
+        _row_ld(out, h, "out"), _addr(flag), _raw_stream(ids))
     if code != VPCE_OK:
         raise VPCEError(code, "vpce_embedding_dropout_forward")
     return out
@@ -969,7 +988,8 @@ def vpce_embedding_dropout_backward(grad_out, ids, grad_shards, vocab_start=None
     table, into the fp32 ``grad_shards`` (in place): added to what they hold,
     or, with ``accumulate=False``, written in full (zero rows for ids that do
     not occur).  ``scale``, ``p``, ``rng`` and ``padding_id`` are the
-    forward's."""
+    forward's.  A ``grad_out`` expanded over its rows (autograd's gradient of
+    a sum over them) is read through a dense copy."""
     import torch
 
     gdt, h, ptrs, starts, ld = _row_shards(grad_shards, vocab_start)
@@ -980,6 +1000,7 @@ def vpce_embedding_dropout_backward(grad_out, ids, grad_shards, vocab_start=None
     code_dt = {torch.bfloat16: VPCE_BF16, torch.float32: VPCE_FP32}.get(grad_out.dtype)
     if code_dt is None:
         raise TypeError("grad_out dtype must be bf16 or fp32")
+    grad_out = _rows_of_their_own(grad_out)
     s = grad_out.shape[0]
     _check_ids(ids, s)
     _check_rng(rng)
@@ -988,7 +1009,7 @@ def vpce_embedding_dropout_backward(grad_out, ids, grad_shards, vocab_start=None
         workspace = torch.empty(lib.vpce_embedding_dropout_backward_workspace_bytes(s, starts[-1], h),
                                 dtype=torch.uint8, device=ids.device)
     code = lib.vpce_embedding_dropout_backward(
-        _addr(grad_out), code_dt, _row_stride(grad_out, h), _addr(ids), s,
+        _addr(grad_out), code_dt, _row_ld(grad_out, h, "grad_out"), _addr(ids), s,
         INT64_MIN if padding_id is None else int(padding_id), scale, p, _addr(rng), ptrs, len(grad_shards), starts,
         h, ld, int(bool(accumulate)), _addr(workspace), workspace.numel(), _raw_stream(ids))
     if code != VPCE_OK:
