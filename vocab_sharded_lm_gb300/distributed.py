@@ -43,8 +43,7 @@ class CudaBackend:
                                      int(dtype), t, int(s), vpce._i64_array(vs), int(ld),
                                      ctypes.c_void_p(targets.data_ptr()), int(ignore_index),
                                      ctypes.c_void_p(part.data_ptr()), ctypes.c_void_p(tgt.data_ptr()),
-                                     ctypes.c_void_p(workspace.data_ptr()), workspace.numel(),
-                                     vpce._stream_ptr(stream)))
+                                     *vpce._workspace(workspace), vpce._stream_ptr(stream)))
         if code != vpce.VPCE_OK:
             raise vpce.VPCEError(code, "vpce_partials")
         return part, tgt
@@ -73,8 +72,7 @@ class CudaBackend:
                                              ctypes.c_void_p(tgt.data_ptr()), int(s), int(V),
                                              ctypes.c_void_p(targets.data_ptr()), int(ignore_index), int(red),
                                              ctypes.c_void_p(loss.data_ptr()), ctypes.c_void_p(row_loss.data_ptr()),
-                                             int(t_local), ctypes.c_void_p(workspace.data_ptr()),
-                                             workspace.numel(), vpce._stream_ptr(stream)))
+                                             int(t_local), *vpce._workspace(workspace), vpce._stream_ptr(stream)))
         if code != vpce.VPCE_OK:
             raise vpce.VPCEError(code, "vpce_combine_partials")
         return (row_loss if reduction == "none" else loss), row_loss

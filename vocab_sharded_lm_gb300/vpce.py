@@ -276,6 +276,13 @@ def new_workspace(t: int, s: int, device=None):
     return torch.empty(n, dtype=torch.uint8, device=device)
 
 
+def _workspace(ws):
+    """Address and size in bytes of a workspace, as the C entries take them."""
+    if not ws.is_cuda or not ws.is_contiguous():
+        raise ValueError("a workspace must be a contiguous CUDA tensor")
+    return ctypes.c_void_p(ws.data_ptr()), ws.numel() * ws.element_size()
+
+
 def _ptr(x):
     return ctypes.c_void_p(x.data_ptr()) if x is not None else None
 
@@ -320,8 +327,7 @@ def vpce_forward(shards, targets, vocab_start=None, *, ignore_index: int = -100,
     red, loss_out, row_loss_out, result = _outputs(reduction, loss_out, row_loss_out, s, dev)
     code = forward_raw([sh.data_ptr() for sh in shards], dtype, t, s, vs, ld,
                        ctypes.c_void_p(targets.data_ptr()), ignore_index, red, _ptr(loss_out),
-                       _ptr(row_loss_out), ctypes.c_void_p(workspace.data_ptr()), workspace.numel(),
-                       _stream_ptr(stream))
+                       _ptr(row_loss_out), *_workspace(workspace), _stream_ptr(stream))
     if code != VPCE_OK:
         raise VPCEError(code, "vpce_forward")
     return result, workspace
@@ -337,13 +343,11 @@ def vpce_backward(shards, targets, workspace, vocab_start=None, *, ignore_index:
     if grad_rows is not None:
         _check_grad_rows(grad_rows, s)
         code = backward_rows_raw(ptrs, dtype, len(shards), s, vs, ld, ctypes.c_void_p(targets.data_ptr()),
-                                 ignore_index, _ptr(grad_rows), ctypes.c_void_p(workspace.data_ptr()),
-                                 workspace.numel(), _stream_ptr(stream))
+                                 ignore_index, _ptr(grad_rows), *_workspace(workspace), _stream_ptr(stream))
         where = "vpce_backward_rows"
     else:
         code = backward_raw(ptrs, dtype, len(shards), s, vs, ld, ctypes.c_void_p(targets.data_ptr()),
-                            ignore_index, grad_output, ctypes.c_void_p(workspace.data_ptr()), workspace.numel(),
-                            _stream_ptr(stream))
+                            ignore_index, grad_output, *_workspace(workspace), _stream_ptr(stream))
         where = "vpce_backward"
     if code != VPCE_OK:
         raise VPCEError(code, where)
@@ -394,13 +398,12 @@ def vpce_forward_backward(shards, targets, vocab_start=None, *, ignore_index: in
         _check_grad_rows(grad_rows, s)
         code = forward_backward_rows_raw(ptrs, dtype, t, s, vs, ld, ctypes.c_void_p(targets.data_ptr()),
                                          ignore_index, red, _ptr(grad_rows), _ptr(loss_out), _ptr(row_loss_out),
-                                         ctypes.c_void_p(workspace.data_ptr()), workspace.numel(),
-                                         _stream_ptr(stream))
+                                         *_workspace(workspace), _stream_ptr(stream))
         where = "vpce_forward_backward_rows"
     else:
         code = forward_backward_raw(ptrs, dtype, t, s, vs, ld, ctypes.c_void_p(targets.data_ptr()), ignore_index,
                                     red, grad_output, _ptr(loss_out), _ptr(row_loss_out),
-                                    ctypes.c_void_p(workspace.data_ptr()), workspace.numel(), _stream_ptr(stream))
+                                    *_workspace(workspace), _stream_ptr(stream))
         where = "vpce_forward_backward"
     if code != VPCE_OK:
         raise VPCEError(code, where)
@@ -506,7 +509,7 @@ def vpce_lmhead_forward(hidden, weight_shards, targets, vocab_start=None, *, ign
     code = lmhead_forward_raw(ctypes.c_void_p(hidden.data_ptr()), ld_x, [w.data_ptr() for w in weight_shards],
                               ld_w, len(weight_shards), s, h, vocab_start, ctypes.c_void_p(targets.data_ptr()),
                               ignore_index, red, _ptr(loss_out), _ptr(row_loss_out),
-                              ctypes.c_void_p(workspace.data_ptr()), workspace.numel(), _stream_ptr(stream))
+                              *_workspace(workspace), _stream_ptr(stream))
     if code != VPCE_OK:
         raise VPCEError(code, "vpce_lmhead_forward")
     return result, workspace
@@ -548,10 +551,10 @@ def vpce_lmhead_backward(hidden, weight_shards, targets, fwd_workspace, vocab_st
         ctypes.c_void_p(hidden.data_ptr()), int(ld_x),
         ctypes.cast(_ptr_array([w.data_ptr() for w in weight_shards]), _P), int(ld_w), len(weight_shards), int(s),
         int(h), _i64_array(vocab_start), ctypes.c_void_p(targets.data_ptr()), int(ignore_index), float(grad_output),
-        _ptr(grad_rows), ctypes.c_void_p(fwd_workspace.data_ptr()), fwd_workspace.numel(),
+        _ptr(grad_rows), *_workspace(fwd_workspace),
         ctypes.c_void_p(grad_hidden.data_ptr()), int(ld_gx),
         ctypes.cast(_ptr_array([g.data_ptr() for g in grad_weight_shards]), _P), int(ld_gw),
-        ctypes.c_void_p(workspace.data_ptr()), workspace.numel(), _stream_ptr(stream)))
+        *_workspace(workspace), _stream_ptr(stream)))
     if code != VPCE_OK:
         raise VPCEError(code, "vpce_lmhead_backward")
     return grad_hidden, grad_weight_shards
@@ -630,7 +633,7 @@ def vpce_lmhead_forward_backward(hidden, weight_shards, targets, vocab_start=Non
         int(ignore_index), red, float(grad_output), _ptr(grad_rows), _ptr(loss_out), _ptr(row_loss_out),
         ctypes.c_void_p(grad_hidden.data_ptr()), int(ld_gx),
         ctypes.cast(_ptr_array([g.data_ptr() for g in grad_weight_shards]), _P), int(ld_gw),
-        ctypes.c_void_p(workspace.data_ptr()), workspace.numel(), _stream_ptr(stream)))
+        *_workspace(workspace), _stream_ptr(stream)))
     if code != VPCE_OK:
         raise VPCEError(code, "vpce_lmhead_forward_backward")
     return result, grad_hidden, grad_weight_shards
@@ -691,8 +694,7 @@ def vpce_embedding_backward(grad_out, ids, grad_shards, vocab_start=None, *, wor
                                            ctypes.c_void_p(ids.data_ptr()), int(s),
                                            ctypes.cast(_ptr_array([g.data_ptr() for g in grad_shards]), _P),
                                            len(grad_shards), _i64_array(vs), int(h), int(ld),
-                                           ctypes.c_void_p(workspace.data_ptr()), workspace.numel(),
-                                           _stream_ptr(stream)))
+                                           *_workspace(workspace), _stream_ptr(stream)))
     if code != VPCE_OK:
         raise VPCEError(code, "vpce_embedding_backward")
     return grad_shards
@@ -1011,7 +1013,7 @@ def vpce_embedding_dropout_backward(grad_out, ids, grad_shards, vocab_start=None
     code = lib.vpce_embedding_dropout_backward(
         _addr(grad_out), code_dt, _row_ld(grad_out, h, "grad_out"), _addr(ids), s,
         INT64_MIN if padding_id is None else int(padding_id), scale, p, _addr(rng), ptrs, len(grad_shards), starts,
-        h, ld, int(bool(accumulate)), _addr(workspace), workspace.numel(), _raw_stream(ids))
+        h, ld, int(bool(accumulate)), *_workspace(workspace), _raw_stream(ids))
     if code != VPCE_OK:
         raise VPCEError(code, "vpce_embedding_dropout_backward")
     return grad_shards
