@@ -31,10 +31,12 @@ from . import vpce
 class CudaBackend:
     """The library's kernels for the three local steps."""
 
+    @vpce._on_its_device
     def partials(self, shards, vocab_start, targets, ignore_index, workspace, stream=None):
         import torch
 
         dtype, s, vs, ld = vpce._describe(shards, vocab_start)
+        vpce._same_device(shards[0], targets=targets, workspace=workspace)
         t = len(shards)
         part = torch.empty((t, s, 2), dtype=torch.float32, device=targets.device)
         tgt = torch.empty(s, dtype=torch.float32, device=targets.device)
@@ -48,6 +50,7 @@ class CudaBackend:
             raise vpce.VPCEError(code, "vpce_partials")
         return part, tgt
 
+    @vpce._on_its_device
     def fold(self, part, stream=None):
         """[t, s, 2] partials -> [1, s, 2], shards folded in order."""
         import torch
@@ -60,10 +63,12 @@ class CudaBackend:
             raise vpce.VPCEError(code, "vpce_fold_partials")
         return out
 
+    @vpce._on_its_device
     def combine(self, part, tgt, V, targets, ignore_index, reduction, t_local, workspace, stream=None):
         import torch
 
         s = tgt.numel()
+        vpce._same_device(part, tgt=tgt, targets=targets, workspace=workspace)
         red = vpce.REDUCTIONS[reduction]
         loss = torch.empty((), dtype=torch.float32, device=tgt.device)
         row_loss = torch.empty(s, dtype=torch.float32, device=tgt.device)

@@ -7,7 +7,10 @@ call raises -- there is no fallback path.
 """
 from __future__ import annotations
 
+import contextlib
 import ctypes
+import functools
+import inspect
 import os
 import threading
 from typing import Any, NamedTuple
@@ -197,6 +200,62 @@ def backward_rows_raw(shard_ptrs, dtype, t, s, vocab_start, ld, targets_ptr, ign
 # ----------------------------------------------------------------------------
 # torch-tensor forms
 # ----------------------------------------------------------------------------
+_HERE = contextlib.nullcontext()
+
+
+def _device_guard(x, stream=None):
+    """Context for a call on ``x``'s device: the library launches on the
+    current device, so that one is made current."""
+    import torch
+
+    dev = x.get_device()
+    if dev < 0:  # not CUDA: the call's own checks say so
+        return _HERE
+    if stream is not None and stream.device.index != dev:
+        raise ValueError(f"stream of {stream.device} for tensors on cuda:{dev}")
+    return _HERE if dev == torch._C._cuda_getDevice() else torch.cuda.device(dev)
+
+
+def _first_operand(fn):
+    """Looks up the first tensor among a call's (or method's) arguments."""
+    names = list(inspect.signature(fn).parameters)
+    at = int(names[0] == "self")
+
+    def of(args, kw):
+        x = args[at] if len(args) > at else kw.get(names[at])
+        if isinstance(x, (list, tuple)):
+            x = x[0] if x else None
+        return x if hasattr(x, "get_device") else None
+
+    return of
+
+
+def _on_its_device(fn):
+    """The call is made on the device of its first operand."""
+    of = _first_operand(fn)
+
+    @functools.wraps(fn)
+    def call(*args, **kw):
+        x = of(args, kw)
+        with _HERE if x is None else _device_guard(x, kw.get("stream")):
+            return fn(*args, **kw)
+
+    return call
+
+
+def _same_device(x, **operands):
+    """Raises unless the operands (None: left out) are on ``x``'s device.
+    Pinned host memory passes: every device reads and writes it."""
+    dev = x.get_device()
+    for name, o in operands.items():
+        if o is not None and o.get_device() != dev and (o.is_cuda or not o.is_pinned()):
+            raise ValueError(f"{name} must be on the same device as the other operands (cuda:{dev})")
+
+
+def _numbered(name, shards):
+    return {f"{name} {i}": x for i, x in enumerate(shards)}
+
+
 def _row_ld(x, width, name):
     """Row stride of ``x`` [rows, width] for a C entry.  The entries read a
     stride of 0 as "dense", so rows that share memory (an expanded tensor's)
@@ -238,8 +297,9 @@ def _describe(shards, vocab_start):
     s = shards[0].shape[0]
     widths = []
     for sh in shards:
-        if sh.dtype != dt or sh.dim() != 2 or sh.shape[0] != s or not sh.is_cuda:
-            raise ValueError("shards must be 2-D CUDA tensors of one dtype and row count")
+        if sh.dtype != dt or sh.dim() != 2 or sh.shape[0] != s or not sh.is_cuda \
+                or sh.get_device() != shards[0].get_device():
+            raise ValueError("shards must be 2-D CUDA tensors of one dtype, row count and device")
         if sh.stride(1) != 1:
             raise ValueError("shard columns must be contiguous")
         _row_ld(sh, sh.shape[1], "shards")
@@ -310,6 +370,7 @@ def _check_grad_rows(grad_rows, s):
         raise ValueError("grad_rows must be a contiguous CUDA float32 tensor with one entry per row")
 
 
+@_on_its_device
 def vpce_forward(shards, targets, vocab_start=None, *, ignore_index: int = -100, reduction: str = "mean",
                  loss_out=None, row_loss_out=None, workspace=None, stream=None):
     """Loss of vocab-sharded logits.  Returns ``(loss, workspace)``; pass the
@@ -322,6 +383,7 @@ def vpce_forward(shards, targets, vocab_start=None, *, ignore_index: int = -100,
     dev = shards[0].device
     if targets.dtype != torch.int64 or not targets.is_cuda or targets.numel() != s:
         raise ValueError("targets must be a CUDA int64 tensor with one entry per row")
+    _same_device(shards[0], targets=targets, loss_out=loss_out, row_loss_out=row_loss_out, workspace=workspace)
     if workspace is None:
         workspace = new_workspace(t, s, dev)
     red, loss_out, row_loss_out, result = _outputs(reduction, loss_out, row_loss_out, s, dev)
@@ -333,12 +395,14 @@ def vpce_forward(shards, targets, vocab_start=None, *, ignore_index: int = -100,
     return result, workspace
 
 
+@_on_its_device
 def vpce_backward(shards, targets, workspace, vocab_start=None, *, ignore_index: int = -100,
                   grad_output: float = 1.0, grad_rows=None, stream=None):
     """Overwrite ``shards`` in place with dlogits of the preceding forward.
     ``grad_rows`` (a float32 vector, one entry per row) selects the per-row
     backward (vpce_backward_rows) instead of the scalar ``grad_output``."""
     dtype, s, vs, ld = _describe(shards, vocab_start)
+    _same_device(shards[0], targets=targets, grad_rows=grad_rows, workspace=workspace)
     ptrs = [sh.data_ptr() for sh in shards]
     if grad_rows is not None:
         _check_grad_rows(grad_rows, s)
@@ -376,6 +440,7 @@ def forward_backward_rows_raw(shard_ptrs, dtype, t, s, vocab_start, ld, targets_
                                               int(ws_bytes), stream))
 
 
+@_on_its_device
 def vpce_forward_backward(shards, targets, vocab_start=None, *, ignore_index: int = -100,
                           reduction: str = "mean", grad_output: float = 1.0, grad_rows=None, loss_out=None,
                           row_loss_out=None, workspace=None, stream=None):
@@ -390,12 +455,14 @@ def vpce_forward_backward(shards, targets, vocab_start=None, *, ignore_index: in
     dev = shards[0].device
     if targets.dtype != torch.int64 or not targets.is_cuda or targets.numel() != s:
         raise ValueError("targets must be a CUDA int64 tensor with one entry per row")
+    _same_device(shards[0], targets=targets, loss_out=loss_out, row_loss_out=row_loss_out, workspace=workspace)
     if workspace is None:
         workspace = new_workspace(t, s, dev)
     red, loss_out, row_loss_out, result = _outputs(reduction, loss_out, row_loss_out, s, dev)
     ptrs = [sh.data_ptr() for sh in shards]
     if grad_rows is not None:
         _check_grad_rows(grad_rows, s)
+        _same_device(shards[0], grad_rows=grad_rows)
         code = forward_backward_rows_raw(ptrs, dtype, t, s, vs, ld, ctypes.c_void_p(targets.data_ptr()),
                                          ignore_index, red, _ptr(grad_rows), _ptr(loss_out), _ptr(row_loss_out),
                                          *_workspace(workspace), _stream_ptr(stream))
@@ -423,8 +490,9 @@ def vpce_fused_plan(dtype: int, vocab_start, s: int) -> dict:
 
 def vpce_read_error_flag(workspace, stream=None) -> int:
     flag = ctypes.c_int(0)
-    code = load_library().vpce_read_error_flag(ctypes.c_void_p(workspace.data_ptr()), ctypes.byref(flag),
-                                               _stream_ptr(stream))
+    with _device_guard(workspace, stream):
+        code = load_library().vpce_read_error_flag(ctypes.c_void_p(workspace.data_ptr()), ctypes.byref(flag),
+                                                   _stream_ptr(stream))
     if code != VPCE_OK:
         raise VPCEError(code, "vpce_read_error_flag")
     return flag.value
@@ -446,11 +514,13 @@ def forward_static_raw(shard_ptrs, dtype, t, s, vocab_start, ld, targets_ptr, ig
                                        loss_ptr, row_loss_ptr, stream))
 
 
+@_on_its_device
 def vpce_forward_static(shards, targets, loss_out, vocab_start=None, *, ignore_index: int = -100,
                         reduction: str = "mean", row_loss_out=None, stream=None):
     """Loss of vocab-sharded logits into the caller's ``loss_out`` (and
     ``row_loss_out``), using no workspace from the caller."""
     dtype, s, vs, ld = _describe(shards, vocab_start)
+    _same_device(shards[0], targets=targets, loss_out=loss_out, row_loss_out=row_loss_out)
     red = REDUCTIONS[reduction]
     code = forward_static_raw([sh.data_ptr() for sh in shards], dtype, len(shards), s, vs, ld,
                               ctypes.c_void_p(targets.data_ptr()), ignore_index, red, _ptr(loss_out),
@@ -478,6 +548,7 @@ def lmhead_forward_raw(hidden_ptr, ld_hidden, weight_ptrs, ld_weight, t, s, h, v
                                        int(reduction), loss_ptr, row_loss_ptr, ws_ptr, int(ws_bytes), stream))
 
 
+@_on_its_device
 def vpce_lmhead_forward(hidden, weight_shards, targets, vocab_start=None, *, ignore_index: int = -100,
                         reduction: str = "mean", loss_out=None, row_loss_out=None, workspace=None, stream=None):
     """Loss of the logits ``hidden @ W_i^T`` of every vocabulary shard, formed
@@ -503,6 +574,8 @@ def vpce_lmhead_forward(hidden, weight_shards, targets, vocab_start=None, *, ign
     if targets.dtype != torch.int64 or not targets.is_cuda or targets.numel() != s:
         raise ValueError("targets must be a CUDA int64 tensor with one entry per row")
     dev = hidden.device
+    _same_device(hidden, targets=targets, loss_out=loss_out, row_loss_out=row_loss_out, workspace=workspace,
+                 **_numbered("weight shard", weight_shards))
     if workspace is None:
         workspace = torch.empty(vpce_lmhead_workspace_bytes(s), dtype=torch.uint8, device=dev)
     red, loss_out, row_loss_out, result = _outputs(reduction, loss_out, row_loss_out, s, dev)
@@ -519,6 +592,7 @@ def vpce_lmhead_backward_workspace_bytes(V: int, h: int) -> int:
     return int(load_library().vpce_lmhead_backward_workspace_bytes(int(V), int(h)))
 
 
+@_on_its_device
 def vpce_lmhead_backward(hidden, weight_shards, targets, fwd_workspace, vocab_start=None, *,
                          ignore_index: int = -100, grad_output: float = 1.0, grad_rows=None, grad_hidden=None,
                          grad_weight_shards=None, workspace=None, stream=None):
@@ -544,6 +618,9 @@ def vpce_lmhead_backward(hidden, weight_shards, targets, fwd_workspace, vocab_st
     ld_gw = _shared_ld(grad_weight_shards, h, "grad_weight_shards")
     if grad_rows is not None:
         _check_grad_rows(grad_rows, s)
+    _same_device(hidden, targets=targets, fwd_workspace=fwd_workspace, grad_rows=grad_rows, grad_hidden=grad_hidden,
+                 workspace=workspace, **_numbered("weight shard", weight_shards),
+                 **_numbered("weight gradient shard", grad_weight_shards))
     if workspace is None:
         workspace = torch.empty(vpce_lmhead_backward_workspace_bytes(vocab_start[-1], h), dtype=torch.uint8,
                                 device=dev)
@@ -571,8 +648,10 @@ def _table_desc(shards, vocab_start):
     dt = shards[0].dtype
     h = shards[0].shape[1]
     for e in shards:
-        if e.dtype != dt or e.dim() != 2 or e.shape[1] != h or not e.is_cuda or e.stride(1) != 1:
-            raise ValueError("table shards must be 2-D CUDA tensors [w_i, h] of one dtype, contiguous columns")
+        if e.dtype != dt or e.dim() != 2 or e.shape[1] != h or not e.is_cuda or e.stride(1) != 1 \
+                or e.get_device() != shards[0].get_device():
+            raise ValueError("table shards must be 2-D CUDA tensors [w_i, h] of one dtype and device, contiguous "
+                             "columns")
     ld = _shared_ld(shards, h, "table shards")
     if vocab_start is None:
         vocab_start = [0]
@@ -586,6 +665,7 @@ def vpce_lmhead_forward_backward_workspace_bytes(s: int, V: int, h: int) -> int:
     return int(load_library().vpce_lmhead_forward_backward_workspace_bytes(int(s), int(V), int(h)))
 
 
+@_on_its_device
 def vpce_lmhead_forward_backward(hidden, weight_shards, targets, vocab_start=None, *, ignore_index: int = -100,
                                  reduction: str = "mean", grad_output: float = 1.0, grad_rows=None, loss_out=None,
                                  row_loss_out=None, grad_hidden=None, grad_weight_shards=None, workspace=None,
@@ -623,6 +703,9 @@ def vpce_lmhead_forward_backward(hidden, weight_shards, targets, vocab_start=Non
     ld_gw = _shared_ld(grad_weight_shards, h, "grad_weight_shards")
     if grad_rows is not None:
         _check_grad_rows(grad_rows, s)
+    _same_device(hidden, targets=targets, loss_out=loss_out, row_loss_out=row_loss_out, grad_rows=grad_rows,
+                 grad_hidden=grad_hidden, workspace=workspace, **_numbered("weight shard", weight_shards),
+                 **_numbered("weight gradient shard", grad_weight_shards))
     if workspace is None:
         workspace = torch.empty(vpce_lmhead_forward_backward_workspace_bytes(s, vocab_start[-1], h),
                                 dtype=torch.uint8, device=dev)
@@ -639,6 +722,7 @@ def vpce_lmhead_forward_backward(hidden, weight_shards, targets, vocab_start=Non
     return result, grad_hidden, grad_weight_shards
 
 
+@_on_its_device
 def vpce_embedding_forward(table_shards, ids, vocab_start=None, *, out=None, flag=None, stream=None):
     """Rows ``table[ids]`` of a vocabulary-split table (zero rows for ids
     outside [0, V)).  ``flag`` (CUDA int32 scalar) receives bit 0 if any id
@@ -651,6 +735,7 @@ def vpce_embedding_forward(table_shards, ids, vocab_start=None, *, out=None, fla
     if ids.dtype != torch.int64 or not ids.is_cuda or ids.dim() != 1:
         raise ValueError("ids must be a 1-D CUDA int64 tensor")
     s = ids.numel()
+    _same_device(table_shards[0], ids=ids, out=out, flag=flag)
     if out is None:
         out = torch.empty((s, h), dtype=table_shards[0].dtype, device=ids.device)
     ld_out = _row_ld(out, h, "out")
@@ -668,6 +753,7 @@ def vpce_embedding_backward_workspace_bytes() -> int:
     return int(load_library().vpce_embedding_backward_workspace_bytes())
 
 
+@_on_its_device
 def vpce_embedding_backward(grad_out, ids, grad_shards, vocab_start=None, *, workspace=None, stream=None):
     """Accumulate the lookup's adjoint into the fp32 gradient-table shards
     (in place): each gradient row is added into its id's row."""
@@ -684,6 +770,7 @@ def vpce_embedding_backward(grad_out, ids, grad_shards, vocab_start=None, *, wor
     s = grad_out.shape[0]
     if ids.dtype != torch.int64 or not ids.is_cuda or ids.numel() != s:
         raise ValueError("ids must be a CUDA int64 tensor with one entry per row")
+    _same_device(grad_out, ids=ids, workspace=workspace, **_numbered("gradient table shard", grad_shards))
     if s > 1 and grad_out.stride(0) == 0:
         with torch.cuda.stream(stream):  # None: the current one
             grad_out = _rows_of_their_own(grad_out)
@@ -721,8 +808,8 @@ def _buffer(x, shape, dtype, device, name):
         import torch
 
         return torch.empty(shape, dtype=dtype, device=device)
-    if x.dtype != dtype or x.shape != shape or not x.is_cuda or not x.is_contiguous():
-        raise ValueError(f"{name} must be a contiguous CUDA {dtype} tensor of shape {shape}")
+    if x.dtype != dtype or x.shape != shape or x.get_device() != device.index or not x.is_contiguous():
+        raise ValueError(f"{name} must be a contiguous {dtype} tensor of shape {shape} on {device}")
     return x
 
 
@@ -744,11 +831,11 @@ def _column_shards(shards, vocab_start):
     code = VPCE_BF16 if dt is torch.bfloat16 else VPCE_FP32 if dt is torch.float32 else None
     if code is None:
         raise TypeError(f"unsupported logits dtype {dt}")
-    ptrs, starts, lds, dense = [], [0], set(), True
+    ptrs, starts, lds, dense, dev = [], [0], set(), True, first.get_device()
     for sh in shards:
         shape, stride = sh.shape, sh.stride()
-        if len(shape) != 2 or shape[0] != s or sh.dtype is not dt or not sh.is_cuda:
-            raise ValueError("shards must be 2-D CUDA tensors of one dtype and row count")
+        if len(shape) != 2 or shape[0] != s or sh.dtype is not dt or dev < 0 or sh.get_device() != dev:
+            raise ValueError("shards must be 2-D CUDA tensors of one dtype, row count and device")
         w = shape[1]
         if stride[1] != 1 and w > 1:
             raise ValueError("shard columns must be contiguous")
@@ -781,36 +868,42 @@ def _raw_stream(like):
 
 
 def _on_stream(fn):
-    """``stream=`` of a call: the whole call is made with that stream current,
-    so that what it allocates (outputs, workspace) belongs to the stream that
-    uses it."""
-    import functools
+    """The call is made on the device of its first operand, and, where
+    ``stream=`` is given, with that stream current, so that what it allocates
+    (outputs, workspace) belongs to the stream that uses it."""
+    of = _first_operand(fn)
 
     @functools.wraps(fn)
     def call(*args, stream=None, **kw):
-        if stream is None:
+        x = of(args, kw)
+        if x is None:
             return fn(*args, **kw)
-        import torch
+        guard = _device_guard(x, stream)
+        if stream is not None:
+            import torch
 
-        with torch.cuda.stream(stream):
+            guard = torch.cuda.stream(stream)  # makes its device current too
+        elif guard is _HERE:
+            return fn(*args, **kw)
+        with guard:
             return fn(*args, **kw)
 
     return call
 
 
-def _check_targets(targets, s):
+def _check_targets(targets, s, dev):
     import torch
 
-    if targets is not None and (targets.dtype is not torch.int64 or not targets.is_cuda or targets.numel() != s
-                                or not targets.is_contiguous()):
-        raise ValueError("targets must be a contiguous CUDA int64 tensor with one entry per row")
+    if targets is not None and (targets.dtype is not torch.int64 or targets.get_device() != dev.index
+                                or targets.numel() != s or not targets.is_contiguous()):
+        raise ValueError(f"targets must be a contiguous int64 tensor on {dev} with one entry per row")
 
 
-def _check_flag(flag):
+def _check_flag(flag, dev):
     import torch
 
-    if flag is not None and (flag.dtype != torch.int32 or not flag.is_cuda or flag.numel() != 1):
-        raise ValueError("flag must be a CUDA int32 tensor of one element")
+    if flag is not None and (flag.dtype != torch.int32 or flag.get_device() != dev.index or flag.numel() != 1):
+        raise ValueError(f"flag must be an int32 tensor of one element on {dev}")
 
 
 @_on_stream
@@ -828,8 +921,8 @@ def vpce_logprob_forward(shards, targets=None, vocab_start=None, *, ignore_index
 
     dtype, s, ptrs, starts, ld = _column_shards(shards, vocab_start)
     dev = shards[0].device
-    _check_targets(targets, s)
-    _check_flag(flag)
+    _check_targets(targets, s, dev)
+    _check_flag(flag, dev)
     if targets is None and logp_out is not None:
         raise ValueError("logp_out needs targets")
     top = int(top)
@@ -865,7 +958,7 @@ def vpce_logprob_backward(shards, targets, stats, vocab_start=None, *, ignore_in
 
     dtype, s, ptrs, starts, ld = _column_shards(shards, vocab_start)
     dev = shards[0].device
-    _check_targets(targets, s)
+    _check_targets(targets, s, dev)
     f32 = torch.float32
     _buffer(stats, (s, 4), f32, dev, "stats")
     for g, name in ((grad_logp, "grad_logp"), (grad_entropy, "grad_entropy")):
@@ -884,8 +977,8 @@ def vpce_logprob_backward(shards, targets, stats, vocab_start=None, *, ignore_in
         gptrs, ld_grad = ptrs, ld
     else:
         gdtype, gs, gptrs, gstarts, ld_grad = _column_shards(grad_shards, None)
-        if gdtype != dtype or gs != s or gstarts[:] != starts[:]:
-            raise ValueError("grad_shards must have the shards' dtype and shapes")
+        if gdtype != dtype or gs != s or gstarts[:] != starts[:] or grad_shards[0].get_device() != dev.index:
+            raise ValueError("grad_shards must have the shards' dtype, shapes and device")
     code = (_lib or load_library()).vpce_logprob_backward(
         ptrs, dtype, len(shards), s, starts, ld, _addr(targets), ignore_index, temperature, _addr(stats),
         _addr(grad_logp), _addr(grad_entropy), top, _addr(top_ids), _addr(grad_top_logp), gptrs, ld_grad,
@@ -898,20 +991,20 @@ def vpce_logprob_backward(shards, targets, stats, vocab_start=None, *, ignore_in
 # ----------------------------------------------------------------------------
 # scaled embedding lookup with dropout
 # ----------------------------------------------------------------------------
-def _check_rng(rng):
+def _check_rng(rng, dev):
     import torch
 
-    if rng is not None and (rng.dtype != torch.int64 or not rng.is_cuda or rng.numel() != 2
+    if rng is not None and (rng.dtype != torch.int64 or rng.get_device() != dev.index or rng.numel() != 2
                             or not rng.is_contiguous()):
-        raise ValueError("rng must be a CUDA int64 tensor of two elements (seed, offset)")
+        raise ValueError(f"rng must be an int64 tensor of two elements (seed, offset) on {dev}")
 
 
-def _check_ids(ids, s=None):
+def _check_ids(ids, dev, s=None):
     import torch
 
-    if ids.dtype != torch.int64 or not ids.is_cuda or ids.dim() != 1 or not ids.is_contiguous() \
+    if ids.dtype != torch.int64 or ids.get_device() != dev.index or ids.dim() != 1 or not ids.is_contiguous() \
             or (s is not None and ids.numel() != s):
-        raise ValueError("ids must be a contiguous 1-D CUDA int64 tensor, one entry per row")
+        raise ValueError(f"ids must be a contiguous 1-D int64 tensor on {dev}, one entry per row")
 
 
 def _row_shards(shards, vocab_start):
@@ -926,11 +1019,13 @@ def _row_shards(shards, vocab_start):
     if code is None:
         raise TypeError("table shards must be bf16 or fp32")
     h = shards[0].shape[-1]
-    ptrs, starts, lds = [], [0], set()
+    ptrs, starts, lds, dev = [], [0], set(), shards[0].get_device()
     for e in shards:
         shape, stride = e.shape, e.stride()
-        if len(shape) != 2 or shape[1] != h or e.dtype is not dt or not e.is_cuda or (stride[1] != 1 and h > 1):
-            raise ValueError("table shards must be 2-D CUDA tensors [w_i, h] of one dtype, contiguous columns")
+        if len(shape) != 2 or shape[1] != h or e.dtype is not dt or dev < 0 or e.get_device() != dev \
+                or (stride[1] != 1 and h > 1):
+            raise ValueError("table shards must be 2-D CUDA tensors [w_i, h] of one dtype and device, contiguous "
+                             "columns")
         if shape[0] > 1:
             lds.add(_row_ld(e, h, "table shards"))
         starts.append(starts[-1] + shape[0])
@@ -956,14 +1051,16 @@ def vpce_embedding_dropout_forward(table_shards, ids, vocab_start=None, *, scale
     import torch
 
     dtype, h, ptrs, starts, ld = _row_shards(table_shards, vocab_start)
-    _check_ids(ids)
-    _check_rng(rng)
-    _check_flag(flag)
+    dev = table_shards[0].device
+    _check_ids(ids, dev)
+    _check_rng(rng, dev)
+    _check_flag(flag, dev)
     s = ids.numel()
     if out is None:
         out = torch.empty((s, h), dtype=out_dtype or table_shards[0].dtype, device=ids.device)
-    elif out.dim() != 2 or tuple(out.shape) != (s, h) or not out.is_cuda or (h > 1 and out.stride(1) != 1):
-        raise ValueError("out must be a CUDA [s, h] tensor with contiguous columns")
+    elif out.dim() != 2 or tuple(out.shape) != (s, h) or out.get_device() != dev.index \
+            or (h > 1 and out.stride(1) != 1):
+        raise ValueError(f"out must be an [s, h] tensor on {dev} with contiguous columns")
     elif out_dtype is not None and out.dtype != out_dtype:
         raise TypeError("out is not of out_dtype")
     odt = {torch.bfloat16: VPCE_BF16, torch.float32: VPCE_FP32}.get(out.dtype)
@@ -997,15 +1094,19 @@ def vpce_embedding_dropout_backward(grad_out, ids, grad_shards, vocab_start=None
     gdt, h, ptrs, starts, ld = _row_shards(grad_shards, vocab_start)
     if gdt != VPCE_FP32:
         raise TypeError("gradient table shards must be fp32")
-    if grad_out.dim() != 2 or grad_out.shape[1] != h or not grad_out.is_cuda or (h > 1 and grad_out.stride(1) != 1):
-        raise ValueError("grad_out must be a CUDA [s, h] tensor with contiguous columns")
+    dev = grad_shards[0].device
+    if grad_out.dim() != 2 or grad_out.shape[1] != h or grad_out.get_device() != dev.index \
+            or (h > 1 and grad_out.stride(1) != 1):
+        raise ValueError(f"grad_out must be an [s, h] tensor on {dev} with contiguous columns")
     code_dt = {torch.bfloat16: VPCE_BF16, torch.float32: VPCE_FP32}.get(grad_out.dtype)
     if code_dt is None:
         raise TypeError("grad_out dtype must be bf16 or fp32")
     grad_out = _rows_of_their_own(grad_out)
     s = grad_out.shape[0]
-    _check_ids(ids, s)
-    _check_rng(rng)
+    _check_ids(ids, dev, s)
+    _check_rng(rng, dev)
+    if workspace is not None:
+        _same_device(grad_out, workspace=workspace)
     lib = _lib or load_library()
     if workspace is None:
         workspace = torch.empty(lib.vpce_embedding_dropout_backward_workspace_bytes(s, starts[-1], h),
