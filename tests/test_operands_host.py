@@ -206,3 +206,14 @@ def test_local_steps_of_the_process_group_run_on_their_operands_device(lib, devi
     with pytest.raises(ValueError):
         be.combine(new(1, S, 2), new(S), V, ids(), -100, "mean", 1, new(256, dtype=U8, index=1))
     assert lib.calls == [] and devices == []
+
+
+@pytest.mark.parametrize("call", CALLS, ids=lambda v: v.__name__)
+@pytest.mark.parametrize("how", ["one word for all", "every second word"])
+def test_targets_and_ids_are_consecutive_words(lib, monkeypatch, call, how):
+    """The kernels read s words from the address on."""
+    bad = new(1, dtype=I64).expand(S) if how == "one word for all" else new(2 * S, dtype=I64)[::2]
+    monkeypatch.setitem(globals(), "ids", lambda: bad)
+    with pytest.raises(ValueError):
+        call(-1)
+    assert lib.calls == []

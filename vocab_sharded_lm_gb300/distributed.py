@@ -36,6 +36,7 @@ class CudaBackend:
         import torch
 
         dtype, s, vs, ld = vpce._describe(shards, vocab_start)
+        vpce._check_index(targets, s, "targets")
         vpce._same_device(shards[0], targets=targets, workspace=workspace)
         t = len(shards)
         part = torch.empty((t, s, 2), dtype=torch.float32, device=targets.device)
@@ -68,6 +69,7 @@ class CudaBackend:
         import torch
 
         s = tgt.numel()
+        vpce._check_index(targets, s, "targets")
         vpce._same_device(part, tgt=tgt, targets=targets, workspace=workspace)
         red = vpce.REDUCTIONS[reduction]
         loss = torch.empty((), dtype=torch.float32, device=tgt.device)

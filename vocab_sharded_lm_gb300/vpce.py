@@ -362,6 +362,14 @@ def _outputs(reduction, loss_out, row_loss_out, s, dev):
     return red, loss_out, row_loss_out, loss_out
 
 
+def _check_index(x, s, name):
+    """Targets or ids: one int64 per row, read as s consecutive words."""
+    import torch
+
+    if x.dtype != torch.int64 or not x.is_cuda or x.numel() != s or not x.is_contiguous():
+        raise ValueError(f"{name} must be a contiguous CUDA int64 tensor with one entry per row")
+
+
 def _check_grad_rows(grad_rows, s):
     import torch
 
@@ -381,8 +389,7 @@ def vpce_forward(shards, targets, vocab_start=None, *, ignore_index: int = -100,
     dtype, s, vs, ld = _describe(shards, vocab_start)
     t = len(shards)
     dev = shards[0].device
-    if targets.dtype != torch.int64 or not targets.is_cuda or targets.numel() != s:
-        raise ValueError("targets must be a CUDA int64 tensor with one entry per row")
+    _check_index(targets, s, "targets")
     _same_device(shards[0], targets=targets, loss_out=loss_out, row_loss_out=row_loss_out, workspace=workspace)
     if workspace is None:
         workspace = new_workspace(t, s, dev)
@@ -402,6 +409,7 @@ def vpce_backward(shards, targets, workspace, vocab_start=None, *, ignore_index:
     ``grad_rows`` (a float32 vector, one entry per row) selects the per-row
     backward (vpce_backward_rows) instead of the scalar ``grad_output``."""
     dtype, s, vs, ld = _describe(shards, vocab_start)
+    _check_index(targets, s, "targets")
     _same_device(shards[0], targets=targets, grad_rows=grad_rows, workspace=workspace)
     ptrs = [sh.data_ptr() for sh in shards]
     if grad_rows is not None:
@@ -453,8 +461,7 @@ def vpce_forward_backward(shards, targets, vocab_start=None, *, ignore_index: in
     dtype, s, vs, ld = _describe(shards, vocab_start)
     t = len(shards)
     dev = shards[0].device
-    if targets.dtype != torch.int64 or not targets.is_cuda or targets.numel() != s:
-        raise ValueError("targets must be a CUDA int64 tensor with one entry per row")
+    _check_index(targets, s, "targets")
     _same_device(shards[0], targets=targets, loss_out=loss_out, row_loss_out=row_loss_out, workspace=workspace)
     if workspace is None:
         workspace = new_workspace(t, s, dev)
@@ -520,6 +527,7 @@ def vpce_forward_static(shards, targets, loss_out, vocab_start=None, *, ignore_i
     """Loss of vocab-sharded logits into the caller's ``loss_out`` (and
     ``row_loss_out``), using no workspace from the caller."""
     dtype, s, vs, ld = _describe(shards, vocab_start)
+    _check_index(targets, s, "targets")
     _same_device(shards[0], targets=targets, loss_out=loss_out, row_loss_out=row_loss_out)
     red = REDUCTIONS[reduction]
     code = forward_static_raw([sh.data_ptr() for sh in shards], dtype, len(shards), s, vs, ld,
@@ -571,8 +579,7 @@ def vpce_lmhead_forward(hidden, weight_shards, targets, vocab_start=None, *, ign
         vocab_start = [0]
         for w in weight_shards:
             vocab_start.append(vocab_start[-1] + w.shape[0])
-    if targets.dtype != torch.int64 or not targets.is_cuda or targets.numel() != s:
-        raise ValueError("targets must be a CUDA int64 tensor with one entry per row")
+    _check_index(targets, s, "targets")
     dev = hidden.device
     _same_device(hidden, targets=targets, loss_out=loss_out, row_loss_out=row_loss_out, workspace=workspace,
                  **_numbered("weight shard", weight_shards))
@@ -602,6 +609,7 @@ def vpce_lmhead_backward(hidden, weight_shards, targets, fwd_workspace, vocab_st
     import torch
 
     s, h = hidden.shape
+    _check_index(targets, s, "targets")
     if vocab_start is None:
         vocab_start = [0]
         for w in weight_shards:
@@ -692,8 +700,7 @@ def vpce_lmhead_forward_backward(hidden, weight_shards, targets, vocab_start=Non
         for w in weight_shards:
             vocab_start.append(vocab_start[-1] + w.shape[0])
     vocab_start = [int(v) for v in vocab_start]
-    if targets.dtype != torch.int64 or not targets.is_cuda or targets.numel() != s:
-        raise ValueError("targets must be a CUDA int64 tensor with one entry per row")
+    _check_index(targets, s, "targets")
     dev = hidden.device
     if grad_hidden is None:
         grad_hidden = torch.empty((s, h), dtype=torch.bfloat16, device=dev)
@@ -732,9 +739,10 @@ def vpce_embedding_forward(table_shards, ids, vocab_start=None, *, out=None, fla
     dtype, h, ld, vs = _table_desc(table_shards, vocab_start)
     if dtype is None:
         raise TypeError("table dtype must be bf16 or fp32")
-    if ids.dtype != torch.int64 or not ids.is_cuda or ids.dim() != 1:
+    if ids.dim() != 1:
         raise ValueError("ids must be a 1-D CUDA int64 tensor")
     s = ids.numel()
+    _check_index(ids, s, "ids")
     _same_device(table_shards[0], ids=ids, out=out, flag=flag)
     if out is None:
         out = torch.empty((s, h), dtype=table_shards[0].dtype, device=ids.device)
@@ -768,8 +776,7 @@ def vpce_embedding_backward(grad_out, ids, grad_shards, vocab_start=None, *, wor
     if code_dt is None:
         raise TypeError("grad_out dtype must be bf16 or fp32")
     s = grad_out.shape[0]
-    if ids.dtype != torch.int64 or not ids.is_cuda or ids.numel() != s:
-        raise ValueError("ids must be a CUDA int64 tensor with one entry per row")
+    _check_index(ids, s, "ids")
     _same_device(grad_out, ids=ids, workspace=workspace, **_numbered("gradient table shard", grad_shards))
     if s > 1 and grad_out.stride(0) == 0:
         with torch.cuda.stream(stream):  # None: the current one
