@@ -7,7 +7,6 @@ call raises -- there is no fallback path.
 """
 from __future__ import annotations
 
-import contextlib
 import ctypes
 import functools
 import inspect
@@ -200,45 +199,35 @@ def backward_rows_raw(shard_ptrs, dtype, t, s, vocab_start, ld, targets_ptr, ign
 # ----------------------------------------------------------------------------
 # torch-tensor forms
 # ----------------------------------------------------------------------------
-_HERE = contextlib.nullcontext()
-
-
-def _device_guard(x, stream=None):
-    """Context for a call on ``x``'s device: the library launches on the
-    current device, so that one is made current."""
-    import torch
-
-    dev = x.get_device()
-    if dev < 0:  # not CUDA: the call's own checks say so
-        return _HERE
-    if stream is not None and stream.device.index != dev:
-        raise ValueError(f"stream of {stream.device} for tensors on cuda:{dev}")
-    return _HERE if dev == torch._C._cuda_getDevice() else torch.cuda.device(dev)
-
-
-def _first_operand(fn):
-    """Looks up the first tensor among a call's (or method's) arguments."""
+def _on_its_device(fn, own_stream=False):
+    """The call is made on the device of its first operand (the first tensor of
+    its first argument, a method's second).  own_stream: and, where ``stream=``
+    is given, with that stream current, so that what it allocates (outputs,
+    workspace) belongs to the stream that uses it."""
     names = list(inspect.signature(fn).parameters)
     at = int(names[0] == "self")
-
-    def of(args, kw):
-        x = args[at] if len(args) > at else kw.get(names[at])
-        if isinstance(x, (list, tuple)):
-            x = x[0] if x else None
-        return x if hasattr(x, "get_device") else None
-
-    return of
-
-
-def _on_its_device(fn):
-    """The call is made on the device of its first operand."""
-    of = _first_operand(fn)
+    name = names[at]
 
     @functools.wraps(fn)
-    def call(*args, **kw):
-        x = of(args, kw)
-        with _HERE if x is None else _device_guard(x, kw.get("stream")):
-            return fn(*args, **kw)
+    def call(*args, stream=None, **kw):
+        import torch
+
+        x = args[at] if len(args) > at else kw.get(name)
+        if isinstance(x, (list, tuple)) and x:
+            x = x[0]
+        dev = x.get_device() if isinstance(x, torch.Tensor) else -1  # -1: the call's own checks refuse it
+        if stream is None:
+            if dev < 0 or dev == torch._C._cuda_getDevice():
+                return fn(*args, **kw)
+            with torch.cuda.device(dev):
+                return fn(*args, **kw)
+        if dev >= 0 and stream.device.index != dev:
+            raise ValueError(f"stream of {stream.device} for tensors on cuda:{dev}")
+        if own_stream:
+            with torch.cuda.stream(stream):  # makes its device current too
+                return fn(*args, **kw)
+        with torch.cuda.device(dev if dev >= 0 else None):
+            return fn(*args, stream=stream, **kw)
 
     return call
 
@@ -322,8 +311,9 @@ def _describe(shards, vocab_start):
 def _stream_ptr(stream):
     import torch
 
-    st = torch.cuda.current_stream() if stream is None else stream
-    return ctypes.c_void_p(st.cuda_stream)
+    if stream is None:
+        return ctypes.c_void_p(_raw_stream(torch._C._cuda_getDevice()))
+    return ctypes.c_void_p(stream.cuda_stream)
 
 
 def new_workspace(t: int, s: int, device=None):
@@ -495,11 +485,11 @@ def vpce_fused_plan(dtype: int, vocab_start, s: int) -> dict:
     return {"kernel": ["split", "stream"][k.value], "cluster": c.value, "grid": g.value}
 
 
+@_on_its_device
 def vpce_read_error_flag(workspace, stream=None) -> int:
     flag = ctypes.c_int(0)
-    with _device_guard(workspace, stream):
-        code = load_library().vpce_read_error_flag(ctypes.c_void_p(workspace.data_ptr()), ctypes.byref(flag),
-                                                   _stream_ptr(stream))
+    code = load_library().vpce_read_error_flag(ctypes.c_void_p(workspace.data_ptr()), ctypes.byref(flag),
+                                               _stream_ptr(stream))
     if code != VPCE_OK:
         raise VPCEError(code, "vpce_read_error_flag")
     return flag.value
@@ -809,14 +799,15 @@ class LogprobResult(NamedTuple):
     stats: Any
 
 
-def _buffer(x, shape, dtype, device, name):
-    """``x`` checked, or a new tensor: contiguous CUDA memory of this shape."""
+def _buffer(x, shape, dtype, like, dev, name):
+    """``x`` checked, or a new tensor: contiguous memory of this shape where
+    ``like`` is, GPU ``dev``."""
     if x is None:
         import torch
 
-        return torch.empty(shape, dtype=dtype, device=device)
-    if x.dtype != dtype or x.shape != shape or x.get_device() != device.index or not x.is_contiguous():
-        raise ValueError(f"{name} must be a contiguous {dtype} tensor of shape {shape} on {device}")
+        return torch.empty(shape, dtype=dtype, device=like.device)
+    if x.dtype != dtype or x.shape != shape or x.get_device() != dev or not x.is_contiguous():
+        raise ValueError(f"{name} must be a contiguous {dtype} tensor of shape {shape} on cuda:{dev}")
     return x
 
 
@@ -866,54 +857,34 @@ def _column_shards(shards, vocab_start):
     return code, s, (ctypes.c_void_p * n)(*ptrs), (ctypes.c_int64 * (n + 1))(*starts), ld
 
 
-def _raw_stream(like):
-    """Handle of the current stream of ``like``'s device (read as an integer:
+def _raw_stream(dev):
+    """Handle of the current stream of GPU ``dev`` (read as an integer:
     building a Stream object costs some microseconds)."""
     import torch
 
-    return torch._C._cuda_getCurrentRawStream(like.get_device())
-
-
-def _on_stream(fn):
-    """The call is made on the device of its first operand, and, where
-    ``stream=`` is given, with that stream current, so that what it allocates
-    (outputs, workspace) belongs to the stream that uses it."""
-    of = _first_operand(fn)
-
-    @functools.wraps(fn)
-    def call(*args, stream=None, **kw):
-        x = of(args, kw)
-        if x is None:
-            return fn(*args, **kw)
-        guard = _device_guard(x, stream)
-        if stream is not None:
-            import torch
-
-            guard = torch.cuda.stream(stream)  # makes its device current too
-        elif guard is _HERE:
-            return fn(*args, **kw)
-        with guard:
-            return fn(*args, **kw)
-
-    return call
+    return torch._C._cuda_getCurrentRawStream(dev)
 
 
 def _check_targets(targets, s, dev):
+    if targets is None:
+        return
     import torch
 
-    if targets is not None and (targets.dtype is not torch.int64 or targets.get_device() != dev.index
-                                or targets.numel() != s or not targets.is_contiguous()):
-        raise ValueError(f"targets must be a contiguous int64 tensor on {dev} with one entry per row")
+    if targets.dtype is not torch.int64 or targets.get_device() != dev or targets.numel() != s \
+            or not targets.is_contiguous():
+        raise ValueError(f"targets must be a contiguous int64 tensor on cuda:{dev} with one entry per row")
 
 
 def _check_flag(flag, dev):
+    if flag is None:
+        return
     import torch
 
-    if flag is not None and (flag.dtype != torch.int32 or flag.get_device() != dev.index or flag.numel() != 1):
-        raise ValueError(f"flag must be an int32 tensor of one element on {dev}")
+    if flag.dtype != torch.int32 or flag.get_device() != dev or flag.numel() != 1:
+        raise ValueError(f"flag must be an int32 tensor of one element on cuda:{dev}")
 
 
-@_on_stream
+@functools.partial(_on_its_device, own_stream=True)
 def vpce_logprob_forward(shards, targets=None, vocab_start=None, *, ignore_index: int = -100,
                          temperature: float = 1.0, top: int = 0, logp_out=None, entropy_out=None, top_ids_out=None,
                          top_logp_out=None, stats_out=None, flag=None) -> LogprobResult:
@@ -927,7 +898,7 @@ def vpce_logprob_forward(shards, targets=None, vocab_start=None, *, ignore_index
     import torch
 
     dtype, s, ptrs, starts, ld = _column_shards(shards, vocab_start)
-    dev = shards[0].device
+    dev = shards[0].get_device()
     _check_targets(targets, s, dev)
     _check_flag(flag, dev)
     if targets is None and logp_out is not None:
@@ -938,20 +909,20 @@ def vpce_logprob_forward(shards, targets=None, vocab_start=None, *, ignore_index
     if top == 0 and (top_ids_out is not None or top_logp_out is not None):
         raise ValueError("top_ids_out and top_logp_out need top > 0")
     f32 = torch.float32
-    logp = _buffer(logp_out, (s,), f32, dev, "logp_out") if targets is not None else None
-    entropy = _buffer(entropy_out, (s,), f32, dev, "entropy_out")
-    ids = _buffer(top_ids_out, (s, top), torch.int64, dev, "top_ids_out") if top else None
-    top_logp = _buffer(top_logp_out, (s, top), f32, dev, "top_logp_out") if top else None
-    stats = _buffer(stats_out, (s, 4), f32, dev, "stats_out")
+    logp = _buffer(logp_out, (s,), f32, shards[0], dev, "logp_out") if targets is not None else None
+    entropy = _buffer(entropy_out, (s,), f32, shards[0], dev, "entropy_out")
+    ids = _buffer(top_ids_out, (s, top), torch.int64, shards[0], dev, "top_ids_out") if top else None
+    top_logp = _buffer(top_logp_out, (s, top), f32, shards[0], dev, "top_logp_out") if top else None
+    stats = _buffer(stats_out, (s, 4), f32, shards[0], dev, "stats_out")
     code = (_lib or load_library()).vpce_logprob_forward(
         ptrs, dtype, len(shards), s, starts, ld, _addr(targets), ignore_index, temperature, top, _addr(logp),
-        _addr(entropy), _addr(ids), _addr(top_logp), _addr(stats), _addr(flag), _raw_stream(shards[0]))
+        _addr(entropy), _addr(ids), _addr(top_logp), _addr(stats), _addr(flag), _raw_stream(dev))
     if code != VPCE_OK:
         raise VPCEError(code, "vpce_logprob_forward")
     return LogprobResult(logp, entropy, ids, top_logp, stats)
 
 
-@_on_stream
+@functools.partial(_on_its_device, own_stream=True)
 def vpce_logprob_backward(shards, targets, stats, vocab_start=None, *, ignore_index: int = -100,
                           temperature: float = 1.0, grad_logp=None, grad_entropy=None, top_ids=None,
                           grad_top_logp=None, grad_shards=None):
@@ -964,32 +935,32 @@ def vpce_logprob_backward(shards, targets, stats, vocab_start=None, *, ignore_in
     import torch
 
     dtype, s, ptrs, starts, ld = _column_shards(shards, vocab_start)
-    dev = shards[0].device
+    dev = shards[0].get_device()
     _check_targets(targets, s, dev)
     f32 = torch.float32
-    _buffer(stats, (s, 4), f32, dev, "stats")
+    _buffer(stats, (s, 4), f32, shards[0], dev, "stats")
     for g, name in ((grad_logp, "grad_logp"), (grad_entropy, "grad_entropy")):
         if g is not None:
-            _buffer(g, (s,), f32, dev, name)
+            _buffer(g, (s,), f32, shards[0], dev, name)
     if (top_ids is None) != (grad_top_logp is None):
         raise ValueError("top_ids and grad_top_logp go together")
     top = 0
     if top_ids is not None:
         top = top_ids.shape[-1]
-        _buffer(top_ids, (s, top), torch.int64, dev, "top_ids")
-        _buffer(grad_top_logp, (s, top), f32, dev, "grad_top_logp")
+        _buffer(top_ids, (s, top), torch.int64, shards[0], dev, "top_ids")
+        _buffer(grad_top_logp, (s, top), f32, shards[0], dev, "grad_top_logp")
     if grad_shards is None:
-        grad_shards = [torch.empty(sh.shape, dtype=sh.dtype, device=dev) for sh in shards]
+        grad_shards = [torch.empty(sh.shape, dtype=sh.dtype, device=sh.device) for sh in shards]
     if grad_shards is shards:
         gptrs, ld_grad = ptrs, ld
     else:
         gdtype, gs, gptrs, gstarts, ld_grad = _column_shards(grad_shards, None)
-        if gdtype != dtype or gs != s or gstarts[:] != starts[:] or grad_shards[0].get_device() != dev.index:
+        if gdtype != dtype or gs != s or gstarts[:] != starts[:] or grad_shards[0].get_device() != dev:
             raise ValueError("grad_shards must have the shards' dtype, shapes and device")
     code = (_lib or load_library()).vpce_logprob_backward(
         ptrs, dtype, len(shards), s, starts, ld, _addr(targets), ignore_index, temperature, _addr(stats),
         _addr(grad_logp), _addr(grad_entropy), top, _addr(top_ids), _addr(grad_top_logp), gptrs, ld_grad,
-        _raw_stream(shards[0]))
+        _raw_stream(dev))
     if code != VPCE_OK:
         raise VPCEError(code, "vpce_logprob_backward")
     return grad_shards
@@ -999,19 +970,20 @@ def vpce_logprob_backward(shards, targets, stats, vocab_start=None, *, ignore_in
 # scaled embedding lookup with dropout
 # ----------------------------------------------------------------------------
 def _check_rng(rng, dev):
+    if rng is None:
+        return
     import torch
 
-    if rng is not None and (rng.dtype != torch.int64 or rng.get_device() != dev.index or rng.numel() != 2
-                            or not rng.is_contiguous()):
-        raise ValueError(f"rng must be an int64 tensor of two elements (seed, offset) on {dev}")
+    if rng.dtype != torch.int64 or rng.get_device() != dev or rng.numel() != 2 or not rng.is_contiguous():
+        raise ValueError(f"rng must be an int64 tensor of two elements (seed, offset) on cuda:{dev}")
 
 
 def _check_ids(ids, dev, s=None):
     import torch
 
-    if ids.dtype != torch.int64 or ids.get_device() != dev.index or ids.dim() != 1 or not ids.is_contiguous() \
+    if ids.dtype != torch.int64 or ids.get_device() != dev or ids.dim() != 1 or not ids.is_contiguous() \
             or (s is not None and ids.numel() != s):
-        raise ValueError(f"ids must be a contiguous 1-D int64 tensor on {dev}, one entry per row")
+        raise ValueError(f"ids must be a contiguous 1-D int64 tensor on cuda:{dev}, one entry per row")
 
 
 def _row_shards(shards, vocab_start):
@@ -1045,7 +1017,7 @@ def _row_shards(shards, vocab_start):
     return code, h, (ctypes.c_void_p * n)(*ptrs), (ctypes.c_int64 * (n + 1))(*starts), lds.pop() if lds else h
 
 
-@_on_stream
+@functools.partial(_on_its_device, own_stream=True)
 def vpce_embedding_dropout_forward(table_shards, ids, vocab_start=None, *, scale: float = 1.0, p: float = 0.0,
                                    rng=None, padding_id=None, out=None, out_dtype=None, flag=None):
     """Rows ``scale * dropout(table[ids], p)`` of a vocabulary-split table.
@@ -1058,25 +1030,28 @@ def vpce_embedding_dropout_forward(table_shards, ids, vocab_start=None, *, scale
     import torch
 
     dtype, h, ptrs, starts, ld = _row_shards(table_shards, vocab_start)
-    dev = table_shards[0].device
+    dev = table_shards[0].get_device()
     _check_ids(ids, dev)
     _check_rng(rng, dev)
     _check_flag(flag, dev)
     s = ids.numel()
     if out is None:
         out = torch.empty((s, h), dtype=out_dtype or table_shards[0].dtype, device=ids.device)
-    elif out.dim() != 2 or tuple(out.shape) != (s, h) or out.get_device() != dev.index \
-            or (h > 1 and out.stride(1) != 1):
-        raise ValueError(f"out must be an [s, h] tensor on {dev} with contiguous columns")
-    elif out_dtype is not None and out.dtype != out_dtype:
-        raise TypeError("out is not of out_dtype")
+        ld_out = h
+    else:
+        stride = out.stride()
+        if out.shape != (s, h) or out.get_device() != dev or (h > 1 and stride[1] != 1):
+            raise ValueError(f"out must be an [s, h] tensor on cuda:{dev} with contiguous columns")
+        if out_dtype is not None and out.dtype != out_dtype:
+            raise TypeError("out is not of out_dtype")
+        ld_out = (stride[0] or _row_ld(out, h, "out")) if s > 1 else h
     odt = {torch.bfloat16: VPCE_BF16, torch.float32: VPCE_FP32}.get(out.dtype)
     if odt is None:
         raise TypeError("out dtype must be bf16 or fp32")
     code = (_lib or load_library()).vpce_embedding_dropout_forward(
         ptrs, dtype, len(table_shards), starts, h, ld, _addr(ids), s,
         INT64_MIN if padding_id is None else int(padding_id), scale, p, _addr(rng), _addr(out), odt,
-        _row_ld(out, h, "out"), _addr(flag), _raw_stream(ids))
+        ld_out, _addr(flag), _raw_stream(dev))
     if code != VPCE_OK:
         raise VPCEError(code, "vpce_embedding_dropout_forward")
     return out
@@ -1086,7 +1061,7 @@ def vpce_embedding_dropout_backward_workspace_bytes(s: int, V: int, h: int) -> i
     return int(load_library().vpce_embedding_dropout_backward_workspace_bytes(int(s), int(V), int(h)))
 
 
-@_on_stream
+@functools.partial(_on_its_device, own_stream=True)
 def vpce_embedding_dropout_backward(grad_out, ids, grad_shards, vocab_start=None, *, scale: float = 1.0,
                                     p: float = 0.0, rng=None, padding_id=None, accumulate: bool = True,
                                     workspace=None):
@@ -1101,27 +1076,29 @@ def vpce_embedding_dropout_backward(grad_out, ids, grad_shards, vocab_start=None
     gdt, h, ptrs, starts, ld = _row_shards(grad_shards, vocab_start)
     if gdt != VPCE_FP32:
         raise TypeError("gradient table shards must be fp32")
-    dev = grad_shards[0].device
-    if grad_out.dim() != 2 or grad_out.shape[1] != h or grad_out.get_device() != dev.index \
-            or (h > 1 and grad_out.stride(1) != 1):
-        raise ValueError(f"grad_out must be an [s, h] tensor on {dev} with contiguous columns")
+    dev = grad_shards[0].get_device()
+    shape, stride = grad_out.shape, grad_out.stride()
+    if len(shape) != 2 or shape[1] != h or grad_out.get_device() != dev or (h > 1 and stride[1] != 1):
+        raise ValueError(f"grad_out must be an [s, h] tensor on cuda:{dev} with contiguous columns")
     code_dt = {torch.bfloat16: VPCE_BF16, torch.float32: VPCE_FP32}.get(grad_out.dtype)
     if code_dt is None:
         raise TypeError("grad_out dtype must be bf16 or fp32")
-    grad_out = _rows_of_their_own(grad_out)
-    s = grad_out.shape[0]
+    s = shape[0]
+    ld_out = stride[0] if s > 1 else h
+    if ld_out == 0:
+        grad_out, ld_out = _rows_of_their_own(grad_out), h
     _check_ids(ids, dev, s)
     _check_rng(rng, dev)
-    if workspace is not None:
-        _same_device(grad_out, workspace=workspace)
     lib = _lib or load_library()
     if workspace is None:
         workspace = torch.empty(lib.vpce_embedding_dropout_backward_workspace_bytes(s, starts[-1], h),
-                                dtype=torch.uint8, device=ids.device)
+                                dtype=torch.uint8, device=dev)
+    elif workspace.get_device() != dev:
+        raise ValueError(f"workspace must be on cuda:{dev}")
     code = lib.vpce_embedding_dropout_backward(
-        _addr(grad_out), code_dt, _row_ld(grad_out, h, "grad_out"), _addr(ids), s,
+        _addr(grad_out), code_dt, ld_out, _addr(ids), s,
         INT64_MIN if padding_id is None else int(padding_id), scale, p, _addr(rng), ptrs, len(grad_shards), starts,
-        h, ld, int(bool(accumulate)), *_workspace(workspace), _raw_stream(ids))
+        h, ld, int(bool(accumulate)), *_workspace(workspace), _raw_stream(dev))
     if code != VPCE_OK:
         raise VPCEError(code, "vpce_embedding_dropout_backward")
     return grad_shards
