@@ -26,6 +26,8 @@
 // 0.012 ms, the gradient 0.62 ms written in full (4.2 GB of table, 6.9 TB/s) and
 // 0.11 ms accumulated.  Longer segments cost more (128 rows: 0.123 ms
 // accumulated), and so did long runs summed by whole CTAs (0.142 ms).
+#include <climits>
+
 #include "vpce_embed_dropout.cuh"
 
 namespace vpce {
@@ -138,7 +140,8 @@ __global__ void __launch_bounds__(kEdThreads) embed_dropout_forward_kernel(const
   if (r >= p.s) return;
   const long long c0 = (w - r * per) * (256 * kEfBlocks) + lane * 8;
   const long long id = __ldg(p.ids + r);
-  const bool pad = id == p.padding_id, in = id >= 0 && id < p.V, live = in && !pad;
+  // INT64_MIN as padding id means none: an id of that value is out of range
+  const bool pad = id == p.padding_id && id != LLONG_MIN, in = id >= 0 && id < p.V, live = in && !pad;
   if (!in && !pad && lane == 0 && p.flag != nullptr) atomicOr(p.flag, VPCE_FLAG_BAD_TARGET);
   const int i = live ? shard_holding(p.sh, p.t, id) : 0;
   const unsigned char* src = live ? p.sh.ptr[i] + (id - p.sh.start[i]) * p.sh.ld_bytes[i] : nullptr;
