@@ -1,5 +1,6 @@
 """Edges of the scaled embedding with dropout on the GPU: ids of the padding
-sentinel's value."""
+sentinel's value, and gradients whose rows share memory."""
+import numpy as np
 import pytest
 import torch
 
@@ -30,3 +31,36 @@ def test_an_id_of_the_sentinels_value_is_out_of_range(padding_id, bad):
     want = torch.stack([table[2], torch.zeros(8, device="cuda"),
                         torch.zeros(8, device="cuda") if padding_id == 3 else table[3], table[9]])
     assert torch.equal(out, want)
+
+
+@pytest.mark.parametrize("dtype", [torch.float32, torch.bfloat16])
+def test_the_gradient_of_a_sum_over_rows(dtype):
+    """It arrives with row stride 0 and gives what its dense copy gives, bit
+    for bit (with dropout: the mask differs from row to row)."""
+    s, h, V = 300, 40, 50
+    x = torch.zeros(s, h, dtype=dtype, device="cuda", requires_grad=True)
+    seen = []
+    x.register_hook(seen.append)
+    (x.sum(0) * torch.linspace(-1, 2, h, device="cuda").to(dtype)).sum().backward()
+    grad = seen[0]
+    assert grad.stride() == (0, 1)
+    ids = torch.from_numpy(np.random.default_rng(1).integers(0, V, s)).cuda()
+    rng = torch.tensor([3, 4], dtype=torch.int64, device="cuda")
+
+    def tables():
+        return [torch.ones(20, h, device="cuda"), torch.ones(V - 20, h, device="cuda")]
+
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    for stream in (None, side):
+        a = vpce.vpce_embedding_dropout_backward(grad, ids, tables(), p=0.3, rng=rng, stream=stream)
+        b = vpce.vpce_embedding_dropout_backward(grad.contiguous(), ids, tables(), p=0.3, rng=rng)
+        torch.cuda.synchronize()
+        assert all(torch.equal(p, q) for p, q in zip(a, b))
+        # the plain lookup's adjoint adds in any order: counts times the row
+        c = vpce.vpce_embedding_backward(grad, ids, tables(), stream=stream)
+        torch.cuda.synchronize()
+        count = torch.bincount(ids, minlength=V).double()[:, None]
+        want = 1 + count * grad[0].double()
+        got = torch.cat(c).double()
+        assert bool(((got - want).abs() <= (count + 3) * 2.0 ** -24 * (1 + count * grad[0].double().abs())).all())
