@@ -552,6 +552,7 @@ vpce_status vpce_logprob_backward(const void* const* shards, vpce_dtype dtype, i
  * never stored: vpce_embedding_dropout_backward forms it again.
  *   table_shards, dtype, t, vocab_start, h, ld_table   as
  *                 vpce_embedding_forward (V, h < 2^31).
+ *   s             rows, 0 .. 2^31, and s ceil(h / 1024) < 2^34.
  *   ids           device int64[s].  padding_id gives a zero row, whether it
  *                 lies in [0, V) or not (INT64_MIN: no padding); any other id
  *                 outside [0, V) gives a zero row and the flag.
@@ -580,6 +581,7 @@ vpce_status vpce_embedding_dropout_forward(const void* const* table_shards, vpce
  * reproducible.
  *   grad_out      device [s, h] of grad_dtype, row stride ld_grad (0 = h),
  *                 element aligned.
+ *   s             rows, 0 .. 2^31 - 4096.
  *   ids, padding_id, scale, drop_p, rng   the forward's (rng's words as the
  *                 forward read them).
  *   grad_shards   host array of t device float pointers, shard i [w_i, h], row

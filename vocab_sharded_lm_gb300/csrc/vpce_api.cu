@@ -933,7 +933,7 @@ vpce_status vpce_embedding_dropout_forward(const void* const* table_shards, vpce
   if (st != VPCE_OK) return st;
   const int eb = dtype == VPCE_BF16 ? 2 : 4, ob = out_dtype == VPCE_BF16 ? 2 : 4;
   const int64_t ldt = ld_table == 0 ? h : ld_table, ldo = ld_out == 0 ? h : ld_out;
-  if (ldt < h || ldo < h) return VPCE_ERR_INVALID_ARG;
+  if (ldt < h || ldo < h || embed_dropout_forward_blocks(s, h) >= (int64_t(1) << 31)) return VPCE_ERR_INVALID_ARG;
   if ((st = split_table(table_shards, t, vocab_start, ldt, eb, s > 0, &p.sh)) != VPCE_OK) return st;
   if (s > 0 && out == nullptr) return VPCE_ERR_INVALID_ARG;
   if (!aligned(out, size_t(ob)) || !aligned(flag_out, 4)) return VPCE_ERR_ALIGNMENT;
@@ -954,7 +954,7 @@ vpce_status vpce_embedding_dropout_forward(const void* const* table_shards, vpce
 }
 
 size_t vpce_embedding_dropout_backward_workspace_bytes(int64_t s, int64_t V, int64_t h) {
-  if (s < 0 || s > (int64_t(1) << 31) || V < 1 || V >= (int64_t(1) << 31) || h < 1 || h >= (int64_t(1) << 31))
+  if (s < 0 || s > kEmbedDropMaxRows || V < 1 || V >= (int64_t(1) << 31) || h < 1 || h >= (int64_t(1) << 31))
     return 0;
   return embed_dropout_workspace_bytes(s, V, h);
 }
@@ -971,7 +971,8 @@ vpce_status vpce_embedding_dropout_backward(const void* grad_out, vpce_dtype gra
   if (st != VPCE_OK) return st;
   const int eb = grad_dtype == VPCE_BF16 ? 2 : 4;
   const int64_t ldg = ld_grad == 0 ? h : ld_grad, ldt = ld_grad_table == 0 ? h : ld_grad_table;
-  if (ldg < h || ldt < h || (accumulate != 0 && accumulate != 1)) return VPCE_ERR_INVALID_ARG;
+  if (s > kEmbedDropMaxRows || ldg < h || ldt < h || (accumulate != 0 && accumulate != 1))
+    return VPCE_ERR_INVALID_ARG;
   // an empty batch still writes the table's zeros, so the shards are needed
   if ((st = split_table(reinterpret_cast<const void* const*>(grad_shards), t, vocab_start, ldt, 4,
                         /*need_ptrs=*/true, &p.sh)) != VPCE_OK)

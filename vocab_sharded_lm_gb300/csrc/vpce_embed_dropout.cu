@@ -626,9 +626,13 @@ __global__ void __launch_bounds__(kEdThreads, 2) embed_sum_kernel(const __grid_c
 
 }  // namespace
 
+long long embed_dropout_forward_blocks(long long s, long long h) {
+  const long long units = s * ((h + 256 * kEfBlocks - 1) / (256 * kEfBlocks));
+  return (units + kEdWarps - 1) / kEdWarps;
+}
+
 void launch_embed_dropout_forward(const EmbedDropParams& p, bool table_bf16, bool out_bf16, cudaStream_t st) {
-  const long long units = p.s * ((p.h + 256 * kEfBlocks - 1) / (256 * kEfBlocks));
-  const unsigned grid = unsigned((units + kEdWarps - 1) / kEdWarps);
+  const unsigned grid = unsigned(embed_dropout_forward_blocks(p.s, p.h));
   if (table_bf16 && out_bf16) embed_dropout_forward_kernel<__nv_bfloat16, __nv_bfloat16><<<grid, kEdThreads, 0, st>>>(p);
   else if (table_bf16) embed_dropout_forward_kernel<__nv_bfloat16, float><<<grid, kEdThreads, 0, st>>>(p);
   else if (out_bf16) embed_dropout_forward_kernel<float, __nv_bfloat16><<<grid, kEdThreads, 0, st>>>(p);

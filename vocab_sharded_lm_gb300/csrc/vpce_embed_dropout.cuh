@@ -52,6 +52,12 @@ __device__ __forceinline__ uint4 drop_block(const DropKey& key, long long r, uns
   return c;
 }
 
+// Rows of the table gradient: positions in the sorted order, with a task's or a
+// CTA's stride past the last one, are 32-bit.
+constexpr long long kEmbedDropMaxRows = (1ll << 31) - 4096;
+
+// CTAs of the lookup
+long long embed_dropout_forward_blocks(long long s, long long h);
 void launch_embed_dropout_forward(const EmbedDropParams& p, bool table_bf16, bool out_bf16, cudaStream_t st);
 size_t embed_dropout_workspace_bytes(long long s, long long V, long long h);
 cudaError_t launch_embed_dropout_backward(const EmbedDropParams& p, bool grad_bf16, void* ws, int sms,
