@@ -34,15 +34,11 @@
 // 0.374 ms with 20 alternatives; the loss's statistics alone take 0.306 ms).
 // Fewer streaming warps are better for fp32 (12: 0.376, 16: 0.404 ms), more are
 // for bf16 until their registers run out (12: 0.416, 16: 0.374, 18: 0.47 ms).
-#include <cooperative_groups.h>
-
 #include "vpce_logprob.cuh"
 
 namespace vpce {
 
 namespace {
-
-namespace cg = cooperative_groups;
 
 // Warps that stream pieces and warps that finish rows, one CTA per SM.
 template <typename T> struct LpShape;
@@ -91,7 +87,6 @@ struct __align__(16) Piece {
   unsigned bytes;             // of a row
   int col;                    // its first column
   int off;
-  int pad;
 };
 
 // A warp's room for finding a row's alternatives.
@@ -613,8 +608,8 @@ __device__ __forceinline__ void cut_row(const LogprobParams& p, Piece* piece, in
       if (lane >= o) upto += x;
     }
     for (int k = 0; k < mine; ++k)
-      piece[before + upto - mine + k] = Piece{p.sh.ptr[i],          p.sh.ld_bytes[i], unsigned(w) * unsigned(Elem<T>::kBytes),
-                                              int(p.sh.start[i]), k * p.len,        0};
+      piece[before + upto - mine + k] = Piece{p.sh.ptr[i], p.sh.ld_bytes[i],
+                                              unsigned(w) * unsigned(Elem<T>::kBytes), int(p.sh.start[i]), k * p.len};
     before += __shfl_sync(kFull, upto, 31);
   }
 }

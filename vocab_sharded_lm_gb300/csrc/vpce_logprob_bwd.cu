@@ -33,8 +33,6 @@ constexpr int kLbChunk = 32 * kLbVecs;        // vectors per chunk
 struct RowGrad {
   float m, lse2, a, b;  // largest logit; log2 S; the factor a + b v
   float gl;             // g_l / T
-  long long y;
-  bool ignored;
 };
 
 __device__ __forceinline__ float top_weight(const LogprobBwdParams& p, long long row, int lane, long long& id,
@@ -58,8 +56,6 @@ __device__ __forceinline__ float top_weight(const LogprobBwdParams& p, long long
 __device__ __forceinline__ RowGrad row_grad(const LogprobBwdParams& p, long long row, long long y, float tops) {
   const float4 st = __ldg(p.stats + row);
   RowGrad r;
-  r.y = y;
-  r.ignored = p.targets != nullptr && y == p.ignore_index;
   const float gl = p.g_logp != nullptr ? __ldg(p.g_logp + row) : 0.f;
   const float gh = p.g_entropy != nullptr ? __ldg(p.g_entropy + row) : 0.f;
   float w = gl + tops;
