@@ -14,6 +14,8 @@ import os
 import threading
 from typing import Any, NamedTuple
 
+import torch
+
 PKG = os.path.dirname(os.path.abspath(__file__))
 LIB_PATH = os.path.join(PKG, "_lib", "libvpce.so")
 
@@ -210,12 +212,12 @@ def _on_its_device(fn, own_stream=False):
 
     @functools.wraps(fn)
     def call(*args, stream=None, **kw):
-        import torch
-
         x = args[at] if len(args) > at else kw.get(name)
-        if isinstance(x, (list, tuple)) and x:
-            x = x[0]
-        dev = x.get_device() if isinstance(x, torch.Tensor) else -1  # -1: the call's own checks refuse it
+        try:
+            dev = (x[0] if type(x) is list or type(x) is tuple else x).get_device()
+        except (AttributeError, IndexError):
+            dev = -1
+        # -1: not a CUDA tensor; the call's own checks refuse it
         if stream is None:
             if dev < 0 or dev == torch._C._cuda_getDevice():
                 return fn(*args, **kw)
@@ -272,8 +274,6 @@ def _rows_of_their_own(x):
 
 
 def _describe(shards, vocab_start):
-    import torch
-
     if not shards:
         raise ValueError("need at least one shard")
     dt = shards[0].dtype
@@ -309,16 +309,12 @@ def _describe(shards, vocab_start):
 
 
 def _stream_ptr(stream):
-    import torch
-
     if stream is None:
         return ctypes.c_void_p(_raw_stream(torch._C._cuda_getDevice()))
     return ctypes.c_void_p(stream.cuda_stream)
 
 
 def new_workspace(t: int, s: int, device=None):
-    import torch
-
     n = vpce_workspace_bytes(t, s)
     if n == 0:
         raise ValueError("t or s out of range")
@@ -330,7 +326,7 @@ def _workspace(ws):
     """Address and size in bytes of a workspace, as the C entries take them."""
     if not ws.is_cuda or not ws.is_contiguous():
         raise ValueError("a workspace must be a contiguous CUDA tensor")
-    return ctypes.c_void_p(ws.data_ptr()), ws.numel() * ws.element_size()
+    return ws.data_ptr(), ws.nbytes
 
 
 def _ptr(x):
@@ -340,8 +336,6 @@ def _ptr(x):
 def _outputs(reduction, loss_out, row_loss_out, s, dev):
     """The reduction code and the loss buffers: 'none' returns the per-row
     vector (allocated if not given); the others a scalar."""
-    import torch
-
     red = REDUCTIONS[reduction]
     if red == VPCE_NONE:
         if row_loss_out is None:
@@ -354,15 +348,11 @@ def _outputs(reduction, loss_out, row_loss_out, s, dev):
 
 def _check_index(x, s, name):
     """Targets or ids: one int64 per row, read as s consecutive words."""
-    import torch
-
     if x.dtype != torch.int64 or not x.is_cuda or x.numel() != s or not x.is_contiguous():
         raise ValueError(f"{name} must be a contiguous CUDA int64 tensor with one entry per row")
 
 
 def _check_grad_rows(grad_rows, s):
-    import torch
-
     if grad_rows.dtype != torch.float32 or not grad_rows.is_cuda or grad_rows.numel() != s \
             or (s > 1 and grad_rows.stride(0) != 1):
         raise ValueError("grad_rows must be a contiguous CUDA float32 tensor with one entry per row")
@@ -374,8 +364,6 @@ def vpce_forward(shards, targets, vocab_start=None, *, ignore_index: int = -100,
     """Loss of vocab-sharded logits.  Returns ``(loss, workspace)``; pass the
     workspace unchanged to :func:`vpce_backward`.  With ``reduction='none'``
     the loss returned is the per-row vector."""
-    import torch
-
     dtype, s, vs, ld = _describe(shards, vocab_start)
     t = len(shards)
     dev = shards[0].device
@@ -446,8 +434,6 @@ def vpce_forward_backward(shards, targets, vocab_start=None, *, ignore_index: in
     way).  Returns ``(loss, workspace)`` (the per-row vector for
     ``reduction='none'``); ``shards`` now hold dlogits.  ``grad_rows`` (one
     float32 per row) replaces the scalar ``grad_output``."""
-    import torch
-
     dtype, s, vs, ld = _describe(shards, vocab_start)
     t = len(shards)
     dev = shards[0].device
@@ -553,8 +539,6 @@ def vpce_lmhead_forward(hidden, weight_shards, targets, vocab_start=None, *, ign
     and reduced tile by tile on the tensor cores.  ``hidden``: CUDA bf16
     ``[s, h]``; ``weight_shards``: CUDA bf16 ``[w_i, h]`` sharing one row
     stride.  Returns ``(loss, workspace)`` (the per-row vector for 'none')."""
-    import torch
-
     if hidden.dtype != torch.bfloat16 or hidden.dim() != 2 or not hidden.is_cuda or hidden.stride(1) != 1:
         raise ValueError("hidden must be a CUDA bf16 [s, h] tensor with contiguous columns")
     s, h = hidden.shape
@@ -596,8 +580,6 @@ def vpce_lmhead_backward(hidden, weight_shards, targets, fwd_workspace, vocab_st
     """dX (bf16, overwritten) and dW_i (fp32, accumulated) of the loss of
     the preceding :func:`vpce_lmhead_forward` (same inputs, its workspace).
     Returns ``(grad_hidden, grad_weight_shards)``."""
-    import torch
-
     s, h = hidden.shape
     _check_index(targets, s, "targets")
     if vocab_start is None:
@@ -639,8 +621,6 @@ def vpce_lmhead_backward(hidden, weight_shards, targets, fwd_workspace, vocab_st
 # vocabulary-parallel input embedding
 # ----------------------------------------------------------------------------
 def _table_desc(shards, vocab_start):
-    import torch
-
     if not shards:
         raise ValueError("need at least one shard")
     dt = shards[0].dtype
@@ -673,8 +653,6 @@ def vpce_lmhead_forward_backward(hidden, weight_shards, targets, vocab_start=Non
     formed once and kept in the workspace for its gradient.  Returns
     ``(loss, grad_hidden, grad_weight_shards)`` (the per-row vector as the
     loss for 'none'); dX is overwritten, dW accumulated."""
-    import torch
-
     if hidden.dtype != torch.bfloat16 or hidden.dim() != 2 or not hidden.is_cuda or hidden.stride(1) != 1:
         raise ValueError("hidden must be a CUDA bf16 [s, h] tensor with contiguous columns")
     s, h = hidden.shape
@@ -724,8 +702,6 @@ def vpce_embedding_forward(table_shards, ids, vocab_start=None, *, out=None, fla
     """Rows ``table[ids]`` of a vocabulary-split table (zero rows for ids
     outside [0, V)).  ``flag`` (CUDA int32 scalar) receives bit 0 if any id
     was outside."""
-    import torch
-
     dtype, h, ld, vs = _table_desc(table_shards, vocab_start)
     if dtype is None:
         raise TypeError("table dtype must be bf16 or fp32")
@@ -755,8 +731,6 @@ def vpce_embedding_backward_workspace_bytes() -> int:
 def vpce_embedding_backward(grad_out, ids, grad_shards, vocab_start=None, *, workspace=None, stream=None):
     """Accumulate the lookup's adjoint into the fp32 gradient-table shards
     (in place): each gradient row is added into its id's row."""
-    import torch
-
     gdt, h, ld, vs = _table_desc(grad_shards, vocab_start)
     if gdt != VPCE_FP32:
         raise TypeError("gradient table shards must be fp32")
@@ -803,8 +777,6 @@ def _buffer(x, shape, dtype, like, dev, name):
     """``x`` checked, or a new tensor: contiguous memory of this shape where
     ``like`` is, GPU ``dev``."""
     if x is None:
-        import torch
-
         return torch.empty(shape, dtype=dtype, device=like.device)
     if x.dtype != dtype or x.shape != shape or x.get_device() != dev or not x.is_contiguous():
         raise ValueError(f"{name} must be a contiguous {dtype} tensor of shape {shape} on cuda:{dev}")
@@ -819,8 +791,6 @@ def _column_shards(shards, vocab_start):
     """What the C entries take of a list of logits shards: dtype, rows, the
     pointers, the vocabulary offsets, the row stride (0: each is dense).  One
     look at each tensor: a decode step calls this for every token."""
-    import torch
-
     if not shards:
         raise ValueError("need at least one shard")
     first = shards[0]
@@ -860,16 +830,12 @@ def _column_shards(shards, vocab_start):
 def _raw_stream(dev):
     """Handle of the current stream of GPU ``dev`` (read as an integer:
     building a Stream object costs some microseconds)."""
-    import torch
-
     return torch._C._cuda_getCurrentRawStream(dev)
 
 
 def _check_targets(targets, s, dev):
     if targets is None:
         return
-    import torch
-
     if targets.dtype is not torch.int64 or targets.get_device() != dev or targets.numel() != s \
             or not targets.is_contiguous():
         raise ValueError(f"targets must be a contiguous int64 tensor on cuda:{dev} with one entry per row")
@@ -878,8 +844,6 @@ def _check_targets(targets, s, dev):
 def _check_flag(flag, dev):
     if flag is None:
         return
-    import torch
-
     if flag.dtype != torch.int32 or flag.get_device() != dev or flag.numel() != 1:
         raise ValueError(f"flag must be an int32 tensor of one element on cuda:{dev}")
 
@@ -895,8 +859,6 @@ def vpce_logprob_forward(shards, targets=None, vocab_start=None, *, ignore_index
     ``ignore_index`` give zeros and top ids -1; without ``targets`` every row
     is scored.  The ``*_out`` tensors are allocated where not given; ``flag``
     (CUDA int32 scalar) receives bit 0 if a target was outside [0, V)."""
-    import torch
-
     dtype, s, ptrs, starts, ld = _column_shards(shards, vocab_start)
     dev = shards[0].get_device()
     _check_targets(targets, s, dev)
@@ -932,8 +894,6 @@ def vpce_logprob_backward(shards, targets, stats, vocab_start=None, *, ignore_in
     may be left out).  ``stats`` is the forward's.  Written into
     ``grad_shards``, a list like ``shards``: None allocates it, and passing
     ``shards`` itself overwrites the logits in place.  Returns the list."""
-    import torch
-
     dtype, s, ptrs, starts, ld = _column_shards(shards, vocab_start)
     dev = shards[0].get_device()
     _check_targets(targets, s, dev)
@@ -972,25 +932,20 @@ def vpce_logprob_backward(shards, targets, stats, vocab_start=None, *, ignore_in
 def _check_rng(rng, dev):
     if rng is None:
         return
-    import torch
-
     if rng.dtype != torch.int64 or rng.get_device() != dev or rng.numel() != 2 or not rng.is_contiguous():
         raise ValueError(f"rng must be an int64 tensor of two elements (seed, offset) on cuda:{dev}")
 
 
 def _check_ids(ids, dev, s=None):
-    import torch
-
-    if ids.dtype != torch.int64 or ids.get_device() != dev or ids.dim() != 1 or not ids.is_contiguous() \
-            or (s is not None and ids.numel() != s):
+    shape = ids.shape
+    if ids.dtype is not torch.int64 or ids.get_device() != dev or len(shape) != 1 or not ids.is_contiguous() \
+            or (s is not None and shape[0] != s):
         raise ValueError(f"ids must be a contiguous 1-D int64 tensor on cuda:{dev}, one entry per row")
 
 
 def _row_shards(shards, vocab_start):
     """What the C entries take of a list of table shards [w_i, h]: dtype, h,
     the pointers, the vocabulary offsets, the row stride."""
-    import torch
-
     if not shards:
         raise ValueError("need at least one shard")
     dt = shards[0].dtype
@@ -1006,7 +961,7 @@ def _row_shards(shards, vocab_start):
             raise ValueError("table shards must be 2-D CUDA tensors [w_i, h] of one dtype and device, contiguous "
                              "columns")
         if shape[0] > 1:
-            lds.add(_row_ld(e, h, "table shards"))
+            lds.add(stride[0] or _row_ld(e, h, "table shards"))
         starts.append(starts[-1] + shape[0])
         ptrs.append(e.data_ptr())
     if len(lds) > 1:
@@ -1027,8 +982,6 @@ def vpce_embedding_dropout_forward(table_shards, ids, vocab_start=None, *, scale
     ``padding_id`` (None: none) gives zero rows; other ids outside [0, V) give
     zero rows and bit 0 of ``flag``.  The output is ``out_dtype`` (the table's
     by default)."""
-    import torch
-
     dtype, h, ptrs, starts, ld = _row_shards(table_shards, vocab_start)
     dev = table_shards[0].get_device()
     _check_ids(ids, dev)
@@ -1071,14 +1024,12 @@ def vpce_embedding_dropout_backward(grad_out, ids, grad_shards, vocab_start=None
     not occur).  ``scale``, ``p``, ``rng`` and ``padding_id`` are the
     forward's.  A ``grad_out`` expanded over its rows (autograd's gradient of
     a sum over them) is read through a dense copy."""
-    import torch
-
     gdt, h, ptrs, starts, ld = _row_shards(grad_shards, vocab_start)
     if gdt != VPCE_FP32:
         raise TypeError("gradient table shards must be fp32")
     dev = grad_shards[0].get_device()
     shape, stride = grad_out.shape, grad_out.stride()
-    if len(shape) != 2 or shape[1] != h or grad_out.get_device() != dev or (h > 1 and stride[1] != 1):
+    if len(shape) != 2 or shape[1] != h or grad_out.get_device() != dev or (stride[1] != 1 and h > 1):
         raise ValueError(f"grad_out must be an [s, h] tensor on cuda:{dev} with contiguous columns")
     code_dt = {torch.bfloat16: VPCE_BF16, torch.float32: VPCE_FP32}.get(grad_out.dtype)
     if code_dt is None:
