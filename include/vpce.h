@@ -475,7 +475,14 @@ vpce_status vpce_embedding_backward(const void* grad_out, vpce_dtype grad_dtype,
  *     top_ids[r] = the `top` columns of largest logit, largest first; equal
  *                  logits rank by column, lowest first
  *     top_logp[r][j] = ln p_r[top_ids[r][j]].
- * The logits are read once; nothing but the outputs is written.
+ * The logits are read once, and the stretches that may hold alternatives
+ * again (3 to 5% more bytes at V = 128256); nothing but the outputs is written.
+ * Two kinds of rows are read a second time by a single warp, right but slower
+ * (s = 8192, V = 128256 bf16, every row such a one, against 0.38 ms):
+ *   - rows whose largest logit is 726817 temperature (2^20 ln 2) or more from 0,
+ *     as ordinary logits are from temperatures of about 1e-5 down: 6.5 ms;
+ *   - with alternatives, rows in which over 128 columns come into question for
+ *     them (many equal logits, fewer unmasked ones than `top`): 1.0 ms.
  *   shards .. ld     as vpce_forward (read only).
  *   targets          device int64[s], or NULL when logp_out is NULL.  A target
  *                    equal to ignore_index skips its row: its logits are not
@@ -527,7 +534,8 @@ vpce_status vpce_logprob_forward(const void* const* shards, vpce_dtype dtype, in
  *                    of ignored targets get zeros.  grad_shards[i] may be
  *                    shards[i] (in place, same stride); other overlaps are not
  *                    allowed.  Padding columns are not written.
- * At least one upstream gradient is required.  Columns at -inf get 0.  A row
+ * At least one upstream gradient is required.  Columns at -inf have p = 0 and
+ * get 0 plus their onehot terms.  A row
  * without a distribution gets NaN, and so does, when grad_logp is given, a row
  * whose target is outside [0, V).
  */

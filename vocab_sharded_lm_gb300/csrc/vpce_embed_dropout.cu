@@ -21,11 +21,16 @@
 //          the rows of ids that do not occur.
 //
 // Measured at s = 8192 Zipf ids, h = 8192, V = 128256, bf16, dropout 0.1: the
-// lookup 0.057 ms (0.042 without dropout; its output and distinct rows are
-// 0.026 ms of HBM traffic: the generator's wide products bound it), the sort
-// 0.012 ms, the gradient 0.62 ms written in full (4.2 GB of table, 6.9 TB/s) and
-// 0.11 ms accumulated.  Longer segments cost more (128 rows: 0.123 ms
-// accumulated), and so did long runs summed by whole CTAs (0.142 ms).
+// lookup 0.055 ms and 0.042 without dropout, against 0.026 ms of HBM traffic
+// (output and distinct rows): the generator adds 0.013, and the other 0.016 is a
+// warp's chain of id, shard, loads and store, with nothing of another unit under
+// way in it (how it divides is not measured).  The sort 0.012 ms; the gradient
+// 0.62 ms written in full (4.2 GB of table, 6.9 TB/s) and 0.11 ms accumulated,
+// against 0.046 ms for the gradient rows and the distinct table rows read and
+// written: the SMs work 44% of the sum's time on average (h = 2048), the rest is
+// waiting for the last of them.  Longer segments cost more (128 rows: 0.123 ms
+// accumulated), and so did long runs summed by whole CTAs (0.142 ms).  Segment
+// length and the sort's 128 CTAs were chosen on Zipf ids at this h.
 #include <climits>
 
 #include "vpce_embed_dropout.cuh"

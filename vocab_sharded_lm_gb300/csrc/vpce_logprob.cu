@@ -10,7 +10,9 @@
 // own rounding costs nothing.  Logits below -2^21 / c enter at that floor,
 // where 2^v is 0: a column at -inf adds 0 and not 0 * inf.  Rows whose largest
 // logit is itself 2^20 / c or more from 0 (filled with the type's lowest value,
-// say) are summed again by subtraction (sum_far).
+// say, or any ordinary row at T near 1e-5 or below) are summed again by
+// subtraction, by one warp with single loads (sum_far: 6.5 ms instead of 0.38
+// where all 8192 rows of V = 128256 are such ones).
 //
 // A row is cut into pieces (part of one shard, 16-byte vectors).  A streaming
 // warp takes pieces from a shared counter and reads them through two 4 KB
@@ -34,6 +36,8 @@
 // 0.374 ms with 20 alternatives; the loss's statistics alone take 0.306 ms).
 // Fewer streaming warps are better for fp32 (12: 0.376, 16: 0.404 ms), more are
 // for bf16 until their registers run out (12: 0.416, 16: 0.374, 18: 0.47 ms).
+// At 16 the 96 registers a thread are already short: the compiler reports 164
+// bytes of spill stores and 276 of loads (none for fp32 at 12, 128 registers).
 #include "vpce_logprob.cuh"
 
 namespace vpce {
@@ -50,14 +54,15 @@ constexpr int kLpUnit = 32 * kLpVecs;             // vectors per unit: one buffe
 constexpr int kLpStep = 2 * kLpUnit;              // vectors per step: four batches of 4 vectors a lane
 template <typename T> constexpr int kLpRing = LpShape<T>::kStream * 2 * kLpUnit * 16;  // bytes of all buffers
 constexpr int kLpMaxPieces = 64;   // pieces per row (as many as shards can be)
-constexpr int kLpPieces = 40;      // aimed at
+constexpr int kLpPieces = 40;      // aimed at: as many as leave bf16 kLpSlots rows in kLpSmem, two for each finishing
+                                   // warp (40 (16 + 256) 8 = 87 KB next to 128 KB of buffers; fp32: 4 rows, one each)
 constexpr int kLpSlots = 8;        // rows with partials in shared memory at a time, where there is room
 constexpr int kLpMaxSlots = 192;   // and where rows are short
-constexpr int kLpSmem = 215 * 1024;     // room for the buffers and them
+constexpr int kLpSmem = 215 * 1024;     // room for the buffers and them: 227 KB less the static 11 KB
 constexpr int kLpCand = 128;       // candidate words per warp
 constexpr int kLpList = 128;       // batches listed per warp before they are re-read
 constexpr float kLpFloor = -256.f;      // 2^v is 0 here
-constexpr float kLpFar = 1048576.f;      // |K| from here on: K's rounding is no longer small (sum_far)
+constexpr float kLpFar = 1048576.f;      // |K| from here on: K's rounding, up to 2^-5 below, is no longer small (sum_far)
 
 // The maxima of a lane's four batches of a piece; bf16 ones are kept as they
 // are (a maximum is one of its values).

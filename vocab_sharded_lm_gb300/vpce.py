@@ -855,7 +855,9 @@ def vpce_logprob_forward(shards, targets=None, vocab_start=None, *, ignore_index
     """Log probability of each row's target under softmax(logits /
     temperature), the entropy, and the ``top`` most likely columns with their
     log probabilities (equal logits by column, lowest first), from
-    vocabulary-sharded logits read once.  Rows whose target is
+    vocabulary-sharded logits read once (the stretches that may hold
+    alternatives twice, and whole rows at temperatures near 0: for greedy
+    scores take ``top=1`` at temperature 1).  Rows whose target is
     ``ignore_index`` give zeros and top ids -1; without ``targets`` every row
     is scored.  The ``*_out`` tensors are allocated where not given; ``flag``
     (CUDA int32 scalar) receives bit 0 if a target was outside [0, V)."""
