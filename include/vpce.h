@@ -610,6 +610,184 @@ vpce_status vpce_embedding_dropout_backward(const void* grad_out, vpce_dtype gra
                                             vpce_stream_t stream);
 
 /*
+ * Root-mean-square norm with the residual's addition: what stands in front of
+ * the LM head (its `hidden`) and of every product of a transformer.  Per row
+ *     r = x + residual            (x alone without a residual),
+ *     rstd = 1 / sqrt(mean_c r_c^2 + eps),
+ *     out_c = r_c rstd weight_c,
+ * all in fp32 from the inputs as they are; r is rounded once where it is
+ * stored, and so is out (the norm is the unrounded r's).
+ *   x              device [s, h] of dtype, row stride ld_x elements (0 = h).
+ *   residual       device [s, h] of residual_dtype, stride ld_residual, or
+ *                  NULL.  residual_dtype: dtype, or VPCE_FP32 beside bf16 x.
+ *   weight         device [h] of weight_dtype.
+ *   eps            finite, >= 0.
+ *   s, h           rows 0 .. 2^31, columns 1 .. VPCE_MAX_NORM_COLUMNS.
+ *   residual_out   device [s, h] of residual_dtype, stride ld_residual_out: r.
+ *                  Required with a residual, NULL without one.
+ *   out            device [s, h] of dtype, stride ld_out.
+ *   rstd_out       device float[s], or NULL; for vpce_rmsnorm_backward.
+ * Every pointer needs only element alignment; rows of whole 16-byte vectors
+ * (h a multiple of 8, all addresses and strides multiples of 16 bytes) are
+ * read in vectors.  In place: residual_out may be residual, and residual_out
+ * or out may be x, where type and stride are the same; no other overlap of an
+ * output with another operand is allowed.  Columns past h are not written.
+ * The squares' sum is fp32 in a fixed order: rows whose mean square
+ * passes fp32's range (|r| about 2^64) give rstd 0, and out 0 (NaN at an
+ * infinite r); a NaN makes its row NaN.  Results are bitwise reproducible.
+ */
+#define VPCE_MAX_NORM_COLUMNS 32768
+vpce_status vpce_rmsnorm_forward(const void* x, vpce_dtype dtype, int64_t ld_x, const void* residual,
+                                 vpce_dtype residual_dtype, int64_t ld_residual, const void* weight,
+                                 vpce_dtype weight_dtype, float eps, int64_t s, int64_t h, void* residual_out,
+                                 int64_t ld_residual_out, void* out, int64_t ld_out, float* rstd_out,
+                                 vpce_stream_t stream);
+
+/*
+ * The same norm with its output in 8 bits, for products in 8 bits: per row and
+ * group of `group` consecutive columns (the last may be shorter),
+ *     scale = max_c |out_c| / 448, at least 2^-126,
+ *     q_c = out_c / scale rounded to the nearest e4m3 value,
+ * from the unrounded out, so q_c scale is within 2^-4 of out_c (or half of
+ * e4m3's smallest step, 2^-10 scale).  A NaN or infinite out makes its group's scale
+ * so; its own codes are NaN.
+ *   group          0 (one scale per row) or a multiple of 16.
+ *   q_out          device bytes [s, h], stride ld_q (0 = h): e4m3 codes.
+ *   scale_out      device float [s][ceil(h / group)] ([s] for group 0).
+ * Other arguments as vpce_rmsnorm_forward; vector rows also need q_out and
+ * ld_q to be multiples of 8.
+ */
+vpce_status vpce_rmsnorm_quantized_forward(const void* x, vpce_dtype dtype, int64_t ld_x, const void* residual,
+                                           vpce_dtype residual_dtype, int64_t ld_residual, const void* weight,
+                                           vpce_dtype weight_dtype, float eps, int64_t s, int64_t h, int64_t group,
+                                           void* residual_out, int64_t ld_residual_out, void* q_out, int64_t ld_q,
+                                           float* scale_out, float* rstd_out, vpce_stream_t stream);
+
+/*
+ * Gradient of vpce_rmsnorm_forward with respect to r (so to x and to residual
+ * alike) and to the weight.  With n = r rstd and dy = grad_out,
+ *     grad_in_c = grad_residual_c + rstd (weight_c dy_c - n_c mean_k(weight_k dy_k n_k)),
+ *     grad_weight_c (=, or += when accumulate) sum over rows dy_c n_c,
+ * in fp32, rounded once.  r is read as the forward stored it.
+ *   grad_out       device [s, h] of grad_dtype, stride ld_grad (0 = h).
+ *   x              device [s, h] of x_dtype, stride ld_x: the forward's
+ *                  residual_out, or its x where it had no residual.  x_dtype:
+ *                  grad_dtype, or VPCE_FP32 beside bf16 grad_out.
+ *   rstd           the forward's rstd_out.
+ *   grad_residual  device [s, h] of x_dtype, stride ld_grad_residual, or NULL:
+ *                  the gradient that reaches r through residual_out.
+ *   grad_in        device [s, h] of x_dtype, stride ld_grad_in.  May be
+ *                  grad_residual, x or grad_out where type and stride are the
+ *                  same (in place); other overlaps are not allowed.
+ *   grad_weight    device float[h].
+ *   workspace      vpce_rmsnorm_backward_workspace_bytes(s, h) bytes, 256-byte
+ *                  aligned, no initialisation needed.
+ * The rows' terms of grad_weight are summed in fp32 in an order that s, h, the
+ * types, alignments and the GPU's SM count fix: bitwise reproducible.  s = 0
+ * writes zeros to grad_weight (or leaves it alone when accumulate).
+ */
+size_t vpce_rmsnorm_backward_workspace_bytes(int64_t s, int64_t h);
+vpce_status vpce_rmsnorm_backward(const void* grad_out, vpce_dtype grad_dtype, int64_t ld_grad, const void* x,
+                                  vpce_dtype x_dtype, int64_t ld_x, const void* weight, vpce_dtype weight_dtype,
+                                  const float* rstd, const void* grad_residual, int64_t ld_grad_residual,
+                                  int64_t s, int64_t h, void* grad_in, int64_t ld_grad_in, float* grad_weight,
+                                  int accumulate, void* workspace, size_t workspace_bytes, vpce_stream_t stream);
+
+/*
+ * One tensor of an optimizer step: n consecutive elements of each array.
+ * Arrays need only element alignment; those on 16 bytes (32 for fp32) are
+ * moved in vectors.
+ *   param         fp32 or bf16, read and written.
+ *   grad          fp32 or bf16, read.
+ *   copy          bf16[n], written with the new param rounded, or NULL: the
+ *                 weights that the LM head reads beside fp32 masters.
+ *   exp_avg, exp_avg_sq   float[n] each; or e4m3 codes, a byte each, with
+ *   exp_avg_scale, exp_avg_sq_scale   float[ceil(n / 256)] (NULL in 32 bits).
+ *   weight_decay  of this tensor, finite.
+ * n = 0 is skipped.
+ */
+typedef struct {
+  void* param;
+  const void* grad;
+  void* copy;
+  void* exp_avg;
+  void* exp_avg_sq;
+  float* exp_avg_scale;
+  float* exp_avg_sq_scale;
+  int64_t n;
+  float weight_decay;
+} vpce_adamw_tensor;
+
+/*
+ * Norm of all gradients and the factor that clips it, left on the device:
+ *     norm = sqrt(sum of g^2 over every element of every tensor),
+ *     scale = min(1, max_norm / norm), and 0 where norm is not finite,
+ * so that vpce_adamw_step with grad_scale = scale_out clips, and skips the
+ * step of a batch with an infinity or NaN in its gradients.
+ *   tensors       host array; only grad and n are looked at.  n < 2^40.
+ *   grad_dtype    of every grad.
+ *   max_norm      > 0; infinity never clips.
+ *   norm_out, scale_out   device float, or NULL (not both).
+ *   workspace     vpce_grad_norm_workspace_bytes(n_tensors) bytes, 256-byte
+ *                 aligned, no initialisation needed.
+ * Squares are summed in fp32 (elements of about 2^64 overflow to an infinite
+ * norm, ones below 2^-63 lose their squares' last bits, below 2^-75 all) and
+ * joined in fp64, in a fixed order: bitwise reproducible.
+ */
+size_t vpce_grad_norm_workspace_bytes(int64_t n_tensors);
+vpce_status vpce_grad_norm(const vpce_adamw_tensor* tensors, int64_t n_tensors, vpce_dtype grad_dtype,
+                           float max_norm, float* norm_out, float* scale_out, void* workspace,
+                           size_t workspace_bytes, vpce_stream_t stream);
+
+/*
+ * One AdamW step (Loshchilov and Hutter, "Decoupled weight decay
+ * regularization", ICLR 2019) of many tensors, in as few launches as the
+ * kernels' parameters hold (440 tensors each).  Per element, with g = grad *
+ * grad_scale and t = *step, in fp32:
+ *     m = beta1 m + (1 - beta1) g,    v = beta2 v + (1 - beta2) g^2,
+ *     p = p (1 - lr weight_decay)
+ *         - lr / (1 - beta1^t) * m / (sqrt(v / (1 - beta2^t)) + eps).
+ * param is rounded to nearest in its own type: a bf16 param without an fp32
+ * master loses updates below 2^-9 of it.
+ *   param_dtype, grad_dtype   of every param and grad.  copy needs fp32 params.
+ *   state_bits    32: exp_avg and exp_avg_sq hold m and v.  8: they hold e4m3
+ *                 codes of m and of sqrt(v) in blocks of 256 consecutive
+ *                 elements of a tensor, value = code * scale, scale = the
+ *                 block's largest magnitude / 448, at least 2^-126; all-zero
+ *                 codes and scales are states of 0.  Codes are rounded
+ *                 stochastically, since v moves by 1 - beta2 a step and e4m3's
+ *                 steps are 6 to 12%: rounding to nearest would never move
+ *                 an element's v against its block's.  With u the element's 16
+ *                 random bits, a value x between neighbouring codes' values
+ *                 lo, hi takes hi where (u + 1/2) / 2^16 < (x - lo) / (hi -
+ *                 lo); for sqrt(v) the three are squared, which leaves v's
+ *                 expectation as it was.  A v above 0 takes at least the
+ *                 smallest code above 0, so that m never meets a v of 0.  The update
+ *                 itself uses the unrounded m and v.  u is half k % 8 (low
+ *                 halves first) of the Philox4x32-10 block of
+ *                 vpce_embedding_dropout_forward with counter = (k / 8, the
+ *                 tensor's position in `tensors`, offset's two words), k the
+ *                 element's index.  A NaN or infinity in a block's m or v
+ *                 spreads over the block's codes of it at the next step.
+ *   step          device int64[1]: t, from 1 (smaller is taken as 1); read by
+ *                 the kernel, so that a captured graph advances with it.
+ *   lr, lr_dev    the rate; lr_dev, a device float, replaces lr where not NULL.
+ *                 lr finite, >= 0 (lr_dev's value is not checked).
+ *   beta1, beta2  0 <= beta < 1.    eps finite, >= 0.
+ *   grad_scale    device float, or NULL (1).  A value of 0 skips the step:
+ *                 nothing is written.
+ *   rng           device int64[2]: seed and offset, for state_bits 8 (else
+ *                 NULL is taken too); pass another offset every step, and
+ *                 another seed than a dropout's.
+ * No two arrays of the list may overlap (two tensors may share a grad).
+ * Results are bitwise reproducible.
+ */
+vpce_status vpce_adamw_step(const vpce_adamw_tensor* tensors, int64_t n_tensors, vpce_dtype param_dtype,
+                            vpce_dtype grad_dtype, int state_bits, const int64_t* step, float lr,
+                            const float* lr_dev, double beta1, double beta2, float eps, const float* grad_scale,
+                            const int64_t* rng, vpce_stream_t stream);
+
+/*
  * Synchronise `stream`, then copy the workspace error flag to *flag (bit 0:
  * bad target seen by the last forward; bit 1: a device wait timed out, in
  * which case the forward's loss is NaN).

@@ -1,0 +1,460 @@
+// AdamW over many tensors in one launch, states in fp32 or in e4m3 with a
+// scale per 256 elements, and the norm of all gradients.
+//
+// The tensors' addresses travel in the kernels' parameters (32 KB hold 440),
+// so that a step is one launch, captured graphs carry them by value, and
+// nothing is copied to the device.  A CTA takes a run of consecutive elements
+// of one tensor, found by bisection over the runs' numbers.  Both kernels are
+// bound by HBM: 30 bytes an element move for some 16 operations with fp32
+// states, 18 bytes for some 50 with 8-bit ones.
+#include <cmath>
+
+#include <cuda_fp8.h>
+
+#include "vpce_adamw.cuh"
+#include "vpce_embed_dropout.cuh"
+
+namespace vpce {
+namespace {
+
+constexpr int kThreads = 256;
+constexpr int kPer = 8;                       // consecutive elements of a thread
+constexpr int kTile = kThreads * kPer;        // elements of a CTA's turn
+constexpr float kTiny = 1.17549435e-38f;      // 2^-126: the least scale, so that 1 / scale is finite
+
+struct AdamTensor {
+  unsigned char *p, *m, *v, *copy;
+  const unsigned char* g;
+  float *ms, *vs;
+  long long n;
+  float wd;
+  int run0;  // number of its first run
+};
+
+template <int kCap> struct AdamArgs {
+  AdamHyper hy;
+  int n, base;     // tensors here, and position of the first in the caller's list
+  int run;         // elements of a run
+  AdamTensor t[kCap];
+};
+static_assert(sizeof(AdamArgs<kAdamTensors>) <= 32764, "kernel parameters");
+
+template <int kCap> struct NormArgs {
+  int n, runs;
+  float* part;
+  const unsigned char* g[kCap];
+  long long count[kCap];
+  int run0[kCap];
+};
+static_assert(sizeof(NormArgs<kAdamTensors>) <= 32764, "kernel parameters");
+
+// Eight consecutive elements: one or two vectors where `vec`, else one by one,
+// `left` of them (the others 0).
+__device__ __forceinline__ void load8(const unsigned char* base, long long e, int left, bool vec, float (&x)[8], float) {
+  const float* p = reinterpret_cast<const float*>(base) + e;
+  if (vec && left >= 8) {
+    const float4 a = *reinterpret_cast<const float4*>(p), b = *(reinterpret_cast<const float4*>(p) + 1);
+    x[0] = a.x, x[1] = a.y, x[2] = a.z, x[3] = a.w, x[4] = b.x, x[5] = b.y, x[6] = b.z, x[7] = b.w;
+  } else {
+#pragma unroll
+    for (int j = 0; j < 8; ++j) x[j] = j < left ? p[j] : 0.f;
+  }
+}
+__device__ __forceinline__ void load8(const unsigned char* base, long long e, int left, bool vec, float (&x)[8],
+                                      __nv_bfloat16 t) {
+  const unsigned char* p = base + e * 2;
+  if (vec && left >= 8) {
+    unpack(*reinterpret_cast<const uint4*>(p), x, t);
+  } else {
+#pragma unroll
+    for (int j = 0; j < 8; ++j) x[j] = j < left ? Elem<__nv_bfloat16>::load(p + j * 2) : 0.f;
+  }
+}
+__device__ __forceinline__ void store8(unsigned char* base, long long e, int left, bool vec, const float (&x)[8], float) {
+  float* p = reinterpret_cast<float*>(base) + e;
+  if (vec && left >= 8) {
+    *reinterpret_cast<float4*>(p) = make_float4(x[0], x[1], x[2], x[3]);
+    *(reinterpret_cast<float4*>(p) + 1) = make_float4(x[4], x[5], x[6], x[7]);
+  } else {
+#pragma unroll
+    for (int j = 0; j < 8; ++j)
+      if (j < left) p[j] = x[j];
+  }
+}
+__device__ __forceinline__ void store8(unsigned char* base, long long e, int left, bool vec, const float (&x)[8],
+                                       __nv_bfloat16 t) {
+  unsigned char* p = base + e * 2;
+  if (vec && left >= 8) {
+    *reinterpret_cast<uint4*>(p) = pack(x, t);
+  } else {
+#pragma unroll
+    for (int j = 0; j < 8; ++j)
+      if (j < left) Elem<__nv_bfloat16>::store(p + j * 2, x[j]);
+  }
+}
+__device__ __forceinline__ uint2 load_codes(const unsigned char* p, int left, bool vec) {
+  if (vec && left >= 8) return *reinterpret_cast<const uint2*>(p);
+  uint2 c = make_uint2(0, 0);
+#pragma unroll
+  for (int j = 0; j < 8; ++j)
+    if (j < left) (j < 4 ? c.x : c.y) |= unsigned(p[j]) << (8 * (j & 3));
+  return c;
+}
+__device__ __forceinline__ void store_codes(unsigned char* p, int left, bool vec, uint2 c) {
+  if (vec && left >= 8) {
+    *reinterpret_cast<uint2*>(p) = c;
+  } else {
+#pragma unroll
+    for (int j = 0; j < 8; ++j)
+      if (j < left) p[j] = (unsigned char)((j < 4 ? c.x : c.y) >> (8 * (j & 3)));
+  }
+}
+
+// values of four e4m3 codes
+__device__ __forceinline__ void decode4(unsigned c, float (&x)[8], int at) {
+#pragma unroll
+  for (int i = 0; i < 2; ++i) {
+    const __half2_raw h = __nv_cvt_fp8x2_to_halfraw2((__nv_fp8x2_storage_t)((c >> (16 * i)) & 0xffff), __NV_E4M3);
+    const float2 f = __half22float2(__half2(h));
+    x[at + 2 * i] = f.x;
+    x[at + 2 * i + 1] = f.y;
+  }
+}
+
+__device__ __forceinline__ float approx_sqrt(float x) {
+  float y;
+  asm("sqrt.approx.f32 %0, %1;" : "=f"(y) : "f"(x));
+  return y;
+}
+
+__device__ __forceinline__ float block_scale(unsigned top) {
+  const float s = __fdiv_rn(__uint_as_float(top), 448.f);
+  return s < kTiny ? kTiny : s;  // a NaN stays
+}
+
+// e4m3 code of 0 <= a <= 448 (a little above is taken as 448), rounded up with
+// the random half u.  Codes count up with the values: a normal code is the top
+// bits of the fp32 word, and adding 2^-6 brings the values below e4m3's least
+// normal one into a binade whose 8 steps are e4m3's subnormal step.  The bits
+// below the code are then the fraction f of the step.  kSquares: the chance is
+// that of the squares, f (2 L + f) / (2 L + 1) with lo = L steps.
+template <bool kSquares> __device__ __forceinline__ unsigned round_code(float a, unsigned u) {
+  const bool small = a < 0.015625f;
+  const unsigned bits = __float_as_uint(small ? a + 0.015625f : a);
+  unsigned code = (bits >> 20) - (small ? 968u : 960u);
+  const float f = float(bits & 0xfffffu) * 0x1p-20f, r = float(2 * u + 1) * 0x1p-17f;
+  bool up;
+  if constexpr (kSquares) {
+    const float L = float(code < 8 ? code : 8 + (code & 7));
+    up = r * (2.f * L + 1.f) < f * (2.f * L + f);
+  } else {
+    up = r < f;
+  }
+  code += up;
+  if (!(a < 448.f)) code = a != a ? 127u : 126u;
+  return code;
+}
+
+template <int kCap> __device__ __forceinline__ int find_tensor(const AdamArgs<kCap>& a, int run) {
+  int lo = 0, hi = a.n;
+  while (hi - lo > 1) {
+    const int mid = (lo + hi) >> 1;
+    if (a.t[mid].run0 <= run) lo = mid;
+    else hi = mid;
+  }
+  return lo;
+}
+
+template <typename PT, typename GT, int kBits, int kCap>
+__global__ void __launch_bounds__(kThreads) adamw_kernel(const __grid_constant__ AdamArgs<kCap> a) {
+  const AdamHyper& hy = a.hy;
+  const float gs = hy.grad_scale != nullptr ? __ldg(hy.grad_scale) : 1.f;
+  if (gs == 0.f) return;  // the step is skipped
+  const int i = find_tensor(a, blockIdx.x);
+  const AdamTensor& t = a.t[i];
+  const float lr = hy.lr_dev != nullptr ? __ldg(hy.lr_dev) : hy.lr;
+  const long long step = __ldg(hy.step);
+  const float ft = float(step > 1 ? step : 1);
+  // 1 - beta^t without cancellation
+  const float rate = lr / -expm1f(ft * hy.ln_b1), inv2 = rsqrtf(-expm1f(ft * hy.ln_b2));
+  const float keep = 1.f - lr * t.wd;
+  unsigned char *const p = t.p, *const m = t.m, *const v = t.v, *const copy = t.copy;
+  const unsigned char* const g = t.g;
+  const long long n = t.n, e0 = (long long)(blockIdx.x - t.run0) * a.run;
+  const long long e1 = e0 + a.run < n ? e0 + a.run : n;
+  const uintptr_t where = uintptr_t(p) | uintptr_t(g) | uintptr_t(copy);
+  const bool vec = kBits == 32 ? ((where | uintptr_t(m) | uintptr_t(v)) & 15) == 0
+                               : (where & 15) == 0 && ((uintptr_t(m) | uintptr_t(v)) & 7) == 0;
+  DropKey key;
+  if constexpr (kBits == 8) key.set(hy.rng);
+  // (8-bit states: a warp's 32 threads hold one block of 256 elements)
+  for (long long e = e0 + (long long)threadIdx.x * kPer; e - (threadIdx.x & 31) * kPer < e1; e += kTile) {
+    const int left = e1 > e ? int(e1 - e < kPer ? e1 - e : kPer) : 0;
+    float xp[8], xg[8], xm[8], xv[8];
+    load8(p, e, left, vec, xp, PT());
+    load8(g, e, left, vec, xg, GT());
+    if constexpr (kBits == 32) {
+      load8(m, e, left, vec, xm, 0.f);
+      load8(v, e, left, vec, xv, 0.f);
+    } else {
+      const uint2 cm = load_codes(m + e, left, vec), cv = load_codes(v + e, left, vec);
+      const float sm = t.ms[e / kAdamBlock], sv = t.vs[e / kAdamBlock];
+      decode4(cm.x, xm, 0);
+      decode4(cm.y, xm, 4);
+      decode4(cv.x, xv, 0);
+      decode4(cv.y, xv, 4);
+#pragma unroll
+      for (int j = 0; j < 8; ++j) {
+        xm[j] *= sm;
+        xv[j] *= sv;
+        xv[j] *= xv[j];
+      }
+    }
+#pragma unroll
+    for (int j = 0; j < 8; ++j) {
+      const float gj = xg[j] * gs;
+      xm[j] = fmaf(hy.b1, xm[j], hy.a1 * gj);
+      xv[j] = fmaf(hy.b2, xv[j], hy.a2 * gj * gj);
+      const float root = approx_sqrt(xv[j]);
+      xp[j] = fmaf(-rate, __fdividef(xm[j], fmaf(root, inv2, hy.eps)), xp[j] * keep);
+      if constexpr (kBits == 8) xv[j] = root;
+    }
+    store8(p, e, left, vec, xp, PT());
+    if (copy != nullptr) store8(copy, e, left, vec, xp, __nv_bfloat16());
+    if constexpr (kBits == 32) {
+      store8(m, e, left, vec, xm, 0.f);
+      store8(v, e, left, vec, xv, 0.f);
+    } else {
+      unsigned tm = 0, tv = 0;
+#pragma unroll
+      for (int j = 0; j < 8; ++j) {
+        tm = max(tm, __float_as_uint(xm[j]) & 0x7fffffffu);
+        tv = max(tv, __float_as_uint(xv[j]) & 0x7fffffffu);
+      }
+      const float sm = block_scale(__reduce_max_sync(kFull, tm)), sv = block_scale(__reduce_max_sync(kFull, tv));
+      const float im = __fdiv_rn(1.f, sm), iv = __fdiv_rn(1.f, sv);
+      const long long k8 = e >> 3;
+      const uint4 u = drop_block(key, a.base + i, unsigned(k8));
+      const unsigned word[4] = {u.x, u.y, u.z, u.w};
+      uint2 cm = make_uint2(0, 0), cv = make_uint2(0, 0);
+#pragma unroll
+      for (int j = 0; j < 8; ++j) {
+        const unsigned h = (word[j >> 1] >> (16 * (j & 1))) & 0xffffu;
+        const unsigned sign = (__float_as_uint(xm[j]) >> 24) & 0x80u;
+        const unsigned a8 = round_code<false>(fabsf(xm[j]) * im, h) | sign;
+        unsigned b8 = round_code<true>(xv[j] * iv, h);
+        if (xv[j] > 0.f && b8 == 0) b8 = 1;
+        (j < 4 ? cm.x : cm.y) |= a8 << (8 * (j & 3));
+        (j < 4 ? cv.x : cv.y) |= b8 << (8 * (j & 3));
+      }
+      store_codes(m + e, left, vec, cm);
+      store_codes(v + e, left, vec, cv);
+      if ((threadIdx.x & 31) == 0) {
+        t.ms[e / kAdamBlock] = sm;
+        t.vs[e / kAdamBlock] = sv;
+      }
+    }
+  }
+}
+
+// ---------------------------------------------------------------------------
+// norm of all gradients
+// ---------------------------------------------------------------------------
+// sum over a CTA of kNormThreads threads, in a fixed order; thread 0 has it
+__device__ __forceinline__ float cta_sum(float v, float* sm) {
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) v += __shfl_xor_sync(kFull, v, o);
+  if ((threadIdx.x & 31) == 0) sm[threadIdx.x >> 5] = v;
+  __syncthreads();
+  if (threadIdx.x < 32) {
+    v = threadIdx.x < kNormThreads / 32 ? sm[threadIdx.x] : 0.f;
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) v += __shfl_xor_sync(kFull, v, o);
+  }
+  return v;
+}
+
+constexpr int kNormRun = kNormThreads * kPer * 4;  // elements of a CTA's turn
+
+// Squares of the runs blockIdx.x, blockIdx.x + gridDim.x, ...: eight sums a
+// thread, joined by a tree.
+template <typename GT, int kCap>
+__global__ void __launch_bounds__(kNormThreads) grad_norm_kernel(const __grid_constant__ NormArgs<kCap> a) {
+  __shared__ float sm[kNormThreads / 32];
+  float s[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
+  for (int run = blockIdx.x; run < a.runs; run += gridDim.x) {
+    int lo = 0, hi = a.n;
+    while (hi - lo > 1) {
+      const int mid = (lo + hi) >> 1;
+      if (a.run0[mid] <= run) lo = mid;
+      else hi = mid;
+    }
+    const unsigned char* g = a.g[lo];
+    const long long e0 = (long long)(run - a.run0[lo]) * kNormRun, n = a.count[lo];
+    const bool vec = (uintptr_t(g) & 15) == 0;
+    if (vec && e0 + kNormRun <= n) {
+      float x[4][8];
+#pragma unroll
+      for (int k = 0; k < 4; ++k) load8(g, e0 + (k * kNormThreads + threadIdx.x) * kPer, 8, true, x[k], GT());
+#pragma unroll
+      for (int k = 0; k < 4; ++k)
+#pragma unroll
+        for (int j = 0; j < 8; ++j) s[j] = fmaf(x[k][j], x[k][j], s[j]);
+    } else {
+#pragma unroll 1
+      for (int k = 0; k < 4; ++k) {
+        const long long e = e0 + (k * kNormThreads + threadIdx.x) * kPer;
+        const int left = n > e ? int(n - e < kPer ? n - e : kPer) : 0;
+        float x[8];
+        load8(g, e, left, vec, x, GT());
+#pragma unroll
+        for (int j = 0; j < 8; ++j) s[j] = fmaf(x[j], x[j], s[j]);
+      }
+    }
+  }
+  grid_launch_dependents();
+  const float v = ((s[0] + s[1]) + (s[2] + s[3])) + ((s[4] + s[5]) + (s[6] + s[7]));
+  const float total = cta_sum(v, sm);
+  if (threadIdx.x == 0) a.part[blockIdx.x] = total;
+}
+
+// The CTAs' sums in fp64, in a fixed order: thread i takes every 256th.
+__global__ void __launch_bounds__(256) grad_norm_finish(const float* part, int parts, float max_norm, float* norm_out,
+                                                        float* scale_out) {
+  __shared__ double sm[256];
+  grid_dependency_wait();
+  double v = 0.0;
+  for (int i = threadIdx.x; i < parts; i += 256) v += double(__ldcg(part + i));
+  sm[threadIdx.x] = v;
+  __syncthreads();
+  for (int o = 128; o > 0; o >>= 1) {
+    if (threadIdx.x < o) sm[threadIdx.x] += sm[threadIdx.x + o];
+    __syncthreads();
+  }
+  if (threadIdx.x == 0) {
+    const float norm = float(sqrt(sm[0]));
+    if (norm_out != nullptr) *norm_out = norm;
+    if (scale_out != nullptr) {
+      const float scale = norm > max_norm ? float(double(max_norm) / sqrt(sm[0])) : 1.f;
+      *scale_out = isfinite(norm) ? scale : 0.f;
+    }
+  }
+}
+
+template <typename PT, typename GT, int kBits, int kCap>
+void step_launch(const vpce_adamw_tensor* tensors, long long first, long long count, const AdamHyper& hy, int sms,
+                 cudaStream_t st) {
+  AdamArgs<kCap> a;
+  a.hy = hy;
+  a.base = int(first);
+  a.n = 0;
+  long long total = 0;
+  for (long long i = 0; i < count; ++i) total += tensors[first + i].n;
+  // a run: long enough to spread a CTA's start over several turns, short
+  // enough that every SM has some
+  long long turns = total / ((long long)kTile * sms * 8);
+  turns = turns < 1 ? 1 : turns > 8 ? 8 : turns;
+  a.run = int(turns) * kTile;
+  long long runs = 0;
+  for (long long i = 0; i < count; ++i) {
+    const vpce_adamw_tensor& t = tensors[first + i];
+    AdamTensor& d = a.t[a.n++];
+    d.p = static_cast<unsigned char*>(t.param);
+    d.g = static_cast<const unsigned char*>(t.grad);
+    d.copy = static_cast<unsigned char*>(t.copy);
+    d.m = static_cast<unsigned char*>(t.exp_avg);
+    d.v = static_cast<unsigned char*>(t.exp_avg_sq);
+    d.ms = t.exp_avg_scale;
+    d.vs = t.exp_avg_sq_scale;
+    d.n = t.n;
+    d.wd = t.weight_decay;
+    d.run0 = int(runs);
+    runs += (t.n + a.run - 1) / a.run;
+  }
+  if (runs > 0) adamw_kernel<PT, GT, kBits, kCap><<<int(runs), kThreads, 0, st>>>(a);
+}
+
+template <typename PT, typename GT, int kBits>
+void step_all(const vpce_adamw_tensor* tensors, long long n, const AdamHyper& hy, int sms, cudaStream_t st) {
+  for (long long i = 0; i < n; i += kAdamTensors) {
+    const long long count = n - i < kAdamTensors ? n - i : kAdamTensors;
+    if (count <= kAdamFewTensors) step_launch<PT, GT, kBits, kAdamFewTensors>(tensors, i, count, hy, sms, st);
+    else step_launch<PT, GT, kBits, kAdamTensors>(tensors, i, count, hy, sms, st);
+  }
+}
+
+template <typename PT, typename GT>
+void step_bits(const vpce_adamw_tensor* tensors, long long n, int bits, const AdamHyper& hy, int sms, cudaStream_t st) {
+  if (bits == 32) step_all<PT, GT, 32>(tensors, n, hy, sms, st);
+  else step_all<PT, GT, 8>(tensors, n, hy, sms, st);
+}
+
+template <typename GT, int kCap>
+int norm_launch(const vpce_adamw_tensor* tensors, long long count, float* part, int sms, cudaStream_t st) {
+  NormArgs<kCap> a;
+  a.n = int(count);
+  a.part = part;
+  long long runs = 0;
+  for (long long i = 0; i < count; ++i) {
+    a.g[i] = static_cast<const unsigned char*>(tensors[i].grad);
+    a.count[i] = tensors[i].n;
+    a.run0[i] = int(runs);
+    runs += (tensors[i].n + kNormRun - 1) / kNormRun;
+  }
+  if (runs == 0) return 0;
+  a.runs = int(runs);
+  const int most = sms * 4 < kNormMaxCtas ? sms * 4 : kNormMaxCtas;
+  const int grid = int(runs < most ? runs : most);
+  grad_norm_kernel<GT, kCap><<<grid, kNormThreads, 0, st>>>(a);
+  return grid;
+}
+
+template <typename GT>
+int norm_all(const vpce_adamw_tensor* tensors, long long n, float* part, int sms, cudaStream_t st) {
+  int parts = 0;
+  for (long long i = 0; i < n; i += kAdamTensors) {
+    const long long count = n - i < kAdamTensors ? n - i : kAdamTensors;
+    parts += count <= kAdamFewTensors ? norm_launch<GT, kAdamFewTensors>(tensors + i, count, part + parts, sms, st)
+                                      : norm_launch<GT, kAdamTensors>(tensors + i, count, part + parts, sms, st);
+  }
+  return parts;
+}
+
+}  // namespace
+
+void launch_adamw(const vpce_adamw_tensor* tensors, long long n, bool param_bf16, bool grad_bf16, int bits,
+                  const AdamHyper& hy, int sms, cudaStream_t st) {
+  if (param_bf16) {
+    if (grad_bf16) step_bits<__nv_bfloat16, __nv_bfloat16>(tensors, n, bits, hy, sms, st);
+    else step_bits<__nv_bfloat16, float>(tensors, n, bits, hy, sms, st);
+  } else {
+    if (grad_bf16) step_bits<float, __nv_bfloat16>(tensors, n, bits, hy, sms, st);
+    else step_bits<float, float>(tensors, n, bits, hy, sms, st);
+  }
+}
+
+size_t grad_norm_workspace_bytes(long long n) {
+  return round256(size_t((n + kAdamTensors - 1) / kAdamTensors) * kNormMaxCtas * sizeof(float) + 256);
+}
+
+cudaError_t launch_grad_norm(const vpce_adamw_tensor* tensors, long long n, bool grad_bf16, float max_norm,
+                             float* norm_out, float* scale_out, void* ws, int sms, cudaStream_t st) {
+  float* part = static_cast<float*>(ws);
+  const int parts = grad_bf16 ? norm_all<__nv_bfloat16>(tensors, n, part, sms, st) : norm_all<float>(tensors, n, part, sms, st);
+  cudaError_t e = cudaGetLastError();
+  if (e != cudaSuccess) return e;
+  // a programmatic dependent: its launch is hidden behind the last runs
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(1);
+  cfg.blockDim = dim3(256);
+  cfg.stream = st;
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = parts > 0 ? 1 : 0;
+  e = cudaLaunchKernelEx(&cfg, grad_norm_finish, (const float*)part, parts, max_norm, norm_out, scale_out);
+  return e == cudaSuccess ? cudaGetLastError() : e;
+}
+
+}  // namespace vpce

@@ -5,9 +5,11 @@
 #include <cstring>
 #include <mutex>
 
+#include "vpce_adamw.cuh"
 #include "vpce_embed_dropout.cuh"
 #include "vpce_kernels.cuh"
 #include "vpce_logprob.cuh"
+#include "vpce_rmsnorm.cuh"
 
 namespace vpce {
 cudaError_t set_backward_smem();
@@ -992,6 +994,219 @@ vpce_status vpce_embedding_dropout_backward(const void* grad_out, vpce_dtype gra
   const cudaError_t e = launch_embed_dropout_backward(p, grad_dtype == VPCE_BF16, workspace, sms,
                                                       reinterpret_cast<cudaStream_t>(stream));
   return e == cudaSuccess ? VPCE_OK : VPCE_ERR_CUDA;
+}
+
+static bool good_dtype(vpce_dtype d) { return d == VPCE_FP32 || d == VPCE_BF16; }
+static int64_t dtype_bytes(vpce_dtype d) { return d == VPCE_BF16 ? 2 : 4; }
+
+// One [s, h] operand of the norm: its row stride in bytes (ld = 0: dense) and
+// whether its rows can be read in vectors.
+static vpce_status norm_rows(const void* p, int64_t ld, int64_t s, int64_t h, int64_t eb, int64_t vec_bytes,
+                             bool need, long long* ld_bytes, bool* vectors) {
+  const int64_t stride = ld == 0 ? h : ld;
+  if (stride < h || stride >= (int64_t(1) << 48) || (need && s > 0 && p == nullptr)) return VPCE_ERR_INVALID_ARG;
+  if (!aligned(p, size_t(eb))) return VPCE_ERR_ALIGNMENT;
+  *ld_bytes = stride * eb;
+  if (p != nullptr && (!aligned(p, size_t(vec_bytes)) || (s > 1 && *ld_bytes % vec_bytes != 0))) *vectors = false;
+  return VPCE_OK;
+}
+
+// What both outputs of the norm share.
+static vpce_status rmsnorm_impl(const void* x, vpce_dtype dtype, int64_t ld_x, const void* residual,
+                                vpce_dtype residual_dtype, int64_t ld_residual, const void* weight,
+                                vpce_dtype weight_dtype, float eps, int64_t s, int64_t h, int64_t group,
+                                void* residual_out, int64_t ld_residual_out, void* out, int64_t ld_out,
+                                float* scale_out, bool codes, float* rstd_out, vpce_stream_t stream) {
+  if (!good_dtype(dtype) || !good_dtype(weight_dtype) || !good_dtype(residual_dtype)) return VPCE_ERR_DTYPE;
+  if (residual == nullptr) residual_dtype = dtype;
+  if (dtype == VPCE_FP32 && residual_dtype == VPCE_BF16) return VPCE_ERR_DTYPE;
+  if (s < 0 || s > (int64_t(1) << 31) || h < 1 || h > VPCE_MAX_NORM_COLUMNS || !std::isfinite(eps) || eps < 0.f)
+    return VPCE_ERR_INVALID_ARG;
+  if (group < 0 || group % 16 != 0) return VPCE_ERR_INVALID_ARG;
+  if (weight == nullptr || (residual == nullptr && residual_out != nullptr && s > 0)) return VPCE_ERR_INVALID_ARG;
+  if (codes && s > 0 && scale_out == nullptr) return VPCE_ERR_INVALID_ARG;
+  const int64_t eb = dtype_bytes(dtype), rb = dtype_bytes(residual_dtype), wb = dtype_bytes(weight_dtype);
+  RmsNormParams p;
+  std::memset(&p, 0, sizeof(p));
+  bool vectors = h % 8 == 0 && aligned(weight, 16);
+  vpce_status st;
+  if ((st = norm_rows(x, ld_x, s, h, eb, 16, true, &p.ld_x, &vectors)) != VPCE_OK ||
+      (st = norm_rows(residual, ld_residual, s, h, rb, 16, false, &p.ld_res, &vectors)) != VPCE_OK ||
+      (st = norm_rows(residual_out, ld_residual_out, s, h, rb, 16, residual != nullptr, &p.ld_res_out, &vectors)) !=
+          VPCE_OK ||
+      (st = norm_rows(out, ld_out, s, h, codes ? 1 : eb, codes ? 8 : 16, true, &p.ld_out, &vectors)) != VPCE_OK)
+    return st;
+  if (!aligned(weight, size_t(wb)) || !aligned(scale_out, 4) || !aligned(rstd_out, 4)) return VPCE_ERR_ALIGNMENT;
+  int sms = 0;
+  if ((st = device_setup(&sms)) != VPCE_OK) return st;
+  if (s == 0) return VPCE_OK;
+  p.x = static_cast<const unsigned char*>(x);
+  p.res = static_cast<const unsigned char*>(residual);
+  p.w = static_cast<const unsigned char*>(weight);
+  p.w_bf16 = weight_dtype == VPCE_BF16;
+  p.eps = eps;
+  p.s = s;
+  p.h = int(h);
+  p.res_out = static_cast<unsigned char*>(residual_out);
+  p.out = static_cast<unsigned char*>(out);
+  p.scale = scale_out;
+  p.group = int(group == 0 || group > h ? h : group);
+  p.groups = int((h + p.group - 1) / p.group);
+  p.rstd = rstd_out;
+  launch_rmsnorm_forward(p, dtype == VPCE_BF16, residual_dtype == VPCE_BF16, codes, vectors, sms,
+                         reinterpret_cast<cudaStream_t>(stream));
+  return launch_status();
+}
+
+vpce_status vpce_rmsnorm_forward(const void* x, vpce_dtype dtype, int64_t ld_x, const void* residual,
+                                 vpce_dtype residual_dtype, int64_t ld_residual, const void* weight,
+                                 vpce_dtype weight_dtype, float eps, int64_t s, int64_t h, void* residual_out,
+                                 int64_t ld_residual_out, void* out, int64_t ld_out, float* rstd_out,
+                                 vpce_stream_t stream) {
+  return rmsnorm_impl(x, dtype, ld_x, residual, residual_dtype, ld_residual, weight, weight_dtype, eps, s, h, 0,
+                      residual_out, ld_residual_out, out, ld_out, nullptr, false, rstd_out, stream);
+}
+
+vpce_status vpce_rmsnorm_quantized_forward(const void* x, vpce_dtype dtype, int64_t ld_x, const void* residual,
+                                           vpce_dtype residual_dtype, int64_t ld_residual, const void* weight,
+                                           vpce_dtype weight_dtype, float eps, int64_t s, int64_t h, int64_t group,
+                                           void* residual_out, int64_t ld_residual_out, void* q_out, int64_t ld_q,
+                                           float* scale_out, float* rstd_out, vpce_stream_t stream) {
+  return rmsnorm_impl(x, dtype, ld_x, residual, residual_dtype, ld_residual, weight, weight_dtype, eps, s, h, group,
+                      residual_out, ld_residual_out, q_out, ld_q, scale_out, true, rstd_out, stream);
+}
+
+size_t vpce_rmsnorm_backward_workspace_bytes(int64_t s, int64_t h) {
+  if (s < 0 || s > (int64_t(1) << 31) || h < 1 || h > VPCE_MAX_NORM_COLUMNS) return 0;
+  return rmsnorm_backward_workspace_bytes(s, h);
+}
+
+vpce_status vpce_rmsnorm_backward(const void* grad_out, vpce_dtype grad_dtype, int64_t ld_grad, const void* x,
+                                  vpce_dtype x_dtype, int64_t ld_x, const void* weight, vpce_dtype weight_dtype,
+                                  const float* rstd, const void* grad_residual, int64_t ld_grad_residual,
+                                  int64_t s, int64_t h, void* grad_in, int64_t ld_grad_in, float* grad_weight,
+                                  int accumulate, void* workspace, size_t workspace_bytes, vpce_stream_t stream) {
+  if (!good_dtype(grad_dtype) || !good_dtype(x_dtype) || !good_dtype(weight_dtype)) return VPCE_ERR_DTYPE;
+  if (grad_dtype == VPCE_FP32 && x_dtype == VPCE_BF16) return VPCE_ERR_DTYPE;
+  if (s < 0 || s > (int64_t(1) << 31) || h < 1 || h > VPCE_MAX_NORM_COLUMNS || (accumulate != 0 && accumulate != 1))
+    return VPCE_ERR_INVALID_ARG;
+  if (weight == nullptr || grad_weight == nullptr || (s > 0 && rstd == nullptr) || workspace == nullptr)
+    return VPCE_ERR_INVALID_ARG;
+  const int64_t gb = dtype_bytes(grad_dtype), xb = dtype_bytes(x_dtype);
+  RmsNormBwdParams p;
+  std::memset(&p, 0, sizeof(p));
+  bool vectors = h % 8 == 0 && aligned(weight, 16);
+  vpce_status st;
+  if ((st = norm_rows(grad_out, ld_grad, s, h, gb, 16, true, &p.ld_dy, &vectors)) != VPCE_OK ||
+      (st = norm_rows(x, ld_x, s, h, xb, 16, true, &p.ld_x, &vectors)) != VPCE_OK ||
+      (st = norm_rows(grad_residual, ld_grad_residual, s, h, xb, 16, false, &p.ld_dres, &vectors)) != VPCE_OK ||
+      (st = norm_rows(grad_in, ld_grad_in, s, h, xb, 16, true, &p.ld_dx, &vectors)) != VPCE_OK)
+    return st;
+  if (!aligned(weight, size_t(dtype_bytes(weight_dtype))) || !aligned(rstd, 4) || !aligned(grad_weight, 4) ||
+      !aligned(workspace, 256))
+    return VPCE_ERR_ALIGNMENT;
+  if (workspace_bytes < rmsnorm_backward_workspace_bytes(s, h)) return VPCE_ERR_WORKSPACE;
+  int sms = 0;
+  if ((st = device_setup(&sms)) != VPCE_OK) return st;
+  if (s == 0 && accumulate) return VPCE_OK;
+  p.dy = static_cast<const unsigned char*>(grad_out);
+  p.x = static_cast<const unsigned char*>(x);
+  p.w = static_cast<const unsigned char*>(weight);
+  p.w_bf16 = weight_dtype == VPCE_BF16;
+  p.rstd = rstd;
+  p.dres = static_cast<const unsigned char*>(grad_residual);
+  p.s = s;
+  p.h = int(h);
+  p.dx = static_cast<unsigned char*>(grad_in);
+  p.part = static_cast<float*>(workspace);
+  p.dw = grad_weight;
+  p.accumulate = accumulate;
+  const cudaError_t e = launch_rmsnorm_backward(p, grad_dtype == VPCE_BF16, x_dtype == VPCE_BF16, vectors, sms,
+                                                reinterpret_cast<cudaStream_t>(stream));
+  return e == cudaSuccess ? VPCE_OK : VPCE_ERR_CUDA;
+}
+
+// Elements of one tensor (8-bit states count groups of 8 in 32 bits) and of a list.
+static constexpr int64_t kMaxTensorElements = int64_t(1) << 35, kMaxListElements = int64_t(1) << 40;
+
+// The lists' common rule: sizes, and the gradients that both calls read.
+static vpce_status check_tensors(const vpce_adamw_tensor* tensors, int64_t n, vpce_dtype grad_dtype) {
+  if (n < 0 || n > (int64_t(1) << 31) - 1 || (n > 0 && tensors == nullptr)) return VPCE_ERR_INVALID_ARG;
+  int64_t total = 0;
+  for (int64_t i = 0; i < n; ++i) {
+    const vpce_adamw_tensor& t = tensors[i];
+    if (t.n < 0 || t.n >= kMaxTensorElements || (total += t.n) > kMaxListElements) return VPCE_ERR_INVALID_ARG;
+    if (t.n > 0 && t.grad == nullptr) return VPCE_ERR_INVALID_ARG;
+    if (!aligned(t.grad, size_t(dtype_bytes(grad_dtype)))) return VPCE_ERR_ALIGNMENT;
+  }
+  return VPCE_OK;
+}
+
+size_t vpce_grad_norm_workspace_bytes(int64_t n_tensors) {
+  if (n_tensors < 0 || n_tensors > (int64_t(1) << 31) - 1) return 0;
+  return grad_norm_workspace_bytes(n_tensors);
+}
+
+vpce_status vpce_grad_norm(const vpce_adamw_tensor* tensors, int64_t n_tensors, vpce_dtype grad_dtype,
+                           float max_norm, float* norm_out, float* scale_out, void* workspace,
+                           size_t workspace_bytes, vpce_stream_t stream) {
+  if (!good_dtype(grad_dtype)) return VPCE_ERR_DTYPE;
+  vpce_status st = check_tensors(tensors, n_tensors, grad_dtype);
+  if (st != VPCE_OK) return st;
+  if (!(max_norm > 0.f) || (norm_out == nullptr && scale_out == nullptr) || workspace == nullptr)
+    return VPCE_ERR_INVALID_ARG;
+  if (!aligned(norm_out, 4) || !aligned(scale_out, 4) || !aligned(workspace, 256)) return VPCE_ERR_ALIGNMENT;
+  if (workspace_bytes < grad_norm_workspace_bytes(n_tensors)) return VPCE_ERR_WORKSPACE;
+  int sms = 0;
+  if ((st = device_setup(&sms)) != VPCE_OK) return st;
+  const cudaError_t e = launch_grad_norm(tensors, n_tensors, grad_dtype == VPCE_BF16, max_norm, norm_out, scale_out,
+                                         workspace, sms, reinterpret_cast<cudaStream_t>(stream));
+  return e == cudaSuccess ? VPCE_OK : VPCE_ERR_CUDA;
+}
+
+vpce_status vpce_adamw_step(const vpce_adamw_tensor* tensors, int64_t n_tensors, vpce_dtype param_dtype,
+                            vpce_dtype grad_dtype, int state_bits, const int64_t* step, float lr,
+                            const float* lr_dev, double beta1, double beta2, float eps, const float* grad_scale,
+                            const int64_t* rng, vpce_stream_t stream) {
+  if (!good_dtype(param_dtype) || !good_dtype(grad_dtype)) return VPCE_ERR_DTYPE;
+  if (state_bits != 32 && state_bits != 8) return VPCE_ERR_INVALID_ARG;
+  vpce_status st = check_tensors(tensors, n_tensors, grad_dtype);
+  if (st != VPCE_OK) return st;
+  if (step == nullptr || (state_bits == 8 && rng == nullptr)) return VPCE_ERR_INVALID_ARG;
+  if (!std::isfinite(lr) || lr < 0.f || !std::isfinite(eps) || eps < 0.f || !(beta1 >= 0.0 && beta1 < 1.0) ||
+      !(beta2 >= 0.0 && beta2 < 1.0))
+    return VPCE_ERR_INVALID_ARG;
+  if (!aligned(step, 8) || !aligned(lr_dev, 4) || !aligned(grad_scale, 4) || !aligned(rng, 8))
+    return VPCE_ERR_ALIGNMENT;
+  const size_t pb = size_t(dtype_bytes(param_dtype)), mb = state_bits == 8 ? 1 : 4;
+  for (int64_t i = 0; i < n_tensors; ++i) {
+    const vpce_adamw_tensor& t = tensors[i];
+    if (!std::isfinite(t.weight_decay) || (t.copy != nullptr && param_dtype != VPCE_FP32)) return VPCE_ERR_INVALID_ARG;
+    if (t.n > 0 && (t.param == nullptr || t.exp_avg == nullptr || t.exp_avg_sq == nullptr)) return VPCE_ERR_INVALID_ARG;
+    if (t.n > 0 && (state_bits == 8) != (t.exp_avg_scale != nullptr && t.exp_avg_sq_scale != nullptr))
+      return VPCE_ERR_INVALID_ARG;
+    if (!aligned(t.param, pb) || !aligned(t.copy, 2) || !aligned(t.exp_avg, mb) || !aligned(t.exp_avg_sq, mb) ||
+        !aligned(t.exp_avg_scale, 4) || !aligned(t.exp_avg_sq_scale, 4))
+      return VPCE_ERR_ALIGNMENT;
+  }
+  int sms = 0;
+  if ((st = device_setup(&sms)) != VPCE_OK) return st;
+  AdamHyper hy;
+  hy.step = reinterpret_cast<const long long*>(step);
+  hy.lr_dev = lr_dev;
+  hy.grad_scale = grad_scale;
+  hy.rng = reinterpret_cast<const unsigned long long*>(rng);
+  hy.lr = lr;
+  hy.eps = eps;
+  hy.b1 = float(beta1);
+  hy.a1 = float(1.0 - beta1);
+  hy.b2 = float(beta2);
+  hy.a2 = float(1.0 - beta2);
+  hy.ln_b1 = float(std::log(beta1));
+  hy.ln_b2 = float(std::log(beta2));
+  launch_adamw(tensors, n_tensors, param_dtype == VPCE_BF16, grad_dtype == VPCE_BF16, state_bits, hy, sms,
+               reinterpret_cast<cudaStream_t>(stream));
+  return launch_status();
 }
 
 const char* vpce_status_string(vpce_status status) {

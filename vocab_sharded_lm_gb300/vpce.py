@@ -38,6 +38,8 @@ VPCE_FLAG_WAIT_TIMEOUT = 2
 VPCE_STATIC_SCRATCH_BYTES = 8 * 1024 * 1024
 VPCE_LMHEAD_MAX_GROUPS = 256
 VPCE_MAX_TOP = 32
+VPCE_MAX_NORM_COLUMNS = 32768
+ADAMW_BLOCK = 256  # elements that share a scale of 8-bit states
 INT64_MIN = -(1 << 63)
 
 _lib = None
@@ -136,6 +138,26 @@ def load_library(path: str | None = None) -> ctypes.CDLL:
         lib.vpce_embedding_dropout_backward.argtypes = [_P, ctypes.c_int, _I64, _P, _I64, _I64, ctypes.c_float,
                                                         ctypes.c_float, _P, _P, ctypes.c_int, _P, _I64, _I64,
                                                         ctypes.c_int, _P, ctypes.c_size_t, _P]
+        _F = ctypes.c_float
+        _E = ctypes.c_int
+        lib.vpce_rmsnorm_forward.restype = ctypes.c_int
+        lib.vpce_rmsnorm_forward.argtypes = [_P, _E, _I64, _P, _E, _I64, _P, _E, _F, _I64, _I64, _P, _I64, _P, _I64,
+                                             _P, _P]
+        lib.vpce_rmsnorm_quantized_forward.restype = ctypes.c_int
+        lib.vpce_rmsnorm_quantized_forward.argtypes = [_P, _E, _I64, _P, _E, _I64, _P, _E, _F, _I64, _I64, _I64, _P,
+                                                       _I64, _P, _I64, _P, _P, _P]
+        lib.vpce_rmsnorm_backward_workspace_bytes.restype = ctypes.c_size_t
+        lib.vpce_rmsnorm_backward_workspace_bytes.argtypes = [_I64, _I64]
+        lib.vpce_rmsnorm_backward.restype = ctypes.c_int
+        lib.vpce_rmsnorm_backward.argtypes = [_P, _E, _I64, _P, _E, _I64, _P, _E, _P, _P, _I64, _I64, _I64, _P, _I64,
+                                              _P, ctypes.c_int, _P, ctypes.c_size_t, _P]
+        lib.vpce_grad_norm_workspace_bytes.restype = ctypes.c_size_t
+        lib.vpce_grad_norm_workspace_bytes.argtypes = [_I64]
+        lib.vpce_grad_norm.restype = ctypes.c_int
+        lib.vpce_grad_norm.argtypes = [_P, _I64, _E, _F, _P, _P, _P, ctypes.c_size_t, _P]
+        lib.vpce_adamw_step.restype = ctypes.c_int
+        lib.vpce_adamw_step.argtypes = [_P, _I64, _E, _E, ctypes.c_int, _P, _F, _P, ctypes.c_double, ctypes.c_double,
+                                        _F, _P, _P, _P]
         lib.vpce_read_error_flag.restype = ctypes.c_int
         lib.vpce_read_error_flag.argtypes = [_P, ctypes.POINTER(ctypes.c_int), _P]
         lib.vpce_status_string.restype = ctypes.c_char_p
@@ -1055,3 +1077,386 @@ def vpce_embedding_dropout_backward(grad_out, ids, grad_shards, vocab_start=None
     if code != VPCE_OK:
         raise VPCEError(code, "vpce_embedding_dropout_backward")
     return grad_shards
+
+
+# ----------------------------------------------------------------------------
+# root-mean-square norm with the residual's addition
+# ----------------------------------------------------------------------------
+class RmsnormResult(NamedTuple):
+    """What :func:`vpce_rmsnorm_forward` computed: the normalised ``out``,
+    ``residual`` (the sum ``x + residual``; ``x`` itself without a residual)
+    and float32 ``rstd`` [s]; the last two are for
+    :func:`vpce_rmsnorm_backward`."""
+    out: Any
+    residual: Any
+    rstd: Any
+
+
+class RmsnormQuantizedResult(NamedTuple):
+    """What :func:`vpce_rmsnorm_quantized_forward` computed: e4m3 ``q`` [s, h]
+    and float32 ``scale`` [s, groups] with ``out = q * scale``, and
+    ``residual`` and ``rstd`` as :class:`RmsnormResult`."""
+    q: Any
+    scale: Any
+    residual: Any
+    rstd: Any
+
+
+def _dtype_code(dt, name):
+    if dt is torch.bfloat16:
+        return VPCE_BF16
+    if dt is torch.float32:
+        return VPCE_FP32
+    raise TypeError(f"{name} must be bf16 or fp32")
+
+
+def _norm_rows(x, shape, dtype, dev, name):
+    """Row stride of an [s, h] operand of the norm."""
+    if x.shape != shape or x.get_device() != dev or (x.stride(1) != 1 and shape[1] > 1):
+        raise ValueError(f"{name} must be a tensor of shape {tuple(shape)} on cuda:{dev} with contiguous columns")
+    if dtype is not None and x.dtype is not dtype:
+        raise TypeError(f"{name} must be {dtype}")
+    if shape[0] <= 1:
+        return shape[1]
+    return x.stride(0) or _row_ld(x, shape[1], name)
+
+
+def _norm_weight(weight, h, dev):
+    if weight.dim() != 1 or weight.shape[0] != h or weight.get_device() != dev or not weight.is_contiguous():
+        raise ValueError(f"weight must be a contiguous tensor of {h} elements on cuda:{dev}")
+    return _dtype_code(weight.dtype, "weight")
+
+
+def _norm_inputs(x, weight, residual, residual_out, rstd_out):
+    """What both forms of the norm take: checked operands, as the C entries
+    want them, and the outputs that both have."""
+    if x.dim() != 2:
+        raise ValueError("x must be 2-D")
+    dev = x.get_device()
+    if dev < 0:
+        raise ValueError("x must be a CUDA tensor")
+    shape = x.shape
+    code = _dtype_code(x.dtype, "x")
+    ld = _norm_rows(x, shape, None, dev, "x")
+    wcode = _norm_weight(weight, shape[1], dev)
+    if residual is None:
+        if residual_out is not None:
+            raise ValueError("residual_out needs a residual")
+        rcode, ld_r, ld_ro = code, 0, 0
+    else:
+        rcode = _dtype_code(residual.dtype, "residual")
+        if code == VPCE_FP32 and rcode != VPCE_FP32:
+            raise TypeError("the residual of fp32 rows must be fp32")
+        ld_r = _norm_rows(residual, shape, None, dev, "residual")
+        if residual_out is None:
+            residual_out = torch.empty(shape, dtype=residual.dtype, device=x.device)
+            ld_ro = shape[1]
+        else:
+            ld_ro = _norm_rows(residual_out, shape, residual.dtype, dev, "residual_out")
+    rstd = _buffer(rstd_out, (shape[0],), torch.float32, x, dev, "rstd_out")
+    return dev, shape, (x.data_ptr(), code, ld, _addr(residual), rcode, ld_r, weight.data_ptr(), wcode), residual_out, \
+        ld_ro, rstd
+
+
+@functools.partial(_on_its_device, own_stream=True)
+def vpce_rmsnorm_forward(x, weight, residual=None, *, eps: float = 1e-6, out=None, residual_out=None,
+                         rstd_out=None) -> RmsnormResult:
+    """Rows of ``r = x + residual`` (``x`` without one) divided by their
+    root mean square, times ``weight``: ``r * rstd * weight`` with ``rstd =
+    (mean(r^2) + eps) ** -0.5``, in fp32 from the unrounded sum.  ``x`` [s, h]
+    is bf16 or fp32, ``residual`` its type or fp32, ``weight`` [h] either.
+    ``residual_out`` (given a residual) receives the sum in the residual's
+    type: passing ``residual`` itself updates the stream in place."""
+    dev, shape, head, residual_out, ld_ro, rstd = _norm_inputs(x, weight, residual, residual_out, rstd_out)
+    if out is None:
+        out = torch.empty(shape, dtype=x.dtype, device=x.device)
+        ld_out = shape[1]
+    else:
+        ld_out = _norm_rows(out, shape, x.dtype, dev, "out")
+    code = (_lib or load_library()).vpce_rmsnorm_forward(
+        *head, eps, shape[0], shape[1], _addr(residual_out), ld_ro, out.data_ptr(), ld_out, rstd.data_ptr(),
+        _raw_stream(dev))
+    if code != VPCE_OK:
+        raise VPCEError(code, "vpce_rmsnorm_forward")
+    return RmsnormResult(out, x if residual is None else residual_out, rstd)
+
+
+@functools.partial(_on_its_device, own_stream=True)
+def vpce_rmsnorm_quantized_forward(x, weight, residual=None, *, eps: float = 1e-6, group: int = 0, q_out=None,
+                                   scale_out=None, residual_out=None, rstd_out=None) -> RmsnormQuantizedResult:
+    """:func:`vpce_rmsnorm_forward` with its output as ``torch.float8_e4m3fn``
+    values ``q`` and one float32 ``scale`` per row (``group=0``) or per
+    ``group`` consecutive columns (a multiple of 16): ``scale`` is the group's
+    largest magnitude over 448, and ``q * scale`` the output."""
+    group = int(group)
+    if group < 0 or group % 16:
+        raise ValueError("group must be 0 (one scale per row) or a multiple of 16")
+    dev, shape, head, residual_out, ld_ro, rstd = _norm_inputs(x, weight, residual, residual_out, rstd_out)
+    s, h = shape
+    if q_out is None:
+        q_out = torch.empty(shape, dtype=torch.float8_e4m3fn, device=x.device)
+        ld_q = h
+    else:
+        ld_q = _norm_rows(q_out, shape, torch.float8_e4m3fn, dev, "q_out")
+    scale = _buffer(scale_out, (s, -(-h // group) if group else 1), torch.float32, x, dev, "scale_out")
+    code = (_lib or load_library()).vpce_rmsnorm_quantized_forward(
+        *head, eps, s, h, group, _addr(residual_out), ld_ro, q_out.data_ptr(), ld_q, scale.data_ptr(),
+        rstd.data_ptr(), _raw_stream(dev))
+    if code != VPCE_OK:
+        raise VPCEError(code, "vpce_rmsnorm_quantized_forward")
+    return RmsnormQuantizedResult(q_out, scale, x if residual is None else residual_out, rstd)
+
+
+def vpce_rmsnorm_backward_workspace_bytes(s: int, h: int) -> int:
+    return int(load_library().vpce_rmsnorm_backward_workspace_bytes(int(s), int(h)))
+
+
+@functools.partial(_on_its_device, own_stream=True)
+def vpce_rmsnorm_backward(grad_out, x, weight, rstd, *, grad_residual=None, grad_in=None, grad_weight=None,
+                          accumulate: bool = False, workspace=None):
+    """Gradient of :func:`vpce_rmsnorm_forward` for the upstream ``grad_out``
+    [s, h]: returns ``(grad_in, grad_weight)``.  ``x`` and ``rstd`` are the
+    forward's ``residual`` and ``rstd``.  ``grad_in``, in ``x``'s type, is the
+    gradient of the sum, so of ``x`` and ``residual`` alike, with
+    ``grad_residual`` (what reaches the sum by the residual stream) added; it
+    may be ``grad_residual`` itself.  ``grad_weight`` is float32 [h]:
+    overwritten, or added to with ``accumulate=True``.  A ``grad_out`` or
+    ``grad_residual`` expanded over its rows is read through a dense copy."""
+    if grad_out.dim() != 2:
+        raise ValueError("grad_out must be 2-D")
+    dev = grad_out.get_device()
+    if dev < 0:
+        raise ValueError("grad_out must be a CUDA tensor")
+    shape = grad_out.shape
+    s, h = shape
+    gcode, xcode = _dtype_code(grad_out.dtype, "grad_out"), _dtype_code(x.dtype, "x")
+    if gcode == VPCE_FP32 and xcode != VPCE_FP32:
+        raise TypeError("x must be fp32 beside an fp32 grad_out")
+    grad_out = _rows_of_their_own(grad_out)
+    ld_g = _norm_rows(grad_out, shape, None, dev, "grad_out")
+    ld_x = _norm_rows(x, shape, None, dev, "x")
+    wcode = _norm_weight(weight, h, dev)
+    _buffer(rstd, (s,), torch.float32, x, dev, "rstd")
+    ld_r = 0
+    if grad_residual is not None:
+        grad_residual = _rows_of_their_own(grad_residual)
+        ld_r = _norm_rows(grad_residual, shape, x.dtype, dev, "grad_residual")
+    if grad_in is None:
+        grad_in = torch.empty(shape, dtype=x.dtype, device=x.device)
+        ld_in = h
+    else:
+        ld_in = _norm_rows(grad_in, shape, x.dtype, dev, "grad_in")
+    if grad_weight is None:
+        if accumulate:
+            raise ValueError("accumulate needs a grad_weight")
+        grad_weight = torch.empty((h,), dtype=torch.float32, device=x.device)
+    else:
+        _buffer(grad_weight, (h,), torch.float32, x, dev, "grad_weight")
+    lib = _lib or load_library()
+    if workspace is None:
+        workspace = torch.empty(lib.vpce_rmsnorm_backward_workspace_bytes(s, h), dtype=torch.uint8, device=x.device)
+    elif workspace.get_device() != dev:
+        raise ValueError(f"workspace must be on cuda:{dev}")
+    code = lib.vpce_rmsnorm_backward(
+        grad_out.data_ptr(), gcode, ld_g, x.data_ptr(), xcode, ld_x, weight.data_ptr(), wcode, rstd.data_ptr(),
+        _addr(grad_residual), ld_r, s, h, grad_in.data_ptr(), ld_in, grad_weight.data_ptr(), int(bool(accumulate)),
+        *_workspace(workspace), _raw_stream(dev))
+    if code != VPCE_OK:
+        raise VPCEError(code, "vpce_rmsnorm_backward")
+    return grad_in, grad_weight
+
+
+# ----------------------------------------------------------------------------
+# norm of all gradients, and the AdamW step
+# ----------------------------------------------------------------------------
+class _AdamWTensor(ctypes.Structure):
+    """vpce_adamw_tensor"""
+    _fields_ = [("param", _P), ("grad", _P), ("copy", _P), ("exp_avg", _P), ("exp_avg_sq", _P),
+                ("exp_avg_scale", _P), ("exp_avg_sq_scale", _P), ("n", _I64), ("weight_decay", ctypes.c_float)]
+
+
+def _list_of(xs, like, dev, name, dtype, sizes):
+    """A list of contiguous tensors, one per entry of ``like``, checked or, for
+    None, made of zeros."""
+    if xs is None:
+        return [torch.zeros(n, dtype=dtype, device=x.device) for x, n in zip(like, sizes)]
+    xs = list(xs)
+    if len(xs) != len(like):
+        raise ValueError(f"{name}: one tensor per parameter")
+    for x, n in zip(xs, sizes):
+        if x.get_device() != dev or x.numel() != n or not x.is_contiguous():
+            raise ValueError(f"{name} must be contiguous tensors on cuda:{dev} of their parameters' sizes")
+        if x.dtype is not dtype:
+            raise TypeError(f"{name} must be {dtype}")
+    return xs
+
+
+def _no_overlap(written, read):
+    """Raises where two tensors that a step writes share memory, or one of them
+    and a tensor that it reads."""
+    spans = sorted((x.data_ptr(), x.data_ptr() + x.nbytes, w) for xs, w in ((written, True), (read, False))
+                   for x in xs if x.nbytes)
+    end, end_written = 0, 0  # of everything so far, and of what is written
+    for a, b, w in spans:
+        if a < (end if w else end_written):
+            raise ValueError("tensors that the step writes must not share memory with another of its tensors")
+        end = max(end, b)
+        if w:
+            end_written = max(end_written, b)
+
+
+class AdamWPlan:
+    """Tensors that :func:`vpce_adamw_step` updates together, their gradients
+    and their states; made by :func:`vpce_adamw_plan`.  The lists ``params``,
+    ``grads``, ``copies``, ``exp_avg``, ``exp_avg_sq`` (and, for 8-bit states,
+    ``exp_avg_scale`` and ``exp_avg_sq_scale``) hold the tensors, as a
+    checkpoint saves them; entries are not to be replaced."""
+
+    def __init__(self, params, grads, copies, weight_decay, state_bits, exp_avg, exp_avg_sq, exp_avg_scale,
+                 exp_avg_sq_scale):
+        params, grads = list(params), list(grads)
+        if not params or len(params) != len(grads):
+            raise ValueError("need at least one parameter, and one gradient for each")
+        dev = params[0].get_device()
+        if dev < 0:
+            raise ValueError("params must be CUDA tensors")
+        dtype, gdtype = params[0].dtype, grads[0].dtype
+        self.param_code, self.grad_code = _dtype_code(dtype, "params"), _dtype_code(gdtype, "grads")
+        if state_bits not in (32, 8):
+            raise ValueError("state_bits must be 32 or 8")
+        sizes = [x.numel() for x in params]
+        _list_of(params, params, dev, "params", dtype, sizes)
+        _list_of(grads, params, dev, "grads", gdtype, sizes)
+        if copies is not None:
+            if dtype is not torch.float32:
+                raise TypeError("copies are bf16 beside fp32 params")
+            copies = _list_of(copies, params, dev, "copies", torch.bfloat16, sizes)
+        sdtype = torch.float32 if state_bits == 32 else torch.float8_e4m3fn
+        exp_avg = _list_of(exp_avg, params, dev, "exp_avg", sdtype, sizes)
+        exp_avg_sq = _list_of(exp_avg_sq, params, dev, "exp_avg_sq", sdtype, sizes)
+        if state_bits == 8:
+            blocks = [-(-n // ADAMW_BLOCK) for n in sizes]
+            exp_avg_scale = _list_of(exp_avg_scale, params, dev, "exp_avg_scale", torch.float32, blocks)
+            exp_avg_sq_scale = _list_of(exp_avg_sq_scale, params, dev, "exp_avg_sq_scale", torch.float32, blocks)
+        elif exp_avg_scale is not None or exp_avg_sq_scale is not None:
+            raise ValueError("scales belong to 8-bit states")
+        decays = [float(weight_decay)] * len(params) if isinstance(weight_decay, (int, float)) \
+            else [float(w) for w in weight_decay]
+        if len(decays) != len(params):
+            raise ValueError("weight_decay: one value, or one per parameter")
+        none = [None] * len(params)
+        written = [exp_avg, exp_avg_sq, copies or [], exp_avg_scale or [], exp_avg_sq_scale or [], params]
+        _no_overlap([x for xs in written for x in xs], grads)
+        self.params, self.grads, self.copies, self.state_bits = params, grads, copies, state_bits
+        self.exp_avg, self.exp_avg_sq = exp_avg, exp_avg_sq
+        self.exp_avg_scale, self.exp_avg_sq_scale = exp_avg_scale, exp_avg_sq_scale
+        self._dev = dev
+        self._seen = self._addresses()
+        n = len(params)
+        self._table = (_AdamWTensor * n)(*[
+            _AdamWTensor(p, g, _addr(c), m.data_ptr(), v.data_ptr(), _addr(ms), _addr(vs), k, wd)
+            for p, g, c, m, v, ms, vs, k, wd in zip(self._seen[:n], self._seen[n:], copies or none, exp_avg,
+                                                    exp_avg_sq, exp_avg_scale or none, exp_avg_sq_scale or none,
+                                                    sizes, decays)])
+
+    def get_device(self):
+        return self._dev
+
+    def _addresses(self):
+        return [x.data_ptr() for x in self.params] + [x.data_ptr() for x in self.grads]
+
+    def table(self):
+        """The C entries' list; raises where a parameter or gradient has been
+        given other memory since the plan was made."""
+        if self._addresses() != self._seen:
+            raise ValueError("a parameter's or gradient's memory has moved: make a new plan")
+        return self._table
+
+
+@_on_its_device
+def vpce_adamw_plan(params, grads, *, copies=None, weight_decay=0.01, state_bits: int = 32, exp_avg=None,
+                    exp_avg_sq=None, exp_avg_scale=None, exp_avg_sq_scale=None) -> AdamWPlan:
+    """The tensors of an AdamW step, checked once: ``params`` (all bf16 or all
+    fp32), ``grads`` (likewise; read at every step where they are now),
+    ``copies`` (bf16, written with the new fp32 params: the weights that the
+    LM head reads), ``weight_decay`` (one value, or one per parameter).  The
+    states are made of zeros where they are not given: float32, or with
+    ``state_bits=8`` ``torch.float8_e4m3fn`` with a float32 scale per 256
+    elements, ``exp_avg`` for m and ``exp_avg_sq`` for the square root of v."""
+    return AdamWPlan(params, grads, copies, weight_decay, state_bits, exp_avg, exp_avg_sq, exp_avg_scale,
+                     exp_avg_sq_scale)
+
+
+def _check_scalar(x, dtype, dev, name):
+    if x is not None and (x.dtype is not dtype or x.get_device() != dev or x.numel() != 1):
+        raise ValueError(f"{name} must be a {dtype} tensor of one element on cuda:{dev}")
+
+
+@functools.partial(_on_its_device, own_stream=True)
+def vpce_grad_norm(grads, max_norm: float = float("inf"), *, norm_out=None, scale_out=None, workspace=None):
+    """``(norm, scale)``, two float32 scalars on the device: the square root
+    of the sum of all squares of ``grads`` (a list of contiguous tensors of
+    one type, or an :class:`AdamWPlan`), and ``min(1, max_norm / norm)``, or 0
+    where the norm is not finite: the ``grad_scale`` of
+    :func:`vpce_adamw_step`, without the host looking at it."""
+    if isinstance(grads, AdamWPlan):
+        table, n, code, dev = grads.table(), len(grads.grads), grads.grad_code, grads._dev
+    else:
+        grads = list(grads)
+        if not grads:
+            raise ValueError("need at least one gradient")
+        dev, n = grads[0].get_device(), len(grads)
+        if dev < 0:
+            raise ValueError("grads must be CUDA tensors")
+        code = _dtype_code(grads[0].dtype, "grads")
+        _list_of(grads, grads, dev, "grads", grads[0].dtype, [g.numel() for g in grads])
+        table = (_AdamWTensor * n)(*[_AdamWTensor(None, g.data_ptr(), None, None, None, None, None, g.numel(), 0.0)
+                                     for g in grads])
+    _check_scalar(norm_out, torch.float32, dev, "norm_out")
+    _check_scalar(scale_out, torch.float32, dev, "scale_out")
+    if norm_out is None:
+        norm_out = torch.empty((), dtype=torch.float32, device=torch.device("cuda", dev))
+    if scale_out is None:
+        scale_out = torch.empty((), dtype=torch.float32, device=torch.device("cuda", dev))
+    lib = _lib or load_library()
+    if workspace is None:
+        workspace = torch.empty(lib.vpce_grad_norm_workspace_bytes(n), dtype=torch.uint8,
+                                device=torch.device("cuda", dev))
+    elif workspace.get_device() != dev:
+        raise ValueError(f"workspace must be on cuda:{dev}")
+    status = lib.vpce_grad_norm(table, n, code, max_norm, norm_out.data_ptr(), scale_out.data_ptr(),
+                                *_workspace(workspace), _raw_stream(dev))
+    if status != VPCE_OK:
+        raise VPCEError(status, "vpce_grad_norm")
+    return norm_out, scale_out
+
+
+@functools.partial(_on_its_device, own_stream=True)
+def vpce_adamw_step(plan, step, *, lr, betas=(0.9, 0.999), eps: float = 1e-8, grad_scale=None, rng=None) -> None:
+    """One AdamW step of every tensor of ``plan`` (:func:`vpce_adamw_plan`), in
+    place.  ``step`` is a CUDA int64 tensor of one element, the step's number
+    from 1; ``lr`` a number or a CUDA float32 tensor of one element; both, like
+    ``grad_scale`` (float32, one element, from :func:`vpce_grad_norm`;
+    gradients are multiplied by it, and 0 skips the step), are read by the
+    kernel, so that a captured step goes on with new values.  8-bit states
+    need ``rng`` (CUDA int64 ``[seed, offset]``), the words of their stochastic
+    rounding: another offset every step."""
+    if not isinstance(plan, AdamWPlan):
+        raise TypeError("plan must come from vpce_adamw_plan")
+    dev = plan._dev
+    if step is None:
+        raise ValueError("step must be a CUDA int64 tensor of one element")
+    _check_scalar(step, torch.int64, dev, "step")
+    _check_scalar(grad_scale, torch.float32, dev, "grad_scale")
+    _check_rng(rng, dev)
+    lr_dev = None
+    if isinstance(lr, torch.Tensor):
+        _check_scalar(lr, torch.float32, dev, "lr")
+        lr, lr_dev = 0.0, lr.data_ptr()
+    if plan.state_bits == 8 and rng is None:
+        raise ValueError("8-bit states need rng")
+    code = (_lib or load_library()).vpce_adamw_step(
+        plan.table(), len(plan.params), plan.param_code, plan.grad_code, plan.state_bits, step.data_ptr(), lr, lr_dev,
+        betas[0], betas[1], eps, _addr(grad_scale), _addr(rng), _raw_stream(dev))
+    if code != VPCE_OK:
+        raise VPCEError(code, "vpce_adamw_step")
