@@ -768,7 +768,7 @@ vpce_status vpce_grad_norm(const vpce_adamw_tensor* tensors, int64_t n_tensors, 
  *                 vpce_embedding_dropout_forward with counter = (k / 8, the
  *                 tensor's position in `tensors`, offset's two words), k the
  *                 element's index.  A NaN or infinity in a block's m or v
- *                 spreads over the block's codes of it at the next step.
+ *                 spreads over all of the block's codes of it.
  *   step          device int64[1]: t, from 1 (smaller is taken as 1); read by
  *                 the kernel, so that a captured graph advances with it.
  *   lr, lr_dev    the rate; lr_dev, a device float, replaces lr where not NULL.

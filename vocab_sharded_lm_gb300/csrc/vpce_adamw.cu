@@ -121,38 +121,61 @@ __device__ __forceinline__ void decode4(unsigned c, float (&x)[8], int at) {
   }
 }
 
-__device__ __forceinline__ float approx_sqrt(float x) {
-  float y;
-  asm("sqrt.approx.f32 %0, %1;" : "=f"(y) : "f"(x));
-  return y;
-}
-
 __device__ __forceinline__ float block_scale(unsigned top) {
-  const float s = __fdiv_rn(__uint_as_float(top), 448.f);
+  const float s = __fmul_rn(__uint_as_float(top), 1.f / 448.f);
   return s < kTiny ? kTiny : s;  // a NaN stays
 }
 
-// e4m3 code of 0 <= a <= 448 (a little above is taken as 448), rounded up with
-// the random half u.  Codes count up with the values: a normal code is the top
-// bits of the fp32 word, and adding 2^-6 brings the values below e4m3's least
-// normal one into a binade whose 8 steps are e4m3's subnormal step.  The bits
-// below the code are then the fraction f of the step.  kSquares: the chance is
-// that of the squares, f (2 L + f) / (2 L + 1) with lo = L steps.
-template <bool kSquares> __device__ __forceinline__ unsigned round_code(float a, unsigned u) {
-  const bool small = a < 0.015625f;
-  const unsigned bits = __float_as_uint(small ? a + 0.015625f : a);
-  unsigned code = (bits >> 20) - (small ? 968u : 960u);
-  const float f = float(bits & 0xfffffu) * 0x1p-20f, r = float(2 * u + 1) * 0x1p-17f;
+// x / s correctly rounded, for inv = 1 / s correctly rounded and x <= 448 s
+// (Markstein, "Computation of elementary functions on the IBM RISC System/6000
+// processor", 1990: one residual step).
+__device__ __forceinline__ float quotient(float x, float s, float inv) {
+  const float q = __fmul_rn(x, inv);
+  return __fmaf_rn(__fmaf_rn(-q, s, x), inv, q);
+}
+
+// The e4m3 value that a, 0 <= a <= 448, takes with the random fraction
+// c = (u + 1/2) / 2^16: the neighbour above where c is below a's place between
+// the two, as fl((a - lo) / (hi - lo)) > c says, with a and the neighbours
+// squared for kSquares.  Counted in steps hi - lo, A = a, L = lo: the
+// differences are exact, and so is that of the squares A^2 - L^2 from the
+// rounded A^2; its quotient by 2 L + 1 rounds to more than c, which has 17
+// bits, where it is over c by more than half of c's last place.  (Above 448
+// the conversion saturates; a NaN stays one.)
+template <bool kSquares> __device__ __forceinline__ float round_value(float a, float c) {
+  const unsigned bits = __float_as_uint(a);
+  float A, L;
+  if (a < 0.015625f) {  // e4m3's subnormal values, in steps of 2^-9
+    A = a * 512.f;
+    L = truncf(A);
+  } else {  // a normal one has eight to fifteen steps
+    A = __uint_as_float((bits & 0x7fffffu) | 0x41000000u);
+    L = __uint_as_float(__float_as_uint(A) & 0xfff00000u);
+  }
   bool up;
   if constexpr (kSquares) {
-    const float L = float(code < 8 ? code : 8 + (code & 7));
-    up = r * (2.f * L + 1.f) < f * (2.f * L + f);
+    const float D = fmaf(2.f, L, 1.f), N = __fsub_rn(__fmul_rn(A, A), L * L);
+    up = __fmaf_rn(-D, c, N) > D * __uint_as_float((__float_as_uint(c) & 0x7f800000u) - (24u << 23));
   } else {
-    up = r < f;
+    up = A - L > c;
   }
-  code += up;
-  if (!(a < 448.f)) code = a != a ? 127u : 126u;
-  return code;
+  if (a < 0.015625f) {
+    L = (L + (up ? 1.f : 0.f)) * 0x1p-9f;
+    return kSquares && a > 0.f ? fmaxf(L, 0x1p-9f) : L;
+  }
+  return __uint_as_float((bits & 0xfff00000u) + (up && a < 480.f ? 0x100000u : 0u));  // (a NaN's bits stay one's)
+}
+
+// (u + 1/2) / 2^16 of a word's low or high half
+template <bool kHigh> __device__ __forceinline__ float random_fraction(unsigned word) {
+  return __uint_as_float(((kHigh ? word >> 9 : word << 7) & 0x7fff80u) | 0x3f800040u) - 1.f;
+}
+
+// two values that are e4m3 values already (or past 448) as codes
+__device__ __forceinline__ unsigned pack_codes(float lo, float hi) {
+  unsigned short r;
+  asm("cvt.rn.satfinite.e4m3x2.f32 %0, %1, %2;" : "=h"(r) : "f"(hi), "f"(lo));
+  return r;
 }
 
 template <int kCap> __device__ __forceinline__ int find_tensor(const AdamArgs<kCap>& a, int run) {
@@ -205,17 +228,19 @@ __global__ void __launch_bounds__(kThreads) adamw_kernel(const __grid_constant__
       decode4(cv.y, xv, 4);
 #pragma unroll
       for (int j = 0; j < 8; ++j) {
-        xm[j] *= sm;
-        xv[j] *= sv;
-        xv[j] *= xv[j];
+        xm[j] = __fmul_rn(xm[j], sm);
+        xv[j] = __fmul_rn(xv[j], sv);
+        xv[j] = __fmul_rn(xv[j], xv[j]);
       }
     }
 #pragma unroll
     for (int j = 0; j < 8; ++j) {
-      const float gj = xg[j] * gs;
-      xm[j] = fmaf(hy.b1, xm[j], hy.a1 * gj);
-      xv[j] = fmaf(hy.b2, xv[j], hy.a2 * gj * gj);
-      const float root = approx_sqrt(xv[j]);
+      // each operation rounded by itself: the states, and so their codes, are
+      // those of the formula as it stands, in fp32 on any machine
+      const float gj = __fmul_rn(xg[j], gs);
+      xm[j] = __fadd_rn(__fmul_rn(hy.b1, xm[j]), __fmul_rn(hy.a1, gj));
+      xv[j] = __fadd_rn(__fmul_rn(hy.b2, xv[j]), __fmul_rn(__fmul_rn(hy.a2, gj), gj));
+      const float root = __fsqrt_rn(xv[j]);
       xp[j] = fmaf(-rate, __fdividef(xm[j], fmaf(root, inv2, hy.eps)), xp[j] * keep);
       if constexpr (kBits == 8) xv[j] = root;
     }
@@ -233,20 +258,21 @@ __global__ void __launch_bounds__(kThreads) adamw_kernel(const __grid_constant__
       }
       const float sm = block_scale(__reduce_max_sync(kFull, tm)), sv = block_scale(__reduce_max_sync(kFull, tv));
       const float im = __fdiv_rn(1.f, sm), iv = __fdiv_rn(1.f, sv);
-      const long long k8 = e >> 3;
-      const uint4 u = drop_block(key, a.base + i, unsigned(k8));
+      const uint4 u = drop_block(key, a.base + i, unsigned(e >> 3));
       const unsigned word[4] = {u.x, u.y, u.z, u.w};
-      uint2 cm = make_uint2(0, 0), cv = make_uint2(0, 0);
+      unsigned cm2[4], cv2[4];
 #pragma unroll
-      for (int j = 0; j < 8; ++j) {
-        const unsigned h = (word[j >> 1] >> (16 * (j & 1))) & 0xffffu;
-        const unsigned sign = (__float_as_uint(xm[j]) >> 24) & 0x80u;
-        const unsigned a8 = round_code<false>(fabsf(xm[j]) * im, h) | sign;
-        unsigned b8 = round_code<true>(xv[j] * iv, h);
-        if (xv[j] > 0.f && b8 == 0) b8 = 1;
-        (j < 4 ? cm.x : cm.y) |= a8 << (8 * (j & 3));
-        (j < 4 ? cv.x : cv.y) |= b8 << (8 * (j & 3));
+      for (int j = 0; j < 8; j += 2) {
+        const float c0 = random_fraction<false>(word[j / 2]), c1 = random_fraction<true>(word[j / 2]);
+        const float m0 = round_value<false>(quotient(fabsf(xm[j]), sm, im), c0);
+        const float m1 = round_value<false>(quotient(fabsf(xm[j + 1]), sm, im), c1);
+        const float v0 = round_value<true>(quotient(xv[j], sv, iv), c0);
+        const float v1 = round_value<true>(quotient(xv[j + 1], sv, iv), c1);
+        cm2[j / 2] = pack_codes(copysignf(m0, xm[j]), copysignf(m1, xm[j + 1]));
+        cv2[j / 2] = pack_codes(v0, v1);
       }
+      const uint2 cm = make_uint2(cm2[0] | cm2[1] << 16, cm2[2] | cm2[3] << 16);
+      const uint2 cv = make_uint2(cv2[0] | cv2[1] << 16, cv2[2] | cv2[3] << 16);
       store_codes(m + e, left, vec, cm);
       store_codes(v + e, left, vec, cv);
       if ((threadIdx.x & 31) == 0) {

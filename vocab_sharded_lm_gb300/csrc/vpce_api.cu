@@ -28,6 +28,7 @@ cudaError_t set_gemm_bwd_smem();
 cudaError_t set_embed_smem();
 cudaError_t set_logprob_smem();
 cudaError_t set_embed_dropout_smem();
+cudaError_t set_rmsnorm_smem();
 size_t lmhead_bwd_workspace_bytes(long long V, long long h);
 size_t lmhead_bwd_min_workspace_bytes(long long V, long long h);
 vpce_status lmhead_backward_run(const void* x, long long ld_x, const void* const* w, long long ld_w, int t,
@@ -95,7 +96,7 @@ vpce_status device_setup(int* sms) {
     } else if (set_backward_smem() != cudaSuccess ||
                set_fused_smem() != cudaSuccess || set_gemm_smem() != cudaSuccess || set_gemm_bwd_smem() != cudaSuccess ||
                set_embed_smem() != cudaSuccess || set_logprob_smem() != cudaSuccess ||
-               set_embed_dropout_smem() != cudaSuccess) {
+               set_embed_dropout_smem() != cudaSuccess || set_rmsnorm_smem() != cudaSuccess) {
       cudaGetLastError();
       return VPCE_ERR_CUDA;
     } else {

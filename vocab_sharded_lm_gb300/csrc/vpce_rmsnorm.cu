@@ -32,14 +32,20 @@ __device__ __forceinline__ void store_codes(unsigned char* p, const float (&v)[1
 __device__ __forceinline__ unsigned mag(float v) { return __float_as_uint(v) & 0x7fffffffu; }
 
 __device__ __forceinline__ float group_scale(unsigned top) {
-  const float s = __fdiv_rn(__uint_as_float(top), 448.f);
+  const float s = __fmul_rn(__uint_as_float(top), 1.f / 448.f);
   return s < kTiny ? kTiny : s;  // a NaN stays
 }
 
-template <typename XT, typename RT, bool kCodes, int U, int NU, bool kWarp, int kMaxT>
+// Where a group's largest magnitude is found: in the lanes of a warp that hold
+// the group (16, 32, .. 256 columns in vectors), by the whole team (one group a
+// row), or through shared memory.
+enum GroupKind { kNoCodes, kLanes, kRow, kShared };
+
+template <typename XT, typename RT, GroupKind kGroups, int U, int NU, bool kWarp, int kMaxT>
 __global__ void __launch_bounds__(kMaxT) rmsnorm_forward_kernel(const __grid_constant__ RmsNormParams p) {
-  extern __shared__ unsigned top_sm[];  // [teams][2][groups], codes only
+  extern __shared__ unsigned top_sm[];  // [teams][2][groups], kShared only
   __shared__ float red[2][32];
+  [[maybe_unused]] __shared__ unsigned top_row[2][32];
   const int lane = threadIdx.x & 31;
   const int team = kWarp ? int(threadIdx.x >> 5) : 0, teams = kWarp ? int(blockDim.x >> 5) : 1;
   const int tid = kWarp ? lane : int(threadIdx.x), T = kWarp ? 32 : int(blockDim.x);
@@ -80,80 +86,111 @@ __global__ void __launch_bounds__(kMaxT) rmsnorm_forward_kernel(const __grid_con
     }
     // the two buffers alternate: who still reads one row's is at most a
     // barrier behind whoever writes the next row's
-    unsigned* top = kCodes ? top_sm + (team * 2 + parity) * p.groups : nullptr;
-    if constexpr (kCodes) {
+    [[maybe_unused]] unsigned* top = nullptr;
+    if constexpr (kGroups == kShared) {
+      top = top_sm + (team * 2 + parity) * p.groups;
       for (int g = tid; g < p.groups; g += T) top[g] = 0;
       if constexpr (kWarp) __syncwarp();
     }
     ss = team_sum<kWarp>(ss, red[parity]);
-    parity ^= 1;
     const float rstd = rsqrtf(ss / float(p.h) + p.eps);
     if (tid == 0 && p.rstd != nullptr) p.rstd[row] = rstd;
+    [[maybe_unused]] unsigned m[NU], all = 0;
 #pragma unroll
     for (int k = 0; k < NU; ++k) {
       const int c = (k * T + tid) * U;
+      m[k] = 0;
       if (c < p.h) {
         float w[U];
         load_weight(p.w, p.w_bf16, c, w);
 #pragma unroll
         for (int j = 0; j < U; ++j) r[k][j] = r[k][j] * rstd * w[j];
-        if constexpr (!kCodes) {
+        if constexpr (kGroups == kNoCodes) {
           store_unit(p.out + row * p.ld_out, c, r[k], XT());
         } else {
-          unsigned m = 0;
 #pragma unroll
-          for (int j = 0; j < U; ++j) m = max(m, mag(r[k][j]));
-          atomicMax(top + c / p.group, m);  // shared memory; the order does not matter
+          for (int j = 0; j < U; ++j) m[k] = max(m[k], mag(r[k][j]));
+          if constexpr (kGroups == kShared) atomicMax(top + c / p.group, m[k]);  // the order does not matter
+          if constexpr (kGroups == kRow) all = max(all, m[k]);
         }
       }
     }
-    if constexpr (kCodes) {
+    if constexpr (kGroups == kLanes) {
+      const int lanes = p.group / U;
+#pragma unroll
+      for (int o = 1; o < 32; o <<= 1) {
+        if (o < lanes) {
+#pragma unroll
+          for (int k = 0; k < NU; ++k) m[k] = max(m[k], __shfl_xor_sync(kFull, m[k], o));
+        }
+      }
+    } else if constexpr (kGroups == kRow) {
+      all = __reduce_max_sync(kFull, all);
+      if constexpr (!kWarp) {
+        const int warps = T >> 5;
+        if (lane == 0) top_row[parity][threadIdx.x >> 5] = all;
+        __syncthreads();
+        all = __reduce_max_sync(kFull, lane < warps ? top_row[parity][lane] : 0u);
+      }
+#pragma unroll
+      for (int k = 0; k < NU; ++k) m[k] = all;
+    } else if constexpr (kGroups == kShared) {
       if constexpr (kWarp) __syncwarp();
       else __syncthreads();
-      for (int g = tid; g < p.groups; g += T) p.scale[row * p.groups + g] = group_scale(top[g]);
+    }
+    if constexpr (kGroups != kNoCodes) {
 #pragma unroll
       for (int k = 0; k < NU; ++k) {
         const int c = (k * T + tid) * U;
         if (c < p.h) {
-          const float inv = __fdiv_rn(1.f, group_scale(top[c / p.group]));
+          const int g = kGroups == kRow ? 0 : c / p.group;
+          const float scale = group_scale(kGroups == kShared ? top[g] : m[k]), inv = __fdiv_rn(1.f, scale);
+          if (c == g * p.group) p.scale[row * p.groups + g] = scale;
 #pragma unroll
           for (int j = 0; j < U; ++j) r[k][j] *= inv;
           store_codes(p.out + row * p.ld_out + c, r[k]);
         }
       }
     }
+    parity ^= 1;
   }
 }
 
-template <typename XT, typename RT, bool kCodes, int U, int NU, bool kWarp, int kMaxT = 128>
+template <typename XT, typename RT, GroupKind kGroups, int U, int NU, bool kWarp, int kMaxT = 128>
 void launch(const RmsNormParams& p, int threads, int sms, cudaStream_t st) {
   const int teams = kWarp ? 4 : 1;
   const long long rows = (p.s + teams - 1) / teams, most = (long long)sms * 64;
-  const size_t smem = kCodes ? size_t(teams) * 2 * p.groups * sizeof(unsigned) : 0;
-  rmsnorm_forward_kernel<XT, RT, kCodes, U, NU, kWarp, kMaxT>
+  const size_t smem = kGroups == kShared ? size_t(teams) * 2 * p.groups * sizeof(unsigned) : 0;
+  rmsnorm_forward_kernel<XT, RT, kGroups, U, NU, kWarp, kMaxT>
       <<<int(rows < most ? rows : most), kWarp ? 128 : threads, smem, st>>>(p);
 }
 
-template <typename XT, typename RT, bool kCodes> void pick(const RmsNormParams& p, bool vectors, int sms, cudaStream_t st) {
+template <typename XT, typename RT, GroupKind kGroups>
+void pick(const RmsNormParams& p, bool vectors, int sms, cudaStream_t st) {
   const int h = p.h;
   if (vectors) {
     const int units = h / 8;
-    if (units <= 32) return launch<XT, RT, kCodes, 8, 1, true>(p, 32, sms, st);
-    if (units <= 128) return launch<XT, RT, kCodes, 8, 4, true>(p, 32, sms, st);
+    if (units <= 32) return launch<XT, RT, kGroups, 8, 1, true>(p, 32, sms, st);
+    if (units <= 128) return launch<XT, RT, kGroups, 8, 4, true>(p, 32, sms, st);
     const int threads = ((units + 3) / 4 + 31) / 32 * 32;
-    if (threads <= 512) return launch<XT, RT, kCodes, 8, 4, false, 512>(p, threads, sms, st);
-    return launch<XT, RT, kCodes, 8, 4, false, 1024>(p, threads, sms, st);
+    if (threads <= 512) return launch<XT, RT, kGroups, 8, 4, false, 512>(p, threads, sms, st);
+    return launch<XT, RT, kGroups, 8, 4, false, 1024>(p, threads, sms, st);
   }
-  if (h <= 256) return launch<XT, RT, kCodes, 1, 8, true>(p, 32, sms, st);
-  if (h <= 1024) return launch<XT, RT, kCodes, 1, 32, true>(p, 32, sms, st);
-  const int threads = ((h + 31) / 32 + 31) / 32 * 32;
-  if (threads <= 512) return launch<XT, RT, kCodes, 1, 32, false, 512>(p, threads, sms, st);
-  launch<XT, RT, kCodes, 1, 32, false, 1024>(p, threads, sms, st);
+  if constexpr (kGroups != kLanes) {
+    if (h <= 256) return launch<XT, RT, kGroups, 1, 8, true>(p, 32, sms, st);
+    const int threads = ((h + 7) / 8 + 31) / 32 * 32;
+    if (threads <= 512) return launch<XT, RT, kGroups, 1, 8, false, 512>(p, threads, sms, st);
+    launch<XT, RT, kGroups, 1, 32, false, 1024>(p, ((h + 31) / 32 + 31) / 32 * 32, sms, st);
+  }
 }
 
-template <typename XT, typename RT> void pick(const RmsNormParams& p, bool codes, bool vectors, int sms, cudaStream_t st) {
-  if (codes) pick<XT, RT, true>(p, vectors, sms, st);
-  else pick<XT, RT, false>(p, vectors, sms, st);
+template <typename XT, typename RT>
+void pick(const RmsNormParams& p, bool codes, bool vectors, int sms, cudaStream_t st) {
+  const bool lanes = p.group <= 256 && (p.group & (p.group - 1)) == 0;
+  if (!codes) pick<XT, RT, kNoCodes>(p, vectors, sms, st);
+  else if (p.groups == 1) pick<XT, RT, kRow>(p, vectors, sms, st);
+  else if (vectors && lanes) pick<XT, RT, kLanes>(p, vectors, sms, st);
+  else pick<XT, RT, kShared>(p, vectors, sms, st);
 }
 
 }  // namespace

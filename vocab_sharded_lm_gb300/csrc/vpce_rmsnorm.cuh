@@ -57,6 +57,11 @@ template <> struct RawUnit<float, 8> {
     a = p[0];
     b = p[1];
   }
+  // from a thread's own slots in shared memory, `pitch` vectors apart
+  __device__ __forceinline__ void take(const uint4* p, int pitch) {
+    a = p[0];
+    b = p[pitch];
+  }
   __device__ __forceinline__ void get(float (&v)[8]) const {
     v[0] = __uint_as_float(a.x), v[1] = __uint_as_float(a.y), v[2] = __uint_as_float(a.z), v[3] = __uint_as_float(a.w);
     v[4] = __uint_as_float(b.x), v[5] = __uint_as_float(b.y), v[6] = __uint_as_float(b.z), v[7] = __uint_as_float(b.w);
@@ -68,6 +73,7 @@ template <> struct RawUnit<__nv_bfloat16, 8> {
   __device__ __forceinline__ void load(const unsigned char* row, int c) {
     a = *reinterpret_cast<const uint4*>(row + size_t(c) * 2);
   }
+  __device__ __forceinline__ void take(const uint4* p, int) { a = p[0]; }
   __device__ __forceinline__ void get(float (&v)[8]) const { unpack(a, v, __nv_bfloat16()); }
   __device__ __forceinline__ void zero() { a = make_uint4(0, 0, 0, 0); }
 };
@@ -134,12 +140,6 @@ template <bool kWarp> __device__ __forceinline__ float team_sum(float v, float* 
   }
   return v;
 }
-
-// How a row is shared out: `threads` of a CTA take it (32: one warp, four rows
-// a CTA), each NU units of U columns.
-struct RmsShape {
-  int unit, per_thread, threads;
-};
 
 void launch_rmsnorm_forward(const RmsNormParams& p, bool x_bf16, bool res_bf16, bool codes, bool vectors, int sms,
                             cudaStream_t st);

@@ -2,55 +2,156 @@
 //     dr = dresidual + rstd (w dy - n mean(w dy n)),    dw = sum over rows dy n.
 //
 // One pass over dy, r and dresidual.  A thread keeps the same columns on every
-// row that its CTA takes, so dw's terms add up in its registers; each CTA then
+// row that its team takes, so dw's terms add up in its registers; each CTA then
 // leaves one partial row, and a second kernel adds those in a fixed order.
+//
+// The row's mean is a barrier in every row, so what keeps HBM busy is what a
+// team has asked for ahead: rows in vectors come through a ring of shared
+// memory that every thread fills for itself (cp.async: each reads only what it
+// copied, so no barrier goes with it), a few rows deep.  Rows off 16 bytes are
+// read element by element by smaller teams, several in a CTA.
 #include "vpce_rmsnorm.cuh"
 
 namespace vpce {
 namespace {
 
-constexpr int kColumns = 32, kRowLanes = 16;  // of the kernel that adds the partial rows
+constexpr int kColumns = 32, kRowLanes = 32;  // of the kernel that adds the partial rows
 
-template <typename GT, typename RT, int U, int NU, bool kWarp, int kMaxT>
-__global__ void __launch_bounds__(kMaxT) rmsnorm_backward_kernel(const __grid_constant__ RmsNormBwdParams p) {
-  extern __shared__ float sums[];  // [warps][h], one-warp teams only
-  __shared__ float red[2][32];
-  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-  const int teams = kWarp ? int(blockDim.x >> 5) : 1;
-  const int tid = kWarp ? lane : int(threadIdx.x), T = kWarp ? 32 : int(blockDim.x);
+__device__ __forceinline__ void copy_async16(uint32_t dst, const void* src) {
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(dst), "l"(src) : "memory");
+}
+__device__ __forceinline__ void copy_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
+template <int N> __device__ __forceinline__ void copy_wait() {
+  asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
+}
+
+// The threads of one team: whole warps, with a barrier of their own (not 0,
+// which is the CTA's).
+struct Team {
+  int id, tid, threads;
+  float* red;  // [2][32]
+  __device__ __forceinline__ float sum(float v, int parity) const {
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) v += __shfl_xor_sync(kFull, v, o);
+    if (threads > 32) {
+      const int lane = tid & 31, warps = threads >> 5;
+      float* r = red + parity * 32;
+      if (lane == 0) r[tid >> 5] = v;
+      asm volatile("bar.sync %0, %1;" ::"r"(id + 1), "r"(threads) : "memory");
+      v = lane < warps ? r[lane] : 0.f;
+#pragma unroll
+      for (int o = 16; o > 0; o >>= 1) v += __shfl_xor_sync(kFull, v, o);
+    }
+    return v;
+  }
+};
+
+// Vectors of one row that a thread copies ahead: `16 * kParts` bytes a unit of
+// eight elements.
+template <typename T> constexpr int kParts = sizeof(T) / 2;
+
+// kStages: rows of the ring ahead (0: none, rows are loaded when they are due).
+// kKeep: a row's values stay in registers until its mean is known; else (four
+// units of vectors, or 32 elements, a thread) they are read a second time, from
+// the ring or through L1.
+template <typename GT, typename RT, int U, int NU, int kStages, int kMaxT, int kCtas, bool kKeep>
+__global__ void __launch_bounds__(kMaxT, kCtas) rmsnorm_backward_kernel(const __grid_constant__ RmsNormBwdParams p,
+                                                                 int team_threads) {
+  extern __shared__ uint4 smem[];  // the ring, and at the end sums [teams][h]
+  __shared__ float red[kMaxT / 32][2][32];
+  constexpr bool kRing = kStages > 0;
+  Team team;
+  const int teams = blockDim.x / team_threads;
+  team.id = threadIdx.x / team_threads;
+  team.tid = threadIdx.x - team.id * team_threads;
+  team.threads = team_threads;
+  team.red = &red[team.id][0][0];
+  const int T = team_threads, tid = team.tid;
   float acc[NU][U];
 #pragma unroll
   for (int k = 0; k < NU; ++k)
 #pragma unroll
     for (int j = 0; j < U; ++j) acc[k][j] = 0.f;
-  int parity = 0;
-  for (long long row = (long long)blockIdx.x * teams + (kWarp ? warp : 0); row < p.s;
-       row += (long long)gridDim.x * teams) {
-    const unsigned char *gr = p.dy + row * p.ld_dy, *xr = p.x + row * p.ld_x;
-    RawUnit<GT, U> g[NU];
-    RawUnit<RT, U> x[NU], d[NU];
+
+  // ring slot of vector v of a stage: this thread's own 16 bytes
+  constexpr int kVecs = NU * (kParts<GT> + 2 * kParts<RT>);
+  const auto slot = [&](int stage, int v) { return smem + (stage * kVecs + v) * blockDim.x + threadIdx.x; };
+  const auto fetch = [&](long long row, int stage) {
+    if (row < p.s) {
 #pragma unroll
-    for (int k = 0; k < NU; ++k) {
-      const int c = (k * T + tid) * U;
-      g[k].zero();
-      x[k].zero();
-      d[k].zero();
-      if (c < p.h) {
-        g[k].load(gr, c);
-        x[k].load(xr, c);
-        if (p.dres != nullptr) d[k].load(p.dres + row * p.ld_dres, c);
+      for (int k = 0; k < NU; ++k) {
+        const int c = (k * T + tid) * U;
+        if (c < p.h) {
+          const unsigned char *g = p.dy + row * p.ld_dy + size_t(c) * sizeof(GT),
+                              *x = p.x + row * p.ld_x + size_t(c) * sizeof(RT);
+#pragma unroll
+          for (int i = 0; i < kParts<GT>; ++i) copy_async16(smem_addr(slot(stage, k * kParts<GT> + i)), g + 16 * i);
+#pragma unroll
+          for (int i = 0; i < kParts<RT>; ++i)
+            copy_async16(smem_addr(slot(stage, NU * kParts<GT> + k * kParts<RT> + i)), x + 16 * i);
+          if (p.dres != nullptr) {
+            const unsigned char* d = p.dres + row * p.ld_dres + size_t(c) * sizeof(RT);
+#pragma unroll
+            for (int i = 0; i < kParts<RT>; ++i)
+              copy_async16(smem_addr(slot(stage, NU * (kParts<GT> + kParts<RT>) + k * kParts<RT> + i)), d + 16 * i);
+          }
+        }
       }
     }
+    copy_commit();  // (an empty group past the end keeps the count)
+  };
+
+  const long long first = (long long)blockIdx.x * teams + team.id, stride = (long long)gridDim.x * teams;
+  if constexpr (kRing) {
+#pragma unroll
+    for (int i = 0; i < kStages; ++i) fetch(first + i * stride, i);
+  }
+  int parity = 0, stage = 0;
+  for (long long row = first; row < p.s; row += stride) {
     const float rstd = __ldg(p.rstd + row);
+    const auto load_g = [&](RawUnit<GT, U>& g, int k, int c) {
+      if constexpr (kRing) g.take(slot(stage, k * kParts<GT>), blockDim.x);
+      else g.load(p.dy + row * p.ld_dy, c);
+    };
+    const auto load_x = [&](RawUnit<RT, U>& x, int k, int c) {
+      if constexpr (kRing) x.take(slot(stage, NU * kParts<GT> + k * kParts<RT>), blockDim.x);
+      else x.load(p.x + row * p.ld_x, c);
+    };
+    const auto load_d = [&](RawUnit<RT, U>& d, int k, int c) {
+      if constexpr (kRing) d.take(slot(stage, NU * (kParts<GT> + kParts<RT>) + k * kParts<RT>), blockDim.x);
+      else d.load(p.dres + row * p.ld_dres, c);
+    };
+    if constexpr (kRing) copy_wait<(kRing ? kStages - 1 : 0)>();
+    constexpr int kKept = kKeep ? NU : 1;
+    RawUnit<GT, U> g[kKept];
+    RawUnit<RT, U> x[kKept], d[kKept];
+    if constexpr (kKeep) {
+#pragma unroll
+      for (int k = 0; k < NU; ++k) {
+        const int c = (k * T + tid) * U;
+        g[k].zero();
+        x[k].zero();
+        d[k].zero();
+        if (c < p.h) {
+          load_g(g[k], k, c);
+          load_x(x[k], k, c);
+          if (p.dres != nullptr) load_d(d[k], k, c);
+        }
+      }
+    }
     float dot = 0.f;
 #pragma unroll
     for (int k = 0; k < NU; ++k) {
-      const int c = (k * T + tid) * U;
+      const int c = (k * T + tid) * U, at = kKeep ? k : 0;
       if (c < p.h) {
         float w[U], dy[U], n[U];
         load_weight(p.w, p.w_bf16, c, w);
-        g[k].get(dy);
-        x[k].get(n);
+        if constexpr (!kKeep) {
+          load_g(g[0], k, c);
+          load_x(x[0], k, c);
+        }
+        g[at].get(dy);
+        x[at].get(n);
 #pragma unroll
         for (int j = 0; j < U; ++j) {
           n[j] *= rstd;
@@ -59,99 +160,142 @@ __global__ void __launch_bounds__(kMaxT) rmsnorm_backward_kernel(const __grid_co
         }
       }
     }
-    dot = team_sum<kWarp>(dot, red[parity]) / float(p.h);
+    dot = team.sum(dot, parity) / float(p.h);
     parity ^= 1;
+    if constexpr (kRing && kKeep) fetch(row + kStages * stride, stage);  // (the stage's values are in registers)
 #pragma unroll
     for (int k = 0; k < NU; ++k) {
-      const int c = (k * T + tid) * U;
+      const int c = (k * T + tid) * U, at = kKeep ? k : 0;
       if (c < p.h) {
         float w[U], dy[U], n[U], o[U];
         load_weight(p.w, p.w_bf16, c, w);
-        g[k].get(dy);
-        x[k].get(n);
-        d[k].get(o);
+        if constexpr (!kKeep) {
+          load_g(g[0], k, c);
+          load_x(x[0], k, c);
+          d[0].zero();
+          if (p.dres != nullptr) load_d(d[0], k, c);
+        }
+        g[at].get(dy);
+        x[at].get(n);
+        d[at].get(o);
 #pragma unroll
         for (int j = 0; j < U; ++j) o[j] = fmaf(rstd, w[j] * dy[j] - n[j] * rstd * dot, o[j]);
         store_unit(p.dx + row * p.ld_dx, c, o, RT());
       }
     }
+    if constexpr (kRing) {
+      if constexpr (!kKeep) fetch(row + kStages * stride, stage);
+      stage = stage + 1 == kStages ? 0 : stage + 1;
+    }
   }
   grid_launch_dependents();
   float* part = p.part + (long long)blockIdx.x * p.h;
-  if constexpr (kWarp) {
-    float* mine = sums + warp * p.h;
+  float* mine = part;
+  if (teams > 1) {
+    if constexpr (kRing) {  // (what was copied past the last row is nothing)
+      copy_wait<0>();
+      __syncthreads();
+    }
+    mine = reinterpret_cast<float*>(smem) + team.id * p.h;
+  }
 #pragma unroll
-    for (int k = 0; k < NU; ++k)
+  for (int k = 0; k < NU; ++k)
 #pragma unroll
-      for (int j = 0; j < U; ++j) {
-        const int c = (k * T + tid) * U + j;
-        if (c < p.h) mine[c] = acc[k][j];
-      }
+    for (int j = 0; j < U; ++j) {
+      const int c = (k * T + tid) * U + j;
+      if (c < p.h) mine[c] = acc[k][j];
+    }
+  if (teams > 1) {
     __syncthreads();
+    const float* sums = reinterpret_cast<const float*>(smem);
     for (int c = threadIdx.x; c < p.h; c += blockDim.x) {
-      float v = 0.f;
-      for (int i = 0; i < teams; ++i) v += sums[i * p.h + c];
+      float v = sums[c];
+      for (int i = 1; i < teams; ++i) v += sums[i * p.h + c];
       part[c] = v;
     }
-  } else {
-#pragma unroll
-    for (int k = 0; k < NU; ++k)
-#pragma unroll
-      for (int j = 0; j < U; ++j) {
-        const int c = (k * T + tid) * U + j;
-        if (c < p.h) part[c] = acc[k][j];
-      }
   }
 }
 
 // dw[c] (+)= sum over the partial rows, in a fixed order: kRowLanes threads
-// take every kRowLanes-th row, then one adds their sums in turn.
-__global__ void rmsnorm_weight_kernel(const float* part, int parts, int h, float* dw, int accumulate) {
-  __shared__ float sm[kRowLanes][kColumns];
+// take every kRowLanes-th row, then a warp adds their sums by a tree.
+__global__ void __launch_bounds__(kColumns * kRowLanes) rmsnorm_weight_kernel(const float* part, int parts, int h,
+                                                                            float* dw, int accumulate) {
+  __shared__ float sm[kRowLanes][kColumns + 1];
   grid_dependency_wait();
   const int x = threadIdx.x % kColumns, y = threadIdx.x / kColumns, c = blockIdx.x * kColumns + x;
   float v = 0.f;
   if (c < h) {
-#pragma unroll 4
+#pragma unroll 8
     for (int i = y; i < parts; i += kRowLanes) v += __ldcg(part + (long long)i * h + c);
   }
   sm[y][x] = v;
   __syncthreads();
-  if (y == 0 && c < h) {
-    v = sm[0][x];
+  // warp y holds column y
+  v = sm[x][y];
 #pragma unroll
-    for (int i = 1; i < kRowLanes; ++i) v += sm[i][x];
-    dw[c] = accumulate ? dw[c] + v : v;
+  for (int o = 16; o > 0; o >>= 1) v += __shfl_xor_sync(kFull, v, o);
+  const int col = blockIdx.x * kColumns + y;
+  if (x == 0 && col < h) dw[col] = accumulate ? dw[col] + v : v;
+}
+
+template <typename GT, typename RT, int U, int NU, int kStages, int kMaxT, int kCtas, bool kKeep = true>
+cudaError_t launch(const RmsNormBwdParams& p, int team_threads, int sms, cudaStream_t st, int* parts) {
+  const auto kernel = rmsnorm_backward_kernel<GT, RT, U, NU, kStages, kMaxT, kCtas, kKeep>;
+  const int teams = team_threads < kMaxT ? kMaxT / team_threads : 1, threads = team_threads * teams;
+  constexpr size_t kVecs = NU * (kParts<GT> + 2 * kParts<RT>);
+  static_assert(kStages * kVecs * 16 * kMaxT <= 227 * 1024 - 4096, "the ring and the sums' words fit an SM");
+  size_t smem = kStages * kVecs * 16 * threads;
+  const size_t sums = teams > 1 ? size_t(teams) * p.h * sizeof(float) : 0;
+  if (sums > smem) smem = sums;
+  if (sms == 0) {  // device set-up: room for the ring, and for a row of sums a team
+    const size_t ring = kStages * kVecs * 16 * kMaxT, most = size_t(kMaxT) * NU * U * sizeof(float);
+    return cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, int(ring > most ? ring : most));
   }
-}
-
-template <typename GT, typename RT, int U, int NU, bool kWarp, int kMaxT = 128>
-int launch(const RmsNormBwdParams& p, int threads, int sms, cudaStream_t st) {
-  const int warps = 4, teams = kWarp ? warps : 1;
   const long long rows = (p.s + teams - 1) / teams;
-  const int per_sm = kWarp ? 6 : threads <= 256 ? 4 : threads <= 512 ? 2 : 1;
-  const int most = sms * per_sm < kRmsMaxParts ? sms * per_sm : kRmsMaxParts;
-  const int grid = int(rows < most ? rows : most);
-  const size_t smem = kWarp ? size_t(warps) * p.h * sizeof(float) : 0;
-  rmsnorm_backward_kernel<GT, RT, U, NU, kWarp, kMaxT><<<grid, kWarp ? warps * 32 : threads, smem, st>>>(p);
-  return grid;
+  const int most = sms * kCtas < kRmsMaxParts ? sms * kCtas : kRmsMaxParts;
+  *parts = int(rows < most ? rows : most);
+  kernel<<<*parts, threads, smem, st>>>(p, team_threads);
+  return cudaGetLastError();
 }
 
-template <typename GT, typename RT> int pick(const RmsNormBwdParams& p, bool vectors, int sms, cudaStream_t st) {
+template <typename GT, typename RT>
+cudaError_t pick(const RmsNormBwdParams& p, bool vectors, int sms, cudaStream_t st, int* parts) {
   const int h = p.h;
+  constexpr bool kSmall = sizeof(GT) + 2 * sizeof(RT) <= 6;  // a ring of bf16 rows holds twice as many
+  const auto whole_warps = [](int n) { return (n + 31) / 32 * 32; };
   if (vectors) {
     const int units = h / 8;
-    if (units <= 32) return launch<GT, RT, 8, 1, true>(p, 32, sms, st);
-    if (units <= 128) return launch<GT, RT, 8, 4, true>(p, 32, sms, st);
-    if (units <= 1024) return launch<GT, RT, 8, 2, false, 512>(p, ((units + 1) / 2 + 31) / 32 * 32, sms, st);
-    return launch<GT, RT, 8, 4, false, 1024>(p, ((units + 3) / 4 + 31) / 32 * 32, sms, st);
+    if (units <= 32) return launch<GT, RT, 8, 1, kSmall ? 8 : 4, 512, 1>(p, 32, sms, st, parts);
+    if (units <= 1024)
+      return launch<GT, RT, 8, 2, kSmall ? 4 : 2, 512, 1>(p, whole_warps((units + 1) / 2), sms, st, parts);
+    if (units <= 2048)
+      return launch<GT, RT, 8, 4, kSmall ? 2 : 1, 512, 1, false>(p, whole_warps((units + 3) / 4), sms, st, parts);
+    return launch<GT, RT, 8, 4, kSmall ? 1 : 0, 1024, 1, false>(p, whole_warps((units + 3) / 4), sms, st, parts);
   }
-  if (h <= 256) return launch<GT, RT, 1, 8, true>(p, 32, sms, st);
-  if (h <= 1024) return launch<GT, RT, 1, 32, true>(p, 32, sms, st);
-  return launch<GT, RT, 1, 32, false, 1024>(p, ((h + 31) / 32 + 31) / 32 * 32, sms, st);
+  if (h <= 256) return launch<GT, RT, 1, 8, 0, 512, 2>(p, 32, sms, st, parts);
+  if (h <= 4096) return launch<GT, RT, 1, 8, 0, 512, 2>(p, whole_warps((h + 7) / 8), sms, st, parts);
+  return launch<GT, RT, 1, 32, 0, 1024, 1, false>(p, whole_warps((h + 31) / 32), sms, st, parts);
+}
+
+// one call of each kind of row, with no SMs
+template <typename GT, typename RT> cudaError_t set_up() {
+  RmsNormBwdParams p = {};
+  cudaError_t e = cudaSuccess;
+  for (int h : {256, 4096, 8192, 16384, VPCE_MAX_NORM_COLUMNS}) {
+    p.h = h;
+    for (const bool vectors : {false, true})
+      if (e == cudaSuccess) e = pick<GT, RT>(p, vectors, 0, nullptr, nullptr);
+  }
+  return e;
 }
 
 }  // namespace
+
+cudaError_t set_rmsnorm_smem() {
+  cudaError_t e = set_up<float, float>();
+  if (e == cudaSuccess) e = set_up<__nv_bfloat16, __nv_bfloat16>();
+  return e == cudaSuccess ? set_up<__nv_bfloat16, float>() : e;
+}
 
 size_t rmsnorm_backward_workspace_bytes(long long s, long long h) {
   return round256(size_t(s < kRmsMaxParts ? (s > 0 ? s : 1) : kRmsMaxParts) * size_t(h) * sizeof(float));
@@ -160,11 +304,11 @@ size_t rmsnorm_backward_workspace_bytes(long long s, long long h) {
 cudaError_t launch_rmsnorm_backward(const RmsNormBwdParams& p, bool dy_bf16, bool x_bf16, bool vectors, int sms,
                                     cudaStream_t st) {
   int parts = 0;
+  cudaError_t e = cudaSuccess;
   if (p.s > 0) {
-    parts = !dy_bf16 ? pick<float, float>(p, vectors, sms, st)
-            : x_bf16 ? pick<__nv_bfloat16, __nv_bfloat16>(p, vectors, sms, st)
-                     : pick<__nv_bfloat16, float>(p, vectors, sms, st);
-    const cudaError_t e = cudaGetLastError();
+    e = !dy_bf16 ? pick<float, float>(p, vectors, sms, st, &parts)
+        : x_bf16 ? pick<__nv_bfloat16, __nv_bfloat16>(p, vectors, sms, st, &parts)
+                 : pick<__nv_bfloat16, float>(p, vectors, sms, st, &parts);
     if (e != cudaSuccess) return e;
   }
   // the partial rows are added by a programmatic dependent: its launch is
@@ -178,8 +322,7 @@ cudaError_t launch_rmsnorm_backward(const RmsNormBwdParams& p, bool dy_bf16, boo
   attr[0].val.programmaticStreamSerializationAllowed = 1;
   cfg.attrs = attr;
   cfg.numAttrs = p.s > 0 ? 1 : 0;
-  const cudaError_t e = cudaLaunchKernelEx(&cfg, rmsnorm_weight_kernel, (const float*)p.part, parts, p.h, p.dw,
-                                           p.accumulate);
+  e = cudaLaunchKernelEx(&cfg, rmsnorm_weight_kernel, (const float*)p.part, parts, p.h, p.dw, p.accumulate);
   return e == cudaSuccess ? cudaGetLastError() : e;
 }
 
