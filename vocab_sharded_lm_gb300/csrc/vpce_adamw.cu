@@ -121,6 +121,12 @@ __device__ __forceinline__ void decode4(unsigned c, float (&x)[8], int at) {
   }
 }
 
+__device__ __forceinline__ float approx_rcp(float x) {
+  float y;
+  asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+  return y;
+}
+
 __device__ __forceinline__ float block_scale(unsigned top) {
   const float s = __fmul_rn(__uint_as_float(top), 1.f / 448.f);
   return s < kTiny ? kTiny : s;  // a NaN stays
@@ -134,41 +140,55 @@ __device__ __forceinline__ float quotient(float x, float s, float inv) {
   return __fmaf_rn(__fmaf_rn(-q, s, x), inv, q);
 }
 
-// The e4m3 value that a, 0 <= a <= 448, takes with the random fraction
-// c = (u + 1/2) / 2^16: the neighbour above where c is below a's place between
-// the two, as fl((a - lo) / (hi - lo)) > c says, with a and the neighbours
-// squared for kSquares.  Counted in steps hi - lo, A = a, L = lo: the
-// differences are exact, and so is that of the squares A^2 - L^2 from the
-// rounded A^2; its quotient by 2 L + 1 rounds to more than c, which has 17
-// bits, where it is over c by more than half of c's last place.  (Above 448
-// the conversion saturates; a NaN stays one.)
-template <bool kSquares> __device__ __forceinline__ float round_value(float a, float c) {
-  const unsigned bits = __float_as_uint(a);
-  float A, L;
-  if (a < 0.015625f) {  // e4m3's subnormal values, in steps of 2^-9
-    A = a * 512.f;
-    L = truncf(A);
-  } else {  // a normal one has eight to fifteen steps
-    A = __uint_as_float((bits & 0x7fffffu) | 0x41000000u);
-    L = __uint_as_float(__float_as_uint(A) & 0xfff00000u);
+// Stochastic rounding to e4m3.  A value a takes the e4m3 neighbour above it
+// where c = (u + 1/2) / 2^16, u a random half, is below a's place between its
+// neighbours lo and hi: fl((a - lo) / (hi - lo)) > c, and for kSquares
+// fl((fl(a^2) - lo^2) / (hi^2 - lo^2)) > c.
+//
+// For e4m3's normal values (2^-6 <= |a|, up to 448 or what rounds past it; the
+// conversion saturates) both are decided without a quotient:
+// * the place is the 20 bits of the fp32 word below e4m3's, so adding
+//   2^20 - 1 - 2^20 c to the word carries exactly where it is above c;
+// * counted in steps hi - lo, A = a and L = lo (8 to 15), the squares' test is
+//   fl(A^2) > L^2 + (2 L + 1) c.  The quotient's rounding cannot matter: c has
+//   17 bits, so it would have to lie within (2 L + 1) 2^-25 above the right
+//   side, nearer than the last place (2^-17 or 2^-16) of A^2; and the right
+//   side, of at most 25 bits, is rounded down, which no A^2 lies between.
+// Smaller values and what is not finite take the formulas as they stand.
+struct RoundWord {
+  unsigned carry;  // 2^20 - 1 - 2^20 c
+  float c1;        // 1 + c
+  template <bool kHigh> __device__ __forceinline__ void set(unsigned word) {
+    carry = (~(kHigh ? word >> 12 : word << 4) & 0xffff0u) | 7u;
+    c1 = __uint_as_float(((kHigh ? word >> 9 : word << 7) & 0x7fff80u) | 0x3f800040u);
   }
-  bool up;
-  if constexpr (kSquares) {
-    const float D = fmaf(2.f, L, 1.f), N = __fsub_rn(__fmul_rn(A, A), L * L);
-    up = __fmaf_rn(-D, c, N) > D * __uint_as_float((__float_as_uint(c) & 0x7f800000u) - (24u << 23));
-  } else {
-    up = A - L > c;
-  }
-  if (a < 0.015625f) {
-    L = (L + (up ? 1.f : 0.f)) * 0x1p-9f;
-    return kSquares && a > 0.f ? fmaxf(L, 0x1p-9f) : L;
-  }
-  return __uint_as_float((bits & 0xfff00000u) + (up && a < 480.f ? 0x100000u : 0u));  // (a NaN's bits stay one's)
+};
+
+__device__ __forceinline__ float round_linear(float a, const RoundWord& u) {  // either sign
+  return __uint_as_float((__float_as_uint(a) + u.carry) & 0xfff00000u);
 }
 
-// (u + 1/2) / 2^16 of a word's low or high half
-template <bool kHigh> __device__ __forceinline__ float random_fraction(unsigned word) {
-  return __uint_as_float(((kHigh ? word >> 9 : word << 7) & 0x7fff80u) | 0x3f800040u) - 1.f;
+__device__ __forceinline__ float round_squares(float a, const RoundWord& u) {
+  const unsigned bits = __float_as_uint(a);
+  const float A = __uint_as_float((bits & 0x7fffffu) | 0x41000000u);
+  const float L = __uint_as_float(__float_as_uint(A) & 0xfff00000u), D = fmaf(2.f, L, 1.f);
+  // (L^2 - D) + D (1 + c)
+  const bool up = __fmul_rn(A, A) > __fmaf_rd(D, u.c1, fmaf(L, L, -D));
+  return __uint_as_float((bits & 0xfff00000u) + (up ? 0x100000u : 0u));
+}
+
+// Any value: e4m3's subnormal ones are steps of 2^-9 from 0; a NaN stays one,
+// and for kSquares what is above 0 stays above it.
+template <bool kSquares> __device__ __noinline__ float round_any(float a, RoundWord u) {
+  const float x = fabsf(a), c = u.c1 - 1.f;
+  if (x >= 0.015625f || a != a) {
+    if (a != a || x > 480.f) return a;
+    return kSquares ? round_squares(a, u) : round_linear(a, u);
+  }
+  const float A = x * 512.f, L = truncf(A);
+  const bool up = kSquares ? __fdiv_rn(__fsub_rn(__fmul_rn(A, A), L * L), fmaf(2.f, L, 1.f)) > c : A - L > c;
+  const float r = (L + (up ? 1.f : 0.f)) * 0x1p-9f;
+  return kSquares && x > 0.f ? fmaxf(r, 0x1p-9f) : copysignf(r, a);
 }
 
 // two values that are e4m3 values already (or past 448) as codes
@@ -241,7 +261,7 @@ __global__ void __launch_bounds__(kThreads) adamw_kernel(const __grid_constant__
       xm[j] = __fadd_rn(__fmul_rn(hy.b1, xm[j]), __fmul_rn(hy.a1, gj));
       xv[j] = __fadd_rn(__fmul_rn(hy.b2, xv[j]), __fmul_rn(__fmul_rn(hy.a2, gj), gj));
       const float root = __fsqrt_rn(xv[j]);
-      xp[j] = fmaf(-rate, __fdividef(xm[j], fmaf(root, inv2, hy.eps)), xp[j] * keep);
+      xp[j] = fmaf(-rate, xm[j] * approx_rcp(fmaf(root, inv2, hy.eps)), xp[j] * keep);
       if constexpr (kBits == 8) xv[j] = root;
     }
     store8(p, e, left, vec, xp, PT());
@@ -250,26 +270,41 @@ __global__ void __launch_bounds__(kThreads) adamw_kernel(const __grid_constant__
       store8(m, e, left, vec, xm, 0.f);
       store8(v, e, left, vec, xv, 0.f);
     } else {
-      unsigned tm = 0, tv = 0;
+      unsigned tm = 0, tv = 0, lm = 0x7f800000u, lv = 0x7f800000u;
 #pragma unroll
       for (int j = 0; j < 8; ++j) {
-        tm = max(tm, __float_as_uint(xm[j]) & 0x7fffffffu);
-        tv = max(tv, __float_as_uint(xv[j]) & 0x7fffffffu);
+        const unsigned a = __float_as_uint(xm[j]) & 0x7fffffffu, b = __float_as_uint(xv[j]);
+        tm = max(tm, a), lm = min(lm, a);
+        tv = max(tv, b), lv = min(lv, b);
       }
-      const float sm = block_scale(__reduce_max_sync(kFull, tm)), sv = block_scale(__reduce_max_sync(kFull, tv));
+      tm = __reduce_max_sync(kFull, tm), tv = __reduce_max_sync(kFull, tv);
+      const float sm = block_scale(tm), sv = block_scale(tv);
       const float im = __fdiv_rn(1.f, sm), iv = __fdiv_rn(1.f, sv);
+      const bool normal = __uint_as_float(lm) >= sm * 0x1.1p-6f && __uint_as_float(lv) >= sv * 0x1.1p-6f &&
+                          tm < 0x7f800000u && tv < 0x7f800000u;  // of e4m3, with some room
       const uint4 u = drop_block(key, a.base + i, unsigned(e >> 3));
       const unsigned word[4] = {u.x, u.y, u.z, u.w};
       unsigned cm2[4], cv2[4];
+      // (about one block in 50 of normally distributed gradients has an element
+      // that is not; a ragged block always)
+      if (__all_sync(kFull, normal || left == 0)) {
 #pragma unroll
-      for (int j = 0; j < 8; j += 2) {
-        const float c0 = random_fraction<false>(word[j / 2]), c1 = random_fraction<true>(word[j / 2]);
-        const float m0 = round_value<false>(quotient(fabsf(xm[j]), sm, im), c0);
-        const float m1 = round_value<false>(quotient(fabsf(xm[j + 1]), sm, im), c1);
-        const float v0 = round_value<true>(quotient(xv[j], sv, iv), c0);
-        const float v1 = round_value<true>(quotient(xv[j + 1], sv, iv), c1);
-        cm2[j / 2] = pack_codes(copysignf(m0, xm[j]), copysignf(m1, xm[j + 1]));
-        cv2[j / 2] = pack_codes(v0, v1);
+        for (int j = 0; j < 8; j += 2) {
+          RoundWord u0, u1;
+          u0.set<false>(word[j / 2]);
+          u1.set<true>(word[j / 2]);
+          cm2[j / 2] = pack_codes(round_linear(quotient(xm[j], sm, im), u0), round_linear(quotient(xm[j + 1], sm, im), u1));
+          cv2[j / 2] = pack_codes(round_squares(quotient(xv[j], sv, iv), u0), round_squares(quotient(xv[j + 1], sv, iv), u1));
+        }
+      } else {
+#pragma unroll
+        for (int j = 0; j < 8; j += 2) {
+          RoundWord u0, u1;
+          u0.set<false>(word[j / 2]);
+          u1.set<true>(word[j / 2]);
+          cm2[j / 2] = pack_codes(round_any<false>(quotient(xm[j], sm, im), u0), round_any<false>(quotient(xm[j + 1], sm, im), u1));
+          cv2[j / 2] = pack_codes(round_any<true>(quotient(xv[j], sv, iv), u0), round_any<true>(quotient(xv[j + 1], sv, iv), u1));
+        }
       }
       const uint2 cm = make_uint2(cm2[0] | cm2[1] << 16, cm2[2] | cm2[3] << 16);
       const uint2 cv = make_uint2(cv2[0] | cv2[1] << 16, cv2[2] | cv2[3] << 16);

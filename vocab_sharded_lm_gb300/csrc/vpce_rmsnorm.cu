@@ -31,6 +31,14 @@ __device__ __forceinline__ void store_codes(unsigned char* p, const float (&v)[1
 // a maximum of these bits carries a NaN on.
 __device__ __forceinline__ unsigned mag(float v) { return __float_as_uint(v) & 0x7fffffffu; }
 
+// y / s correctly rounded, for inv = 1 / s (Markstein, "Computation of
+// elementary functions on the IBM RISC System/6000 processor", 1990: one
+// residual step); where s is infinite, y inv.
+__device__ __forceinline__ float quotient(float y, float s, float inv) {
+  const float q = __fmul_rn(y, inv);
+  return __fmaf_rn(__fmaf_rn(-q, s, y), inv, q);
+}
+
 __device__ __forceinline__ float group_scale(unsigned top) {
   const float s = __fmul_rn(__uint_as_float(top), 1.f / 448.f);
   return s < kTiny ? kTiny : s;  // a NaN stays
@@ -42,7 +50,7 @@ __device__ __forceinline__ float group_scale(unsigned top) {
 enum GroupKind { kNoCodes, kLanes, kRow, kShared };
 
 template <typename XT, typename RT, GroupKind kGroups, int U, int NU, bool kWarp, int kMaxT>
-__global__ void __launch_bounds__(kMaxT) rmsnorm_forward_kernel(const __grid_constant__ RmsNormParams p) {
+__global__ void __launch_bounds__(kMaxT, kMaxT == 256 ? 3 : 1) rmsnorm_forward_kernel(const __grid_constant__ RmsNormParams p) {
   extern __shared__ unsigned top_sm[];  // [teams][2][groups], kShared only
   __shared__ float red[2][32];
   [[maybe_unused]] __shared__ unsigned top_row[2][32];
@@ -147,7 +155,7 @@ __global__ void __launch_bounds__(kMaxT) rmsnorm_forward_kernel(const __grid_con
           const float scale = group_scale(kGroups == kShared ? top[g] : m[k]), inv = __fdiv_rn(1.f, scale);
           if (c == g * p.group) p.scale[row * p.groups + g] = scale;
 #pragma unroll
-          for (int j = 0; j < U; ++j) r[k][j] *= inv;
+          for (int j = 0; j < U; ++j) r[k][j] = quotient(r[k][j], isinf(scale) ? 0.f : scale, inv);
           store_codes(p.out + row * p.ld_out + c, r[k]);
         }
       }
@@ -173,6 +181,8 @@ void pick(const RmsNormParams& p, bool vectors, int sms, cudaStream_t st) {
     if (units <= 32) return launch<XT, RT, kGroups, 8, 1, true>(p, 32, sms, st);
     if (units <= 128) return launch<XT, RT, kGroups, 8, 4, true>(p, 32, sms, st);
     const int threads = ((units + 3) / 4 + 31) / 32 * 32;
+    // (at most 85 registers a thread: three CTAs of 256 on an SM)
+    if (threads <= 256) return launch<XT, RT, kGroups, 8, 4, false, 256>(p, threads, sms, st);
     if (threads <= 512) return launch<XT, RT, kGroups, 8, 4, false, 512>(p, threads, sms, st);
     return launch<XT, RT, kGroups, 8, 4, false, 1024>(p, threads, sms, st);
   }

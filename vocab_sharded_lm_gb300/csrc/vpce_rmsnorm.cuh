@@ -58,9 +58,9 @@ template <> struct RawUnit<float, 8> {
     b = p[1];
   }
   // from a thread's own slots in shared memory, `pitch` vectors apart
-  __device__ __forceinline__ void take(const uint4* p, int pitch) {
-    a = p[0];
-    b = p[pitch];
+  __device__ __forceinline__ void take(const unsigned char* p, int pitch) {
+    a = *reinterpret_cast<const uint4*>(p);
+    b = *(reinterpret_cast<const uint4*>(p) + pitch);
   }
   __device__ __forceinline__ void get(float (&v)[8]) const {
     v[0] = __uint_as_float(a.x), v[1] = __uint_as_float(a.y), v[2] = __uint_as_float(a.z), v[3] = __uint_as_float(a.w);
@@ -73,7 +73,7 @@ template <> struct RawUnit<__nv_bfloat16, 8> {
   __device__ __forceinline__ void load(const unsigned char* row, int c) {
     a = *reinterpret_cast<const uint4*>(row + size_t(c) * 2);
   }
-  __device__ __forceinline__ void take(const uint4* p, int) { a = p[0]; }
+  __device__ __forceinline__ void take(const unsigned char* p, int) { a = *reinterpret_cast<const uint4*>(p); }
   __device__ __forceinline__ void get(float (&v)[8]) const { unpack(a, v, __nv_bfloat16()); }
   __device__ __forceinline__ void zero() { a = make_uint4(0, 0, 0, 0); }
 };
@@ -82,6 +82,7 @@ template <> struct RawUnit<float, 1> {
   __device__ __forceinline__ void load(const unsigned char* row, int c) {
     a = *reinterpret_cast<const float*>(row + size_t(c) * 4);
   }
+  __device__ __forceinline__ void take(const unsigned char* p, int) { a = *reinterpret_cast<const float*>(p); }
   __device__ __forceinline__ void get(float (&v)[1]) const { v[0] = a; }
   __device__ __forceinline__ void zero() { a = 0.f; }
 };

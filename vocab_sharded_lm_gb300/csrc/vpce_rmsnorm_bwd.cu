@@ -20,6 +20,9 @@ constexpr int kColumns = 32, kRowLanes = 32;  // of the kernel that adds the par
 __device__ __forceinline__ void copy_async16(uint32_t dst, const void* src) {
   asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(dst), "l"(src) : "memory");
 }
+__device__ __forceinline__ void copy_async4(uint32_t dst, const void* src) {
+  asm volatile("cp.async.ca.shared.global [%0], [%1], 4;" ::"r"(dst), "l"(src) : "memory");
+}
 __device__ __forceinline__ void copy_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
 template <int N> __device__ __forceinline__ void copy_wait() {
   asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
@@ -46,54 +49,69 @@ struct Team {
   }
 };
 
-// Vectors of one row that a thread copies ahead: `16 * kParts` bytes a unit of
-// eight elements.
-template <typename T> constexpr int kParts = sizeof(T) / 2;
+// What a thread copies ahead of a unit: vectors of 16 bytes, or one fp32 word.
+template <typename T, int U> constexpr int kParts = U == 8 ? int(sizeof(T)) / 2 : 1;
+template <int U> constexpr int kSlotBytes = U == 8 ? 16 : 4;
 
 // kStages: rows of the ring ahead (0: none, rows are loaded when they are due).
-// kKeep: a row's values stay in registers until its mean is known; else (four
-// units of vectors, or 32 elements, a thread) they are read a second time, from
-// the ring or through L1.
-template <typename GT, typename RT, int U, int NU, int kStages, int kMaxT, int kCtas, bool kKeep>
+// kT: threads of a team, known when compiled (addresses of single elements are
+// then one register and constants), or 0.  kKeep: products of a row's values
+// stay in registers until its mean is known, and the weights for all rows; else
+// (32 columns a thread) they are read a second time, from the ring or through
+// L1.
+template <typename GT, typename RT, int U, int NU, int kStages, int kMaxT, int kCtas, int kT, bool kKeep>
 __global__ void __launch_bounds__(kMaxT, kCtas) rmsnorm_backward_kernel(const __grid_constant__ RmsNormBwdParams p,
                                                                  int team_threads) {
   extern __shared__ uint4 smem[];  // the ring, and at the end sums [teams][h]
   __shared__ float red[kMaxT / 32][2][32];
   constexpr bool kRing = kStages > 0;
+  const int T = kT > 0 ? kT : team_threads;
   Team team;
-  const int teams = blockDim.x / team_threads;
-  team.id = threadIdx.x / team_threads;
-  team.tid = threadIdx.x - team.id * team_threads;
-  team.threads = team_threads;
+  const int teams = blockDim.x / T;
+  team.id = threadIdx.x / T;
+  team.tid = threadIdx.x - team.id * T;
+  team.threads = T;
   team.red = &red[team.id][0][0];
-  const int T = team_threads, tid = team.tid;
-  float acc[NU][U];
+  const int tid = team.tid;
+  // (units past the row are skipped by all of a team's threads)
+  const auto past = [&](int k) { return U == 1 && k * T >= p.h; };
+  float acc[NU][U], w[kKeep ? NU : 1][U];
 #pragma unroll
-  for (int k = 0; k < NU; ++k)
+  for (int k = 0; k < NU; ++k) {
 #pragma unroll
     for (int j = 0; j < U; ++j) acc[k][j] = 0.f;
+    if constexpr (kKeep) {
+      const int c = (k * T + tid) * U;
+      if (c < p.h) load_weight(p.w, p.w_bf16, c, w[k]);
+    }
+  }
 
-  // ring slot of vector v of a stage: this thread's own 16 bytes
-  constexpr int kVecs = NU * (kParts<GT> + 2 * kParts<RT>);
-  const auto slot = [&](int stage, int v) { return smem + (stage * kVecs + v) * blockDim.x + threadIdx.x; };
+  // ring slot of part v of a stage: this thread's own bytes
+  constexpr int kG = kParts<GT, U>, kR = kParts<RT, U>, kVecs = NU * (kG + 2 * kR), kSlot = kSlotBytes<U>;
+  const auto slot = [&](int stage, int v) {
+    return reinterpret_cast<unsigned char*>(smem) + ((stage * kVecs + v) * int(blockDim.x) + int(threadIdx.x)) * kSlot;
+  };
+  const auto copy = [&](int stage, int v, const unsigned char* src) {
+    if constexpr (U == 8) copy_async16(smem_addr(slot(stage, v)), src);
+    else copy_async4(smem_addr(slot(stage, v)), src);
+  };
   const auto fetch = [&](long long row, int stage) {
     if (row < p.s) {
 #pragma unroll
       for (int k = 0; k < NU; ++k) {
+        if (past(k)) break;
         const int c = (k * T + tid) * U;
         if (c < p.h) {
           const unsigned char *g = p.dy + row * p.ld_dy + size_t(c) * sizeof(GT),
                               *x = p.x + row * p.ld_x + size_t(c) * sizeof(RT);
 #pragma unroll
-          for (int i = 0; i < kParts<GT>; ++i) copy_async16(smem_addr(slot(stage, k * kParts<GT> + i)), g + 16 * i);
+          for (int i = 0; i < kG; ++i) copy(stage, k * kG + i, g + 16 * i);
 #pragma unroll
-          for (int i = 0; i < kParts<RT>; ++i)
-            copy_async16(smem_addr(slot(stage, NU * kParts<GT> + k * kParts<RT> + i)), x + 16 * i);
+          for (int i = 0; i < kR; ++i) copy(stage, NU * kG + k * kR + i, x + 16 * i);
           if (p.dres != nullptr) {
             const unsigned char* d = p.dres + row * p.ld_dres + size_t(c) * sizeof(RT);
 #pragma unroll
-            for (int i = 0; i < kParts<RT>; ++i)
-              copy_async16(smem_addr(slot(stage, NU * (kParts<GT> + kParts<RT>) + k * kParts<RT> + i)), d + 16 * i);
+            for (int i = 0; i < kR; ++i) copy(stage, NU * (kG + kR) + k * kR + i, d + 16 * i);
           }
         }
       }
@@ -107,30 +125,44 @@ __global__ void __launch_bounds__(kMaxT, kCtas) rmsnorm_backward_kernel(const __
     for (int i = 0; i < kStages; ++i) fetch(first + i * stride, i);
   }
   int parity = 0, stage = 0;
+  float next_rstd = first < p.s ? __ldg(p.rstd + first) : 0.f;
   for (long long row = first; row < p.s; row += stride) {
-    const float rstd = __ldg(p.rstd + row);
+    const float rstd = next_rstd;
+    if (row + stride < p.s) next_rstd = __ldg(p.rstd + row + stride);
     const auto load_g = [&](RawUnit<GT, U>& g, int k, int c) {
-      if constexpr (kRing) g.take(slot(stage, k * kParts<GT>), blockDim.x);
+      if constexpr (kRing) g.take(slot(stage, k * kG), blockDim.x);
       else g.load(p.dy + row * p.ld_dy, c);
     };
     const auto load_x = [&](RawUnit<RT, U>& x, int k, int c) {
-      if constexpr (kRing) x.take(slot(stage, NU * kParts<GT> + k * kParts<RT>), blockDim.x);
+      if constexpr (kRing) x.take(slot(stage, NU * kG + k * kR), blockDim.x);
       else x.load(p.x + row * p.ld_x, c);
     };
     const auto load_d = [&](RawUnit<RT, U>& d, int k, int c) {
-      if constexpr (kRing) d.take(slot(stage, NU * (kParts<GT> + kParts<RT>) + k * kParts<RT>), blockDim.x);
+      if constexpr (kRing) d.take(slot(stage, NU * (kG + kR) + k * kR), blockDim.x);
       else d.load(p.dres + row * p.ld_dres, c);
+    };
+    // t = w dy and n = r rstd of a unit
+    const auto terms = [&](int k, int c, const RawUnit<GT, U>& g, const RawUnit<RT, U>& x, float (&dy)[U], float (&t)[U],
+                           float (&n)[U]) {
+      if constexpr (!kKeep) load_weight(p.w, p.w_bf16, c, w[0]);
+      g.get(dy);
+      x.get(n);
+#pragma unroll
+      for (int j = 0; j < U; ++j) {
+        n[j] *= rstd;
+        t[j] = w[kKeep ? k : 0][j] * dy[j];
+      }
     };
     if constexpr (kRing) copy_wait<(kRing ? kStages - 1 : 0)>();
     constexpr int kKept = kKeep ? NU : 1;
     RawUnit<GT, U> g[kKept];
     RawUnit<RT, U> x[kKept], d[kKept];
+    float t[kKept][U], n[kKept][U];
     if constexpr (kKeep) {
 #pragma unroll
       for (int k = 0; k < NU; ++k) {
+        if (past(k)) break;
         const int c = (k * T + tid) * U;
-        g[k].zero();
-        x[k].zero();
         d[k].zero();
         if (c < p.h) {
           load_g(g[k], k, c);
@@ -142,21 +174,19 @@ __global__ void __launch_bounds__(kMaxT, kCtas) rmsnorm_backward_kernel(const __
     float dot = 0.f;
 #pragma unroll
     for (int k = 0; k < NU; ++k) {
+      if (past(k)) break;
       const int c = (k * T + tid) * U, at = kKeep ? k : 0;
       if (c < p.h) {
-        float w[U], dy[U], n[U];
-        load_weight(p.w, p.w_bf16, c, w);
         if constexpr (!kKeep) {
           load_g(g[0], k, c);
           load_x(x[0], k, c);
         }
-        g[at].get(dy);
-        x[at].get(n);
+        float dy[U];
+        terms(k, c, g[at], x[at], dy, t[at], n[at]);
 #pragma unroll
         for (int j = 0; j < U; ++j) {
-          n[j] *= rstd;
-          acc[k][j] = fmaf(dy[j], n[j], acc[k][j]);
-          dot = fmaf(w[j] * dy[j], n[j], dot);
+          acc[k][j] = fmaf(dy[j], n[at][j], acc[k][j]);
+          dot = fmaf(t[at][j], n[at][j], dot);
         }
       }
     }
@@ -165,21 +195,21 @@ __global__ void __launch_bounds__(kMaxT, kCtas) rmsnorm_backward_kernel(const __
     if constexpr (kRing && kKeep) fetch(row + kStages * stride, stage);  // (the stage's values are in registers)
 #pragma unroll
     for (int k = 0; k < NU; ++k) {
+      if (past(k)) break;
       const int c = (k * T + tid) * U, at = kKeep ? k : 0;
       if (c < p.h) {
-        float w[U], dy[U], n[U], o[U];
-        load_weight(p.w, p.w_bf16, c, w);
         if constexpr (!kKeep) {
+          float dy[U];
           load_g(g[0], k, c);
           load_x(x[0], k, c);
           d[0].zero();
           if (p.dres != nullptr) load_d(d[0], k, c);
+          terms(k, c, g[0], x[0], dy, t[0], n[0]);
         }
-        g[at].get(dy);
-        x[at].get(n);
+        float o[U];
         d[at].get(o);
 #pragma unroll
-        for (int j = 0; j < U; ++j) o[j] = fmaf(rstd, w[j] * dy[j] - n[j] * rstd * dot, o[j]);
+        for (int j = 0; j < U; ++j) o[j] = fmaf(rstd, fmaf(-n[at][j], dot, t[at][j]), o[j]);
         store_unit(p.dx + row * p.ld_dx, c, o, RT());
       }
     }
@@ -238,17 +268,17 @@ __global__ void __launch_bounds__(kColumns * kRowLanes) rmsnorm_weight_kernel(co
   if (x == 0 && col < h) dw[col] = accumulate ? dw[col] + v : v;
 }
 
-template <typename GT, typename RT, int U, int NU, int kStages, int kMaxT, int kCtas, bool kKeep = true>
+template <typename GT, typename RT, int U, int NU, int kStages, int kMaxT, int kCtas, int kT, bool kKeep>
 cudaError_t launch(const RmsNormBwdParams& p, int team_threads, int sms, cudaStream_t st, int* parts) {
-  const auto kernel = rmsnorm_backward_kernel<GT, RT, U, NU, kStages, kMaxT, kCtas, kKeep>;
+  const auto kernel = rmsnorm_backward_kernel<GT, RT, U, NU, kStages, kMaxT, kCtas, kT, kKeep>;
   const int teams = team_threads < kMaxT ? kMaxT / team_threads : 1, threads = team_threads * teams;
-  constexpr size_t kVecs = NU * (kParts<GT> + 2 * kParts<RT>);
-  static_assert(kStages * kVecs * 16 * kMaxT <= 227 * 1024 - 4096, "the ring and the sums' words fit an SM");
-  size_t smem = kStages * kVecs * 16 * threads;
+  constexpr size_t kStageBytes = size_t(NU) * (kParts<GT, U> + 2 * kParts<RT, U>)*kSlotBytes<U>;  // of a thread
+  static_assert(kStages * kStageBytes * kMaxT * kCtas <= 227 * 1024 - kCtas * 8192, "the rings fit an SM");
+  size_t smem = kStages * kStageBytes * threads;
   const size_t sums = teams > 1 ? size_t(teams) * p.h * sizeof(float) : 0;
   if (sums > smem) smem = sums;
   if (sms == 0) {  // device set-up: room for the ring, and for a row of sums a team
-    const size_t ring = kStages * kVecs * 16 * kMaxT, most = size_t(kMaxT) * NU * U * sizeof(float);
+    const size_t ring = kStages * kStageBytes * kMaxT, most = size_t(kMaxT) * NU * U * sizeof(float);
     return cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, int(ring > most ? ring : most));
   }
   const long long rows = (p.s + teams - 1) / teams;
@@ -265,23 +295,25 @@ cudaError_t pick(const RmsNormBwdParams& p, bool vectors, int sms, cudaStream_t 
   const auto whole_warps = [](int n) { return (n + 31) / 32 * 32; };
   if (vectors) {
     const int units = h / 8;
-    if (units <= 32) return launch<GT, RT, 8, 1, kSmall ? 8 : 4, 512, 1>(p, 32, sms, st, parts);
+    if (units <= 32) return launch<GT, RT, 8, 1, kSmall ? 8 : 4, 512, 1, 32, true>(p, 32, sms, st, parts);
     if (units <= 1024)
-      return launch<GT, RT, 8, 2, kSmall ? 4 : 2, 512, 1>(p, whole_warps((units + 1) / 2), sms, st, parts);
+      return launch<GT, RT, 8, 2, kSmall ? 4 : 2, 512, 1, 0, true>(p, whole_warps((units + 1) / 2), sms, st, parts);
     if (units <= 2048)
-      return launch<GT, RT, 8, 4, kSmall ? 2 : 1, 512, 1, false>(p, whole_warps((units + 3) / 4), sms, st, parts);
-    return launch<GT, RT, 8, 4, kSmall ? 1 : 0, 1024, 1, false>(p, whole_warps((units + 3) / 4), sms, st, parts);
+      return launch<GT, RT, 8, 4, kSmall ? 2 : 1, 512, 1, 0, false>(p, whole_warps((units + 3) / 4), sms, st, parts);
+    return launch<GT, RT, 8, 4, kSmall ? 1 : 0, 1024, 1, 0, false>(p, whole_warps((units + 3) / 4), sms, st, parts);
   }
-  if (h <= 256) return launch<GT, RT, 1, 8, 0, 512, 2>(p, 32, sms, st, parts);
-  if (h <= 4096) return launch<GT, RT, 1, 8, 0, 512, 2>(p, whole_warps((h + 7) / 8), sms, st, parts);
-  return launch<GT, RT, 1, 32, 0, 1024, 1, false>(p, whole_warps((h + 31) / 32), sms, st, parts);
+  constexpr int kAhead = sizeof(GT) == 4 ? 2 : 0;  // cp.async has no 2-byte form
+  if (h <= 256) return launch<GT, RT, 1, 8, kAhead, 512, 2, 32, true>(p, 32, sms, st, parts);
+  if (h <= 1024) return launch<GT, RT, 1, 8, kAhead, 512, 2, 128, true>(p, 128, sms, st, parts);
+  if (h <= 4096) return launch<GT, RT, 1, 8, kAhead, 512, 2, 512, true>(p, 512, sms, st, parts);
+  return launch<GT, RT, 1, 32, 0, 1024, 1, 0, false>(p, whole_warps((h + 31) / 32), sms, st, parts);
 }
 
 // one call of each kind of row, with no SMs
 template <typename GT, typename RT> cudaError_t set_up() {
   RmsNormBwdParams p = {};
   cudaError_t e = cudaSuccess;
-  for (int h : {256, 4096, 8192, 16384, VPCE_MAX_NORM_COLUMNS}) {
+  for (int h : {256, 1024, 4096, 8192, 16384, VPCE_MAX_NORM_COLUMNS}) {
     p.h = h;
     for (const bool vectors : {false, true})
       if (e == cudaSuccess) e = pick<GT, RT>(p, vectors, 0, nullptr, nullptr);
