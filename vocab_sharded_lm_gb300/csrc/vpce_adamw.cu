@@ -208,19 +208,179 @@ template <int kCap> __device__ __forceinline__ int find_tensor(const AdamArgs<kC
   return lo;
 }
 
+// What one step's arithmetic needs besides the elements.
+struct StepScalars {
+  float gs, b1, a1, b2, a2, rate, inv2, eps, keep;
+};
+
+// p of one element from its new m and v; v becomes its root.
+__device__ __forceinline__ void apply(const StepScalars& c, float& p, float m, float& v) {
+  v = __fsqrt_rn(v);
+  p = fmaf(-c.rate, m * approx_rcp(fmaf(v, c.inv2, c.eps)), p * c.keep);
+}
+
+// m, v and p of eight elements; xv becomes v, or its root for kRoot.  Each
+// operation on m and v is rounded by itself: the states, and so their codes,
+// are those of the formula as it stands, in fp32 on any machine.
+template <bool kRoot>
+__device__ __forceinline__ void update8(const StepScalars& c, float (&xp)[8], const float (&xg)[8], float (&xm)[8],
+                                        float (&xv)[8]) {
+#pragma unroll
+  for (int j = 0; j < 8; ++j) {
+    const float g = __fmul_rn(xg[j], c.gs);
+    xm[j] = __fadd_rn(__fmul_rn(c.b1, xm[j]), __fmul_rn(c.a1, g));
+    xv[j] = __fadd_rn(__fmul_rn(c.b2, xv[j]), __fmul_rn(__fmul_rn(c.a2, g), g));
+    float root = xv[j];
+    apply(c, xp[j], xm[j], root);
+    if constexpr (kRoot) xv[j] = root;
+  }
+}
+
+__device__ __forceinline__ void decode8(uint2 cm, uint2 cv, float sm, float sv, float (&xm)[8], float (&xv)[8]) {
+  decode4(cm.x, xm, 0);
+  decode4(cm.y, xm, 4);
+  decode4(cv.x, xv, 0);
+  decode4(cv.y, xv, 4);
+#pragma unroll
+  for (int j = 0; j < 8; ++j) {
+    xm[j] = __fmul_rn(xm[j], sm);
+    xv[j] = __fmul_rn(xv[j], sv);
+    xv[j] = __fmul_rn(xv[j], xv[j]);
+  }
+}
+
+// New codes and scales of a block of 256 elements, eight a lane: m in xm, the
+// root of v in xv, `inside` false on lanes past the block's end.
+__device__ __forceinline__ void encode8(const float (&xm)[8], const float (&xv)[8], uint4 random, bool inside, uint2& cm,
+                                        uint2& cv, float& sm, float& sv) {
+  unsigned tm = 0, tv = 0, lm = 0x7f800000u, lv = 0x7f800000u;
+#pragma unroll
+  for (int j = 0; j < 8; ++j) {
+    const unsigned a = __float_as_uint(xm[j]) & 0x7fffffffu, b = __float_as_uint(xv[j]);
+    tm = max(tm, a), lm = min(lm, a);
+    tv = max(tv, b), lv = min(lv, b);
+  }
+  tm = __reduce_max_sync(kFull, tm), tv = __reduce_max_sync(kFull, tv);
+  sm = block_scale(tm), sv = block_scale(tv);
+  const float im = __fdiv_rn(1.f, sm), iv = __fdiv_rn(1.f, sv);
+  const bool normal = __uint_as_float(lm) >= sm * 0x1.1p-6f && __uint_as_float(lv) >= sv * 0x1.1p-6f &&
+                      tm < 0x7f800000u && tv < 0x7f800000u;  // of e4m3, with some room
+  const unsigned word[4] = {random.x, random.y, random.z, random.w};
+  unsigned m2[4], v2[4];
+  // (about one block in 50 of normally distributed gradients has an element
+  // that is not; a ragged block always)
+  if (__all_sync(kFull, normal || !inside)) {
+#pragma unroll
+    for (int j = 0; j < 8; j += 2) {
+      RoundWord u0, u1;
+      u0.set<false>(word[j / 2]);
+      u1.set<true>(word[j / 2]);
+      m2[j / 2] = pack_codes(round_linear(quotient(xm[j], sm, im), u0), round_linear(quotient(xm[j + 1], sm, im), u1));
+      v2[j / 2] = pack_codes(round_squares(quotient(xv[j], sv, iv), u0), round_squares(quotient(xv[j + 1], sv, iv), u1));
+    }
+  } else {
+#pragma unroll
+    for (int j = 0; j < 8; j += 2) {
+      RoundWord u0, u1;
+      u0.set<false>(word[j / 2]);
+      u1.set<true>(word[j / 2]);
+      m2[j / 2] = pack_codes(round_any<false>(quotient(xm[j], sm, im), u0), round_any<false>(quotient(xm[j + 1], sm, im), u1));
+      v2[j / 2] = pack_codes(round_any<true>(quotient(xv[j], sv, iv), u0), round_any<true>(quotient(xv[j + 1], sv, iv), u1));
+    }
+  }
+  cm = make_uint2(m2[0] | m2[1] << 16, m2[2] | m2[3] << 16);
+  cv = make_uint2(v2[0] | v2[1] << 16, v2[2] | v2[3] << 16);
+}
+
+// ---------------------------------------------------------------------------
+// The same on pairs of fp32 values (one instruction for two), for blocks whose
+// values are all ordinary: no quotient, no special case, 45 instructions an
+// element instead of 90.  m, v and the codes are the same bits.
+// ---------------------------------------------------------------------------
+__device__ __forceinline__ f32x2 both(float x) { return f2_pack(x, x); }
+__device__ __forceinline__ f32x2 f2_fma_down(f32x2 a, f32x2 b, f32x2 c) {
+  f32x2 d;
+  asm("fma.rm.f32x2 %0, %1, %2, %3;" : "=l"(d) : "l"(a), "l"(b), "l"(c));
+  return d;
+}
+// The sums of two pairs of products, which a packed sum would fuse with one of
+// them (measured: the packed forms are contracted where the single ones, with
+// their rounding named, are not).
+__device__ __forceinline__ f32x2 sum2(f32x2 a, f32x2 b) {
+  float a0, a1, b0, b1;
+  f2_unpack(a, a0, a1);
+  f2_unpack(b, b0, b1);
+  return f2_pack(__fadd_rn(a0, b0), __fadd_rn(a1, b1));
+}
+__device__ __forceinline__ f32x2 f2_neg(f32x2 a) { return a ^ 0x8000000080000000ull; }
+
+struct StepPairs {
+  f32x2 gs, b1, a1, b2, a2, rate, inv2, eps, keep;
+  __device__ __forceinline__ explicit StepPairs(const StepScalars& c)
+      : gs(both(c.gs)), b1(both(c.b1)), a1(both(c.a1)), b2(both(c.b2)), a2(both(c.a2)), rate(both(-c.rate)),
+        inv2(both(c.inv2)), eps(both(c.eps)), keep(both(c.keep)) {}
+};
+
+// Root of v, 2^-100 <= v < 2^127, correctly rounded: the residual step of
+// Markstein's paper above on v rsqrt(v).
+__device__ __forceinline__ f32x2 root2(f32x2 v) {
+  float a, b, ya, yb;
+  f2_unpack(v, a, b);
+  asm("rsqrt.approx.ftz.f32 %0, %1;" : "=f"(ya) : "f"(a));
+  asm("rsqrt.approx.ftz.f32 %0, %1;" : "=f"(yb) : "f"(b));
+  const f32x2 y = f2_pack(ya, yb), r = f2_mul(v, y), h = f2_mul(y, both(0.5f));
+  return f2_fma(f2_fma(f2_neg(r), r, v), h, r);
+}
+
+__device__ __forceinline__ f32x2 quotient2(f32x2 x, f32x2 minus_s, f32x2 inv) {
+  const f32x2 q = f2_mul(x, inv);
+  return f2_fma(f2_fma(q, minus_s, x), inv, q);
+}
+
+// round_linear and round_squares of two values
+__device__ __forceinline__ unsigned linear_codes2(f32x2 a, const RoundWord& u0, const RoundWord& u1) {
+  float x, y;
+  f2_unpack(a, x, y);
+  return pack_codes(round_linear(x, u0), round_linear(y, u1));
+}
+__device__ __forceinline__ unsigned square_codes2(f32x2 a, const RoundWord& u0, const RoundWord& u1) {
+  float x, y, ax, ay, tx, ty;
+  f2_unpack(a, x, y);
+  const unsigned bx = __float_as_uint(x), by = __float_as_uint(y);
+  const unsigned Ax = (bx & 0x7fffffu) | 0x41000000u, Ay = (by & 0x7fffffu) | 0x41000000u;
+  const f32x2 A = f2_pack(__uint_as_float(Ax), __uint_as_float(Ay));
+  const f32x2 L = f2_pack(__uint_as_float(Ax & 0xfff00000u), __uint_as_float(Ay & 0xfff00000u));
+  const f32x2 D = f2_fma(L, both(2.f), both(1.f));
+  f2_unpack(f2_mul(A, A), ax, ay);
+  f2_unpack(f2_fma_down(D, f2_pack(u0.c1, u1.c1), f2_fma(L, L, f2_neg(D))), tx, ty);
+  return pack_codes(__uint_as_float((bx & 0xfff00000u) + (ax > tx ? 0x100000u : 0u)),
+                    __uint_as_float((by & 0xfff00000u) + (ay > ty ? 0x100000u : 0u)));
+}
+
+// One element type's part of the ring: eight elements a thread, in one or two
+// vectors of shared memory kThreads apart.
+template <typename T> struct Ahead {
+  uint4 v[sizeof(T) / 2][kThreads];
+  __device__ __forceinline__ void copy(const unsigned char* src) {
+    copy_async<16, sizeof(T) == 4>(&v[0][threadIdx.x], src);  // (two vectors share sectors: through L1)
+    if constexpr (sizeof(T) == 4) copy_async<16, true>(&v[1][threadIdx.x], src + 16);
+  }
+  __device__ __forceinline__ void get(float (&x)[8]) const {
+    if constexpr (sizeof(T) == 2) {
+      unpack(v[0][threadIdx.x], x, T());
+    } else {
+      const float4 a = *reinterpret_cast<const float4*>(&v[0][threadIdx.x]),
+                   b = *reinterpret_cast<const float4*>(&v[1][threadIdx.x]);
+      x[0] = a.x, x[1] = a.y, x[2] = a.z, x[3] = a.w, x[4] = b.x, x[5] = b.y, x[6] = b.z, x[7] = b.w;
+    }
+  }
+};
+
 template <typename PT, typename GT, int kBits, int kCap>
-__global__ void __launch_bounds__(kThreads) adamw_kernel(const __grid_constant__ AdamArgs<kCap> a) {
+__global__ void __launch_bounds__(kThreads, 3) adamw_kernel(const __grid_constant__ AdamArgs<kCap> a) {
   const AdamHyper& hy = a.hy;
-  const float gs = hy.grad_scale != nullptr ? __ldg(hy.grad_scale) : 1.f;
-  if (gs == 0.f) return;  // the step is skipped
   const int i = find_tensor(a, blockIdx.x);
   const AdamTensor& t = a.t[i];
-  const float lr = hy.lr_dev != nullptr ? __ldg(hy.lr_dev) : hy.lr;
-  const long long step = __ldg(hy.step);
-  const float ft = float(step > 1 ? step : 1);
-  // 1 - beta^t without cancellation
-  const float rate = lr / -expm1f(ft * hy.ln_b1), inv2 = rsqrtf(-expm1f(ft * hy.ln_b2));
-  const float keep = 1.f - lr * t.wd;
   unsigned char *const p = t.p, *const m = t.m, *const v = t.v, *const copy = t.copy;
   const unsigned char* const g = t.g;
   const long long n = t.n, e0 = (long long)(blockIdx.x - t.run0) * a.run;
@@ -228,10 +388,148 @@ __global__ void __launch_bounds__(kThreads) adamw_kernel(const __grid_constant__
   const uintptr_t where = uintptr_t(p) | uintptr_t(g) | uintptr_t(copy);
   const bool vec = kBits == 32 ? ((where | uintptr_t(m) | uintptr_t(v)) & 15) == 0
                                : (where & 15) == 0 && ((uintptr_t(m) | uintptr_t(v)) & 7) == 0;
-  DropKey key;
+  // Whole runs of 8-bit states in vectors come through a ring of two turns that
+  // each thread fills for itself, the first of them before anything else is
+  // read: the codes' arithmetic takes half of the SM's issue slots, so loads
+  // have to be under way meanwhile.
+  constexpr bool kRing = kBits == 8;
+  __shared__ Ahead<PT> rp[kRing ? 2 : 1];
+  __shared__ Ahead<GT> rg[kRing ? 2 : 1];
+  __shared__ uint2 rm[kRing ? 2 : 1][kThreads], rv[kRing ? 2 : 1][kThreads];
+  const auto fetch = [&](long long at, int stage) {
+    rp[stage].copy(p + at * sizeof(PT));
+    rg[stage].copy(g + at * sizeof(GT));
+    copy_async<8>(&rm[stage][threadIdx.x], m + at);
+    copy_async<8>(&rv[stage][threadIdx.x], v + at);
+  };
+  const bool ring = kRing && vec && e1 - e0 == a.run;
+  const int turns = a.run / kTile;
+  long long e = e0 + (long long)threadIdx.x * kPer;
+  float sm = 0.f, sv = 0.f;
+  if (ring) {
+    fetch(e, 0);
+    copy_commit();
+    if (turns > 1) fetch(e + kTile, 1);
+    copy_commit();
+    sm = t.ms[e / kAdamBlock], sv = t.vs[e / kAdamBlock];
+  }
+  const float gs = hy.grad_scale != nullptr ? __ldg(hy.grad_scale) : 1.f;
+  const float lr = hy.lr_dev != nullptr ? __ldg(hy.lr_dev) : hy.lr;
+  const long long step = __ldg(hy.step);
+  [[maybe_unused]] DropKey key;
   if constexpr (kBits == 8) key.set(hy.rng);
+  if (gs == 0.f) {  // the step is skipped
+    copy_wait<0>();
+    return;
+  }
+  const float ft = float(step > 1 ? step : 1);
+  // 1 - beta^t without cancellation
+  const StepScalars c = {gs, hy.b1, hy.a1, hy.b2, hy.a2, lr / -expm1f(ft * hy.ln_b1), rsqrtf(-expm1f(ft * hy.ln_b2)),
+                         hy.eps, 1.f - lr * t.wd};
+
+  if constexpr (kRing) {
+    if (ring) {
+      const StepPairs c2(c);
+      for (int turn = 0; turn < turns; ++turn, e += kTile) {
+        const int stage = turn & 1;
+        float next_sm = 0.f, next_sv = 0.f;
+        if (turn + 1 < turns) {
+          next_sm = t.ms[(e + kTile) / kAdamBlock];
+          next_sv = t.vs[(e + kTile) / kAdamBlock];
+        }
+        const uint4 random = drop_block(key, a.base + i, unsigned(e >> 3));
+        copy_wait<1>();
+        f32x2 xp[4], xm[4], xv[4];
+        {
+          float p8[8], g8[8], m8[8], v8[8];
+          rp[stage].get(p8);
+          rg[stage].get(g8);
+          const uint2 cm = rm[stage][threadIdx.x], cv = rv[stage][threadIdx.x];
+          decode4(cm.x, m8, 0);
+          decode4(cm.y, m8, 4);
+          decode4(cv.x, v8, 0);
+          decode4(cv.y, v8, 4);
+          const f32x2 sm2 = both(sm), sv2 = both(sv);
+#pragma unroll
+          for (int j = 0; j < 4; ++j) {
+            const f32x2 g = f2_mul(f2_pack(g8[2 * j], g8[2 * j + 1]), c2.gs);
+            const f32x2 m0 = f2_mul(f2_pack(m8[2 * j], m8[2 * j + 1]), sm2);
+            f32x2 v0 = f2_mul(f2_pack(v8[2 * j], v8[2 * j + 1]), sv2);
+            v0 = f2_mul(v0, v0);
+            xm[j] = sum2(f2_mul(c2.b1, m0), f2_mul(c2.a1, g));
+            xv[j] = sum2(f2_mul(c2.b2, v0), f2_mul(f2_mul(c2.a2, g), g));
+            xp[j] = f2_pack(p8[2 * j], p8[2 * j + 1]);
+          }
+        }
+        if (turn + 2 < turns) fetch(e + 2 * kTile, stage);  // (the stage's values are in registers)
+        copy_commit();
+        float m8[8], v8[8], p8[8];
+        unsigned tm = 0, tv = 0, lm = 0x7f800000u, lv = 0x7f800000u;
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+          f2_unpack(xm[j], m8[2 * j], m8[2 * j + 1]);
+          f2_unpack(xv[j], v8[2 * j], v8[2 * j + 1]);
+        }
+#pragma unroll
+        for (int j = 0; j < 8; ++j) {
+          const unsigned x = __float_as_uint(m8[j]) & 0x7fffffffu, y = __float_as_uint(v8[j]);
+          tm = max(tm, x), lm = min(lm, x);
+          tv = max(tv, y), lv = min(lv, y);
+        }
+        tm = __reduce_max_sync(kFull, tm), tv = __reduce_max_sync(kFull, tv);
+        // (the root is monotone: the largest v's is the largest)
+        sm = block_scale(tm), sv = block_scale(__float_as_uint(__fsqrt_rn(__uint_as_float(tv))));
+        // of e4m3's normal values, with some room, and of root2's range
+        // (2.4e-4 > (2^-6)^2: v is compared with the scale's square)
+        const bool ordinary = __uint_as_float(lm) >= sm * 0x1.1p-6f && __uint_as_float(lv) >= sv * sv * 2.8e-4f &&
+                              lv >= 0x0d800000u && tm < 0x7f800000u && tv < 0x7f000000u;
+        uint2 cm, cv;
+        // (about one block in 50 of normally distributed gradients has an
+        // element that is not)
+        if (__all_sync(kFull, ordinary)) {
+          const float im = __fdiv_rn(1.f, sm), iv = __fdiv_rn(1.f, sv);
+          const f32x2 im2 = both(im), iv2 = both(iv), nsm = both(-sm), nsv = both(-sv);
+          const unsigned word[4] = {random.x, random.y, random.z, random.w};
+          unsigned mc[4], vc[4];
+#pragma unroll
+          for (int j = 0; j < 4; ++j) {
+            const f32x2 root = root2(xv[j]);
+            float d0, d1;
+            f2_unpack(f2_fma(root, c2.inv2, c2.eps), d0, d1);
+            xp[j] = f2_fma(c2.rate, f2_mul(xm[j], f2_pack(approx_rcp(d0), approx_rcp(d1))), f2_mul(xp[j], c2.keep));
+            RoundWord u0, u1;
+            u0.set<false>(word[j]);
+            u1.set<true>(word[j]);
+            mc[j] = linear_codes2(quotient2(xm[j], nsm, im2), u0, u1);
+            vc[j] = square_codes2(quotient2(root, nsv, iv2), u0, u1);
+          }
+          cm = make_uint2(mc[0] | mc[1] << 16, mc[2] | mc[3] << 16);
+          cv = make_uint2(vc[0] | vc[1] << 16, vc[2] | vc[3] << 16);
+#pragma unroll
+          for (int j = 0; j < 4; ++j) f2_unpack(xp[j], p8[2 * j], p8[2 * j + 1]);
+        } else {
+#pragma unroll
+          for (int j = 0; j < 4; ++j) f2_unpack(xp[j], p8[2 * j], p8[2 * j + 1]);
+#pragma unroll
+          for (int j = 0; j < 8; ++j) apply(c, p8[j], m8[j], v8[j]);
+          encode8(m8, v8, random, true, cm, cv, sm, sv);
+        }
+        store8(p, e, 8, true, p8, PT());
+        if (copy != nullptr) store8(copy, e, 8, true, p8, __nv_bfloat16());
+        *reinterpret_cast<uint2*>(m + e) = cm;
+        *reinterpret_cast<uint2*>(v + e) = cv;
+        if ((threadIdx.x & 31) == 0) {
+          t.ms[e / kAdamBlock] = sm;
+          t.vs[e / kAdamBlock] = sv;
+        }
+        sm = next_sm;
+        sv = next_sv;
+      }
+      return;
+    }
+  }
   // (8-bit states: a warp's 32 threads hold one block of 256 elements)
-  for (long long e = e0 + (long long)threadIdx.x * kPer; e - (threadIdx.x & 31) * kPer < e1; e += kTile) {
+  for (; e - (threadIdx.x & 31) * kPer < e1; e += kTile) {
     const int left = e1 > e ? int(e1 - e < kPer ? e1 - e : kPer) : 0;
     float xp[8], xg[8], xm[8], xv[8];
     load8(p, e, left, vec, xp, PT());
@@ -239,30 +537,11 @@ __global__ void __launch_bounds__(kThreads) adamw_kernel(const __grid_constant__
     if constexpr (kBits == 32) {
       load8(m, e, left, vec, xm, 0.f);
       load8(v, e, left, vec, xv, 0.f);
+      update8<false>(c, xp, xg, xm, xv);
     } else {
       const uint2 cm = load_codes(m + e, left, vec), cv = load_codes(v + e, left, vec);
-      const float sm = t.ms[e / kAdamBlock], sv = t.vs[e / kAdamBlock];
-      decode4(cm.x, xm, 0);
-      decode4(cm.y, xm, 4);
-      decode4(cv.x, xv, 0);
-      decode4(cv.y, xv, 4);
-#pragma unroll
-      for (int j = 0; j < 8; ++j) {
-        xm[j] = __fmul_rn(xm[j], sm);
-        xv[j] = __fmul_rn(xv[j], sv);
-        xv[j] = __fmul_rn(xv[j], xv[j]);
-      }
-    }
-#pragma unroll
-    for (int j = 0; j < 8; ++j) {
-      // each operation rounded by itself: the states, and so their codes, are
-      // those of the formula as it stands, in fp32 on any machine
-      const float gj = __fmul_rn(xg[j], gs);
-      xm[j] = __fadd_rn(__fmul_rn(hy.b1, xm[j]), __fmul_rn(hy.a1, gj));
-      xv[j] = __fadd_rn(__fmul_rn(hy.b2, xv[j]), __fmul_rn(__fmul_rn(hy.a2, gj), gj));
-      const float root = __fsqrt_rn(xv[j]);
-      xp[j] = fmaf(-rate, xm[j] * approx_rcp(fmaf(root, inv2, hy.eps)), xp[j] * keep);
-      if constexpr (kBits == 8) xv[j] = root;
+      decode8(cm, cv, t.ms[e / kAdamBlock], t.vs[e / kAdamBlock], xm, xv);
+      update8<true>(c, xp, xg, xm, xv);
     }
     store8(p, e, left, vec, xp, PT());
     if (copy != nullptr) store8(copy, e, left, vec, xp, __nv_bfloat16());
@@ -270,44 +549,8 @@ __global__ void __launch_bounds__(kThreads) adamw_kernel(const __grid_constant__
       store8(m, e, left, vec, xm, 0.f);
       store8(v, e, left, vec, xv, 0.f);
     } else {
-      unsigned tm = 0, tv = 0, lm = 0x7f800000u, lv = 0x7f800000u;
-#pragma unroll
-      for (int j = 0; j < 8; ++j) {
-        const unsigned a = __float_as_uint(xm[j]) & 0x7fffffffu, b = __float_as_uint(xv[j]);
-        tm = max(tm, a), lm = min(lm, a);
-        tv = max(tv, b), lv = min(lv, b);
-      }
-      tm = __reduce_max_sync(kFull, tm), tv = __reduce_max_sync(kFull, tv);
-      const float sm = block_scale(tm), sv = block_scale(tv);
-      const float im = __fdiv_rn(1.f, sm), iv = __fdiv_rn(1.f, sv);
-      const bool normal = __uint_as_float(lm) >= sm * 0x1.1p-6f && __uint_as_float(lv) >= sv * 0x1.1p-6f &&
-                          tm < 0x7f800000u && tv < 0x7f800000u;  // of e4m3, with some room
-      const uint4 u = drop_block(key, a.base + i, unsigned(e >> 3));
-      const unsigned word[4] = {u.x, u.y, u.z, u.w};
-      unsigned cm2[4], cv2[4];
-      // (about one block in 50 of normally distributed gradients has an element
-      // that is not; a ragged block always)
-      if (__all_sync(kFull, normal || left == 0)) {
-#pragma unroll
-        for (int j = 0; j < 8; j += 2) {
-          RoundWord u0, u1;
-          u0.set<false>(word[j / 2]);
-          u1.set<true>(word[j / 2]);
-          cm2[j / 2] = pack_codes(round_linear(quotient(xm[j], sm, im), u0), round_linear(quotient(xm[j + 1], sm, im), u1));
-          cv2[j / 2] = pack_codes(round_squares(quotient(xv[j], sv, iv), u0), round_squares(quotient(xv[j + 1], sv, iv), u1));
-        }
-      } else {
-#pragma unroll
-        for (int j = 0; j < 8; j += 2) {
-          RoundWord u0, u1;
-          u0.set<false>(word[j / 2]);
-          u1.set<true>(word[j / 2]);
-          cm2[j / 2] = pack_codes(round_any<false>(quotient(xm[j], sm, im), u0), round_any<false>(quotient(xm[j + 1], sm, im), u1));
-          cv2[j / 2] = pack_codes(round_any<true>(quotient(xv[j], sv, iv), u0), round_any<true>(quotient(xv[j + 1], sv, iv), u1));
-        }
-      }
-      const uint2 cm = make_uint2(cm2[0] | cm2[1] << 16, cm2[2] | cm2[3] << 16);
-      const uint2 cv = make_uint2(cv2[0] | cv2[1] << 16, cv2[2] | cv2[3] << 16);
+      uint2 cm, cv;
+      encode8(xm, xv, drop_block(key, a.base + i, unsigned(e >> 3)), left > 0, cm, cv, sm, sv);
       store_codes(m + e, left, vec, cm);
       store_codes(v + e, left, vec, cv);
       if ((threadIdx.x & 31) == 0) {
@@ -414,7 +657,7 @@ void step_launch(const vpce_adamw_tensor* tensors, long long first, long long co
   // a run: long enough to spread a CTA's start over several turns, short
   // enough that every SM has some
   long long turns = total / ((long long)kTile * sms * 8);
-  turns = turns < 1 ? 1 : turns > 8 ? 8 : turns;
+  turns = turns < 1 ? 1 : turns > 16 ? 16 : turns;
   a.run = int(turns) * kTile;
   long long runs = 0;
   for (long long i = 0; i < count; ++i) {

@@ -186,6 +186,21 @@ __device__ __forceinline__ void bulk_store(void* dst, const void* src_smem, uint
 
 __device__ __forceinline__ void bulk_commit() { asm volatile("cp.async.bulk.commit_group;" ::: "memory"); }
 
+// global -> shared copies of 4, 8 or 16 bytes that every thread makes for
+// itself (cp.async).  kThroughL1: also for 16 bytes (the others always do).
+template <int kBytes, bool kThroughL1 = kBytes != 16>
+__device__ __forceinline__ void copy_async(void* dst_smem, const void* src) {
+  if constexpr (kThroughL1)
+    asm volatile("cp.async.ca.shared.global [%0], [%1], %2;" ::"r"(smem_addr(dst_smem)), "l"(src), "n"(kBytes) : "memory");
+  else
+    asm volatile("cp.async.cg.shared.global [%0], [%1], %2;" ::"r"(smem_addr(dst_smem)), "l"(src), "n"(kBytes) : "memory");
+}
+__device__ __forceinline__ void copy_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
+// Wait until at most N of this thread's groups of them are incomplete.
+template <int N> __device__ __forceinline__ void copy_wait() {
+  asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
+}
+
 // Wait until at most N of this thread's bulk groups still read shared memory.
 template <int N>
 __device__ __forceinline__ void bulk_wait_read() {

@@ -10,23 +10,14 @@
 // memory that every thread fills for itself (cp.async: each reads only what it
 // copied, so no barrier goes with it), a few rows deep.  Rows off 16 bytes are
 // read element by element by smaller teams, several in a CTA.
+#include <type_traits>
+
 #include "vpce_rmsnorm.cuh"
 
 namespace vpce {
 namespace {
 
 constexpr int kColumns = 32, kRowLanes = 32;  // of the kernel that adds the partial rows
-
-__device__ __forceinline__ void copy_async16(uint32_t dst, const void* src) {
-  asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(dst), "l"(src) : "memory");
-}
-__device__ __forceinline__ void copy_async4(uint32_t dst, const void* src) {
-  asm volatile("cp.async.ca.shared.global [%0], [%1], 4;" ::"r"(dst), "l"(src) : "memory");
-}
-__device__ __forceinline__ void copy_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
-template <int N> __device__ __forceinline__ void copy_wait() {
-  asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
-}
 
 // The threads of one team: whole warps, with a barrier of their own (not 0,
 // which is the CTA's).
@@ -91,10 +82,14 @@ __global__ void __launch_bounds__(kMaxT, kCtas) rmsnorm_backward_kernel(const __
   const auto slot = [&](int stage, int v) {
     return reinterpret_cast<unsigned char*>(smem) + ((stage * kVecs + v) * int(blockDim.x) + int(threadIdx.x)) * kSlot;
   };
-  const auto copy = [&](int stage, int v, const unsigned char* src) {
-    if constexpr (U == 8) copy_async16(smem_addr(slot(stage, v)), src);
-    else copy_async4(smem_addr(slot(stage, v)), src);
+  // (the two vectors of eight fp32 values share sectors with each other: those go through L1)
+  const auto copy = [&](int stage, int v, const unsigned char* src, auto fp32) {
+    if constexpr (U == 1) copy_async<4>(slot(stage, v), src);
+    else if constexpr (fp32) copy_async<16, true>(slot(stage, v), src);
+    else copy_async<16>(slot(stage, v), src);
   };
+  constexpr std::bool_constant<sizeof(GT) == 4> g32{};
+  constexpr std::bool_constant<sizeof(RT) == 4> r32{};
   const auto fetch = [&](long long row, int stage) {
     if (row < p.s) {
 #pragma unroll
@@ -105,13 +100,13 @@ __global__ void __launch_bounds__(kMaxT, kCtas) rmsnorm_backward_kernel(const __
           const unsigned char *g = p.dy + row * p.ld_dy + size_t(c) * sizeof(GT),
                               *x = p.x + row * p.ld_x + size_t(c) * sizeof(RT);
 #pragma unroll
-          for (int i = 0; i < kG; ++i) copy(stage, k * kG + i, g + 16 * i);
+          for (int i = 0; i < kG; ++i) copy(stage, k * kG + i, g + 16 * i, g32);
 #pragma unroll
-          for (int i = 0; i < kR; ++i) copy(stage, NU * kG + k * kR + i, x + 16 * i);
+          for (int i = 0; i < kR; ++i) copy(stage, NU * kG + k * kR + i, x + 16 * i, r32);
           if (p.dres != nullptr) {
             const unsigned char* d = p.dres + row * p.ld_dres + size_t(c) * sizeof(RT);
 #pragma unroll
-            for (int i = 0; i < kR; ++i) copy(stage, NU * (kG + kR) + k * kR + i, d + 16 * i);
+            for (int i = 0; i < kR; ++i) copy(stage, NU * (kG + kR) + k * kR + i, d + 16 * i, r32);
           }
         }
       }
