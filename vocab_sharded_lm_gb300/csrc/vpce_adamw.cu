@@ -148,7 +148,8 @@ __device__ __forceinline__ float quotient(float x, float s, float inv) {
 // For e4m3's normal values (2^-6 <= |a|, up to 448 or what rounds past it; the
 // conversion saturates) both are decided without a quotient:
 // * the place is the 20 bits of the fp32 word below e4m3's, so adding
-//   2^20 - 1 - 2^20 c to the word carries exactly where it is above c;
+//   2^20 - 1 - 2^20 c to the word carries exactly where it is above c (c1 >> 3
+//   is 2^20 c + 0x17f00000);
 // * counted in steps hi - lo, A = a and L = lo (8 to 15), the squares' test is
 //   fl(A^2) > L^2 + (2 L + 1) c.  The quotient's rounding cannot matter: c has
 //   17 bits, so it would have to lie within (2 L + 1) 2^-25 above the right
@@ -156,31 +157,31 @@ __device__ __forceinline__ float quotient(float x, float s, float inv) {
 //   side, of at most 25 bits, is rounded down, which no A^2 lies between.
 // Smaller values and what is not finite take the formulas as they stand.
 struct RoundWord {
-  unsigned carry;  // 2^20 - 1 - 2^20 c
-  float c1;        // 1 + c
+  unsigned c1;  // bits of -(1 + c)
   template <bool kHigh> __device__ __forceinline__ void set(unsigned word) {
-    carry = (~(kHigh ? word >> 12 : word << 4) & 0xffff0u) | 7u;
-    c1 = __uint_as_float(((kHigh ? word >> 9 : word << 7) & 0x7fff80u) | 0x3f800040u);
+    c1 = ((kHigh ? word >> 9 : word << 7) & 0x7fff80u) | 0xbf800040u;
   }
+  __device__ __forceinline__ float minus() const { return __uint_as_float(c1); }
 };
 
 __device__ __forceinline__ float round_linear(float a, const RoundWord& u) {  // either sign
-  return __uint_as_float((__float_as_uint(a) + u.carry) & 0xfff00000u);
+  // (2^20 c is c1's mantissa, an eighth of it)
+  return __uint_as_float((__float_as_uint(a) + 0x17ffffffu - (u.c1 >> 3)) & 0xfff00000u);
 }
 
 __device__ __forceinline__ float round_squares(float a, const RoundWord& u) {
   const unsigned bits = __float_as_uint(a);
   const float A = __uint_as_float((bits & 0x7fffffu) | 0x41000000u);
-  const float L = __uint_as_float(__float_as_uint(A) & 0xfff00000u), D = fmaf(2.f, L, 1.f);
-  // (L^2 - D) + D (1 + c)
-  const bool up = __fmul_rn(A, A) > __fmaf_rd(D, u.c1, fmaf(L, L, -D));
+  const float L = __uint_as_float(__float_as_uint(A) & 0xfff00000u), minus_d = fmaf(-2.f, L, -1.f);
+  // (L^2 - D) + D (1 + c), D = 2 L + 1
+  const bool up = __fmul_rn(A, A) > __fmaf_rd(minus_d, u.minus(), fmaf(L, L, minus_d));
   return __uint_as_float((bits & 0xfff00000u) + (up ? 0x100000u : 0u));
 }
 
 // Any value: e4m3's subnormal ones are steps of 2^-9 from 0; a NaN stays one,
 // and for kSquares what is above 0 stays above it.
 template <bool kSquares> __device__ __noinline__ float round_any(float a, RoundWord u) {
-  const float x = fabsf(a), c = u.c1 - 1.f;
+  const float x = fabsf(a), c = -u.minus() - 1.f;
   if (x >= 0.015625f || a != a) {
     if (a != a || x > 480.f) return a;
     return kSquares ? round_squares(a, u) : round_linear(a, u);
@@ -312,7 +313,6 @@ __device__ __forceinline__ f32x2 sum2(f32x2 a, f32x2 b) {
   f2_unpack(b, b0, b1);
   return f2_pack(__fadd_rn(a0, b0), __fadd_rn(a1, b1));
 }
-__device__ __forceinline__ f32x2 f2_neg(f32x2 a) { return a ^ 0x8000000080000000ull; }
 
 struct StepPairs {
   f32x2 gs, b1, a1, b2, a2, rate, inv2, eps, keep;
@@ -329,7 +329,7 @@ __device__ __forceinline__ f32x2 root2(f32x2 v) {
   asm("rsqrt.approx.ftz.f32 %0, %1;" : "=f"(ya) : "f"(a));
   asm("rsqrt.approx.ftz.f32 %0, %1;" : "=f"(yb) : "f"(b));
   const f32x2 y = f2_pack(ya, yb), r = f2_mul(v, y), h = f2_mul(y, both(0.5f));
-  return f2_fma(f2_fma(f2_neg(r), r, v), h, r);
+  return f2_fma(f2_fma(f2_mul(r, both(-1.f)), r, v), h, r);
 }
 
 __device__ __forceinline__ f32x2 quotient2(f32x2 x, f32x2 minus_s, f32x2 inv) {
@@ -350,11 +350,29 @@ __device__ __forceinline__ unsigned square_codes2(f32x2 a, const RoundWord& u0, 
   const unsigned Ax = (bx & 0x7fffffu) | 0x41000000u, Ay = (by & 0x7fffffu) | 0x41000000u;
   const f32x2 A = f2_pack(__uint_as_float(Ax), __uint_as_float(Ay));
   const f32x2 L = f2_pack(__uint_as_float(Ax & 0xfff00000u), __uint_as_float(Ay & 0xfff00000u));
-  const f32x2 D = f2_fma(L, both(2.f), both(1.f));
+  const f32x2 minus_d = f2_fma(L, both(-2.f), both(-1.f));
   f2_unpack(f2_mul(A, A), ax, ay);
-  f2_unpack(f2_fma_down(D, f2_pack(u0.c1, u1.c1), f2_fma(L, L, f2_neg(D))), tx, ty);
+  f2_unpack(f2_fma_down(minus_d, f2_pack(u0.minus(), u1.minus()), f2_fma(L, L, minus_d)), tx, ty);
   return pack_codes(__uint_as_float((bx & 0xfff00000u) + (ax > tx ? 0x100000u : 0u)),
                     __uint_as_float((by & 0xfff00000u) + (ay > ty ? 0x100000u : 0u)));
+}
+
+// The largest (a NaN if there is one) and the least magnitude of eight.
+__device__ __forceinline__ float most_magnitude(const float (&x)[8]) {
+  float a, b, c;
+  asm("max.NaN.abs.f32 %0, %1, %2, %3;" : "=f"(a) : "f"(x[0]), "f"(x[1]), "f"(x[2]));
+  asm("max.NaN.abs.f32 %0, %1, %2, %3;" : "=f"(b) : "f"(x[3]), "f"(x[4]), "f"(x[5]));
+  asm("max.NaN.abs.f32 %0, %1, %2, %3;" : "=f"(c) : "f"(x[6]), "f"(x[7]), "f"(a));
+  asm("max.NaN.abs.f32 %0, %1, %2, %2;" : "=f"(a) : "f"(b), "f"(c));
+  return a;
+}
+__device__ __forceinline__ float least_magnitude(const float (&x)[8]) {
+  float a, b, c;
+  asm("min.abs.f32 %0, %1, %2, %3;" : "=f"(a) : "f"(x[0]), "f"(x[1]), "f"(x[2]));
+  asm("min.abs.f32 %0, %1, %2, %3;" : "=f"(b) : "f"(x[3]), "f"(x[4]), "f"(x[5]));
+  asm("min.abs.f32 %0, %1, %2, %3;" : "=f"(c) : "f"(x[6]), "f"(x[7]), "f"(a));
+  asm("min.abs.f32 %0, %1, %2, %2;" : "=f"(a) : "f"(b), "f"(c));
+  return a;
 }
 
 // One element type's part of the ring: eight elements a thread, in one or two
@@ -377,7 +395,7 @@ template <typename T> struct Ahead {
 };
 
 template <typename PT, typename GT, int kBits, int kCap>
-__global__ void __launch_bounds__(kThreads, 3) adamw_kernel(const __grid_constant__ AdamArgs<kCap> a) {
+__global__ void __launch_bounds__(kThreads, kBits == 8 ? 4 : 3) adamw_kernel(const __grid_constant__ AdamArgs<kCap> a) {
   const AdamHyper& hy = a.hy;
   const int i = find_tensor(a, blockIdx.x);
   const AdamTensor& t = a.t[i];
@@ -464,30 +482,29 @@ __global__ void __launch_bounds__(kThreads, 3) adamw_kernel(const __grid_constan
         if (turn + 2 < turns) fetch(e + 2 * kTile, stage);  // (the stage's values are in registers)
         copy_commit();
         float m8[8], v8[8], p8[8];
-        unsigned tm = 0, tv = 0, lm = 0x7f800000u, lv = 0x7f800000u;
 #pragma unroll
         for (int j = 0; j < 4; ++j) {
           f2_unpack(xm[j], m8[2 * j], m8[2 * j + 1]);
           f2_unpack(xv[j], v8[2 * j], v8[2 * j + 1]);
         }
-#pragma unroll
-        for (int j = 0; j < 8; ++j) {
-          const unsigned x = __float_as_uint(m8[j]) & 0x7fffffffu, y = __float_as_uint(v8[j]);
-          tm = max(tm, x), lm = min(lm, x);
-          tv = max(tv, y), lv = min(lv, y);
-        }
-        tm = __reduce_max_sync(kFull, tm), tv = __reduce_max_sync(kFull, tv);
+        const float lm = least_magnitude(m8), lv = least_magnitude(v8);
+        const unsigned tm = __reduce_max_sync(kFull, __float_as_uint(most_magnitude(m8)));
+        const unsigned tv = __reduce_max_sync(kFull, __float_as_uint(most_magnitude(v8)));
+        // half of the warp finds m's scale and its reciprocal, half sqrt(v)'s
         // (the root is monotone: the largest v's is the largest)
-        sm = block_scale(tm), sv = block_scale(__float_as_uint(__fsqrt_rn(__uint_as_float(tv))));
+        const bool second = (threadIdx.x & 16) != 0;
+        const float root_top = __fsqrt_rn(__uint_as_float(tv));
+        const float scale = block_scale(second ? __float_as_uint(root_top) : tm), inv = __frcp_rn(scale);
+        sm = __shfl_sync(kFull, scale, 0), sv = __shfl_sync(kFull, scale, 16);
         // of e4m3's normal values, with some room, and of root2's range
         // (2.4e-4 > (2^-6)^2: v is compared with the scale's square)
-        const bool ordinary = __uint_as_float(lm) >= sm * 0x1.1p-6f && __uint_as_float(lv) >= sv * sv * 2.8e-4f &&
-                              lv >= 0x0d800000u && tm < 0x7f800000u && tv < 0x7f000000u;
+        const bool ordinary = lm >= sm * 0x1.1p-6f && lv >= fmaxf(sv * sv * 2.8e-4f, 0x1p-100f) && tm < 0x7f800000u &&
+                              tv < 0x7f000000u;
         uint2 cm, cv;
         // (about one block in 50 of normally distributed gradients has an
         // element that is not)
         if (__all_sync(kFull, ordinary)) {
-          const float im = __fdiv_rn(1.f, sm), iv = __fdiv_rn(1.f, sv);
+          const float im = __shfl_sync(kFull, inv, 0), iv = __shfl_sync(kFull, inv, 16);
           const f32x2 im2 = both(im), iv2 = both(iv), nsm = both(-sm), nsv = both(-sv);
           const unsigned word[4] = {random.x, random.y, random.z, random.w};
           unsigned mc[4], vc[4];
