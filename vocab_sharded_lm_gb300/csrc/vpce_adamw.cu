@@ -169,6 +169,13 @@ __device__ __forceinline__ float round_linear(float a, const RoundWord& u) {  //
   return __uint_as_float((__float_as_uint(a) + 0x17ffffffu - (u.c1 >> 3)) & 0xfff00000u);
 }
 
+// The same for any finite value: below 2^-6, adding 2^-6 gives the word whose
+// 20 lower bits are the place (rounded up, which no c lies between).
+__device__ __forceinline__ float round_linear_small(float a, const RoundWord& u) {
+  const float x = fabsf(a), by = x < 0x1p-6f ? 0x1p-6f : 0.f;
+  return copysignf(round_linear(__fadd_ru(x, by), u) - by, a);
+}
+
 __device__ __forceinline__ float round_squares(float a, const RoundWord& u) {
   const unsigned bits = __float_as_uint(a);
   const float A = __uint_as_float((bits & 0x7fffffu) | 0x41000000u);
@@ -186,10 +193,10 @@ template <bool kSquares> __device__ __noinline__ float round_any(float a, RoundW
     if (a != a || x > 480.f) return a;
     return kSquares ? round_squares(a, u) : round_linear(a, u);
   }
+  if (!kSquares) return round_linear_small(a, u);
   const float A = x * 512.f, L = truncf(A);
-  const bool up = kSquares ? __fdiv_rn(__fsub_rn(__fmul_rn(A, A), L * L), fmaf(2.f, L, 1.f)) > c : A - L > c;
-  const float r = (L + (up ? 1.f : 0.f)) * 0x1p-9f;
-  return kSquares && x > 0.f ? fmaxf(r, 0x1p-9f) : copysignf(r, a);
+  const bool up = __fdiv_rn(__fsub_rn(__fmul_rn(A, A), L * L), fmaf(2.f, L, 1.f)) > c;
+  return x > 0.f ? fmaxf((L + (up ? 1.f : 0.f)) * 0x1p-9f, 0x1p-9f) : 0.f;
 }
 
 // two values that are e4m3 values already (or past 448) as codes
@@ -337,10 +344,11 @@ __device__ __forceinline__ f32x2 quotient2(f32x2 x, f32x2 minus_s, f32x2 inv) {
   return f2_fma(f2_fma(q, minus_s, x), inv, q);
 }
 
-// round_linear and round_squares of two values
-__device__ __forceinline__ unsigned linear_codes2(f32x2 a, const RoundWord& u0, const RoundWord& u1) {
+// round_linear (with `small`: round_linear_small) and round_squares of two values
+__device__ __forceinline__ unsigned linear_codes2(f32x2 a, const RoundWord& u0, const RoundWord& u1, bool small) {
   float x, y;
   f2_unpack(a, x, y);
+  if (small) return pack_codes(round_linear_small(x, u0), round_linear_small(y, u1));
   return pack_codes(round_linear(x, u0), round_linear(y, u1));
 }
 __device__ __forceinline__ unsigned square_codes2(f32x2 a, const RoundWord& u0, const RoundWord& u1) {
@@ -496,13 +504,12 @@ __global__ void __launch_bounds__(kThreads, kBits == 8 ? 4 : 3) adamw_kernel(con
         const float root_top = __fsqrt_rn(__uint_as_float(tv));
         const float scale = block_scale(second ? __float_as_uint(root_top) : tm), inv = __frcp_rn(scale);
         sm = __shfl_sync(kFull, scale, 0), sv = __shfl_sync(kFull, scale, 16);
-        // of e4m3's normal values, with some room, and of root2's range
-        // (2.4e-4 > (2^-6)^2: v is compared with the scale's square)
-        const bool ordinary = lm >= sm * 0x1.1p-6f && lv >= fmaxf(sv * sv * 2.8e-4f, 0x1p-100f) && tm < 0x7f800000u &&
-                              tv < 0x7f000000u;
+        // v: of e4m3's normal values, with some room, and of root2's range
+        // (2.4e-4 > (2^-6)^2: v is compared with the scale's square).  About
+        // one block in 50 of normally distributed gradients has an m below them.
+        const bool ordinary = lv >= fmaxf(sv * sv * 2.8e-4f, 0x1p-100f) && tm < 0x7f800000u && tv < 0x7f000000u;
+        const bool small = !__all_sync(kFull, lm >= sm * 0x1.1p-6f);
         uint2 cm, cv;
-        // (about one block in 50 of normally distributed gradients has an
-        // element that is not)
         if (__all_sync(kFull, ordinary)) {
           const float im = __shfl_sync(kFull, inv, 0), iv = __shfl_sync(kFull, inv, 16);
           const f32x2 im2 = both(im), iv2 = both(iv), nsm = both(-sm), nsv = both(-sv);
@@ -517,13 +524,18 @@ __global__ void __launch_bounds__(kThreads, kBits == 8 ? 4 : 3) adamw_kernel(con
             RoundWord u0, u1;
             u0.set<false>(word[j]);
             u1.set<true>(word[j]);
-            mc[j] = linear_codes2(quotient2(xm[j], nsm, im2), u0, u1);
+            mc[j] = linear_codes2(quotient2(xm[j], nsm, im2), u0, u1, small);
             vc[j] = square_codes2(quotient2(root, nsv, iv2), u0, u1);
           }
           cm = make_uint2(mc[0] | mc[1] << 16, mc[2] | mc[3] << 16);
           cv = make_uint2(vc[0] | vc[1] << 16, vc[2] | vc[3] << 16);
 #pragma unroll
           for (int j = 0; j < 4; ++j) f2_unpack(xp[j], p8[2 * j], p8[2 * j + 1]);
+        } else if (tm == 0 && tv == 0 && c.eps > 0.f) {
+          // a block that has had no gradient yet, as rows of a table do
+          cm = cv = make_uint2(0, 0);
+#pragma unroll
+          for (int j = 0; j < 4; ++j) f2_unpack(f2_mul(xp[j], c2.keep), p8[2 * j], p8[2 * j + 1]);
         } else {
 #pragma unroll
           for (int j = 0; j < 4; ++j) f2_unpack(xp[j], p8[2 * j], p8[2 * j + 1]);
