@@ -1053,6 +1053,7 @@ static vpce_status rmsnorm_impl(const void* x, vpce_dtype dtype, int64_t ld_x, c
   p.scale = scale_out;
   p.group = int(group == 0 || group > h ? h : group);
   p.groups = int((h + p.group - 1) / p.group);
+  p.group_inverse = p.group == 1 ? 0xffffffffu : unsigned(((uint64_t(1) << 32) + p.group - 1) / p.group);
   p.rstd = rstd_out;
   launch_rmsnorm_forward(p, dtype == VPCE_BF16, residual_dtype == VPCE_BF16, codes, vectors, sms,
                          reinterpret_cast<cudaStream_t>(stream));

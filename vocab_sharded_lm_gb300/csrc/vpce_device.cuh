@@ -195,6 +195,10 @@ __device__ __forceinline__ void copy_async(void* dst_smem, const void* src) {
   else
     asm volatile("cp.async.cg.shared.global [%0], [%1], %2;" ::"r"(smem_addr(dst_smem)), "l"(src), "n"(kBytes) : "memory");
 }
+// 16 bytes to shared memory of which `bytes` are read and the others set to 0
+__device__ __forceinline__ void copy_async_part(void* dst_smem, const void* src, int bytes) {
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(smem_addr(dst_smem)), "l"(src), "r"(bytes) : "memory");
+}
 __device__ __forceinline__ void copy_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
 // Wait until at most N of this thread's groups of them are incomplete.
 template <int N> __device__ __forceinline__ void copy_wait() {

@@ -49,14 +49,18 @@ __device__ __forceinline__ float group_scale(unsigned top) {
 // row), or through shared memory.
 enum GroupKind { kNoCodes, kLanes, kRow, kShared };
 
-template <typename XT, typename RT, GroupKind kGroups, int U, int NU, bool kWarp, int kMaxT>
-__global__ void __launch_bounds__(kMaxT, kMaxT == 256 ? 3 : 1) rmsnorm_forward_kernel(const __grid_constant__ RmsNormParams p) {
-  extern __shared__ unsigned top_sm[];  // [teams][2][groups], kShared only
+// kT: threads of a team, known when compiled (single elements: their addresses
+// are then one register and constants), or 0.
+template <typename XT, typename RT, GroupKind kGroups, int U, int NU, bool kWarp, int kMaxT, int kT>
+__global__ void __launch_bounds__(kMaxT, U == 1 ? (kMaxT < 512 ? 512 / kMaxT : 1) : kMaxT == 256 ? 3 : 1) rmsnorm_forward_kernel(const __grid_constant__ RmsNormParams p) {
+  extern __shared__ unsigned top_sm[];  // [teams][2][2][groups], kShared only
   __shared__ float red[2][32];
   [[maybe_unused]] __shared__ unsigned top_row[2][32];
   const int lane = threadIdx.x & 31;
   const int team = kWarp ? int(threadIdx.x >> 5) : 0, teams = kWarp ? int(blockDim.x >> 5) : 1;
-  const int tid = kWarp ? lane : int(threadIdx.x), T = kWarp ? 32 : int(blockDim.x);
+  const int tid = kWarp ? lane : int(threadIdx.x), T = kT > 0 ? kT : int(blockDim.x);
+  // (elements past the row are skipped by all of a team's threads)
+  const auto past = [&](int k) { return U == 1 && k * T >= p.h; };
   int parity = 0;
   for (long long row = (long long)blockIdx.x * teams + team; row < p.s; row += (long long)gridDim.x * teams) {
     const unsigned char* xr = p.x + row * p.ld_x;
@@ -64,6 +68,7 @@ __global__ void __launch_bounds__(kMaxT, kMaxT == 256 ? 3 : 1) rmsnorm_forward_k
     RawUnit<RT, U> b[NU];
 #pragma unroll
     for (int k = 0; k < NU; ++k) {
+      if (past(k)) break;
       const int c = (k * T + tid) * U;
       a[k].zero();
       if (c < p.h) a[k].load(xr, c);
@@ -72,6 +77,7 @@ __global__ void __launch_bounds__(kMaxT, kMaxT == 256 ? 3 : 1) rmsnorm_forward_k
       const unsigned char* rr = p.res + row * p.ld_res;
 #pragma unroll
       for (int k = 0; k < NU; ++k) {
+        if (past(k)) break;
         const int c = (k * T + tid) * U;
         b[k].zero();
         if (c < p.h) b[k].load(rr, c);
@@ -80,6 +86,7 @@ __global__ void __launch_bounds__(kMaxT, kMaxT == 256 ? 3 : 1) rmsnorm_forward_k
     float r[NU][U], ss = 0.f;
 #pragma unroll
     for (int k = 0; k < NU; ++k) {
+      if (past(k)) break;
       const int c = (k * T + tid) * U;
       a[k].get(r[k]);
       if (p.res != nullptr) {
@@ -95,8 +102,10 @@ __global__ void __launch_bounds__(kMaxT, kMaxT == 256 ? 3 : 1) rmsnorm_forward_k
     // the two buffers alternate: who still reads one row's is at most a
     // barrier behind whoever writes the next row's
     [[maybe_unused]] unsigned* top = nullptr;
+    [[maybe_unused]] float* inverse = nullptr;
     if constexpr (kGroups == kShared) {
-      top = top_sm + (team * 2 + parity) * p.groups;
+      top = top_sm + (team * 2 + parity) * 2 * p.groups;
+      inverse = reinterpret_cast<float*>(top + p.groups);
       for (int g = tid; g < p.groups; g += T) top[g] = 0;
       if constexpr (kWarp) __syncwarp();
     }
@@ -106,8 +115,10 @@ __global__ void __launch_bounds__(kMaxT, kMaxT == 256 ? 3 : 1) rmsnorm_forward_k
     [[maybe_unused]] unsigned m[NU], all = 0;
 #pragma unroll
     for (int k = 0; k < NU; ++k) {
+      if (past(k)) break;
       const int c = (k * T + tid) * U;
       m[k] = 0;
+      const int group = kGroups == kShared || kGroups == kLanes ? int(__umulhi(unsigned(c), p.group_inverse)) : 0;
       if (c < p.h) {
         float w[U];
         load_weight(p.w, p.w_bf16, c, w);
@@ -118,8 +129,18 @@ __global__ void __launch_bounds__(kMaxT, kMaxT == 256 ? 3 : 1) rmsnorm_forward_k
         } else {
 #pragma unroll
           for (int j = 0; j < U; ++j) m[k] = max(m[k], mag(r[k][j]));
-          if constexpr (kGroups == kShared) atomicMax(top + c / p.group, m[k]);  // the order does not matter
           if constexpr (kGroups == kRow) all = max(all, m[k]);
+        }
+      }
+      if constexpr (kGroups == kShared) {
+        // (atomics on shared memory; their order does not matter)
+        if (U == 1) {
+          // 32 consecutive columns: of one group, or 16 and 16 of one each
+          const unsigned half = p.group % 32 == 0 ? kFull : lane < 16 ? 0xffffu : 0xffff0000u;
+          const unsigned t = __reduce_max_sync(half, m[k]);
+          if ((lane == 0 || (lane == 16 && half != kFull)) && c < p.h) atomicMax(top + group, t);
+        } else if (c < p.h) {
+          atomicMax(top + group, m[k]);
         }
       }
     }
@@ -140,20 +161,43 @@ __global__ void __launch_bounds__(kMaxT, kMaxT == 256 ? 3 : 1) rmsnorm_forward_k
         __syncthreads();
         all = __reduce_max_sync(kFull, lane < warps ? top_row[parity][lane] : 0u);
       }
-#pragma unroll
-      for (int k = 0; k < NU; ++k) m[k] = all;
     } else if constexpr (kGroups == kShared) {
+      // each group's scale and its reciprocal, in the maximum's place
+      if constexpr (kWarp) __syncwarp();
+      else __syncthreads();
+      for (int g = tid; g < p.groups; g += T) {
+        const float scale = group_scale(top[g]);
+        p.scale[row * p.groups + g] = scale;
+        top[g] = __float_as_uint(scale);
+        inverse[g] = __fdiv_rn(1.f, scale);
+      }
       if constexpr (kWarp) __syncwarp();
       else __syncthreads();
     }
     if constexpr (kGroups != kNoCodes) {
+      [[maybe_unused]] float row_scale = 0.f, row_inv = 0.f;
+      if constexpr (kGroups == kRow) {
+        row_scale = group_scale(all);
+        row_inv = __fdiv_rn(1.f, row_scale);
+        if (tid == 0) p.scale[row] = row_scale;
+      }
 #pragma unroll
       for (int k = 0; k < NU; ++k) {
+        if (past(k)) break;
         const int c = (k * T + tid) * U;
         if (c < p.h) {
-          const int g = kGroups == kRow ? 0 : c / p.group;
-          const float scale = group_scale(kGroups == kShared ? top[g] : m[k]), inv = __fdiv_rn(1.f, scale);
-          if (c == g * p.group) p.scale[row * p.groups + g] = scale;
+          float scale, inv;
+          if constexpr (kGroups == kRow) {
+            scale = row_scale, inv = row_inv;
+          } else {
+            const int g = int(__umulhi(unsigned(c), p.group_inverse));
+            if constexpr (kGroups == kShared) {
+              scale = __uint_as_float(top[g]), inv = inverse[g];
+            } else {
+              scale = group_scale(m[k]), inv = __fdiv_rn(1.f, scale);
+              if (c == g * p.group) p.scale[row * p.groups + g] = scale;
+            }
+          }
 #pragma unroll
           for (int j = 0; j < U; ++j) r[k][j] = quotient(r[k][j], isinf(scale) ? 0.f : scale, inv);
           store_codes(p.out + row * p.ld_out + c, r[k]);
@@ -164,12 +208,12 @@ __global__ void __launch_bounds__(kMaxT, kMaxT == 256 ? 3 : 1) rmsnorm_forward_k
   }
 }
 
-template <typename XT, typename RT, GroupKind kGroups, int U, int NU, bool kWarp, int kMaxT = 128>
+template <typename XT, typename RT, GroupKind kGroups, int U, int NU, bool kWarp, int kMaxT = 128, int kT = kWarp ? 32 : 0>
 void launch(const RmsNormParams& p, int threads, int sms, cudaStream_t st) {
   const int teams = kWarp ? 4 : 1;
   const long long rows = (p.s + teams - 1) / teams, most = (long long)sms * 64;
-  const size_t smem = kGroups == kShared ? size_t(teams) * 2 * p.groups * sizeof(unsigned) : 0;
-  rmsnorm_forward_kernel<XT, RT, kGroups, U, NU, kWarp, kMaxT>
+  const size_t smem = kGroups == kShared ? size_t(teams) * 4 * p.groups * sizeof(unsigned) : 0;
+  rmsnorm_forward_kernel<XT, RT, kGroups, U, NU, kWarp, kMaxT, kT>
       <<<int(rows < most ? rows : most), kWarp ? 128 : threads, smem, st>>>(p);
 }
 
@@ -187,10 +231,14 @@ void pick(const RmsNormParams& p, bool vectors, int sms, cudaStream_t st) {
     return launch<XT, RT, kGroups, 8, 4, false, 1024>(p, threads, sms, st);
   }
   if constexpr (kGroups != kLanes) {
-    if (h <= 256) return launch<XT, RT, kGroups, 1, 8, true>(p, 32, sms, st);
-    const int threads = ((h + 7) / 8 + 31) / 32 * 32;
-    if (threads <= 512) return launch<XT, RT, kGroups, 1, 8, false, 512>(p, threads, sms, st);
-    launch<XT, RT, kGroups, 1, 32, false, 1024>(p, ((h + 31) / 32 + 31) / 32 * 32, sms, st);
+    // few warps a row: what a row costs besides its elements (sums, addresses)
+    // is paid by every one of them
+    if (h <= 1024) return launch<XT, RT, kGroups, 1, 32, true>(p, 32, sms, st);
+    if (h <= 2048) return launch<XT, RT, kGroups, 1, 32, false, 64, 64>(p, 64, sms, st);
+    if (h <= 4096) return launch<XT, RT, kGroups, 1, 32, false, 128, 128>(p, 128, sms, st);
+    if (h <= 8192) return launch<XT, RT, kGroups, 1, 32, false, 256, 256>(p, 256, sms, st);
+    if (h <= 16384) return launch<XT, RT, kGroups, 1, 32, false, 512, 512>(p, 512, sms, st);
+    launch<XT, RT, kGroups, 1, 32, false, 1024, 1024>(p, 1024, sms, st);
   }
 }
 

@@ -22,6 +22,7 @@ struct RmsNormParams {
   long long ld_out;
   float* scale;              // [s][groups], codes only
   int group, groups;
+  unsigned group_inverse;    // ceil(2^32 / group): a column's group is the product's high word (columns < 2^15)
   float* rstd;               // may be null
 };
 
@@ -82,7 +83,6 @@ template <> struct RawUnit<float, 1> {
   __device__ __forceinline__ void load(const unsigned char* row, int c) {
     a = *reinterpret_cast<const float*>(row + size_t(c) * 4);
   }
-  __device__ __forceinline__ void take(const unsigned char* p, int) { a = *reinterpret_cast<const float*>(p); }
   __device__ __forceinline__ void get(float (&v)[1]) const { v[0] = a; }
   __device__ __forceinline__ void zero() { a = 0.f; }
 };

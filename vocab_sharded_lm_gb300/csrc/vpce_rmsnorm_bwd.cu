@@ -24,6 +24,10 @@ constexpr int kColumns = 32, kRowLanes = 32;  // of the kernel that adds the par
 struct Team {
   int id, tid, threads;
   float* red;  // [2][32]
+  __device__ __forceinline__ void sync() const {
+    if (threads == 32) __syncwarp();
+    else asm volatile("bar.sync %0, %1;" ::"r"(id + 1), "r"(threads) : "memory");
+  }
   __device__ __forceinline__ float sum(float v, int parity) const {
 #pragma unroll
     for (int o = 16; o > 0; o >>= 1) v += __shfl_xor_sync(kFull, v, o);
@@ -31,7 +35,7 @@ struct Team {
       const int lane = tid & 31, warps = threads >> 5;
       float* r = red + parity * 32;
       if (lane == 0) r[tid >> 5] = v;
-      asm volatile("bar.sync %0, %1;" ::"r"(id + 1), "r"(threads) : "memory");
+      sync();
       v = lane < warps ? r[lane] : 0.f;
 #pragma unroll
       for (int o = 16; o > 0; o >>= 1) v += __shfl_xor_sync(kFull, v, o);
@@ -40,23 +44,41 @@ struct Team {
   }
 };
 
-// What a thread copies ahead of a unit: vectors of 16 bytes, or one fp32 word.
-template <typename T, int U> constexpr int kParts = U == 8 ? int(sizeof(T)) / 2 : 1;
-template <int U> constexpr int kSlotBytes = U == 8 ? 16 : 4;
+// Where a team puts its sums of the weight's gradient: the CTA's partial row,
+// or a row of shared memory where the CTA has several teams (all its threads
+// call this, and then join_sums).
+__device__ __forceinline__ float* own_sums(const RmsNormBwdParams& p, uint4* smem, int teams, int team) {
+  if (teams == 1) return p.part + (long long)blockIdx.x * p.h;
+  __syncthreads();
+  return reinterpret_cast<float*>(smem) + team * p.h;
+}
+__device__ __forceinline__ void join_sums(const RmsNormBwdParams& p, const uint4* smem, int teams) {
+  if (teams == 1) return;
+  __syncthreads();
+  const float* sums = reinterpret_cast<const float*>(smem);
+  float* part = p.part + (long long)blockIdx.x * p.h;
+  for (int c = threadIdx.x; c < p.h; c += blockDim.x) {
+    float v = sums[c];
+    for (int i = 1; i < teams; ++i) v += sums[i * p.h + c];
+    part[c] = v;
+  }
+}
 
-// kStages: rows of the ring ahead (0: none, rows are loaded when they are due).
-// kT: threads of a team, known when compiled (addresses of single elements are
-// then one register and constants), or 0.  kKeep: products of a row's values
-// stay in registers until its mean is known, and the weights for all rows; else
-// (32 columns a thread) they are read a second time, from the ring or through
-// L1.
-template <typename GT, typename RT, int U, int NU, int kStages, int kMaxT, int kCtas, int kT, bool kKeep>
-__global__ void __launch_bounds__(kMaxT, kCtas) rmsnorm_backward_kernel(const __grid_constant__ RmsNormBwdParams p,
-                                                                 int team_threads) {
+// Rows of 16-byte vectors.  NU units of eight columns a thread; kStages: rows
+// of the ring ahead (0: none, rows are loaded when they are due).  kKeep:
+// products of a row's values stay in registers until its mean is known, and the
+// weights for all rows; else (32 columns a thread) they are read a second time,
+// from the ring or through L1.
+template <typename T> constexpr int kParts = int(sizeof(T)) / 2;  // vectors of a unit
+
+template <typename GT, typename RT, int NU, int kStages, int kMaxT, bool kKeep>
+__global__ void __launch_bounds__(kMaxT, 1) rmsnorm_backward_kernel(const __grid_constant__ RmsNormBwdParams p,
+                                                                    int team_threads) {
+  constexpr int U = 8;
   extern __shared__ uint4 smem[];  // the ring, and at the end sums [teams][h]
   __shared__ float red[kMaxT / 32][2][32];
   constexpr bool kRing = kStages > 0;
-  const int T = kT > 0 ? kT : team_threads;
+  const int T = team_threads;
   Team team;
   const int teams = blockDim.x / T;
   team.id = threadIdx.x / T;
@@ -64,8 +86,6 @@ __global__ void __launch_bounds__(kMaxT, kCtas) rmsnorm_backward_kernel(const __
   team.threads = T;
   team.red = &red[team.id][0][0];
   const int tid = team.tid;
-  // (units past the row are skipped by all of a team's threads)
-  const auto past = [&](int k) { return U == 1 && k * T >= p.h; };
   float acc[NU][U], w[kKeep ? NU : 1][U];
 #pragma unroll
   for (int k = 0; k < NU; ++k) {
@@ -78,14 +98,13 @@ __global__ void __launch_bounds__(kMaxT, kCtas) rmsnorm_backward_kernel(const __
   }
 
   // ring slot of part v of a stage: this thread's own bytes
-  constexpr int kG = kParts<GT, U>, kR = kParts<RT, U>, kVecs = NU * (kG + 2 * kR), kSlot = kSlotBytes<U>;
+  constexpr int kG = kParts<GT>, kR = kParts<RT>, kVecs = NU * (kG + 2 * kR), kSlot = 16;
   const auto slot = [&](int stage, int v) {
     return reinterpret_cast<unsigned char*>(smem) + ((stage * kVecs + v) * int(blockDim.x) + int(threadIdx.x)) * kSlot;
   };
   // (the two vectors of eight fp32 values share sectors with each other: those go through L1)
   const auto copy = [&](int stage, int v, const unsigned char* src, auto fp32) {
-    if constexpr (U == 1) copy_async<4>(slot(stage, v), src);
-    else if constexpr (fp32) copy_async<16, true>(slot(stage, v), src);
+    if constexpr (fp32) copy_async<16, true>(slot(stage, v), src);
     else copy_async<16>(slot(stage, v), src);
   };
   constexpr std::bool_constant<sizeof(GT) == 4> g32{};
@@ -94,7 +113,6 @@ __global__ void __launch_bounds__(kMaxT, kCtas) rmsnorm_backward_kernel(const __
     if (row < p.s) {
 #pragma unroll
       for (int k = 0; k < NU; ++k) {
-        if (past(k)) break;
         const int c = (k * T + tid) * U;
         if (c < p.h) {
           const unsigned char *g = p.dy + row * p.ld_dy + size_t(c) * sizeof(GT),
@@ -156,7 +174,6 @@ __global__ void __launch_bounds__(kMaxT, kCtas) rmsnorm_backward_kernel(const __
     if constexpr (kKeep) {
 #pragma unroll
       for (int k = 0; k < NU; ++k) {
-        if (past(k)) break;
         const int c = (k * T + tid) * U;
         d[k].zero();
         if (c < p.h) {
@@ -169,7 +186,6 @@ __global__ void __launch_bounds__(kMaxT, kCtas) rmsnorm_backward_kernel(const __
     float dot = 0.f;
 #pragma unroll
     for (int k = 0; k < NU; ++k) {
-      if (past(k)) break;
       const int c = (k * T + tid) * U, at = kKeep ? k : 0;
       if (c < p.h) {
         if constexpr (!kKeep) {
@@ -190,7 +206,6 @@ __global__ void __launch_bounds__(kMaxT, kCtas) rmsnorm_backward_kernel(const __
     if constexpr (kRing && kKeep) fetch(row + kStages * stride, stage);  // (the stage's values are in registers)
 #pragma unroll
     for (int k = 0; k < NU; ++k) {
-      if (past(k)) break;
       const int c = (k * T + tid) * U, at = kKeep ? k : 0;
       if (c < p.h) {
         if constexpr (!kKeep) {
@@ -214,15 +229,8 @@ __global__ void __launch_bounds__(kMaxT, kCtas) rmsnorm_backward_kernel(const __
     }
   }
   grid_launch_dependents();
-  float* part = p.part + (long long)blockIdx.x * p.h;
-  float* mine = part;
-  if (teams > 1) {
-    if constexpr (kRing) {  // (what was copied past the last row is nothing)
-      copy_wait<0>();
-      __syncthreads();
-    }
-    mine = reinterpret_cast<float*>(smem) + team.id * p.h;
-  }
+  if constexpr (kRing) copy_wait<0>();  // (what was copied past the last row is nothing)
+  float* const mine = own_sums(p, smem, teams, team.id);
 #pragma unroll
   for (int k = 0; k < NU; ++k)
 #pragma unroll
@@ -230,15 +238,127 @@ __global__ void __launch_bounds__(kMaxT, kCtas) rmsnorm_backward_kernel(const __
       const int c = (k * T + tid) * U + j;
       if (c < p.h) mine[c] = acc[k][j];
     }
-  if (teams > 1) {
-    __syncthreads();
-    const float* sums = reinterpret_cast<const float*>(smem);
-    for (int c = threadIdx.x; c < p.h; c += blockDim.x) {
-      float v = sums[c];
-      for (int i = 1; i < teams; ++i) v += sums[i * p.h + c];
-      part[c] = v;
+  join_sums(p, smem, teams);
+}
+
+// Rows off 16 bytes: kT threads a row, column k kT + thread, up to 32 a thread.
+// kStages rows of the ring are under way (0: none).  A row's bytes are copied as
+// the 16-byte vectors that hold them, the last cut to the row's end; the first
+// may begin in the row before (row 0's is copied by elements).  Elements are
+// then read from shared memory, where alignment costs nothing.
+struct OddRing {
+  int dy_bytes, x_bytes;  // of a row, with room for its offset, a multiple of 16
+  __host__ __device__ int row_bytes(bool dres) const { return dy_bytes + (dres ? 2 : 1) * x_bytes; }
+};
+
+template <typename GT, typename RT, int kT, int kStages>
+__global__ void __launch_bounds__(kT > 512 ? kT : 512, 1) rmsnorm_backward_odd_kernel(const __grid_constant__ RmsNormBwdParams p,
+                                                                                     const OddRing ring) {
+  extern __shared__ uint4 smem[];  // the rings [teams][kStages], and at the end sums [teams][h]
+  constexpr int kMaxTeams = kT > 512 ? 1 : 512 / kT, kNU = 32;
+  constexpr bool kRing = kStages > 0;
+  __shared__ float red[kMaxTeams][2][32];
+  Team team;
+  const int teams = blockDim.x / kT;
+  team.id = threadIdx.x / kT;
+  team.tid = threadIdx.x % kT;
+  team.threads = kT;
+  team.red = &red[team.id][0][0];
+  const int tid = team.tid, h = p.h;
+  float acc[kNU];
+#pragma unroll
+  for (int k = 0; k < kNU; ++k) acc[k] = 0.f;
+
+  const int stage_bytes = ring.row_bytes(p.dres != nullptr);
+  unsigned char* const mine = reinterpret_cast<unsigned char*>(smem) + team.id * kStages * stage_bytes;
+  const auto copy_row = [&](unsigned char* dst, const unsigned char* base, long long row, long long ld, int bytes,
+                            int element) {
+    const unsigned char* const src = base + row * ld;
+    const int off = int(uintptr_t(src) & 15), end = off + bytes;
+    for (int v = tid * 16; v < end; v += kT * 16) {
+      if (v == 0 && off > 0 && row == 0) {
+        for (int i = off; i < 16 && i < end; i += element) {
+          if (element == 2) *reinterpret_cast<short*>(dst + i) = *reinterpret_cast<const short*>(src - off + i);
+          else *reinterpret_cast<int*>(dst + i) = *reinterpret_cast<const int*>(src - off + i);
+        }
+      } else {
+        copy_async_part(dst + v, src - off + v, end - v < 16 ? end - v : 16);
+      }
     }
+  };
+  const auto fetch = [&](long long row, int stage) {
+    if (row < p.s) {
+      unsigned char* const dst = mine + stage * stage_bytes;
+      copy_row(dst, p.dy, row, p.ld_dy, h * int(sizeof(GT)), sizeof(GT));
+      copy_row(dst + ring.dy_bytes, p.x, row, p.ld_x, h * int(sizeof(RT)), sizeof(RT));
+      if (p.dres != nullptr)
+        copy_row(dst + ring.dy_bytes + ring.x_bytes, p.dres, row, p.ld_dres, h * int(sizeof(RT)), sizeof(RT));
+    }
+    copy_commit();  // (an empty group past the end keeps the count)
+  };
+
+  const long long first = (long long)blockIdx.x * teams + team.id, stride = (long long)gridDim.x * teams;
+  if constexpr (kRing) {
+#pragma unroll
+    for (int i = 0; i + 1 < kStages; ++i) fetch(first + i * stride, i);
   }
+  int parity = 0, stage = 0;
+  float next_rstd = first < p.s ? __ldg(p.rstd + first) : 0.f;
+  for (long long row = first; row < p.s; row += stride) {
+    const float rstd = next_rstd;
+    if (row + stride < p.s) next_rstd = __ldg(p.rstd + row + stride);
+    const unsigned char *gr = p.dy + row * p.ld_dy, *xr = p.x + row * p.ld_x,
+                        *dr = p.dres != nullptr ? p.dres + row * p.ld_dres : nullptr;
+    if constexpr (kRing) {
+      // this row's copies are in, everybody's; and everybody is done with the
+      // stage of the row before, which is filled next
+      copy_wait<(kRing ? kStages - 2 : 0)>();
+      team.sync();
+      fetch(row + (kStages - 1) * stride, stage == 0 ? kStages - 1 : stage - 1);
+      unsigned char* const at = mine + stage * stage_bytes;
+      gr = at + (uintptr_t(gr) & 15);
+      xr = at + ring.dy_bytes + (uintptr_t(xr) & 15);
+      if (dr != nullptr) dr = at + ring.dy_bytes + ring.x_bytes + (uintptr_t(dr) & 15);
+    }
+    float dot = 0.f;
+#pragma unroll
+    for (int k = 0; k < kNU; ++k) {
+      if (k * kT >= h) break;
+      const int c = k * kT + tid;
+      if (c < h) {
+        float w[1];
+        load_weight(p.w, p.w_bf16, c, w);
+        const float dy = Elem<GT>::load(gr + c * int(sizeof(GT))), n = Elem<RT>::load(xr + c * int(sizeof(RT))) * rstd;
+        acc[k] = fmaf(dy, n, acc[k]);
+        dot = fmaf(w[0] * dy, n, dot);
+      }
+    }
+    dot = team.sum(dot, parity) / float(h);
+    parity ^= 1;
+    unsigned char* const out = p.dx + row * p.ld_dx;
+#pragma unroll
+    for (int k = 0; k < kNU; ++k) {
+      if (k * kT >= h) break;
+      const int c = k * kT + tid;
+      if (c < h) {
+        float w[1];
+        load_weight(p.w, p.w_bf16, c, w);
+        const float dy = Elem<GT>::load(gr + c * int(sizeof(GT))), n = Elem<RT>::load(xr + c * int(sizeof(RT))) * rstd;
+        const float d = dr != nullptr ? Elem<RT>::load(dr + c * int(sizeof(RT))) : 0.f;
+        Elem<RT>::store(out + c * int(sizeof(RT)), fmaf(rstd, fmaf(-n, dot, w[0] * dy), d));
+      }
+    }
+    stage = stage + 1 == kStages ? 0 : stage + 1;
+  }
+  grid_launch_dependents();
+  if constexpr (kRing) copy_wait<0>();
+  float* const sums = own_sums(p, smem, teams, team.id);
+#pragma unroll
+  for (int k = 0; k < kNU; ++k) {
+    const int c = k * kT + tid;
+    if (c < h) sums[c] = acc[k];
+  }
+  join_sums(p, smem, teams);
 }
 
 // dw[c] (+)= sum over the partial rows, in a fixed order: kRowLanes threads
@@ -263,52 +383,85 @@ __global__ void __launch_bounds__(kColumns * kRowLanes) rmsnorm_weight_kernel(co
   if (x == 0 && col < h) dw[col] = accumulate ? dw[col] + v : v;
 }
 
-template <typename GT, typename RT, int U, int NU, int kStages, int kMaxT, int kCtas, int kT, bool kKeep>
+constexpr int kMaxSmem = 200 * 1024;  // dynamic shared memory of a CTA
+
+template <typename GT, typename RT, int NU, int kStages, int kMaxT, bool kKeep>
 cudaError_t launch(const RmsNormBwdParams& p, int team_threads, int sms, cudaStream_t st, int* parts) {
-  const auto kernel = rmsnorm_backward_kernel<GT, RT, U, NU, kStages, kMaxT, kCtas, kT, kKeep>;
+  const auto kernel = rmsnorm_backward_kernel<GT, RT, NU, kStages, kMaxT, kKeep>;
+  if (sms == 0) return cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kMaxSmem);  // set-up
   const int teams = team_threads < kMaxT ? kMaxT / team_threads : 1, threads = team_threads * teams;
-  constexpr size_t kStageBytes = size_t(NU) * (kParts<GT, U> + 2 * kParts<RT, U>)*kSlotBytes<U>;  // of a thread
-  static_assert(kStages * kStageBytes * kMaxT * kCtas <= 227 * 1024 - kCtas * 8192, "the rings fit an SM");
+  constexpr size_t kStageBytes = size_t(NU) * (kParts<GT> + 2 * kParts<RT>)*16;  // of a thread
+  static_assert(kStages * kStageBytes * kMaxT <= kMaxSmem && NU * 8 * 4 * kMaxT <= kMaxSmem, "fits an SM");
   size_t smem = kStages * kStageBytes * threads;
   const size_t sums = teams > 1 ? size_t(teams) * p.h * sizeof(float) : 0;
   if (sums > smem) smem = sums;
-  if (sms == 0) {  // device set-up: room for the ring, and for a row of sums a team
-    const size_t ring = kStages * kStageBytes * kMaxT, most = size_t(kMaxT) * NU * U * sizeof(float);
-    return cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, int(ring > most ? ring : most));
-  }
   const long long rows = (p.s + teams - 1) / teams;
-  const int most = sms * kCtas < kRmsMaxParts ? sms * kCtas : kRmsMaxParts;
-  *parts = int(rows < most ? rows : most);
+  *parts = int(rows < sms ? rows : sms);
   kernel<<<*parts, threads, smem, st>>>(p, team_threads);
   return cudaGetLastError();
+}
+
+template <typename GT, typename RT, int kT, int kStages>
+cudaError_t launch_odd(const RmsNormBwdParams& p, const OddRing& ring, int teams, int sms, cudaStream_t st, int* parts) {
+  const auto kernel = rmsnorm_backward_odd_kernel<GT, RT, kT, kStages>;
+  if (sms == 0) return cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kMaxSmem);
+  size_t smem = size_t(teams) * kStages * ring.row_bytes(p.dres != nullptr);
+  const size_t sums = teams > 1 ? size_t(teams) * p.h * sizeof(float) : 0;
+  if (sums > smem) smem = sums;
+  const long long rows = (p.s + teams - 1) / teams;
+  *parts = int(rows < sms ? rows : sms);
+  kernel<<<*parts, kT * teams, smem, st>>>(p, ring);
+  return cudaGetLastError();
+}
+
+// As many teams as 512 threads and the rings allow: three rows each where that
+// leaves eight warps at work, else two, else no ring.
+template <typename GT, typename RT, int kT>
+cudaError_t pick_odd(const RmsNormBwdParams& p, int sms, cudaStream_t st, int* parts) {
+  const auto room = [&](int element) { return (p.h * element + 15 + 15) / 16 * 16; };
+  const OddRing ring = {room(sizeof(GT)), room(sizeof(RT))};
+  const int most = kT >= 512 ? 1 : 512 / kT, row = ring.row_bytes(p.dres != nullptr);
+  const auto fit = [&](int stages) {
+    const int n = kMaxSmem / (stages * row);
+    return n < most ? n : most;
+  };
+  if (sms == 0) {
+    cudaError_t e = launch_odd<GT, RT, kT, 3>(p, ring, 1, 0, st, parts);
+    if (e == cudaSuccess) e = launch_odd<GT, RT, kT, 2>(p, ring, 1, 0, st, parts);
+    return e == cudaSuccess ? launch_odd<GT, RT, kT, 0>(p, ring, 1, 0, st, parts) : e;
+  }
+  if (fit(3) * kT >= 256 || fit(3) == most) return launch_odd<GT, RT, kT, 3>(p, ring, fit(3), sms, st, parts);
+  if (fit(2) >= 1) return launch_odd<GT, RT, kT, 2>(p, ring, fit(2), sms, st, parts);
+  return launch_odd<GT, RT, kT, 0>(p, ring, most, sms, st, parts);
 }
 
 template <typename GT, typename RT>
 cudaError_t pick(const RmsNormBwdParams& p, bool vectors, int sms, cudaStream_t st, int* parts) {
   const int h = p.h;
-  constexpr bool kSmall = sizeof(GT) + 2 * sizeof(RT) <= 6;  // a ring of bf16 rows holds twice as many
-  const auto whole_warps = [](int n) { return (n + 31) / 32 * 32; };
   if (vectors) {
+    constexpr bool kSmall = sizeof(GT) + 2 * sizeof(RT) <= 6;  // a ring of bf16 rows holds twice as many
+    const auto whole_warps = [](int n) { return (n + 31) / 32 * 32; };
     const int units = h / 8;
-    if (units <= 32) return launch<GT, RT, 8, 1, kSmall ? 8 : 4, 512, 1, 32, true>(p, 32, sms, st, parts);
+    if (units <= 32) return launch<GT, RT, 1, kSmall ? 8 : 4, 512, true>(p, 32, sms, st, parts);
     if (units <= 1024)
-      return launch<GT, RT, 8, 2, kSmall ? 4 : 2, 512, 1, 0, true>(p, whole_warps((units + 1) / 2), sms, st, parts);
+      return launch<GT, RT, 2, kSmall ? 4 : 2, 512, true>(p, whole_warps((units + 1) / 2), sms, st, parts);
     if (units <= 2048)
-      return launch<GT, RT, 8, 4, kSmall ? 2 : 1, 512, 1, 0, false>(p, whole_warps((units + 3) / 4), sms, st, parts);
-    return launch<GT, RT, 8, 4, kSmall ? 1 : 0, 1024, 1, 0, false>(p, whole_warps((units + 3) / 4), sms, st, parts);
+      return launch<GT, RT, 4, kSmall ? 2 : 1, 512, false>(p, whole_warps((units + 3) / 4), sms, st, parts);
+    return launch<GT, RT, 4, kSmall ? 1 : 0, 1024, false>(p, whole_warps((units + 3) / 4), sms, st, parts);
   }
-  constexpr int kAhead = sizeof(GT) == 4 ? 2 : 0;  // cp.async has no 2-byte form
-  if (h <= 256) return launch<GT, RT, 1, 8, kAhead, 512, 2, 32, true>(p, 32, sms, st, parts);
-  if (h <= 1024) return launch<GT, RT, 1, 8, kAhead, 512, 2, 128, true>(p, 128, sms, st, parts);
-  if (h <= 4096) return launch<GT, RT, 1, 8, kAhead, 512, 2, 512, true>(p, 512, sms, st, parts);
-  return launch<GT, RT, 1, 32, 0, 1024, 1, 0, false>(p, whole_warps((h + 31) / 32), sms, st, parts);
+  if (h <= 1024) return pick_odd<GT, RT, 32>(p, sms, st, parts);
+  if (h <= 2048) return pick_odd<GT, RT, 64>(p, sms, st, parts);
+  if (h <= 4096) return pick_odd<GT, RT, 128>(p, sms, st, parts);
+  if (h <= 8192) return pick_odd<GT, RT, 256>(p, sms, st, parts);
+  if (h <= 16384) return pick_odd<GT, RT, 512>(p, sms, st, parts);
+  return pick_odd<GT, RT, 1024>(p, sms, st, parts);
 }
 
 // one call of each kind of row, with no SMs
 template <typename GT, typename RT> cudaError_t set_up() {
   RmsNormBwdParams p = {};
   cudaError_t e = cudaSuccess;
-  for (int h : {256, 1024, 4096, 8192, 16384, VPCE_MAX_NORM_COLUMNS}) {
+  for (int h : {256, 1024, 2048, 4096, 8192, 16384, VPCE_MAX_NORM_COLUMNS}) {
     p.h = h;
     for (const bool vectors : {false, true})
       if (e == cudaSuccess) e = pick<GT, RT>(p, vectors, 0, nullptr, nullptr);
