@@ -23,9 +23,7 @@ __device__ __forceinline__ void store_codes(unsigned char* p, const float (&v)[8
   const uint32_t b = e4m3x2(v[4], v[5]) | uint32_t(e4m3x2(v[6], v[7])) << 16;
   *reinterpret_cast<uint2*>(p) = make_uint2(a, b);
 }
-__device__ __forceinline__ void store_codes(unsigned char* p, const float (&v)[1]) {
-  *p = (unsigned char)(e4m3x2(v[0], 0.f) & 0xff);
-}
+__device__ __forceinline__ void store_code(unsigned char* p, float v) { *p = (unsigned char)(e4m3x2(v, 0.f) & 0xff); }
 
 // |v| as ordered bits: infinities above every number, NaN above them, so that
 // a maximum of these bits carries a NaN on.
@@ -49,26 +47,64 @@ __device__ __forceinline__ float group_scale(unsigned top) {
 // row), or through shared memory.
 enum GroupKind { kNoCodes, kLanes, kRow, kShared };
 
-// kT: threads of a team, known when compiled (single elements: their addresses
-// are then one register and constants), or 0.
-template <typename XT, typename RT, GroupKind kGroups, int U, int NU, bool kWarp, int kMaxT, int kT>
-__global__ void __launch_bounds__(kMaxT, U == 1 ? (kMaxT < 512 ? 512 / kMaxT : 1) : kMaxT == 256 ? 3 : 1) rmsnorm_forward_kernel(const __grid_constant__ RmsNormParams p) {
-  extern __shared__ unsigned top_sm[];  // [teams][2][2][groups], kShared only
+// Per team, twice (the rows alternate: who still reads one row's is at most a
+// barrier behind whoever writes the next row's): the groups' maxima, then their
+// scales, and the reciprocals of those.
+struct SharedGroups {
+  unsigned* top;
+  float* inverse;
+  __device__ __forceinline__ SharedGroups(unsigned* sm, int team, int parity, int groups)
+      : top(sm + (team * 2 + parity) * 2 * groups), inverse(reinterpret_cast<float*>(top + groups)) {}
+  __device__ __forceinline__ void clear(int groups, int tid, int T) const {
+    for (int g = tid; g < groups; g += T) top[g] = 0;
+  }
+  __device__ __forceinline__ void scales(int groups, int tid, int T, float* out) const {
+    for (int g = tid; g < groups; g += T) {
+      const float scale = group_scale(top[g]);
+      out[g] = scale;
+      top[g] = __float_as_uint(scale);
+      inverse[g] = __fdiv_rn(1.f, scale);
+    }
+  }
+};
+
+template <bool kWarp> __device__ __forceinline__ void team_sync() {
+  if constexpr (kWarp) __syncwarp();
+  else __syncthreads();
+}
+
+// Largest of a team's values; every thread gets it.
+template <bool kWarp> __device__ __forceinline__ unsigned team_max(unsigned v, unsigned* sm) {
+  v = __reduce_max_sync(kFull, v);
+  if constexpr (!kWarp) {
+    const int lane = threadIdx.x & 31, warps = blockDim.x >> 5;
+    if (lane == 0) sm[threadIdx.x >> 5] = v;
+    __syncthreads();
+    v = __reduce_max_sync(kFull, lane < warps ? sm[lane] : 0u);
+  }
+  return v;
+}
+
+__device__ __forceinline__ int group_of(const RmsNormParams& p, int c) { return int(__umulhi(unsigned(c), p.group_inverse)); }
+
+// Rows of 16-byte vectors: a warp (four a CTA) or a CTA a row, NU units of eight
+// columns a thread.
+template <typename XT, typename RT, GroupKind kGroups, int NU, bool kWarp, int kMaxT>
+__global__ void __launch_bounds__(kMaxT, kMaxT == 256 ? 3 : 1) rmsnorm_forward_kernel(const __grid_constant__ RmsNormParams p) {
+  extern __shared__ unsigned group_sm[];  // [teams][2][2][groups], kShared only
   __shared__ float red[2][32];
   [[maybe_unused]] __shared__ unsigned top_row[2][32];
+  constexpr int U = 8;
   const int lane = threadIdx.x & 31;
   const int team = kWarp ? int(threadIdx.x >> 5) : 0, teams = kWarp ? int(blockDim.x >> 5) : 1;
-  const int tid = kWarp ? lane : int(threadIdx.x), T = kT > 0 ? kT : int(blockDim.x);
-  // (elements past the row are skipped by all of a team's threads)
-  const auto past = [&](int k) { return U == 1 && k * T >= p.h; };
+  const int tid = kWarp ? lane : int(threadIdx.x), T = kWarp ? 32 : int(blockDim.x);
   int parity = 0;
-  for (long long row = (long long)blockIdx.x * teams + team; row < p.s; row += (long long)gridDim.x * teams) {
+  for (long long row = (long long)blockIdx.x * teams + team; row < p.s; row += (long long)gridDim.x * teams, parity ^= 1) {
     const unsigned char* xr = p.x + row * p.ld_x;
-    RawUnit<XT, U> a[NU];
-    RawUnit<RT, U> b[NU];
+    RawUnit<XT> a[NU];
+    RawUnit<RT> b[NU];
 #pragma unroll
     for (int k = 0; k < NU; ++k) {
-      if (past(k)) break;
       const int c = (k * T + tid) * U;
       a[k].zero();
       if (c < p.h) a[k].load(xr, c);
@@ -77,7 +113,6 @@ __global__ void __launch_bounds__(kMaxT, U == 1 ? (kMaxT < 512 ? 512 / kMaxT : 1
       const unsigned char* rr = p.res + row * p.ld_res;
 #pragma unroll
       for (int k = 0; k < NU; ++k) {
-        if (past(k)) break;
         const int c = (k * T + tid) * U;
         b[k].zero();
         if (c < p.h) b[k].load(rr, c);
@@ -86,7 +121,6 @@ __global__ void __launch_bounds__(kMaxT, U == 1 ? (kMaxT < 512 ? 512 / kMaxT : 1
     float r[NU][U], ss = 0.f;
 #pragma unroll
     for (int k = 0; k < NU; ++k) {
-      if (past(k)) break;
       const int c = (k * T + tid) * U;
       a[k].get(r[k]);
       if (p.res != nullptr) {
@@ -99,14 +133,9 @@ __global__ void __launch_bounds__(kMaxT, U == 1 ? (kMaxT < 512 ? 512 / kMaxT : 1
 #pragma unroll
       for (int j = 0; j < U; ++j) ss = fmaf(r[k][j], r[k][j], ss);
     }
-    // the two buffers alternate: who still reads one row's is at most a
-    // barrier behind whoever writes the next row's
-    [[maybe_unused]] unsigned* top = nullptr;
-    [[maybe_unused]] float* inverse = nullptr;
+    const SharedGroups shared(group_sm, team, parity, p.groups);
     if constexpr (kGroups == kShared) {
-      top = top_sm + (team * 2 + parity) * 2 * p.groups;
-      inverse = reinterpret_cast<float*>(top + p.groups);
-      for (int g = tid; g < p.groups; g += T) top[g] = 0;
+      shared.clear(p.groups, tid, T);
       if constexpr (kWarp) __syncwarp();
     }
     ss = team_sum<kWarp>(ss, red[parity]);
@@ -115,10 +144,8 @@ __global__ void __launch_bounds__(kMaxT, U == 1 ? (kMaxT < 512 ? 512 / kMaxT : 1
     [[maybe_unused]] unsigned m[NU], all = 0;
 #pragma unroll
     for (int k = 0; k < NU; ++k) {
-      if (past(k)) break;
       const int c = (k * T + tid) * U;
       m[k] = 0;
-      const int group = kGroups == kShared || kGroups == kLanes ? int(__umulhi(unsigned(c), p.group_inverse)) : 0;
       if (c < p.h) {
         float w[U];
         load_weight(p.w, p.w_bf16, c, w);
@@ -129,18 +156,8 @@ __global__ void __launch_bounds__(kMaxT, U == 1 ? (kMaxT < 512 ? 512 / kMaxT : 1
         } else {
 #pragma unroll
           for (int j = 0; j < U; ++j) m[k] = max(m[k], mag(r[k][j]));
-          if constexpr (kGroups == kRow) all = max(all, m[k]);
-        }
-      }
-      if constexpr (kGroups == kShared) {
-        // (atomics on shared memory; their order does not matter)
-        if (U == 1) {
-          // 32 consecutive columns: of one group, or 16 and 16 of one each
-          const unsigned half = p.group % 32 == 0 ? kFull : lane < 16 ? 0xffffu : 0xffff0000u;
-          const unsigned t = __reduce_max_sync(half, m[k]);
-          if ((lane == 0 || (lane == 16 && half != kFull)) && c < p.h) atomicMax(top + group, t);
-        } else if (c < p.h) {
-          atomicMax(top + group, m[k]);
+          if constexpr (kGroups == kShared) atomicMax(shared.top + group_of(p, c), m[k]);  // (the order does not matter)
+          all = max(all, m[k]);
         }
       }
     }
@@ -153,50 +170,30 @@ __global__ void __launch_bounds__(kMaxT, U == 1 ? (kMaxT < 512 ? 512 / kMaxT : 1
           for (int k = 0; k < NU; ++k) m[k] = max(m[k], __shfl_xor_sync(kFull, m[k], o));
         }
       }
-    } else if constexpr (kGroups == kRow) {
-      all = __reduce_max_sync(kFull, all);
-      if constexpr (!kWarp) {
-        const int warps = T >> 5;
-        if (lane == 0) top_row[parity][threadIdx.x >> 5] = all;
-        __syncthreads();
-        all = __reduce_max_sync(kFull, lane < warps ? top_row[parity][lane] : 0u);
-      }
     } else if constexpr (kGroups == kShared) {
-      // each group's scale and its reciprocal, in the maximum's place
-      if constexpr (kWarp) __syncwarp();
-      else __syncthreads();
-      for (int g = tid; g < p.groups; g += T) {
-        const float scale = group_scale(top[g]);
-        p.scale[row * p.groups + g] = scale;
-        top[g] = __float_as_uint(scale);
-        inverse[g] = __fdiv_rn(1.f, scale);
-      }
-      if constexpr (kWarp) __syncwarp();
-      else __syncthreads();
+      team_sync<kWarp>();
+      shared.scales(p.groups, tid, T, p.scale + row * p.groups);
+      team_sync<kWarp>();
     }
     if constexpr (kGroups != kNoCodes) {
       [[maybe_unused]] float row_scale = 0.f, row_inv = 0.f;
       if constexpr (kGroups == kRow) {
-        row_scale = group_scale(all);
+        row_scale = group_scale(team_max<kWarp>(all, top_row[parity]));
         row_inv = __fdiv_rn(1.f, row_scale);
         if (tid == 0) p.scale[row] = row_scale;
       }
 #pragma unroll
       for (int k = 0; k < NU; ++k) {
-        if (past(k)) break;
         const int c = (k * T + tid) * U;
         if (c < p.h) {
-          float scale, inv;
-          if constexpr (kGroups == kRow) {
-            scale = row_scale, inv = row_inv;
-          } else {
-            const int g = int(__umulhi(unsigned(c), p.group_inverse));
-            if constexpr (kGroups == kShared) {
-              scale = __uint_as_float(top[g]), inv = inverse[g];
-            } else {
-              scale = group_scale(m[k]), inv = __fdiv_rn(1.f, scale);
-              if (c == g * p.group) p.scale[row * p.groups + g] = scale;
-            }
+          float scale = row_scale, inv = row_inv;
+          if constexpr (kGroups == kShared) {
+            const int g = group_of(p, c);
+            scale = __uint_as_float(shared.top[g]), inv = shared.inverse[g];
+          } else if constexpr (kGroups == kLanes) {
+            const int g = group_of(p, c);
+            scale = group_scale(m[k]), inv = __fdiv_rn(1.f, scale);
+            if (c == g * p.group) p.scale[row * p.groups + g] = scale;
           }
 #pragma unroll
           for (int j = 0; j < U; ++j) r[k][j] = quotient(r[k][j], isinf(scale) ? 0.f : scale, inv);
@@ -204,17 +201,103 @@ __global__ void __launch_bounds__(kMaxT, U == 1 ? (kMaxT < 512 ? 512 / kMaxT : 1
         }
       }
     }
-    parity ^= 1;
   }
 }
 
-template <typename XT, typename RT, GroupKind kGroups, int U, int NU, bool kWarp, int kMaxT = 128, int kT = kWarp ? 32 : 0>
-void launch(const RmsNormParams& p, int threads, int sms, cudaStream_t st) {
-  const int teams = kWarp ? 4 : 1;
+// Rows off 16 bytes, element by element: kT threads a row, few of them, since
+// what a row costs besides its elements (sums, addresses) is paid by every warp.
+template <typename XT, typename RT, GroupKind kGroups, int kT>
+__global__ void __launch_bounds__(kT == 32 ? 128 : kT, kT >= 512 ? 1 : kT == 32 ? 4 : 512 / kT)
+    rmsnorm_forward_odd_kernel(const __grid_constant__ RmsNormParams p) {
+  extern __shared__ unsigned group_sm[];
+  __shared__ float red[2][32];
+  [[maybe_unused]] __shared__ unsigned top_row[2][32];
+  constexpr bool kWarp = kT == 32;
+  constexpr int XB = Elem<XT>::kBytes, RB = Elem<RT>::kBytes;
+  const int lane = threadIdx.x & 31, h = p.h;
+  const int team = kWarp ? int(threadIdx.x >> 5) : 0, teams = kWarp ? 4 : 1;
+  const int tid = kWarp ? lane : int(threadIdx.x);
+  int parity = 0;
+  for (long long row = (long long)blockIdx.x * teams + team; row < p.s; row += (long long)gridDim.x * teams, parity ^= 1) {
+    const unsigned char* const xr = p.x + row * p.ld_x;
+    float r[kOddColumns], ss = 0.f;
+    odd_columns<kT>(h, tid, [&](int k, int c, bool) { r[k] = Elem<XT>::load(xr + c * XB); });
+    if (p.res != nullptr) {
+      const unsigned char* const rr = p.res + row * p.ld_res;
+      unsigned char* const to = p.res_out + row * p.ld_res_out;
+      odd_columns<kT>(h, tid, [&](int k, int c, bool) { r[k] += Elem<RT>::load(rr + c * RB); });
+      // (in place, column 0 is written only after every lane has read it)
+      team_sync<kWarp>();
+      odd_columns<kT>(h, tid, [&](int k, int c, bool inside) {
+        if (inside) Elem<RT>::store(to + c * RB, r[k]);
+      });
+    }
+    odd_columns<kT>(h, tid, [&](int k, int, bool inside) { ss = inside ? fmaf(r[k], r[k], ss) : ss; });
+    const SharedGroups shared(group_sm, team, parity, p.groups);
+    if constexpr (kGroups == kShared) {
+      shared.clear(p.groups, tid, kT);
+      if constexpr (kWarp) __syncwarp();
+    }
+    ss = team_sum<kWarp>(ss, red[parity]);
+    const float rstd = rsqrtf(ss / float(h) + p.eps);
+    if (tid == 0 && p.rstd != nullptr) p.rstd[row] = rstd;
+    unsigned char* const out = p.out + row * p.ld_out;
+    [[maybe_unused]] unsigned all = 0;
+    odd_columns<kT>(h, tid, [&](int k, int c, bool inside) {
+      r[k] = r[k] * rstd * load_weight(p.w, p.w_bf16, c);
+      if constexpr (kGroups == kNoCodes) {
+        if (inside) Elem<XT>::store(out + c * XB, r[k]);
+      } else if constexpr (kGroups == kRow) {
+        all = max(all, inside ? mag(r[k]) : 0u);
+      } else {
+        // 32 consecutive columns: of one group, or 16 and 16 of one each
+        // (atomics on shared memory; their order does not matter)
+        const unsigned half = p.group % 32 == 0 ? kFull : lane < 16 ? 0xffffu : 0xffff0000u;
+        const unsigned t = __reduce_max_sync(half, inside ? mag(r[k]) : 0u);
+        if (inside && (lane == 0 || (lane == 16 && half != kFull))) atomicMax(shared.top + group_of(p, c), t);
+      }
+    });
+    if constexpr (kGroups == kRow) {
+      const float scale = group_scale(team_max<kWarp>(all, top_row[parity])), inv = __fdiv_rn(1.f, scale);
+      const float s = isinf(scale) ? 0.f : scale;
+      if (tid == 0) p.scale[row] = scale;
+      odd_columns<kT>(h, tid, [&](int k, int c, bool inside) {
+        if (inside) store_code(out + c, quotient(r[k], s, inv));
+      });
+    } else if constexpr (kGroups == kShared) {
+      team_sync<kWarp>();
+      shared.scales(p.groups, tid, kT, p.scale + row * p.groups);
+      team_sync<kWarp>();
+      odd_columns<kT>(h, tid, [&](int k, int c, bool inside) {
+        const int g = group_of(p, c);
+        const float scale = __uint_as_float(shared.top[g]);
+        if (inside) store_code(out + c, quotient(r[k], isinf(scale) ? 0.f : scale, shared.inverse[g]));
+      });
+    }
+  }
+}
+
+template <typename P> size_t group_bytes(GroupKind kind, int teams, const P& p) {
+  return kind == kShared ? size_t(teams) * 4 * p.groups * sizeof(unsigned) : 0;
+}
+
+int row_grid(const RmsNormParams& p, int teams, int sms) {
   const long long rows = (p.s + teams - 1) / teams, most = (long long)sms * 64;
-  const size_t smem = kGroups == kShared ? size_t(teams) * 4 * p.groups * sizeof(unsigned) : 0;
-  rmsnorm_forward_kernel<XT, RT, kGroups, U, NU, kWarp, kMaxT, kT>
-      <<<int(rows < most ? rows : most), kWarp ? 128 : threads, smem, st>>>(p);
+  return int(rows < most ? rows : most);
+}
+
+template <typename XT, typename RT, GroupKind kGroups, int NU, bool kWarp, int kMaxT = 128>
+void launch(const RmsNormParams& p, int threads, int sms, cudaStream_t st) {
+  constexpr int kTeams = kWarp ? 4 : 1;
+  rmsnorm_forward_kernel<XT, RT, kGroups, NU, kWarp, kMaxT>
+      <<<row_grid(p, kTeams, sms), kWarp ? 128 : threads, group_bytes(kGroups, kTeams, p), st>>>(p);
+}
+
+template <typename XT, typename RT, GroupKind kGroups, int kT>
+void launch_odd(const RmsNormParams& p, int sms, cudaStream_t st) {
+  constexpr int kTeams = kT == 32 ? 4 : 1;
+  rmsnorm_forward_odd_kernel<XT, RT, kGroups, kT>
+      <<<row_grid(p, kTeams, sms), kT == 32 ? 128 : kT, group_bytes(kGroups, kTeams, p), st>>>(p);
 }
 
 template <typename XT, typename RT, GroupKind kGroups>
@@ -222,23 +305,21 @@ void pick(const RmsNormParams& p, bool vectors, int sms, cudaStream_t st) {
   const int h = p.h;
   if (vectors) {
     const int units = h / 8;
-    if (units <= 32) return launch<XT, RT, kGroups, 8, 1, true>(p, 32, sms, st);
-    if (units <= 128) return launch<XT, RT, kGroups, 8, 4, true>(p, 32, sms, st);
+    if (units <= 32) return launch<XT, RT, kGroups, 1, true>(p, 32, sms, st);
+    if (units <= 128) return launch<XT, RT, kGroups, 4, true>(p, 32, sms, st);
     const int threads = ((units + 3) / 4 + 31) / 32 * 32;
     // (at most 85 registers a thread: three CTAs of 256 on an SM)
-    if (threads <= 256) return launch<XT, RT, kGroups, 8, 4, false, 256>(p, threads, sms, st);
-    if (threads <= 512) return launch<XT, RT, kGroups, 8, 4, false, 512>(p, threads, sms, st);
-    return launch<XT, RT, kGroups, 8, 4, false, 1024>(p, threads, sms, st);
+    if (threads <= 256) return launch<XT, RT, kGroups, 4, false, 256>(p, threads, sms, st);
+    if (threads <= 512) return launch<XT, RT, kGroups, 4, false, 512>(p, threads, sms, st);
+    return launch<XT, RT, kGroups, 4, false, 1024>(p, threads, sms, st);
   }
   if constexpr (kGroups != kLanes) {
-    // few warps a row: what a row costs besides its elements (sums, addresses)
-    // is paid by every one of them
-    if (h <= 1024) return launch<XT, RT, kGroups, 1, 32, true>(p, 32, sms, st);
-    if (h <= 2048) return launch<XT, RT, kGroups, 1, 32, false, 64, 64>(p, 64, sms, st);
-    if (h <= 4096) return launch<XT, RT, kGroups, 1, 32, false, 128, 128>(p, 128, sms, st);
-    if (h <= 8192) return launch<XT, RT, kGroups, 1, 32, false, 256, 256>(p, 256, sms, st);
-    if (h <= 16384) return launch<XT, RT, kGroups, 1, 32, false, 512, 512>(p, 512, sms, st);
-    launch<XT, RT, kGroups, 1, 32, false, 1024, 1024>(p, 1024, sms, st);
+    if (h <= 1024) return launch_odd<XT, RT, kGroups, 32>(p, sms, st);
+    if (h <= 2048) return launch_odd<XT, RT, kGroups, 64>(p, sms, st);
+    if (h <= 4096) return launch_odd<XT, RT, kGroups, 128>(p, sms, st);
+    if (h <= 8192) return launch_odd<XT, RT, kGroups, 256>(p, sms, st);
+    if (h <= 16384) return launch_odd<XT, RT, kGroups, 512>(p, sms, st);
+    launch_odd<XT, RT, kGroups, 1024>(p, sms, st);
   }
 }
 

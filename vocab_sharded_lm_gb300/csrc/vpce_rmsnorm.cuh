@@ -48,10 +48,9 @@ struct RmsNormBwdParams {
 // CTAs whose sums of the weight's gradient the workspace holds.
 constexpr int kRmsMaxParts = 1024;
 
-// U consecutive elements of a row as they lie in memory: 8 in 16-byte vectors,
-// or one.
-template <typename T, int U> struct RawUnit;
-template <> struct RawUnit<float, 8> {
+// Eight consecutive elements of a row as they lie in memory, in 16-byte vectors.
+template <typename T> struct RawUnit;
+template <> struct RawUnit<float> {
   uint4 a, b;
   __device__ __forceinline__ void load(const unsigned char* row, int c) {
     const uint4* p = reinterpret_cast<const uint4*>(row + size_t(c) * 4);
@@ -69,7 +68,7 @@ template <> struct RawUnit<float, 8> {
   }
   __device__ __forceinline__ void zero() { a = b = make_uint4(0, 0, 0, 0); }
 };
-template <> struct RawUnit<__nv_bfloat16, 8> {
+template <> struct RawUnit<__nv_bfloat16> {
   uint4 a;
   __device__ __forceinline__ void load(const unsigned char* row, int c) {
     a = *reinterpret_cast<const uint4*>(row + size_t(c) * 2);
@@ -78,23 +77,6 @@ template <> struct RawUnit<__nv_bfloat16, 8> {
   __device__ __forceinline__ void get(float (&v)[8]) const { unpack(a, v, __nv_bfloat16()); }
   __device__ __forceinline__ void zero() { a = make_uint4(0, 0, 0, 0); }
 };
-template <> struct RawUnit<float, 1> {
-  float a;
-  __device__ __forceinline__ void load(const unsigned char* row, int c) {
-    a = *reinterpret_cast<const float*>(row + size_t(c) * 4);
-  }
-  __device__ __forceinline__ void get(float (&v)[1]) const { v[0] = a; }
-  __device__ __forceinline__ void zero() { a = 0.f; }
-};
-template <> struct RawUnit<__nv_bfloat16, 1> {
-  unsigned short a;
-  __device__ __forceinline__ void load(const unsigned char* row, int c) {
-    a = *reinterpret_cast<const unsigned short*>(row + size_t(c) * 2);
-  }
-  __device__ __forceinline__ void get(float (&v)[1]) const { v[0] = __uint_as_float(uint32_t(a) << 16); }
-  __device__ __forceinline__ void zero() { a = 0; }
-};
-
 __device__ __forceinline__ void store_unit(unsigned char* row, int c, const float (&v)[8], float) {
   uint4* p = reinterpret_cast<uint4*>(row + size_t(c) * 4);
   p[0] = make_uint4(__float_as_uint(v[0]), __float_as_uint(v[1]), __float_as_uint(v[2]), __float_as_uint(v[3]));
@@ -103,26 +85,40 @@ __device__ __forceinline__ void store_unit(unsigned char* row, int c, const floa
 __device__ __forceinline__ void store_unit(unsigned char* row, int c, const float (&v)[8], __nv_bfloat16 t) {
   *reinterpret_cast<uint4*>(row + size_t(c) * 2) = pack(v, t);
 }
-__device__ __forceinline__ void store_unit(unsigned char* row, int c, const float (&v)[1], float) {
-  Elem<float>::store(row + size_t(c) * 4, v[0]);
+// The weights of eight columns, or one, through the read-only path (every row reads them).
+__device__ __forceinline__ void load_weight(const unsigned char* w, int w_bf16, int c, float (&v)[8]) {
+  if (w_bf16) {
+    unpack(__ldg(reinterpret_cast<const uint4*>(w + size_t(c) * 2)), v, __nv_bfloat16());
+  } else {
+    const float4* p = reinterpret_cast<const float4*>(w + size_t(c) * 4);
+    const float4 a = __ldg(p), b = __ldg(p + 1);
+    v[0] = a.x, v[1] = a.y, v[2] = a.z, v[3] = a.w, v[4] = b.x, v[5] = b.y, v[6] = b.z, v[7] = b.w;
+  }
 }
-__device__ __forceinline__ void store_unit(unsigned char* row, int c, const float (&v)[1], __nv_bfloat16) {
-  Elem<__nv_bfloat16>::store(row + size_t(c) * 2, v[0]);
+__device__ __forceinline__ float load_weight(const unsigned char* w, int w_bf16, int c) {
+  return w_bf16 ? __uint_as_float(uint32_t(__ldg(reinterpret_cast<const unsigned short*>(w) + c)) << 16)
+                : __ldg(reinterpret_cast<const float*>(w) + c);
 }
 
-// The weights of U columns, through the read-only path (every row reads them).
-template <int U> __device__ __forceinline__ void load_weight(const unsigned char* w, int w_bf16, int c, float (&v)[U]) {
-  if constexpr (U == 8) {
-    if (w_bf16) {
-      unpack(__ldg(reinterpret_cast<const uint4*>(w + size_t(c) * 2)), v, __nv_bfloat16());
+// Rows off 16 bytes: kT threads take column k kT + tid, k < kOddColumns.  Calls
+// f(k, c, inside) for every k that has columns, four at a time without a branch
+// between them (so that their loads go together): for the last four, `inside`
+// may be false, and c is then 0.
+constexpr int kOddColumns = 32;
+template <int kT, typename F> __device__ __forceinline__ void odd_columns(int h, int tid, F f) {
+#pragma unroll
+  for (int k = 0; k < kOddColumns; k += 4) {
+    if (k * kT >= h) break;
+    if ((k + 4) * kT <= h) {
+#pragma unroll
+      for (int i = 0; i < 4; ++i) f(k + i, (k + i) * kT + tid, true);
     } else {
-      const float4* p = reinterpret_cast<const float4*>(w + size_t(c) * 4);
-      const float4 a = __ldg(p), b = __ldg(p + 1);
-      v[0] = a.x, v[1] = a.y, v[2] = a.z, v[3] = a.w, v[4] = b.x, v[5] = b.y, v[6] = b.z, v[7] = b.w;
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        const int c = (k + i) * kT + tid;
+        f(k + i, c < h ? c : 0, c < h);
+      }
     }
-  } else {
-    v[0] = w_bf16 ? __uint_as_float(uint32_t(__ldg(reinterpret_cast<const unsigned short*>(w) + c)) << 16)
-                  : __ldg(reinterpret_cast<const float*>(w) + c);
   }
 }
 

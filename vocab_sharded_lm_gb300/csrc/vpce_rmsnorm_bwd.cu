@@ -142,20 +142,20 @@ __global__ void __launch_bounds__(kMaxT, 1) rmsnorm_backward_kernel(const __grid
   for (long long row = first; row < p.s; row += stride) {
     const float rstd = next_rstd;
     if (row + stride < p.s) next_rstd = __ldg(p.rstd + row + stride);
-    const auto load_g = [&](RawUnit<GT, U>& g, int k, int c) {
+    const auto load_g = [&](RawUnit<GT>& g, int k, int c) {
       if constexpr (kRing) g.take(slot(stage, k * kG), blockDim.x);
       else g.load(p.dy + row * p.ld_dy, c);
     };
-    const auto load_x = [&](RawUnit<RT, U>& x, int k, int c) {
+    const auto load_x = [&](RawUnit<RT>& x, int k, int c) {
       if constexpr (kRing) x.take(slot(stage, NU * kG + k * kR), blockDim.x);
       else x.load(p.x + row * p.ld_x, c);
     };
-    const auto load_d = [&](RawUnit<RT, U>& d, int k, int c) {
+    const auto load_d = [&](RawUnit<RT>& d, int k, int c) {
       if constexpr (kRing) d.take(slot(stage, NU * (kG + kR) + k * kR), blockDim.x);
       else d.load(p.dres + row * p.ld_dres, c);
     };
     // t = w dy and n = r rstd of a unit
-    const auto terms = [&](int k, int c, const RawUnit<GT, U>& g, const RawUnit<RT, U>& x, float (&dy)[U], float (&t)[U],
+    const auto terms = [&](int k, int c, const RawUnit<GT>& g, const RawUnit<RT>& x, float (&dy)[U], float (&t)[U],
                            float (&n)[U]) {
       if constexpr (!kKeep) load_weight(p.w, p.w_bf16, c, w[0]);
       g.get(dy);
@@ -168,8 +168,8 @@ __global__ void __launch_bounds__(kMaxT, 1) rmsnorm_backward_kernel(const __grid
     };
     if constexpr (kRing) copy_wait<(kRing ? kStages - 1 : 0)>();
     constexpr int kKept = kKeep ? NU : 1;
-    RawUnit<GT, U> g[kKept];
-    RawUnit<RT, U> x[kKept], d[kKept];
+    RawUnit<GT> g[kKept];
+    RawUnit<RT> x[kKept], d[kKept];
     float t[kKept][U], n[kKept][U];
     if constexpr (kKeep) {
 #pragma unroll
@@ -255,7 +255,7 @@ template <typename GT, typename RT, int kT, int kStages>
 __global__ void __launch_bounds__(kT > 512 ? kT : 512, 1) rmsnorm_backward_odd_kernel(const __grid_constant__ RmsNormBwdParams p,
                                                                                      const OddRing ring) {
   extern __shared__ uint4 smem[];  // the rings [teams][kStages], and at the end sums [teams][h]
-  constexpr int kMaxTeams = kT > 512 ? 1 : 512 / kT, kNU = 32;
+  constexpr int kMaxTeams = kT > 512 ? 1 : 512 / kT, GB = Elem<GT>::kBytes, RB = Elem<RT>::kBytes;
   constexpr bool kRing = kStages > 0;
   __shared__ float red[kMaxTeams][2][32];
   Team team;
@@ -265,9 +265,13 @@ __global__ void __launch_bounds__(kT > 512 ? kT : 512, 1) rmsnorm_backward_odd_k
   team.threads = kT;
   team.red = &red[team.id][0][0];
   const int tid = team.tid, h = p.h;
-  float acc[kNU];
+  constexpr bool kHoldWeights = kT <= 512;  // (64 registers a thread otherwise)
+  float acc[kOddColumns], weight[kHoldWeights ? kOddColumns : 1];
 #pragma unroll
-  for (int k = 0; k < kNU; ++k) acc[k] = 0.f;
+  for (int k = 0; k < kOddColumns; ++k) acc[k] = 0.f;
+  if constexpr (kHoldWeights)
+    odd_columns<kT>(h, tid, [&](int k, int c, bool) { weight[k] = load_weight(p.w, p.w_bf16, c); });
+  const auto weight_of = [&](int k, int c) { return kHoldWeights ? weight[kHoldWeights ? k : 0] : load_weight(p.w, p.w_bf16, c); };
 
   const int stage_bytes = ring.row_bytes(p.dres != nullptr);
   unsigned char* const mine = reinterpret_cast<unsigned char*>(smem) + team.id * kStages * stage_bytes;
@@ -321,40 +325,29 @@ __global__ void __launch_bounds__(kT > 512 ? kT : 512, 1) rmsnorm_backward_odd_k
       if (dr != nullptr) dr = at + ring.dy_bytes + ring.x_bytes + (uintptr_t(dr) & 15);
     }
     float dot = 0.f;
-#pragma unroll
-    for (int k = 0; k < kNU; ++k) {
-      if (k * kT >= h) break;
-      const int c = k * kT + tid;
-      if (c < h) {
-        float w[1];
-        load_weight(p.w, p.w_bf16, c, w);
-        const float dy = Elem<GT>::load(gr + c * int(sizeof(GT))), n = Elem<RT>::load(xr + c * int(sizeof(RT))) * rstd;
-        acc[k] = fmaf(dy, n, acc[k]);
-        dot = fmaf(w[0] * dy, n, dot);
-      }
-    }
+    odd_columns<kT>(h, tid, [&](int k, int c, bool inside) {
+      const float dy = inside ? Elem<GT>::load(gr + c * GB) : 0.f, n = Elem<RT>::load(xr + c * RB) * rstd;
+      acc[k] = fmaf(dy, n, acc[k]);
+      dot = inside ? fmaf(weight_of(k, c) * dy, n, dot) : dot;
+    });
     dot = team.sum(dot, parity) / float(h);
     parity ^= 1;
     unsigned char* const out = p.dx + row * p.ld_dx;
-#pragma unroll
-    for (int k = 0; k < kNU; ++k) {
-      if (k * kT >= h) break;
-      const int c = k * kT + tid;
-      if (c < h) {
-        float w[1];
-        load_weight(p.w, p.w_bf16, c, w);
-        const float dy = Elem<GT>::load(gr + c * int(sizeof(GT))), n = Elem<RT>::load(xr + c * int(sizeof(RT))) * rstd;
-        const float d = dr != nullptr ? Elem<RT>::load(dr + c * int(sizeof(RT))) : 0.f;
-        Elem<RT>::store(out + c * int(sizeof(RT)), fmaf(rstd, fmaf(-n, dot, w[0] * dy), d));
+    const bool add = dr != nullptr;
+    odd_columns<kT>(h, tid, [&](int k, int c, bool inside) {
+      if (inside) {
+        const float dy = Elem<GT>::load(gr + c * GB), n = Elem<RT>::load(xr + c * RB) * rstd;
+        const float d = add ? Elem<RT>::load(dr + c * RB) : 0.f;
+        Elem<RT>::store(out + c * RB, fmaf(rstd, fmaf(-n, dot, weight_of(k, c) * dy), d));
       }
-    }
+    });
     stage = stage + 1 == kStages ? 0 : stage + 1;
   }
   grid_launch_dependents();
   if constexpr (kRing) copy_wait<0>();
   float* const sums = own_sums(p, smem, teams, team.id);
 #pragma unroll
-  for (int k = 0; k < kNU; ++k) {
+  for (int k = 0; k < kOddColumns; ++k) {
     const int c = k * kT + tid;
     if (c < h) sums[c] = acc[k];
   }
@@ -415,7 +408,7 @@ cudaError_t launch_odd(const RmsNormBwdParams& p, const OddRing& ring, int teams
 }
 
 // As many teams as 512 threads and the rings allow: three rows each where that
-// leaves eight warps at work, else two, else no ring.
+// leaves every team its ring, else two, else no ring.
 template <typename GT, typename RT, int kT>
 cudaError_t pick_odd(const RmsNormBwdParams& p, int sms, cudaStream_t st, int* parts) {
   const auto room = [&](int element) { return (p.h * element + 15 + 15) / 16 * 16; };
@@ -430,7 +423,7 @@ cudaError_t pick_odd(const RmsNormBwdParams& p, int sms, cudaStream_t st, int* p
     if (e == cudaSuccess) e = launch_odd<GT, RT, kT, 2>(p, ring, 1, 0, st, parts);
     return e == cudaSuccess ? launch_odd<GT, RT, kT, 0>(p, ring, 1, 0, st, parts) : e;
   }
-  if (fit(3) * kT >= 256 || fit(3) == most) return launch_odd<GT, RT, kT, 3>(p, ring, fit(3), sms, st, parts);
+  if (fit(3) == most) return launch_odd<GT, RT, kT, 3>(p, ring, fit(3), sms, st, parts);
   if (fit(2) >= 1) return launch_odd<GT, RT, kT, 2>(p, ring, fit(2), sms, st, parts);
   return launch_odd<GT, RT, kT, 0>(p, ring, most, sms, st, parts);
 }
@@ -452,7 +445,6 @@ cudaError_t pick(const RmsNormBwdParams& p, bool vectors, int sms, cudaStream_t 
   if (h <= 1024) return pick_odd<GT, RT, 32>(p, sms, st, parts);
   if (h <= 2048) return pick_odd<GT, RT, 64>(p, sms, st, parts);
   if (h <= 4096) return pick_odd<GT, RT, 128>(p, sms, st, parts);
-  if (h <= 8192) return pick_odd<GT, RT, 256>(p, sms, st, parts);
   if (h <= 16384) return pick_odd<GT, RT, 512>(p, sms, st, parts);
   return pick_odd<GT, RT, 1024>(p, sms, st, parts);
 }
@@ -461,7 +453,7 @@ cudaError_t pick(const RmsNormBwdParams& p, bool vectors, int sms, cudaStream_t 
 template <typename GT, typename RT> cudaError_t set_up() {
   RmsNormBwdParams p = {};
   cudaError_t e = cudaSuccess;
-  for (int h : {256, 1024, 2048, 4096, 8192, 16384, VPCE_MAX_NORM_COLUMNS}) {
+  for (int h : {256, 2048, 4096, 8192, 16384, VPCE_MAX_NORM_COLUMNS}) {
     p.h = h;
     for (const bool vectors : {false, true})
       if (e == cudaSuccess) e = pick<GT, RT>(p, vectors, 0, nullptr, nullptr);
