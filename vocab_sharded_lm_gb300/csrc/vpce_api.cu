@@ -28,6 +28,7 @@ cudaError_t set_gemm_bwd_smem();
 cudaError_t set_embed_smem();
 cudaError_t set_logprob_smem();
 cudaError_t set_embed_dropout_smem();
+cudaError_t set_rmsnorm_forward_smem();
 cudaError_t set_rmsnorm_smem();
 size_t lmhead_bwd_workspace_bytes(long long V, long long h);
 size_t lmhead_bwd_min_workspace_bytes(long long V, long long h);
@@ -96,7 +97,8 @@ vpce_status device_setup(int* sms) {
     } else if (set_backward_smem() != cudaSuccess ||
                set_fused_smem() != cudaSuccess || set_gemm_smem() != cudaSuccess || set_gemm_bwd_smem() != cudaSuccess ||
                set_embed_smem() != cudaSuccess || set_logprob_smem() != cudaSuccess ||
-               set_embed_dropout_smem() != cudaSuccess || set_rmsnorm_smem() != cudaSuccess) {
+               set_embed_dropout_smem() != cudaSuccess || set_rmsnorm_forward_smem() != cudaSuccess ||
+               set_rmsnorm_smem() != cudaSuccess) {
       cudaGetLastError();
       return VPCE_ERR_CUDA;
     } else {

@@ -10,43 +10,6 @@
 namespace vpce {
 namespace {
 
-constexpr float kTiny = 1.17549435e-38f;  // 2^-126: the least scale, so that 1 / scale is finite
-
-__device__ __forceinline__ unsigned short e4m3x2(float lo, float hi) {
-  unsigned short r;
-  asm("cvt.rn.satfinite.e4m3x2.f32 %0, %1, %2;" : "=h"(r) : "f"(hi), "f"(lo));
-  return r;
-}
-
-__device__ __forceinline__ void store_codes(unsigned char* p, const float (&v)[8]) {
-  const uint32_t a = e4m3x2(v[0], v[1]) | uint32_t(e4m3x2(v[2], v[3])) << 16;
-  const uint32_t b = e4m3x2(v[4], v[5]) | uint32_t(e4m3x2(v[6], v[7])) << 16;
-  *reinterpret_cast<uint2*>(p) = make_uint2(a, b);
-}
-__device__ __forceinline__ void store_code(unsigned char* p, float v) { *p = (unsigned char)(e4m3x2(v, 0.f) & 0xff); }
-
-// |v| as ordered bits: infinities above every number, NaN above them, so that
-// a maximum of these bits carries a NaN on.
-__device__ __forceinline__ unsigned mag(float v) { return __float_as_uint(v) & 0x7fffffffu; }
-
-// y / s correctly rounded, for inv = 1 / s (Markstein, "Computation of
-// elementary functions on the IBM RISC System/6000 processor", 1990: one
-// residual step); where s is infinite, y inv.
-__device__ __forceinline__ float quotient(float y, float s, float inv) {
-  const float q = __fmul_rn(y, inv);
-  return __fmaf_rn(__fmaf_rn(-q, s, y), inv, q);
-}
-
-__device__ __forceinline__ float group_scale(unsigned top) {
-  const float s = __fmul_rn(__uint_as_float(top), 1.f / 448.f);
-  return s < kTiny ? kTiny : s;  // a NaN stays
-}
-
-// Where a group's largest magnitude is found: in the lanes of a warp that hold
-// the group (16, 32, .. 256 columns in vectors), by the whole team (one group a
-// row), or through shared memory.
-enum GroupKind { kNoCodes, kLanes, kRow, kShared };
-
 // Per team, twice (the rows alternate: who still reads one row's is at most a
 // barrier behind whoever writes the next row's): the groups' maxima, then their
 // scales, and the reciprocals of those.
@@ -68,6 +31,22 @@ struct SharedGroups {
   }
 };
 
+// Sum over a team: one warp, or the CTA's warps through `red` (32 floats).
+// The order is fixed, and every thread gets the same bits.
+template <bool kWarp> __device__ __forceinline__ float team_sum(float v, float* red) {
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) v += __shfl_xor_sync(kFull, v, o);
+  if constexpr (!kWarp) {
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, warps = blockDim.x >> 5;
+    if (lane == 0) red[warp] = v;
+    __syncthreads();
+    v = lane < warps ? red[lane] : 0.f;
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) v += __shfl_xor_sync(kFull, v, o);
+  }
+  return v;
+}
+
 template <bool kWarp> __device__ __forceinline__ void team_sync() {
   if constexpr (kWarp) __syncwarp();
   else __syncthreads();
@@ -84,8 +63,6 @@ template <bool kWarp> __device__ __forceinline__ unsigned team_max(unsigned v, u
   }
   return v;
 }
-
-__device__ __forceinline__ int group_of(const RmsNormParams& p, int c) { return int(__umulhi(unsigned(c), p.group_inverse)); }
 
 // Rows of 16-byte vectors: a warp (four a CTA) or a CTA a row, NU units of eight
 // columns a thread.
@@ -204,79 +181,6 @@ __global__ void __launch_bounds__(kMaxT, kMaxT == 256 ? 3 : 1) rmsnorm_forward_k
   }
 }
 
-// Rows off 16 bytes, element by element: kT threads a row, few of them, since
-// what a row costs besides its elements (sums, addresses) is paid by every warp.
-template <typename XT, typename RT, GroupKind kGroups, int kT>
-__global__ void __launch_bounds__(kT == 32 ? 128 : kT, kT >= 512 ? 1 : kT == 32 ? 4 : 512 / kT)
-    rmsnorm_forward_odd_kernel(const __grid_constant__ RmsNormParams p) {
-  extern __shared__ unsigned group_sm[];
-  __shared__ float red[2][32];
-  [[maybe_unused]] __shared__ unsigned top_row[2][32];
-  constexpr bool kWarp = kT == 32;
-  constexpr int XB = Elem<XT>::kBytes, RB = Elem<RT>::kBytes;
-  const int lane = threadIdx.x & 31, h = p.h;
-  const int team = kWarp ? int(threadIdx.x >> 5) : 0, teams = kWarp ? 4 : 1;
-  const int tid = kWarp ? lane : int(threadIdx.x);
-  int parity = 0;
-  for (long long row = (long long)blockIdx.x * teams + team; row < p.s; row += (long long)gridDim.x * teams, parity ^= 1) {
-    const unsigned char* const xr = p.x + row * p.ld_x;
-    float r[kOddColumns], ss = 0.f;
-    odd_columns<kT>(h, tid, [&](int k, int c, bool) { r[k] = Elem<XT>::load(xr + c * XB); });
-    if (p.res != nullptr) {
-      const unsigned char* const rr = p.res + row * p.ld_res;
-      unsigned char* const to = p.res_out + row * p.ld_res_out;
-      odd_columns<kT>(h, tid, [&](int k, int c, bool) { r[k] += Elem<RT>::load(rr + c * RB); });
-      // (in place, column 0 is written only after every lane has read it)
-      team_sync<kWarp>();
-      odd_columns<kT>(h, tid, [&](int k, int c, bool inside) {
-        if (inside) Elem<RT>::store(to + c * RB, r[k]);
-      });
-    }
-    odd_columns<kT>(h, tid, [&](int k, int, bool inside) { ss = inside ? fmaf(r[k], r[k], ss) : ss; });
-    const SharedGroups shared(group_sm, team, parity, p.groups);
-    if constexpr (kGroups == kShared) {
-      shared.clear(p.groups, tid, kT);
-      if constexpr (kWarp) __syncwarp();
-    }
-    ss = team_sum<kWarp>(ss, red[parity]);
-    const float rstd = rsqrtf(ss / float(h) + p.eps);
-    if (tid == 0 && p.rstd != nullptr) p.rstd[row] = rstd;
-    unsigned char* const out = p.out + row * p.ld_out;
-    [[maybe_unused]] unsigned all = 0;
-    odd_columns<kT>(h, tid, [&](int k, int c, bool inside) {
-      r[k] = r[k] * rstd * load_weight(p.w, p.w_bf16, c);
-      if constexpr (kGroups == kNoCodes) {
-        if (inside) Elem<XT>::store(out + c * XB, r[k]);
-      } else if constexpr (kGroups == kRow) {
-        all = max(all, inside ? mag(r[k]) : 0u);
-      } else {
-        // 32 consecutive columns: of one group, or 16 and 16 of one each
-        // (atomics on shared memory; their order does not matter)
-        const unsigned half = p.group % 32 == 0 ? kFull : lane < 16 ? 0xffffu : 0xffff0000u;
-        const unsigned t = __reduce_max_sync(half, inside ? mag(r[k]) : 0u);
-        if (inside && (lane == 0 || (lane == 16 && half != kFull))) atomicMax(shared.top + group_of(p, c), t);
-      }
-    });
-    if constexpr (kGroups == kRow) {
-      const float scale = group_scale(team_max<kWarp>(all, top_row[parity])), inv = __fdiv_rn(1.f, scale);
-      const float s = isinf(scale) ? 0.f : scale;
-      if (tid == 0) p.scale[row] = scale;
-      odd_columns<kT>(h, tid, [&](int k, int c, bool inside) {
-        if (inside) store_code(out + c, quotient(r[k], s, inv));
-      });
-    } else if constexpr (kGroups == kShared) {
-      team_sync<kWarp>();
-      shared.scales(p.groups, tid, kT, p.scale + row * p.groups);
-      team_sync<kWarp>();
-      odd_columns<kT>(h, tid, [&](int k, int c, bool inside) {
-        const int g = group_of(p, c);
-        const float scale = __uint_as_float(shared.top[g]);
-        if (inside) store_code(out + c, quotient(r[k], isinf(scale) ? 0.f : scale, shared.inverse[g]));
-      });
-    }
-  }
-}
-
 template <typename P> size_t group_bytes(GroupKind kind, int teams, const P& p) {
   return kind == kShared ? size_t(teams) * 4 * p.groups * sizeof(unsigned) : 0;
 }
@@ -293,46 +197,41 @@ void launch(const RmsNormParams& p, int threads, int sms, cudaStream_t st) {
       <<<row_grid(p, kTeams, sms), kWarp ? 128 : threads, group_bytes(kGroups, kTeams, p), st>>>(p);
 }
 
-template <typename XT, typename RT, GroupKind kGroups, int kT>
-void launch_odd(const RmsNormParams& p, int sms, cudaStream_t st) {
-  constexpr int kTeams = kT == 32 ? 4 : 1;
-  rmsnorm_forward_odd_kernel<XT, RT, kGroups, kT>
-      <<<row_grid(p, kTeams, sms), kT == 32 ? 128 : kT, group_bytes(kGroups, kTeams, p), st>>>(p);
-}
-
 template <typename XT, typename RT, GroupKind kGroups>
-void pick(const RmsNormParams& p, bool vectors, int sms, cudaStream_t st) {
-  const int h = p.h;
-  if (vectors) {
-    const int units = h / 8;
-    if (units <= 32) return launch<XT, RT, kGroups, 1, true>(p, 32, sms, st);
-    if (units <= 128) return launch<XT, RT, kGroups, 4, true>(p, 32, sms, st);
-    const int threads = ((units + 3) / 4 + 31) / 32 * 32;
-    // (at most 85 registers a thread: three CTAs of 256 on an SM)
-    if (threads <= 256) return launch<XT, RT, kGroups, 4, false, 256>(p, threads, sms, st);
-    if (threads <= 512) return launch<XT, RT, kGroups, 4, false, 512>(p, threads, sms, st);
-    return launch<XT, RT, kGroups, 4, false, 1024>(p, threads, sms, st);
-  }
-  if constexpr (kGroups != kLanes) {
-    if (h <= 1024) return launch_odd<XT, RT, kGroups, 32>(p, sms, st);
-    if (h <= 2048) return launch_odd<XT, RT, kGroups, 64>(p, sms, st);
-    if (h <= 4096) return launch_odd<XT, RT, kGroups, 128>(p, sms, st);
-    if (h <= 8192) return launch_odd<XT, RT, kGroups, 256>(p, sms, st);
-    if (h <= 16384) return launch_odd<XT, RT, kGroups, 512>(p, sms, st);
-    launch_odd<XT, RT, kGroups, 1024>(p, sms, st);
-  }
+void pick_vectors(const RmsNormParams& p, int sms, cudaStream_t st) {
+  const int units = p.h / 8;
+  if (units <= 32) return launch<XT, RT, kGroups, 1, true>(p, 32, sms, st);
+  if (units <= 128) return launch<XT, RT, kGroups, 4, true>(p, 32, sms, st);
+  const int threads = ((units + 3) / 4 + 31) / 32 * 32;
+  // (at most 85 registers a thread: three CTAs of 256 on an SM)
+  if (threads <= 256) return launch<XT, RT, kGroups, 4, false, 256>(p, threads, sms, st);
+  if (threads <= 512) return launch<XT, RT, kGroups, 4, false, 512>(p, threads, sms, st);
+  launch<XT, RT, kGroups, 4, false, 1024>(p, threads, sms, st);
 }
 
 template <typename XT, typename RT>
 void pick(const RmsNormParams& p, bool codes, bool vectors, int sms, cudaStream_t st) {
-  const bool lanes = p.group <= 256 && (p.group & (p.group - 1)) == 0;
-  if (!codes) pick<XT, RT, kNoCodes>(p, vectors, sms, st);
-  else if (p.groups == 1) pick<XT, RT, kRow>(p, vectors, sms, st);
-  else if (vectors && lanes) pick<XT, RT, kLanes>(p, vectors, sms, st);
-  else pick<XT, RT, kShared>(p, vectors, sms, st);
+  const GroupKind kind = !codes ? kNoCodes
+                         : p.groups == 1 ? kRow
+                         : vectors && p.group <= 256 && (p.group & (p.group - 1)) == 0 ? kLanes
+                                                                                       : kShared;
+  if (vectors) {
+    if (kind == kNoCodes) pick_vectors<XT, RT, kNoCodes>(p, sms, st);
+    else if (kind == kRow) pick_vectors<XT, RT, kRow>(p, sms, st);
+    else if (kind == kLanes) pick_vectors<XT, RT, kLanes>(p, sms, st);
+    else pick_vectors<XT, RT, kShared>(p, sms, st);
+  } else {
+    rmsnorm_forward_odd<XT, RT>(p, kind, sms, st);
+  }
 }
 
 }  // namespace
+
+cudaError_t set_rmsnorm_forward_smem() {
+  cudaError_t e = set_rmsnorm_odd_smem<float, float>();
+  if (e == cudaSuccess) e = set_rmsnorm_odd_smem<__nv_bfloat16, __nv_bfloat16>();
+  return e == cudaSuccess ? set_rmsnorm_odd_smem<__nv_bfloat16, float>() : e;
+}
 
 void launch_rmsnorm_forward(const RmsNormParams& p, bool x_bf16, bool res_bf16, bool codes, bool vectors, int sms,
                             cudaStream_t st) {

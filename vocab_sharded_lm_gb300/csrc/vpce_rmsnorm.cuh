@@ -122,21 +122,135 @@ template <int kT, typename F> __device__ __forceinline__ void odd_columns(int h,
   }
 }
 
-// Sum over a team: one warp, or the CTA's warps through `red` (32 floats).
-// The order is fixed, and every thread gets the same bits.
-template <bool kWarp> __device__ __forceinline__ float team_sum(float v, float* red) {
-#pragma unroll
-  for (int o = 16; o > 0; o >>= 1) v += __shfl_xor_sync(kFull, v, o);
-  if constexpr (!kWarp) {
-    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, warps = blockDim.x >> 5;
-    if (lane == 0) red[warp] = v;
-    __syncthreads();
-    v = lane < warps ? red[lane] : 0.f;
+// The threads of one team: whole warps, with a barrier of their own (not 0,
+// which is the CTA's).
+struct Team {
+  int id, tid, threads;
+  float* red;  // [2][32]
+  __device__ __forceinline__ void sync() const {
+    if (threads == 32) __syncwarp();
+    else asm volatile("bar.sync %0, %1;" ::"r"(id + 1), "r"(threads) : "memory");
+  }
+  // largest of the team's values, through 32 words of shared memory
+  __device__ __forceinline__ unsigned max(unsigned v, unsigned* sm) const {
+    v = __reduce_max_sync(kFull, v);
+    if (threads > 32) {
+      const int lane = tid & 31, warps = threads >> 5;
+      if (lane == 0) sm[tid >> 5] = v;
+      sync();
+      v = __reduce_max_sync(kFull, lane < warps ? sm[lane] : 0u);
+    }
+    return v;
+  }
+  __device__ __forceinline__ float sum(float v, int parity) const {
 #pragma unroll
     for (int o = 16; o > 0; o >>= 1) v += __shfl_xor_sync(kFull, v, o);
+    if (threads > 32) {
+      const int lane = tid & 31, warps = threads >> 5;
+      float* r = red + parity * 32;
+      if (lane == 0) r[tid >> 5] = v;
+      sync();
+      v = lane < warps ? r[lane] : 0.f;
+#pragma unroll
+      for (int o = 16; o > 0; o >>= 1) v += __shfl_xor_sync(kFull, v, o);
+    }
+    return v;
   }
-  return v;
+};
+
+// Rows off 16 bytes come through a ring of shared memory per team: a row's bytes
+// are copied as the 16-byte vectors that hold them, the last cut to the row's
+// end; the first may begin in the row before (row 0's is copied by elements).
+// Elements are then read from shared memory, where alignment costs nothing.
+struct OddRing {
+  int first, other;  // bytes of a row of the first array and of the others, with room for its offset
+  __host__ __device__ OddRing(int h, int first_element, int other_element)
+      : first((h * first_element + 30) / 16 * 16), other((h * other_element + 30) / 16 * 16) {}
+  __host__ __device__ int bytes(int others) const { return first + others * other; }
+};
+
+template <int kElement, int kT>
+__device__ __forceinline__ void copy_odd_row(unsigned char* dst, const unsigned char* base, long long row, long long ld, int h,
+                                             int tid) {
+  const unsigned char* const src = base + row * ld;
+  const int off = int(uintptr_t(src) & 15), end = off + h * kElement;
+  for (int v = tid * 16; v < end; v += kT * 16) {
+    if (v == 0 && off > 0 && row == 0) {
+      for (int i = off; i < 16 && i < end; i += kElement) {
+        if constexpr (kElement == 2) *reinterpret_cast<short*>(dst + i) = *reinterpret_cast<const short*>(src - off + i);
+        else *reinterpret_cast<int*>(dst + i) = *reinterpret_cast<const int*>(src - off + i);
+      }
+    } else {
+      copy_async_part(dst + v, src - off + v, end - v < 16 ? end - v : 16);
+    }
+  }
 }
+
+constexpr int kMaxSmem = 200 * 1024;  // dynamic shared memory of a CTA that has an SM for itself
+
+// Teams of kT threads on an SM, 512 threads at most (or one team), and the rows
+// of each ring: three where every team can have them, else two, else no ring.
+// `more`: other shared memory of a team.
+struct OddPlan {
+  int teams, stages;
+  OddPlan(int row_bytes, int more, int T) {
+    const int most = T >= 512 ? 1 : 512 / T;
+    for (stages = 3; stages >= 2; --stages) {
+      teams = kMaxSmem / (stages * row_bytes + more);
+      if (teams > most) teams = most;
+      if ((stages == 3 && teams == most && T <= 512) || (stages == 2 && teams >= 1)) return;
+    }
+    stages = 0;
+    teams = most;
+  }
+};
+
+// ---------------------------------------------------------------------------
+// e4m3 output
+// ---------------------------------------------------------------------------
+constexpr float kTiny = 1.17549435e-38f;  // 2^-126: the least scale, so that 1 / scale is finite
+
+__device__ __forceinline__ unsigned short e4m3x2(float lo, float hi) {
+  unsigned short r;
+  asm("cvt.rn.satfinite.e4m3x2.f32 %0, %1, %2;" : "=h"(r) : "f"(hi), "f"(lo));
+  return r;
+}
+
+__device__ __forceinline__ void store_codes(unsigned char* p, const float (&v)[8]) {
+  const uint32_t a = e4m3x2(v[0], v[1]) | uint32_t(e4m3x2(v[2], v[3])) << 16;
+  const uint32_t b = e4m3x2(v[4], v[5]) | uint32_t(e4m3x2(v[6], v[7])) << 16;
+  *reinterpret_cast<uint2*>(p) = make_uint2(a, b);
+}
+__device__ __forceinline__ void store_code(unsigned char* p, float v) { *p = (unsigned char)(e4m3x2(v, 0.f) & 0xff); }
+
+// |v| as ordered bits: infinities above every number, NaN above them, so that
+// a maximum of these bits carries a NaN on.
+__device__ __forceinline__ unsigned mag(float v) { return __float_as_uint(v) & 0x7fffffffu; }
+
+// y / s correctly rounded, for inv = 1 / s (Markstein, "Computation of
+// elementary functions on the IBM RISC System/6000 processor", 1990: one
+// residual step); where s is infinite, y inv.
+__device__ __forceinline__ float quotient(float y, float s, float inv) {
+  const float q = __fmul_rn(y, inv);
+  return __fmaf_rn(__fmaf_rn(-q, s, y), inv, q);
+}
+
+__device__ __forceinline__ float group_scale(unsigned top) {
+  const float s = __fmul_rn(__uint_as_float(top), 1.f / 448.f);
+  return s < kTiny ? kTiny : s;  // a NaN stays
+}
+
+// Where a group's largest magnitude is found: in the lanes of a warp that hold
+// the group (16, 32, .. 256 columns in vectors), by the whole team (one group a
+// row), or through shared memory.
+enum GroupKind { kNoCodes, kLanes, kRow, kShared };
+
+__device__ __forceinline__ int group_of(const RmsNormParams& p, int c) { return int(__umulhi(unsigned(c), p.group_inverse)); }
+
+// Rows off 16 bytes, and their device set-up: one translation unit for each pair
+// of types (they are many kernels).
+template <typename XT, typename RT> cudaError_t rmsnorm_forward_odd(const RmsNormParams& p, GroupKind kind, int sms, cudaStream_t st);
+template <typename XT, typename RT> cudaError_t set_rmsnorm_odd_smem();
 
 void launch_rmsnorm_forward(const RmsNormParams& p, bool x_bf16, bool res_bf16, bool codes, bool vectors, int sms,
                             cudaStream_t st);

@@ -19,31 +19,6 @@ namespace {
 
 constexpr int kColumns = 32, kRowLanes = 32;  // of the kernel that adds the partial rows
 
-// The threads of one team: whole warps, with a barrier of their own (not 0,
-// which is the CTA's).
-struct Team {
-  int id, tid, threads;
-  float* red;  // [2][32]
-  __device__ __forceinline__ void sync() const {
-    if (threads == 32) __syncwarp();
-    else asm volatile("bar.sync %0, %1;" ::"r"(id + 1), "r"(threads) : "memory");
-  }
-  __device__ __forceinline__ float sum(float v, int parity) const {
-#pragma unroll
-    for (int o = 16; o > 0; o >>= 1) v += __shfl_xor_sync(kFull, v, o);
-    if (threads > 32) {
-      const int lane = tid & 31, warps = threads >> 5;
-      float* r = red + parity * 32;
-      if (lane == 0) r[tid >> 5] = v;
-      sync();
-      v = lane < warps ? r[lane] : 0.f;
-#pragma unroll
-      for (int o = 16; o > 0; o >>= 1) v += __shfl_xor_sync(kFull, v, o);
-    }
-    return v;
-  }
-};
-
 // Where a team puts its sums of the weight's gradient: the CTA's partial row,
 // or a row of shared memory where the CTA has several teams (all its threads
 // call this, and then join_sums).
@@ -241,16 +216,8 @@ __global__ void __launch_bounds__(kMaxT, 1) rmsnorm_backward_kernel(const __grid
   join_sums(p, smem, teams);
 }
 
-// Rows off 16 bytes: kT threads a row, column k kT + thread, up to 32 a thread.
-// kStages rows of the ring are under way (0: none).  A row's bytes are copied as
-// the 16-byte vectors that hold them, the last cut to the row's end; the first
-// may begin in the row before (row 0's is copied by elements).  Elements are
-// then read from shared memory, where alignment costs nothing.
-struct OddRing {
-  int dy_bytes, x_bytes;  // of a row, with room for its offset, a multiple of 16
-  __host__ __device__ int row_bytes(bool dres) const { return dy_bytes + (dres ? 2 : 1) * x_bytes; }
-};
-
+// Rows off 16 bytes: dy, r and dresidual through an OddRing.  kStages: rows of
+// it (0: none, rows are loaded when they are due).
 template <typename GT, typename RT, int kT, int kStages>
 __global__ void __launch_bounds__(kT > 512 ? kT : 512, 1) rmsnorm_backward_odd_kernel(const __grid_constant__ RmsNormBwdParams p,
                                                                                      const OddRing ring) {
@@ -273,30 +240,14 @@ __global__ void __launch_bounds__(kT > 512 ? kT : 512, 1) rmsnorm_backward_odd_k
     odd_columns<kT>(h, tid, [&](int k, int c, bool) { weight[k] = load_weight(p.w, p.w_bf16, c); });
   const auto weight_of = [&](int k, int c) { return kHoldWeights ? weight[kHoldWeights ? k : 0] : load_weight(p.w, p.w_bf16, c); };
 
-  const int stage_bytes = ring.row_bytes(p.dres != nullptr);
+  const int stage_bytes = ring.bytes(p.dres != nullptr ? 2 : 1);
   unsigned char* const mine = reinterpret_cast<unsigned char*>(smem) + team.id * kStages * stage_bytes;
-  const auto copy_row = [&](unsigned char* dst, const unsigned char* base, long long row, long long ld, int bytes,
-                            int element) {
-    const unsigned char* const src = base + row * ld;
-    const int off = int(uintptr_t(src) & 15), end = off + bytes;
-    for (int v = tid * 16; v < end; v += kT * 16) {
-      if (v == 0 && off > 0 && row == 0) {
-        for (int i = off; i < 16 && i < end; i += element) {
-          if (element == 2) *reinterpret_cast<short*>(dst + i) = *reinterpret_cast<const short*>(src - off + i);
-          else *reinterpret_cast<int*>(dst + i) = *reinterpret_cast<const int*>(src - off + i);
-        }
-      } else {
-        copy_async_part(dst + v, src - off + v, end - v < 16 ? end - v : 16);
-      }
-    }
-  };
   const auto fetch = [&](long long row, int stage) {
     if (row < p.s) {
       unsigned char* const dst = mine + stage * stage_bytes;
-      copy_row(dst, p.dy, row, p.ld_dy, h * int(sizeof(GT)), sizeof(GT));
-      copy_row(dst + ring.dy_bytes, p.x, row, p.ld_x, h * int(sizeof(RT)), sizeof(RT));
-      if (p.dres != nullptr)
-        copy_row(dst + ring.dy_bytes + ring.x_bytes, p.dres, row, p.ld_dres, h * int(sizeof(RT)), sizeof(RT));
+      copy_odd_row<GB, kT>(dst, p.dy, row, p.ld_dy, h, tid);
+      copy_odd_row<RB, kT>(dst + ring.first, p.x, row, p.ld_x, h, tid);
+      if (p.dres != nullptr) copy_odd_row<RB, kT>(dst + ring.first + ring.other, p.dres, row, p.ld_dres, h, tid);
     }
     copy_commit();  // (an empty group past the end keeps the count)
   };
@@ -321,8 +272,8 @@ __global__ void __launch_bounds__(kT > 512 ? kT : 512, 1) rmsnorm_backward_odd_k
       fetch(row + (kStages - 1) * stride, stage == 0 ? kStages - 1 : stage - 1);
       unsigned char* const at = mine + stage * stage_bytes;
       gr = at + (uintptr_t(gr) & 15);
-      xr = at + ring.dy_bytes + (uintptr_t(xr) & 15);
-      if (dr != nullptr) dr = at + ring.dy_bytes + ring.x_bytes + (uintptr_t(dr) & 15);
+      xr = at + ring.first + (uintptr_t(xr) & 15);
+      if (dr != nullptr) dr = at + ring.first + ring.other + (uintptr_t(dr) & 15);
     }
     float dot = 0.f;
     odd_columns<kT>(h, tid, [&](int k, int c, bool inside) {
@@ -376,8 +327,6 @@ __global__ void __launch_bounds__(kColumns * kRowLanes) rmsnorm_weight_kernel(co
   if (x == 0 && col < h) dw[col] = accumulate ? dw[col] + v : v;
 }
 
-constexpr int kMaxSmem = 200 * 1024;  // dynamic shared memory of a CTA
-
 template <typename GT, typename RT, int NU, int kStages, int kMaxT, bool kKeep>
 cudaError_t launch(const RmsNormBwdParams& p, int team_threads, int sms, cudaStream_t st, int* parts) {
   const auto kernel = rmsnorm_backward_kernel<GT, RT, NU, kStages, kMaxT, kKeep>;
@@ -398,7 +347,7 @@ template <typename GT, typename RT, int kT, int kStages>
 cudaError_t launch_odd(const RmsNormBwdParams& p, const OddRing& ring, int teams, int sms, cudaStream_t st, int* parts) {
   const auto kernel = rmsnorm_backward_odd_kernel<GT, RT, kT, kStages>;
   if (sms == 0) return cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kMaxSmem);
-  size_t smem = size_t(teams) * kStages * ring.row_bytes(p.dres != nullptr);
+  size_t smem = size_t(teams) * kStages * ring.bytes(p.dres != nullptr ? 2 : 1);
   const size_t sums = teams > 1 ? size_t(teams) * p.h * sizeof(float) : 0;
   if (sums > smem) smem = sums;
   const long long rows = (p.s + teams - 1) / teams;
@@ -407,25 +356,17 @@ cudaError_t launch_odd(const RmsNormBwdParams& p, const OddRing& ring, int teams
   return cudaGetLastError();
 }
 
-// As many teams as 512 threads and the rings allow: three rows each where that
-// leaves every team its ring, else two, else no ring.
 template <typename GT, typename RT, int kT>
 cudaError_t pick_odd(const RmsNormBwdParams& p, int sms, cudaStream_t st, int* parts) {
-  const auto room = [&](int element) { return (p.h * element + 15 + 15) / 16 * 16; };
-  const OddRing ring = {room(sizeof(GT)), room(sizeof(RT))};
-  const int most = kT >= 512 ? 1 : 512 / kT, row = ring.row_bytes(p.dres != nullptr);
-  const auto fit = [&](int stages) {
-    const int n = kMaxSmem / (stages * row);
-    return n < most ? n : most;
-  };
-  if (sms == 0) {
-    cudaError_t e = launch_odd<GT, RT, kT, 3>(p, ring, 1, 0, st, parts);
-    if (e == cudaSuccess) e = launch_odd<GT, RT, kT, 2>(p, ring, 1, 0, st, parts);
-    return e == cudaSuccess ? launch_odd<GT, RT, kT, 0>(p, ring, 1, 0, st, parts) : e;
-  }
-  if (fit(3) == most) return launch_odd<GT, RT, kT, 3>(p, ring, fit(3), sms, st, parts);
-  if (fit(2) >= 1) return launch_odd<GT, RT, kT, 2>(p, ring, fit(2), sms, st, parts);
-  return launch_odd<GT, RT, kT, 0>(p, ring, most, sms, st, parts);
+  const OddRing ring(p.h, sizeof(GT), sizeof(RT));
+  const OddPlan plan(ring.bytes(p.dres != nullptr ? 2 : 1), 0, kT);
+  cudaError_t e = cudaSuccess;
+  if constexpr (kT <= 512)
+    if (sms == 0 || plan.stages == 3) e = launch_odd<GT, RT, kT, 3>(p, ring, plan.teams, sms, st, parts);
+  if (e == cudaSuccess && (sms == 0 || plan.stages == 2)) e = launch_odd<GT, RT, kT, 2>(p, ring, plan.teams, sms, st, parts);
+  if constexpr (kT >= 512)  // (shorter rows always have a ring)
+    if (e == cudaSuccess && (sms == 0 || plan.stages == 0)) e = launch_odd<GT, RT, kT, 0>(p, ring, plan.teams, sms, st, parts);
+  return e;
 }
 
 template <typename GT, typename RT>
@@ -443,7 +384,6 @@ cudaError_t pick(const RmsNormBwdParams& p, bool vectors, int sms, cudaStream_t 
     return launch<GT, RT, 4, kSmall ? 1 : 0, 1024, false>(p, whole_warps((units + 3) / 4), sms, st, parts);
   }
   if (h <= 1024) return pick_odd<GT, RT, 32>(p, sms, st, parts);
-  if (h <= 2048) return pick_odd<GT, RT, 64>(p, sms, st, parts);
   if (h <= 4096) return pick_odd<GT, RT, 128>(p, sms, st, parts);
   if (h <= 16384) return pick_odd<GT, RT, 512>(p, sms, st, parts);
   return pick_odd<GT, RT, 1024>(p, sms, st, parts);
@@ -453,7 +393,7 @@ cudaError_t pick(const RmsNormBwdParams& p, bool vectors, int sms, cudaStream_t 
 template <typename GT, typename RT> cudaError_t set_up() {
   RmsNormBwdParams p = {};
   cudaError_t e = cudaSuccess;
-  for (int h : {256, 2048, 4096, 8192, 16384, VPCE_MAX_NORM_COLUMNS}) {
+  for (int h : {256, 4096, 8192, 16384, VPCE_MAX_NORM_COLUMNS}) {
     p.h = h;
     for (const bool vectors : {false, true})
       if (e == cudaSuccess) e = pick<GT, RT>(p, vectors, 0, nullptr, nullptr);

@@ -1,0 +1,198 @@
+// The norm of rows off 16 bytes: h not a multiple of 8, or addresses or strides
+// that are not whole vectors.
+#pragma once
+
+#include "vpce_rmsnorm.cuh"
+
+namespace vpce {
+namespace {
+
+// Rows off 16 bytes, through an OddRing (kStages rows of it; 0: none, rows are
+// loaded when they are due).  For kShared, a warp's 32 (or 16 and 16)
+// consecutive columns leave their maximum in shared memory, and the team's first
+// threads join those of a group.
+struct OddGroups {
+  int segment, segments, groups;  // columns of a segment, segments and groups of a row
+  __host__ __device__ int bytes() const { return (segments + 2 * groups + 3) / 4 * 16; }
+};
+
+template <typename XT, typename RT, GroupKind kGroups, int kT, int kStages>
+__global__ void __launch_bounds__(kT > 512 ? kT : 512, 1)
+    rmsnorm_forward_odd_kernel(const __grid_constant__ RmsNormParams p, const OddRing ring, const OddGroups og) {
+  extern __shared__ uint4 smem[];  // [teams][groups' words, kStages rows]
+  constexpr int kMaxTeams = kT > 512 ? 1 : 512 / kT, XB = Elem<XT>::kBytes, RB = Elem<RT>::kBytes;
+  constexpr bool kRing = kStages > 0, kHoldWeights = kT <= 512;  // (64 registers a thread otherwise)
+  __shared__ float red[kMaxTeams][2][32];
+  [[maybe_unused]] __shared__ unsigned top_row[kMaxTeams][2][32];
+  Team team;
+  const int teams = blockDim.x / kT, lane = threadIdx.x & 31, h = p.h;
+  team.id = threadIdx.x / kT;
+  team.tid = threadIdx.x % kT;
+  team.threads = kT;
+  team.red = &red[team.id][0][0];
+  const int tid = team.tid;
+  float weight[kHoldWeights ? kOddColumns : 1];
+  if constexpr (kHoldWeights)
+    odd_columns<kT>(h, tid, [&](int k, int c, bool) { weight[k] = load_weight(p.w, p.w_bf16, c); });
+  const auto weight_of = [&](int k, int c) { return kHoldWeights ? weight[kHoldWeights ? k : 0] : load_weight(p.w, p.w_bf16, c); };
+
+  const int stage_bytes = ring.bytes(p.res != nullptr ? 1 : 0);
+  const int own = (kGroups == kShared ? og.bytes() : 0) + kStages * stage_bytes;
+  unsigned char* const base = reinterpret_cast<unsigned char*>(smem) + team.id * own;
+  [[maybe_unused]] unsigned* const tops = reinterpret_cast<unsigned*>(base);
+  [[maybe_unused]] float *const scales = reinterpret_cast<float*>(tops + og.segments), *const inverses = scales + og.groups;
+  unsigned char* const rows = base + (kGroups == kShared ? og.bytes() : 0);
+  const auto fetch = [&](long long row, int stage) {
+    if (row < p.s) {
+      unsigned char* const dst = rows + stage * stage_bytes;
+      copy_odd_row<XB, kT>(dst, p.x, row, p.ld_x, h, tid);
+      if (p.res != nullptr) copy_odd_row<RB, kT>(dst + ring.first, p.res, row, p.ld_res, h, tid);
+    }
+    copy_commit();  // (an empty group past the end keeps the count)
+  };
+
+  const long long first = (long long)blockIdx.x * teams + team.id, stride = (long long)gridDim.x * teams;
+  if constexpr (kRing) {
+#pragma unroll
+    for (int i = 0; i + 1 < kStages; ++i) fetch(first + i * stride, i);
+  }
+  int parity = 0, stage = 0;
+  for (long long row = first; row < p.s; row += stride, parity ^= 1) {
+    const unsigned char *xr = p.x + row * p.ld_x, *rr = p.res != nullptr ? p.res + row * p.ld_res : nullptr;
+    if constexpr (kRing) {
+      // this row's copies are in, everybody's; and everybody is done with the
+      // stage of the row before, which is filled next
+      copy_wait<(kRing ? kStages - 2 : 0)>();
+      team.sync();
+      fetch(row + (kStages - 1) * stride, stage == 0 ? kStages - 1 : stage - 1);
+      const unsigned char* const at = rows + stage * stage_bytes;
+      xr = at + (uintptr_t(xr) & 15);
+      if (rr != nullptr) rr = at + ring.first + (uintptr_t(rr) & 15);
+      stage = stage + 1 == kStages ? 0 : stage + 1;
+    }
+    float r[kOddColumns], ss = 0.f;
+    if (rr != nullptr) {
+      unsigned char* const to = p.res_out + row * p.ld_res_out;
+      // (lanes past the row read nothing that is written here: in place, without
+      // a ring, column 0 may be)
+      odd_columns<kT>(h, tid, [&](int k, int c, bool inside) {
+        r[k] = inside ? Elem<XT>::load(xr + c * XB) + Elem<RT>::load(rr + c * RB) : 0.f;
+        ss = fmaf(r[k], r[k], ss);
+        if (inside) Elem<RT>::store(to + c * RB, r[k]);
+      });
+    } else {
+      odd_columns<kT>(h, tid, [&](int k, int c, bool inside) {
+        r[k] = inside ? Elem<XT>::load(xr + c * XB) : 0.f;
+        ss = fmaf(r[k], r[k], ss);
+      });
+    }
+    ss = team.sum(ss, parity);
+    const float rstd = rsqrtf(ss / float(h) + p.eps);
+    if (tid == 0 && p.rstd != nullptr) p.rstd[row] = rstd;
+    unsigned char* const out = p.out + row * p.ld_out;
+    [[maybe_unused]] unsigned all = 0;
+    odd_columns<kT>(h, tid, [&](int k, int c, bool inside) {
+      r[k] = r[k] * rstd * weight_of(k, c);
+      if constexpr (kGroups == kNoCodes) {
+        if (inside) Elem<XT>::store(out + c * XB, r[k]);
+      } else {
+        const unsigned m = inside ? mag(r[k]) : 0u;
+        if constexpr (kGroups == kRow) {
+          all = max(all, m);
+        } else {
+          const unsigned part = og.segment == 32 ? kFull : lane < 16 ? 0xffffu : 0xffff0000u;
+          const unsigned t = __reduce_max_sync(part, m);
+          if (inside && (lane & (og.segment - 1)) == 0) tops[c / 16 >> (og.segment == 32)] = t;
+        }
+      }
+    });
+    if constexpr (kGroups == kRow) {
+      const float scale = group_scale(team.max(all, top_row[team.id][parity])), inv = __fdiv_rn(1.f, scale);
+      const float s = isinf(scale) ? 0.f : scale;
+      if (tid == 0) p.scale[row] = scale;
+      odd_columns<kT>(h, tid, [&](int k, int c, bool inside) {
+        if (inside) store_code(out + c, quotient(r[k], s, inv));
+      });
+    } else if constexpr (kGroups == kShared) {
+      team.sync();
+      for (int g = tid; g < og.groups; g += kT) {
+        unsigned t = 0;
+        const int per = p.group / og.segment, end = (g + 1) * per < og.segments ? (g + 1) * per : og.segments;
+        for (int i = g * per; i < end; ++i) t = max(t, tops[i]);
+        const float scale = group_scale(t);
+        p.scale[row * og.groups + g] = scale;
+        scales[g] = isinf(scale) ? 0.f : scale;
+        inverses[g] = __fdiv_rn(1.f, scale);
+      }
+      team.sync();
+      odd_columns<kT>(h, tid, [&](int k, int c, bool inside) {
+        const int g = group_of(p, c);
+        if (inside) store_code(out + c, quotient(r[k], scales[g], inverses[g]));
+      });
+    }
+  }
+  if constexpr (kRing) copy_wait<0>();  // (what was copied past the last row is nothing)
+}
+
+template <typename XT, typename RT, GroupKind kGroups, int kT, int kStages>
+cudaError_t launch_odd(const RmsNormParams& p, int teams, const OddRing& ring, const OddGroups& og, int sms, cudaStream_t st) {
+  const auto kernel = rmsnorm_forward_odd_kernel<XT, RT, kGroups, kT, kStages>;
+  if (sms == 0) return cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kMaxSmem);  // set-up
+  const size_t smem = size_t(teams) * (kStages * ring.bytes(p.res != nullptr ? 1 : 0) + (kGroups == kShared ? og.bytes() : 0));
+  const long long rows = (p.s + teams - 1) / teams;
+  kernel<<<int(rows < sms ? rows : sms), kT * teams, smem, st>>>(p, ring, og);
+  return cudaSuccess;
+}
+
+template <typename XT, typename RT, GroupKind kGroups, int kT>
+cudaError_t pick_odd(const RmsNormParams& p, int sms, cudaStream_t st) {
+  const OddRing ring(p.h, sizeof(XT), sizeof(RT));
+  OddGroups og = {};
+  og.segment = p.group % 32 == 0 ? 32 : 16;
+  og.segments = (p.h + og.segment - 1) / og.segment;
+  og.groups = p.groups;
+  const OddPlan plan(ring.bytes(p.res != nullptr ? 1 : 0), kGroups == kShared ? og.bytes() : 0, kT);
+  cudaError_t e = cudaSuccess;
+  if constexpr (kT <= 512)
+    if (sms == 0 || plan.stages == 3) e = launch_odd<XT, RT, kGroups, kT, 3>(p, plan.teams, ring, og, sms, st);
+  if (e == cudaSuccess && (sms == 0 || plan.stages == 2)) e = launch_odd<XT, RT, kGroups, kT, 2>(p, plan.teams, ring, og, sms, st);
+  if constexpr (kT >= 512)  // (shorter rows always have a ring)
+    if (e == cudaSuccess && (sms == 0 || plan.stages == 0)) e = launch_odd<XT, RT, kGroups, kT, 0>(p, plan.teams, ring, og, sms, st);
+  return e;
+}
+
+template <typename XT, typename RT, GroupKind kGroups>
+cudaError_t pick_odd(const RmsNormParams& p, int sms, cudaStream_t st) {
+  // few warps a row: what a row costs besides its elements (sums, addresses) is
+  // paid by every one of them
+  if (p.h <= 1024) return pick_odd<XT, RT, kGroups, 32>(p, sms, st);
+  if (p.h <= 4096) return pick_odd<XT, RT, kGroups, 128>(p, sms, st);
+  if (p.h <= 16384) return pick_odd<XT, RT, kGroups, 512>(p, sms, st);
+  return pick_odd<XT, RT, kGroups, 1024>(p, sms, st);
+}
+
+// one call of each kind of row, with no SMs
+template <typename XT, typename RT, GroupKind kGroups> cudaError_t set_up() {
+  RmsNormParams p = {};
+  cudaError_t e = cudaSuccess;
+  for (int h : {1024, 4096, 16384, VPCE_MAX_NORM_COLUMNS}) {
+    p.h = p.group = h;
+    p.groups = 1;
+    if (e == cudaSuccess) e = pick_odd<XT, RT, kGroups>(p, 0, nullptr);
+  }
+  return e;
+}
+}  // namespace
+
+template <typename XT, typename RT> cudaError_t rmsnorm_forward_odd(const RmsNormParams& p, GroupKind kind, int sms, cudaStream_t st) {
+  if (kind == kNoCodes) return pick_odd<XT, RT, kNoCodes>(p, sms, st);
+  return kind == kRow ? pick_odd<XT, RT, kRow>(p, sms, st) : pick_odd<XT, RT, kShared>(p, sms, st);
+}
+
+template <typename XT, typename RT> cudaError_t set_rmsnorm_odd_smem() {
+  cudaError_t e = set_up<XT, RT, kNoCodes>();
+  if (e == cudaSuccess) e = set_up<XT, RT, kRow>();
+  return e == cudaSuccess ? set_up<XT, RT, kShared>() : e;
+}
+
+}  // namespace vpce
