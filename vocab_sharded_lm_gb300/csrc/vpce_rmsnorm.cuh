@@ -100,27 +100,41 @@ __device__ __forceinline__ float load_weight(const unsigned char* w, int w_bf16,
                 : __ldg(reinterpret_cast<const float*>(w) + c);
 }
 
-// Rows off 16 bytes: kT threads take column k kT + tid, k < kOddColumns.  Calls
-// f(k, c, inside) for every k that has columns, four at a time without a branch
-// between them (so that their loads go together): for the last four, `inside`
-// may be false, and c is then 0.
+// Rows off 16 bytes: the columns of one thread of a team of kT.  A warp has a
+// run of columns, up to eight times 128; a lane every 32nd of them.  (A run keeps
+// a group's columns together, and the addresses of a lane's columns are one
+// register and constants.)
 constexpr int kOddColumns = 32;
-template <int kT, typename F> __device__ __forceinline__ void odd_columns(int h, int tid, F f) {
+template <int kT> struct OddColumns {
+  int h, lane, start, quads;  // start: the warp's first column; quads: 128 columns each
+  __device__ __forceinline__ OddColumns(int h_, int tid) : h(h_), lane(tid & 31) {
+    constexpr int kWarps = kT / 32;
+    quads = ((h + 127) / 128 + kWarps - 1) / kWarps;
+    start = (tid >> 5) * quads * 128;
+  }
+  // f(q, first column, all): for every 128 columns; `all`: they are all of the row
+  template <typename F> __device__ __forceinline__ void by_quads(F f) const {
 #pragma unroll
-  for (int k = 0; k < kOddColumns; k += 4) {
-    if (k * kT >= h) break;
-    if ((k + 4) * kT <= h) {
-#pragma unroll
-      for (int i = 0; i < 4; ++i) f(k + i, (k + i) * kT + tid, true);
-    } else {
-#pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        const int c = (k + i) * kT + tid;
-        f(k + i, c < h ? c : 0, c < h);
-      }
+    for (int q = 0; q < kOddColumns / 4; ++q) {
+      const int c = start + q * 128;
+      if (q >= quads || c >= h) break;
+      if (c + 128 <= h) f(q, c, true);
+      else f(q, c, false);
     }
   }
-}
+  // f(k, c, inside): for the thread's k-th column, four at a time without a
+  // branch between them (so that their loads go together); in the row's last
+  // 128, `inside` may be false, and c is then 0
+  template <typename F> __device__ __forceinline__ void each(F f) const {
+    by_quads([&](int q, int first, bool all) {
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        const int c = first + i * 32 + lane;
+        f(q * 4 + i, all || c < h ? c : 0, all || c < h);
+      }
+    });
+  }
+};
 
 // The threads of one team: whole warps, with a barrier of their own (not 0,
 // which is the CTA's).

@@ -232,12 +232,13 @@ __global__ void __launch_bounds__(kT > 512 ? kT : 512, 1) rmsnorm_backward_odd_k
   team.threads = kT;
   team.red = &red[team.id][0][0];
   const int tid = team.tid, h = p.h;
+  const OddColumns<kT> columns(h, tid);
   constexpr bool kHoldWeights = kT <= 512;  // (64 registers a thread otherwise)
   float acc[kOddColumns], weight[kHoldWeights ? kOddColumns : 1];
 #pragma unroll
   for (int k = 0; k < kOddColumns; ++k) acc[k] = 0.f;
   if constexpr (kHoldWeights)
-    odd_columns<kT>(h, tid, [&](int k, int c, bool) { weight[k] = load_weight(p.w, p.w_bf16, c); });
+    columns.each([&](int k, int c, bool) { weight[k] = load_weight(p.w, p.w_bf16, c); });
   const auto weight_of = [&](int k, int c) { return kHoldWeights ? weight[kHoldWeights ? k : 0] : load_weight(p.w, p.w_bf16, c); };
 
   const int stage_bytes = ring.bytes(p.dres != nullptr ? 2 : 1);
@@ -276,7 +277,7 @@ __global__ void __launch_bounds__(kT > 512 ? kT : 512, 1) rmsnorm_backward_odd_k
       if (dr != nullptr) dr = at + ring.first + ring.other + (uintptr_t(dr) & 15);
     }
     float dot = 0.f;
-    odd_columns<kT>(h, tid, [&](int k, int c, bool inside) {
+    columns.each([&](int k, int c, bool inside) {
       const float dy = inside ? Elem<GT>::load(gr + c * GB) : 0.f, n = Elem<RT>::load(xr + c * RB) * rstd;
       acc[k] = fmaf(dy, n, acc[k]);
       dot = inside ? fmaf(weight_of(k, c) * dy, n, dot) : dot;
@@ -285,7 +286,7 @@ __global__ void __launch_bounds__(kT > 512 ? kT : 512, 1) rmsnorm_backward_odd_k
     parity ^= 1;
     unsigned char* const out = p.dx + row * p.ld_dx;
     const bool add = dr != nullptr;
-    odd_columns<kT>(h, tid, [&](int k, int c, bool inside) {
+    columns.each([&](int k, int c, bool inside) {
       if (inside) {
         const float dy = Elem<GT>::load(gr + c * GB), n = Elem<RT>::load(xr + c * RB) * rstd;
         const float d = add ? Elem<RT>::load(dr + c * RB) : 0.f;
@@ -297,11 +298,9 @@ __global__ void __launch_bounds__(kT > 512 ? kT : 512, 1) rmsnorm_backward_odd_k
   grid_launch_dependents();
   if constexpr (kRing) copy_wait<0>();
   float* const sums = own_sums(p, smem, teams, team.id);
-#pragma unroll
-  for (int k = 0; k < kOddColumns; ++k) {
-    const int c = k * kT + tid;
-    if (c < h) sums[c] = acc[k];
-  }
+  columns.each([&](int k, int c, bool inside) {
+    if (inside) sums[c] = acc[k];
+  });
   join_sums(p, smem, teams);
 }
 

@@ -8,11 +8,11 @@ namespace vpce {
 namespace {
 
 // Rows off 16 bytes, through an OddRing (kStages rows of it; 0: none, rows are
-// loaded when they are due).  For kShared, a warp's 32 (or 16 and 16)
-// consecutive columns leave their maximum in shared memory, and the team's first
-// threads join those of a group.
+// loaded when they are due).  For kShared, each 128, 64, 32 or 16 columns, the
+// largest of these that a group is a multiple of, leave their maximum in shared
+// memory, and the team's first threads join those of a group.
 struct OddGroups {
-  int segment, segments, groups;  // columns of a segment, segments and groups of a row
+  int segment, segments, groups;  // columns of a segment, segments (of whole 128 columns) and groups of a row
   __host__ __device__ int bytes() const { return (segments + 2 * groups + 3) / 4 * 16; }
 };
 
@@ -31,9 +31,10 @@ __global__ void __launch_bounds__(kT > 512 ? kT : 512, 1)
   team.threads = kT;
   team.red = &red[team.id][0][0];
   const int tid = team.tid;
+  const OddColumns<kT> columns(h, tid);
   float weight[kHoldWeights ? kOddColumns : 1];
   if constexpr (kHoldWeights)
-    odd_columns<kT>(h, tid, [&](int k, int c, bool) { weight[k] = load_weight(p.w, p.w_bf16, c); });
+    columns.each([&](int k, int c, bool) { weight[k] = load_weight(p.w, p.w_bf16, c); });
   const auto weight_of = [&](int k, int c) { return kHoldWeights ? weight[kHoldWeights ? k : 0] : load_weight(p.w, p.w_bf16, c); };
 
   const int stage_bytes = ring.bytes(p.res != nullptr ? 1 : 0);
@@ -75,13 +76,13 @@ __global__ void __launch_bounds__(kT > 512 ? kT : 512, 1)
       unsigned char* const to = p.res_out + row * p.ld_res_out;
       // (lanes past the row read nothing that is written here: in place, without
       // a ring, column 0 may be)
-      odd_columns<kT>(h, tid, [&](int k, int c, bool inside) {
+      columns.each([&](int k, int c, bool inside) {
         r[k] = inside ? Elem<XT>::load(xr + c * XB) + Elem<RT>::load(rr + c * RB) : 0.f;
         ss = fmaf(r[k], r[k], ss);
         if (inside) Elem<RT>::store(to + c * RB, r[k]);
       });
     } else {
-      odd_columns<kT>(h, tid, [&](int k, int c, bool inside) {
+      columns.each([&](int k, int c, bool inside) {
         r[k] = inside ? Elem<XT>::load(xr + c * XB) : 0.f;
         ss = fmaf(r[k], r[k], ss);
       });
@@ -91,26 +92,49 @@ __global__ void __launch_bounds__(kT > 512 ? kT : 512, 1)
     if (tid == 0 && p.rstd != nullptr) p.rstd[row] = rstd;
     unsigned char* const out = p.out + row * p.ld_out;
     [[maybe_unused]] unsigned all = 0;
-    odd_columns<kT>(h, tid, [&](int k, int c, bool inside) {
-      r[k] = r[k] * rstd * weight_of(k, c);
-      if constexpr (kGroups == kNoCodes) {
-        if (inside) Elem<XT>::store(out + c * XB, r[k]);
-      } else {
-        const unsigned m = inside ? mag(r[k]) : 0u;
-        if constexpr (kGroups == kRow) {
-          all = max(all, m);
-        } else {
-          const unsigned part = og.segment == 32 ? kFull : lane < 16 ? 0xffffu : 0xffff0000u;
-          const unsigned t = __reduce_max_sync(part, m);
-          if (inside && (lane & (og.segment - 1)) == 0) tops[c / 16 >> (og.segment == 32)] = t;
+    if constexpr (kGroups != kShared) {
+      columns.each([&](int k, int c, bool inside) {
+        r[k] = r[k] * rstd * weight_of(k, c);
+        if constexpr (kGroups == kRow) all = max(all, inside ? mag(r[k]) : 0u);
+        else if (inside) Elem<XT>::store(out + c * XB, r[k]);
+      });
+    } else {
+      columns.by_quads([&](int q, int quad, bool whole) {
+        unsigned m[4];
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          const int k = q * 4 + i, c = quad + i * 32 + lane;
+          r[k] = r[k] * rstd * weight_of(k, whole || c < h ? c : 0);
+          m[i] = whole || c < h ? mag(r[k]) : 0u;
         }
-      }
-    });
+        unsigned* const to = tops + quad / og.segment;
+        if (og.segment == 128) {
+          const unsigned t = __reduce_max_sync(kFull, max(max(m[0], m[1]), max(m[2], m[3])));
+          if (lane == 0) *to = t;
+        } else if (og.segment == 64) {
+          const unsigned t = __reduce_max_sync(kFull, max(m[0], m[1])), u = __reduce_max_sync(kFull, max(m[2], m[3]));
+          if (lane < 2) to[lane] = lane == 0 ? t : u;
+        } else if (og.segment == 32) {
+#pragma unroll
+          for (int i = 0; i < 4; ++i) {
+            const unsigned t = __reduce_max_sync(kFull, m[i]);
+            if (lane == 0) to[i] = t;
+          }
+        } else {
+#pragma unroll
+          for (int i = 0; i < 4; ++i) {
+#pragma unroll
+            for (int o = 1; o < 16; o <<= 1) m[i] = max(m[i], __shfl_xor_sync(kFull, m[i], o));
+            if ((lane & 15) == 0) to[2 * i + (lane >> 4)] = m[i];
+          }
+        }
+      });
+    }
     if constexpr (kGroups == kRow) {
       const float scale = group_scale(team.max(all, top_row[team.id][parity])), inv = __fdiv_rn(1.f, scale);
       const float s = isinf(scale) ? 0.f : scale;
       if (tid == 0) p.scale[row] = scale;
-      odd_columns<kT>(h, tid, [&](int k, int c, bool inside) {
+      columns.each([&](int k, int c, bool inside) {
         if (inside) store_code(out + c, quotient(r[k], s, inv));
       });
     } else if constexpr (kGroups == kShared) {
@@ -125,9 +149,18 @@ __global__ void __launch_bounds__(kT > 512 ? kT : 512, 1)
         inverses[g] = __fdiv_rn(1.f, scale);
       }
       team.sync();
-      odd_columns<kT>(h, tid, [&](int k, int c, bool inside) {
-        const int g = group_of(p, c);
-        if (inside) store_code(out + c, quotient(r[k], scales[g], inverses[g]));
+      columns.by_quads([&](int q, int quad, bool whole) {
+        int g = group_of(p, quad);
+        float scale = scales[g], inverse = inverses[g];
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          const int k = q * 4 + i, c = quad + i * 32 + lane;
+          if (og.segment < 128) {
+            g = group_of(p, whole || c < h ? c : 0);
+            scale = scales[g], inverse = inverses[g];
+          }
+          if (whole || c < h) store_code(out + c, quotient(r[k], scale, inverse));
+        }
       });
     }
   }
@@ -148,8 +181,8 @@ template <typename XT, typename RT, GroupKind kGroups, int kT>
 cudaError_t pick_odd(const RmsNormParams& p, int sms, cudaStream_t st) {
   const OddRing ring(p.h, sizeof(XT), sizeof(RT));
   OddGroups og = {};
-  og.segment = p.group % 32 == 0 ? 32 : 16;
-  og.segments = (p.h + og.segment - 1) / og.segment;
+  og.segment = p.group % 128 == 0 ? 128 : p.group % 64 == 0 ? 64 : p.group % 32 == 0 ? 32 : 16;
+  og.segments = (p.h + 127) / 128 * (128 / og.segment);
   og.groups = p.groups;
   const OddPlan plan(ring.bytes(p.res != nullptr ? 1 : 0), kGroups == kShared ? og.bytes() : 0, kT);
   cudaError_t e = cudaSuccess;
