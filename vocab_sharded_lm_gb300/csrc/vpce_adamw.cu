@@ -365,24 +365,6 @@ __device__ __forceinline__ unsigned square_codes2(f32x2 a, const RoundWord& u0, 
                     __uint_as_float((by & 0xfff00000u) + (ay > ty ? 0x100000u : 0u)));
 }
 
-// The largest (a NaN if there is one) and the least magnitude of eight.
-__device__ __forceinline__ float most_magnitude(const float (&x)[8]) {
-  float a, b, c;
-  asm("max.NaN.abs.f32 %0, %1, %2, %3;" : "=f"(a) : "f"(x[0]), "f"(x[1]), "f"(x[2]));
-  asm("max.NaN.abs.f32 %0, %1, %2, %3;" : "=f"(b) : "f"(x[3]), "f"(x[4]), "f"(x[5]));
-  asm("max.NaN.abs.f32 %0, %1, %2, %3;" : "=f"(c) : "f"(x[6]), "f"(x[7]), "f"(a));
-  asm("max.NaN.abs.f32 %0, %1, %2, %2;" : "=f"(a) : "f"(b), "f"(c));
-  return a;
-}
-__device__ __forceinline__ float least_magnitude(const float (&x)[8]) {
-  float a, b, c;
-  asm("min.abs.f32 %0, %1, %2, %3;" : "=f"(a) : "f"(x[0]), "f"(x[1]), "f"(x[2]));
-  asm("min.abs.f32 %0, %1, %2, %3;" : "=f"(b) : "f"(x[3]), "f"(x[4]), "f"(x[5]));
-  asm("min.abs.f32 %0, %1, %2, %3;" : "=f"(c) : "f"(x[6]), "f"(x[7]), "f"(a));
-  asm("min.abs.f32 %0, %1, %2, %2;" : "=f"(a) : "f"(b), "f"(c));
-  return a;
-}
-
 // One element type's part of the ring: eight elements a thread, in one or two
 // vectors of shared memory kThreads apart.
 template <typename T> struct Ahead {

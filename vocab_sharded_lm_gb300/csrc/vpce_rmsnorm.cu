@@ -10,27 +10,6 @@
 namespace vpce {
 namespace {
 
-// Per team, twice (the rows alternate: who still reads one row's is at most a
-// barrier behind whoever writes the next row's): the groups' maxima, then their
-// scales, and the reciprocals of those.
-struct SharedGroups {
-  unsigned* top;
-  float* inverse;
-  __device__ __forceinline__ SharedGroups(unsigned* sm, int team, int parity, int groups)
-      : top(sm + (team * 2 + parity) * 2 * groups), inverse(reinterpret_cast<float*>(top + groups)) {}
-  __device__ __forceinline__ void clear(int groups, int tid, int T) const {
-    for (int g = tid; g < groups; g += T) top[g] = 0;
-  }
-  __device__ __forceinline__ void scales(int groups, int tid, int T, float* out) const {
-    for (int g = tid; g < groups; g += T) {
-      const float scale = group_scale(top[g]);
-      out[g] = scale;
-      top[g] = __float_as_uint(scale);
-      inverse[g] = __fdiv_rn(1.f, scale);
-    }
-  }
-};
-
 // Sum over a team: one warp, or the CTA's warps through `red` (32 floats).
 // The order is fixed, and every thread gets the same bits.
 template <bool kWarp> __device__ __forceinline__ float team_sum(float v, float* red) {
@@ -45,6 +24,39 @@ template <bool kWarp> __device__ __forceinline__ float team_sum(float v, float* 
     for (int o = 16; o > 0; o >>= 1) v += __shfl_xor_sync(kFull, v, o);
   }
   return v;
+}
+
+// Eight values as pairs (one instruction for two), their squares added to ss.
+__device__ __forceinline__ void add_squares(const float (&v)[8], f32x2 (&r)[4], f32x2& ss) {
+#pragma unroll
+  for (int j = 0; j < 4; ++j) {
+    r[j] = f2_pack(v[2 * j], v[2 * j + 1]);
+    ss = f2_fma(r[j], r[j], ss);
+  }
+}
+
+// Eight codes: quotient() of pairs.
+__device__ __forceinline__ void store_quotients(unsigned char* to, const f32x2 (&r)[4], float scale, float inv) {
+  const float minus = isinf(scale) ? 0.f : -scale;
+  const f32x2 minus2 = f2_pack(minus, minus), inv2 = f2_pack(inv, inv);
+  float v[8];
+#pragma unroll
+  for (int j = 0; j < 4; ++j) {
+    const f32x2 q = f2_mul(r[j], inv2);
+    f2_unpack(f2_fma(f2_fma(q, minus2, r[j]), inv2, q), v[2 * j], v[2 * j + 1]);
+  }
+  store_codes(to, v);
+}
+
+// Maxima of the 16 columns of each two lanes.
+template <int NU>
+__device__ __forceinline__ void segments16(const GroupWords& words, const unsigned (&m)[NU], int tid, int T, int h) {
+#pragma unroll
+  for (int k = 0; k < NU; ++k) {
+    const int c = (k * T + tid) * 8;
+    const unsigned t = max(m[k], __shfl_xor_sync(kFull, m[k], 1));
+    if (c < h && (tid & 1) == 0) words.tops[c / 16] = t;
+  }
 }
 
 template <bool kWarp> __device__ __forceinline__ void team_sync() {
@@ -67,14 +79,15 @@ template <bool kWarp> __device__ __forceinline__ unsigned team_max(unsigned v, u
 // Rows of 16-byte vectors: a warp (four a CTA) or a CTA a row, NU units of eight
 // columns a thread.
 template <typename XT, typename RT, GroupKind kGroups, int NU, bool kWarp, int kMaxT>
-__global__ void __launch_bounds__(kMaxT, kMaxT == 256 ? 3 : 1) rmsnorm_forward_kernel(const __grid_constant__ RmsNormParams p) {
-  extern __shared__ unsigned group_sm[];  // [teams][2][2][groups], kShared only
+__global__ void __launch_bounds__(kMaxT, kMaxT == 256 ? 3 : 1) rmsnorm_forward_kernel(const __grid_constant__ RmsNormParams p, const GroupPlan plan) {
+  extern __shared__ uint4 smem[];  // [teams] GroupWords, kShared only
   __shared__ float red[2][32];
   [[maybe_unused]] __shared__ unsigned top_row[2][32];
   constexpr int U = 8;
   const int lane = threadIdx.x & 31;
   const int team = kWarp ? int(threadIdx.x >> 5) : 0, teams = kWarp ? int(blockDim.x >> 5) : 1;
   const int tid = kWarp ? lane : int(threadIdx.x), T = kWarp ? 32 : int(blockDim.x);
+  const GroupWords words(reinterpret_cast<unsigned char*>(smem) + team * plan.bytes(), plan);
   int parity = 0;
   for (long long row = (long long)blockIdx.x * teams + team; row < p.s; row += (long long)gridDim.x * teams, parity ^= 1) {
     const unsigned char* xr = p.x + row * p.ld_x;
@@ -95,28 +108,24 @@ __global__ void __launch_bounds__(kMaxT, kMaxT == 256 ? 3 : 1) rmsnorm_forward_k
         if (c < p.h) b[k].load(rr, c);
       }
     }
-    float r[NU][U], ss = 0.f;
+    f32x2 r[NU][4], ss = 0;
 #pragma unroll
     for (int k = 0; k < NU; ++k) {
       const int c = (k * T + tid) * U;
-      a[k].get(r[k]);
+      float v[U];
+      a[k].get(v);
       if (p.res != nullptr) {
         float q[U];
         b[k].get(q);
 #pragma unroll
-        for (int j = 0; j < U; ++j) r[k][j] += q[j];
-        if (c < p.h) store_unit(p.res_out + row * p.ld_res_out, c, r[k], RT());
+        for (int j = 0; j < U; ++j) v[j] += q[j];
+        if (c < p.h) store_unit(p.res_out + row * p.ld_res_out, c, v, RT());
       }
-#pragma unroll
-      for (int j = 0; j < U; ++j) ss = fmaf(r[k][j], r[k][j], ss);
+      add_squares(v, r[k], ss);
     }
-    const SharedGroups shared(group_sm, team, parity, p.groups);
-    if constexpr (kGroups == kShared) {
-      shared.clear(p.groups, tid, T);
-      if constexpr (kWarp) __syncwarp();
-    }
-    ss = team_sum<kWarp>(ss, red[parity]);
-    const float rstd = rsqrtf(ss / float(p.h) + p.eps);
+    float s0, s1;
+    f2_unpack(ss, s0, s1);
+    const float rstd = rsqrtf(team_sum<kWarp>(s0 + s1, red[parity]) / float(p.h) + p.eps);
     if (tid == 0 && p.rstd != nullptr) p.rstd[row] = rstd;
     [[maybe_unused]] unsigned m[NU], all = 0;
 #pragma unroll
@@ -124,16 +133,17 @@ __global__ void __launch_bounds__(kMaxT, kMaxT == 256 ? 3 : 1) rmsnorm_forward_k
       const int c = (k * T + tid) * U;
       m[k] = 0;
       if (c < p.h) {
-        float w[U];
+        float w[U], v[U];
         load_weight(p.w, p.w_bf16, c, w);
 #pragma unroll
-        for (int j = 0; j < U; ++j) r[k][j] = r[k][j] * rstd * w[j];
+        for (int j = 0; j < 4; ++j) {
+          r[k][j] = f2_mul(f2_mul(r[k][j], f2_pack(rstd, rstd)), f2_pack(w[2 * j], w[2 * j + 1]));
+          f2_unpack(r[k][j], v[2 * j], v[2 * j + 1]);
+        }
         if constexpr (kGroups == kNoCodes) {
-          store_unit(p.out + row * p.ld_out, c, r[k], XT());
+          store_unit(p.out + row * p.ld_out, c, v, XT());
         } else {
-#pragma unroll
-          for (int j = 0; j < U; ++j) m[k] = max(m[k], mag(r[k][j]));
-          if constexpr (kGroups == kShared) atomicMax(shared.top + group_of(p, c), m[k]);  // (the order does not matter)
+          m[k] = __float_as_uint(most_magnitude(v));
           all = max(all, m[k]);
         }
       }
@@ -148,15 +158,16 @@ __global__ void __launch_bounds__(kMaxT, kMaxT == 256 ? 3 : 1) rmsnorm_forward_k
         }
       }
     } else if constexpr (kGroups == kShared) {
+      segments16(words, m, tid, T, p.h);
       team_sync<kWarp>();
-      shared.scales(p.groups, tid, T, p.scale + row * p.groups);
+      words.join(plan, p.group, tid, T, p.scale + row * p.groups);
       team_sync<kWarp>();
     }
     if constexpr (kGroups != kNoCodes) {
       [[maybe_unused]] float row_scale = 0.f, row_inv = 0.f;
       if constexpr (kGroups == kRow) {
         row_scale = group_scale(team_max<kWarp>(all, top_row[parity]));
-        row_inv = __fdiv_rn(1.f, row_scale);
+        row_inv = __frcp_rn(row_scale);
         if (tid == 0) p.scale[row] = row_scale;
       }
 #pragma unroll
@@ -166,23 +177,158 @@ __global__ void __launch_bounds__(kMaxT, kMaxT == 256 ? 3 : 1) rmsnorm_forward_k
           float scale = row_scale, inv = row_inv;
           if constexpr (kGroups == kShared) {
             const int g = group_of(p, c);
-            scale = __uint_as_float(shared.top[g]), inv = shared.inverse[g];
+            scale = words.scales[g], inv = words.inverses[g];
           } else if constexpr (kGroups == kLanes) {
             const int g = group_of(p, c);
-            scale = group_scale(m[k]), inv = __fdiv_rn(1.f, scale);
+            scale = group_scale(m[k]), inv = __frcp_rn(scale);
             if (c == g * p.group) p.scale[row * p.groups + g] = scale;
           }
-#pragma unroll
-          for (int j = 0; j < U; ++j) r[k][j] = quotient(r[k][j], isinf(scale) ? 0.f : scale, inv);
-          store_codes(p.out + row * p.ld_out + c, r[k]);
+          store_quotients(p.out + row * p.ld_out + c, r[k], scale, inv);
         }
       }
     }
   }
 }
 
-template <typename P> size_t group_bytes(GroupKind kind, int teams, const P& p) {
-  return kind == kShared ? size_t(teams) * 4 * p.groups * sizeof(unsigned) : 0;
+// The same for longer rows, which come through a ring that every thread fills
+// for itself (cp.async: each reads only what it copied): kStages rows, one CTA
+// an SM of several teams.  The weights stay in registers.
+template <typename XT, typename RT, GroupKind kGroups, int NU, int kStages>
+__global__ void __launch_bounds__(512, 1) rmsnorm_forward_ring_kernel(const __grid_constant__ RmsNormParams p, const GroupPlan plan,
+                                                               int T) {
+  extern __shared__ uint4 smem[];  // the ring, and [teams] GroupWords, kShared only
+  constexpr int U = 8, kX = int(sizeof(XT)) / 2, kR = int(sizeof(RT)) / 2, kVecs = NU * (kX + kR);
+  __shared__ float red[16][2][32];
+  [[maybe_unused]] __shared__ unsigned top_row[16][2][32];
+  Team team;
+  const int teams = blockDim.x / T;
+  team.id = threadIdx.x / T;
+  team.tid = threadIdx.x - team.id * T;
+  team.threads = T;
+  team.red = &red[team.id][0][0];
+  const int tid = team.tid;
+  f32x2 w[NU][4];
+#pragma unroll
+  for (int k = 0; k < NU; ++k) {
+    const int c = (k * T + tid) * U;
+    float v[U] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
+    if (c < p.h) load_weight(p.w, p.w_bf16, c, v);
+#pragma unroll
+    for (int j = 0; j < 4; ++j) w[k][j] = f2_pack(v[2 * j], v[2 * j + 1]);
+  }
+  const auto slot = [&](int stage, int v) {
+    return reinterpret_cast<unsigned char*>(smem + (stage * kVecs + v) * int(blockDim.x) + int(threadIdx.x));
+  };
+  const auto fetch = [&](long long row, int stage) {
+    if (row < p.s) {
+#pragma unroll
+      for (int k = 0; k < NU; ++k) {
+        const int c = (k * T + tid) * U;
+        if (c < p.h) {
+          const unsigned char* x = p.x + row * p.ld_x + size_t(c) * sizeof(XT);
+#pragma unroll
+          for (int i = 0; i < kX; ++i) copy_async<16, kX == 2>(slot(stage, k * kX + i), x + 16 * i);
+          if (p.res != nullptr) {
+            const unsigned char* r = p.res + row * p.ld_res + size_t(c) * sizeof(RT);
+#pragma unroll
+            for (int i = 0; i < kR; ++i) copy_async<16, kR == 2>(slot(stage, NU * kX + k * kR + i), r + 16 * i);
+          }
+        }
+      }
+    }
+    copy_commit();  // (an empty group past the end keeps the count)
+  };
+  const GroupWords words(reinterpret_cast<unsigned char*>(smem + kStages * kVecs * int(blockDim.x)) + team.id * plan.bytes(), plan);
+  const long long first = (long long)blockIdx.x * teams + team.id, stride = (long long)gridDim.x * teams;
+#pragma unroll
+  for (int i = 0; i < kStages; ++i) fetch(first + i * stride, i);
+  int parity = 0, stage = 0;
+  for (long long row = first; row < p.s; row += stride, parity ^= 1) {
+    copy_wait<kStages - 1>();
+    f32x2 r[NU][4], ss = 0;
+#pragma unroll
+    for (int k = 0; k < NU; ++k) {
+      const int c = (k * T + tid) * U;
+      RawUnit<XT> a;
+      a.zero();
+      if (c < p.h) a.take(slot(stage, k * kX), blockDim.x);
+      float v[U];
+      a.get(v);
+      if (p.res != nullptr) {
+        RawUnit<RT> b;
+        b.zero();
+        if (c < p.h) b.take(slot(stage, NU * kX + k * kR), blockDim.x);
+        float q[U];
+        b.get(q);
+#pragma unroll
+        for (int j = 0; j < U; ++j) v[j] += q[j];
+        if (c < p.h) store_unit(p.res_out + row * p.ld_res_out, c, v, RT());
+      }
+      add_squares(v, r[k], ss);
+    }
+    float s0, s1;
+    f2_unpack(ss, s0, s1);
+    const float rstd = rsqrtf(team.sum(s0 + s1, parity) / float(p.h) + p.eps);
+    fetch(row + kStages * stride, stage);  // (the stage's values are in registers)
+    stage = stage + 1 == kStages ? 0 : stage + 1;
+    if (tid == 0 && p.rstd != nullptr) p.rstd[row] = rstd;
+    const f32x2 rstd2 = f2_pack(rstd, rstd);
+    [[maybe_unused]] unsigned m[NU], all = 0;
+#pragma unroll
+    for (int k = 0; k < NU; ++k) {
+      const int c = (k * T + tid) * U;
+      float v[U];
+#pragma unroll
+      for (int j = 0; j < 4; ++j) {
+        r[k][j] = f2_mul(f2_mul(r[k][j], rstd2), w[k][j]);
+        f2_unpack(r[k][j], v[2 * j], v[2 * j + 1]);
+      }
+      if constexpr (kGroups == kNoCodes) {
+        if (c < p.h) store_unit(p.out + row * p.ld_out, c, v, XT());
+      } else {
+        m[k] = __float_as_uint(most_magnitude(v));
+        all = max(all, m[k]);
+      }
+    }
+    if constexpr (kGroups == kLanes) {
+      const int lanes = p.group / U;
+#pragma unroll
+      for (int o = 1; o < 32; o <<= 1) {
+        if (o < lanes) {
+#pragma unroll
+          for (int k = 0; k < NU; ++k) m[k] = max(m[k], __shfl_xor_sync(kFull, m[k], o));
+        }
+      }
+    } else if constexpr (kGroups == kShared) {
+      segments16(words, m, tid, T, p.h);
+      team.sync();
+      words.join(plan, p.group, tid, T, p.scale + row * p.groups);
+      team.sync();
+    }
+    if constexpr (kGroups != kNoCodes) {
+      float scale = 0.f, inv = 0.f;
+      if constexpr (kGroups == kRow) {
+        scale = group_scale(team.max(all, top_row[team.id][parity]));
+        inv = __frcp_rn(scale);
+        if (tid == 0) p.scale[row] = scale;
+      }
+#pragma unroll
+      for (int k = 0; k < NU; ++k) {
+        const int c = (k * T + tid) * U;
+        if (c < p.h) {
+          if constexpr (kGroups == kLanes) {
+            const int g = group_of(p, c);
+            scale = group_scale(m[k]), inv = __frcp_rn(scale);
+            if (c == g * p.group) p.scale[row * p.groups + g] = scale;
+          } else if constexpr (kGroups == kShared) {
+            const int g = group_of(p, c);
+            scale = words.scales[g], inv = words.inverses[g];
+          }
+          store_quotients(p.out + row * p.ld_out + c, r[k], scale, inv);
+        }
+      }
+    }
+  }
 }
 
 int row_grid(const RmsNormParams& p, int teams, int sms) {
@@ -193,8 +339,23 @@ int row_grid(const RmsNormParams& p, int teams, int sms) {
 template <typename XT, typename RT, GroupKind kGroups, int NU, bool kWarp, int kMaxT = 128>
 void launch(const RmsNormParams& p, int threads, int sms, cudaStream_t st) {
   constexpr int kTeams = kWarp ? 4 : 1;
+  const GroupPlan plan(p, 16, 16);
   rmsnorm_forward_kernel<XT, RT, kGroups, NU, kWarp, kMaxT>
-      <<<row_grid(p, kTeams, sms), kWarp ? 128 : threads, group_bytes(kGroups, kTeams, p), st>>>(p);
+      <<<row_grid(p, kTeams, sms), kWarp ? 128 : threads, kGroups == kShared ? kTeams * plan.bytes() : 0, st>>>(p, plan);
+}
+
+template <typename XT, typename RT, GroupKind kGroups>
+cudaError_t launch_ring(const RmsNormParams& p, int sms, cudaStream_t st) {
+  constexpr int NU = 4, kVecs = NU * int(sizeof(XT) + sizeof(RT)) / 2, kStages = kMaxSmem / (kVecs * 16 * 512);
+  const auto kernel = rmsnorm_forward_ring_kernel<XT, RT, kGroups, NU, kStages>;
+  if (sms == 0)  // set-up (a CTA's GroupWords: three words for 16 columns)
+    return cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kMaxSmem + (kGroups == kShared ? 16 * 1024 : 0));
+  const GroupPlan plan(p, 16, 16);
+  const int T = (p.h / 8 + NU * 32 - 1) / (NU * 32) * 32, teams = 512 / T;
+  const long long rows = (p.s + teams - 1) / teams;
+  const int smem = kStages * kVecs * 16 * T * teams + (kGroups == kShared ? teams * plan.bytes() : 0);
+  kernel<<<int(rows < sms ? rows : sms), T * teams, smem, st>>>(p, plan, T);
+  return cudaSuccess;
 }
 
 template <typename XT, typename RT, GroupKind kGroups>
@@ -205,7 +366,14 @@ void pick_vectors(const RmsNormParams& p, int sms, cudaStream_t st) {
   const int threads = ((units + 3) / 4 + 31) / 32 * 32;
   // (at most 85 registers a thread: three CTAs of 256 on an SM)
   if (threads <= 256) return launch<XT, RT, kGroups, 4, false, 256>(p, threads, sms, st);
-  if (threads <= 512) return launch<XT, RT, kGroups, 4, false, 512>(p, threads, sms, st);
+  // a CTA of more has an SM for itself, and its row's loads, sum and stores would
+  // follow one another: the ring keeps loads under way (s = 4096, h = 16384 bf16
+  // with a residual 105 -> 92 us, without 71 -> 47, in 8 bits 121 -> 84; for
+  // shorter rows three CTAs do that better: s = h = 8192 86 us against 94)
+  if (threads <= 512) {
+    launch_ring<XT, RT, kGroups>(p, sms, st);
+    return;
+  }
   launch<XT, RT, kGroups, 4, false, 1024>(p, threads, sms, st);
 }
 
@@ -225,12 +393,23 @@ void pick(const RmsNormParams& p, bool codes, bool vectors, int sms, cudaStream_
   }
 }
 
+template <typename XT, typename RT, GroupKind kGroups> cudaError_t set_up_ring() {
+  return launch_ring<XT, RT, kGroups>(RmsNormParams{}, 0, nullptr);
+}
+template <typename XT, typename RT> cudaError_t set_up() {
+  cudaError_t e = set_rmsnorm_odd_smem<XT, RT>();
+  if (e == cudaSuccess) e = set_up_ring<XT, RT, kNoCodes>();
+  if (e == cudaSuccess) e = set_up_ring<XT, RT, kLanes>();
+  if (e == cudaSuccess) e = set_up_ring<XT, RT, kShared>();
+  return e == cudaSuccess ? set_up_ring<XT, RT, kRow>() : e;
+}
+
 }  // namespace
 
 cudaError_t set_rmsnorm_forward_smem() {
-  cudaError_t e = set_rmsnorm_odd_smem<float, float>();
-  if (e == cudaSuccess) e = set_rmsnorm_odd_smem<__nv_bfloat16, __nv_bfloat16>();
-  return e == cudaSuccess ? set_rmsnorm_odd_smem<__nv_bfloat16, float>() : e;
+  cudaError_t e = set_up<float, float>();
+  if (e == cudaSuccess) e = set_up<__nv_bfloat16, __nv_bfloat16>();
+  return e == cudaSuccess ? set_up<__nv_bfloat16, float>() : e;
 }
 
 void launch_rmsnorm_forward(const RmsNormParams& p, bool x_bf16, bool res_bf16, bool codes, bool vectors, int sms,

@@ -243,7 +243,7 @@ __device__ __forceinline__ unsigned mag(float v) { return __float_as_uint(v) & 0
 
 // y / s correctly rounded, for inv = 1 / s (Markstein, "Computation of
 // elementary functions on the IBM RISC System/6000 processor", 1990: one
-// residual step); where s is infinite, y inv.
+// residual step); where s is infinite, y inv, with 0 for s.
 __device__ __forceinline__ float quotient(float y, float s, float inv) {
   const float q = __fmul_rn(y, inv);
   return __fmaf_rn(__fmaf_rn(-q, s, y), inv, q);
@@ -260,6 +260,33 @@ __device__ __forceinline__ float group_scale(unsigned top) {
 enum GroupKind { kNoCodes, kLanes, kRow, kShared };
 
 __device__ __forceinline__ int group_of(const RmsNormParams& p, int c) { return int(__umulhi(unsigned(c), p.group_inverse)); }
+
+// kShared: every `segment` columns leave their maximum in shared memory, and a
+// team's first threads join those of a group.
+struct GroupPlan {
+  int segment, segments, groups;  // columns of a segment; segments (up to a multiple of `whole` columns) and groups of a row
+  GroupPlan(const RmsNormParams& p, int segment_, int whole)
+      : segment(segment_), segments((p.h + whole - 1) / whole * (whole / segment_)), groups(p.groups) {}
+  __host__ __device__ int bytes() const { return (segments + 2 * groups + 3) / 4 * 16; }
+};
+struct GroupWords {
+  unsigned* tops;            // [segments]
+  float *scales, *inverses;  // [groups]; an infinite scale is held as 0 (see quotient)
+  __device__ __forceinline__ GroupWords(void* sm, const GroupPlan& g)
+      : tops(static_cast<unsigned*>(sm)), scales(reinterpret_cast<float*>(tops + g.segments)), inverses(scales + g.groups) {}
+  __device__ __forceinline__ void join(const GroupPlan& g, int group, int tid, int T, float* out) const {
+    const int per = group / g.segment;
+    for (int i = tid; i < g.groups; i += T) {
+      const int end = (i + 1) * per < g.segments ? (i + 1) * per : g.segments;
+      unsigned t = 0;
+      for (int j = i * per; j < end; ++j) t = max(t, tops[j]);
+      const float scale = group_scale(t);
+      out[i] = scale;
+      scales[i] = isinf(scale) ? 0.f : scale;
+      inverses[i] = __frcp_rn(scale);
+    }
+  }
+};
 
 // Rows off 16 bytes, and their device set-up: one translation unit for each pair
 // of types (they are many kernels).

@@ -11,14 +11,9 @@ namespace {
 // loaded when they are due).  For kShared, each 128, 64, 32 or 16 columns, the
 // largest of these that a group is a multiple of, leave their maximum in shared
 // memory, and the team's first threads join those of a group.
-struct OddGroups {
-  int segment, segments, groups;  // columns of a segment, segments (of whole 128 columns) and groups of a row
-  __host__ __device__ int bytes() const { return (segments + 2 * groups + 3) / 4 * 16; }
-};
-
 template <typename XT, typename RT, GroupKind kGroups, int kT, int kStages>
 __global__ void __launch_bounds__(kT > 512 ? kT : 512, 1)
-    rmsnorm_forward_odd_kernel(const __grid_constant__ RmsNormParams p, const OddRing ring, const OddGroups og) {
+    rmsnorm_forward_odd_kernel(const __grid_constant__ RmsNormParams p, const OddRing ring, const GroupPlan og) {
   extern __shared__ uint4 smem[];  // [teams][groups' words, kStages rows]
   constexpr int kMaxTeams = kT > 512 ? 1 : 512 / kT, XB = Elem<XT>::kBytes, RB = Elem<RT>::kBytes;
   constexpr bool kRing = kStages > 0, kHoldWeights = kT <= 512;  // (64 registers a thread otherwise)
@@ -40,8 +35,7 @@ __global__ void __launch_bounds__(kT > 512 ? kT : 512, 1)
   const int stage_bytes = ring.bytes(p.res != nullptr ? 1 : 0);
   const int own = (kGroups == kShared ? og.bytes() : 0) + kStages * stage_bytes;
   unsigned char* const base = reinterpret_cast<unsigned char*>(smem) + team.id * own;
-  [[maybe_unused]] unsigned* const tops = reinterpret_cast<unsigned*>(base);
-  [[maybe_unused]] float *const scales = reinterpret_cast<float*>(tops + og.segments), *const inverses = scales + og.groups;
+  const GroupWords words(base, og);
   unsigned char* const rows = base + (kGroups == kShared ? og.bytes() : 0);
   const auto fetch = [&](long long row, int stage) {
     if (row < p.s) {
@@ -107,7 +101,7 @@ __global__ void __launch_bounds__(kT > 512 ? kT : 512, 1)
           r[k] = r[k] * rstd * weight_of(k, whole || c < h ? c : 0);
           m[i] = whole || c < h ? mag(r[k]) : 0u;
         }
-        unsigned* const to = tops + quad / og.segment;
+        unsigned* const to = words.tops + quad / og.segment;
         if (og.segment == 128) {
           const unsigned t = __reduce_max_sync(kFull, max(max(m[0], m[1]), max(m[2], m[3])));
           if (lane == 0) *to = t;
@@ -131,7 +125,7 @@ __global__ void __launch_bounds__(kT > 512 ? kT : 512, 1)
       });
     }
     if constexpr (kGroups == kRow) {
-      const float scale = group_scale(team.max(all, top_row[team.id][parity])), inv = __fdiv_rn(1.f, scale);
+      const float scale = group_scale(team.max(all, top_row[team.id][parity])), inv = __frcp_rn(scale);
       const float s = isinf(scale) ? 0.f : scale;
       if (tid == 0) p.scale[row] = scale;
       columns.each([&](int k, int c, bool inside) {
@@ -139,25 +133,17 @@ __global__ void __launch_bounds__(kT > 512 ? kT : 512, 1)
       });
     } else if constexpr (kGroups == kShared) {
       team.sync();
-      for (int g = tid; g < og.groups; g += kT) {
-        unsigned t = 0;
-        const int per = p.group / og.segment, end = (g + 1) * per < og.segments ? (g + 1) * per : og.segments;
-        for (int i = g * per; i < end; ++i) t = max(t, tops[i]);
-        const float scale = group_scale(t);
-        p.scale[row * og.groups + g] = scale;
-        scales[g] = isinf(scale) ? 0.f : scale;
-        inverses[g] = __fdiv_rn(1.f, scale);
-      }
+      words.join(og, p.group, tid, kT, p.scale + row * og.groups);
       team.sync();
       columns.by_quads([&](int q, int quad, bool whole) {
         int g = group_of(p, quad);
-        float scale = scales[g], inverse = inverses[g];
+        float scale = words.scales[g], inverse = words.inverses[g];
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
           const int k = q * 4 + i, c = quad + i * 32 + lane;
           if (og.segment < 128) {
             g = group_of(p, whole || c < h ? c : 0);
-            scale = scales[g], inverse = inverses[g];
+            scale = words.scales[g], inverse = words.inverses[g];
           }
           if (whole || c < h) store_code(out + c, quotient(r[k], scale, inverse));
         }
@@ -168,7 +154,7 @@ __global__ void __launch_bounds__(kT > 512 ? kT : 512, 1)
 }
 
 template <typename XT, typename RT, GroupKind kGroups, int kT, int kStages>
-cudaError_t launch_odd(const RmsNormParams& p, int teams, const OddRing& ring, const OddGroups& og, int sms, cudaStream_t st) {
+cudaError_t launch_odd(const RmsNormParams& p, int teams, const OddRing& ring, const GroupPlan& og, int sms, cudaStream_t st) {
   const auto kernel = rmsnorm_forward_odd_kernel<XT, RT, kGroups, kT, kStages>;
   if (sms == 0) return cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kMaxSmem);  // set-up
   const size_t smem = size_t(teams) * (kStages * ring.bytes(p.res != nullptr ? 1 : 0) + (kGroups == kShared ? og.bytes() : 0));
@@ -180,10 +166,7 @@ cudaError_t launch_odd(const RmsNormParams& p, int teams, const OddRing& ring, c
 template <typename XT, typename RT, GroupKind kGroups, int kT>
 cudaError_t pick_odd(const RmsNormParams& p, int sms, cudaStream_t st) {
   const OddRing ring(p.h, sizeof(XT), sizeof(RT));
-  OddGroups og = {};
-  og.segment = p.group % 128 == 0 ? 128 : p.group % 64 == 0 ? 64 : p.group % 32 == 0 ? 32 : 16;
-  og.segments = (p.h + 127) / 128 * (128 / og.segment);
-  og.groups = p.groups;
+  const GroupPlan og(p, p.group % 128 == 0 ? 128 : p.group % 64 == 0 ? 64 : p.group % 32 == 0 ? 32 : 16, 128);
   const OddPlan plan(ring.bytes(p.res != nullptr ? 1 : 0), kGroups == kShared ? og.bytes() : 0, kT);
   cudaError_t e = cudaSuccess;
   if constexpr (kT <= 512)
