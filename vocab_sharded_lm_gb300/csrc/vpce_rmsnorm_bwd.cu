@@ -61,15 +61,22 @@ __global__ void __launch_bounds__(kMaxT, 1) rmsnorm_backward_kernel(const __grid
   team.threads = T;
   team.red = &red[team.id][0][0];
   const int tid = team.tid;
-  float acc[NU][U], w[kKeep ? NU : 1][U];
+  // (pairs of fp32 values: one instruction for two)
+  f32x2 acc[NU][4], w[kKeep ? NU : 1][4];
+  const auto pairs = [](const float (&v)[U], f32x2 (&q)[4]) {
+#pragma unroll
+    for (int j = 0; j < 4; ++j) q[j] = f2_pack(v[2 * j], v[2 * j + 1]);
+  };
+  const auto load_w = [&](int c, f32x2 (&q)[4]) {
+    float v[U] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
+    if (c < p.h) load_weight(p.w, p.w_bf16, c, v);
+    pairs(v, q);
+  };
 #pragma unroll
   for (int k = 0; k < NU; ++k) {
 #pragma unroll
-    for (int j = 0; j < U; ++j) acc[k][j] = 0.f;
-    if constexpr (kKeep) {
-      const int c = (k * T + tid) * U;
-      if (c < p.h) load_weight(p.w, p.w_bf16, c, w[k]);
-    }
+    for (int j = 0; j < 4; ++j) acc[k][j] = 0;
+    if constexpr (kKeep) load_w((k * T + tid) * U, w[k]);
   }
 
   // ring slot of part v of a stage: this thread's own bytes
@@ -129,23 +136,27 @@ __global__ void __launch_bounds__(kMaxT, 1) rmsnorm_backward_kernel(const __grid
       if constexpr (kRing) d.take(slot(stage, NU * (kG + kR) + k * kR), blockDim.x);
       else d.load(p.dres + row * p.ld_dres, c);
     };
-    // t = w dy and n = r rstd of a unit
-    const auto terms = [&](int k, int c, const RawUnit<GT>& g, const RawUnit<RT>& x, float (&dy)[U], float (&t)[U],
-                           float (&n)[U]) {
-      if constexpr (!kKeep) load_weight(p.w, p.w_bf16, c, w[0]);
-      g.get(dy);
-      x.get(n);
+    // dy, t = w dy and n = r rstd of a unit
+    const f32x2 rstd2 = f2_pack(rstd, rstd);
+    const auto terms = [&](int k, int c, const RawUnit<GT>& g, const RawUnit<RT>& x, f32x2 (&dy)[4], f32x2 (&t)[4],
+                           f32x2 (&n)[4]) {
+      if constexpr (!kKeep) load_w(c, w[0]);
+      float v[U];
+      g.get(v);
+      pairs(v, dy);
+      x.get(v);
+      pairs(v, n);
 #pragma unroll
-      for (int j = 0; j < U; ++j) {
-        n[j] *= rstd;
-        t[j] = w[kKeep ? k : 0][j] * dy[j];
+      for (int j = 0; j < 4; ++j) {
+        n[j] = f2_mul(n[j], rstd2);
+        t[j] = f2_mul(w[kKeep ? k : 0][j], dy[j]);
       }
     };
     if constexpr (kRing) copy_wait<(kRing ? kStages - 1 : 0)>();
     constexpr int kKept = kKeep ? NU : 1;
     RawUnit<GT> g[kKept];
     RawUnit<RT> x[kKept], d[kKept];
-    float t[kKept][U], n[kKept][U];
+    f32x2 t[kKept][4], n[kKept][4];
     if constexpr (kKeep) {
 #pragma unroll
       for (int k = 0; k < NU; ++k) {
@@ -158,7 +169,7 @@ __global__ void __launch_bounds__(kMaxT, 1) rmsnorm_backward_kernel(const __grid
         }
       }
     }
-    float dot = 0.f;
+    f32x2 dot2 = 0;
 #pragma unroll
     for (int k = 0; k < NU; ++k) {
       const int c = (k * T + tid) * U, at = kKeep ? k : 0;
@@ -167,16 +178,19 @@ __global__ void __launch_bounds__(kMaxT, 1) rmsnorm_backward_kernel(const __grid
           load_g(g[0], k, c);
           load_x(x[0], k, c);
         }
-        float dy[U];
+        f32x2 dy[4];
         terms(k, c, g[at], x[at], dy, t[at], n[at]);
 #pragma unroll
-        for (int j = 0; j < U; ++j) {
-          acc[k][j] = fmaf(dy[j], n[at][j], acc[k][j]);
-          dot = fmaf(t[at][j], n[at][j], dot);
+        for (int j = 0; j < 4; ++j) {
+          acc[k][j] = f2_fma(dy[j], n[at][j], acc[k][j]);
+          dot2 = f2_fma(t[at][j], n[at][j], dot2);
         }
       }
     }
-    dot = team.sum(dot, parity) / float(p.h);
+    float d0, d1;
+    f2_unpack(dot2, d0, d1);
+    const float minus_dot = -team.sum(d0 + d1, parity) / float(p.h);
+    const f32x2 minus_dot2 = f2_pack(minus_dot, minus_dot);
     parity ^= 1;
     if constexpr (kRing && kKeep) fetch(row + kStages * stride, stage);  // (the stage's values are in registers)
 #pragma unroll
@@ -184,7 +198,7 @@ __global__ void __launch_bounds__(kMaxT, 1) rmsnorm_backward_kernel(const __grid
       const int c = (k * T + tid) * U, at = kKeep ? k : 0;
       if (c < p.h) {
         if constexpr (!kKeep) {
-          float dy[U];
+          f32x2 dy[4];
           load_g(g[0], k, c);
           load_x(x[0], k, c);
           d[0].zero();
@@ -194,7 +208,9 @@ __global__ void __launch_bounds__(kMaxT, 1) rmsnorm_backward_kernel(const __grid
         float o[U];
         d[at].get(o);
 #pragma unroll
-        for (int j = 0; j < U; ++j) o[j] = fmaf(rstd, fmaf(-n[at][j], dot, t[at][j]), o[j]);
+        for (int j = 0; j < 4; ++j)
+          f2_unpack(f2_fma(rstd2, f2_fma(n[at][j], minus_dot2, t[at][j]), f2_pack(o[2 * j], o[2 * j + 1])), o[2 * j],
+                    o[2 * j + 1]);
         store_unit(p.dx + row * p.ld_dx, c, o, RT());
       }
     }
@@ -207,12 +223,13 @@ __global__ void __launch_bounds__(kMaxT, 1) rmsnorm_backward_kernel(const __grid
   if constexpr (kRing) copy_wait<0>();  // (what was copied past the last row is nothing)
   float* const mine = own_sums(p, smem, teams, team.id);
 #pragma unroll
-  for (int k = 0; k < NU; ++k)
+  for (int k = 0; k < NU; ++k) {
+    const int c = (k * T + tid) * U;
+    if (c < p.h) {
 #pragma unroll
-    for (int j = 0; j < U; ++j) {
-      const int c = (k * T + tid) * U + j;
-      if (c < p.h) mine[c] = acc[k][j];
+      for (int j = 0; j < 4; ++j) f2_unpack(acc[k][j], mine[c + 2 * j], mine[c + 2 * j + 1]);
     }
+  }
   join_sums(p, smem, teams);
 }
 
