@@ -67,16 +67,28 @@ __global__ void __launch_bounds__(kMaxT, 1) rmsnorm_backward_kernel(const __grid
 #pragma unroll
     for (int j = 0; j < 4; ++j) q[j] = f2_pack(v[2 * j], v[2 * j + 1]);
   };
-  const auto load_w = [&](int c, f32x2 (&q)[4]) {
+  // bf16 weights are held as they are where fp32 pairs have no room (read through
+  // L1, which the ring leaves too small for a row of them, s = 4096, h = 16384
+  // bf16 took 140 us against 97)
+  constexpr bool kHold16 = !kKeep && kMaxT == 512;
+  [[maybe_unused]] uint4 w16[kHold16 ? NU : 1];
+  const auto load_w = [&](int k, int c, f32x2 (&q)[4]) {
     float v[U] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
-    if (c < p.h) load_weight(p.w, p.w_bf16, c, v);
+    if (kHold16 && p.w_bf16) unpack(w16[kHold16 ? k : 0], v, __nv_bfloat16());
+    else if (c < p.h) load_weight(p.w, p.w_bf16, c, v);
     pairs(v, q);
   };
 #pragma unroll
   for (int k = 0; k < NU; ++k) {
 #pragma unroll
     for (int j = 0; j < 4; ++j) acc[k][j] = 0;
-    if constexpr (kKeep) load_w((k * T + tid) * U, w[k]);
+    const int c = (k * T + tid) * U;
+    if constexpr (kKeep) {
+      load_w(k, c, w[k]);
+    } else if constexpr (kHold16) {
+      w16[k] = make_uint4(0, 0, 0, 0);
+      if (p.w_bf16 && c < p.h) w16[k] = __ldg(reinterpret_cast<const uint4*>(p.w + size_t(c) * 2));
+    }
   }
 
   // ring slot of part v of a stage: this thread's own bytes
@@ -140,7 +152,7 @@ __global__ void __launch_bounds__(kMaxT, 1) rmsnorm_backward_kernel(const __grid
     const f32x2 rstd2 = f2_pack(rstd, rstd);
     const auto terms = [&](int k, int c, const RawUnit<GT>& g, const RawUnit<RT>& x, f32x2 (&dy)[4], f32x2 (&t)[4],
                            f32x2 (&n)[4]) {
-      if constexpr (!kKeep) load_w(c, w[0]);
+      if constexpr (!kKeep) load_w(k, c, w[0]);
       float v[U];
       g.get(v);
       pairs(v, dy);
