@@ -695,8 +695,8 @@ vpce_status vpce_rmsnorm_backward(const void* grad_out, vpce_dtype grad_dtype, i
 
 /*
  * One tensor of an optimizer step: n consecutive elements of each array.
- * Arrays need only element alignment; those on 16 bytes (32 for fp32) are
- * moved in vectors.
+ * Arrays need only element alignment; a tensor is moved in vectors where all of
+ * them are on 16 bytes (8-bit states on 8).
  *   param         fp32 or bf16, read and written.
  *   grad          fp32 or bf16, read.
  *   copy          bf16[n], written with the new param rounded, or NULL: the
@@ -762,8 +762,11 @@ vpce_status vpce_grad_norm(const vpce_adamw_tensor* tensors, int64_t n_tensors, 
  *                 lo, hi takes hi where (u + 1/2) / 2^16 < (x - lo) / (hi -
  *                 lo); for sqrt(v) the three are squared, which leaves v's
  *                 expectation as it was.  A v above 0 takes at least the
- *                 smallest code above 0, so that m never meets a v of 0.  The update
- *                 itself uses the unrounded m and v.  u is half k % 8 (low
+ *                 smallest code above 0, so that m never meets a v of 0.  m
+ *                 and v are formed with every fp32 operation rounded by itself,
+ *                 so that the codes are those of a plain evaluation (scale =
+ *                 largest magnitude times fl(1 / 448)).  The update itself
+ *                 uses the unrounded m and v.  u is half k % 8 (low
  *                 halves first) of the Philox4x32-10 block of
  *                 vpce_embedding_dropout_forward with counter = (k / 8, the
  *                 tensor's position in `tensors`, offset's two words), k the
@@ -773,7 +776,8 @@ vpce_status vpce_grad_norm(const vpce_adamw_tensor* tensors, int64_t n_tensors, 
  *                 the kernel, so that a captured graph advances with it.
  *   lr, lr_dev    the rate; lr_dev, a device float, replaces lr where not NULL.
  *                 lr finite, >= 0 (lr_dev's value is not checked).
- *   beta1, beta2  0 <= beta < 1.    eps finite, >= 0.
+ *   beta1, beta2  0 <= beta < 1.
+ *   eps           0, or 2^-126 or more, finite.
  *   grad_scale    device float, or NULL (1).  A value of 0 skips the step:
  *                 nothing is written.
  *   rng           device int64[2]: seed and offset, for state_bits 8 (else

@@ -172,6 +172,81 @@ def test_step_matches_the_oracle(sizes, param, grad, copy, bits, misalign):
         _check(model, before, t, 1e-2, 0.9, b2, 1e-8, 1.0 if scale is None else scale, words)
 
 
+@pytest.mark.parametrize("bits,param,grad", [(32, "fp32", "fp32"), (8, "fp32", "fp32"), (8, "bf16", "bf16"),
+                                             (8, "fp32", "bf16")])
+def test_tensors_of_many_turns(bits, param, grad):
+    # 12 M elements: a CTA takes several turns of 2048 elements
+    model = Model([9000001, 6144, 3000000], param, grad, param == "fp32", bits, seed=11)
+    words = (17, (1 << 33) + 3)
+    before = model.snapshot()
+    vpce.vpce_adamw_step(model.plan, _step(7), lr=1e-2, betas=(0.9, 0.95), grad_scale=torch.tensor([0.5], device="cuda"),
+                         rng=_words(*words))
+    _check(model, before, 7, 1e-2, 0.9, 0.95, 1e-8, 0.5, words)
+
+
+def test_blocks_of_every_kind_in_vectors_and_element_by_element():
+    # blocks of zeros, with a tiny m, a tiny v, of one value, denormal squares:
+    # against the oracle, and the same bits off 16 bytes, where another path runs
+    n, r = 40 * 256, np.random.default_rng(3)
+    g = r.normal(size=(40, 256)) * 1e-2
+    g[0:4] = 0
+    g[4, 3:] = 0                                  # one element of the block
+    g[5:9, ::17] = 1e-9                           # m below e4m3's normal values, v too
+    g[9] = 0.25
+    g[10:14] *= 1e-17                             # squares below fp32's normal numbers
+    g[14, 100] = 1e4                              # all others small beside it
+    g[15:17] *= 1e15
+    out = []
+    for misalign in (0, 1):
+        p = _on_gpu(r.normal(size=n) if not misalign else out[0][0], torch.float32, misalign)
+        start = p.clone()
+        model_g = _on_gpu(g.reshape(-1), torch.float32, misalign)
+        codes = [torch.zeros(n + misalign, dtype=torch.float8_e4m3fn, device="cuda")[misalign:] for _ in range(2)]
+        plan = vpce.vpce_adamw_plan([p], [model_g], weight_decay=0.1, state_bits=8, exp_avg=[codes[0]],
+                                    exp_avg_sq=[codes[1]])
+        for t in (1, 2, 3):
+            vpce.vpce_adamw_step(plan, _step(t), lr=1e-2, betas=(0.9, 0.95), rng=_words(5, t))
+        states = [plan.exp_avg[0].view(torch.uint8), plan.exp_avg_sq[0].view(torch.uint8), plan.exp_avg_scale[0],
+                  plan.exp_avg_sq_scale[0], p]
+        out.append((start.double().cpu().numpy(), [x.clone() for x in states]))
+    assert all(torch.equal(a, b) for a, b in zip(out[0][1], out[1][1]))
+    m8, v8, ms, vs, p = out[0][1]
+    assert not m8[: 4 * 256].any() and not v8[: 4 * 256].any() and bool((ms[:4] == T.TINY).all())
+    keep = (1 - F32(1e-2) * F32(0.1)) ** 3
+    assert np.allclose(p[: 4 * 256].double().cpu().numpy(), out[0][0][: 4 * 256] * keep, rtol=1e-6)
+    assert bool(p.isfinite().all()) and bool(vs.isfinite().all())
+
+
+def test_more_than_31_bits_of_elements():
+    n = (1 << 31) + 4099
+    p = torch.zeros(n, dtype=torch.bfloat16, device="cuda")
+    g = torch.ones(n, dtype=torch.bfloat16, device="cuda")
+    plan = vpce.vpce_adamw_plan([p], [g], weight_decay=0.0, state_bits=8)
+    norm, scale = vpce.vpce_grad_norm(plan, 1.0)
+    assert abs(norm.item() / n ** 0.5 - 1) <= 1e-5 and abs(scale.item() * n ** 0.5 - 1) <= 1e-5
+    vpce.vpce_adamw_step(plan, _step(1), lr=0.5, rng=_words(1, 1))
+    assert bool((p == -0.5).all())
+    for codes, scales in ((plan.exp_avg[0], plan.exp_avg_scale[0]), (plan.exp_avg_sq[0], plan.exp_avg_sq_scale[0])):
+        assert bool((codes.view(torch.uint8) == 0x7E).all()) and bool((scales == scales[0]).all())
+    # the last elements' random words
+    g.mul_(torch.linspace(0.1, 1.0, 1024, device="cuda", dtype=torch.bfloat16).repeat(n // 1024 + 1)[:n])
+    tail = slice(n - n % 256 - 512, n)
+    before = [_np(x) for x in (plan.exp_avg[0][tail], plan.exp_avg_sq[0][tail])]
+    sc = [scales[0].double().item() for scales in (plan.exp_avg_scale[0], plan.exp_avg_sq_scale[0])]
+    vpce.vpce_adamw_step(plan, _step(2), lr=0.5, rng=_words(9, 10))
+    m = 0.9 * before[0] * sc[0] + 0.1 * _np(g[tail])
+    v = 0.999 * (before[1] * sc[1]) ** 2 + 0.001 * _np(g[tail]) ** 2
+    k = np.arange(tail.start, n)
+    words = T.philox4x32_10((k // 8 & 0xFFFFFFFF, 0 * k, 0 * k + 10, 0 * k), (9, 0))
+    half = np.stack([w >> np.uint64(16 * i) & np.uint64(0xFFFF) for w in words for i in (0, 1)], axis=1)
+    u = half[np.arange(k.size), k % 8].astype(np.int64)
+    for x, codes, sq in ((m, plan.exp_avg[0], False), (np.sqrt(v), plan.exp_avg_sq[0], True)):
+        _, each = T.block_scales(x)
+        want, far = T.stochastic_codes(x, each, u, sq)
+        off = _np(codes[tail]) != want
+        assert np.all(far[off] <= 2.0) and off.mean() < 1e-2
+
+
 def test_more_tensors_than_a_launch_holds():
     for bits in (32, 8):
         model = Model([17 + i % 300 for i in range(1000)], bits=bits, seed=3)

@@ -184,8 +184,9 @@ def test_gradient_against_differences(x, residual):
             assert abs((up - down) / (2 * step) - want) <= mag * 2.0 ** -18 / step + step ** 2 * mag * 4
 
 
-def test_in_place_and_empty():
-    s, h = 37, 520
+@pytest.mark.parametrize("h", [520, 515, 4097, 8200])
+def test_in_place_and_empty(h):
+    s = 337
     xs, _ = _rows(1, s, h, "bf16")
     rs, _ = _rows(2, s, h, "bf16", 2.0)
     w, _ = _rows(3, 1, h, "bf16")
@@ -207,7 +208,7 @@ def test_in_place_and_empty():
     none = xs[:0]
     f = vpce.vpce_rmsnorm_forward(none, w[0])
     assert f.out.shape == (0, h)
-    assert vpce.vpce_rmsnorm_quantized_forward(none, w[0], group=64).scale.shape == (0, 9)
+    assert vpce.vpce_rmsnorm_quantized_forward(none, w[0], group=64).scale.shape == (0, -(-h // 64))
     g = torch.full((h,), 2.0, device="cuda")
     vpce.vpce_rmsnorm_backward(none, none, w[0], f.rstd, grad_weight=g, accumulate=True)
     assert bool((g == 2.0).all())
@@ -243,14 +244,26 @@ def test_rows_of_zeros_and_of_what_is_not_finite(h, group):
 
 
 def test_offsets_past_32_bits():
-    # 5 rows, 2^31 elements apart
+    # rows 2^31 elements apart
     s, h, ld = 3, 264, 1 << 31
     big = torch.empty((s - 1) * ld + h, dtype=torch.bfloat16, device="cuda")
     x = big.as_strided((s, h), (ld, 1))
     dense, _ = _rows(1, s, h, "bf16")
     x.copy_(dense)
     w, _ = _rows(2, 1, h, "bf16")
-    assert torch.equal(vpce.vpce_rmsnorm_forward(x, w[0]).out, vpce.vpce_rmsnorm_forward(dense, w[0]).out)
+    f, fd = vpce.vpce_rmsnorm_forward(x, w[0]), vpce.vpce_rmsnorm_forward(dense, w[0])
+    assert torch.equal(f.out, fd.out)
+    q, qd = (vpce.vpce_rmsnorm_quantized_forward(v, w[0], group=16) for v in (x, dense))
+    assert torch.equal(q.q.view(torch.uint8), qd.q.view(torch.uint8)) and torch.equal(q.scale, qd.scale)
+    a, b = (vpce.vpce_rmsnorm_backward(v, v, w[0], f.rstd, grad_residual=v) for v in (x, dense))
+    assert torch.equal(a[0], b[0]) and torch.equal(a[1], b[1])
+    x = big[1:].as_strided((s, h - 1), (ld - 1, 1))          # and off 16 bytes
+    x.copy_(dense[:, 1:])
+    odd = dense[:, 1:].contiguous()
+    f, fd = vpce.vpce_rmsnorm_forward(x, w[0][1:]), vpce.vpce_rmsnorm_forward(odd, w[0][1:])
+    assert torch.equal(f.out, fd.out)
+    a, b = (vpce.vpce_rmsnorm_backward(v, v, w[0][1:], f.rstd, grad_residual=v) for v in (x, odd))
+    assert torch.equal(a[0], b[0]) and torch.equal(a[1], b[1])
 
 
 def test_another_stream_gives_the_same_bits():

@@ -106,7 +106,7 @@ EIGHT = dict(exp_avg_scale=FAKE, exp_avg_sq_scale=FAKE)
     ({}, dict(step=None), 1), ({}, dict(step=FAKE + 4), 2),
     ({}, dict(lr=-1.0), 1), ({}, dict(lr=NAN), 1), ({}, dict(lr=INF), 1), ({}, dict(lr_dev=FAKE + 2), 2),
     ({}, dict(b1=1.0), 1), ({}, dict(b1=-0.1), 1), ({}, dict(b2=1.0), 1), ({}, dict(b2=NAN), 1),
-    ({}, dict(eps=-1e-8), 1), ({}, dict(eps=INF), 1), ({}, dict(scale=FAKE + 1), 2),
+    ({}, dict(eps=-1e-8), 1), ({}, dict(eps=INF), 1), ({}, dict(eps=1e-39), 1), ({}, dict(scale=FAKE + 1), 2),
     (dict(n=-1), {}, 1), (dict(n=1 << 35), {}, 1),
     (dict(param=None), {}, 1), (dict(grad=None), {}, 1), (dict(exp_avg=None), {}, 1), (dict(exp_avg_sq=None), {}, 1),
     (dict(weight_decay=INF), {}, 1), (dict(weight_decay=NAN), {}, 1),

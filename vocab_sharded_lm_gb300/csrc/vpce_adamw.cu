@@ -694,6 +694,7 @@ void step_all(const vpce_adamw_tensor* tensors, long long n, const AdamHyper& hy
   for (long long i = 0; i < n; i += kAdamTensors) {
     const long long count = n - i < kAdamTensors ? n - i : kAdamTensors;
     if (count <= kAdamFewTensors) step_launch<PT, GT, kBits, kAdamFewTensors>(tensors, i, count, hy, sms, st);
+    else if (count <= kAdamSomeTensors) step_launch<PT, GT, kBits, kAdamSomeTensors>(tensors, i, count, hy, sms, st);
     else step_launch<PT, GT, kBits, kAdamTensors>(tensors, i, count, hy, sms, st);
   }
 }
@@ -729,8 +730,9 @@ int norm_all(const vpce_adamw_tensor* tensors, long long n, float* part, int sms
   int parts = 0;
   for (long long i = 0; i < n; i += kAdamTensors) {
     const long long count = n - i < kAdamTensors ? n - i : kAdamTensors;
-    parts += count <= kAdamFewTensors ? norm_launch<GT, kAdamFewTensors>(tensors + i, count, part + parts, sms, st)
-                                      : norm_launch<GT, kAdamTensors>(tensors + i, count, part + parts, sms, st);
+    parts += count <= kAdamFewTensors    ? norm_launch<GT, kAdamFewTensors>(tensors + i, count, part + parts, sms, st)
+             : count <= kAdamSomeTensors ? norm_launch<GT, kAdamSomeTensors>(tensors + i, count, part + parts, sms, st)
+                                         : norm_launch<GT, kAdamTensors>(tensors + i, count, part + parts, sms, st);
   }
   return parts;
 }

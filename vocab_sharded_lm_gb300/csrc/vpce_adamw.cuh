@@ -8,7 +8,8 @@ namespace vpce {
 
 constexpr int kAdamBlock = 256;       // elements that share a scale of 8-bit states
 constexpr int kAdamTensors = 440;     // of one launch: what 32 KB of kernel parameters hold
-constexpr int kAdamFewTensors = 24;   // of the short form: a launch copies its parameters
+constexpr int kAdamFewTensors = 24;   // of the short forms: a launch copies its parameters
+constexpr int kAdamSomeTensors = 100;
 constexpr int kNormThreads = 512;
 constexpr int kNormMaxCtas = 1024;    // of one launch: partial sums that the workspace holds
 

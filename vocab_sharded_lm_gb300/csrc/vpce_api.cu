@@ -1177,7 +1177,8 @@ vpce_status vpce_adamw_step(const vpce_adamw_tensor* tensors, int64_t n_tensors,
   vpce_status st = check_tensors(tensors, n_tensors, grad_dtype);
   if (st != VPCE_OK) return st;
   if (step == nullptr || (state_bits == 8 && rng == nullptr)) return VPCE_ERR_INVALID_ARG;
-  if (!std::isfinite(lr) || lr < 0.f || !std::isfinite(eps) || eps < 0.f || !(beta1 >= 0.0 && beta1 < 1.0) ||
+  // (below fp32's normal numbers eps would vanish in the reciprocal)
+  if (!std::isfinite(lr) || lr < 0.f || !std::isfinite(eps) || !(eps == 0.f || eps >= 0x1p-126f) || !(beta1 >= 0.0 && beta1 < 1.0) ||
       !(beta2 >= 0.0 && beta2 < 1.0))
     return VPCE_ERR_INVALID_ARG;
   if (!aligned(step, 8) || !aligned(lr_dev, 4) || !aligned(grad_scale, 4) || !aligned(rng, 8))

@@ -45,8 +45,8 @@ struct RmsNormBwdParams {
   int accumulate;
 };
 
-// CTAs whose sums of the weight's gradient the workspace holds.
-constexpr int kRmsMaxParts = 1024;
+// CTAs (one an SM) whose sums of the weight's gradient the workspace holds.
+constexpr int kRmsMaxParts = 256;
 
 // Eight consecutive elements of a row as they lie in memory, in 16-byte vectors.
 template <typename T> struct RawUnit;

@@ -366,7 +366,8 @@ cudaError_t launch(const RmsNormBwdParams& p, int team_threads, int sms, cudaStr
   const size_t sums = teams > 1 ? size_t(teams) * p.h * sizeof(float) : 0;
   if (sums > smem) smem = sums;
   const long long rows = (p.s + teams - 1) / teams;
-  *parts = int(rows < sms ? rows : sms);
+  const int most = sms < kRmsMaxParts ? sms : kRmsMaxParts;
+  *parts = int(rows < most ? rows : most);
   kernel<<<*parts, threads, smem, st>>>(p, team_threads);
   return cudaGetLastError();
 }
@@ -379,7 +380,8 @@ cudaError_t launch_odd(const RmsNormBwdParams& p, const OddRing& ring, int teams
   const size_t sums = teams > 1 ? size_t(teams) * p.h * sizeof(float) : 0;
   if (sums > smem) smem = sums;
   const long long rows = (p.s + teams - 1) / teams;
-  *parts = int(rows < sms ? rows : sms);
+  const int most = sms < kRmsMaxParts ? sms : kRmsMaxParts;
+  *parts = int(rows < most ? rows : most);
   kernel<<<*parts, kT * teams, smem, st>>>(p, ring);
   return cudaGetLastError();
 }

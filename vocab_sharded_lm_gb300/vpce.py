@@ -1112,17 +1112,20 @@ def _dtype_code(dt, name):
 
 def _norm_rows(x, shape, dtype, dev, name):
     """Row stride of an [s, h] operand of the norm."""
-    if x.shape != shape or x.get_device() != dev or (x.stride(1) != 1 and shape[1] > 1):
-        raise ValueError(f"{name} must be a tensor of shape {tuple(shape)} on cuda:{dev} with contiguous columns")
+    if x.shape != shape or x.get_device() != dev:
+        raise ValueError(f"{name} must be a tensor of shape {tuple(shape)} on cuda:{dev}")
     if dtype is not None and x.dtype is not dtype:
         raise TypeError(f"{name} must be {dtype}")
-    if shape[0] <= 1:
+    if x.is_contiguous():  # (a decode step calls this for every token)
         return shape[1]
-    return x.stride(0) or _row_ld(x, shape[1], name)
+    ld, column = x.stride()
+    if column != 1 and shape[1] > 1:
+        raise ValueError(f"{name} must have contiguous columns")
+    return (ld or _row_ld(x, shape[1], name)) if shape[0] > 1 else shape[1]
 
 
 def _norm_weight(weight, h, dev):
-    if weight.dim() != 1 or weight.shape[0] != h or weight.get_device() != dev or not weight.is_contiguous():
+    if weight.dim() != 1 or weight.numel() != h or weight.get_device() != dev or not weight.is_contiguous():
         raise ValueError(f"weight must be a contiguous tensor of {h} elements on cuda:{dev}")
     return _dtype_code(weight.dtype, "weight")
 
@@ -1305,6 +1308,9 @@ def _no_overlap(written, read):
             end_written = max(end_written, b)
 
 
+_data_ptr = torch.Tensor.data_ptr
+
+
 class AdamWPlan:
     """Tensors that :func:`vpce_adamw_step` updates together, their gradients
     and their states; made by :func:`vpce_adamw_plan`.  The lists ``params``,
@@ -1350,8 +1356,9 @@ class AdamWPlan:
         self.params, self.grads, self.copies, self.state_bits = params, grads, copies, state_bits
         self.exp_avg, self.exp_avg_sq = exp_avg, exp_avg_sq
         self.exp_avg_scale, self.exp_avg_sq_scale = exp_avg_scale, exp_avg_sq_scale
-        self._dev = dev
-        self._seen = self._addresses()
+        self._dev, self.device = dev, params[0].device
+        self._all = params + grads
+        self._seen = list(map(_data_ptr, self._all))
         n = len(params)
         self._table = (_AdamWTensor * n)(*[
             _AdamWTensor(p, g, _addr(c), m.data_ptr(), v.data_ptr(), _addr(ms), _addr(vs), k, wd)
@@ -1362,13 +1369,10 @@ class AdamWPlan:
     def get_device(self):
         return self._dev
 
-    def _addresses(self):
-        return [x.data_ptr() for x in self.params] + [x.data_ptr() for x in self.grads]
-
     def table(self):
         """The C entries' list; raises where a parameter or gradient has been
         given other memory since the plan was made."""
-        if self._addresses() != self._seen:
+        if list(map(_data_ptr, self._all)) != self._seen:
             raise ValueError("a parameter's or gradient's memory has moved: make a new plan")
         return self._table
 
@@ -1400,7 +1404,7 @@ def vpce_grad_norm(grads, max_norm: float = float("inf"), *, norm_out=None, scal
     where the norm is not finite: the ``grad_scale`` of
     :func:`vpce_adamw_step`, without the host looking at it."""
     if isinstance(grads, AdamWPlan):
-        table, n, code, dev = grads.table(), len(grads.grads), grads.grad_code, grads._dev
+        table, n, code, dev, device = grads.table(), len(grads.grads), grads.grad_code, grads._dev, grads.device
     else:
         grads = list(grads)
         if not grads:
@@ -1408,20 +1412,19 @@ def vpce_grad_norm(grads, max_norm: float = float("inf"), *, norm_out=None, scal
         dev, n = grads[0].get_device(), len(grads)
         if dev < 0:
             raise ValueError("grads must be CUDA tensors")
-        code = _dtype_code(grads[0].dtype, "grads")
+        code, device = _dtype_code(grads[0].dtype, "grads"), grads[0].device
         _list_of(grads, grads, dev, "grads", grads[0].dtype, [g.numel() for g in grads])
         table = (_AdamWTensor * n)(*[_AdamWTensor(None, g.data_ptr(), None, None, None, None, None, g.numel(), 0.0)
                                      for g in grads])
     _check_scalar(norm_out, torch.float32, dev, "norm_out")
     _check_scalar(scale_out, torch.float32, dev, "scale_out")
     if norm_out is None:
-        norm_out = torch.empty((), dtype=torch.float32, device=torch.device("cuda", dev))
+        norm_out = torch.empty((), dtype=torch.float32, device=device)
     if scale_out is None:
-        scale_out = torch.empty((), dtype=torch.float32, device=torch.device("cuda", dev))
+        scale_out = torch.empty((), dtype=torch.float32, device=device)
     lib = _lib or load_library()
     if workspace is None:
-        workspace = torch.empty(lib.vpce_grad_norm_workspace_bytes(n), dtype=torch.uint8,
-                                device=torch.device("cuda", dev))
+        workspace = torch.empty(lib.vpce_grad_norm_workspace_bytes(n), dtype=torch.uint8, device=device)
     elif workspace.get_device() != dev:
         raise ValueError(f"workspace must be on cuda:{dev}")
     status = lib.vpce_grad_norm(table, n, code, max_norm, norm_out.data_ptr(), scale_out.data_ptr(),
