@@ -665,10 +665,12 @@ void step_launch(const vpce_adamw_tensor* tensors, long long first, long long co
   a.n = 0;
   long long total = 0;
   for (long long i = 0; i < count; ++i) total += tensors[first + i].n;
-  // a run: long enough to spread a CTA's start over several turns, short
-  // enough that every SM has some
-  long long turns = total / ((long long)kTile * sms * 8);
-  turns = turns < 1 ? 1 : turns > 16 ? 16 : turns;
+  // a run: long enough to spread a CTA's start over several turns, and some 32
+  // runs an SM, of which three or four are resident, so that the last ones do
+  // not leave SMs idle (12 layers of 512, 8-bit states: 8 runs an SM 119 us, 32
+  // 110; 50304 x 4096: turns up to 16 667 us, up to 10 638)
+  long long turns = total / ((long long)kTile * sms * 32);
+  turns = turns < 1 ? 1 : turns > 10 ? 10 : turns;
   a.run = int(turns) * kTile;
   long long runs = 0;
   for (long long i = 0; i < count; ++i) {
