@@ -1,6 +1,7 @@
 """A policy-gradient step of a tied, vocabulary-sharded language model.
 
     python examples/policy_step.py [--steps 20] [--tokens 1024] [--vocab 16000] [--hidden 512] [--shards 4]
+                                   [--optimizer sgd|adamw] [--state-bits 32|8]
 
 The model is the two ends of one: tokens are looked up in the sharded table
 (scaled, with dropout), the same table is the output head, and the logits of
@@ -17,7 +18,9 @@ every shard stay where the head's product leaves them.  A step
 
 ``--steps`` of plain gradient descent on tokens with a fixed rule (the
 advantage is positive where the sampled token follows it) raise the rule's
-probability; the mask's offset is the step number.
+probability; the mask's offset is the step number.  With ``--optimizer adamw``
+the gradients are clipped to norm 1 (``vpce_grad_norm``) and one
+``vpce_adamw_step`` updates the fp32 shards, their states and the bf16 table.
 """
 from __future__ import annotations
 
@@ -68,8 +71,11 @@ def main(argv=None) -> list[float]:
     ap.add_argument("--vocab", type=int, default=16000)
     ap.add_argument("--hidden", type=int, default=512)
     ap.add_argument("--shards", type=int, default=4)
-    ap.add_argument("--lr", type=float, default=2.0)
+    ap.add_argument("--lr", type=float, default=None, help="2 for sgd, 0.01 for adamw")
+    ap.add_argument("--optimizer", choices=("sgd", "adamw"), default="sgd")
+    ap.add_argument("--state-bits", type=int, choices=(32, 8), default=32)
     a = ap.parse_args(argv)
+    lr = a.lr if a.lr is not None else 2.0 if a.optimizer == "sgd" else 0.01
     gen = torch.Generator(device="cuda")
     gen.manual_seed(1)
     V, h, t = a.vocab, a.hidden, a.shards
@@ -81,13 +87,25 @@ def main(argv=None) -> list[float]:
     targets = (ids * 7 + 3) % V                      # the rule
     targets[:: 16] = -100                            # the prompt's tokens
     advantage = torch.ones(a.tokens, device="cuda")
+    if a.optimizer == "adamw":
+        table = [w.to(torch.bfloat16) for w in master]
+        plan = vpce.vpce_adamw_plan(master, grads, copies=table, weight_decay=0.0, state_bits=a.state_bits)
+        words = torch.tensor([4321, 0], dtype=torch.int64, device="cuda")
+        number = torch.zeros(1, dtype=torch.int64, device="cuda")
     history = []
     for step in range(a.steps):
         rng[1] = step
-        table = [w.to(torch.bfloat16) for w in master]
+        if a.optimizer == "sgd":
+            table = [w.to(torch.bfloat16) for w in master]
         objective, scores = policy_step(table, grads, ids, targets, advantage, vs, rng=rng)
-        for w, g in zip(master, grads):
-            w -= a.lr * g
+        if a.optimizer == "sgd":
+            for w, g in zip(master, grads):
+                w -= lr * g
+        else:
+            number += 1
+            words[1] = step
+            _, scale = vpce.vpce_grad_norm(plan, 1.0)
+            vpce.vpce_adamw_step(plan, number, lr=lr, grad_scale=scale, rng=words)
         live = targets != -100
         logp, entropy = scores.logp[live].mean().item(), scores.entropy[live].mean().item()
         hit = (scores.top_ids[:, 0] == targets)[live].float().mean().item()
