@@ -33,7 +33,7 @@ LIBS = {
     "libvpce_synth.so": ["synth_gen.cu"],
 }
 HEADERS = ["vpce_device.cuh", "vpce_kernels.cuh", "vpce_chunk.cuh", "vpce_tc.cuh", "vpce_logprob.cuh",
-           "vpce_embed_dropout.cuh", "vpce_rmsnorm.cuh", "vpce_rmsnorm_odd.cuh", "vpce_adamw.cuh"]
+           "vpce_embed_dropout.cuh", "vpce_rmsnorm.cuh", "vpce_rmsnorm_odd.cuh", "vpce_adamw.cuh", "vpce_rows.cuh"]
 LINK: dict[str, list[str]] = {}
 
 

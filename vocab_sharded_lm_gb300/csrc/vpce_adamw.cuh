@@ -2,7 +2,7 @@
 // host hands to the kernels.
 #pragma once
 
-#include "vpce_device.cuh"
+#include "vpce_rows.cuh"
 
 namespace vpce {
 

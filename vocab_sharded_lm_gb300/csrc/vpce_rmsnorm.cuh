@@ -2,7 +2,7 @@
 // element access shared by the forward and the gradient.
 #pragma once
 
-#include "vpce_device.cuh"
+#include "vpce_rows.cuh"
 
 namespace vpce {
 

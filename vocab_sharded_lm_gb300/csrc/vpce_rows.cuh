@@ -1,0 +1,46 @@
+// Device-side pieces of the norm and of the AdamW step: copies that every thread
+// makes for itself, and magnitudes of eight values.
+#pragma once
+
+#include "vpce_device.cuh"
+
+namespace vpce {
+
+// global -> shared copies of 4, 8 or 16 bytes that every thread makes for
+// itself (cp.async).  kThroughL1: also for 16 bytes (the others always do).
+template <int kBytes, bool kThroughL1 = kBytes != 16>
+__device__ __forceinline__ void copy_async(void* dst_smem, const void* src) {
+  if constexpr (kThroughL1)
+    asm volatile("cp.async.ca.shared.global [%0], [%1], %2;" ::"r"(smem_addr(dst_smem)), "l"(src), "n"(kBytes) : "memory");
+  else
+    asm volatile("cp.async.cg.shared.global [%0], [%1], %2;" ::"r"(smem_addr(dst_smem)), "l"(src), "n"(kBytes) : "memory");
+}
+// 16 bytes to shared memory of which `bytes` are read and the others set to 0
+__device__ __forceinline__ void copy_async_part(void* dst_smem, const void* src, int bytes) {
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(smem_addr(dst_smem)), "l"(src), "r"(bytes) : "memory");
+}
+__device__ __forceinline__ void copy_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
+// Wait until at most N of this thread's groups of them are incomplete.
+template <int N> __device__ __forceinline__ void copy_wait() {
+  asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
+}
+
+// The largest (a NaN if there is one) and the least magnitude of eight.
+__device__ __forceinline__ float most_magnitude(const float (&x)[8]) {
+  float a, b, c;
+  asm("max.NaN.abs.f32 %0, %1, %2, %3;" : "=f"(a) : "f"(x[0]), "f"(x[1]), "f"(x[2]));
+  asm("max.NaN.abs.f32 %0, %1, %2, %3;" : "=f"(b) : "f"(x[3]), "f"(x[4]), "f"(x[5]));
+  asm("max.NaN.abs.f32 %0, %1, %2, %3;" : "=f"(c) : "f"(x[6]), "f"(x[7]), "f"(a));
+  asm("max.NaN.abs.f32 %0, %1, %2, %2;" : "=f"(a) : "f"(b), "f"(c));
+  return a;
+}
+__device__ __forceinline__ float least_magnitude(const float (&x)[8]) {
+  float a, b, c;
+  asm("min.abs.f32 %0, %1, %2, %3;" : "=f"(a) : "f"(x[0]), "f"(x[1]), "f"(x[2]));
+  asm("min.abs.f32 %0, %1, %2, %3;" : "=f"(b) : "f"(x[3]), "f"(x[4]), "f"(x[5]));
+  asm("min.abs.f32 %0, %1, %2, %3;" : "=f"(c) : "f"(x[6]), "f"(x[7]), "f"(a));
+  asm("min.abs.f32 %0, %1, %2, %2;" : "=f"(a) : "f"(b), "f"(c));
+  return a;
+}
+
+}  // namespace vpce
