@@ -49,6 +49,9 @@ CASES = [
     # s, h, x, residual, weight, pad, misalign
     (1, 1, "fp32", None, "fp32", 0, 0),
     (3, 7, "bf16", "bf16", "fp32", 0, 0),
+    (50, 1, "fp32", "fp32", "fp32", 0, 2),
+    (50, 1, "bf16", "bf16", "bf16", 0, 5),
+    (40, 3, "bf16", "fp32", "fp32", 0, 3),
     (5, 8, "bf16", "fp32", "bf16", 0, 0),
     (9, 256, "bf16", "bf16", "bf16", 8, 0),
     (9, 264, "fp32", "fp32", "bf16", 0, 0),

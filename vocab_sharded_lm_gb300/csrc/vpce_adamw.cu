@@ -20,7 +20,6 @@ namespace {
 constexpr int kThreads = 256;
 constexpr int kPer = 8;                       // consecutive elements of a thread
 constexpr int kTile = kThreads * kPer;        // elements of a CTA's turn
-constexpr float kTiny = 1.17549435e-38f;      // 2^-126: the least scale, so that 1 / scale is finite
 
 struct AdamTensor {
   unsigned char *p, *m, *v, *copy;
@@ -125,19 +124,6 @@ __device__ __forceinline__ float approx_rcp(float x) {
   float y;
   asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
   return y;
-}
-
-__device__ __forceinline__ float block_scale(unsigned top) {
-  const float s = __fmul_rn(__uint_as_float(top), 1.f / 448.f);
-  return s < kTiny ? kTiny : s;  // a NaN stays
-}
-
-// x / s correctly rounded, for inv = 1 / s correctly rounded and x <= 448 s
-// (Markstein, "Computation of elementary functions on the IBM RISC System/6000
-// processor", 1990: one residual step).
-__device__ __forceinline__ float quotient(float x, float s, float inv) {
-  const float q = __fmul_rn(x, inv);
-  return __fmaf_rn(__fmaf_rn(-q, s, x), inv, q);
 }
 
 // Stochastic rounding to e4m3.  A value a takes the e4m3 neighbour above it
@@ -269,7 +255,7 @@ __device__ __forceinline__ void encode8(const float (&xm)[8], const float (&xv)[
     tv = max(tv, b), lv = min(lv, b);
   }
   tm = __reduce_max_sync(kFull, tm), tv = __reduce_max_sync(kFull, tv);
-  sm = block_scale(tm), sv = block_scale(tv);
+  sm = e4m3_scale(tm), sv = e4m3_scale(tv);
   const float im = __fdiv_rn(1.f, sm), iv = __fdiv_rn(1.f, sv);
   const bool normal = __uint_as_float(lm) >= sm * 0x1.1p-6f && __uint_as_float(lv) >= sv * 0x1.1p-6f &&
                       tm < 0x7f800000u && tv < 0x7f800000u;  // of e4m3, with some room
@@ -484,7 +470,7 @@ __global__ void __launch_bounds__(kThreads, kBits == 8 ? 4 : 3) adamw_kernel(con
         // (the root is monotone: the largest v's is the largest)
         const bool second = (threadIdx.x & 16) != 0;
         const float root_top = __fsqrt_rn(__uint_as_float(tv));
-        const float scale = block_scale(second ? __float_as_uint(root_top) : tm), inv = __frcp_rn(scale);
+        const float scale = e4m3_scale(second ? __float_as_uint(root_top) : tm), inv = __frcp_rn(scale);
         sm = __shfl_sync(kFull, scale, 0), sv = __shfl_sync(kFull, scale, 16);
         // v: of e4m3's normal values, with some room, and of root2's range
         // (2.4e-4 > (2^-6)^2: v is compared with the scale's square).  About

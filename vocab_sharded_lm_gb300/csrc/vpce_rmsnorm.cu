@@ -166,7 +166,7 @@ __global__ void __launch_bounds__(kMaxT, kMaxT == 256 ? 3 : 1) rmsnorm_forward_k
     if constexpr (kGroups != kNoCodes) {
       [[maybe_unused]] float row_scale = 0.f, row_inv = 0.f;
       if constexpr (kGroups == kRow) {
-        row_scale = group_scale(team_max<kWarp>(all, top_row[parity]));
+        row_scale = e4m3_scale(team_max<kWarp>(all, top_row[parity]));
         row_inv = __frcp_rn(row_scale);
         if (tid == 0) p.scale[row] = row_scale;
       }
@@ -180,7 +180,7 @@ __global__ void __launch_bounds__(kMaxT, kMaxT == 256 ? 3 : 1) rmsnorm_forward_k
             scale = words.scales[g], inv = words.inverses[g];
           } else if constexpr (kGroups == kLanes) {
             const int g = group_of(p, c);
-            scale = group_scale(m[k]), inv = __frcp_rn(scale);
+            scale = e4m3_scale(m[k]), inv = __frcp_rn(scale);
             if (c == g * p.group) p.scale[row * p.groups + g] = scale;
           }
           store_quotients(p.out + row * p.ld_out + c, r[k], scale, inv);
@@ -308,7 +308,7 @@ __global__ void __launch_bounds__(512, 1) rmsnorm_forward_ring_kernel(const __gr
     if constexpr (kGroups != kNoCodes) {
       float scale = 0.f, inv = 0.f;
       if constexpr (kGroups == kRow) {
-        scale = group_scale(team.max(all, top_row[team.id][parity]));
+        scale = e4m3_scale(team.max(all, top_row[team.id][parity]));
         inv = __frcp_rn(scale);
         if (tid == 0) p.scale[row] = scale;
       }
@@ -318,7 +318,7 @@ __global__ void __launch_bounds__(512, 1) rmsnorm_forward_ring_kernel(const __gr
         if (c < p.h) {
           if constexpr (kGroups == kLanes) {
             const int g = group_of(p, c);
-            scale = group_scale(m[k]), inv = __frcp_rn(scale);
+            scale = e4m3_scale(m[k]), inv = __frcp_rn(scale);
             if (c == g * p.group) p.scale[row * p.groups + g] = scale;
           } else if constexpr (kGroups == kShared) {
             const int g = group_of(p, c);

@@ -174,7 +174,8 @@ struct Team {
 
 // Rows off 16 bytes come through a ring of shared memory per team: a row's bytes
 // are copied as the 16-byte vectors that hold them, the last cut to the row's
-// end; the first may begin in the row before (row 0's is copied by elements).
+// end; the first may begin in the row before (where that is before the array's
+// first element, it is copied by elements).
 // Elements are then read from shared memory, where alignment costs nothing.
 struct OddRing {
   int first, other;  // bytes of a row of the first array and of the others, with room for its offset
@@ -189,7 +190,7 @@ __device__ __forceinline__ void copy_odd_row(unsigned char* dst, const unsigned 
   const unsigned char* const src = base + row * ld;
   const int off = int(uintptr_t(src) & 15), end = off + h * kElement;
   for (int v = tid * 16; v < end; v += kT * 16) {
-    if (v == 0 && off > 0 && row == 0) {
+    if (v == 0 && src - off < base) {
       for (int i = off; i < 16 && i < end; i += kElement) {
         if constexpr (kElement == 2) *reinterpret_cast<short*>(dst + i) = *reinterpret_cast<const short*>(src - off + i);
         else *reinterpret_cast<int*>(dst + i) = *reinterpret_cast<const int*>(src - off + i);
@@ -222,8 +223,6 @@ struct OddPlan {
 // ---------------------------------------------------------------------------
 // e4m3 output
 // ---------------------------------------------------------------------------
-constexpr float kTiny = 1.17549435e-38f;  // 2^-126: the least scale, so that 1 / scale is finite
-
 __device__ __forceinline__ unsigned short e4m3x2(float lo, float hi) {
   unsigned short r;
   asm("cvt.rn.satfinite.e4m3x2.f32 %0, %1, %2;" : "=h"(r) : "f"(hi), "f"(lo));
@@ -240,19 +239,6 @@ __device__ __forceinline__ void store_code(unsigned char* p, float v) { *p = (un
 // |v| as ordered bits: infinities above every number, NaN above them, so that
 // a maximum of these bits carries a NaN on.
 __device__ __forceinline__ unsigned mag(float v) { return __float_as_uint(v) & 0x7fffffffu; }
-
-// y / s correctly rounded, for inv = 1 / s (Markstein, "Computation of
-// elementary functions on the IBM RISC System/6000 processor", 1990: one
-// residual step); where s is infinite, y inv, with 0 for s.
-__device__ __forceinline__ float quotient(float y, float s, float inv) {
-  const float q = __fmul_rn(y, inv);
-  return __fmaf_rn(__fmaf_rn(-q, s, y), inv, q);
-}
-
-__device__ __forceinline__ float group_scale(unsigned top) {
-  const float s = __fmul_rn(__uint_as_float(top), 1.f / 448.f);
-  return s < kTiny ? kTiny : s;  // a NaN stays
-}
 
 // Where a group's largest magnitude is found: in the lanes of a warp that hold
 // the group (16, 32, .. 256 columns in vectors), by the whole team (one group a
@@ -280,7 +266,7 @@ struct GroupWords {
       const int end = (i + 1) * per < g.segments ? (i + 1) * per : g.segments;
       unsigned t = 0;
       for (int j = i * per; j < end; ++j) t = max(t, tops[j]);
-      const float scale = group_scale(t);
+      const float scale = e4m3_scale(t);
       out[i] = scale;
       scales[i] = isinf(scale) ? 0.f : scale;
       inverses[i] = __frcp_rn(scale);

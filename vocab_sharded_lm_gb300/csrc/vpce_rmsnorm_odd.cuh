@@ -125,7 +125,7 @@ __global__ void __launch_bounds__(kT > 512 ? kT : 512, 1)
       });
     }
     if constexpr (kGroups == kRow) {
-      const float scale = group_scale(team.max(all, top_row[team.id][parity])), inv = __frcp_rn(scale);
+      const float scale = e4m3_scale(team.max(all, top_row[team.id][parity])), inv = __frcp_rn(scale);
       const float s = isinf(scale) ? 0.f : scale;
       if (tid == 0) p.scale[row] = scale;
       columns.each([&](int k, int c, bool inside) {

@@ -1,5 +1,5 @@
 // Device-side pieces of the norm and of the AdamW step: copies that every thread
-// makes for itself, and magnitudes of eight values.
+// makes for itself, magnitudes of eight values, and scales of e4m3 codes.
 #pragma once
 
 #include "vpce_device.cuh"
@@ -41,6 +41,22 @@ __device__ __forceinline__ float least_magnitude(const float (&x)[8]) {
   asm("min.abs.f32 %0, %1, %2, %3;" : "=f"(c) : "f"(x[6]), "f"(x[7]), "f"(a));
   asm("min.abs.f32 %0, %1, %2, %2;" : "=f"(a) : "f"(b), "f"(c));
   return a;
+}
+
+// Scale of values whose largest magnitude has the bits `top`: that over e4m3's
+// largest value, at least 2^-126, so that its reciprocal is finite.  A NaN stays.
+__device__ __forceinline__ float e4m3_scale(unsigned top) {
+  const float s = __fmul_rn(__uint_as_float(top), 1.f / 448.f);
+  return s < 0x1p-126f ? 0x1p-126f : s;
+}
+
+// x / s correctly rounded, for inv = 1 / s correctly rounded and |x| at most
+// 448 s or so (Markstein, "Computation of elementary functions on the IBM RISC
+// System/6000 processor", 1990: one residual step).  For an infinite scale, s is
+// given as 0: the result is x inv, 0 or, of an infinity, NaN.
+__device__ __forceinline__ float quotient(float x, float s, float inv) {
+  const float q = __fmul_rn(x, inv);
+  return __fmaf_rn(__fmaf_rn(-q, s, x), inv, q);
 }
 
 }  // namespace vpce

@@ -1346,8 +1346,8 @@ class AdamWPlan:
             exp_avg_sq_scale = _list_of(exp_avg_sq_scale, params, dev, "exp_avg_sq_scale", torch.float32, blocks)
         elif exp_avg_scale is not None or exp_avg_sq_scale is not None:
             raise ValueError("scales belong to 8-bit states")
-        decays = [float(weight_decay)] * len(params) if isinstance(weight_decay, (int, float)) \
-            else [float(w) for w in weight_decay]
+        decays = [float(w) for w in weight_decay] if hasattr(weight_decay, "__len__") \
+            else [float(weight_decay)] * len(params)
         if len(decays) != len(params):
             raise ValueError("weight_decay: one value, or one per parameter")
         none = [None] * len(params)
@@ -1377,7 +1377,7 @@ class AdamWPlan:
         return self._table
 
 
-@_on_its_device
+@functools.partial(_on_its_device, own_stream=True)
 def vpce_adamw_plan(params, grads, *, copies=None, weight_decay=0.01, state_bits: int = 32, exp_avg=None,
                     exp_avg_sq=None, exp_avg_scale=None, exp_avg_sq_scale=None) -> AdamWPlan:
     """The tensors of an AdamW step, checked once: ``params`` (all bf16 or all
