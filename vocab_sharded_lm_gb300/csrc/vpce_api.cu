@@ -28,8 +28,6 @@ cudaError_t set_gemm_bwd_smem();
 cudaError_t set_embed_smem();
 cudaError_t set_logprob_smem();
 cudaError_t set_embed_dropout_smem();
-cudaError_t set_rmsnorm_forward_smem();
-cudaError_t set_rmsnorm_smem();
 size_t lmhead_bwd_workspace_bytes(long long V, long long h);
 size_t lmhead_bwd_min_workspace_bytes(long long V, long long h);
 vpce_status lmhead_backward_run(const void* x, long long ld_x, const void* const* w, long long ld_w, int t,
@@ -97,8 +95,7 @@ vpce_status device_setup(int* sms) {
     } else if (set_backward_smem() != cudaSuccess ||
                set_fused_smem() != cudaSuccess || set_gemm_smem() != cudaSuccess || set_gemm_bwd_smem() != cudaSuccess ||
                set_embed_smem() != cudaSuccess || set_logprob_smem() != cudaSuccess ||
-               set_embed_dropout_smem() != cudaSuccess || set_rmsnorm_forward_smem() != cudaSuccess ||
-               set_rmsnorm_smem() != cudaSuccess) {
+               set_embed_dropout_smem() != cudaSuccess) {
       cudaGetLastError();
       return VPCE_ERR_CUDA;
     } else {
@@ -1057,9 +1054,9 @@ static vpce_status rmsnorm_impl(const void* x, vpce_dtype dtype, int64_t ld_x, c
   p.groups = int((h + p.group - 1) / p.group);
   p.group_inverse = p.group == 1 ? 0xffffffffu : unsigned(((uint64_t(1) << 32) + p.group - 1) / p.group);
   p.rstd = rstd_out;
-  launch_rmsnorm_forward(p, dtype == VPCE_BF16, residual_dtype == VPCE_BF16, codes, vectors, sms,
-                         reinterpret_cast<cudaStream_t>(stream));
-  return launch_status();
+  const cudaError_t e = launch_rmsnorm_forward(p, dtype == VPCE_BF16, residual_dtype == VPCE_BF16, codes, vectors, sms,
+                                               reinterpret_cast<cudaStream_t>(stream));
+  return e == cudaSuccess ? VPCE_OK : VPCE_ERR_CUDA;
 }
 
 vpce_status vpce_rmsnorm_forward(const void* x, vpce_dtype dtype, int64_t ld_x, const void* residual,

@@ -1,10 +1,14 @@
 // Root-mean-square norm with the residual's addition, its output as it is or
-// as e4m3 codes with scales per group of columns.
+// as e4m3 codes with scales per group of columns: rows of 16-byte vectors.
 //
 // One pass: a row is read once into registers as fp32 (r = x + residual), its
 // squares are summed over the row's threads, and the same registers give the
-// output, so the only traffic is the operands'.  It is bound by HBM: at
-// h = 8192 bf16 a row moves 64 KB for some 5 operations an element.
+// output, so the only traffic is the operands'.  It is bound by HBM where there
+// is a residual (64 KB a row at h = 8192 bf16): s = h = 8192 bf16 82 us, 6.5 TB/s
+// of the copy rate's 6.8; with e4m3 output in groups of 128 79 us (5.9 TB/s, the
+// issue slots 56% busy); the latter without a residual is bound by issue (62 us
+// for 203 MB).  Up to 1024 columns a warp takes a row (no barrier), up to 8192 a
+// CTA of at most 256 threads, three of which share an SM; above, the ring kernel.
 #include "vpce_rmsnorm.cuh"
 
 namespace vpce {
@@ -337,29 +341,31 @@ int row_grid(const RmsNormParams& p, int teams, int sms) {
 }
 
 template <typename XT, typename RT, GroupKind kGroups, int NU, bool kWarp, int kMaxT = 128>
-void launch(const RmsNormParams& p, int threads, int sms, cudaStream_t st) {
+cudaError_t launch(const RmsNormParams& p, int threads, int sms, cudaStream_t st) {
   constexpr int kTeams = kWarp ? 4 : 1;
   const GroupPlan plan(p, 16, 16);
   rmsnorm_forward_kernel<XT, RT, kGroups, NU, kWarp, kMaxT>
       <<<row_grid(p, kTeams, sms), kWarp ? 128 : threads, kGroups == kShared ? kTeams * plan.bytes() : 0, st>>>(p, plan);
+  return cudaGetLastError();
 }
 
 template <typename XT, typename RT, GroupKind kGroups>
 cudaError_t launch_ring(const RmsNormParams& p, int sms, cudaStream_t st) {
   constexpr int NU = 4, kVecs = NU * int(sizeof(XT) + sizeof(RT)) / 2, kStages = kMaxSmem / (kVecs * 16 * 512);
   const auto kernel = rmsnorm_forward_ring_kernel<XT, RT, kGroups, NU, kStages>;
-  if (sms == 0)  // set-up (a CTA's GroupWords: three words for 16 columns)
-    return cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kMaxSmem + (kGroups == kShared ? 16 * 1024 : 0));
   const GroupPlan plan(p, 16, 16);
   const int T = (p.h / 8 + NU * 32 - 1) / (NU * 32) * 32, teams = 512 / T;
   const long long rows = (p.s + teams - 1) / teams;
+  // (GroupWords: three words for 16 columns, 12 KB)
   const int smem = kStages * kVecs * 16 * T * teams + (kGroups == kShared ? teams * plan.bytes() : 0);
+  const cudaError_t e = allow_smem(kernel, smem);
+  if (e != cudaSuccess) return e;
   kernel<<<int(rows < sms ? rows : sms), T * teams, smem, st>>>(p, plan, T);
-  return cudaSuccess;
+  return cudaGetLastError();
 }
 
 template <typename XT, typename RT, GroupKind kGroups>
-void pick_vectors(const RmsNormParams& p, int sms, cudaStream_t st) {
+cudaError_t pick_vectors(const RmsNormParams& p, int sms, cudaStream_t st) {
   const int units = p.h / 8;
   if (units <= 32) return launch<XT, RT, kGroups, 1, true>(p, 32, sms, st);
   if (units <= 128) return launch<XT, RT, kGroups, 4, true>(p, 32, sms, st);
@@ -370,53 +376,29 @@ void pick_vectors(const RmsNormParams& p, int sms, cudaStream_t st) {
   // follow one another: the ring keeps loads under way (s = 4096, h = 16384 bf16
   // with a residual 105 -> 92 us, without 71 -> 47, in 8 bits 121 -> 84; for
   // shorter rows three CTAs do that better: s = h = 8192 86 us against 94)
-  if (threads <= 512) {
-    launch_ring<XT, RT, kGroups>(p, sms, st);
-    return;
-  }
-  launch<XT, RT, kGroups, 4, false, 1024>(p, threads, sms, st);
+  if (threads <= 512) return launch_ring<XT, RT, kGroups>(p, sms, st);
+  return launch<XT, RT, kGroups, 4, false, 1024>(p, threads, sms, st);
 }
 
 template <typename XT, typename RT>
-void pick(const RmsNormParams& p, bool codes, bool vectors, int sms, cudaStream_t st) {
+cudaError_t pick(const RmsNormParams& p, bool codes, bool vectors, int sms, cudaStream_t st) {
   const GroupKind kind = !codes ? kNoCodes
                          : p.groups == 1 ? kRow
                          : vectors && p.group <= 256 && (p.group & (p.group - 1)) == 0 ? kLanes
                                                                                        : kShared;
-  if (vectors) {
-    if (kind == kNoCodes) pick_vectors<XT, RT, kNoCodes>(p, sms, st);
-    else if (kind == kRow) pick_vectors<XT, RT, kRow>(p, sms, st);
-    else if (kind == kLanes) pick_vectors<XT, RT, kLanes>(p, sms, st);
-    else pick_vectors<XT, RT, kShared>(p, sms, st);
-  } else {
-    rmsnorm_forward_odd<XT, RT>(p, kind, sms, st);
-  }
-}
-
-template <typename XT, typename RT, GroupKind kGroups> cudaError_t set_up_ring() {
-  return launch_ring<XT, RT, kGroups>(RmsNormParams{}, 0, nullptr);
-}
-template <typename XT, typename RT> cudaError_t set_up() {
-  cudaError_t e = set_rmsnorm_odd_smem<XT, RT>();
-  if (e == cudaSuccess) e = set_up_ring<XT, RT, kNoCodes>();
-  if (e == cudaSuccess) e = set_up_ring<XT, RT, kLanes>();
-  if (e == cudaSuccess) e = set_up_ring<XT, RT, kShared>();
-  return e == cudaSuccess ? set_up_ring<XT, RT, kRow>() : e;
+  if (!vectors) return rmsnorm_forward_odd<XT, RT>(p, kind, sms, st);
+  if (kind == kNoCodes) return pick_vectors<XT, RT, kNoCodes>(p, sms, st);
+  if (kind == kRow) return pick_vectors<XT, RT, kRow>(p, sms, st);
+  return kind == kLanes ? pick_vectors<XT, RT, kLanes>(p, sms, st) : pick_vectors<XT, RT, kShared>(p, sms, st);
 }
 
 }  // namespace
 
-cudaError_t set_rmsnorm_forward_smem() {
-  cudaError_t e = set_up<float, float>();
-  if (e == cudaSuccess) e = set_up<__nv_bfloat16, __nv_bfloat16>();
-  return e == cudaSuccess ? set_up<__nv_bfloat16, float>() : e;
-}
-
-void launch_rmsnorm_forward(const RmsNormParams& p, bool x_bf16, bool res_bf16, bool codes, bool vectors, int sms,
-                            cudaStream_t st) {
-  if (!x_bf16) pick<float, float>(p, codes, vectors, sms, st);
-  else if (res_bf16) pick<__nv_bfloat16, __nv_bfloat16>(p, codes, vectors, sms, st);
-  else pick<__nv_bfloat16, float>(p, codes, vectors, sms, st);
+cudaError_t launch_rmsnorm_forward(const RmsNormParams& p, bool x_bf16, bool res_bf16, bool codes, bool vectors, int sms,
+                                   cudaStream_t st) {
+  if (!x_bf16) return pick<float, float>(p, codes, vectors, sms, st);
+  if (res_bf16) return pick<__nv_bfloat16, __nv_bfloat16>(p, codes, vectors, sms, st);
+  return pick<__nv_bfloat16, float>(p, codes, vectors, sms, st);
 }
 
 }  // namespace vpce

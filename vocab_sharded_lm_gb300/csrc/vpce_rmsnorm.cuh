@@ -201,7 +201,15 @@ __device__ __forceinline__ void copy_odd_row(unsigned char* dst, const unsigned 
   }
 }
 
-constexpr int kMaxSmem = 200 * 1024;  // dynamic shared memory of a CTA that has an SM for itself
+constexpr int kMaxSmem = 200 * 1024;  // a CTA's rings, where it has an SM for itself
+
+// Lets a kernel have more than 48 KB of dynamic shared memory (always the same
+// bound, so that calls from several threads agree).  Done when it is launched:
+// for all of these kernels in a device's set-up it would load them all.
+template <typename K> cudaError_t allow_smem(K* kernel, size_t bytes) {
+  return bytes > 48 * 1024 ? cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kMaxSmem + 16 * 1024)
+                           : cudaSuccess;
+}
 
 // Teams of kT threads on an SM, 512 threads at most (or one team), and the rows
 // of each ring: three where every team can have them, else two, else no ring.
@@ -274,12 +282,11 @@ struct GroupWords {
   }
 };
 
-// Rows off 16 bytes, and their device set-up: one translation unit for each pair
-// of types (they are many kernels).
+// Rows off 16 bytes: one translation unit for each pair of types (they are many
+// kernels).
 template <typename XT, typename RT> cudaError_t rmsnorm_forward_odd(const RmsNormParams& p, GroupKind kind, int sms, cudaStream_t st);
-template <typename XT, typename RT> cudaError_t set_rmsnorm_odd_smem();
 
-void launch_rmsnorm_forward(const RmsNormParams& p, bool x_bf16, bool res_bf16, bool codes, bool vectors, int sms,
+cudaError_t launch_rmsnorm_forward(const RmsNormParams& p, bool x_bf16, bool res_bf16, bool codes, bool vectors, int sms,
                             cudaStream_t st);
 cudaError_t launch_rmsnorm_backward(const RmsNormBwdParams& p, bool dy_bf16, bool x_bf16, bool vectors, int sms,
                                     cudaStream_t st);

@@ -1,5 +1,9 @@
 // The norm of rows off 16 bytes: h not a multiple of 8, or addresses or strides
-// that are not whole vectors.
+// that are not whole vectors.  Read element by element from HBM these rows took
+// twice the time (s = 30001, h = 515 fp32 52 us, with a residual 64); through the
+// ring 25 and 44 us, 5.0 and 5.6 TB/s.  What bounds them now is a row's chain of
+// steps (copies in, sum, output) with one CTA of 16 warps an SM; two CTAs with
+// half the ring and half the registers each were slower (32 and 49 us).
 #pragma once
 
 #include "vpce_rmsnorm.cuh"
@@ -156,11 +160,12 @@ __global__ void __launch_bounds__(kT > 512 ? kT : 512, 1)
 template <typename XT, typename RT, GroupKind kGroups, int kT, int kStages>
 cudaError_t launch_odd(const RmsNormParams& p, int teams, const OddRing& ring, const GroupPlan& og, int sms, cudaStream_t st) {
   const auto kernel = rmsnorm_forward_odd_kernel<XT, RT, kGroups, kT, kStages>;
-  if (sms == 0) return cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kMaxSmem);  // set-up
   const size_t smem = size_t(teams) * (kStages * ring.bytes(p.res != nullptr ? 1 : 0) + (kGroups == kShared ? og.bytes() : 0));
+  const cudaError_t e = allow_smem(kernel, smem);
+  if (e != cudaSuccess) return e;
   const long long rows = (p.s + teams - 1) / teams;
   kernel<<<int(rows < sms ? rows : sms), kT * teams, smem, st>>>(p, ring, og);
-  return cudaSuccess;
+  return cudaGetLastError();
 }
 
 template <typename XT, typename RT, GroupKind kGroups, int kT>
@@ -168,13 +173,11 @@ cudaError_t pick_odd(const RmsNormParams& p, int sms, cudaStream_t st) {
   const OddRing ring(p.h, sizeof(XT), sizeof(RT));
   const GroupPlan og(p, p.group % 128 == 0 ? 128 : p.group % 64 == 0 ? 64 : p.group % 32 == 0 ? 32 : 16, 128);
   const OddPlan plan(ring.bytes(p.res != nullptr ? 1 : 0), kGroups == kShared ? og.bytes() : 0, kT);
-  cudaError_t e = cudaSuccess;
   if constexpr (kT <= 512)
-    if (sms == 0 || plan.stages == 3) e = launch_odd<XT, RT, kGroups, kT, 3>(p, plan.teams, ring, og, sms, st);
-  if (e == cudaSuccess && (sms == 0 || plan.stages == 2)) e = launch_odd<XT, RT, kGroups, kT, 2>(p, plan.teams, ring, og, sms, st);
+    if (plan.stages == 3) return launch_odd<XT, RT, kGroups, kT, 3>(p, plan.teams, ring, og, sms, st);
   if constexpr (kT >= 512)  // (shorter rows always have a ring)
-    if (e == cudaSuccess && (sms == 0 || plan.stages == 0)) e = launch_odd<XT, RT, kGroups, kT, 0>(p, plan.teams, ring, og, sms, st);
-  return e;
+    if (plan.stages == 0) return launch_odd<XT, RT, kGroups, kT, 0>(p, plan.teams, ring, og, sms, st);
+  return launch_odd<XT, RT, kGroups, kT, 2>(p, plan.teams, ring, og, sms, st);
 }
 
 template <typename XT, typename RT, GroupKind kGroups>
@@ -187,28 +190,11 @@ cudaError_t pick_odd(const RmsNormParams& p, int sms, cudaStream_t st) {
   return pick_odd<XT, RT, kGroups, 1024>(p, sms, st);
 }
 
-// one call of each kind of row, with no SMs
-template <typename XT, typename RT, GroupKind kGroups> cudaError_t set_up() {
-  RmsNormParams p = {};
-  cudaError_t e = cudaSuccess;
-  for (int h : {1024, 4096, 16384, VPCE_MAX_NORM_COLUMNS}) {
-    p.h = p.group = h;
-    p.groups = 1;
-    if (e == cudaSuccess) e = pick_odd<XT, RT, kGroups>(p, 0, nullptr);
-  }
-  return e;
-}
 }  // namespace
 
 template <typename XT, typename RT> cudaError_t rmsnorm_forward_odd(const RmsNormParams& p, GroupKind kind, int sms, cudaStream_t st) {
   if (kind == kNoCodes) return pick_odd<XT, RT, kNoCodes>(p, sms, st);
   return kind == kRow ? pick_odd<XT, RT, kRow>(p, sms, st) : pick_odd<XT, RT, kShared>(p, sms, st);
-}
-
-template <typename XT, typename RT> cudaError_t set_rmsnorm_odd_smem() {
-  cudaError_t e = set_up<XT, RT, kNoCodes>();
-  if (e == cudaSuccess) e = set_up<XT, RT, kRow>();
-  return e == cudaSuccess ? set_up<XT, RT, kShared>() : e;
 }
 
 }  // namespace vpce

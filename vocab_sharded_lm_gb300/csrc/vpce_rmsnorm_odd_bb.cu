@@ -3,5 +3,4 @@
 
 namespace vpce {
 template cudaError_t rmsnorm_forward_odd<__nv_bfloat16, __nv_bfloat16>(const RmsNormParams&, GroupKind, int, cudaStream_t);
-template cudaError_t set_rmsnorm_odd_smem<__nv_bfloat16, __nv_bfloat16>();
 }  // namespace vpce

@@ -3,5 +3,4 @@
 
 namespace vpce {
 template cudaError_t rmsnorm_forward_odd<float, float>(const RmsNormParams&, GroupKind, int, cudaStream_t);
-template cudaError_t set_rmsnorm_odd_smem<float, float>();
 }  // namespace vpce
