@@ -634,7 +634,8 @@ vpce_status vpce_embedding_dropout_backward(const void* grad_out, vpce_dtype gra
  * output with another operand is allowed.  Columns past h are not written.
  * The squares' sum is fp32 in a fixed order: rows whose mean square
  * passes fp32's range (|r| about 2^64) give rstd 0, and out 0 (NaN at an
- * infinite r); a NaN makes its row NaN.  Results are bitwise reproducible.
+ * infinite r); a NaN makes its row NaN, and so does a row of zeros at eps 0.
+ * Results are bitwise reproducible.
  */
 #define VPCE_MAX_NORM_COLUMNS 32768
 vpce_status vpce_rmsnorm_forward(const void* x, vpce_dtype dtype, int64_t ld_x, const void* residual,

@@ -389,8 +389,8 @@ __global__ void __launch_bounds__(kThreads, kBits == 8 ? 4 : 3) adamw_kernel(con
                                : (where & 15) == 0 && ((uintptr_t(m) | uintptr_t(v)) & 7) == 0;
   // Whole runs of 8-bit states in vectors come through a ring of two turns that
   // each thread fills for itself, the first of them before anything else is
-  // read: the codes' arithmetic takes half of the SM's issue slots, so loads
-  // have to be under way meanwhile.
+  // read: the codes' arithmetic takes about 70% of the SM's issue slots, so
+  // loads have to be under way meanwhile.
   constexpr bool kRing = kBits == 8;
   __shared__ Ahead<PT> rp[kRing ? 2 : 1];
   __shared__ Ahead<GT> rg[kRing ? 2 : 1];
