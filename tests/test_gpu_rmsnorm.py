@@ -149,6 +149,21 @@ def test_backward_matches_the_oracle(s, h, x, residual, weight, pad, misalign, a
     assert torch.equal(dx2, dx[:, :h]) and torch.equal(dw2, dw)   # the same bits
 
 
+@pytest.mark.parametrize("residual", [False, True])
+@pytest.mark.parametrize("x,r", [("bf16", "bf16"), ("bf16", "fp32"), ("fp32", "fp32")])
+@pytest.mark.parametrize("s,h", [(9, 256), (170, 512), (9, 1024), (330, 2048), (6, 5120), (4, 8192), (3, 16384)])
+def test_rows_that_fill_their_threads(s, h, x, r, residual):
+    # every thread's columns are all of the row's: forms without the branches of
+    # other rows, with and without a residual
+    if r != x and not residual:
+        pytest.skip("the residual's type without a residual")
+    case = (s, h, x, r if residual else None, "bf16", 0, 0)
+    test_forward_matches_the_oracle(*case)
+    for group in (0, 48, 128):
+        test_quantized_forward_matches_the_oracle(*case, group)
+    test_backward_matches_the_oracle(*case, False)
+
+
 def test_backward_of_many_rows_adds_every_row():
     # 20000 rows of equal terms: each column's sum is exact in fp32
     s, h = 20000, 72

@@ -4,11 +4,11 @@
 // One pass: a row is read once into registers as fp32 (r = x + residual), its
 // squares are summed over the row's threads, and the same registers give the
 // output, so the only traffic is the operands'.  It is bound by HBM where there
-// is a residual (64 KB a row at h = 8192 bf16): s = h = 8192 bf16 82 us, 6.5 TB/s
-// of the copy rate's 6.8; with e4m3 output in groups of 128 79 us (5.9 TB/s, the
-// issue slots 56% busy); the latter without a residual is bound by issue (62 us
-// for 203 MB).  Up to 1024 columns a warp takes a row (no barrier), up to 8192 a
-// CTA of at most 256 threads, three of which share an SM; above, the ring kernel.
+// is a residual (64 KB a row at h = 8192 bf16): s = h = 8192 bf16 80 us, 6.7 TB/s
+// of the copy rate's 6.8; with e4m3 output in groups of 128 74 us, 6.4 TB/s; the
+// latter without a residual is bound by issue (53 us for 203 MB).  Up to 1024
+// columns a warp takes a row (no barrier), up to 8192 a CTA of at most 256
+// threads, three of which share an SM; above, the ring kernel.
 #include "vpce_rmsnorm.cuh"
 
 namespace vpce {
@@ -81,13 +81,19 @@ template <bool kWarp> __device__ __forceinline__ unsigned team_max(unsigned v, u
 }
 
 // Rows of 16-byte vectors: a warp (four a CTA) or a CTA a row, NU units of eight
-// columns a thread.
-template <typename XT, typename RT, GroupKind kGroups, int NU, bool kWarp, int kMaxT>
+// columns a thread.  kWhole: every thread's columns are all of the row's, and
+// there is no residual (1) or one (2).  Without a branch around each unit its
+// loads go together: s = h = 8192 bf16 with a residual 80 us instead of 84, in
+// e4m3 with groups of 128 74 instead of 80 (without a residual 53 instead of 62),
+// of 48 76 instead of 95; s = 32768, h = 1024 in e4m3 41 instead of 52.
+template <typename XT, typename RT, GroupKind kGroups, int NU, bool kWarp, int kMaxT, int kWhole>
 __global__ void __launch_bounds__(kMaxT, kMaxT == 256 ? 3 : 1) rmsnorm_forward_kernel(const __grid_constant__ RmsNormParams p, const GroupPlan plan) {
   extern __shared__ uint4 smem[];  // [teams] GroupWords, kShared only
   __shared__ float red[2][32];
   [[maybe_unused]] __shared__ unsigned top_row[2][32];
   constexpr int U = 8;
+  const auto inside = [&](int c) { return kWhole != 0 || c < p.h; };
+  const bool with_res = kWhole != 0 ? kWhole == 2 : p.res != nullptr;
   const int lane = threadIdx.x & 31;
   const int team = kWarp ? int(threadIdx.x >> 5) : 0, teams = kWarp ? int(blockDim.x >> 5) : 1;
   const int tid = kWarp ? lane : int(threadIdx.x), T = kWarp ? 32 : int(blockDim.x);
@@ -101,15 +107,15 @@ __global__ void __launch_bounds__(kMaxT, kMaxT == 256 ? 3 : 1) rmsnorm_forward_k
     for (int k = 0; k < NU; ++k) {
       const int c = (k * T + tid) * U;
       a[k].zero();
-      if (c < p.h) a[k].load(xr, c);
+      if (inside(c)) a[k].load(xr, c);
     }
-    if (p.res != nullptr) {
+    if (with_res) {
       const unsigned char* rr = p.res + row * p.ld_res;
 #pragma unroll
       for (int k = 0; k < NU; ++k) {
         const int c = (k * T + tid) * U;
         b[k].zero();
-        if (c < p.h) b[k].load(rr, c);
+        if (inside(c)) b[k].load(rr, c);
       }
     }
     f32x2 r[NU][4], ss = 0;
@@ -118,12 +124,12 @@ __global__ void __launch_bounds__(kMaxT, kMaxT == 256 ? 3 : 1) rmsnorm_forward_k
       const int c = (k * T + tid) * U;
       float v[U];
       a[k].get(v);
-      if (p.res != nullptr) {
+      if (with_res) {
         float q[U];
         b[k].get(q);
 #pragma unroll
         for (int j = 0; j < U; ++j) v[j] += q[j];
-        if (c < p.h) store_unit(p.res_out + row * p.ld_res_out, c, v, RT());
+        if (inside(c)) store_unit(p.res_out + row * p.ld_res_out, c, v, RT());
       }
       add_squares(v, r[k], ss);
     }
@@ -136,7 +142,7 @@ __global__ void __launch_bounds__(kMaxT, kMaxT == 256 ? 3 : 1) rmsnorm_forward_k
     for (int k = 0; k < NU; ++k) {
       const int c = (k * T + tid) * U;
       m[k] = 0;
-      if (c < p.h) {
+      if (inside(c)) {
         float w[U], v[U];
         load_weight(p.w, p.w_bf16, c, w);
 #pragma unroll
@@ -177,7 +183,7 @@ __global__ void __launch_bounds__(kMaxT, kMaxT == 256 ? 3 : 1) rmsnorm_forward_k
 #pragma unroll
       for (int k = 0; k < NU; ++k) {
         const int c = (k * T + tid) * U;
-        if (c < p.h) {
+        if (inside(c)) {
           float scale = row_scale, inv = row_inv;
           if constexpr (kGroups == kShared) {
             const int g = group_of(p, c);
@@ -197,13 +203,15 @@ __global__ void __launch_bounds__(kMaxT, kMaxT == 256 ? 3 : 1) rmsnorm_forward_k
 // The same for longer rows, which come through a ring that every thread fills
 // for itself (cp.async: each reads only what it copied): kStages rows, one CTA
 // an SM of several teams.  The weights stay in registers.
-template <typename XT, typename RT, GroupKind kGroups, int NU, int kStages>
+template <typename XT, typename RT, GroupKind kGroups, int NU, int kStages, int kWhole>
 __global__ void __launch_bounds__(512, 1) rmsnorm_forward_ring_kernel(const __grid_constant__ RmsNormParams p, const GroupPlan plan,
                                                                int T) {
   extern __shared__ uint4 smem[];  // the ring, and [teams] GroupWords, kShared only
   constexpr int U = 8, kX = int(sizeof(XT)) / 2, kR = int(sizeof(RT)) / 2, kVecs = NU * (kX + kR);
   __shared__ float red[16][2][32];
   [[maybe_unused]] __shared__ unsigned top_row[16][2][32];
+  const auto inside = [&](int c) { return kWhole != 0 || c < p.h; };
+  const bool with_res = kWhole != 0 ? kWhole == 2 : p.res != nullptr;
   Team team;
   const int teams = blockDim.x / T;
   team.id = threadIdx.x / T;
@@ -216,23 +224,23 @@ __global__ void __launch_bounds__(512, 1) rmsnorm_forward_ring_kernel(const __gr
   for (int k = 0; k < NU; ++k) {
     const int c = (k * T + tid) * U;
     float v[U] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
-    if (c < p.h) load_weight(p.w, p.w_bf16, c, v);
+    if (inside(c)) load_weight(p.w, p.w_bf16, c, v);
 #pragma unroll
     for (int j = 0; j < 4; ++j) w[k][j] = f2_pack(v[2 * j], v[2 * j + 1]);
   }
   const auto slot = [&](int stage, int v) {
-    return reinterpret_cast<unsigned char*>(smem + (stage * kVecs + v) * int(blockDim.x) + int(threadIdx.x));
+    return reinterpret_cast<unsigned char*>(smem + (stage * kVecs + v) * 512 + int(threadIdx.x));
   };
   const auto fetch = [&](long long row, int stage) {
     if (row < p.s) {
 #pragma unroll
       for (int k = 0; k < NU; ++k) {
         const int c = (k * T + tid) * U;
-        if (c < p.h) {
+        if (inside(c)) {
           const unsigned char* x = p.x + row * p.ld_x + size_t(c) * sizeof(XT);
 #pragma unroll
           for (int i = 0; i < kX; ++i) copy_async<16, kX == 2>(slot(stage, k * kX + i), x + 16 * i);
-          if (p.res != nullptr) {
+          if (with_res) {
             const unsigned char* r = p.res + row * p.ld_res + size_t(c) * sizeof(RT);
 #pragma unroll
             for (int i = 0; i < kR; ++i) copy_async<16, kR == 2>(slot(stage, NU * kX + k * kR + i), r + 16 * i);
@@ -242,7 +250,7 @@ __global__ void __launch_bounds__(512, 1) rmsnorm_forward_ring_kernel(const __gr
     }
     copy_commit();  // (an empty group past the end keeps the count)
   };
-  const GroupWords words(reinterpret_cast<unsigned char*>(smem + kStages * kVecs * int(blockDim.x)) + team.id * plan.bytes(), plan);
+  const GroupWords words(reinterpret_cast<unsigned char*>(smem + kStages * kVecs * 512) + team.id * plan.bytes(), plan);
   const long long first = (long long)blockIdx.x * teams + team.id, stride = (long long)gridDim.x * teams;
 #pragma unroll
   for (int i = 0; i < kStages; ++i) fetch(first + i * stride, i);
@@ -255,18 +263,18 @@ __global__ void __launch_bounds__(512, 1) rmsnorm_forward_ring_kernel(const __gr
       const int c = (k * T + tid) * U;
       RawUnit<XT> a;
       a.zero();
-      if (c < p.h) a.take(slot(stage, k * kX), blockDim.x);
+      if (inside(c)) a.take(slot(stage, k * kX), 512);
       float v[U];
       a.get(v);
-      if (p.res != nullptr) {
+      if (with_res) {
         RawUnit<RT> b;
         b.zero();
-        if (c < p.h) b.take(slot(stage, NU * kX + k * kR), blockDim.x);
+        if (inside(c)) b.take(slot(stage, NU * kX + k * kR), 512);
         float q[U];
         b.get(q);
 #pragma unroll
         for (int j = 0; j < U; ++j) v[j] += q[j];
-        if (c < p.h) store_unit(p.res_out + row * p.ld_res_out, c, v, RT());
+        if (inside(c)) store_unit(p.res_out + row * p.ld_res_out, c, v, RT());
       }
       add_squares(v, r[k], ss);
     }
@@ -288,7 +296,7 @@ __global__ void __launch_bounds__(512, 1) rmsnorm_forward_ring_kernel(const __gr
         f2_unpack(r[k][j], v[2 * j], v[2 * j + 1]);
       }
       if constexpr (kGroups == kNoCodes) {
-        if (c < p.h) store_unit(p.out + row * p.ld_out, c, v, XT());
+        if (inside(c)) store_unit(p.out + row * p.ld_out, c, v, XT());
       } else {
         m[k] = __float_as_uint(most_magnitude(v));
         all = max(all, m[k]);
@@ -319,7 +327,7 @@ __global__ void __launch_bounds__(512, 1) rmsnorm_forward_ring_kernel(const __gr
 #pragma unroll
       for (int k = 0; k < NU; ++k) {
         const int c = (k * T + tid) * U;
-        if (c < p.h) {
+        if (inside(c)) {
           if constexpr (kGroups == kLanes) {
             const int g = group_of(p, c);
             scale = e4m3_scale(m[k]), inv = __frcp_rn(scale);
@@ -340,24 +348,33 @@ int row_grid(const RmsNormParams& p, int teams, int sms) {
   return int(rows < most ? rows : most);
 }
 
-template <typename XT, typename RT, GroupKind kGroups, int NU, bool kWarp, int kMaxT = 128>
+template <typename XT, typename RT, GroupKind kGroups, int NU, bool kWarp, int kMaxT = 128, int kWhole = 0>
 cudaError_t launch(const RmsNormParams& p, int threads, int sms, cudaStream_t st) {
+  if constexpr (kMaxT <= 256 && kWhole == 0) {
+    if (p.h == NU * 8 * threads)
+      return p.res != nullptr ? launch<XT, RT, kGroups, NU, kWarp, kMaxT, 2>(p, threads, sms, st)
+                              : launch<XT, RT, kGroups, NU, kWarp, kMaxT, 1>(p, threads, sms, st);
+  }
   constexpr int kTeams = kWarp ? 4 : 1;
   const GroupPlan plan(p, 16, 16);
-  rmsnorm_forward_kernel<XT, RT, kGroups, NU, kWarp, kMaxT>
+  rmsnorm_forward_kernel<XT, RT, kGroups, NU, kWarp, kMaxT, kWhole>
       <<<row_grid(p, kTeams, sms), kWarp ? 128 : threads, kGroups == kShared ? kTeams * plan.bytes() : 0, st>>>(p, plan);
   return cudaGetLastError();
 }
 
-template <typename XT, typename RT, GroupKind kGroups>
+template <typename XT, typename RT, GroupKind kGroups, int kWhole = 0>
 cudaError_t launch_ring(const RmsNormParams& p, int sms, cudaStream_t st) {
   constexpr int NU = 4, kVecs = NU * int(sizeof(XT) + sizeof(RT)) / 2, kStages = kMaxSmem / (kVecs * 16 * 512);
-  const auto kernel = rmsnorm_forward_ring_kernel<XT, RT, kGroups, NU, kStages>;
-  const GroupPlan plan(p, 16, 16);
   const int T = (p.h / 8 + NU * 32 - 1) / (NU * 32) * 32, teams = 512 / T;
+  if constexpr (kWhole == 0) {
+    if (p.h == NU * 8 * T)
+      return p.res != nullptr ? launch_ring<XT, RT, kGroups, 2>(p, sms, st) : launch_ring<XT, RT, kGroups, 1>(p, sms, st);
+  }
+  const auto kernel = rmsnorm_forward_ring_kernel<XT, RT, kGroups, NU, kStages, kWhole>;
+  const GroupPlan plan(p, 16, 16);
   const long long rows = (p.s + teams - 1) / teams;
   // (GroupWords: three words for 16 columns, 12 KB)
-  const int smem = kStages * kVecs * 16 * T * teams + (kGroups == kShared ? teams * plan.bytes() : 0);
+  const int smem = kStages * kVecs * 16 * 512 + (kGroups == kShared ? teams * plan.bytes() : 0);
   const cudaError_t e = allow_smem(kernel, smem);
   if (e != cudaSuccess) return e;
   kernel<<<int(rows < sms ? rows : sms), T * teams, smem, st>>>(p, plan, T);
@@ -374,8 +391,9 @@ cudaError_t pick_vectors(const RmsNormParams& p, int sms, cudaStream_t st) {
   if (threads <= 256) return launch<XT, RT, kGroups, 4, false, 256>(p, threads, sms, st);
   // a CTA of more has an SM for itself, and its row's loads, sum and stores would
   // follow one another: the ring keeps loads under way (s = 4096, h = 16384 bf16
-  // with a residual 105 -> 92 us, without 71 -> 47, in 8 bits 121 -> 84; for
-  // shorter rows three CTAs do that better: s = h = 8192 86 us against 94)
+  // with a residual 105 -> 90 us, without 71 -> 47, in 8 bits 121 -> 84; for
+  // shorter rows three CTAs do that better: s = h = 8192 86 us against 94 when
+  // neither had kWhole)
   if (threads <= 512) return launch_ring<XT, RT, kGroups>(p, sms, st);
   return launch<XT, RT, kGroups, 4, false, 1024>(p, threads, sms, st);
 }

@@ -11,10 +11,10 @@
 // copied, so no barrier goes with it), a few rows deep; rows off 16 bytes through
 // one that its team fills.
 //
-// s = h = 8192 bf16 with dresidual: 91 us, 5.9 TB/s over dy, r, dresidual and dr
+// s = h = 8192 bf16 with dresidual: 88 us, 6.1 TB/s over dy, r, dresidual and dr
 // (one team of 512 threads an SM: its barrier and the two passes around it are
-// not hidden by another row's; s = 16384, h = 4096 with two teams 86 us).
-// s = 30001, h = 515 fp32: 40 us, 4.7 TB/s, about 3 us of it the second kernel.
+// not hidden by another row's; s = 16384, h = 4096 with two teams 84 us).
+// s = 30001, h = 515 fp32: 40 us, 4.7 TB/s, about 2 us of it the second kernel.
 #include <type_traits>
 
 #include "vpce_rmsnorm.cuh"
@@ -48,10 +48,14 @@ __device__ __forceinline__ void join_sums(const RmsNormBwdParams& p, const uint4
 // of the ring ahead (0: none, rows are loaded when they are due).  kKeep:
 // products of a row's values stay in registers until its mean is known, and the
 // weights for all rows; else (32 columns a thread) they are read a second time,
-// from the ring or through L1.
+// from the ring or through L1.  kWhole: every thread's columns are all of the
+// row's, and there is no dresidual (1) or one (2): without a branch around each
+// unit and operand s = h = 8192 bf16 takes 88 us instead of 91, without dresidual
+// 73 instead of 78, s = 8192, h = 4096 fp32 115 instead of 138.  (32 columns a
+// thread would spill: s = 4096, h = 16384 bf16 111 us instead of 97.)
 template <typename T> constexpr int kParts = int(sizeof(T)) / 2;  // vectors of a unit
 
-template <typename GT, typename RT, int NU, int kStages, int kMaxT, bool kKeep>
+template <typename GT, typename RT, int NU, int kStages, int kMaxT, bool kKeep, int kWhole>
 __global__ void __launch_bounds__(kMaxT, 1) rmsnorm_backward_kernel(const __grid_constant__ RmsNormBwdParams p,
                                                                     int team_threads) {
   constexpr int U = 8;
@@ -59,6 +63,10 @@ __global__ void __launch_bounds__(kMaxT, 1) rmsnorm_backward_kernel(const __grid
   __shared__ float red[kMaxT / 32][2][32];
   constexpr bool kRing = kStages > 0;
   const int T = team_threads;
+  const auto inside = [&](int c) { return kWhole != 0 || c < p.h; };
+  const bool with_dres = kWhole != 0 ? kWhole == 2 : p.dres != nullptr;
+  // (a constant where an SM's shared memory is the ring's anyway)
+  const int pitch = kMaxT == 512 ? kMaxT : int(blockDim.x);
   Team team;
   const int teams = blockDim.x / T;
   team.id = threadIdx.x / T;
@@ -80,7 +88,7 @@ __global__ void __launch_bounds__(kMaxT, 1) rmsnorm_backward_kernel(const __grid
   const auto load_w = [&](int k, int c, f32x2 (&q)[4]) {
     float v[U] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
     if (kHold16 && p.w_bf16) unpack(w16[kHold16 ? k : 0], v, __nv_bfloat16());
-    else if (c < p.h) load_weight(p.w, p.w_bf16, c, v);
+    else if (inside(c)) load_weight(p.w, p.w_bf16, c, v);
     pairs(v, q);
   };
 #pragma unroll
@@ -92,14 +100,14 @@ __global__ void __launch_bounds__(kMaxT, 1) rmsnorm_backward_kernel(const __grid
       load_w(k, c, w[k]);
     } else if constexpr (kHold16) {
       w16[k] = make_uint4(0, 0, 0, 0);
-      if (p.w_bf16 && c < p.h) w16[k] = __ldg(reinterpret_cast<const uint4*>(p.w + size_t(c) * 2));
+      if (p.w_bf16 && inside(c)) w16[k] = __ldg(reinterpret_cast<const uint4*>(p.w + size_t(c) * 2));
     }
   }
 
   // ring slot of part v of a stage: this thread's own bytes
   constexpr int kG = kParts<GT>, kR = kParts<RT>, kVecs = NU * (kG + 2 * kR), kSlot = 16;
   const auto slot = [&](int stage, int v) {
-    return reinterpret_cast<unsigned char*>(smem) + ((stage * kVecs + v) * int(blockDim.x) + int(threadIdx.x)) * kSlot;
+    return reinterpret_cast<unsigned char*>(smem) + ((stage * kVecs + v) * pitch + int(threadIdx.x)) * kSlot;
   };
   // (the two vectors of eight fp32 values share sectors with each other: those go through L1)
   const auto copy = [&](int stage, int v, const unsigned char* src, auto fp32) {
@@ -113,14 +121,14 @@ __global__ void __launch_bounds__(kMaxT, 1) rmsnorm_backward_kernel(const __grid
 #pragma unroll
       for (int k = 0; k < NU; ++k) {
         const int c = (k * T + tid) * U;
-        if (c < p.h) {
+        if (inside(c)) {
           const unsigned char *g = p.dy + row * p.ld_dy + size_t(c) * sizeof(GT),
                               *x = p.x + row * p.ld_x + size_t(c) * sizeof(RT);
 #pragma unroll
           for (int i = 0; i < kG; ++i) copy(stage, k * kG + i, g + 16 * i, g32);
 #pragma unroll
           for (int i = 0; i < kR; ++i) copy(stage, NU * kG + k * kR + i, x + 16 * i, r32);
-          if (p.dres != nullptr) {
+          if (with_dres) {
             const unsigned char* d = p.dres + row * p.ld_dres + size_t(c) * sizeof(RT);
 #pragma unroll
             for (int i = 0; i < kR; ++i) copy(stage, NU * (kG + kR) + k * kR + i, d + 16 * i, r32);
@@ -142,15 +150,15 @@ __global__ void __launch_bounds__(kMaxT, 1) rmsnorm_backward_kernel(const __grid
     const float rstd = next_rstd;
     if (row + stride < p.s) next_rstd = __ldg(p.rstd + row + stride);
     const auto load_g = [&](RawUnit<GT>& g, int k, int c) {
-      if constexpr (kRing) g.take(slot(stage, k * kG), blockDim.x);
+      if constexpr (kRing) g.take(slot(stage, k * kG), pitch);
       else g.load(p.dy + row * p.ld_dy, c);
     };
     const auto load_x = [&](RawUnit<RT>& x, int k, int c) {
-      if constexpr (kRing) x.take(slot(stage, NU * kG + k * kR), blockDim.x);
+      if constexpr (kRing) x.take(slot(stage, NU * kG + k * kR), pitch);
       else x.load(p.x + row * p.ld_x, c);
     };
     const auto load_d = [&](RawUnit<RT>& d, int k, int c) {
-      if constexpr (kRing) d.take(slot(stage, NU * (kG + kR) + k * kR), blockDim.x);
+      if constexpr (kRing) d.take(slot(stage, NU * (kG + kR) + k * kR), pitch);
       else d.load(p.dres + row * p.ld_dres, c);
     };
     // dy, t = w dy and n = r rstd of a unit
@@ -179,10 +187,10 @@ __global__ void __launch_bounds__(kMaxT, 1) rmsnorm_backward_kernel(const __grid
       for (int k = 0; k < NU; ++k) {
         const int c = (k * T + tid) * U;
         d[k].zero();
-        if (c < p.h) {
+        if (inside(c)) {
           load_g(g[k], k, c);
           load_x(x[k], k, c);
-          if (p.dres != nullptr) load_d(d[k], k, c);
+          if (with_dres) load_d(d[k], k, c);
         }
       }
     }
@@ -190,7 +198,7 @@ __global__ void __launch_bounds__(kMaxT, 1) rmsnorm_backward_kernel(const __grid
 #pragma unroll
     for (int k = 0; k < NU; ++k) {
       const int c = (k * T + tid) * U, at = kKeep ? k : 0;
-      if (c < p.h) {
+      if (inside(c)) {
         if constexpr (!kKeep) {
           load_g(g[0], k, c);
           load_x(x[0], k, c);
@@ -213,13 +221,13 @@ __global__ void __launch_bounds__(kMaxT, 1) rmsnorm_backward_kernel(const __grid
 #pragma unroll
     for (int k = 0; k < NU; ++k) {
       const int c = (k * T + tid) * U, at = kKeep ? k : 0;
-      if (c < p.h) {
+      if (inside(c)) {
         if constexpr (!kKeep) {
           f32x2 dy[4];
           load_g(g[0], k, c);
           load_x(x[0], k, c);
           d[0].zero();
-          if (p.dres != nullptr) load_d(d[0], k, c);
+          if (with_dres) load_d(d[0], k, c);
           terms(k, c, g[0], x[0], dy, t[0], n[0]);
         }
         float o[U];
@@ -242,7 +250,7 @@ __global__ void __launch_bounds__(kMaxT, 1) rmsnorm_backward_kernel(const __grid
 #pragma unroll
   for (int k = 0; k < NU; ++k) {
     const int c = (k * T + tid) * U;
-    if (c < p.h) {
+    if (inside(c)) {
 #pragma unroll
       for (int j = 0; j < 4; ++j) f2_unpack(acc[k][j], mine[c + 2 * j], mine[c + 2 * j + 1]);
     }
@@ -319,14 +327,16 @@ __global__ void __launch_bounds__(kT > 512 ? kT : 512, 1) rmsnorm_backward_odd_k
     dot = team.sum(dot, parity) / float(h);
     parity ^= 1;
     unsigned char* const out = p.dx + row * p.ld_dx;
-    const bool add = dr != nullptr;
-    columns.each([&](int k, int c, bool inside) {
-      if (inside) {
-        const float dy = Elem<GT>::load(gr + c * GB), n = Elem<RT>::load(xr + c * RB) * rstd;
-        const float d = add ? Elem<RT>::load(dr + c * RB) : 0.f;
-        Elem<RT>::store(out + c * RB, fmaf(rstd, fmaf(-n, dot, weight_of(k, c) * dy), d));
-      }
-    });
+    const auto second = [&](auto d_of) {
+      columns.each([&](int k, int c, bool inside) {
+        if (inside) {
+          const float dy = Elem<GT>::load(gr + c * GB), n = Elem<RT>::load(xr + c * RB) * rstd;
+          Elem<RT>::store(out + c * RB, fmaf(rstd, fmaf(-n, dot, weight_of(k, c) * dy), d_of(c)));
+        }
+      });
+    };
+    if (dr != nullptr) second([&](int c) { return Elem<RT>::load(dr + c * RB); });
+    else second([](int) { return 0.f; });
     stage = stage + 1 == kStages ? 0 : stage + 1;
   }
   grid_launch_dependents();
@@ -347,8 +357,15 @@ __global__ void __launch_bounds__(kColumns * kRowLanes) rmsnorm_weight_kernel(co
   const int x = threadIdx.x % kColumns, y = threadIdx.x / kColumns, c = blockIdx.x * kColumns + x;
   float v = 0.f;
   if (c < h) {
-#pragma unroll 8
-    for (int i = y; i < parts; i += kRowLanes) v += __ldcg(part + (long long)i * h + c);
+    // (all of a thread's loads go together)
+    float t[kRmsMaxParts / kRowLanes];
+#pragma unroll
+    for (int k = 0; k < kRmsMaxParts / kRowLanes; ++k) {
+      const int i = k * kRowLanes + y;
+      t[k] = i < parts ? __ldcg(part + (long long)i * h + c) : 0.f;
+    }
+#pragma unroll
+    for (int k = 0; k < kRmsMaxParts / kRowLanes; ++k) v += t[k];
   }
   sm[y][x] = v;
   __syncthreads();
@@ -360,13 +377,18 @@ __global__ void __launch_bounds__(kColumns * kRowLanes) rmsnorm_weight_kernel(co
   if (x == 0 && col < h) dw[col] = accumulate ? dw[col] + v : v;
 }
 
-template <typename GT, typename RT, int NU, int kStages, int kMaxT, bool kKeep>
+template <typename GT, typename RT, int NU, int kStages, int kMaxT, bool kKeep, int kWhole = 0>
 cudaError_t launch(const RmsNormBwdParams& p, int team_threads, int sms, cudaStream_t st, int* parts) {
-  const auto kernel = rmsnorm_backward_kernel<GT, RT, NU, kStages, kMaxT, kKeep>;
+  if constexpr (kKeep && NU > 1 && kWhole == 0) {
+    if (p.h == NU * 8 * team_threads)
+      return p.dres != nullptr ? launch<GT, RT, NU, kStages, kMaxT, kKeep, 2>(p, team_threads, sms, st, parts)
+                               : launch<GT, RT, NU, kStages, kMaxT, kKeep, 1>(p, team_threads, sms, st, parts);
+  }
+  const auto kernel = rmsnorm_backward_kernel<GT, RT, NU, kStages, kMaxT, kKeep, kWhole>;
   const int teams = team_threads < kMaxT ? kMaxT / team_threads : 1, threads = team_threads * teams;
   constexpr size_t kStageBytes = size_t(NU) * (kParts<GT> + 2 * kParts<RT>)*16;  // of a thread
   static_assert(kStages * kStageBytes * kMaxT <= kMaxSmem && NU * 8 * 4 * kMaxT <= kMaxSmem, "fits an SM");
-  size_t smem = kStages * kStageBytes * threads;
+  size_t smem = kStages * kStageBytes * (kMaxT == 512 ? kMaxT : threads);
   const size_t sums = teams > 1 ? size_t(teams) * p.h * sizeof(float) : 0;
   if (sums > smem) smem = sums;
   const cudaError_t e = allow_smem(kernel, smem);
