@@ -234,6 +234,11 @@ def test_in_place_and_empty(h):
     assert not g.any()
 
 
+@pytest.mark.parametrize("h", [256, 512, 1024, 8192, 16384])
+def test_in_place_in_rows_that_fill_their_threads(h):
+    test_in_place_and_empty(h)
+
+
 @pytest.mark.parametrize("h,group", [(512, 128), (515, 64), (2048, 0)])
 def test_rows_of_zeros_and_of_what_is_not_finite(h, group):
     x = torch.ones(6, h, device="cuda")
