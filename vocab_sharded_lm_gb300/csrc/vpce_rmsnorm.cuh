@@ -203,11 +203,12 @@ __device__ __forceinline__ void copy_odd_row(unsigned char* dst, const unsigned 
 
 constexpr int kMaxSmem = 200 * 1024;  // a CTA's rings, where it has an SM for itself
 
-// Lets a kernel have more than 48 KB of dynamic shared memory (always the same
-// bound, so that calls from several threads agree).  Done when it is launched:
-// for all of these kernels in a device's set-up it would load them all.
+// Lets a kernel have more shared memory than every launch may: 48 KB of static
+// and dynamic memory together, and these kernels' own is 8 KB at most.  (Always
+// the same bound, so that calls from several threads agree.  Done when a kernel
+// is launched: for all of these kernels in a device's set-up it would load them all.)
 template <typename K> cudaError_t allow_smem(K* kernel, size_t bytes) {
-  return bytes > 48 * 1024 ? cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kMaxSmem + 16 * 1024)
+  return bytes > 40 * 1024 ? cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kMaxSmem + 16 * 1024)
                            : cudaSuccess;
 }
 
