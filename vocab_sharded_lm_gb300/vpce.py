@@ -10,6 +10,7 @@ from __future__ import annotations
 import ctypes
 import functools
 import inspect
+import itertools
 import os
 import threading
 from typing import Any, NamedTuple
@@ -1316,7 +1317,9 @@ class AdamWPlan:
     and their states; made by :func:`vpce_adamw_plan`.  The lists ``params``,
     ``grads``, ``copies``, ``exp_avg``, ``exp_avg_sq`` (and, for 8-bit states,
     ``exp_avg_scale`` and ``exp_avg_sq_scale``) hold the tensors, as a
-    checkpoint saves them; entries are not to be replaced."""
+    checkpoint saves them; one is loaded by ``copy_`` into them.  The addresses
+    are those of the plan's making, and the plan keeps that memory: a step
+    raises where an entry was replaced or its tensor given other memory."""
 
     def __init__(self, params, grads, copies, weight_decay, state_bits, exp_avg, exp_avg_sq, exp_avg_scale,
                  exp_avg_sq_scale):
@@ -1357,23 +1360,34 @@ class AdamWPlan:
         self.exp_avg, self.exp_avg_sq = exp_avg, exp_avg_sq
         self.exp_avg_scale, self.exp_avg_sq_scale = exp_avg_scale, exp_avg_sq_scale
         self._dev, self.device = dev, params[0].device
-        self._all = params + grads
-        self._seen = list(map(_data_ptr, self._all))
+        self._lists = [xs for xs in (params, grads, copies, exp_avg, exp_avg_sq, exp_avg_scale, exp_avg_sq_scale)
+                       if xs is not None]
+        self._seen, self._seen_grads = self._addresses(), list(map(_data_ptr, grads))
+        self._held = [x.untyped_storage() for xs in self._lists for x in xs]  # (no other tensor gets their addresses)
         n = len(params)
         self._table = (_AdamWTensor * n)(*[
-            _AdamWTensor(p, g, _addr(c), m.data_ptr(), v.data_ptr(), _addr(ms), _addr(vs), k, wd)
-            for p, g, c, m, v, ms, vs, k, wd in zip(self._seen[:n], self._seen[n:], copies or none, exp_avg,
+            _AdamWTensor(p.data_ptr(), g.data_ptr(), _addr(c), m.data_ptr(), v.data_ptr(), _addr(ms), _addr(vs), k, wd)
+            for p, g, c, m, v, ms, vs, k, wd in zip(params, grads, copies or none, exp_avg,
                                                     exp_avg_sq, exp_avg_scale or none, exp_avg_sq_scale or none,
                                                     sizes, decays)])
 
     def get_device(self):
         return self._dev
 
+    def _addresses(self):
+        return list(map(_data_ptr, itertools.chain.from_iterable(self._lists)))
+
     def table(self):
-        """The C entries' list; raises where a parameter or gradient has been
-        given other memory since the plan was made."""
-        if list(map(_data_ptr, self._all)) != self._seen:
-            raise ValueError("a parameter's or gradient's memory has moved: make a new plan")
+        """The C entries' list; raises where a tensor of the plan is not in the
+        memory that it was in when the plan was made."""
+        if self._addresses() != self._seen:
+            raise ValueError("the memory of a parameter, gradient, copy or state has moved: make a new plan")
+        return self._table
+
+    def grad_table(self):
+        """The same for a call that reads the gradients alone."""
+        if list(map(_data_ptr, self.grads)) != self._seen_grads:
+            raise ValueError("a gradient's memory has moved: make a new plan")
         return self._table
 
 
@@ -1381,7 +1395,8 @@ class AdamWPlan:
 def vpce_adamw_plan(params, grads, *, copies=None, weight_decay=0.01, state_bits: int = 32, exp_avg=None,
                     exp_avg_sq=None, exp_avg_scale=None, exp_avg_sq_scale=None) -> AdamWPlan:
     """The tensors of an AdamW step, checked once: ``params`` (all bf16 or all
-    fp32), ``grads`` (likewise; read at every step where they are now),
+    fp32), ``grads`` (likewise; these tensors' values at the time of a step: a
+    loop that drops its gradients and gets others makes a new plan for them),
     ``copies`` (bf16, written with the new fp32 params: the weights that the
     LM head reads), ``weight_decay`` (one value, or one per parameter).  The
     states are made of zeros where they are not given: float32, or with
@@ -1404,7 +1419,7 @@ def vpce_grad_norm(grads, max_norm: float = float("inf"), *, norm_out=None, scal
     where the norm is not finite: the ``grad_scale`` of
     :func:`vpce_adamw_step`, without the host looking at it."""
     if isinstance(grads, AdamWPlan):
-        table, n, code, dev, device = grads.table(), len(grads.grads), grads.grad_code, grads._dev, grads.device
+        table, n, code, dev, device = grads.grad_table(), len(grads.grads), grads.grad_code, grads._dev, grads.device
     else:
         grads = list(grads)
         if not grads:
