@@ -102,9 +102,9 @@ def main(argv=None) -> list[float]:
             for w, g in zip(master, grads):
                 w -= lr * g
         else:
-            number += 1
             words[1] = step
             _, scale = vpce.vpce_grad_norm(plan, 1.0)
+            number += scale != 0     # a step that is skipped is not counted, and the host does not look
             vpce.vpce_adamw_step(plan, number, lr=lr, grad_scale=scale, rng=words)
         live = targets != -100
         logp, entropy = scores.logp[live].mean().item(), scores.entropy[live].mean().item()

@@ -780,7 +780,9 @@ vpce_status vpce_grad_norm(const vpce_adamw_tensor* tensors, int64_t n_tensors, 
  *   beta1, beta2  0 <= beta < 1.
  *   eps           0, or 2^-126 or more, finite.
  *   grad_scale    device float, or NULL (1).  A value of 0 skips the step:
- *                 nothing is written.
+ *                 nothing is written.  A caller that counts steps should not
+ *                 count it (beta^t belongs to the updates that m and v have
+ *                 had): on the device, t += grad_scale != 0 before the call.
  *   rng           device int64[2]: seed and offset, for state_bits 8 (else
  *                 NULL is taken too); pass another offset every step, and
  *                 another seed than a dropout's.

@@ -1456,7 +1456,9 @@ def vpce_adamw_step(plan, step, *, lr, betas=(0.9, 0.999), eps: float = 1e-8, gr
     from 1; ``lr`` a number or a CUDA float32 tensor of one element; both, like
     ``grad_scale`` (float32, one element, from :func:`vpce_grad_norm`;
     gradients are multiplied by it, and 0 skips the step), are read by the
-    kernel, so that a captured step goes on with new values.  8-bit states
+    kernel, so that a captured step goes on with new values.  A skipped step
+    is none of the states' steps: ``step += grad_scale != 0`` before the call
+    counts without the host looking.  8-bit states
     need ``rng`` (CUDA int64 ``[seed, offset]``), the words of their stochastic
     rounding: another offset every step."""
     if not isinstance(plan, AdamWPlan):
