@@ -248,6 +248,18 @@ __device__ __forceinline__ void decode8(uint2 cm, uint2 cv, float sm, float sv, 
   }
 }
 
+// quotient() is correctly rounded for scales from 2^-95 up; below, its residual
+// passes fp32's smallest number.  m's scale may lie there (rows of a table that
+// have had no gradient for long), the root of v's not: v is 0 or 2^-149 at least.
+constexpr float kExactScale = 0x1p-94f;
+// What both sides of such a quotient are multiplied by, and the reciprocal
+// divided by, without rounding.
+struct ExactScale {
+  float up, down;
+  __device__ __forceinline__ explicit ExactScale(float s)
+      : up(s < kExactScale ? 0x1p64f : 1.f), down(s < kExactScale ? 0x1p-64f : 1.f) {}
+};
+
 // New codes and scales of a block of 256 elements, eight a lane: m in xm, the
 // root of v in xv, `inside` false on lanes past the block's end.
 __device__ __forceinline__ void encode8(const float (&xm)[8], const float (&xv)[8], uint4 random, bool inside, uint2& cm,
@@ -263,7 +275,7 @@ __device__ __forceinline__ void encode8(const float (&xm)[8], const float (&xv)[
   sm = e4m3_scale(tm), sv = e4m3_scale(tv);
   const float im = __fdiv_rn(1.f, sm), iv = __fdiv_rn(1.f, sv);
   const bool normal = __uint_as_float(lm) >= sm * 0x1.1p-6f && __uint_as_float(lv) >= sv * 0x1.1p-6f &&
-                      tm < 0x7f800000u && tv < 0x7f800000u;  // of e4m3, with some room
+                      tm < 0x7f800000u && tv < 0x7f800000u && sm >= kExactScale;  // of e4m3, with some room
   const unsigned word[4] = {random.x, random.y, random.z, random.w};
   unsigned m2[4], v2[4];
   // (about one block in 50 of normally distributed gradients has an element
@@ -278,12 +290,15 @@ __device__ __forceinline__ void encode8(const float (&xm)[8], const float (&xv)[
       v2[j / 2] = pack_codes(round_squares(quotient(xv[j], sv, iv), u0), round_squares(quotient(xv[j + 1], sv, iv), u1));
     }
   } else {
+    const ExactScale by(sm);
+    const float s = sm * by.up, inv = im * by.down;
 #pragma unroll
     for (int j = 0; j < 8; j += 2) {
       RoundWord u0, u1;
       u0.set<false>(word[j / 2]);
       u1.set<true>(word[j / 2]);
-      m2[j / 2] = pack_codes(round_any<false>(quotient(xm[j], sm, im), u0), round_any<false>(quotient(xm[j + 1], sm, im), u1));
+      m2[j / 2] = pack_codes(round_any<false>(quotient(xm[j] * by.up, s, inv), u0),
+                             round_any<false>(quotient(xm[j + 1] * by.up, s, inv), u1));
       v2[j / 2] = pack_codes(round_any<true>(quotient(xv[j], sv, iv), u0), round_any<true>(quotient(xv[j + 1], sv, iv), u1));
     }
   }
@@ -335,12 +350,18 @@ __device__ __forceinline__ f32x2 quotient2(f32x2 x, f32x2 minus_s, f32x2 inv) {
   return f2_fma(f2_fma(q, minus_s, x), inv, q);
 }
 
-// round_linear (with `small`: round_linear_small) and round_squares of two values
-__device__ __forceinline__ unsigned linear_codes2(f32x2 a, const RoundWord& u0, const RoundWord& u1, bool small) {
-  float x, y;
-  f2_unpack(a, x, y);
-  if (small) return pack_codes(round_linear_small(x, u0), round_linear_small(y, u1));
-  return pack_codes(round_linear(x, u0), round_linear(y, u1));
+// round_linear of two quotients x / s (with `small`: round_linear_small, and x
+// and s as ExactScale has them), and round_squares of two values
+__device__ __forceinline__ unsigned linear_codes2(f32x2 x, float s, float inv, const RoundWord& u0, const RoundWord& u1,
+                                                  bool small) {
+  float a, b;
+  if (small) {
+    const ExactScale by(s);
+    f2_unpack(quotient2(f2_mul(x, both(by.up)), both(-s * by.up), both(inv * by.down)), a, b);
+    return pack_codes(round_linear_small(a, u0), round_linear_small(b, u1));
+  }
+  f2_unpack(quotient2(x, both(-s), both(inv)), a, b);
+  return pack_codes(round_linear(a, u0), round_linear(b, u1));
 }
 __device__ __forceinline__ unsigned square_codes2(f32x2 a, const RoundWord& u0, const RoundWord& u1) {
   float x, y, ax, ay, tx, ty;
@@ -481,11 +502,11 @@ __global__ void __launch_bounds__(kThreads, kBits == 8 ? 4 : 3) adamw_kernel(con
         // (2.4e-4 > (2^-6)^2: v is compared with the scale's square).  About
         // one block in 50 of normally distributed gradients has an m below them.
         const bool ordinary = lv >= fmaxf(sv * sv * 2.8e-4f, 0x1p-100f) && tm < 0x7f800000u && tv < 0x7f000000u;
-        const bool small = !__all_sync(kFull, lm >= sm * 0x1.1p-6f);
+        const bool small = !__all_sync(kFull, lm >= sm * 0x1.1p-6f) || sm < kExactScale;
         uint2 cm, cv;
         if (__all_sync(kFull, ordinary)) {
           const float im = __shfl_sync(kFull, inv, 0), iv = __shfl_sync(kFull, inv, 16);
-          const f32x2 im2 = both(im), iv2 = both(iv), nsm = both(-sm), nsv = both(-sv);
+          const f32x2 iv2 = both(iv), nsv = both(-sv);
           const unsigned word[4] = {random.x, random.y, random.z, random.w};
           unsigned mc[4], vc[4];
 #pragma unroll
@@ -497,7 +518,7 @@ __global__ void __launch_bounds__(kThreads, kBits == 8 ? 4 : 3) adamw_kernel(con
             RoundWord u0, u1;
             u0.set<false>(word[j]);
             u1.set<true>(word[j]);
-            mc[j] = linear_codes2(quotient2(xm[j], nsm, im2), u0, u1, small);
+            mc[j] = linear_codes2(xm[j], sm, im, u0, u1, small);
             vc[j] = square_codes2(quotient2(root, nsv, iv2), u0, u1);
           }
           cm = make_uint2(mc[0] | mc[1] << 16, mc[2] | mc[3] << 16);

@@ -50,10 +50,11 @@ __device__ __forceinline__ float e4m3_scale(unsigned top) {
   return s < 0x1p-126f ? 0x1p-126f : s;
 }
 
-// x / s correctly rounded, for inv = 1 / s correctly rounded and |x| at most
-// 448 s or so (Markstein, "Computation of elementary functions on the IBM RISC
-// System/6000 processor", 1990: one residual step).  For an infinite scale, s is
-// given as 0: the result is x inv, 0 or, of an infinity, NaN.
+// x / s correctly rounded, for inv = 1 / s correctly rounded, s from 2^-95 up and
+// |x| at most 448 s or so (Markstein, "Computation of elementary functions on the
+// IBM RISC System/6000 processor", 1990: one residual step).  Below 2^-95 the
+// residual passes fp32's smallest number: the result is within an ulp.  For an
+// infinite scale, s is given as 0: the result is x inv, 0 or, of an infinity, NaN.
 __device__ __forceinline__ float quotient(float x, float s, float inv) {
   const float q = __fmul_rn(x, inv);
   return __fmaf_rn(__fmaf_rn(-q, s, x), inv, q);
