@@ -202,23 +202,16 @@ __global__ void __launch_bounds__(kMaxT, kMaxT == 256 ? 3 : 1) rmsnorm_forward_k
 
 // The same for longer rows, which come through a ring that every thread fills
 // for itself (cp.async: each reads only what it copied): kStages rows, one CTA
-// an SM of several teams.  The weights stay in registers.
+// of 288 to 512 threads an SM.  The weights stay in registers.
 template <typename XT, typename RT, GroupKind kGroups, int NU, int kStages, int kWhole>
-__global__ void __launch_bounds__(512, 1) rmsnorm_forward_ring_kernel(const __grid_constant__ RmsNormParams p, const GroupPlan plan,
-                                                               int T) {
-  extern __shared__ uint4 smem[];  // the ring, and [teams] GroupWords, kShared only
+__global__ void __launch_bounds__(512, 1) rmsnorm_forward_ring_kernel(const __grid_constant__ RmsNormParams p, const GroupPlan plan) {
+  extern __shared__ uint4 smem[];  // the ring, and GroupWords, kShared only
   constexpr int U = 8, kX = int(sizeof(XT)) / 2, kR = int(sizeof(RT)) / 2, kVecs = NU * (kX + kR);
-  __shared__ float red[16][2][32];
-  [[maybe_unused]] __shared__ unsigned top_row[16][2][32];
+  __shared__ float red[2][32];
+  [[maybe_unused]] __shared__ unsigned top_row[2][32];
   const auto inside = [&](int c) { return kWhole != 0 || c < p.h; };
   const bool with_res = kWhole != 0 ? kWhole == 2 : p.res != nullptr;
-  Team team;
-  const int teams = blockDim.x / T;
-  team.id = threadIdx.x / T;
-  team.tid = threadIdx.x - team.id * T;
-  team.threads = T;
-  team.red = &red[team.id][0][0];
-  const int tid = team.tid;
+  const int tid = int(threadIdx.x), T = int(blockDim.x);
   f32x2 w[NU][4];
 #pragma unroll
   for (int k = 0; k < NU; ++k) {
@@ -229,7 +222,7 @@ __global__ void __launch_bounds__(512, 1) rmsnorm_forward_ring_kernel(const __gr
     for (int j = 0; j < 4; ++j) w[k][j] = f2_pack(v[2 * j], v[2 * j + 1]);
   }
   const auto slot = [&](int stage, int v) {
-    return reinterpret_cast<unsigned char*>(smem + (stage * kVecs + v) * 512 + int(threadIdx.x));
+    return reinterpret_cast<unsigned char*>(smem + (stage * kVecs + v) * 512 + tid);
   };
   const auto fetch = [&](long long row, int stage) {
     if (row < p.s) {
@@ -250,8 +243,8 @@ __global__ void __launch_bounds__(512, 1) rmsnorm_forward_ring_kernel(const __gr
     }
     copy_commit();  // (an empty group past the end keeps the count)
   };
-  const GroupWords words(reinterpret_cast<unsigned char*>(smem + kStages * kVecs * 512) + team.id * plan.bytes(), plan);
-  const long long first = (long long)blockIdx.x * teams + team.id, stride = (long long)gridDim.x * teams;
+  const GroupWords words(smem + kStages * kVecs * 512, plan);
+  const long long first = blockIdx.x, stride = gridDim.x;
 #pragma unroll
   for (int i = 0; i < kStages; ++i) fetch(first + i * stride, i);
   int parity = 0, stage = 0;
@@ -280,7 +273,7 @@ __global__ void __launch_bounds__(512, 1) rmsnorm_forward_ring_kernel(const __gr
     }
     float s0, s1;
     f2_unpack(ss, s0, s1);
-    const float rstd = rsqrtf(team.sum(s0 + s1, parity) / float(p.h) + p.eps);
+    const float rstd = rsqrtf(team_sum<false>(s0 + s1, red[parity]) / float(p.h) + p.eps);
     fetch(row + kStages * stride, stage);  // (the stage's values are in registers)
     stage = stage + 1 == kStages ? 0 : stage + 1;
     if (tid == 0 && p.rstd != nullptr) p.rstd[row] = rstd;
@@ -313,14 +306,14 @@ __global__ void __launch_bounds__(512, 1) rmsnorm_forward_ring_kernel(const __gr
       }
     } else if constexpr (kGroups == kShared) {
       segments16(words, m, tid, T, p.h);
-      team.sync();
+      __syncthreads();
       words.join(plan, p.group, tid, T, p.scale + row * p.groups);
-      team.sync();
+      __syncthreads();
     }
     if constexpr (kGroups != kNoCodes) {
       float scale = 0.f, inv = 0.f;
       if constexpr (kGroups == kRow) {
-        scale = e4m3_scale(team.max(all, top_row[team.id][parity]));
+        scale = e4m3_scale(team_max<false>(all, top_row[parity]));
         inv = __frcp_rn(scale);
         if (tid == 0) p.scale[row] = scale;
       }
@@ -365,19 +358,18 @@ cudaError_t launch(const RmsNormParams& p, int threads, int sms, cudaStream_t st
 template <typename XT, typename RT, GroupKind kGroups, int kWhole = 0>
 cudaError_t launch_ring(const RmsNormParams& p, int sms, cudaStream_t st) {
   constexpr int NU = 4, kVecs = NU * int(sizeof(XT) + sizeof(RT)) / 2, kStages = kMaxSmem / (kVecs * 16 * 512);
-  const int T = (p.h / 8 + NU * 32 - 1) / (NU * 32) * 32, teams = 512 / T;
+  const int T = (p.h / 8 + NU * 32 - 1) / (NU * 32) * 32;
   if constexpr (kWhole == 0) {
     if (p.h == NU * 8 * T)
       return p.res != nullptr ? launch_ring<XT, RT, kGroups, 2>(p, sms, st) : launch_ring<XT, RT, kGroups, 1>(p, sms, st);
   }
   const auto kernel = rmsnorm_forward_ring_kernel<XT, RT, kGroups, NU, kStages, kWhole>;
   const GroupPlan plan(p, 16, 16);
-  const long long rows = (p.s + teams - 1) / teams;
   // (GroupWords: three words for 16 columns, 12 KB)
-  const int smem = kStages * kVecs * 16 * 512 + (kGroups == kShared ? teams * plan.bytes() : 0);
+  const int smem = kStages * kVecs * 16 * 512 + (kGroups == kShared ? plan.bytes() : 0);
   const cudaError_t e = allow_smem(kernel, smem);
   if (e != cudaSuccess) return e;
-  kernel<<<int(rows < sms ? rows : sms), T * teams, smem, st>>>(p, plan, T);
+  kernel<<<int(p.s < sms ? p.s : sms), T, smem, st>>>(p, plan);
   return cudaGetLastError();
 }
 
