@@ -311,7 +311,6 @@ __device__ __forceinline__ void encode8(const float (&xm)[8], const float (&xv)[
 // values are all ordinary: no quotient, no special case, 70 instructions an
 // element instead of 118.  m, v and the codes are the same bits.
 // ---------------------------------------------------------------------------
-__device__ __forceinline__ f32x2 both(float x) { return f2_pack(x, x); }
 __device__ __forceinline__ f32x2 f2_fma_down(f32x2 a, f32x2 b, f32x2 c) {
   f32x2 d;
   asm("fma.rm.f32x2 %0, %1, %2, %3;" : "=l"(d) : "l"(a), "l"(b), "l"(c));
@@ -333,22 +332,6 @@ struct StepPairs {
       : gs(both(c.gs)), b1(both(c.b1)), a1(both(c.a1)), b2(both(c.b2)), a2(both(c.a2)), rate(both(-c.rate)),
         inv2(both(c.inv2)), eps(both(c.eps)), keep(both(c.keep)) {}
 };
-
-// Root of v, 2^-100 <= v < 2^127, correctly rounded: the residual step of
-// Markstein's paper above on v rsqrt(v).
-__device__ __forceinline__ f32x2 root2(f32x2 v) {
-  float a, b, ya, yb;
-  f2_unpack(v, a, b);
-  asm("rsqrt.approx.ftz.f32 %0, %1;" : "=f"(ya) : "f"(a));
-  asm("rsqrt.approx.ftz.f32 %0, %1;" : "=f"(yb) : "f"(b));
-  const f32x2 y = f2_pack(ya, yb), r = f2_mul(v, y), h = f2_mul(y, both(0.5f));
-  return f2_fma(f2_fma(f2_mul(r, both(-1.f)), r, v), h, r);
-}
-
-__device__ __forceinline__ f32x2 quotient2(f32x2 x, f32x2 minus_s, f32x2 inv) {
-  const f32x2 q = f2_mul(x, inv);
-  return f2_fma(f2_fma(q, minus_s, x), inv, q);
-}
 
 // round_linear of two quotients x / s (with `small`: round_linear_small, and x
 // and s as ExactScale has them), and round_squares of two values
@@ -499,7 +482,7 @@ __global__ void __launch_bounds__(kThreads, kBits == 8 ? 4 : 3) adamw_kernel(con
         const float scale = e4m3_scale(second ? __float_as_uint(root_top) : tm), inv = __frcp_rn(scale);
         sm = __shfl_sync(kFull, scale, 0), sv = __shfl_sync(kFull, scale, 16);
         // v: of e4m3's normal values, with some room, and of root2's range
-        // (2.4e-4 > (2^-6)^2: v is compared with the scale's square).  About
+        // (2.8e-4 > (2^-6)^2: v is compared with the scale's square).  About
         // one block in 50 of normally distributed gradients has an m below them.
         const bool ordinary = lv >= fmaxf(sv * sv * 2.8e-4f, 0x1p-100f) && tm < 0x7f800000u && tv < 0x7f000000u;
         const bool small = !__all_sync(kFull, lm >= sm * 0x1.1p-6f) || sm < kExactScale;

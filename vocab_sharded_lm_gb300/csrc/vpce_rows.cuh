@@ -53,11 +53,30 @@ __device__ __forceinline__ float e4m3_scale(unsigned top) {
 // x / s correctly rounded, for inv = 1 / s correctly rounded, s from 2^-95 up and
 // |x| at most 448 s or so (Markstein, "Computation of elementary functions on the
 // IBM RISC System/6000 processor", 1990: one residual step).  Below 2^-95 the
-// residual passes fp32's smallest number: the result is within an ulp.  For an
+// residual passes fp32's smallest number: the result is within two ulps.  For an
 // infinite scale, s is given as 0: the result is x inv, 0 or, of an infinity, NaN.
 __device__ __forceinline__ float quotient(float x, float s, float inv) {
   const float q = __fmul_rn(x, inv);
   return __fmaf_rn(__fmaf_rn(-q, s, x), inv, q);
+}
+
+// The same of two values (minus_s = -s).
+__device__ __forceinline__ f32x2 both(float x) { return f2_pack(x, x); }
+__device__ __forceinline__ f32x2 quotient2(f32x2 x, f32x2 minus_s, f32x2 inv) {
+  const f32x2 q = f2_mul(x, inv);
+  return f2_fma(f2_fma(q, minus_s, x), inv, q);
+}
+
+// Roots of two values from 2^-100 to 2^127 by the same paper's residual step on
+// v rsqrt(v): correctly rounded.  No bound of rsqrt.approx's error implies it, so
+// a test compares every value of the range with CUDA's correctly rounded root.
+__device__ __forceinline__ f32x2 root2(f32x2 v) {
+  float a, b, ya, yb;
+  f2_unpack(v, a, b);
+  asm("rsqrt.approx.ftz.f32 %0, %1;" : "=f"(ya) : "f"(a));
+  asm("rsqrt.approx.ftz.f32 %0, %1;" : "=f"(yb) : "f"(b));
+  const f32x2 y = f2_pack(ya, yb), r = f2_mul(v, y), h = f2_mul(y, both(0.5f));
+  return f2_fma(f2_fma(f2_mul(r, both(-1.f)), r, v), h, r);
 }
 
 }  // namespace vpce
