@@ -635,6 +635,8 @@ vpce_status vpce_embedding_dropout_backward(const void* grad_out, vpce_dtype gra
  * The squares' sum is fp32 in a fixed order: rows whose mean square
  * passes fp32's range (|r| about 2^64) give rstd 0, and out 0 (NaN at an
  * infinite r); a NaN makes its row NaN, and so does a row of zeros at eps 0.
+ * Squares below fp32's smallest number (|r| under 2^-75) count as 0: a row of
+ * them alone has an infinite rstd at eps 0.
  * Results are bitwise reproducible.
  */
 #define VPCE_MAX_NORM_COLUMNS 32768
@@ -648,13 +650,14 @@ vpce_status vpce_rmsnorm_forward(const void* x, vpce_dtype dtype, int64_t ld_x, 
  * The same norm with its output in 8 bits, for products in 8 bits: per row and
  * group of `group` consecutive columns (the last may be shorter),
  *     scale = max_c |out_c| / 448, at least 2^-126,
- *     q_c = out_c / scale rounded to the nearest e4m3 value,
+ *     q_c = out_c / scale, in fp32, rounded to the nearest e4m3 value,
  * from the unrounded out, so q_c scale is within 2^-4 of out_c (or half of
  * e4m3's smallest step, 2^-10 scale).  A NaN or infinite out makes its group's scale
  * so; its own codes are NaN.
  *   group          0 (one scale per row) or a multiple of 16.
  *   q_out          device bytes [s, h], stride ld_q (0 = h): e4m3 codes.
- *   scale_out      device float [s][ceil(h / group)] ([s] for group 0).
+ *   scale_out      device float [s][ceil(h / group)] ([s] for group 0): a row's
+ *                  scales are consecutive, rows follow one another without a gap.
  * Other arguments as vpce_rmsnorm_forward; vector rows also need q_out and
  * ld_q to be multiples of 8.
  */

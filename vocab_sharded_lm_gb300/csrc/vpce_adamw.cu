@@ -7,10 +7,10 @@
 // of one tensor, found by bisection over the runs' numbers.
 //
 // With fp32 states HBM bounds the step: 30 bytes an element (weights and
-// gradients fp32, bf16 copies), 128256 x 4096 2302 us, 6.8 TB/s.  With 8-bit
-// states 18 bytes an element come with 70 instructions (ten of them the
-// generator's, some 25 the rounding's): 50304 x 4096 640 us, 5.8 TB/s, the issue
-// slots about 70% busy.  The gradients' norm reads 128256 x 4096 fp32 in 308 us,
+// gradients fp32, bf16 copies), 128256 x 4096 2287 us, 6.9 TB/s.  With 8-bit
+// states 18 bytes an element come with 79 instructions (32 on the integer and
+// logic pipe, 30 on those of multiplications): 50304 x 4096 642 us, 5.8 TB/s, the
+// issue slots 68% busy.  The gradients' norm reads 128256 x 4096 fp32 in 307 us,
 // 6.8 TB/s.
 #include <cmath>
 
@@ -308,8 +308,9 @@ __device__ __forceinline__ void encode8(const float (&xm)[8], const float (&xv)[
 
 // ---------------------------------------------------------------------------
 // The same on pairs of fp32 values (one instruction for two), for blocks whose
-// values are all ordinary: no quotient, no special case, 70 instructions an
-// element instead of 118.  m, v and the codes are the same bits.
+// values are all ordinary: no quotient by a division, no special case, 79
+// instructions an element (118 on single values).  m, v and the codes are the
+// same bits.
 // ---------------------------------------------------------------------------
 __device__ __forceinline__ f32x2 f2_fma_down(f32x2 a, f32x2 b, f32x2 c) {
   f32x2 d;
